@@ -10,6 +10,10 @@ Functions (same names as the C entry points):
     gt_spd_build(indptr, indices, n, D)                       -> spd int8 [n][ld]
     gt_bias_attn_fwd(q, k, v, spd, T, scale=None, kv_block=0) -> (o, lse)
     gt_bias_attn_bwd(q, k, v, o, dO, lse, spd, T, scale=None) -> (dq, dk, dv, dT)
+    gt_layer_norm_fwd(x, gain, shift, eps)                    -> (y, mean, rstd)
+    gt_layer_norm_bwd(dy, x, gain, mean, rstd, dres)          -> (dx, dgain, dshift)
+    gt_linear_fwd(x, w, b, act, r)                            -> (y, pre)
+    gt_linear_bwd(dy, x, w, pre, act, dx_add)                 -> (dx, dw, db)
 The operation follows MegaGraph (abstract: attention scores plus a
 topology-aware bias matrix; Fig. 4: blockwise KV streaming with the bias column
 slice formed per block) with the Graphormer bias b[h][i][j] = T[h][spd[i][j]].
@@ -28,12 +32,16 @@ __all__ = [
     "gt_bias_attn_bwd", "gt_spd_workspace_size", "gt_bias_attn_workspace_size",
     "gt_check_device_status", "gt_status_string", "spd_ld", "GT_F32", "GT_BF16",
     "GT_SPD_AUTO", "GT_SPD_SCAN32", "GT_SPD_SCAN16", "GT_SPD_QUEUE32", "GT_SPD_GLOBAL64",
+    "gt_layer_norm_fwd", "gt_layer_norm_bwd", "gt_layer_norm_workspace_size", "gt_linear_fwd", "gt_linear_bwd",
+    "gt_linear_fwd_workspace_size", "gt_linear_bwd_workspace_size", "GT_ACT_NONE", "GT_ACT_GELU",
 ]
 
 GT_F32 = 0
 GT_BF16 = 1
 # search algorithms of gt_spd_build (include/gt_attn.h)
 GT_SPD_AUTO, GT_SPD_SCAN32, GT_SPD_SCAN16, GT_SPD_QUEUE32, GT_SPD_GLOBAL64 = 0, 1, 2, 3, 4
+# activations of gt_linear_fwd / gt_linear_bwd
+GT_ACT_NONE, GT_ACT_GELU = 0, 1
 GT_OK = 0
 _STATUS = {0: "GT_OK", -1: "GT_ERR_INVALID_ARG", -2: "GT_ERR_UNSUPPORTED", -3: "GT_ERR_CUDA",
            -4: "GT_ERR_TIMEOUT", -5: "GT_ERR_WORKSPACE"}
@@ -115,6 +123,22 @@ def load_library():
         lib.gt_bias_attn_fwd_partial.restype = ctypes.c_int
         lib.gt_bias_attn_merge.argtypes = [i32, i32, i32, i32, i32, P, P, P, P, P]
         lib.gt_bias_attn_merge.restype = ctypes.c_int
+        lib.gt_layer_norm_fwd.argtypes = [i32, i32, i32, i32, P, i64, P, P, f32, P, i64, P, P, P]
+        lib.gt_layer_norm_fwd.restype = ctypes.c_int
+        lib.gt_layer_norm_workspace_size.argtypes = [i32, i32]
+        lib.gt_layer_norm_workspace_size.restype = sz
+        lib.gt_layer_norm_bwd.argtypes = [i32, i32, i32, i32, P, i64, P, i64, P, P, P, P, i64, P, i64, P, P, P, sz, P]
+        lib.gt_layer_norm_bwd.restype = ctypes.c_int
+        lib.gt_linear_fwd_workspace_size.argtypes = [i32, i32, i32, i32, i32]
+        lib.gt_linear_fwd_workspace_size.restype = sz
+        lib.gt_linear_fwd.argtypes = [i32, i32, i32, i32, i32, P, i64, P, i64, P, i32, P, i64, P, i64, P, i64,
+                                      P, sz, P]
+        lib.gt_linear_fwd.restype = ctypes.c_int
+        lib.gt_linear_bwd_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32]
+        lib.gt_linear_bwd_workspace_size.restype = sz
+        lib.gt_linear_bwd.argtypes = [i32, i32, i32, i32, i32, P, i64, P, i64, P, i64, P, i64, i32, P, i64, P, i64,
+                                      P, i64, P, P, sz, P]
+        lib.gt_linear_bwd.restype = ctypes.c_int
         lib.gt_kernel_stats_reset.argtypes = [i32]
         lib.gt_kernel_stats_reset.restype = ctypes.c_int
         lib.gt_kernel_stats_read.argtypes = [ctypes.POINTER(KernelStat), i32, ctypes.POINTER(i32)]
@@ -349,6 +373,224 @@ def gt_layer_bwd(x, params: dict, spd, T, saved: dict, dy, workspace=None, strea
                           workspace.numel(), _stream_handle(stream))
     _check("gt_layer_bwd", rc)
     return dx, grads, dT
+
+
+class _Scope:
+    """Device and stream of one call: the tensors' device, and `stream` (default: that
+    device's current stream).  What is allocated inside belongs to that stream."""
+
+    def __init__(self, device, stream):
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream of {stream.device} given for tensors on {device}")
+        self.caller = None if stream is None else torch.cuda.current_stream(device)
+        self.stream = stream if stream is not None else torch.cuda.current_stream(device)
+        self.handle = int(self.stream.cuda_stream)
+        self.ctx = (torch.cuda.stream(stream) if stream is not None else
+                    torch.cuda.device(device) if device.index != torch.cuda.current_device() else None)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+    def lend(self, given, made):
+        """On another stream than the caller's: the caller's tensors stay allocated until the
+        call's work is done, and the results until the caller's stream is done with them."""
+        if self.caller is None or self.caller == self.stream:
+            return
+        for t in given:
+            if t is not None:
+                t.record_stream(self.stream)
+        for t in made:
+            if t is not None:
+                t.record_stream(self.caller)
+
+
+def _matrix(name, t, rows, cols, dtype, device):
+    """Leading dimension of a [rows][cols] matrix with unit column stride."""
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be on {device}, a CUDA device")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} must be [{rows}][{cols}], got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"the columns of {name} must be contiguous")
+    if rows <= 1:
+        return (cols + 7) // 8 * 8       # one row: its stride means nothing
+    if t.stride(0) < cols:
+        raise ValueError(f"the rows of {name} overlap")
+    return t.stride(0)
+
+
+def _vector(name, t, size, device):
+    if t.device != device or t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != size or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous fp32 [{size}] on {device}")
+
+
+def _buffer(workspace, nbytes, device):
+    if workspace is None:
+        return _workspace(nbytes, device)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {device}")
+    return workspace
+
+
+def _nbytes(t):
+    return t.numel() * t.element_size()
+
+
+def _is_2d(name, t):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions, got {t.dim()}")
+
+
+def gt_layer_norm_workspace_size(n: int, c: int) -> int:
+    """Workspace bytes of gt_layer_norm_bwd (0 for sizes that are not supported)."""
+    return int(load_library().gt_layer_norm_workspace_size(n, c))
+
+
+def gt_layer_norm_fwd(x, gain, shift, eps: float = 1e-5, out_dtype=None, out=None, mean=None, rstd=None,
+                      stream=None):
+    """LayerNorm of the rows of x [n][c] (fp32 or bf16): y [n][c] of out_dtype (default:
+    x's type), and fp32 mean [n] and rstd [n] for the backward.  gain, shift fp32 [c]."""
+    lib = load_library()
+    _is_2d("x", x)
+    (n, c), dev = x.shape, x.device
+    ldx = _matrix("x", x, n, c, x.dtype, dev)
+    _vector("gain", gain, c, dev)
+    _vector("shift", shift, c, dev)
+    with _Scope(dev, stream) as sc:
+        y = torch.empty((n, c), dtype=out_dtype or x.dtype, device=dev) if out is None else out
+        ldy = _matrix("out", y, n, c, out_dtype or y.dtype, dev)
+        mu = torch.empty(n, dtype=torch.float32, device=dev) if mean is None else mean
+        rs = torch.empty(n, dtype=torch.float32, device=dev) if rstd is None else rstd
+        _vector("mean", mu, n, dev)
+        _vector("rstd", rs, n, dev)
+        _check("gt_layer_norm_fwd", lib.gt_layer_norm_fwd(
+            _dtype_code(x), _dtype_code(y), n, c, x.data_ptr(), ldx, gain.data_ptr(), shift.data_ptr(), float(eps),
+            y.data_ptr(), ldy, mu.data_ptr(), rs.data_ptr(), sc.handle))
+        sc.lend((x, gain, shift), (y, mu, rs))
+    return y, mu, rs
+
+
+def gt_layer_norm_bwd(dy, x, gain, mean, rstd, dres=None, dx=None, dgain=None, dshift=None, workspace=None,
+                      stream=None):
+    """LayerNorm backward from dy = dL/dy and the forward's x, mean, rstd: dx [n][c] of x's
+    type (+ dres, the gradient that reaches x around the norm), dgain and dshift fp32 [c]."""
+    lib = load_library()
+    _is_2d("x", x)
+    (n, c), dev = x.shape, x.device
+    ldx = _matrix("x", x, n, c, x.dtype, dev)
+    lddy = _matrix("dy", dy, n, c, dy.dtype, dev)
+    ldr = 0 if dres is None else _matrix("dres", dres, n, c, x.dtype, dev)
+    _vector("gain", gain, c, dev)
+    _vector("mean", mean, n, dev)
+    _vector("rstd", rstd, n, dev)
+    with _Scope(dev, stream) as sc:
+        dx = torch.empty((n, c), dtype=x.dtype, device=dev) if dx is None else dx
+        lddx = _matrix("dx", dx, n, c, x.dtype, dev)
+        dgain = torch.empty(c, dtype=torch.float32, device=dev) if dgain is None else dgain
+        dshift = torch.empty(c, dtype=torch.float32, device=dev) if dshift is None else dshift
+        _vector("dgain", dgain, c, dev)
+        _vector("dshift", dshift, c, dev)
+        ws = _buffer(workspace, lib.gt_layer_norm_workspace_size(n, c), dev)
+        _check("gt_layer_norm_bwd", lib.gt_layer_norm_bwd(
+            _dtype_code(x), _dtype_code(dy), n, c, dy.data_ptr(), lddy, x.data_ptr(), ldx, gain.data_ptr(),
+            mean.data_ptr(), rstd.data_ptr(), _ptr(dres), ldr, dx.data_ptr(), lddx, dgain.data_ptr(),
+            dshift.data_ptr(), ws.data_ptr(), _nbytes(ws), sc.handle))
+        sc.lend((dy, x, gain, mean, rstd, dres, workspace), (dx, dgain, dshift))
+    return dx, dgain, dshift
+
+
+def _aligned(*pairs):
+    """Whether every (tensor, leading dimension) has a base and a row stride of whole 16 bytes."""
+    return int(all(t.data_ptr() % 16 == 0 and ld * t.element_size() % 16 == 0 for t, ld in pairs))
+
+
+def gt_linear_fwd_workspace_size(dtype: int, m: int, k: int, n: int, aligned: bool = True) -> int:
+    return int(load_library().gt_linear_fwd_workspace_size(dtype, m, k, n, int(aligned)))
+
+
+def gt_linear_bwd_workspace_size(dtype: int, ytype: int, m: int, k: int, n: int, act: int = GT_ACT_NONE,
+                                 aligned: bool = True) -> int:
+    return int(load_library().gt_linear_bwd_workspace_size(dtype, ytype, m, k, n, act, int(aligned)))
+
+
+def gt_linear_fwd(x, w, b=None, act: int = GT_ACT_NONE, r=None, out_dtype=None, save_pre: bool = False, out=None,
+                  pre=None, workspace=None, stream=None):
+    """y = act(x w + b) + r: x [m][k] and w [k][n] of one type (fp32 or bf16), b fp32 [n], r
+    [m][n] of y's type.  Returns (y, pre): y of out_dtype (default: r's type, else x's; fp32
+    for fp32 products), pre = x w + b of x's type with save_pre (or given to write to), else None."""
+    lib = load_library()
+    _is_2d("x", x)
+    _is_2d("w", w)
+    (m, k), n, dev = x.shape, w.shape[1], x.device
+    ldx = _matrix("x", x, m, k, x.dtype, dev)
+    ldw = _matrix("w", w, k, n, x.dtype, dev)
+    if b is not None:
+        _vector("b", b, n, dev)
+    yt = out_dtype or (out.dtype if out is not None else r.dtype if r is not None else x.dtype)
+    ldr = 0 if r is None else _matrix("r", r, m, n, yt, dev)
+    dt = _dtype_code(x)
+    with _Scope(dev, stream) as sc:
+        y = torch.empty((m, n), dtype=yt, device=dev) if out is None else out
+        ldy = _matrix("out", y, m, n, yt, dev)
+        a = torch.empty((m, n), dtype=x.dtype, device=dev) if pre is None and save_pre else pre
+        lda = 0 if a is None else _matrix("pre", a, m, n, x.dtype, dev)
+        ws = workspace
+        if ws is None:
+            need = lib.gt_linear_fwd_workspace_size(dt, m, k, n, _aligned((x, ldx), (w, ldw)))
+            ws = _workspace(need, dev)
+        ws = _buffer(ws, 0, dev)
+        _check("gt_linear_fwd", lib.gt_linear_fwd(
+            dt, _dtype_code(y), m, k, n, x.data_ptr(), ldx, w.data_ptr(), ldw, _ptr(b), act, _ptr(r), ldr,
+            y.data_ptr(), ldy, _ptr(a), lda, ws.data_ptr(), _nbytes(ws), sc.handle))
+        sc.lend((x, w, b, r, workspace), (y, a))
+    return y, a
+
+
+def gt_linear_bwd(dy, x, w, pre=None, act: int = GT_ACT_NONE, dx_add=None, need_dx: bool = True,
+                  need_dw: bool = True, need_db: bool = True, dx=None, dw=None, db=None, workspace=None,
+                  stream=None):
+    """Backward of gt_linear_fwd from dy = dL/dy [m][n]: (dx [m][k], dw [k][n], db fp32 [n]), dx
+    and dw of x's type, None for those not needed.  pre: the forward's, with GELU.  dx_add
+    [m][k]: a gradient that reaches x another way, added to dx."""
+    lib = load_library()
+    _is_2d("x", x)
+    _is_2d("w", w)
+    (m, k), n, dev = x.shape, w.shape[1], x.device
+    ldx = _matrix("x", x, m, k, x.dtype, dev)
+    ldw = _matrix("w", w, k, n, x.dtype, dev)
+    lddy = _matrix("dy", dy, m, n, dy.dtype, dev)
+    lda = 0 if pre is None else _matrix("pre", pre, m, n, x.dtype, dev)
+    ldadd = 0 if dx_add is None else _matrix("dx_add", dx_add, m, k, x.dtype, dev)
+    dt, yt = _dtype_code(x), _dtype_code(dy)
+    with _Scope(dev, stream) as sc:
+        if need_dx and dx is None:
+            dx = torch.empty((m, k), dtype=x.dtype, device=dev)
+        if need_dw and dw is None:
+            dw = torch.empty((k, n), dtype=x.dtype, device=dev)
+        if need_db and db is None:
+            db = torch.empty(n, dtype=torch.float32, device=dev)
+        lddx = 0 if dx is None else _matrix("dx", dx, m, k, x.dtype, dev)
+        lddw = 0 if dw is None else _matrix("dw", dw, k, n, x.dtype, dev)
+        if db is not None:
+            _vector("db", db, n, dev)
+        ws = workspace
+        if ws is None:
+            need = lib.gt_linear_bwd_workspace_size(dt, yt, m, k, n, act, _aligned((dy, lddy), (x, ldx), (w, ldw)))
+            ws = _workspace(need, dev)
+        ws = _buffer(ws, 0, dev)
+        _check("gt_linear_bwd", lib.gt_linear_bwd(
+            dt, yt, m, k, n, dy.data_ptr(), lddy, x.data_ptr(), ldx, w.data_ptr(), ldw, _ptr(pre), lda, act,
+            _ptr(dx_add), ldadd, _ptr(dx), lddx, _ptr(dw), lddw, _ptr(db), ws.data_ptr(), _nbytes(ws), sc.handle))
+        sc.lend((dy, x, w, pre, dx_add, workspace), (dx, dw, db))
+    return dx, dw, db
 
 
 def gt_check_device_status(stream=None) -> None:

@@ -1,0 +1,98 @@
+// gt_vec8.cuh -- eight consecutive row elements at a time, as the LayerNorm and
+// linear-layer kernels move them: 16-byte accesses where rows allow them, single
+// elements otherwise; and the fixed-order sum of per-CTA partial rows.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "gt_common.cuh"
+#include "gt_stats.cuh"
+
+namespace gt {
+
+// Whether rows of `ld` elements of type T at p can be moved 16 bytes at a time
+// at column offsets that are multiples of 8 elements.
+inline bool rows16(const void* p, int64_t ld, int elem_bytes) {
+    return aligned16(p) && (ld * elem_bytes) % 16 == 0;
+}
+
+// Eight elements as stored: 16 bytes of bf16 or 32 of fp32.
+template <typename T> struct Raw8;
+template <> struct Raw8<__nv_bfloat16> { uint4 a; };
+template <> struct Raw8<float> { uint4 a, b; };
+
+// Elements p[0 .. 7], those at or past `live` as zeros.
+template <typename T>
+__device__ __forceinline__ Raw8<T> load8(const T* p, int live, bool vec) {
+    Raw8<T> r;
+    if (vec && live >= 8) {
+        const uint4* s = reinterpret_cast<const uint4*>(p);
+        r.a = __ldg(s);
+        if constexpr (sizeof(T) == 4) r.b = __ldg(s + 1);
+    } else if constexpr (sizeof(T) == 4) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = i < live ? __float_as_uint(__ldg(reinterpret_cast<const float*>(p) + i)) : 0u;
+        r.a = make_uint4(w[0], w[1], w[2], w[3]);
+        r.b = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {
+        const unsigned short* s = reinterpret_cast<const unsigned short*>(p);
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = i < live ? (uint32_t)__ldg(s + i) : 0u;
+        r.a = make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16));
+    }
+    return r;
+}
+
+__device__ __forceinline__ void unpack8(const Raw8<float>& r, float (&v)[8]) {
+    v[0] = __uint_as_float(r.a.x); v[1] = __uint_as_float(r.a.y); v[2] = __uint_as_float(r.a.z); v[3] = __uint_as_float(r.a.w);
+    v[4] = __uint_as_float(r.b.x); v[5] = __uint_as_float(r.b.y); v[6] = __uint_as_float(r.b.z); v[7] = __uint_as_float(r.b.w);
+}
+
+__device__ __forceinline__ void unpack8(const Raw8<__nv_bfloat16>& r, float (&v)[8]) {
+    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+__device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// p[0 .. 7] = v, the elements at or past `live` left alone.
+__device__ __forceinline__ void store8(float* p, const float (&v)[8], int live, bool vec) {
+    if (vec && live >= 8) {
+        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < live) p[i] = v[i];
+    }
+}
+
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8], int live, bool vec) {
+    if (vec && live >= 8) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]),
+                                                  bf16x2_bits(v[4], v[5]), bf16x2_bits(v[6], v[7]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < live) p[i] = __float2bfloat16_rn(v[i]);
+    }
+}
+
+// Column sums of part [rows][cols] in a fixed order: column c of the first
+// `split` columns goes to out0[c], the others to out1[c - split].  In gt_norm.cu.
+int launch_col_sum(const char* name, const float* part, int rows, int cols, float* out0, int split, float* out1,
+                   cudaStream_t s);
+
+}  // namespace gt

@@ -356,6 +356,101 @@ int gt_layer_bwd(int32_t n, int32_t h, int32_t d, int32_t f, const float* x, con
                  const float* dy, float* dx, const gt_layer_grads* g, float* dT,
                  void* workspace, size_t ws_bytes, void* stream);
 
+/*
+ * LayerNorm and linear layers at any width: what surrounds the biased attention
+ * in an encoder layer whose widths gt_layer_fwd does not take (the attention
+ * itself takes h <= 16 heads of d <= 64 channels).  The pre-LayerNorm layer above is
+ *   u = gt_layer_norm_fwd(x);  q, k, v = gt_linear_fwd(u, W_q | W_k | W_v);
+ *   o = gt_bias_attn_fwd(q, k, v);  hh = gt_linear_fwd(o, W_o, r = x);
+ *   z = gt_layer_norm_fwd(hh);  g = gt_linear_fwd(z, W_1, act = GELU);
+ *   y = gt_linear_fwd(g, W_2, r = hh)
+ * with a row per node.  Every matrix is row-major with a leading dimension in
+ * elements (ld >= columns), so slices of wider matrices serve; any alignment of
+ * its element type is accepted, and rows whose base and stride are multiples of
+ * 16 bytes move faster.  Statistics and sums are fp32.  Results do not change
+ * from run to run.  Outputs must not overlap each other or any input, except
+ * where a call says so.  A workspace is 16-byte aligned (GT_ERR_WORKSPACE if not);
+ * its contents matter during a call only, and calls that may run at the same time
+ * need workspaces of their own.
+ *
+ * gt_layer_norm_fwd: per row, over its c features,
+ *   mean = sum_j x_j / c, rstd = 1 / sqrt(sum_j (x_j - mean)^2 / c + eps),
+ *   y_j = gain_j (x_j - mean) rstd + shift_j
+ *   xtype, ytype  element types (gt_dtype) of x and of y, any pair.
+ *   x  device [n][ldx], y device [n][ldy]; gain, shift device fp32 [c]; mean,
+ *   rstd device fp32 [n] (outputs: the backward takes them).
+ * Errors: GT_ERR_INVALID_ARG for a NULL pointer, an unknown type, n < 1, c < 1, a
+ * leading dimension below c, or an eps that is not finite and positive;
+ * GT_ERR_UNSUPPORTED for c > 16384.
+ *
+ * gt_layer_norm_bwd: given dy = dL/dy, with xh = (x - mean) rstd and d = gain dy,
+ *   dx = rstd (d - sum_j d_j / c - xh sum_j d_j xh_j / c) + dres
+ *   dgain = sum over rows of dy xh,  dshift = sum over rows of dy
+ *   dy has y's type; dx (output) and dres (NULL: none; the gradient that reaches x
+ *   around the norm) have x's type, and may be one buffer; dgain, dshift device
+ *   fp32 [c] (outputs, overwritten).  workspace: at least
+ *   gt_layer_norm_workspace_size(n, c) bytes (0 for sizes not supported).
+ * Errors as the forward's, plus GT_ERR_WORKSPACE.
+ */
+int gt_layer_norm_fwd(int32_t xtype, int32_t ytype, int32_t n, int32_t c, const void* x, int64_t ldx,
+                      const float* gain, const float* shift, float eps, void* y, int64_t ldy,
+                      float* mean, float* rstd, void* stream);
+size_t gt_layer_norm_workspace_size(int32_t n, int32_t c);
+int gt_layer_norm_bwd(int32_t xtype, int32_t ytype, int32_t n, int32_t c, const void* dy, int64_t lddy,
+                      const void* x, int64_t ldx, const float* gain, const float* mean, const float* rstd,
+                      const void* dres, int64_t ldr, void* dx, int64_t lddx, float* dgain, float* dshift,
+                      void* workspace, size_t ws_bytes, void* stream);
+
+/* Activations of the linear layer: none, or GELU(a) = a Phi(a) (Phi the normal CDF). */
+typedef enum { GT_ACT_NONE = 0, GT_ACT_GELU = 1 } gt_act;
+
+/*
+ * gt_linear_fwd: a = x W + b, y = act(a) + r.
+ *   dtype  type of x, W and pre: GT_BF16 (bf16 products, fp32 sums) or GT_F32
+ *          (products of three-part bf16 splits, fp32 sums: fp32 accuracy; a
+ *          non-finite input makes the sums it enters non-finite, NaN where exact
+ *          arithmetic may give an infinity).
+ *   ytype  type of y and r: GT_F32, or GT_BF16 with dtype GT_BF16.
+ *   x  device [m][ldx >= k]; W device [k][ldw >= n] (in x out); b device fp32 [n] or
+ *   NULL; r device [m][ldr >= n] or NULL (it may be y itself).
+ *   y  device [m][ldy >= n] (output); pre device [m][ldpre >= n] or NULL (output): a,
+ *   rounded to dtype, which the backward of a GELU layer takes.
+ *   workspace: at least gt_linear_fwd_workspace_size bytes (may be NULL where that
+ *   is 0).  `aligned`: non-zero when the bases and row strides of x and W are
+ *   multiples of 16 bytes; else the size includes the copies that bf16 matrices need.
+ * Supported: 1 <= m <= 2^24, 1 <= k, n <= 65536.
+ * Errors: GT_ERR_INVALID_ARG for a NULL x, W or y, an unknown type or activation, m,
+ * k or n < 1, or a leading dimension below its row; GT_ERR_UNSUPPORTED for larger
+ * sizes or a bf16 y of fp32 products; GT_ERR_WORKSPACE.
+ *
+ * gt_linear_bwd: given dy = dL/dy (type ytype), with da = dy act'(pre),
+ *   dx = da W^T + add,  dW = x^T da,  db = sum over rows of da
+ *   (the gradient with respect to r is dy itself).  Any of dx, dw, db may be NULL: it
+ *   is not computed, and what only it reads (W for dx, x for dw) may be NULL too.
+ *   pre    the forward's pre with GT_ACT_GELU; NULL with GT_ACT_NONE.
+ *   add    device [m][ldadd >= k] of dtype or NULL (it may be dx itself): a gradient
+ *          that reaches x another way.
+ *   dx     device [m][lddx >= k] of dtype; dw device [k][lddw >= n] of dtype; db device
+ *          fp32 [n] (outputs, overwritten).
+ *   With dtype GT_BF16 da is rounded to bf16 for the two products (db is summed before
+ *   that rounding).
+ *   workspace: at least gt_linear_bwd_workspace_size bytes (`aligned` as above, for
+ *   dy, x and W).
+ * Errors as the forward's, plus GT_ERR_INVALID_ARG when dx, dw and db are all NULL,
+ * pre and act disagree, or add comes without dx.
+ */
+size_t gt_linear_fwd_workspace_size(int32_t dtype, int32_t m, int32_t k, int32_t n, int32_t aligned);
+int gt_linear_fwd(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n, const void* x, int64_t ldx,
+                  const void* w, int64_t ldw, const float* b, int32_t act, const void* r, int64_t ldr,
+                  void* y, int64_t ldy, void* pre, int64_t ldpre, void* workspace, size_t ws_bytes,
+                  void* stream);
+size_t gt_linear_bwd_workspace_size(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n, int32_t act,
+                                    int32_t aligned);
+int gt_linear_bwd(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n, const void* dy, int64_t lddy,
+                  const void* x, int64_t ldx, const void* w, int64_t ldw, const void* pre, int64_t ldpre,
+                  int32_t act, const void* add, int64_t ldadd, void* dx, int64_t lddx, void* dw, int64_t lddw,
+                  float* db, void* workspace, size_t ws_bytes, void* stream);
+
 /* Static English text for a gt_status value. */
 const char* gt_status_string(int status);
 

@@ -1,0 +1,316 @@
+"""The linear layer's forward and backward on the GPU against fp64, within derived bounds."""
+import math
+
+import pytest
+import torch
+
+import linear_ref as R
+
+pytestmark = pytest.mark.gpu
+F, B = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def gt():
+    import graph_transformer_attention_gb300 as m
+    from graph_transformer_attention_gb300 import build
+    build.build()
+    m.load_library()
+    return m
+
+
+def _mat(rows, cols, dtype, seed, std=1.0, pad=0, offset=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    t = torch.randn(rows, cols + pad + offset, generator=g, device="cuda") * std
+    return t.to(dtype)[:, offset:offset + cols]
+
+
+def _vec(n, seed, std=0.5):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(n, generator=g, device="cuda") * std
+
+
+def _forward(gt, m, k, n, xt, yt, act, bias=True, res=True, pad=0, offset=0):
+    x = _mat(m, k, xt, 1, pad=pad, offset=offset)
+    w = _mat(k, n, xt, 2, 1 / math.sqrt(k), pad=pad, offset=offset)
+    b = _vec(n, 3) if bias else None
+    r = _mat(m, n, yt, 4, pad=pad, offset=offset) if res else None
+    y, pre = gt.gt_linear_fwd(x, w, b, act=act, r=r, out_dtype=yt, save_pre=True)
+    gt.gt_check_device_status()
+    assert y.dtype == yt and pre.dtype == xt
+    R.check({"y": y, "pre": pre}, R.linear_fwd(x, w, b, act == gt.GT_ACT_GELU, r, yt))
+
+
+def _backward(gt, m, k, n, xt, yt, act, add=True, pad=0, offset=0):
+    dy = _mat(m, n, yt, 5, pad=pad, offset=offset)
+    x = _mat(m, k, xt, 1, pad=pad, offset=offset)
+    w = _mat(k, n, xt, 2, 1 / math.sqrt(k), pad=pad, offset=offset)
+    gelu = act == gt.GT_ACT_GELU
+    pre = _mat(m, n, xt, 6, pad=pad, offset=offset) if gelu else None
+    a = _mat(m, k, xt, 7, pad=pad, offset=offset) if add else None
+    dx, dw, db = gt.gt_linear_bwd(dy, x, w, pre=pre, act=act, dx_add=a)
+    gt.gt_check_device_status()
+    R.check({"dx": dx, "dw": dw, "db": db}, R.linear_bwd(dy, x, w, pre, gelu, a))
+
+
+TYPES = [(B, B), (B, F), (F, F)]
+# one row, one feature, tiles exact and one past each of their edges, contractions that end inside a k-block
+SHAPES = [(1, 1, 1), (1, 64, 64), (2, 8, 200), (128, 64, 64), (129, 65, 65), (127, 63, 129), (64, 16, 256),
+          (300, 200, 257), (257, 72, 512), (640, 136, 72), (130, 1000, 40), (17, 520, 1016)]
+
+
+@pytest.mark.parametrize("act", [0, 1])
+@pytest.mark.parametrize("xt,yt", TYPES)
+@pytest.mark.parametrize("m,k,n", SHAPES)
+def test_forward(gt, m, k, n, xt, yt, act):
+    _forward(gt, m, k, n, xt, yt, act)
+
+
+@pytest.mark.parametrize("act", [0, 1])
+@pytest.mark.parametrize("xt,yt", TYPES)
+@pytest.mark.parametrize("m,k,n", SHAPES)
+def test_backward(gt, m, k, n, xt, yt, act):
+    _backward(gt, m, k, n, xt, yt, act)
+
+
+@pytest.mark.parametrize("xt,yt", TYPES)
+@pytest.mark.parametrize("pad,offset", [(8, 0), (5, 0), (0, 8), (8, 1), (0, 3)])
+def test_strided_and_unaligned_operands(gt, xt, yt, pad, offset):
+    _forward(gt, 150, 104, 88, xt, yt, 1, pad=pad, offset=offset)
+    _backward(gt, 150, 104, 88, xt, yt, 1, pad=pad, offset=offset)
+    _backward(gt, 150, 104, 88, xt, yt, 0, pad=pad, offset=offset)
+
+
+@pytest.mark.parametrize("m,k,n,xt,yt", [
+    (3000, 256, 1024, B, B),        # more tiles than SMs: the persistent loop, both accumulators
+    (20000, 64, 192, B, F),         # the tile group order's tail group
+    (5000, 64, 192, F, F),
+    (4100, 64, 64, B, B),           # long contraction of dW over few tiles: splits and their join
+    (4100, 40, 72, F, F),
+    (2, 4000, 24, B, B),            # long contraction of the forward over one tile
+    (40, 24, 4000, F, F),           # ... and of dx
+])
+def test_larger_shapes(gt, m, k, n, xt, yt):
+    for act in (0, 1):
+        _forward(gt, m, k, n, xt, yt, act, res=act == 0)
+        _backward(gt, m, k, n, xt, yt, act, add=act == 0)
+
+
+def test_without_bias_residual_or_add(gt):
+    for xt, yt in TYPES:
+        _forward(gt, 70, 90, 110, xt, yt, 1, bias=False, res=False)
+        _backward(gt, 70, 90, 110, xt, yt, 0, add=False)
+
+
+def test_outputs_into_slices_leave_the_rest_alone(gt):
+    m, k, n = 75, 48, 40
+    for xt, yt in TYPES:
+        for pad in (8, 3):
+            x, w, dy = _mat(m, k, xt, 1), _mat(k, n, xt, 2), _mat(m, n, yt, 3)
+            buf = {s: torch.full((r, c + 2 * pad), 7.0, dtype=t, device="cuda")
+                   for s, r, c, t in (("y", m, n, yt), ("pre", m, n, xt), ("dx", m, k, xt), ("dw", k, n, xt))}
+            cut = {s: t[:, pad:-pad] for s, t in buf.items()}
+            gt.gt_linear_fwd(x, w, None, act=1, out=cut["y"], pre=cut["pre"])
+            R.check({"y": cut["y"], "pre": cut["pre"]}, R.linear_fwd(x, w, None, True, None, yt))
+            gt.gt_linear_bwd(dy, x, w, dx=cut["dx"], dw=cut["dw"])
+            ref = R.linear_bwd(dy, x, w, None, False, None)
+            R.check({"dx": cut["dx"], "dw": cut["dw"]}, ref)
+            for t in buf.values():
+                assert (t[:, :pad] == 7).all() and (t[:, -pad:] == 7).all()
+
+
+def test_parts_of_the_backward(gt):
+    """Each gradient alone equals the one of the whole call."""
+    for xt, yt in TYPES:
+        dy, x, w, pre = _mat(200, 90, yt, 1), _mat(200, 70, xt, 2), _mat(70, 90, xt, 3), _mat(200, 90, xt, 4)
+        for act, p in ((0, None), (1, pre)):
+            dx, dw, db = gt.gt_linear_bwd(dy, x, w, pre=p, act=act)
+            one = gt.gt_linear_bwd(dy, x, w, pre=p, act=act, need_dw=False, need_db=False)
+            two = gt.gt_linear_bwd(dy, x, w, pre=p, act=act, need_dx=False, need_db=False)
+            three = gt.gt_linear_bwd(dy, x, w, pre=p, act=act, need_dx=False, need_dw=False)
+            assert torch.equal(one[0], dx) and one[1] is None and one[2] is None
+            assert torch.equal(two[1], dw) and two[0] is None
+            assert torch.equal(three[2], db) and three[0] is None and three[1] is None
+
+
+def test_in_place_residual_and_accumulated_gradient(gt):
+    for xt, yt in TYPES:
+        x, w, b, r, dy = _mat(90, 60, xt, 1), _mat(60, 70, xt, 2), _vec(70, 3), _mat(90, 70, yt, 4), _mat(90, 70, yt, 5)
+        want, _ = gt.gt_linear_fwd(x, w, b, act=1, r=r)
+        buf = r.clone()
+        got, _ = gt.gt_linear_fwd(x, w, b, act=1, r=buf, out=buf)
+        assert got is buf and torch.equal(got, want)
+        add = _mat(90, 60, xt, 6)
+        want, _, _ = gt.gt_linear_bwd(dy, x, w, dx_add=add)
+        buf = add.clone()
+        got, _, _ = gt.gt_linear_bwd(dy, x, w, dx_add=buf, dx=buf)
+        assert got is buf and torch.equal(got, want)
+
+
+def test_same_result_every_time(gt):
+    for m, k, n, xt in ((4000, 64, 64, B), (3, 2000, 300, B), (700, 100, 60, F)):
+        x, w, dy = _mat(m, k, xt, 1), _mat(k, n, xt, 2), _mat(m, n, xt, 3)
+        y = gt.gt_linear_fwd(x, w)[0]
+        g = gt.gt_linear_bwd(dy, x, w)
+        for _ in range(3):
+            assert torch.equal(gt.gt_linear_fwd(x, w)[0], y)
+            assert all(torch.equal(a, b) for a, b in zip(gt.gt_linear_bwd(dy, x, w), g))
+
+
+def test_fp32_products_keep_fp32_accuracy(gt):
+    """Values over the range of fp32, cancelling sums and exact cases."""
+    # exact: small whole numbers, whose products and sums are whole
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randint(-2000, 2001, (50, 100), generator=g, device="cuda").float()
+    w = torch.randint(-40, 41, (100, 30), generator=g, device="cuda").float()
+    assert torch.equal(gt.gt_linear_fwd(x, w)[0].double(), x.double() @ w.double())
+    # 24-bit values times powers of two: hi, mid and lo all matter, nothing rounds
+    x = (torch.randint(2 ** 23, 2 ** 24, (40, 64), generator=g, device="cuda").float()
+         * 2.0 ** torch.randint(-40, 41, (40, 1), generator=g, device="cuda"))
+    w = torch.zeros(64, 64, device="cuda")
+    w[torch.arange(64), torch.arange(64).flip(0)] = 2.0 ** torch.randint(-20, 21, (64,), generator=g, device="cuda")
+    assert torch.equal(gt.gt_linear_fwd(x, w)[0].double(), x.double() @ w.double())
+    # the largest finite value is split without overflow
+    x = torch.full((2, 8), torch.finfo(F).max, device="cuda")
+    w = torch.zeros(8, 8, device="cuda")
+    w[3] = 0.5
+    assert torch.equal(gt.gt_linear_fwd(x, w)[0], torch.full((2, 8), torch.finfo(F).max / 2, device="cuda"))
+
+
+@pytest.mark.parametrize("xt,yt", TYPES)
+def test_nonfinite_inputs_stay_in_their_rows(gt, xt, yt):
+    m, k, n = 140, 70, 90
+    x, w, dy = _mat(m, k, xt, 1), _mat(k, n, xt, 2, 0.1), _mat(m, n, yt, 3)
+    x[5, 3] = float("inf")
+    x[130, 69] = float("nan")
+    fine = [i for i in range(m) if i not in (5, 130)]
+    y, _ = gt.gt_linear_fwd(x, w, out_dtype=yt)
+    assert not y[5].isfinite().any() and y[130].isnan().all()
+    R.check({"y": y[fine]}, R.linear_fwd(x[fine], w, None, False, None, yt))
+    dx, dw, db = gt.gt_linear_bwd(dy, x, w)
+    ref = R.linear_bwd(dy, x.nan_to_num(0, 0, 0), w, None, False, None)
+    R.check({"dx": dx, "db": db}, ref)
+    rows = [i for i in range(k) if i not in (3, 69)]
+    R.check({"dw": dw[rows]}, {"dw": tuple(t[rows] for t in ref["dw"])})
+    assert not dw[3].isfinite().any() and dw[69].isnan().all()
+
+
+def test_gelu_over_its_range(gt):
+    """GELU and its slope from -30 to 30 and at the ends, through one-feature products."""
+    a = torch.cat([torch.linspace(-30, 30, 2001), torch.tensor([0.0, -0.0, 1e-30, -1e-30, 1e30, -1e30])]).cuda()[:, None]
+    one = torch.ones(1, 1, device="cuda")
+    y, pre = gt.gt_linear_fwd(a, one, act=gt.GT_ACT_GELU, save_pre=True)
+    assert torch.equal(pre, a)
+    R.check({"y": y}, R.linear_fwd(a, one, None, True, None, F))
+    dx, _, _ = gt.gt_linear_bwd(torch.ones_like(a), a, one, pre=a, act=gt.GT_ACT_GELU, need_dw=False, need_db=False)
+    R.check({"dx": dx}, R.linear_bwd(torch.ones_like(a), a, one, a, True, None))
+
+
+def test_gradient_against_differences(gt):
+    m, k, n = 9, 14, 11
+    x, w, b, dy = _mat(m, k, F, 1), _mat(k, n, F, 2, 0.3), _vec(n, 3), _mat(m, n, F, 4)
+    y, pre = gt.gt_linear_fwd(x, w, b, act=1, save_pre=True)
+    dx, dw, db = (R.d(t) for t in gt.gt_linear_bwd(dy, x, w, pre=pre, act=1))
+    xd, wd, bd, dyd = R.d(x), R.d(w), R.d(b), R.d(dy)
+
+    def loss(x_, w_, b_):
+        a = x_ @ w_ + b_
+        return float((a * R.phi(a) * dyd).sum())
+
+    h = 1e-5
+    for i, j in ((0, 0), (4, 7), (8, 10)):
+        for name, grad, idx in (("x", dx, (i, j)), ("w", dw, (i, j)), ("b", db, (j,))):
+            v = {"x": xd.clone(), "w": wd.clone(), "b": bd.clone()}
+            v[name][idx] += h
+            up = loss(**{s + "_": t for s, t in v.items()})
+            v[name][idx] -= 2 * h
+            down = loss(**{s + "_": t for s, t in v.items()})
+            assert abs((up - down) / (2 * h) - float(grad[idx])) < 1e-5, name
+
+
+def test_streams_and_graph(gt):
+    """On a side stream, two calls at once, and captured once and replayed on new inputs."""
+    m, k, n = 300, 500, 60
+    x, w, b, dy = _mat(m, k, B, 1), _mat(k, n, B, 2, 0.05), _vec(n, 3), _mat(m, n, B, 4)
+
+    def both(stream=None):
+        y, pre = gt.gt_linear_fwd(x, w, b, act=1, save_pre=True, stream=stream)
+        return (y, *gt.gt_linear_bwd(dy, x, w, pre=pre, act=1, stream=stream))
+
+    want = both()
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    for s in sides:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [both(s) for s in sides]
+    for s in sides:
+        torch.cuda.current_stream().wait_stream(s)
+    for g in got:
+        assert all(torch.equal(a, c) for a, c in zip(want, g))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = both()
+    for t, seed in ((x, 11), (dy, 14)):
+        t.copy_(_mat(*t.shape, B, seed))
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, c) for a, c in zip(held, both()))
+
+
+@pytest.mark.parametrize("width,heads,ffn,t", [(128, 8, 320, F), (96, 8, 200, B), (72, 4, 130, F)])
+def test_whole_encoder_layer_at_other_widths(gt, width, heads, ffn, t):
+    """LayerNorm, projections, biased attention and FFN together, forward and backward, against the fp64
+    layer oracle: fp32 to 1e-4 and bf16 products (fp32 residual stream) to 2e-2 relative L2 per tensor, the
+    attention's own tolerances."""
+    import numpy as np
+
+    import gt_inputs as gi
+    from oracle import layer as L
+    from oracle import oracle as O
+    O.build()
+    n, D = 333, 6
+    g = gi.barabasi_albert(n, 3, seed=21)
+    spd = O.spd(n, g.indptr, g.indices, D)
+    p = gi.make_gt_layer_params(width, ffn, D + 2, heads, seed=5)
+    io = gi.make_gt_layer_io(n, width, seed=6)
+    dev = torch.device("cuda")
+    spd_d = torch.zeros((n, gt.spd_ld(n)), dtype=torch.int8)
+    spd_d[:, :n] = torch.from_numpy(spd)
+    spd_d = spd_d.to(dev)
+    P = {s: torch.from_numpy(v).to(dev) for s, v in p.items()}
+    x, dy = torch.from_numpy(io["x"]).to(dev), torch.from_numpy(io["dy"]).to(dev)
+    W = {s: P[s].to(t) for s in ("w_qkv", "w_o", "w_1", "w_2")}
+    cut = [slice(i * width, (i + 1) * width) for i in range(3)]
+    d = width // heads
+
+    u, m1, r1 = gt.gt_layer_norm_fwd(x, P["ln1_g"], P["ln1_b"], out_dtype=t)
+    q, k, v = (gt.gt_linear_fwd(u, W["w_qkv"][:, c], P["b_qkv"][c])[0].view(n, heads, d) for c in cut)
+    o, lse = gt.gt_bias_attn_fwd(q, k, v, spd_d, P["T"])
+    hh, _ = gt.gt_linear_fwd(o.view(n, width), W["w_o"], P["b_o"], r=x)
+    z, m2, r2 = gt.gt_layer_norm_fwd(hh, P["ln2_g"], P["ln2_b"], out_dtype=t)
+    act, pre = gt.gt_linear_fwd(z, W["w_1"], P["b_1"], act=gt.GT_ACT_GELU, save_pre=True)
+    y, _ = gt.gt_linear_fwd(act, W["w_2"], P["b_2"], r=hh)
+
+    gr = {}
+    dact, gr["w_2"], gr["b_2"] = gt.gt_linear_bwd(dy, act, W["w_2"])
+    dz, gr["w_1"], gr["b_1"] = gt.gt_linear_bwd(dact, z, W["w_1"], pre=pre, act=gt.GT_ACT_GELU)
+    dhh, gr["ln2_g"], gr["ln2_b"] = gt.gt_layer_norm_bwd(dz, hh, P["ln2_g"], m2, r2, dres=dy)
+    do, gr["w_o"], gr["b_o"] = gt.gt_linear_bwd(dhh, o.view(n, width), W["w_o"])
+    dq, dk, dv, gr["T"] = gt.gt_bias_attn_bwd(q, k, v, o, do.view(n, heads, d), lse, spd_d, P["T"])
+    dw, db, du = torch.empty_like(W["w_qkv"]), torch.empty_like(P["b_qkv"]), None
+    for c, s in zip(cut, (dq, dk, dv)):
+        du, _, db[c] = gt.gt_linear_bwd(s.view(n, width), u, W["w_qkv"][:, c], dx_add=du, dw=dw[:, c])
+    gr["w_qkv"], gr["b_qkv"] = dw, db
+    gr["x"], gr["ln1_g"], gr["ln1_b"] = gt.gt_layer_norm_bwd(du, x, P["ln1_g"], m1, r1, dres=dhh)
+    gt.gt_check_device_status()
+
+    fw = L.layer_fwd(io["x"], p, spd, heads)
+    ref = L.layer_bwd(io["x"], p, spd, heads, fw, io["dy"])
+    tol = 1e-4 if t == F else 2e-2
+
+    def rel(a, c):
+        a, c = R.d(a).numpy().ravel(), np.asarray(c, np.float64).ravel()
+        return float(np.linalg.norm(a - c) / np.linalg.norm(c))
+
+    errs = {"y": rel(y, fw["y"]), **{s: rel(gr[s], ref[s]) for s in gr}}
+    assert all(e <= tol for e in errs.values()), errs
