@@ -40,31 +40,39 @@ using bf16 = __nv_bfloat16;
 
 // ------------------------------------------------------------------------ GELU
 
-// exp(-a^2 / 2) and the normal CDF at -|a|, which is half of
+// exp(-a^2 / 2) and the normal CDF at -|a|, for two values.  The CDF is half of
 // erfc(|a| / sqrt 2) = t (a1 + a2 t + ... + a5 t^4) exp(-a^2 / 2), t = 1 / (1 + p |a| / sqrt 2),
 // Abramowitz and Stegun 7.1.26: at most 1.5e-7 off, the size of an fp32 rounding of the CDF.
-__device__ __forceinline__ void gauss(float a, float& e, float& tail) {
-    const float z = fabsf(a) * 0.70710678118654752f;
-    const float t = __fdividef(1.0f, fmaf(0.3275911f, z, 1.0f));
-    e = ex2(a * a * (-0.5f * tc::kLog2e));
-    float s = fmaf(t, 1.061405429f, -1.453152027f);
-    s = fmaf(t, s, 1.421413741f);
-    s = fmaf(t, s, -0.284496736f);
-    s = fmaf(t, s, 0.254829592f);
-    tail = 0.5f * t * s * e;
+__device__ __forceinline__ float2 f2(float x) { return make_float2(x, x); }
+
+__device__ __forceinline__ void gauss2(float2 a, float2& e, float2& tail) {
+    const float2 d = __ffma2_rn(make_float2(fabsf(a.x), fabsf(a.y)), f2(0.3275911f * 0.70710678118654752f), f2(1.0f));
+    const float2 t = make_float2(__fdividef(1.0f, d.x), __fdividef(1.0f, d.y));
+    const float2 q = __fmul2_rn(__fmul2_rn(a, a), f2(-0.5f * tc::kLog2e));
+    e = make_float2(ex2(q.x), ex2(q.y));
+    float2 s = __ffma2_rn(t, f2(0.5f * 1.061405429f), f2(0.5f * -1.453152027f));
+    s = __ffma2_rn(t, s, f2(0.5f * 1.421413741f));
+    s = __ffma2_rn(t, s, f2(0.5f * -0.284496736f));
+    s = __ffma2_rn(t, s, f2(0.5f * 0.254829592f));
+    tail = __fmul2_rn(__fmul2_rn(t, s), e);
 }
 
-__device__ __forceinline__ float gelu(float a) {
-    float e, tail;
-    gauss(a, e, tail);
-    return a * (a >= 0.f ? 1.0f - tail : tail);
+__device__ __forceinline__ float2 cdf2(float2 a, float2 tail) {
+    const float2 up = __ffma2_rn(tail, f2(-1.0f), f2(1.0f));
+    return make_float2(a.x >= 0.f ? up.x : tail.x, a.y >= 0.f ? up.y : tail.y);
+}
+
+__device__ __forceinline__ float2 gelu2(float2 a) {
+    float2 e, tail;
+    gauss2(a, e, tail);
+    return __fmul2_rn(a, cdf2(a, tail));
 }
 
 // Phi(a) + a phi(a)
-__device__ __forceinline__ float gelu_grad(float a) {
-    float e, tail;
-    gauss(a, e, tail);
-    return fmaf(a * 0.39894228040143268f, e, a >= 0.f ? 1.0f - tail : tail);
+__device__ __forceinline__ float2 gelu_grad2(float2 a) {
+    float2 e, tail;
+    gauss2(a, e, tail);
+    return __ffma2_rn(__fmul2_rn(a, f2(0.39894228040143268f)), e, cdf2(a, tail));
 }
 
 // -------------------------------------------------- operands in the workspace
@@ -112,7 +120,11 @@ linear_prep(int m, int n, int tx, const TI* __restrict__ src, int64_t lds, bool 
                 float a[8];
                 unpack8(load8(pre + row * ldp + col, n - col, pvec), a);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] *= gelu_grad(a[i]);
+                for (int i = 0; i < 8; i += 2) {
+                    const float2 g = gelu_grad2(make_float2(a[i], a[i + 1]));
+                    v[i] *= g.x;
+                    v[i + 1] *= g.y;
+                }
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) acc[i] += v[i];
@@ -152,55 +164,140 @@ linear_prep(int m, int n, int tx, const TI* __restrict__ src, int64_t lds, bool 
 // ------------------------------------------------------------------ the epilogue
 
 // What becomes of a finished sum: a = acc + bias; pre = a; y = act(a) + r.
-// Any pointer but y may be NULL.
+// Any pointer but y may be NULL.  r has y's type.  The accesses are row_access().
 struct Epi {
     const float* bias;
     const void* r;
     void* y;
     void* pre;
     int64_t ldr, ldy, ldpre;
-    bool gelu_act, y_f32, pre_f32;   // r has y's type
-    bool bvec, rvec, yvec, pvec;     // 16-byte accesses allowed
+    bool gelu_act, y_f32, pre_f32, bvec;
+    int racc, yacc, pacc;
 };
 
-// Columns col .. col + 7 of row `row` (live of them, >= 1); b their biases.
-__device__ __forceinline__ void epi8(const Epi& e, int64_t row, int col, int live, float (&v)[8], const float (&b)[8]) {
+// v[0 .. CW - 1] to p[0 .. live - 1]: whole 32-byte sectors where the rows allow them.
+template <int CW>
+__device__ __forceinline__ void put_row(void* base, int64_t at, bool f32, const float (&v)[CW], int live, int acc) {
+    if (f32) {
+        float* p = static_cast<float*>(base) + at;
+        if (live >= CW && acc == 2) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += b[i];
-    if (e.pre) {
-        if (e.pre_f32) store8(static_cast<float*>(e.pre) + row * e.ldpre + col, v, live, e.pvec);
-        else store8(static_cast<bf16*>(e.pre) + row * e.ldpre + col, v, live, e.pvec);
-    }
-    if (e.gelu_act) {
+            for (int g = 0; g < CW / 8; ++g) {
+                uint32_t w[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = gelu(v[i]);
-    }
-    if (e.r) {
-        float r[8];
-        if (e.y_f32) unpack8(load8(static_cast<const float*>(e.r) + row * e.ldr + col, live, e.rvec), r);
-        else unpack8(load8(static_cast<const bf16*>(e.r) + row * e.ldr + col, live, e.rvec), r);
+                for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[8 * g + i]);
+                stg32(p + 8 * g, w);
+            }
+            return;
+        }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += r[i];
+        for (int g = 0; g < CW / 8; ++g) {
+            float t[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[i] = v[8 * g + i];
+            store8(p + 8 * g, t, live - 8 * g, acc > 0);
+        }
+    } else {
+        bf16* p = static_cast<bf16*>(base) + at;
+        if (CW % 16 == 0 && live >= CW && acc == 2) {
+#pragma unroll
+            for (int g = 0; g < CW / 16; ++g) {
+                uint32_t w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[16 * g + 2 * i], v[16 * g + 2 * i + 1]);
+                stg32(p + 16 * g, w);
+            }
+            return;
+        }
+#pragma unroll
+        for (int g = 0; g < CW / 8; ++g) {
+            float t[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[i] = v[8 * g + i];
+            store8(p + 8 * g, t, live - 8 * g, acc > 0);
+        }
     }
-    if (e.y_f32) store8(static_cast<float*>(e.y) + row * e.ldy + col, v, live, e.yvec);
-    else store8(static_cast<bf16*>(e.y) + row * e.ldy + col, v, live, e.yvec);
 }
 
-__device__ __forceinline__ void epi_bias(const Epi& e, int col, int live, float (&b)[8]) {
-    if (e.bias) unpack8(load8(e.bias + col, live, e.bvec), b);
-    else
+// v[i] += base[at + i]
+template <int CW>
+__device__ __forceinline__ void add_row(const void* base, int64_t at, bool f32, float (&v)[CW], int live, int acc) {
+    if (f32) {
+        const float* p = static_cast<const float*>(base) + at;
+        if (live >= CW && acc == 2) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) b[i] = 0.f;
+            for (int g = 0; g < CW / 8; ++g) {
+                uint32_t w[8];
+                ldg32(p + 8 * g, w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[8 * g + i] += __uint_as_float(w[i]);
+            }
+            return;
+        }
+#pragma unroll
+        for (int g = 0; g < CW / 8; ++g) {
+            float t[8];
+            unpack8(load8(p + 8 * g, live - 8 * g, acc > 0), t);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[8 * g + i] += t[i];
+        }
+    } else {
+        const bf16* p = static_cast<const bf16*>(base) + at;
+        if (CW % 16 == 0 && live >= CW && acc == 2) {
+#pragma unroll
+            for (int g = 0; g < CW / 16; ++g) {
+                uint32_t w[8];
+                ldg32(p + 16 * g, w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    v[16 * g + 2 * i] += __uint_as_float(w[i] << 16);
+                    v[16 * g + 2 * i + 1] += __uint_as_float(w[i] & 0xffff0000u);
+                }
+            }
+            return;
+        }
+#pragma unroll
+        for (int g = 0; g < CW / 8; ++g) {
+            float t[8];
+            unpack8(load8(p + 8 * g, live - 8 * g, acc > 0), t);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[8 * g + i] += t[i];
+        }
+    }
+}
+
+// Columns col .. col + CW - 1 (live of them, >= 1) of row `row`.
+template <int CW>
+__device__ __forceinline__ void epilogue(const Epi& e, int64_t row, int col, int live, float (&v)[CW]) {
+    if (e.bias) {
+#pragma unroll
+        for (int g = 0; g < CW / 8; ++g) {
+            float b[8];
+            unpack8(load8(e.bias + col + 8 * g, live - 8 * g, e.bvec), b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[8 * g + i] += b[i];
+        }
+    }
+    if (e.pre) put_row<CW>(e.pre, row * e.ldpre + col, e.pre_f32, v, live, e.pacc);
+    if (e.gelu_act) {
+#pragma unroll
+        for (int i = 0; i < CW; i += 2) {
+            const float2 y = gelu2(make_float2(v[i], v[i + 1]));
+            v[i] = y.x;
+            v[i + 1] = y.y;
+        }
+    }
+    if (e.r) add_row<CW>(e.r, row * e.ldr + col, e.y_f32, v, live, e.racc);
+    put_row<CW>(e.y, row * e.ldy + col, e.y_f32, v, live, e.yacc);
 }
 
 // ------------------------------------------------------------- the product kernel
 
-constexpr int kBM = 128;         // rows of a tile = TMEM lanes
 constexpr int kBK = 64;          // contraction of a k-block: 128 bytes of bf16, one swizzle row
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;
 constexpr int kGemmThreads = (kEpiWarps + 2) * 32;
 constexpr int kTmaWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
-constexpr int kStageA = kBM * kBK * 2;
+constexpr int kStageA = 128 * kBK * 2;
 
 // The terms of a split product, smallest first: planes of A and of B.
 __device__ __forceinline__ int term_plane_a(int t) { return (0x001120 >> (4 * t)) & 15; }   // 0 2 1 1 0 0
@@ -210,35 +307,40 @@ struct GemmShape {
     int M, N;             // of D
     int kblocks;          // of the contraction
     int terms;            // 1, or 6 for split operands
+    int chunk;            // k-blocks that an accumulator may sum (see linear_gemm)
     int tiles_m, tiles_n;
     int splits;           // of the contraction; split s takes k-blocks [s kblocks / splits, (s + 1) kblocks / splits)
     __host__ __device__ int items() const { return tiles_m * tiles_n * splits; }
     __host__ __device__ int kb_lo(int s) const { return (int)((int64_t)s * kblocks / splits); }
 };
 
-// A work item: tile (m, n) and split s.  Tiles run in groups of 16 tile rows, down the
-// group's column before the next, so that the CTAs of one wave share operands in L2.
+// A work item: tile (m, n) and the k-blocks [lo, hi) of split s.  Tiles run in groups of 8 tile
+// rows, down the group's column before the next, so that the CTAs of one wave share operands in L2.
 struct Item {
-    int m, n, s;
+    int m, n, s, lo, hi;
 };
 __device__ __forceinline__ Item item_of(const GemmShape& g, int i) {
-    constexpr int kGroup = 16;
+    constexpr int kGroup = 8;
     const int tiles = g.tiles_m * g.tiles_n;
     const int s = i / tiles, t = i - s * tiles;
     const int per = kGroup * g.tiles_n;
     const int grp = t / per, w = t - grp * per;
     const int gm = g.tiles_m - grp * kGroup < kGroup ? g.tiles_m - grp * kGroup : kGroup;
-    return Item{grp * kGroup + w % gm, w / gm, s};
+    return Item{grp * kGroup + w % gm, w / gm, s, g.kb_lo(s), g.kb_lo(s + 1)};
 }
 
-template <int BN>
+// CTAS CTAs (one, or a pair of a cluster) make a tile of 128 CTAS x BN.  SUM: an item may have
+// several chunks, whose sums wait in registers (a pair's 64 columns per lane leave room for 16 more).
+template <int CTAS, int BN, bool SUM>
 struct GemmCfg {
-    static constexpr int kStageB = BN * kBK * 2;
+    static constexpr int kBM = 128 * CTAS;
+    static constexpr int kStageB = BN / CTAS * kBK * 2;   // a CTA of a pair holds half of B's columns
     static constexpr int kStage = kStageA + kStageB;
     static constexpr int kStages = 192 * 1024 / kStage;
-    static constexpr int kStaging = kEpiWarps * 32 * 32 * 4;
-    static constexpr int kSmem = kStages * kStage + kStaging + 1024;
+    static constexpr int kSmem = kStages * kStage + 1024;
     static constexpr uint32_t kTmemCols = 2 * BN;
+    static constexpr int kCols = BN / 4;                  // accumulator columns of an epilogue warp
+    static constexpr int kCW = kCols < 32 || (SUM && kCols > 32) ? 16 : 32;   // columns taken out at once
 };
 
 struct GemmBars {
@@ -254,20 +356,25 @@ struct GemmBars {
 // finished sums go through `epi`; else split s stores its sums at
 // part + (s M + row) ldpart.
 //
-// One persistent CTA per SM.  Warp kTmaWarp feeds a ring of stages by TMA, warp
-// kMmaWarp issues the products into one of two TMEM accumulators, and eight warps
-// take the other accumulator out (two per TMEM lane quarter, half of the columns
-// each), through a swizzled 4 KB staging tile per warp that turns a lane's row into
-// row pieces of whole sectors, so the epilogue of a tile runs under the next tile's products.
-template <int BN, bool A_MN, bool B_MN>
+// Persistent: one CTA per SM, or pairs of CTAs, walk the items.  Warp kTmaWarp feeds a ring
+// of stages by TMA, warp kMmaWarp (of the pair's first CTA) issues the products into one of two
+// TMEM accumulators, and sixteen warps take the other accumulator out (four per TMEM lane
+// quarter, a quarter of the columns each), so that a tile's epilogue runs under the next
+// tile's products.  A lane holds a row and stores whole 32-byte sectors of it.
+//
+// The tensor core drops what does not fit when it adds to its fp32 accumulator (measured on
+// all-positive sums: 4.4e-8 of the sum lost per 16-deep step).  So an accumulator takes at most
+// g.chunk k-blocks; the warps that take it out add the chunks up in registers, rounding to nearest.
+template <int CTAS, int BN, bool SUM, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kGemmThreads, 1)
 linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const GemmShape g,
             const Epi epi, float* __restrict__ part, int64_t ldpart, int* status) {
-    using C = GemmCfg<BN>;
+    using C = GemmCfg<CTAS, BN, SUM>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ GemmBars bars;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = CTAS == 2 ? cluster_ctarank() : 0;
     if (threadIdx.x == kTmaWarp * 32) {
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(&bars.full[s], 1);
@@ -275,7 +382,7 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&bars.acc_full[a], 1);
-            mbar_init(&bars.acc_empty[a], kEpiWarps);
+            mbar_init(&bars.acc_empty[a], CTAS * kEpiWarps);
         }
         mbar_init(&bars.fin, 1);
         bars.abort = 0;
@@ -283,47 +390,59 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         tma_prefetch_desc(&map_a);
         tma_prefetch_desc(&map_b);
     }
-    if (warp == kMmaWarp) tmem_alloc(&bars.tmem_base, C::kTmemCols);
+    if (warp == kMmaWarp) {
+        if (CTAS == 2) tmem_alloc_pair(&bars.tmem_base, C::kTmemCols);
+        else tmem_alloc(&bars.tmem_base, C::kTmemCols);
+    }
     tc_fence_before();
     __syncthreads();
+    if (CTAS == 2) cluster_sync();   // both CTAs' barriers exist
     tc_fence_after();
     const uint32_t tbase = bars.tmem_base;
     volatile int* abort_flag = &bars.abort;
-    const int items = g.items();
+    const int items = g.items(), first = blockIdx.x / CTAS, stride = gridDim.x / CTAS;
 
     if (warp == kTmaWarp) {
         if (lane == 0) {
             uint32_t it = 0;
             bool ok = true;
-            for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
+            for (int i = first; ok && i < items; i += stride) {
                 const Item w = item_of(g, i);
-                const int lo = g.kb_lo(w.s), hi = g.kb_lo(w.s + 1);
-                for (int t = 0; ok && t < g.terms; ++t) {
-                    const int pa = g.terms == 1 ? 0 : term_plane_a(t), pb = g.terms == 1 ? 0 : term_plane_b(t);
-                    for (int kb = lo; kb < hi; ++kb, ++it) {
-                        const int st = it % C::kStages;
-                        uint64_t* full = &bars.full[st];
-                        if (it >= (uint32_t)C::kStages &&
-                            !mbar_wait(&bars.empty[st], ((it / C::kStages) - 1) & 1, abort_flag, tc::kWaitNs)) {
-                            ok = false;
-                            break;
-                        }
-                        uint8_t* sa = smem + st * C::kStage;
-                        uint8_t* sb = sa + kStageA;
-                        mbar_arrive_expect_tx(full, C::kStage);
-                        if (A_MN) {
+                const int m0 = w.m * C::kBM + 128 * (int)rank, n0 = w.n * BN + BN / CTAS * (int)rank;
+                for (int c0 = w.lo; ok && c0 < w.hi; c0 += g.chunk) {
+                    const int c1 = c0 + g.chunk < w.hi ? c0 + g.chunk : w.hi;
+                    for (int t = 0; ok && t < g.terms; ++t) {
+                        const int pa = g.terms == 1 ? 0 : term_plane_a(t), pb = g.terms == 1 ? 0 : term_plane_b(t);
+                        for (int kb = c0; kb < c1; ++kb, ++it) {
+                            const int st = it % C::kStages;
+                            if (it >= (uint32_t)C::kStages &&
+                                !mbar_wait(&bars.empty[st], ((it / C::kStages) - 1) & 1, abort_flag, tc::kWaitNs)) {
+                                ok = false;
+                                break;
+                            }
+                            uint8_t* sa = smem + st * C::kStage;
+                            uint8_t* sb = sa + kStageA;
+                            uint64_t* full = &bars.full[st];
+                            // both halves of a pair's stage count on the first CTA's barrier
+                            const uint32_t pair_full = CTAS == 2 ? map_to_rank(full, 0) : 0;
+                            if (rank == 0) mbar_arrive_expect_tx(full, CTAS * C::kStage);
+                            auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y, int z) {
+                                if (CTAS == 2) tma_load_3d_pair(dst, map, x, y, z, pair_full);
+                                else tma_load_3d(dst, map, x, y, z, full);
+                            };
+                            if (A_MN) {
 #pragma unroll
-                            for (int b = 0; b < kBM / 64; ++b)
-                                tma_load_3d(sa + b * 8192, &map_a, w.m * kBM + 64 * b, kb * kBK, pa, full);
-                        } else {
-                            tma_load_3d(sa, &map_a, kb * kBK, w.m * kBM, pa, full);
-                        }
-                        if (B_MN) {
+                                for (int b = 0; b < 2; ++b) load(sa + b * 8192, &map_a, m0 + 64 * b, kb * kBK, pa);
+                            } else {
+                                load(sa, &map_a, kb * kBK, m0, pa);
+                            }
+                            if (B_MN) {
 #pragma unroll
-                            for (int b = 0; b < BN / 64; ++b)
-                                tma_load_3d(sb + b * 8192, &map_b, w.n * BN + 64 * b, kb * kBK, pb, full);
-                        } else {
-                            tma_load_3d(sb, &map_b, kb * kBK, w.n * BN, pb, full);
+                                for (int b = 0; b < BN / CTAS / 64; ++b)
+                                    load(sb + b * 8192, &map_b, n0 + 64 * b, kb * kBK, pb);
+                            } else {
+                                load(sb, &map_b, kb * kBK, n0, pb);
+                            }
                         }
                     }
                 }
@@ -331,102 +450,120 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             if (!ok) tc::fail(&bars.abort, status);
             // Nothing may still be on its way into shared memory, or to a barrier in it, when the
             // CTA ends: every stage's last load has landed, and, unless a wait gave up, has been
-            // consumed by products that have completed.
+            // consumed by products that have completed.  (A pair's second CTA has no barrier of its
+            // own for its loads; where its wait gave up, they were issued that wait's limit ago.)
             int never = 0;
             for (uint32_t b = it > (uint32_t)C::kStages ? it - C::kStages : 0; b < it; ++b) {
-                mbar_wait(&bars.full[b % C::kStages], (b / C::kStages) & 1, &never, tc::kWaitNs);
+                if (rank == 0) mbar_wait(&bars.full[b % C::kStages], (b / C::kStages) & 1, &never, tc::kWaitNs);
                 if (ok) ok = mbar_wait(&bars.empty[b % C::kStages], (b / C::kStages) & 1, abort_flag, tc::kWaitNs);
             }
         }
     } else if (warp == kMmaWarp) {
-        constexpr uint32_t id = idesc_bf16(kBM, BN, A_MN, B_MN);
-        // along the contraction: 8-row groups 1024 bytes apart, 32 bytes per k-step; along the
-        // row: 64-element blocks 8192 bytes apart, 8-deep groups 1024 bytes apart, 2048 bytes per k-step
-        const SmemDesc da = smem_desc_split(smem_u32(smem), A_MN ? 8192 : 16, 1024, 2);
-        const SmemDesc db = smem_desc_split(smem_u32(smem) + kStageA, B_MN ? 8192 : 16, 1024, 2);
-        uint32_t it = 0, n = 0;
-        bool ok = true;
-        for (int i = blockIdx.x; ok && i < items; i += gridDim.x, ++n) {
-            const Item w = item_of(g, i);
-            const int steps = g.terms * (g.kb_lo(w.s + 1) - g.kb_lo(w.s));
-            const uint32_t a = n & 1, d = tbase + a * BN;
-            if (n >= 2 && !mbar_wait_all(&bars.acc_empty[a], ((n >> 1) - 1) & 1, abort_flag, tc::kWaitNs)) {
-                ok = false;
-                break;
+        if (rank == 0) {
+            constexpr uint32_t id = idesc_bf16(C::kBM, BN, A_MN, B_MN);
+            // along the contraction: 8-row groups 1024 bytes apart, 32 bytes per k-step; along the
+            // row: 64-element blocks 8192 bytes apart, 8-deep groups 1024 bytes apart, 2048 bytes per k-step
+            const SmemDesc da = smem_desc_split(smem_u32(smem), A_MN ? 8192 : 16, 1024, 2);
+            const SmemDesc db = smem_desc_split(smem_u32(smem) + kStageA, B_MN ? 8192 : 16, 1024, 2);
+            uint32_t it = 0, n = 0;
+            bool ok = true;
+            for (int i = first; ok && i < items; i += stride) {
+                const Item w = item_of(g, i);
+                for (int c0 = w.lo; ok && c0 < w.hi; c0 += g.chunk, ++n) {
+                    const int steps = g.terms * (c0 + g.chunk < w.hi ? g.chunk : w.hi - c0);
+                    const uint32_t a = n & 1, d = tbase + a * BN;
+                    if (n >= 2 && !mbar_wait_all(&bars.acc_empty[a], ((n >> 1) - 1) & 1, abort_flag, tc::kWaitNs)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    for (int k = 0; k < steps; ++k, ++it) {
+                        const int st = it % C::kStages;
+                        if (!mbar_wait_all(&bars.full[st], (it / C::kStages) & 1, abort_flag, tc::kWaitNs)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint32_t off = st * C::kStage;
+#pragma unroll
+                            for (int ks = 0; ks < kBK / 16; ++ks) {
+                                const uint64_t ad = desc_at(da, off + (A_MN ? 2048 : 32) * ks);
+                                const uint64_t bd = desc_at(db, off + (B_MN ? 2048 : 32) * ks);
+                                if (CTAS == 2) mma_ss_pair(d, ad, bd, id, k > 0 || ks > 0);
+                                else mma_ss(d, ad, bd, id, k > 0 || ks > 0);
+                            }
+                            if (CTAS == 2) {
+                                mma_commit_pair(&bars.empty[st]);
+                                if (k == steps - 1) mma_commit_pair(&bars.acc_full[a]);
+                            } else {
+                                mma_commit(&bars.empty[st]);
+                                if (k == steps - 1) mma_commit(&bars.acc_full[a]);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                }
             }
-            tc_fence_after();
-            for (int k = 0; k < steps; ++k, ++it) {
-                const int st = it % C::kStages;
-                if (!mbar_wait_all(&bars.full[st], (it / C::kStages) & 1, abort_flag, tc::kWaitNs)) {
+            if (!ok) {
+                if (lane == 0) tc::fail(&bars.abort, status);
+                int never = 0;
+                if (elect_one()) {
+                    if (CTAS == 2) mma_commit_pair(&bars.fin);
+                    else mma_commit(&bars.fin);
+                }
+                __syncwarp();
+                mbar_wait_all(&bars.fin, 0, &never, tc::kWaitNs);
+            }
+        }
+    } else {
+        constexpr int CW = C::kCW, NC = C::kCols / C::kCW;
+        const int q = warp & 3, c0 = (warp >> 2) * C::kCols;
+        const uint32_t tl = tbase + ((uint32_t)(32 * q) << 16) + c0;
+        uint32_t n = 0;
+        bool ok = true;
+        for (int i = first; ok && i < items; i += stride) {
+            const Item w = item_of(g, i);
+            const int64_t row = (int64_t)w.m * C::kBM + 128 * rank + 32 * q + lane;
+            const int col0 = w.n * BN + c0;
+            float sum[SUM ? NC : 1][CW];
+#pragma unroll
+            for (int c = 0; c < (SUM ? NC : 1); ++c)
+#pragma unroll
+                for (int j = 0; j < CW; ++j) sum[c][j] = 0.f;
+            for (int k0 = w.lo; k0 < w.hi; k0 += g.chunk, ++n) {
+                const uint32_t a = n & 1;
+                if (!mbar_wait_all(&bars.acc_full[a], (n >> 1) & 1, abort_flag, tc::kWaitNs)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t off = st * C::kStage;
+                const bool last = k0 + g.chunk >= w.hi;
 #pragma unroll
-                    for (int ks = 0; ks < kBK / 16; ++ks)
-                        mma_ss(d, desc_at(da, off + (A_MN ? 2048 : 32) * ks), desc_at(db, off + (B_MN ? 2048 : 32) * ks),
-                               id, k > 0 || ks > 0);
-                    mma_commit(&bars.empty[st]);
-                    if (k == steps - 1) mma_commit(&bars.acc_full[a]);
-                }
-                __syncwarp();
-            }
-        }
-        if (!ok) {
-            if (lane == 0) tc::fail(&bars.abort, status);
-            int never = 0;
-            if (elect_one()) mma_commit(&bars.fin);
-            __syncwarp();
-            mbar_wait_all(&bars.fin, 0, &never, tc::kWaitNs);
-        }
-    } else {
-        const uint32_t stg = smem_u32(smem + C::kStages * C::kStage) + warp * 4096;
-        const int q = warp & 3, half = warp >> 2;
-        const uint32_t tl = tbase + ((uint32_t)(32 * q) << 16);
-        uint32_t n = 0;
-        bool ok = true;
-        for (int i = blockIdx.x; ok && i < items; i += gridDim.x, ++n) {
-            const Item w = item_of(g, i);
-            const uint32_t a = n & 1;
-            if (!mbar_wait_all(&bars.acc_full[a], (n >> 1) & 1, abort_flag, tc::kWaitNs)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            const int64_t row0 = (int64_t)w.m * kBM + 32 * q;
-#pragma unroll 1
-            for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 32) {
-                uint32_t v[32];
-                tmem_ld_x32(tl + a * BN + c, v);
-                tmem_wait_ld();
-                if (c + 32 == (half + 1) * (BN / 2)) {   // the accumulator is out
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars.acc_empty[a]);
-                }
-                __syncwarp();   // the staging tile has been read
+                for (int c = 0; c < NC; ++c) {
+                    uint32_t v[CW];
+                    if constexpr (CW == 32) tmem_ld_x32(tl + a * BN + c * CW, v);
+                    else tmem_ld_x16(tl + a * BN + c * CW, v);
+                    tmem_wait_ld();
+                    if (c == NC - 1) {   // the accumulator is out
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (CTAS == 2) mbar_arrive_cluster(map_to_rank(&bars.acc_empty[a], 0));
+                            else mbar_arrive(&bars.acc_empty[a]);
+                        }
+                    }
+                    float(&f)[CW] = sum[SUM ? c : 0];
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(stg + lane * 128 + ((j ^ (lane & 7)) << 4)),
-                                 "r"(v[4 * j]), "r"(v[4 * j + 1]), "r"(v[4 * j + 2]), "r"(v[4 * j + 3])
-                                 : "memory");
-                __syncwarp();
-                const int col = w.n * BN + c + 8 * (lane & 3), live = g.N - col;
-                float b[8];
-                if (live > 0 && !part) epi_bias(epi, col, live, b);
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    const int rl = 8 * p + (lane >> 2);
-                    const int64_t row = row0 + rl;
-                    const uint4 u0 = lds_u4(stg + rl * 128 + (((2 * (lane & 3)) ^ (rl & 7)) << 4));
-                    const uint4 u1 = lds_u4(stg + rl * 128 + (((2 * (lane & 3) + 1) ^ (rl & 7)) << 4));
-                    if (row >= g.M || live <= 0) continue;
-                    float f[8] = {__uint_as_float(u0.x), __uint_as_float(u0.y), __uint_as_float(u0.z), __uint_as_float(u0.w),
-                                  __uint_as_float(u1.x), __uint_as_float(u1.y), __uint_as_float(u1.z), __uint_as_float(u1.w)};
-                    if (part) store8(part + ((int64_t)w.s * g.M + row) * ldpart + col, f, 8, true);
-                    else epi8(epi, row, col, live, f, b);
+                    for (int j = 0; j < CW; ++j) f[j] = SUM ? f[j] + __uint_as_float(v[j]) : __uint_as_float(v[j]);
+                    if (!SUM || last) {
+                        const int col = col0 + c * CW, live = g.N - col;
+                        if (row < g.M && live > 0) {
+                            if (part) put_row<CW>(part, ((int64_t)w.s * g.M + row) * ldpart + col, true, f, (live + 7) & ~7, 2);
+                            else epilogue<CW>(epi, row, col, live, f);
+                        }
+                        __syncwarp();
+                    }
                 }
             }
         }
@@ -434,9 +571,11 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     }
     tc_fence_before();
     __syncthreads();
+    if (CTAS == 2) cluster_sync();   // neither CTA's shared memory or barriers are used by the other any more
     if (warp == kMmaWarp) {
         tc_fence_after();
-        tmem_dealloc(tbase, C::kTmemCols);
+        if (CTAS == 2) tmem_dealloc_pair(tbase, C::kTmemCols);
+        else tmem_dealloc(tbase, C::kTmemCols);
     }
 }
 
@@ -448,7 +587,7 @@ linear_join(int m, int n, int splits, const float* __restrict__ part, int64_t ld
     if (idx >= (int64_t)m * per_row) return;
     const int64_t row = idx / per_row;
     const int col = (int)(idx - row * per_row) * 8, live = n - col;
-    float v[8] = {}, b[8];
+    float v[8] = {};
 #pragma unroll 4
     for (int s = 0; s < splits; ++s) {
         float f[8];
@@ -456,8 +595,7 @@ linear_join(int m, int n, int splits, const float* __restrict__ part, int64_t ld
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += f[i];
     }
-    epi_bias(epi, col, live, b);
-    epi8(epi, row, col, live, v, b);
+    epilogue<8>(epi, row, col, live, v);
 }
 
 // -------------------------------------------------------------------------- host
@@ -472,32 +610,38 @@ struct Operand {
 
 int64_t pad8(int64_t n) { return (n + 7) / 8 * 8; }
 
-// Least contraction of a split: 256 (4 k-blocks) bf16.  Splits fill the SMs when
-// the tiles alone do not.
 struct GemmPlan {
     GemmShape g;
-    int bn;
+    int ctas, bn;
 };
 
-GemmPlan plan_gemm(int M, int N, int K, int terms) {
+// k-blocks an accumulator may sum: 256 deep for an fp32 result (2e-7 lost at most), 4096 deep
+// for a bf16 one (1.1e-5, against a rounding of 3.9e-3).
+int chunk_of(bool f32_out) { return f32_out ? 4 : 64; }
+
+// The tile and the splits of the contraction with the least modelled time: waves of k-block steps
+// (microseconds each as measured per tile), and for splits the partial sums' traffic and a second kernel.
+GemmPlan plan_gemm(int M, int N, int K, int terms, bool f32_out) {
     GemmPlan best{};
     double best_us = 1e30;
     const int sms = num_sms();
     const int kb = (K + kBK - 1) / kBK;
-    for (int bn : {256, 128, 64}) {
-        const int tm = (M + kBM - 1) / kBM, tn = (N + bn - 1) / bn;
-        const int64_t tiles = (int64_t)tm * tn;
-        const double us_kb = bn == 256 ? 0.30 : bn == 128 ? 0.17 : 0.11;
+    const struct { int ctas, bn; double us_kb; } tiles[3] = {{2, 256, 0.30}, {1, 128, 0.17}, {1, 64, 0.11}};
+    for (const auto& t : tiles) {
+        const int bm = 128 * t.ctas, units = sms / t.ctas;
+        const int tm = (M + bm - 1) / bm, tn = (N + t.bn - 1) / t.bn;
+        const int64_t n = (int64_t)tm * tn;
         for (int sp = 1; sp <= 128; sp = sp < 8 ? sp + 1 : sp + sp / 4) {
-            if (sp > 1 && (sp * tiles > 2 * sms || kb / sp < (terms == 1 ? 4 : 2))) break;
-            const int64_t waves = (tiles * sp + sms - 1) / sms;
+            if (sp > 1 && (sp * n > 2 * units || kb / sp < (terms == 1 ? 4 : 2))) break;
+            const int64_t waves = (n * sp + units - 1) / units;
             const int64_t steps = (int64_t)((kb + sp - 1) / sp) * terms;
-            double us = waves * steps * us_kb + 3.0 + 0.004 * bn * (waves < 4 ? waves : 4);
+            double us = waves * steps * t.us_kb + 3.0 + 0.004 * t.bn * (waves < 4 ? waves : 4);
             if (sp > 1) us += 3.0 + (double)M * N * (sp + 2) * 4 / 4e6;
             if (us < best_us) {
                 best_us = us;
-                best.g = GemmShape{M, N, kb, terms, tm, tn, sp};
-                best.bn = bn;
+                best.g = GemmShape{M, N, kb, terms, chunk_of(f32_out), tm, tn, sp};
+                best.ctas = t.ctas;
+                best.bn = t.bn;
             }
         }
     }
@@ -508,19 +652,31 @@ size_t part_floats(const GemmPlan& p) {
     return p.g.splits > 1 ? (size_t)p.g.splits * p.g.M * pad8(p.g.N) : 0;
 }
 
-template <int BN, bool A_MN, bool B_MN>
+template <int CTAS, int BN, bool SUM, bool A_MN, bool B_MN>
 int launch_gemm(const GemmPlan& p, const CUtensorMap& ma, const CUtensorMap& mb, const Epi& epi, float* part,
                 cudaStream_t s) {
-    using C = GemmCfg<BN>;
-    auto kern = linear_gemm<BN, A_MN, B_MN>;
+    using C = GemmCfg<CTAS, BN, SUM>;
+    auto kern = linear_gemm<CTAS, BN, SUM, A_MN, B_MN>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
         return GT_ERR_CUDA;
     int* status = device_status_ptr();
     if (!status) return GT_ERR_CUDA;
-    const int sms = num_sms(), items = p.g.items();
+    const int units = num_sms() / CTAS, items = p.g.items();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(CTAS * (items < units ? items : units)));
+    cfg.blockDim = dim3(kGemmThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CTAS;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CTAS == 2 ? 1 : 0;
     LaunchScope ls("linear_gemm", s);
-    kern<<<items < sms ? items : sms, kGemmThreads, C::kSmem, s>>>(ma, mb, p.g, epi, part, pad8(p.g.N), status);
-    return check_launch();
+    return cudaLaunchKernelEx(&cfg, kern, ma, mb, p.g, epi, part, pad8(p.g.N), status) == cudaSuccess ? check_launch()
+                                                                                                      : GT_ERR_CUDA;
 }
 
 // D = A B through the epilogue.  a_mn / b_mn: the operand's rows run along the contraction's
@@ -529,15 +685,17 @@ template <bool A_MN, bool B_MN>
 int run_gemm(const GemmPlan& p, const Operand& a, const Operand& b, const Epi& epi, float* part, cudaStream_t s) {
     CUtensorMap ma, mb;
     const CUtensorMapDataType ty = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    if (!make_map_3d(&ma, a.p, ty, a.planes, a.rows, a.cols, a.plane * 2, a.ld * 2, A_MN ? kBK : kBM, 64,
+    if (!make_map_3d(&ma, a.p, ty, a.planes, a.rows, a.cols, a.plane * 2, a.ld * 2, A_MN ? kBK : 128, 64,
                      CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_map_3d(&mb, b.p, ty, b.planes, b.rows, b.cols, b.plane * 2, b.ld * 2, B_MN ? kBK : p.bn, 64,
+        !make_map_3d(&mb, b.p, ty, b.planes, b.rows, b.cols, b.plane * 2, b.ld * 2, B_MN ? kBK : p.bn / p.ctas, 64,
                      CU_TENSOR_MAP_SWIZZLE_128B))
         return GT_ERR_CUDA;
     float* out = p.g.splits > 1 ? part : nullptr;
-    int rc = p.bn == 256   ? launch_gemm<256, A_MN, B_MN>(p, ma, mb, epi, out, s)
-             : p.bn == 128 ? launch_gemm<128, A_MN, B_MN>(p, ma, mb, epi, out, s)
-                           : launch_gemm<64, A_MN, B_MN>(p, ma, mb, epi, out, s);
+    const bool one_chunk = (p.g.kblocks + p.g.splits - 1) / p.g.splits <= p.g.chunk;
+    int rc = p.bn == 256   ? (one_chunk ? launch_gemm<2, 256, false, A_MN, B_MN>(p, ma, mb, epi, out, s)
+                                        : launch_gemm<2, 256, true, A_MN, B_MN>(p, ma, mb, epi, out, s))
+             : p.bn == 128 ? launch_gemm<1, 128, true, A_MN, B_MN>(p, ma, mb, epi, out, s)
+                           : launch_gemm<1, 64, true, A_MN, B_MN>(p, ma, mb, epi, out, s);
     if (rc != GT_OK || !out) return rc;
     const int64_t threads = (int64_t)p.g.M * ((p.g.N + 7) / 8);
     LaunchScope ls("linear_join", s);
@@ -608,12 +766,13 @@ struct FwdBufs {
     bf16 *x, *w;
     float* part;
 };
-size_t fwd_bufs(int dtype, int m, int k, int n, bool pack_x, bool pack_w, void* ws, size_t bytes, FwdBufs* out) {
+size_t fwd_bufs(int dtype, bool y_f32, int m, int k, int n, bool pack_x, bool pack_w, void* ws, size_t bytes,
+                FwdBufs* out) {
     Carve c(ws, bytes);
     FwdBufs b;
     b.x = pack_x ? c.take<bf16>(operand_elems(dtype, m, k)) : nullptr;
     b.w = pack_w ? c.take<bf16>(operand_elems(dtype, k, n)) : nullptr;
-    b.part = c.take<float>(part_floats(plan_gemm(m, n, k, terms_of(dtype))));
+    b.part = c.take<float>(part_floats(plan_gemm(m, n, k, terms_of(dtype), y_f32)));
     if (out) *out = b;
     return c.off;
 }
@@ -631,8 +790,8 @@ size_t bwd_bufs(int dtype, int m, int k, int n, bool pack_x, bool pack_w, bool o
     b.x = pack_x ? c.take<bf16>(operand_elems(dtype, m, k)) : nullptr;
     b.w = pack_w ? c.take<bf16>(operand_elems(dtype, k, n)) : nullptr;
     b.da = own_da ? c.take<bf16>(operand_elems(dtype, m, n)) : nullptr;
-    const size_t px = part_floats(plan_gemm(m, k, n, terms_of(dtype)));
-    const size_t pw = part_floats(plan_gemm(k, n, m, terms_of(dtype)));
+    const size_t px = part_floats(plan_gemm(m, k, n, terms_of(dtype), dtype == GT_F32));
+    const size_t pw = part_floats(plan_gemm(k, n, m, terms_of(dtype), dtype == GT_F32));
     b.part = c.take<float>(px > pw ? px : pw);
     b.cols = c.take<float>((size_t)prep_grid(m, n).gy * n);
     if (out) *out = b;
@@ -650,7 +809,7 @@ size_t gt_linear_fwd_workspace_size(int32_t dtype, int32_t m, int32_t k, int32_t
     using namespace gt;
     if (check_linear(dtype, GT_F32, m, k, n, GT_ACT_NONE) != GT_OK) return 0;
     const bool pack = dtype == GT_F32 || !aligned;
-    return fwd_bufs(dtype, m, k, n, pack, pack, nullptr, 0, nullptr) + 256;
+    return fwd_bufs(dtype, false, m, k, n, pack, pack, nullptr, 0, nullptr) + 256;
 }
 
 size_t gt_linear_bwd_workspace_size(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n, int32_t act,
@@ -671,7 +830,7 @@ int gt_linear_fwd(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n,
         return GT_ERR_INVALID_ARG;
     const bool pack_x = dtype == GT_F32 || !rows16(x, ldx, 2), pack_w = dtype == GT_F32 || !rows16(w, ldw, 2);
     FwdBufs bufs;
-    const size_t need = fwd_bufs(dtype, m, k, n, pack_x, pack_w, workspace, ws_bytes, &bufs);
+    const size_t need = fwd_bufs(dtype, ytype == GT_F32, m, k, n, pack_x, pack_w, workspace, ws_bytes, &bufs);
     if (need > 0 && (!workspace || !aligned16(workspace) || ws_bytes < need)) return GT_ERR_WORKSPACE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     Operand ox, ow;
@@ -679,8 +838,8 @@ int gt_linear_fwd(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n,
     if ((rc = make_operand(dtype, k, n, w, ldw, bufs.w, &ow, s)) != GT_OK) return rc;
     const int ey = elem_bytes(ytype), ex = elem_bytes(dtype);
     const Epi epi{b, r, y, pre, ldr, ldy, ldpre, act == GT_ACT_GELU, ytype == GT_F32, dtype == GT_F32,
-                  aligned16(b), r && rows16(r, ldr, ey), rows16(y, ldy, ey), pre && rows16(pre, ldpre, ex)};
-    return run_gemm<false, true>(plan_gemm(m, n, k, terms_of(dtype)), ox, ow, epi, bufs.part, s);
+                  aligned16(b), row_access(r, ldr, ey), row_access(y, ldy, ey), row_access(pre, ldpre, ex)};
+    return run_gemm<false, true>(plan_gemm(m, n, k, terms_of(dtype), ytype == GT_F32), ox, ow, epi, bufs.part, s);
 }
 
 int gt_linear_bwd(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n, const void* dy, int64_t lddy,
@@ -718,15 +877,15 @@ int gt_linear_bwd(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n,
     if (dx) {
         if ((rc = make_operand(dtype, k, n, w, ldw, bufs.w, &o, s)) != GT_OK) return rc;
         const Epi epi{nullptr, add, dx, nullptr, ldadd, lddx, 0, false, dtype == GT_F32, false,
-                      false, add && rows16(add, ldadd, ex), rows16(dx, lddx, ex), false};
-        if ((rc = run_gemm<false, false>(plan_gemm(m, k, n, terms_of(dtype)), oda, o, epi, bufs.part, s)) != GT_OK)
+                      false, row_access(add, ldadd, ex), row_access(dx, lddx, ex), 0};
+        if ((rc = run_gemm<false, false>(plan_gemm(m, k, n, terms_of(dtype), dtype == GT_F32), oda, o, epi, bufs.part, s)) != GT_OK)
             return rc;
     }
     if (dw) {
         if ((rc = make_operand(dtype, m, k, x, ldx, bufs.x, &o, s)) != GT_OK) return rc;
         const Epi epi{nullptr, nullptr, dw, nullptr, 0, lddw, 0, false, dtype == GT_F32, false,
-                      false, false, rows16(dw, lddw, ex), false};
-        if ((rc = run_gemm<true, true>(plan_gemm(k, n, m, terms_of(dtype)), o, oda, epi, bufs.part, s)) != GT_OK)
+                      false, 0, row_access(dw, lddw, ex), 0};
+        if ((rc = run_gemm<true, true>(plan_gemm(k, n, m, terms_of(dtype), dtype == GT_F32), o, oda, epi, bufs.part, s)) != GT_OK)
             return rc;
     }
     return db ? launch_col_sum("linear_bias_sum", bufs.cols, prep_grid(m, n).gy, n, db, n, nullptr, s) : GT_OK;

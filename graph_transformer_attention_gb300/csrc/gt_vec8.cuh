@@ -18,6 +18,13 @@ inline bool rows16(const void* p, int64_t ld, int elem_bytes) {
     return aligned16(p) && (ld * elem_bytes) % 16 == 0;
 }
 
+// How rows can be moved at column offsets that are multiples of 16 elements: 2 by
+// 32 bytes, 1 by 16, 0 by single elements.
+inline int row_access(const void* p, int64_t ld, int elem_bytes) {
+    if (!rows16(p, ld, elem_bytes)) return 0;
+    return (reinterpret_cast<uintptr_t>(p) & 31u) == 0 && (ld * elem_bytes) % 32 == 0 ? 2 : 1;
+}
+
 // Eight elements as stored: 16 bytes of bf16 or 32 of fp32.
 template <typename T> struct Raw8;
 template <> struct Raw8<__nv_bfloat16> { uint4 a; };
@@ -88,6 +95,20 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8], in
         for (int i = 0; i < 8; ++i)
             if (i < live) p[i] = __float2bfloat16_rn(v[i]);
     }
+}
+
+// 32 bytes at once (32-byte aligned).
+__device__ __forceinline__ void ldg32(const void* p, uint32_t (&w)[8]) {
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p)
+                 : "memory");
+}
+
+__device__ __forceinline__ void stg32(void* p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
 }
 
 // Column sums of part [rows][cols] in a fixed order: column c of the first
