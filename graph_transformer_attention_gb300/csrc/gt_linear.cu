@@ -40,39 +40,43 @@ using bf16 = __nv_bfloat16;
 
 // ------------------------------------------------------------------------ GELU
 
-// exp(-a^2 / 2) and the normal CDF at -|a|, for two values.  The CDF is half of
+// For two values: e = exp(-a^2 / 2) and u = 1/2 - (the normal CDF at -|a|).  That CDF is half of
 // erfc(|a| / sqrt 2) = t (a1 + a2 t + ... + a5 t^4) exp(-a^2 / 2), t = 1 / (1 + p |a| / sqrt 2),
 // Abramowitz and Stegun 7.1.26: at most 1.5e-7 off, the size of an fp32 rounding of the CDF.
 __device__ __forceinline__ float2 f2(float x) { return make_float2(x, x); }
 
-__device__ __forceinline__ void gauss2(float2 a, float2& e, float2& tail) {
-    const float2 d = __ffma2_rn(make_float2(fabsf(a.x), fabsf(a.y)), f2(0.3275911f * 0.70710678118654752f), f2(1.0f));
-    const float2 t = make_float2(__fdividef(1.0f, d.x), __fdividef(1.0f, d.y));
-    const float2 q = __fmul2_rn(__fmul2_rn(a, a), f2(-0.5f * tc::kLog2e));
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void gauss2(float2 a, float2 mag, float2& e, float2& u) {
+    const float2 d = __ffma2_rn(mag, f2(0.3275911f * 0.70710678118654752f), f2(1.0f));
+    const float2 t = make_float2(rcp(d.x), rcp(d.y));
+    const float2 q = __fmul2_rn(__fmul2_rn(a, f2(-0.5f * tc::kLog2e)), a);
     e = make_float2(ex2(q.x), ex2(q.y));
-    float2 s = __ffma2_rn(t, f2(0.5f * 1.061405429f), f2(0.5f * -1.453152027f));
-    s = __ffma2_rn(t, s, f2(0.5f * 1.421413741f));
-    s = __ffma2_rn(t, s, f2(0.5f * -0.284496736f));
-    s = __ffma2_rn(t, s, f2(0.5f * 0.254829592f));
-    tail = __fmul2_rn(__fmul2_rn(t, s), e);
+    float2 s = __ffma2_rn(t, f2(-0.5f * 1.061405429f), f2(0.5f * 1.453152027f));
+    s = __ffma2_rn(t, s, f2(-0.5f * 1.421413741f));
+    s = __ffma2_rn(t, s, f2(0.5f * 0.284496736f));
+    s = __ffma2_rn(t, s, f2(-0.5f * 0.254829592f));
+    u = __ffma2_rn(__fmul2_rn(t, s), e, f2(0.5f));
 }
 
-__device__ __forceinline__ float2 cdf2(float2 a, float2 tail) {
-    const float2 up = __ffma2_rn(tail, f2(-1.0f), f2(1.0f));
-    return make_float2(a.x >= 0.f ? up.x : tail.x, a.y >= 0.f ? up.y : tail.y);
-}
-
+// a Phi(a) = a / 2 + |a| u
 __device__ __forceinline__ float2 gelu2(float2 a) {
-    float2 e, tail;
-    gauss2(a, e, tail);
-    return __fmul2_rn(a, cdf2(a, tail));
+    const float2 mag = make_float2(fabsf(a.x), fabsf(a.y));
+    float2 e, u;
+    gauss2(a, mag, e, u);
+    return __ffma2_rn(mag, u, __fmul2_rn(a, f2(0.5f)));
 }
 
-// Phi(a) + a phi(a)
+// Phi(a) + a phi(a), Phi(a) = 1/2 + sign(a) u
 __device__ __forceinline__ float2 gelu_grad2(float2 a) {
-    float2 e, tail;
-    gauss2(a, e, tail);
-    return __ffma2_rn(__fmul2_rn(a, f2(0.39894228040143268f)), e, cdf2(a, tail));
+    float2 e, u;
+    gauss2(a, make_float2(fabsf(a.x), fabsf(a.y)), e, u);
+    const float2 su = make_float2(copysignf(u.x, a.x), copysignf(u.y, a.y));
+    return __ffma2_rn(__fmul2_rn(a, f2(0.39894228040143268f)), e, __fadd2_rn(su, f2(0.5f)));
 }
 
 // -------------------------------------------------- operands in the workspace
@@ -111,40 +115,54 @@ linear_prep(int m, int n, int tx, const TI* __restrict__ src, int64_t lds, bool 
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+    using TP = typename std::conditional<PARTS == 3, float, bf16>::type;
+    constexpr int R = PARTS == 3 ? 2 : 4;   // rows in flight per thread
     if (col < n) {
-#pragma unroll 2
-        for (int64_t row = (int64_t)blockIdx.y * ty + ry; row < m; row += (int64_t)gridDim.y * ty) {
-            float v[8];
-            unpack8(load8(src + row * lds + col, n - col, svec), v);
-            if (pre) {
-                float a[8];
-                unpack8(load8(pre + row * ldp + col, n - col, pvec), a);
+        const int64_t step = (int64_t)gridDim.y * ty;
+        for (int64_t row0 = (int64_t)blockIdx.y * ty + ry; row0 < m; row0 += R * step) {
+            Raw8<TI> rs[R];
+            Raw8<TP> rp[R];
 #pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                    const float2 g = gelu_grad2(make_float2(a[i], a[i + 1]));
-                    v[i] *= g.x;
-                    v[i + 1] *= g.y;
-                }
+            for (int k = 0; k < R; ++k) {
+                const int64_t row = row0 + k * step, r = row < m ? row : row0;
+                rs[k] = load8(src + r * lds + col, row < m ? n - col : 0, svec);
+                if (pre) rp[k] = load8(pre + r * ldp + col, row < m ? n - col : 0, pvec);
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] += v[i];
-            if (!dst) continue;
-            if constexpr (PARTS == 1) {
-                store8(dst + row * ldd + col, v, 8, true);
-            } else {
-                uint32_t w[3][4];
+            for (int k = 0; k < R; ++k) {
+                const int64_t row = row0 + k * step;
+                float v[8];
+                unpack8(rs[k], v);
+                if (pre) {
+                    float a[8];
+                    unpack8(rp[k], a);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t h0, m0, l0, h1, m1, l1;
-                    split3(v[2 * i], h0, m0, l0);
-                    split3(v[2 * i + 1], h1, m1, l1);
-                    w[0][i] = h0 | (h1 << 16);
-                    w[1][i] = m0 | (m1 << 16);
-                    w[2][i] = l0 | (l1 << 16);
+                    for (int i = 0; i < 8; i += 2) {
+                        const float2 g = gelu_grad2(make_float2(a[i], a[i + 1]));
+                        v[i] *= g.x;
+                        v[i + 1] *= g.y;
+                    }
                 }
 #pragma unroll
-                for (int p = 0; p < 3; ++p)
-                    *reinterpret_cast<uint4*>(dst + p * plane + row * ldd + col) = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+                for (int i = 0; i < 8; ++i) acc[i] += v[i];
+                if (!dst || row >= m) continue;
+                if constexpr (PARTS == 1) {
+                    store8(dst + row * ldd + col, v, 8, true);
+                } else {
+                    uint32_t w[3][4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t h0, m0, l0, h1, m1, l1;
+                        split3(v[2 * i], h0, m0, l0);
+                        split3(v[2 * i + 1], h1, m1, l1);
+                        w[0][i] = h0 | (h1 << 16);
+                        w[1][i] = m0 | (m1 << 16);
+                        w[2][i] = l0 | (l1 << 16);
+                    }
+#pragma unroll
+                    for (int p = 0; p < 3; ++p)
+                        *reinterpret_cast<uint4*>(dst + p * plane + row * ldd + col) = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+                }
             }
         }
     }
@@ -171,7 +189,7 @@ struct Epi {
     void* y;
     void* pre;
     int64_t ldr, ldy, ldpre;
-    bool gelu_act, y_f32, pre_f32, bvec;
+    bool gelu_act, y_f32, pre_f32;
     int racc, yacc, pacc;
 };
 
@@ -266,17 +284,15 @@ __device__ __forceinline__ void add_row(const void* base, int64_t at, bool f32, 
     }
 }
 
-// Columns col .. col + CW - 1 (live of them, >= 1) of row `row`.
+// Columns col .. col + CW - 1 (live of them, >= 1) of row `row`; bias: theirs, in shared memory.
 template <int CW>
-__device__ __forceinline__ void epilogue(const Epi& e, int64_t row, int col, int live, float (&v)[CW]) {
-    if (e.bias) {
+__device__ __forceinline__ void epilogue(const Epi& e, int64_t row, int col, int live, float (&v)[CW], uint32_t bias) {
 #pragma unroll
-        for (int g = 0; g < CW / 8; ++g) {
-            float b[8];
-            unpack8(load8(e.bias + col + 8 * g, live - 8 * g, e.bvec), b);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[8 * g + i] += b[i];
-        }
+    for (int i = 0; i < CW; i += 4) {
+        const uint4 w = lds_u4(bias + 4 * i);
+        const float2 a = __fadd2_rn(make_float2(v[i], v[i + 1]), make_float2(__uint_as_float(w.x), __uint_as_float(w.y)));
+        const float2 b = __fadd2_rn(make_float2(v[i + 2], v[i + 3]), make_float2(__uint_as_float(w.z), __uint_as_float(w.w)));
+        v[i] = a.x; v[i + 1] = a.y; v[i + 2] = b.x; v[i + 3] = b.y;
     }
     if (e.pre) put_row<CW>(e.pre, row * e.ldpre + col, e.pre_f32, v, live, e.pacc);
     if (e.gelu_act) {
@@ -373,6 +389,7 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ GemmBars bars;
+    __shared__ alignas(16) float bias_s[kEpiWarps][BN / 4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CTAS == 2 ? cluster_ctarank() : 0;
     if (threadIdx.x == kTmaWarp * 32) {
@@ -519,13 +536,19 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     } else {
         constexpr int CW = C::kCW, NC = C::kCols / C::kCW;
         const int q = warp & 3, c0 = (warp >> 2) * C::kCols;
-        const uint32_t tl = tbase + ((uint32_t)(32 * q) << 16) + c0;
+        const uint32_t tl = tbase + ((uint32_t)(32 * q) << 16) + c0, bias = smem_u32(bias_s[warp]);
         uint32_t n = 0;
         bool ok = true;
         for (int i = first; ok && i < items; i += stride) {
             const Item w = item_of(g, i);
             const int64_t row = (int64_t)w.m * C::kBM + 128 * rank + 32 * q + lane;
             const int col0 = w.n * BN + c0;
+            // this warp's columns of the bias, fetched while the products run
+            __syncwarp();
+#pragma unroll
+            for (int j = lane; j < C::kCols; j += 32)
+                bias_s[warp][j] = epi.bias && col0 + j < g.N ? __ldg(epi.bias + col0 + j) : 0.f;
+            __syncwarp();
             float sum[SUM ? NC : 1][CW];
 #pragma unroll
             for (int c = 0; c < (SUM ? NC : 1); ++c)
@@ -539,8 +562,9 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                 }
                 tc_fence_after();
                 const bool last = k0 + g.chunk >= w.hi;
-#pragma unroll
+#pragma unroll(SUM ? NC : 1)
                 for (int c = 0; c < NC; ++c) {
+                    const int col = col0 + c * CW, live = g.N - col;
                     uint32_t v[CW];
                     if constexpr (CW == 32) tmem_ld_x32(tl + a * BN + c * CW, v);
                     else tmem_ld_x16(tl + a * BN + c * CW, v);
@@ -549,18 +573,17 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) {
-                            if (CTAS == 2) mbar_arrive_cluster(map_to_rank(&bars.acc_empty[a], 0));
-                            else mbar_arrive(&bars.acc_empty[a]);
+                            if (CTAS == 2) mbar_arrive_relaxed_cluster(map_to_rank(&bars.acc_empty[a], 0));
+                            else mbar_arrive_relaxed(&bars.acc_empty[a]);
                         }
                     }
                     float(&f)[CW] = sum[SUM ? c : 0];
 #pragma unroll
                     for (int j = 0; j < CW; ++j) f[j] = SUM ? f[j] + __uint_as_float(v[j]) : __uint_as_float(v[j]);
                     if (!SUM || last) {
-                        const int col = col0 + c * CW, live = g.N - col;
                         if (row < g.M && live > 0) {
                             if (part) put_row<CW>(part, ((int64_t)w.s * g.M + row) * ldpart + col, true, f, (live + 7) & ~7, 2);
-                            else epilogue<CW>(epi, row, col, live, f);
+                            else epilogue<CW>(epi, row, col, live, f, bias + 4 * c * CW);
                         }
                         __syncwarp();
                     }
@@ -582,6 +605,7 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
 // The splits' sums added in a fixed order, then the epilogue.  One thread per 8 columns.
 __global__ void __launch_bounds__(256)
 linear_join(int m, int n, int splits, const float* __restrict__ part, int64_t ldpart, const Epi epi) {
+    __shared__ alignas(16) float bias_s[256][8];
     const int per_row = (n + 7) / 8;
     const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (idx >= (int64_t)m * per_row) return;
@@ -595,7 +619,9 @@ linear_join(int m, int n, int splits, const float* __restrict__ part, int64_t ld
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += f[i];
     }
-    epilogue<8>(epi, row, col, live, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) bias_s[threadIdx.x][i] = epi.bias && i < live ? __ldg(epi.bias + col + i) : 0.f;
+    epilogue<8>(epi, row, col, live, v, smem_u32(bias_s[threadIdx.x]));
 }
 
 // -------------------------------------------------------------------------- host
@@ -714,7 +740,7 @@ PrepGrid prep_grid(int m, int n) {
     while (tx < 32 && tx * 8 < n) tx *= 2;
     const int ty = kPrepThreads / tx, gx = (n + 8 * tx - 1) / (8 * tx);
     int64_t gy = ((int64_t)m + ty - 1) / ty;
-    const int64_t most = (8 * (int64_t)num_sms() + gx - 1) / gx;
+    const int64_t most = (4 * (int64_t)num_sms() + gx - 1) / gx;   // four resident CTAs per SM
     if (gy > most) gy = most;
     if (gy > kPrepSlabs) gy = kPrepSlabs;
     return {tx, gx, (int)gy};
@@ -838,7 +864,7 @@ int gt_linear_fwd(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n,
     if ((rc = make_operand(dtype, k, n, w, ldw, bufs.w, &ow, s)) != GT_OK) return rc;
     const int ey = elem_bytes(ytype), ex = elem_bytes(dtype);
     const Epi epi{b, r, y, pre, ldr, ldy, ldpre, act == GT_ACT_GELU, ytype == GT_F32, dtype == GT_F32,
-                  aligned16(b), row_access(r, ldr, ey), row_access(y, ldy, ey), row_access(pre, ldpre, ex)};
+                  row_access(r, ldr, ey), row_access(y, ldy, ey), row_access(pre, ldpre, ex)};
     return run_gemm<false, true>(plan_gemm(m, n, k, terms_of(dtype), ytype == GT_F32), ox, ow, epi, bufs.part, s);
 }
 
@@ -877,14 +903,14 @@ int gt_linear_bwd(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n,
     if (dx) {
         if ((rc = make_operand(dtype, k, n, w, ldw, bufs.w, &o, s)) != GT_OK) return rc;
         const Epi epi{nullptr, add, dx, nullptr, ldadd, lddx, 0, false, dtype == GT_F32, false,
-                      false, row_access(add, ldadd, ex), row_access(dx, lddx, ex), 0};
+                      row_access(add, ldadd, ex), row_access(dx, lddx, ex), 0};
         if ((rc = run_gemm<false, false>(plan_gemm(m, k, n, terms_of(dtype), dtype == GT_F32), oda, o, epi, bufs.part, s)) != GT_OK)
             return rc;
     }
     if (dw) {
         if ((rc = make_operand(dtype, m, k, x, ldx, bufs.x, &o, s)) != GT_OK) return rc;
         const Epi epi{nullptr, nullptr, dw, nullptr, 0, lddw, 0, false, dtype == GT_F32, false,
-                      false, 0, row_access(dw, lddw, ex), 0};
+                      0, row_access(dw, lddw, ex), 0};
         if ((rc = run_gemm<true, true>(plan_gemm(k, n, m, terms_of(dtype), dtype == GT_F32), o, oda, epi, bufs.part, s)) != GT_OK)
             return rc;
     }

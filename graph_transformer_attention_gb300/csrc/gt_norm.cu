@@ -8,11 +8,9 @@
 //
 // Bandwidth is the bound: every element is read once and written once.  A row
 // stays in registers from its load to its store (mean, then centred squares: two
-// passes over registers, one over memory), TPR threads per row and 8 NV
-// consecutive-in-eights elements per thread.  Statistics and sums are fp32.
-// Rows go to threads by width: 8 threads hold rows of up to 64 features (four
-// rows to a warp), a warp rows of up to 1024, a CTA of 256 or 512 threads wider ones.
-// In the backward a thread keeps the gradient sums of its columns in registers
+// passes over registers, one over memory), eight elements to a thread, and a
+// thread has several rows in flight.  Statistics and sums are fp32.
+// In the backward a thread keeps the gradient sums of its eight columns in registers
 // over all its rows; a CTA adds its row groups' sums in shared memory and stores
 // one partial row, and a second kernel adds the partial rows in a fixed order
 // (no atomics: the same result on every run).
@@ -31,159 +29,213 @@ namespace {
 
 constexpr int kNormMaxC = 16384;
 
-// Sum of v over the TPR threads of a row, in each of them.  Row groups wider
-// than a warp are the whole CTA: `red` holds one value per warp, two buffers in
-// turn so that one barrier per sum suffices.
-template <int TPR>
+// Sums of v[i] over the TPR threads of a row group, in each of them.  Row groups wider
+// than a warp pass their warps' sums through `red`, two buffers in turn, so that one
+// barrier of the CTA per sum suffices.
+template <int TPR, int R, int TH>
 struct RowSum {
-    float2* red;   // [2][TPR / 32] (TPR > 32)
+    float2* red;   // [2][TH / 32][R] (TPR > 32)
     int k;
-    __device__ __forceinline__ float2 operator()(float2 v) {
+    __device__ __forceinline__ void operator()(float2 (&v)[R]) {
 #pragma unroll
         for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) {
-            v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-            v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-        }
-        if constexpr (TPR > 32) {
-            float2* b = red + (k & 1) * (TPR / 32);
-            ++k;
-            if ((threadIdx.x & 31) == 0) b[threadIdx.x >> 5] = v;
-            __syncthreads();
-            v = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < TPR / 32; ++w) {
-                v.x += b[w].x;
-                v.y += b[w].y;
+            for (int i = 0; i < R; ++i) {
+                v[i].x += __shfl_xor_sync(0xffffffffu, v[i].x, o);
+                v[i].y += __shfl_xor_sync(0xffffffffu, v[i].y, o);
             }
         }
-        return v;
+        if constexpr (TPR > 32) {
+            constexpr int W = TPR / 32;
+            float2* b = red + (k & 1) * (TH / 32) * R;
+            ++k;
+            const int warp = threadIdx.x >> 5;
+            if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+                for (int i = 0; i < R; ++i) b[warp * R + i] = v[i];
+            }
+            __syncthreads();
+            const float2* g = b + (warp / W) * W * R;
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                v[i] = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    v[i].x += g[w * R + i].x;
+                    v[i].y += g[w * R + i].y;
+                }
+            }
+        }
     }
 };
 
-template <int TPR>
-constexpr int norm_threads() { return TPR > 256 ? TPR : 256; }
+// A layout of rows over threads: TPR threads hold a row, NV eights of elements each (eight t of
+// turn i at column 8 (i TPR + t)); a CTA of TH threads takes R rows per group at a time.
+template <int TPR_, int NV_, int R_>
+struct NormCfg {
+    static constexpr int TPR = TPR_, NV = NV_, R = R_;
+    static constexpr int TH = TPR > 256 ? TPR : 256, RG = TH / TPR, ROWS = RG * R;
+    static constexpr int RED = TPR > 32 ? 2 * (TH / 32) * R : 1;
+};
 
-template <typename TX, typename TY, int TPR, int NV>
-__global__ void __launch_bounds__(norm_threads<TPR>())
+template <typename TX, typename TY, typename C>
+__global__ void __launch_bounds__(C::TH)
 norm_fwd(int64_t n, int c, const TX* __restrict__ x, int64_t ldx, const float* __restrict__ gain,
          const float* __restrict__ shift, float eps, TY* __restrict__ y, int64_t ldy, float* __restrict__ mean,
          float* __restrict__ rstd, bool vec) {
-    constexpr int RG = norm_threads<TPR>() / TPR;
-    __shared__ float2 red[TPR > 32 ? 2 * (TPR / 32) : 1];
-    RowSum<TPR> rowsum{red, 0};
+    constexpr int TPR = C::TPR, NV = C::NV, R = C::R, RG = C::RG;
+    __shared__ float2 red[C::RED];
+    RowSum<TPR, R, C::TH> rowsum{red, 0};
     const int t = threadIdx.x % TPR, g = threadIdx.x / TPR;
     const float inv_c = 1.0f / (float)c;
     // every thread of a CTA makes the same number of turns (the sums' barriers and shuffles)
-    for (int64_t r0 = (int64_t)blockIdx.x * RG; r0 < n; r0 += (int64_t)gridDim.x * RG) {
-        const int64_t row = r0 + g;
-        const bool live = row < n;
-        Raw8<TX> raw[NV];
+    for (int64_t r0 = (int64_t)blockIdx.x * C::ROWS; r0 < n; r0 += (int64_t)gridDim.x * C::ROWS) {
+        Raw8<TX> raw[R][NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int col = (i * TPR + t) * 8;
-            raw[i] = load8(x + (live ? row : 0) * ldx + col, live ? c - col : 0, vec);
-        }
-        float v[NV][8], s = 0.f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            unpack8(raw[i], v[i]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) s += v[i][j];
-        }
-        const float mu = rowsum(make_float2(s, 0.f)).x * inv_c;
-        float q = 0.f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int col = (i * TPR + t) * 8;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[i][j] -= mu;
-                if (col + j < c) q = fmaf(v[i][j], v[i][j], q);
-            }
-        }
-        const float r = 1.0f / sqrtf(rowsum(make_float2(q, 0.f)).x * inv_c + eps);
-        if (live) {
+        for (int k = 0; k < R; ++k) {
+            const int64_t row = r0 + k * RG + g;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int col = (i * TPR + t) * 8;
-                if (col >= c) continue;
-                float gv[8], sv[8];
-                unpack8(load8(gain + col, c - col, vec), gv);
-                unpack8(load8(shift + col, c - col, vec), sv);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] = fmaf(v[i][j] * r, gv[j], sv[j]);
-                store8(y + row * ldy + col, v[i], c - col, vec);
+                raw[k][i] = load8(x + (row < n ? row : 0) * ldx + col, row < n ? c - col : 0, vec);
             }
-            if (t == 0) {
-                mean[row] = mu;
-                rstd[row] = r;
+        }
+        float v[R][NV][8];
+        float2 s[R];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            float a = 0.f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                unpack8(raw[k][i], v[k][i]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) a += v[k][i][j];
+            }
+            s[k] = make_float2(a, 0.f);
+        }
+        rowsum(s);
+        float mu[R];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            mu[k] = s[k].x * inv_c;
+            float q = 0.f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int col = (i * TPR + t) * 8;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    v[k][i][j] -= mu[k];
+                    if (col + j < c) q = fmaf(v[k][i][j], v[k][i][j], q);
+                }
+            }
+            s[k] = make_float2(q, 0.f);
+        }
+        rowsum(s);
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            s[k].x = 1.0f / sqrtf(s[k].x * inv_c + eps);
+            const int64_t row = r0 + k * RG + g;
+            if (t == 0 && row < n) {
+                mean[row] = mu[k];
+                rstd[row] = s[k].x;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int col = (i * TPR + t) * 8;
+            if (col >= c) continue;
+            float gv[8], sv[8];
+            unpack8(load8(gain + col, c - col, vec), gv);
+            unpack8(load8(shift + col, c - col, vec), sv);
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                const int64_t row = r0 + k * RG + g;
+                if (row >= n) continue;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[k][i][j] = fmaf(v[k][i][j] * s[k].x, gv[j], sv[j]);
+                store8(y + row * ldy + col, v[k][i], c - col, vec);
             }
         }
     }
 }
 
-template <typename TX, typename TY, int TPR, int NV>
-__global__ void __launch_bounds__(norm_threads<TPR>())
+template <typename TX, typename TY, typename C>
+__global__ void __launch_bounds__(C::TH, C::TH <= 256 ? 2 : 1)
 norm_bwd(int64_t n, int c, const TY* __restrict__ dy, int64_t lddy, const TX* __restrict__ x, int64_t ldx,
          const float* __restrict__ gain, const float* __restrict__ mean, const float* __restrict__ rstd,
          const TX* __restrict__ dres, int64_t ldr, TX* __restrict__ dx, int64_t lddx, float* __restrict__ part,
          bool vec) {
-    constexpr int TH = norm_threads<TPR>(), RG = TH / TPR;
-    __shared__ float2 red[TPR > 32 ? 2 * (TPR / 32) : 1];
-    RowSum<TPR> rowsum{red, 0};
+    constexpr int TPR = C::TPR, NV = C::NV, R = C::R, RG = C::RG, TH = C::TH;
+    __shared__ float2 red[C::RED];
+    RowSum<TPR, R, TH> rowsum{red, 0};
     const int t = threadIdx.x % TPR, g = threadIdx.x / TPR;
     const float inv_c = 1.0f / (float)c;
-    float ag[NV][8], as[NV][8];
+    float ag[NV][8], as[NV][8], gv[NV][8];
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+        const int col = (i * TPR + t) * 8;
+        unpack8(load8(gain + col, c - col, vec), gv[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) ag[i][j] = as[i][j] = 0.f;
-    for (int64_t r0 = (int64_t)blockIdx.x * RG; r0 < n; r0 += (int64_t)gridDim.x * RG) {
-        const int64_t row = r0 + g, rr = row < n ? row : 0;
-        const bool live = row < n;
-        Raw8<TX> rx[NV];
-        Raw8<TY> rd[NV];
+    }
+    for (int64_t r0 = (int64_t)blockIdx.x * C::ROWS; r0 < n; r0 += (int64_t)gridDim.x * C::ROWS) {
+        Raw8<TX> rx[R][NV], rr[R][NV];
+        Raw8<TY> rd[R][NV];
+        float mu[R], rs[R];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int col = (i * TPR + t) * 8;
-            rx[i] = load8(x + rr * ldx + col, live ? c - col : 0, vec);
-            rd[i] = load8(dy + rr * lddy + col, live ? c - col : 0, vec);
-        }
-        const float mu = mean[rr], r = rstd[rr];
-        float xh[NV][8], d[NV][8], m1 = 0.f, m2 = 0.f;
+        for (int k = 0; k < R; ++k) {
+            const int64_t row = r0 + k * RG + g, ra = row < n ? row : 0;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int col = (i * TPR + t) * 8;
-            float gv[8];
-            unpack8(load8(gain + col, c - col, vec), gv);
-            unpack8(rx[i], xh[i]);
-            unpack8(rd[i], d[i]);
-            // a dead column or row has dy = 0, and its xh must not bring a NaN into the sums
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                xh[i][j] = live && col + j < c ? (xh[i][j] - mu) * r : 0.f;
-                ag[i][j] = fmaf(d[i][j], xh[i][j], ag[i][j]);
-                as[i][j] += d[i][j];
-                d[i][j] *= gv[j];
-                m1 += d[i][j];
-                m2 = fmaf(d[i][j], xh[i][j], m2);
+            for (int i = 0; i < NV; ++i) {
+                const int col = (i * TPR + t) * 8, live = row < n ? c - col : 0;
+                rx[k][i] = load8(x + ra * ldx + col, live, vec);
+                rd[k][i] = load8(dy + ra * lddy + col, live, vec);
+                if (dres) rr[k][i] = load8(dres + ra * ldr + col, live, vec);
             }
+            mu[k] = mean[ra];
+            rs[k] = rstd[ra];
         }
-        const float2 m = rowsum(make_float2(m1, m2));
-        m1 = m.x * inv_c;
-        m2 = m.y * inv_c;
-        if (live) {
+        // xh of element j, zero where the row or the column is dead (there dy is zero, and
+        // its xh must not bring a NaN into the sums)
+        auto xhat = [&](int k, int i, const float (&xv)[8], int j) {
+            return r0 + k * RG + g < n && (i * TPR + t) * 8 + j < c ? (xv[j] - mu[k]) * rs[k] : 0.f;
+        };
+        float2 m[R];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            float m1 = 0.f, m2 = 0.f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float xv[8], d[8];
+                unpack8(rx[k][i], xv);
+                unpack8(rd[k][i], d);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float xh = xhat(k, i, xv, j);
+                    ag[i][j] = fmaf(d[j], xh, ag[i][j]);
+                    as[i][j] += d[j];
+                    const float dg = d[j] * gv[i][j];
+                    m1 += dg;
+                    m2 = fmaf(dg, xh, m2);
+                }
+            }
+            m[k] = make_float2(m1, m2);
+        }
+        rowsum(m);
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int64_t row = r0 + k * RG + g;
+            const float m1 = m[k].x * inv_c, m2 = m[k].y * inv_c;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int col = (i * TPR + t) * 8;
-                if (col >= c) continue;
-                float o[8];
-                if (dres) unpack8(load8(dres + row * ldr + col, c - col, vec), o);
-                else
+                if (row >= n || col >= c) continue;
+                float xv[8], d[8], o[8] = {};
+                unpack8(rx[k][i], xv);
+                unpack8(rd[k][i], d);
+                if (dres) unpack8(rr[k][i], o);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) o[j] = 0.f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = fmaf(r, d[i][j] - m1 - xh[i][j] * m2, o[j]);
+                for (int j = 0; j < 8; ++j) o[j] = fmaf(rs[k], fmaf(d[j], gv[i][j], -m1) - xhat(k, i, xv, j) * m2, o[j]);
                 store8(dx + row * lddx + col, o, c - col, vec);
             }
         }
@@ -219,68 +271,54 @@ norm_bwd(int64_t n, int c, const TY* __restrict__ dy, int64_t lddy, const TX* __
     }
 }
 
-// One CTA per 32 columns: warp w adds partial rows w, w + 8, ... (coalesced along
-// the columns), then warp 0 adds the 8 warp sums.
-__global__ void __launch_bounds__(256) col_sum(const float* __restrict__ part, int rows, int cols,
-                                               float* __restrict__ out0, int split, float* __restrict__ out1) {
-    __shared__ float red[8][33];
+// One CTA per 32 columns: warp w adds partial rows w, w + 32, ... (coalesced along
+// the columns), then warp 0 adds the 32 warp sums.
+constexpr int kColSumThreads = 1024;
+__global__ void __launch_bounds__(kColSumThreads) col_sum(const float* __restrict__ part, int rows, int cols,
+                                                          float* __restrict__ out0, int split, float* __restrict__ out1) {
+    __shared__ float red[kColSumThreads / 32][33];
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int i = blockIdx.x * 32 + tx;
     float acc = 0.f;
     if (i < cols) {
 #pragma unroll 8
-        for (int p = ty; p < rows; p += 8) acc += part[(int64_t)p * cols + i];
+        for (int p = ty; p < rows; p += kColSumThreads / 32) acc += part[(int64_t)p * cols + i];
     }
     red[ty][tx] = acc;
     __syncthreads();
     if (ty == 0 && i < cols) {
         float sum = 0.f;
 #pragma unroll
-        for (int r = 0; r < 8; ++r) sum += red[r][tx];
+        for (int r = 0; r < kColSumThreads / 32; ++r) sum += red[r][tx];
         if (i < split) out0[i] = sum;
         else out1[i - split] = sum;
     }
 }
 
-// Threads per row and eights per thread of rows with c features.
-struct NormShape {
-    int tpr, nv;
-};
-
-NormShape norm_shape(int c) {
-    if (c <= 64) return {8, 1};
-    if (c <= 256) return {32, 1};
-    if (c <= 512) return {32, 2};
-    if (c <= 1024) return {32, 4};
-    if (c <= 2048) return {256, 1};
-    if (c <= 4096) return {512, 1};
-    if (c <= 8192) return {512, 2};
-    return {512, 4};
+// The layout by width: as many threads as eights, rounded up to a power of two, and the rows in
+// flight that the registers hold (rows of fp32 are twice the registers).
+template <bool WIDE, typename F>
+auto norm_dispatch(int c, F&& f) {
+    constexpr int R = WIDE ? 2 : 4;
+    if (c <= 64) return f(NormCfg<8, 1, R>());
+    if (c <= 128) return f(NormCfg<16, 1, R>());
+    if (c <= 256) return f(NormCfg<32, 1, R>());
+    if (c <= 512) return f(NormCfg<64, 1, R>());
+    if (c <= 1024) return f(NormCfg<128, 1, R>());
+    if (c <= 2048) return f(NormCfg<256, 1, R>());
+    if (c <= 4096) return f(NormCfg<512, 1, 2>());
+    if (c <= 8192) return f(NormCfg<1024, 1, 1>());
+    return f(NormCfg<1024, 2, 1>());
 }
 
-int norm_rows_per_cta(int c) {
-    const int tpr = norm_shape(c).tpr;
-    return tpr >= 256 ? 1 : 256 / tpr;
-}
-
-// CTAs of the backward: two resident per SM make one partial row each.
+// CTAs of the backward, each of which makes one partial row: those that are resident at once.
 int norm_bwd_ctas(int64_t n, int c) {
-    const int rg = norm_rows_per_cta(c);
-    const int64_t want = (n + rg - 1) / rg, most = 2 * (int64_t)num_sms();
-    return (int)(want < most ? want : most);
-}
-
-template <typename F>
-int norm_dispatch(int c, F&& f) {
-    const NormShape s = norm_shape(c);
-    if (s.tpr == 8) return f(std::integral_constant<int, 8>(), std::integral_constant<int, 1>());
-    if (s.tpr == 32 && s.nv == 1) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 1>());
-    if (s.tpr == 32 && s.nv == 2) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 2>());
-    if (s.tpr == 32) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 4>());
-    if (s.tpr == 256) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 1>());
-    if (s.nv == 1) return f(std::integral_constant<int, 512>(), std::integral_constant<int, 1>());
-    if (s.nv == 2) return f(std::integral_constant<int, 512>(), std::integral_constant<int, 2>());
-    return f(std::integral_constant<int, 512>(), std::integral_constant<int, 4>());
+    // the row group's fewest rows at a time, so that the size does not depend on the types
+    return norm_dispatch<true>(c, [&](auto cfg) {
+        using C = decltype(cfg);
+        const int64_t want = (n + C::ROWS - 1) / C::ROWS, most = (int64_t)(C::TH <= 256 ? 2 : 1) * num_sms();
+        return (int)(want < most ? want : most);
+    });
 }
 
 bool valid_type(int t) { return t == GT_F32 || t == GT_BF16; }
@@ -289,12 +327,11 @@ template <typename TX, typename TY>
 int run_fwd(int64_t n, int c, const void* x, int64_t ldx, const float* gain, const float* shift, float eps, void* y,
             int64_t ldy, float* mean, float* rstd, cudaStream_t s) {
     const bool vec = rows16(x, ldx, sizeof(TX)) && rows16(y, ldy, sizeof(TY)) && aligned16(gain) && aligned16(shift);
-    return norm_dispatch(c, [&](auto tpr, auto nv) {
-        constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value, TH = norm_threads<TPR>();
-        constexpr int64_t RG = TH / TPR;
-        const int64_t want = (n + RG - 1) / RG, most = 16 * (int64_t)num_sms();
+    return norm_dispatch<sizeof(TX) == 4>(c, [&](auto cfg) {
+        using C = decltype(cfg);
+        const int64_t want = (n + C::ROWS - 1) / C::ROWS, most = 16 * (int64_t)num_sms();
         LaunchScope ls("norm_fwd", s);
-        norm_fwd<TX, TY, TPR, NV><<<(int)(want < most ? want : most), TH, 0, s>>>(
+        norm_fwd<TX, TY, C><<<(int)(want < most ? want : most), C::TH, 0, s>>>(
             n, c, static_cast<const TX*>(x), ldx, gain, shift, eps, static_cast<TY*>(y), ldy, mean, rstd, vec);
         return check_launch();
     });
@@ -306,10 +343,10 @@ int run_bwd(int64_t n, int c, const void* dy, int64_t lddy, const void* x, int64
             cudaStream_t s) {
     const bool vec = rows16(x, ldx, sizeof(TX)) && rows16(dy, lddy, sizeof(TY)) && rows16(dx, lddx, sizeof(TX)) &&
                      (!dres || rows16(dres, ldr, sizeof(TX))) && aligned16(gain);
-    return norm_dispatch(c, [&](auto tpr, auto nv) {
-        constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value, TH = norm_threads<TPR>();
+    return norm_dispatch<sizeof(TX) == 4 || sizeof(TY) == 4>(c, [&](auto cfg) {
+        using C = decltype(cfg);
         LaunchScope ls("norm_bwd", s);
-        norm_bwd<TX, TY, TPR, NV><<<norm_bwd_ctas(n, c), TH, 0, s>>>(
+        norm_bwd<TX, TY, C><<<norm_bwd_ctas(n, c), C::TH, 0, s>>>(
             n, c, static_cast<const TY*>(dy), lddy, static_cast<const TX*>(x), ldx, gain, mean, rstd,
             static_cast<const TX*>(dres), ldr, static_cast<TX*>(dx), lddx, part, vec);
         return check_launch();
@@ -327,7 +364,7 @@ int check_norm(int xt, int yt, int64_t n, int c) {
 int launch_col_sum(const char* name, const float* part, int rows, int cols, float* out0, int split, float* out1,
                    cudaStream_t s) {
     LaunchScope ls(name, s);
-    col_sum<<<(cols + 31) / 32, 256, 0, s>>>(part, rows, cols, out0, split, out1);
+    col_sum<<<(cols + 31) / 32, kColSumThreads, 0, s>>>(part, rows, cols, out0, split, out1);
     return check_launch();
 }
 

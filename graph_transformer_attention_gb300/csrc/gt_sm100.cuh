@@ -304,8 +304,13 @@ __device__ __forceinline__ uint32_t map_to_rank(const void* p, uint32_t rank) {
     return a;
 }
 
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// Arrivals that order nothing but what tcgen05.wait and tcgen05.fence have ordered already (a release
+// would first wait for this thread's global stores).
+__device__ __forceinline__ void mbar_arrive_relaxed(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_relaxed_cluster(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // 3-D tiled load into this CTA's shared memory, bytes counted on a barrier of either CTA of the pair.
