@@ -21,6 +21,7 @@ slice formed per block) with the Graphormer bias b[h][i][j] = T[h][spd[i][j]].
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -375,78 +376,95 @@ def gt_layer_bwd(x, params: dict, spd, T, saved: dict, dy, workspace=None, strea
     return dx, grads, dT
 
 
-class _Scope:
-    """Device and stream of one call: the tensors' device, and `stream` (default: that
-    device's current stream).  What is allocated inside belongs to that stream."""
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
-    def __init__(self, device, stream):
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream of {stream.device} given for tensors on {device}")
-        self.caller = None if stream is None else torch.cuda.current_stream(device)
-        self.stream = stream if stream is not None else torch.cuda.current_stream(device)
-        self.handle = int(self.stream.cuda_stream)
-        self.ctx = (torch.cuda.stream(stream) if stream is not None else
-                    torch.cuda.device(device) if device.index != torch.cuda.current_device() else None)
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
-
-    def lend(self, given, made):
-        """On another stream than the caller's: the caller's tensors stay allocated until the
-        call's work is done, and the results until the caller's stream is done with them."""
-        if self.caller is None or self.caller == self.stream:
-            return
-        for t in given:
-            if t is not None:
-                t.record_stream(self.stream)
+def _elsewhere(call, first, stream, args):
+    """call(*args) on `stream`, or on the device of the tensor `first` where that is not the
+    current one.  On another stream than the caller's, results and workspace belong to that
+    stream, the caller's tensors stay allocated until its work is done, and the results until the
+    caller's stream is done with them."""
+    if not first.is_cuda:
+        raise ValueError("libgt works on CUDA tensors only")
+    if stream is None:
+        with torch.cuda.device(first.device):
+            return call(*args)
+    if stream.device != first.device:
+        raise ValueError(f"stream of {stream.device} given for tensors on {first.device}")
+    caller = torch.cuda.current_stream(first.device)
+    with torch.cuda.stream(stream):
+        made = call(*args)
+    if caller != stream:
+        for t in args:
+            if isinstance(t, torch.Tensor):
+                t.record_stream(stream)
         for t in made:
             if t is not None:
-                t.record_stream(self.caller)
+                t.record_stream(caller)
+    return made
+
+
+def _is_here(t, stream):
+    """Whether t's device is the current one and the call goes to its current stream."""
+    return stream is None and t.is_cuda and t.device.index == _current_device()
 
 
 def _matrix(name, t, rows, cols, dtype, device):
     """Leading dimension of a [rows][cols] matrix with unit column stride."""
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} must be on {device}, a CUDA device")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}][{cols}], got {tuple(t.shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if cols > 1 and t.stride(1) != 1:
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, not {t.device}")
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
         raise ValueError(f"the columns of {name} must be contiguous")
     if rows <= 1:
         return (cols + 7) // 8 * 8       # one row: its stride means nothing
-    if t.stride(0) < cols:
+    if ld < cols:
         raise ValueError(f"the rows of {name} overlap")
-    return t.stride(0)
+    return ld
 
 
 def _vector(name, t, size, device):
-    if t.device != device or t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != size or not t.is_contiguous():
+    if t.shape != (size,) or t.dtype is not torch.float32 or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous fp32 [{size}] on {device}")
+    return t.data_ptr()
 
 
-def _buffer(workspace, nbytes, device):
-    if workspace is None:
-        return _workspace(nbytes, device)
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous on {device}")
-    return workspace
-
-
-def _nbytes(t):
-    return t.numel() * t.element_size()
-
-
-def _is_2d(name, t):
+def _two_dims(name, t):
     if t.dim() != 2:
         raise ValueError(f"{name} must have 2 dimensions, got {t.dim()}")
+    return t.shape
+
+
+def _room(workspace, need, device):
+    """(workspace, address, bytes): the caller's, or a new one of `need` bytes."""
+    if workspace is None:
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), need
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {device}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+@functools.lru_cache(maxsize=4096)
+def _norm_room(device_index, n, c):
+    return int(load_library().gt_layer_norm_workspace_size(n, c))
+
+
+@functools.lru_cache(maxsize=4096)
+def _linear_fwd_room(device_index, dt, m, k, n, aligned):
+    return int(load_library().gt_linear_fwd_workspace_size(dt, m, k, n, aligned))
+
+
+@functools.lru_cache(maxsize=4096)
+def _linear_bwd_room(device_index, dt, yt, m, k, n, act, aligned):
+    return int(load_library().gt_linear_bwd_workspace_size(dt, yt, m, k, n, act, aligned))
 
 
 def gt_layer_norm_workspace_size(n: int, c: int) -> int:
@@ -454,71 +472,74 @@ def gt_layer_norm_workspace_size(n: int, c: int) -> int:
     return int(load_library().gt_layer_norm_workspace_size(n, c))
 
 
+def gt_linear_fwd_workspace_size(dtype: int, m: int, k: int, n: int, aligned: bool = True) -> int:
+    """Workspace bytes of gt_linear_fwd (0: none needed, or sizes that are not supported)."""
+    return int(load_library().gt_linear_fwd_workspace_size(dtype, m, k, n, int(aligned)))
+
+
+def gt_linear_bwd_workspace_size(dtype: int, ytype: int, m: int, k: int, n: int, act: int = GT_ACT_NONE,
+                                 aligned: bool = True) -> int:
+    """Workspace bytes of gt_linear_bwd (0 for sizes that are not supported)."""
+    return int(load_library().gt_linear_bwd_workspace_size(dtype, ytype, m, k, n, act, int(aligned)))
+
+
 def gt_layer_norm_fwd(x, gain, shift, eps: float = 1e-5, out_dtype=None, out=None, mean=None, rstd=None,
                       stream=None):
     """LayerNorm of the rows of x [n][c] (fp32 or bf16): y [n][c] of out_dtype (default:
     x's type), and fp32 mean [n] and rstd [n] for the backward.  gain, shift fp32 [c]."""
-    lib = load_library()
-    _is_2d("x", x)
-    (n, c), dev = x.shape, x.device
-    ldx = _matrix("x", x, n, c, x.dtype, dev)
-    _vector("gain", gain, c, dev)
-    _vector("shift", shift, c, dev)
-    with _Scope(dev, stream) as sc:
-        y = torch.empty((n, c), dtype=out_dtype or x.dtype, device=dev) if out is None else out
-        ldy = _matrix("out", y, n, c, out_dtype or y.dtype, dev)
-        mu = torch.empty(n, dtype=torch.float32, device=dev) if mean is None else mean
-        rs = torch.empty(n, dtype=torch.float32, device=dev) if rstd is None else rstd
-        _vector("mean", mu, n, dev)
-        _vector("rstd", rs, n, dev)
-        _check("gt_layer_norm_fwd", lib.gt_layer_norm_fwd(
-            _dtype_code(x), _dtype_code(y), n, c, x.data_ptr(), ldx, gain.data_ptr(), shift.data_ptr(), float(eps),
-            y.data_ptr(), ldy, mu.data_ptr(), rs.data_ptr(), sc.handle))
-        sc.lend((x, gain, shift), (y, mu, rs))
-    return y, mu, rs
+    if not _is_here(x, stream):
+        return _elsewhere(gt_layer_norm_fwd, x, stream, (x, gain, shift, eps, out_dtype, out, mean, rstd))
+    lib = _lib or load_library()
+    n, c = _two_dims("x", x)
+    xt, dev = x.dtype, x.device
+    yt = out_dtype or (xt if out is None else out.dtype)
+    ldx = _matrix("x", x, n, c, xt, dev)
+    gp, sp = _vector("gain", gain, c, dev), _vector("shift", shift, c, dev)
+    if out is None:
+        out, ldy = torch.empty((n, c), dtype=yt, device=dev), c
+    else:
+        ldy = _matrix("out", out, n, c, yt, dev)
+    if mean is None:
+        mean = torch.empty(n, dtype=torch.float32, device=dev)
+    if rstd is None:
+        rstd = torch.empty(n, dtype=torch.float32, device=dev)
+    rc = lib.gt_layer_norm_fwd(_dtype_code(x), _dtype_code(out), n, c, x.data_ptr(), ldx, gp, sp, eps, out.data_ptr(),
+                               ldy, _vector("mean", mean, n, dev), _vector("rstd", rstd, n, dev),
+                               _raw_stream(dev.index))
+    if rc:
+        raise GtError("gt_layer_norm_fwd", rc)
+    return out, mean, rstd
 
 
 def gt_layer_norm_bwd(dy, x, gain, mean, rstd, dres=None, dx=None, dgain=None, dshift=None, workspace=None,
                       stream=None):
     """LayerNorm backward from dy = dL/dy and the forward's x, mean, rstd: dx [n][c] of x's
     type (+ dres, the gradient that reaches x around the norm), dgain and dshift fp32 [c]."""
-    lib = load_library()
-    _is_2d("x", x)
-    (n, c), dev = x.shape, x.device
-    ldx = _matrix("x", x, n, c, x.dtype, dev)
+    if not _is_here(x, stream):
+        return _elsewhere(gt_layer_norm_bwd, x, stream,
+                          (dy, x, gain, mean, rstd, dres, dx, dgain, dshift, workspace))
+    lib = _lib or load_library()
+    n, c = _two_dims("x", x)
+    xt, dev = x.dtype, x.device
+    ldx = _matrix("x", x, n, c, xt, dev)
     lddy = _matrix("dy", dy, n, c, dy.dtype, dev)
-    ldr = 0 if dres is None else _matrix("dres", dres, n, c, x.dtype, dev)
-    _vector("gain", gain, c, dev)
-    _vector("mean", mean, n, dev)
-    _vector("rstd", rstd, n, dev)
-    with _Scope(dev, stream) as sc:
-        dx = torch.empty((n, c), dtype=x.dtype, device=dev) if dx is None else dx
-        lddx = _matrix("dx", dx, n, c, x.dtype, dev)
-        dgain = torch.empty(c, dtype=torch.float32, device=dev) if dgain is None else dgain
-        dshift = torch.empty(c, dtype=torch.float32, device=dev) if dshift is None else dshift
-        _vector("dgain", dgain, c, dev)
-        _vector("dshift", dshift, c, dev)
-        ws = _buffer(workspace, lib.gt_layer_norm_workspace_size(n, c), dev)
-        _check("gt_layer_norm_bwd", lib.gt_layer_norm_bwd(
-            _dtype_code(x), _dtype_code(dy), n, c, dy.data_ptr(), lddy, x.data_ptr(), ldx, gain.data_ptr(),
-            mean.data_ptr(), rstd.data_ptr(), _ptr(dres), ldr, dx.data_ptr(), lddx, dgain.data_ptr(),
-            dshift.data_ptr(), ws.data_ptr(), _nbytes(ws), sc.handle))
-        sc.lend((dy, x, gain, mean, rstd, dres, workspace), (dx, dgain, dshift))
+    gp, mp, rp = _vector("gain", gain, c, dev), _vector("mean", mean, n, dev), _vector("rstd", rstd, n, dev)
+    ap, lda = (None, 0) if dres is None else (dres.data_ptr(), _matrix("dres", dres, n, c, xt, dev))
+    if dx is None:
+        dx, lddx = torch.empty((n, c), dtype=xt, device=dev), c
+    else:
+        lddx = _matrix("dx", dx, n, c, xt, dev)
+    if dgain is None:
+        dgain = torch.empty(c, dtype=torch.float32, device=dev)
+    if dshift is None:
+        dshift = torch.empty(c, dtype=torch.float32, device=dev)
+    workspace, wp, wn = _room(workspace, _norm_room(dev.index, n, c), dev)
+    rc = lib.gt_layer_norm_bwd(_dtype_code(x), _dtype_code(dy), n, c, dy.data_ptr(), lddy, x.data_ptr(), ldx, gp, mp,
+                               rp, ap, lda, dx.data_ptr(), lddx, _vector("dgain", dgain, c, dev),
+                               _vector("dshift", dshift, c, dev), wp, wn, _raw_stream(dev.index))
+    if rc:
+        raise GtError("gt_layer_norm_bwd", rc)
     return dx, dgain, dshift
-
-
-def _aligned(*pairs):
-    """Whether every (tensor, leading dimension) has a base and a row stride of whole 16 bytes."""
-    return int(all(t.data_ptr() % 16 == 0 and ld * t.element_size() % 16 == 0 for t, ld in pairs))
-
-
-def gt_linear_fwd_workspace_size(dtype: int, m: int, k: int, n: int, aligned: bool = True) -> int:
-    return int(load_library().gt_linear_fwd_workspace_size(dtype, m, k, n, int(aligned)))
-
-
-def gt_linear_bwd_workspace_size(dtype: int, ytype: int, m: int, k: int, n: int, act: int = GT_ACT_NONE,
-                                 aligned: bool = True) -> int:
-    return int(load_library().gt_linear_bwd_workspace_size(dtype, ytype, m, k, n, act, int(aligned)))
 
 
 def gt_linear_fwd(x, w, b=None, act: int = GT_ACT_NONE, r=None, out_dtype=None, save_pre: bool = False, out=None,
@@ -526,32 +547,33 @@ def gt_linear_fwd(x, w, b=None, act: int = GT_ACT_NONE, r=None, out_dtype=None, 
     """y = act(x w + b) + r: x [m][k] and w [k][n] of one type (fp32 or bf16), b fp32 [n], r
     [m][n] of y's type.  Returns (y, pre): y of out_dtype (default: r's type, else x's; fp32
     for fp32 products), pre = x w + b of x's type with save_pre (or given to write to), else None."""
-    lib = load_library()
-    _is_2d("x", x)
-    _is_2d("w", w)
-    (m, k), n, dev = x.shape, w.shape[1], x.device
-    ldx = _matrix("x", x, m, k, x.dtype, dev)
-    ldw = _matrix("w", w, k, n, x.dtype, dev)
-    if b is not None:
-        _vector("b", b, n, dev)
-    yt = out_dtype or (out.dtype if out is not None else r.dtype if r is not None else x.dtype)
-    ldr = 0 if r is None else _matrix("r", r, m, n, yt, dev)
+    if not _is_here(x, stream):
+        return _elsewhere(gt_linear_fwd, x, stream, (x, w, b, act, r, out_dtype, save_pre, out, pre, workspace))
+    lib = _lib or load_library()
+    m, k = _two_dims("x", x)
+    n = _two_dims("w", w)[1]
+    xt, dev = x.dtype, x.device
     dt = _dtype_code(x)
-    with _Scope(dev, stream) as sc:
-        y = torch.empty((m, n), dtype=yt, device=dev) if out is None else out
-        ldy = _matrix("out", y, m, n, yt, dev)
-        a = torch.empty((m, n), dtype=x.dtype, device=dev) if pre is None and save_pre else pre
-        lda = 0 if a is None else _matrix("pre", a, m, n, x.dtype, dev)
-        ws = workspace
-        if ws is None:
-            need = lib.gt_linear_fwd_workspace_size(dt, m, k, n, _aligned((x, ldx), (w, ldw)))
-            ws = _workspace(need, dev)
-        ws = _buffer(ws, 0, dev)
-        _check("gt_linear_fwd", lib.gt_linear_fwd(
-            dt, _dtype_code(y), m, k, n, x.data_ptr(), ldx, w.data_ptr(), ldw, _ptr(b), act, _ptr(r), ldr,
-            y.data_ptr(), ldy, _ptr(a), lda, ws.data_ptr(), _nbytes(ws), sc.handle))
-        sc.lend((x, w, b, r, workspace), (y, a))
-    return y, a
+    ldx, ldw = _matrix("x", x, m, k, xt, dev), _matrix("w", w, k, n, xt, dev)
+    yt = out_dtype or (out.dtype if out is not None else r.dtype if r is not None else xt)
+    bp = None if b is None else _vector("b", b, n, dev)
+    rp, ldr = (None, 0) if r is None else (r.data_ptr(), _matrix("r", r, m, n, yt, dev))
+    if out is None:
+        out, ldy = torch.empty((m, n), dtype=yt, device=dev), n
+    else:
+        ldy = _matrix("out", out, m, n, yt, dev)
+    if pre is None and save_pre:
+        pre = torch.empty((m, n), dtype=xt, device=dev)
+    pp, ldp = (None, 0) if pre is None else (pre.data_ptr(), _matrix("pre", pre, m, n, xt, dev))
+    xp, wp = x.data_ptr(), w.data_ptr()
+    # rows of whole 16 bytes: a multiple of 8 bf16 (fp32 is split in the workspace in any case)
+    aligned = (xp | wp) % 16 == 0 and (ldx | ldw) % 8 == 0
+    workspace, sp, sn = _room(workspace, _linear_fwd_room(dev.index, dt, m, k, n, aligned), dev)
+    rc = lib.gt_linear_fwd(dt, _dtype_code(out), m, k, n, xp, ldx, wp, ldw, bp, act, rp, ldr, out.data_ptr(), ldy, pp,
+                           ldp, sp, sn, _raw_stream(dev.index))
+    if rc:
+        raise GtError("gt_linear_fwd", rc)
+    return out, pre
 
 
 def gt_linear_bwd(dy, x, w, pre=None, act: int = GT_ACT_NONE, dx_add=None, need_dx: bool = True,
@@ -560,36 +582,34 @@ def gt_linear_bwd(dy, x, w, pre=None, act: int = GT_ACT_NONE, dx_add=None, need_
     """Backward of gt_linear_fwd from dy = dL/dy [m][n]: (dx [m][k], dw [k][n], db fp32 [n]), dx
     and dw of x's type, None for those not needed.  pre: the forward's, with GELU.  dx_add
     [m][k]: a gradient that reaches x another way, added to dx."""
-    lib = load_library()
-    _is_2d("x", x)
-    _is_2d("w", w)
-    (m, k), n, dev = x.shape, w.shape[1], x.device
-    ldx = _matrix("x", x, m, k, x.dtype, dev)
-    ldw = _matrix("w", w, k, n, x.dtype, dev)
-    lddy = _matrix("dy", dy, m, n, dy.dtype, dev)
-    lda = 0 if pre is None else _matrix("pre", pre, m, n, x.dtype, dev)
-    ldadd = 0 if dx_add is None else _matrix("dx_add", dx_add, m, k, x.dtype, dev)
+    if not _is_here(x, stream):
+        return _elsewhere(gt_linear_bwd, x, stream, (dy, x, w, pre, act, dx_add, need_dx, need_dw, need_db, dx, dw, db,
+                                                     workspace))
+    lib = _lib or load_library()
+    m, k = _two_dims("x", x)
+    n = _two_dims("w", w)[1]
+    xt, dev = x.dtype, x.device
     dt, yt = _dtype_code(x), _dtype_code(dy)
-    with _Scope(dev, stream) as sc:
-        if need_dx and dx is None:
-            dx = torch.empty((m, k), dtype=x.dtype, device=dev)
-        if need_dw and dw is None:
-            dw = torch.empty((k, n), dtype=x.dtype, device=dev)
-        if need_db and db is None:
-            db = torch.empty(n, dtype=torch.float32, device=dev)
-        lddx = 0 if dx is None else _matrix("dx", dx, m, k, x.dtype, dev)
-        lddw = 0 if dw is None else _matrix("dw", dw, k, n, x.dtype, dev)
-        if db is not None:
-            _vector("db", db, n, dev)
-        ws = workspace
-        if ws is None:
-            need = lib.gt_linear_bwd_workspace_size(dt, yt, m, k, n, act, _aligned((dy, lddy), (x, ldx), (w, ldw)))
-            ws = _workspace(need, dev)
-        ws = _buffer(ws, 0, dev)
-        _check("gt_linear_bwd", lib.gt_linear_bwd(
-            dt, yt, m, k, n, dy.data_ptr(), lddy, x.data_ptr(), ldx, w.data_ptr(), ldw, _ptr(pre), lda, act,
-            _ptr(dx_add), ldadd, _ptr(dx), lddx, _ptr(dw), lddw, _ptr(db), ws.data_ptr(), _nbytes(ws), sc.handle))
-        sc.lend((dy, x, w, pre, dx_add, workspace), (dx, dw, db))
+    ldx, ldw = _matrix("x", x, m, k, xt, dev), _matrix("w", w, k, n, xt, dev)
+    lddy = _matrix("dy", dy, m, n, dy.dtype, dev)
+    pp, ldp = (None, 0) if pre is None else (pre.data_ptr(), _matrix("pre", pre, m, n, xt, dev))
+    ap, lda = (None, 0) if dx_add is None else (dx_add.data_ptr(), _matrix("dx_add", dx_add, m, k, xt, dev))
+    if need_dx and dx is None:
+        dx = torch.empty((m, k), dtype=xt, device=dev)
+    if need_dw and dw is None:
+        dw = torch.empty((k, n), dtype=xt, device=dev)
+    if need_db and db is None:
+        db = torch.empty(n, dtype=torch.float32, device=dev)
+    dxp, lddx = (None, 0) if dx is None else (dx.data_ptr(), _matrix("dx", dx, m, k, xt, dev))
+    dwp, lddw = (None, 0) if dw is None else (dw.data_ptr(), _matrix("dw", dw, k, n, xt, dev))
+    dbp = None if db is None else _vector("db", db, n, dev)
+    xp, wp, dyp = x.data_ptr(), w.data_ptr(), dy.data_ptr()
+    aligned = (xp | wp | dyp) % 16 == 0 and (ldx | ldw | lddy) % 8 == 0
+    workspace, sp, sn = _room(workspace, _linear_bwd_room(dev.index, dt, yt, m, k, n, act, aligned), dev)
+    rc = lib.gt_linear_bwd(dt, yt, m, k, n, dyp, lddy, xp, ldx, wp, ldw, pp, ldp, act, ap, lda, dxp, lddx, dwp, lddw,
+                           dbp, sp, sn, _raw_stream(dev.index))
+    if rc:
+        raise GtError("gt_linear_bwd", rc)
     return dx, dw, db
 
 

@@ -1,6 +1,7 @@
 // gt_common.cuh -- shared host/device helpers of libgt (status codes, launch checks).
 #pragma once
 
+#include <atomic>
 #include <utility>
 
 #include <cuda_runtime.h>
@@ -28,11 +29,27 @@ inline int check_launch() {
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// SMs of the current device (looked up once per device).
 inline int num_sms() {
+    static std::atomic<int> known[64];
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 1;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
-    return sms > 0 ? sms : 1;
+    if (dev >= 0 && dev < 64 && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0) return 1;
+    if (dev >= 0 && dev < 64) known[dev].store(sms, std::memory_order_relaxed);
+    return sms;
+}
+
+// Raises a kernel's limit of dynamic shared memory, once per device: `done` is the kernel's own
+// set of devices.
+inline bool allow_smem(std::atomic<uint64_t>& done, const void* kern, size_t bytes) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t(1) << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return false;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return true;
 }
 
 // Launches `kern` so that it may overlap the kernel before it in the stream

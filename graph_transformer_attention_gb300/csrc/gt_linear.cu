@@ -99,34 +99,49 @@ __device__ __forceinline__ void split3(float v, uint32_t& hi, uint32_t& mid, uin
 
 constexpr int kPrepThreads = 256;
 
-// Rows [m][n] of src, times act'(pre) when pre is given, as PARTS bf16 planes
+// Rows [m][n] of src (fp32 or bf16), times act'(pre) when pre is given, as bf16 planes
 // [m][ldd] (ldd a multiple of 8; columns n .. ldd - 1 zero); dst NULL: none are
-// written.  colsum (NULL: none): the sums of the products over this CTA's rows,
-// before any rounding, in row blockIdx.y of [gridDim.y][n].
-// A CTA takes 8 tx columns and every (gridDim.y ty)-th group of ty rows, tx ty = 256.
+// written.  colsum (NULL: none): the sums of the products over a CTA's rows,
+// before any rounding, in row y of [gy][n].
+// CTA (x, y) of gx gy takes 8 tx columns and every (gy ty)-th group of ty rows, tx ty = 256.
+struct PrepJob {
+    const void* src;
+    const void* pre;   // of the compute type
+    bf16* dst;
+    float* colsum;
+    int64_t lds, ldp, ldd, plane;
+    int m, n, tx, gx, gy;
+    bool f32, svec, pvec;
+};
+constexpr int kPrepJobs = 3;
+struct PrepJobs {
+    PrepJob j[kPrepJobs];
+    int count;
+};
+
+// What a thread has in flight covers the latency: 4 rows of 16 bytes of each input, 2 of 32.
 template <typename TI, int PARTS>
-__global__ void __launch_bounds__(kPrepThreads)
-linear_prep(int m, int n, int tx, const TI* __restrict__ src, int64_t lds, bool svec,
-            const typename std::conditional<PARTS == 3, float, bf16>::type* __restrict__ pre, int64_t ldp, bool pvec,
-            bf16* __restrict__ dst, int64_t ldd, int64_t plane, float* __restrict__ colsum) {
-    const int ty = kPrepThreads / tx;
+__device__ __forceinline__ void prep_rows(const PrepJob& J, int bx, int by) {
+    using TP = typename std::conditional<PARTS == 3, float, bf16>::type;
+    constexpr int R = PARTS == 3 ? 2 : 4;   // rows in flight per thread
+    const TI* src = static_cast<const TI*>(J.src);
+    const TP* pre = static_cast<const TP*>(J.pre);
+    const int m = J.m, n = J.n, tx = J.tx, ty = kPrepThreads / tx;
     const int cx = threadIdx.x % tx, ry = threadIdx.x / tx;
-    const int col = (blockIdx.x * tx + cx) * 8;
+    const int col = (bx * tx + cx) * 8;
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-    using TP = typename std::conditional<PARTS == 3, float, bf16>::type;
-    constexpr int R = PARTS == 3 ? 2 : 4;   // rows in flight per thread
     if (col < n) {
-        const int64_t step = (int64_t)gridDim.y * ty;
-        for (int64_t row0 = (int64_t)blockIdx.y * ty + ry; row0 < m; row0 += R * step) {
+        const int64_t step = (int64_t)J.gy * ty;
+        for (int64_t row0 = (int64_t)by * ty + ry; row0 < m; row0 += R * step) {
             Raw8<TI> rs[R];
             Raw8<TP> rp[R];
 #pragma unroll
             for (int k = 0; k < R; ++k) {
                 const int64_t row = row0 + k * step, r = row < m ? row : row0;
-                rs[k] = load8(src + r * lds + col, row < m ? n - col : 0, svec);
-                if (pre) rp[k] = load8(pre + r * ldp + col, row < m ? n - col : 0, pvec);
+                rs[k] = load8(src + r * J.lds + col, row < m ? n - col : 0, J.svec);
+                if (pre) rp[k] = load8(pre + r * J.ldp + col, row < m ? n - col : 0, J.pvec);
             }
 #pragma unroll
             for (int k = 0; k < R; ++k) {
@@ -145,9 +160,9 @@ linear_prep(int m, int n, int tx, const TI* __restrict__ src, int64_t lds, bool 
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) acc[i] += v[i];
-                if (!dst || row >= m) continue;
+                if (!J.dst || row >= m) continue;
                 if constexpr (PARTS == 1) {
-                    store8(dst + row * ldd + col, v, 8, true);
+                    store8(J.dst + row * J.ldd + col, v, 8, true);
                 } else {
                     uint32_t w[3][4];
 #pragma unroll
@@ -161,21 +176,41 @@ linear_prep(int m, int n, int tx, const TI* __restrict__ src, int64_t lds, bool 
                     }
 #pragma unroll
                     for (int p = 0; p < 3; ++p)
-                        *reinterpret_cast<uint4*>(dst + p * plane + row * ldd + col) = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+                        *reinterpret_cast<uint4*>(J.dst + p * J.plane + row * J.ldd + col) =
+                            make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
                 }
             }
         }
     }
-    if (!colsum) return;
+    if (!J.colsum) return;
     __shared__ float red[kPrepThreads][9];
 #pragma unroll
     for (int i = 0; i < 8; ++i) red[threadIdx.x][i] = acc[i];
     __syncthreads();
     for (int k = threadIdx.x; k < 8 * tx; k += kPrepThreads) {
-        const int c = blockIdx.x * tx * 8 + k;
+        const int c = bx * tx * 8 + k;
         float s = 0.f;
         for (int y = 0; y < ty; ++y) s += red[y * tx + (k >> 3)][k & 7];
-        if (c < n) colsum[(int64_t)blockIdx.y * n + c] = s;
+        if (c < n) J.colsum[(int64_t)by * n + c] = s;
+    }
+}
+
+// One launch prepares all of a call's operands, a range of CTAs each.
+template <int PARTS>
+__global__ void __launch_bounds__(kPrepThreads) linear_prep(const PrepJobs jobs) {
+    pdl_trigger();
+    int b = blockIdx.x, k = 0;
+    while (k + 1 < jobs.count && b >= jobs.j[k].gx * jobs.j[k].gy) {
+        b -= jobs.j[k].gx * jobs.j[k].gy;
+        ++k;
+    }
+    const PrepJob& J = jobs.j[k];
+    const int by = b / J.gx, bx = b - by * J.gx;
+    if constexpr (PARTS == 3) {
+        prep_rows<float, 3>(J, bx, by);
+    } else {
+        if (J.f32) prep_rows<float, 1>(J, bx, by);
+        else prep_rows<bf16, 1>(J, bx, by);
     }
 }
 
@@ -190,6 +225,7 @@ struct Epi {
     void* pre;
     int64_t ldr, ldy, ldpre;
     bool gelu_act, y_f32, pre_f32;
+    bool single;   // some rows can only be reached by single elements
     int racc, yacc, pacc;
 };
 
@@ -307,6 +343,47 @@ __device__ __forceinline__ void epilogue(const Epi& e, int64_t row, int col, int
     put_row<CW>(e.y, row * e.ldy + col, e.y_f32, v, live, e.yacc);
 }
 
+// The same for a whole warp whose lanes hold rows row0 .. row0 + 31 of an M-row result, where some
+// row can only be reached by single elements: blocks of 16 rows x 16 columns pass through the
+// warp's staging tile `stg`, so that the warp's accesses cover 16 consecutive elements of two rows.
+constexpr int kStgPitch = 17;
+constexpr int kStgBytes = 16 * kStgPitch * 4;
+template <int CW>
+__device__ __forceinline__ void epilogue_single(const Epi& e, int64_t row0, int M, int col, int live, float (&v)[CW],
+                                                uint32_t bias, float* stg) {
+    const int lane = threadIdx.x & 31, c = lane & 15;
+#pragma unroll
+    for (int h = 0; h < 2 * (CW / 16); ++h) {
+        __syncwarp();
+        if ((lane >> 4) == (h & 1)) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) stg[c * kStgPitch + i] = v[16 * (h >> 1) + i];
+        }
+        __syncwarp();
+        const int cc = 16 * (h >> 1) + c;
+        const float b = __uint_as_float(lds_u32(bias + 4 * cc));
+#pragma unroll 1
+        for (int p = lane >> 4; p < 16; p += 2) {
+            const int64_t row = row0 + 16 * (h & 1) + p;
+            if (row >= M || cc >= live) break;
+            float a = stg[p * kStgPitch + c] + b;
+            if (e.pre) {
+                const int64_t at = row * e.ldpre + col + cc;
+                if (e.pre_f32) static_cast<float*>(e.pre)[at] = a;
+                else static_cast<bf16*>(e.pre)[at] = __float2bfloat16_rn(a);
+            }
+            if (e.gelu_act) a = gelu2(make_float2(a, a)).x;
+            if (e.r) {
+                const int64_t at = row * e.ldr + col + cc;
+                a += e.y_f32 ? static_cast<const float*>(e.r)[at] : __bfloat162float(static_cast<const bf16*>(e.r)[at]);
+            }
+            const int64_t at = row * e.ldy + col + cc;
+            if (e.y_f32) static_cast<float*>(e.y)[at] = a;
+            else static_cast<bf16*>(e.y)[at] = __float2bfloat16_rn(a);
+        }
+    }
+}
+
 // ------------------------------------------------------------- the product kernel
 
 constexpr int kBK = 64;          // contraction of a k-block: 128 bytes of bf16, one swizzle row
@@ -390,6 +467,7 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ GemmBars bars;
     __shared__ alignas(16) float bias_s[kEpiWarps][BN / 4];
+    __shared__ float stg_s[kEpiWarps][kStgBytes / 4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CTAS == 2 ? cluster_ctarank() : 0;
     if (threadIdx.x == kTmaWarp * 32) {
@@ -417,6 +495,8 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     tc_fence_after();
     const uint32_t tbase = bars.tmem_base;
     volatile int* abort_flag = &bars.abort;
+    pdl_trigger();   // the call's next kernel may start; it waits for this one before it reads
+    pdl_wait();      // the kernels before this one have finished
     const int items = g.items(), first = blockIdx.x / CTAS, stride = gridDim.x / CTAS;
 
     if (warp == kTmaWarp) {
@@ -581,7 +661,9 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
 #pragma unroll
                     for (int j = 0; j < CW; ++j) f[j] = SUM ? f[j] + __uint_as_float(v[j]) : __uint_as_float(v[j]);
                     if (!SUM || last) {
-                        if (row < g.M && live > 0) {
+                        if (epi.single && !part) {
+                            if (live > 0) epilogue_single<CW>(epi, row - lane, g.M, col, live, f, bias + 4 * c * CW, stg_s[warp]);
+                        } else if (row < g.M && live > 0) {
                             if (part) put_row<CW>(part, ((int64_t)w.s * g.M + row) * ldpart + col, true, f, (live + 7) & ~7, 2);
                             else epilogue<CW>(epi, row, col, live, f, bias + 4 * c * CW);
                         }
@@ -602,12 +684,42 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     }
 }
 
-// The splits' sums added in a fixed order, then the epilogue.  One thread per 8 columns.
-__global__ void __launch_bounds__(256)
-linear_join(int m, int n, int splits, const float* __restrict__ part, int64_t ldpart, const Epi epi) {
-    __shared__ alignas(16) float bias_s[256][8];
+// The end of a call in one launch: the splits' sums added in a fixed order, then the epilogue (CTAs
+// below `join`, a thread per 8 columns), and the column sums of the preparation's partial rows (the
+// CTAs from there on, 32 columns each, as col_sum in gt_norm.cu).
+constexpr int kJoinThreads = 256;
+struct ColSum {
+    const float* part;
+    float* out;
+    int rows, cols;
+};
+__global__ void __launch_bounds__(kJoinThreads)
+linear_join(int join, int m, int n, int splits, const float* __restrict__ part, int64_t ldpart, const Epi epi,
+            const ColSum cs) {
+    __shared__ alignas(16) float bias_s[kJoinThreads][8];
+    pdl_trigger();
+    pdl_wait();
+    if ((int)blockIdx.x >= join) {
+        float(&red)[kJoinThreads][8] = bias_s;
+        const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+        const int i = ((int)blockIdx.x - join) * 32 + tx;
+        float acc = 0.f;
+        if (i < cs.cols) {
+#pragma unroll 8
+            for (int p = ty; p < cs.rows; p += kJoinThreads / 32) acc += cs.part[(int64_t)p * cs.cols + i];
+        }
+        red[tx][ty] = acc;
+        __syncthreads();
+        if (ty == 0 && i < cs.cols) {
+            float sum = 0.f;
+#pragma unroll
+            for (int r = 0; r < kJoinThreads / 32; ++r) sum += red[tx][r];
+            cs.out[i] = sum;
+        }
+        return;
+    }
     const int per_row = (n + 7) / 8;
-    const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t idx = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x;
     if (idx >= (int64_t)m * per_row) return;
     const int64_t row = idx / per_row;
     const int col = (int)(idx - row * per_row) * 8, live = n - col;
@@ -615,7 +727,7 @@ linear_join(int m, int n, int splits, const float* __restrict__ part, int64_t ld
 #pragma unroll 4
     for (int s = 0; s < splits; ++s) {
         float f[8];
-        unpack8(load8(part + ((int64_t)s * m + row) * ldpart + col, 8, true), f);
+        unpack8(load8_cg(part + ((int64_t)s * m + row) * ldpart + col), f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += f[i];
     }
@@ -680,11 +792,11 @@ size_t part_floats(const GemmPlan& p) {
 
 template <int CTAS, int BN, bool SUM, bool A_MN, bool B_MN>
 int launch_gemm(const GemmPlan& p, const CUtensorMap& ma, const CUtensorMap& mb, const Epi& epi, float* part,
-                cudaStream_t s) {
+                bool follows, cudaStream_t s) {
     using C = GemmCfg<CTAS, BN, SUM>;
     auto kern = linear_gemm<CTAS, BN, SUM, A_MN, B_MN>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
-        return GT_ERR_CUDA;
+    static std::atomic<uint64_t> allowed;
+    if (!allow_smem(allowed, reinterpret_cast<const void*>(kern), C::kSmem)) return GT_ERR_CUDA;
     int* status = device_status_ptr();
     if (!status) return GT_ERR_CUDA;
     const int units = num_sms() / CTAS, items = p.g.items();
@@ -693,22 +805,26 @@ int launch_gemm(const GemmPlan& p, const CUtensorMap& ma, const CUtensorMap& mb,
     cfg.blockDim = dim3(kGemmThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CTAS;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = follows;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CTAS;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CTAS == 2 ? 1 : 0;
+    cfg.numAttrs = CTAS;
     LaunchScope ls("linear_gemm", s);
     return cudaLaunchKernelEx(&cfg, kern, ma, mb, p.g, epi, part, pad8(p.g.N), status) == cudaSuccess ? check_launch()
                                                                                                       : GT_ERR_CUDA;
 }
 
-// D = A B through the epilogue.  a_mn / b_mn: the operand's rows run along the contraction's
-// index and its columns along D's (stored [contraction][M] or [contraction][N]).
+// D = A B through the epilogue, or its splits' sums to `part`.  A_MN / B_MN: the operand's rows run
+// along the contraction and its columns along D (stored [contraction][M] or [contraction][N]).
+// follows: a kernel of the same call precedes (this one may start while that one ends).
 template <bool A_MN, bool B_MN>
-int run_gemm(const GemmPlan& p, const Operand& a, const Operand& b, const Epi& epi, float* part, cudaStream_t s) {
+int run_gemm(const GemmPlan& p, const Operand& a, const Operand& b, const Epi& epi, float* part, bool follows,
+             cudaStream_t s) {
     CUtensorMap ma, mb;
     const CUtensorMapDataType ty = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     if (!make_map_3d(&ma, a.p, ty, a.planes, a.rows, a.cols, a.plane * 2, a.ld * 2, A_MN ? kBK : 128, 64,
@@ -718,14 +834,23 @@ int run_gemm(const GemmPlan& p, const Operand& a, const Operand& b, const Epi& e
         return GT_ERR_CUDA;
     float* out = p.g.splits > 1 ? part : nullptr;
     const bool one_chunk = (p.g.kblocks + p.g.splits - 1) / p.g.splits <= p.g.chunk;
-    int rc = p.bn == 256   ? (one_chunk ? launch_gemm<2, 256, false, A_MN, B_MN>(p, ma, mb, epi, out, s)
-                                        : launch_gemm<2, 256, true, A_MN, B_MN>(p, ma, mb, epi, out, s))
-             : p.bn == 128 ? launch_gemm<1, 128, true, A_MN, B_MN>(p, ma, mb, epi, out, s)
-                           : launch_gemm<1, 64, true, A_MN, B_MN>(p, ma, mb, epi, out, s);
-    if (rc != GT_OK || !out) return rc;
-    const int64_t threads = (int64_t)p.g.M * ((p.g.N + 7) / 8);
+    return p.bn == 256   ? (one_chunk ? launch_gemm<2, 256, false, A_MN, B_MN>(p, ma, mb, epi, out, follows, s)
+                                      : launch_gemm<2, 256, true, A_MN, B_MN>(p, ma, mb, epi, out, follows, s))
+           : p.bn == 128 ? launch_gemm<1, 128, true, A_MN, B_MN>(p, ma, mb, epi, out, follows, s)
+                         : launch_gemm<1, 64, true, A_MN, B_MN>(p, ma, mb, epi, out, follows, s);
+}
+
+// The join of p's splits (if it has any) and the column sums (if any), in one launch.
+int run_join(const GemmPlan* p, const float* part, const Epi& epi, const ColSum& cs, cudaStream_t s) {
+    const bool join = p && p->g.splits > 1;
+    if (!join && !cs.out) return GT_OK;
+    const int M = join ? p->g.M : 0, N = join ? p->g.N : 0;
+    const int nj = (int)(((int64_t)M * ((N + 7) / 8) + kJoinThreads - 1) / kJoinThreads);
+    const int nc = cs.out ? (cs.cols + 31) / 32 : 0;
     LaunchScope ls("linear_join", s);
-    linear_join<<<(unsigned)((threads + 255) / 256), 256, 0, s>>>(p.g.M, p.g.N, p.g.splits, part, pad8(p.g.N), epi);
+    if (launch_overlapped(linear_join, dim3(nj + nc), dim3(kJoinThreads), 0, s, nj, M, N, join ? p->g.splits : 0, part,
+                          pad8(N), epi, cs) != cudaSuccess)
+        return GT_ERR_CUDA;
     return check_launch();
 }
 
@@ -746,35 +871,47 @@ PrepGrid prep_grid(int m, int n) {
     return {tx, gx, (int)gy};
 }
 
-template <typename TI, int PARTS>
-int run_prep(int m, int n, const void* src, int64_t lds, const void* pre, int64_t ldp, bf16* dst, float* colsum,
-             cudaStream_t s) {
-    using TP = typename std::conditional<PARTS == 3, float, bf16>::type;
-    const PrepGrid pg = prep_grid(m, n);
-    const int64_t ldd = pad8(n);
-    LaunchScope ls("linear_prep", s);
-    linear_prep<TI, PARTS><<<dim3(pg.gx, pg.gy), kPrepThreads, 0, s>>>(
-        m, n, pg.tx, static_cast<const TI*>(src), lds, rows16(src, lds, sizeof(TI)), static_cast<const TP*>(pre), ldp,
-        pre && rows16(pre, ldp, sizeof(TP)), dst, ldd, (int64_t)m * ldd, colsum);
-    return check_launch();
-}
+int elem_bytes(int t) { return t == GT_F32 ? 4 : 2; }
 
-// src [m][n] of the compute type as an operand: read in place when TMA can, else
-// through `buf` (split in three for fp32, copied for bf16).
-int make_operand(int dtype, int m, int n, const void* src, int64_t ld, bf16* buf, Operand* o, cudaStream_t s) {
-    if (!buf) {
-        *o = Operand{static_cast<const bf16*>(src), ld, ld, 1, m, n};
-        return GT_OK;
+// The preparation of a call: its jobs are collected, then launched at once.
+struct Prep {
+    int dtype;
+    PrepJobs jobs{};
+    int ctas = 0;
+
+    // `src` [m][n] of type t, times act'(pre), as operand planes of the compute type in dst; see PrepJob.
+    void add(int t, int m, int n, const void* src, int64_t lds, const void* pre, int64_t ldp, bf16* dst, float* colsum) {
+        const PrepGrid pg = prep_grid(m, n);
+        PrepJob& j = jobs.j[jobs.count++];
+        j.src = src; j.pre = pre; j.dst = dst; j.colsum = colsum;
+        j.lds = lds; j.ldp = ldp; j.ldd = pad8(n); j.plane = m * j.ldd;
+        j.m = m; j.n = n; j.tx = pg.tx; j.gx = pg.gx; j.gy = pg.gy;
+        j.f32 = t == GT_F32;
+        j.svec = rows16(src, lds, elem_bytes(t));
+        j.pvec = pre && rows16(pre, ldp, elem_bytes(dtype));
+        ctas += pg.gx * pg.gy;
     }
-    const int64_t ldd = pad8(n);
-    *o = Operand{buf, ldd, m * ldd, dtype == GT_F32 ? 3 : 1, m, n};
-    return dtype == GT_F32 ? run_prep<float, 3>(m, n, src, ld, nullptr, 0, buf, nullptr, s)
-                           : run_prep<bf16, 1>(m, n, src, ld, nullptr, 0, buf, nullptr, s);
-}
+    // src [m][n] of the compute type as an operand: read in place (buf NULL), or through buf,
+    // split in three for fp32 and copied for bf16.
+    Operand operand(int m, int n, const void* src, int64_t ld, bf16* buf) {
+        if (!buf) return Operand{static_cast<const bf16*>(src), ld, ld, 1, m, n};
+        add(dtype, m, n, src, ld, nullptr, 0, buf, nullptr);
+        return in_planes(m, n, buf);
+    }
+    Operand in_planes(int m, int n, const bf16* buf) const {
+        return Operand{buf, pad8(n), m * pad8(n), dtype == GT_F32 ? 3 : 1, m, n};
+    }
+    int launch(cudaStream_t s) const {
+        if (jobs.count == 0) return GT_OK;
+        LaunchScope ls("linear_prep", s);
+        if (dtype == GT_F32) linear_prep<3><<<ctas, kPrepThreads, 0, s>>>(jobs);
+        else linear_prep<1><<<ctas, kPrepThreads, 0, s>>>(jobs);
+        return check_launch();
+    }
+};
 
 size_t operand_elems(int dtype, int m, int n) { return (size_t)m * pad8(n) * (dtype == GT_F32 ? 3 : 1); }
 
-int elem_bytes(int t) { return t == GT_F32 ? 4 : 2; }
 int terms_of(int dtype) { return dtype == GT_F32 ? 6 : 1; }
 
 constexpr int kMaxWidth = 65536, kMaxRows = 1 << 24;
@@ -824,6 +961,14 @@ size_t bwd_bufs(int dtype, int m, int k, int n, bool pack_x, bool pack_w, bool o
     return c.off;
 }
 
+Epi make_epi(const float* bias, int act, int ytype, int ptype, const void* r, int64_t ldr, int ey, void* y, int64_t ldy,
+             void* pre, int64_t ldpre, int ep) {
+    Epi e{bias, r, y, pre, ldr, ldy, ldpre, act == GT_ACT_GELU, ytype == GT_F32, ptype == GT_F32, false,
+          row_access(r, ldr, ey), row_access(y, ldy, ey), row_access(pre, ldpre, ep)};
+    e.single = e.yacc == 0 || (r && e.racc == 0) || (pre && e.pacc == 0);
+    return e;
+}
+
 bool ranges_ok(const void* p, int64_t ld, int cols) { return !p || ld >= cols; }
 
 }  // namespace
@@ -835,7 +980,7 @@ size_t gt_linear_fwd_workspace_size(int32_t dtype, int32_t m, int32_t k, int32_t
     using namespace gt;
     if (check_linear(dtype, GT_F32, m, k, n, GT_ACT_NONE) != GT_OK) return 0;
     const bool pack = dtype == GT_F32 || !aligned;
-    return fwd_bufs(dtype, false, m, k, n, pack, pack, nullptr, 0, nullptr) + 256;
+    return fwd_bufs(dtype, false, m, k, n, pack, pack, nullptr, 0, nullptr);
 }
 
 size_t gt_linear_bwd_workspace_size(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n, int32_t act,
@@ -843,7 +988,7 @@ size_t gt_linear_bwd_workspace_size(int32_t dtype, int32_t ytype, int32_t m, int
     using namespace gt;
     if (check_linear(dtype, ytype, m, k, n, act) != GT_OK) return 0;
     const bool pack = dtype == GT_F32 || !aligned;
-    return bwd_bufs(dtype, m, k, n, pack, pack, pack || act != GT_ACT_NONE || ytype != dtype, nullptr, 0, nullptr) + 256;
+    return bwd_bufs(dtype, m, k, n, pack, pack, pack || act != GT_ACT_NONE || ytype != dtype, nullptr, 0, nullptr);
 }
 
 int gt_linear_fwd(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n, const void* x, int64_t ldx,
@@ -859,13 +1004,14 @@ int gt_linear_fwd(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n,
     const size_t need = fwd_bufs(dtype, ytype == GT_F32, m, k, n, pack_x, pack_w, workspace, ws_bytes, &bufs);
     if (need > 0 && (!workspace || !aligned16(workspace) || ws_bytes < need)) return GT_ERR_WORKSPACE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    Operand ox, ow;
-    if ((rc = make_operand(dtype, m, k, x, ldx, bufs.x, &ox, s)) != GT_OK) return rc;
-    if ((rc = make_operand(dtype, k, n, w, ldw, bufs.w, &ow, s)) != GT_OK) return rc;
+    Prep prep{dtype};
+    const Operand ox = prep.operand(m, k, x, ldx, bufs.x), ow = prep.operand(k, n, w, ldw, bufs.w);
+    if ((rc = prep.launch(s)) != GT_OK) return rc;
     const int ey = elem_bytes(ytype), ex = elem_bytes(dtype);
-    const Epi epi{b, r, y, pre, ldr, ldy, ldpre, act == GT_ACT_GELU, ytype == GT_F32, dtype == GT_F32,
-                  row_access(r, ldr, ey), row_access(y, ldy, ey), row_access(pre, ldpre, ex)};
-    return run_gemm<false, true>(plan_gemm(m, n, k, terms_of(dtype), ytype == GT_F32), ox, ow, epi, bufs.part, s);
+    const Epi epi = make_epi(b, act, ytype, dtype, r, ldr, ey, y, ldy, pre, ldpre, ex);
+    const GemmPlan plan = plan_gemm(m, n, k, terms_of(dtype), ytype == GT_F32);
+    if ((rc = run_gemm<false, true>(plan, ox, ow, epi, bufs.part, prep.jobs.count > 0, s)) != GT_OK) return rc;
+    return run_join(&plan, bufs.part, epi, ColSum{}, s);
 }
 
 int gt_linear_bwd(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n, const void* dy, int64_t lddy,
@@ -887,34 +1033,33 @@ int gt_linear_bwd(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n,
     const size_t need = bwd_bufs(dtype, m, k, n, pack_x, pack_w, own_da, workspace, ws_bytes, &bufs);
     if (!workspace || !aligned16(workspace) || ws_bytes < need) return GT_ERR_WORKSPACE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // da, and the column sums' partial rows
-    float* cols = db ? bufs.cols : nullptr;
-    if (own_da || db) {
-        rc = dtype == GT_F32   ? run_prep<float, 3>(m, n, dy, lddy, pre, ldpre, bufs.da, cols, s)
-             : ytype == GT_F32 ? run_prep<float, 1>(m, n, dy, lddy, pre, ldpre, bufs.da, cols, s)
-                               : run_prep<bf16, 1>(m, n, dy, lddy, pre, ldpre, bufs.da, cols, s);
-        if (rc != GT_OK) return rc;
-    }
-    const int64_t ldda = own_da ? pad8(n) : lddy;
-    const Operand oda{own_da ? bufs.da : static_cast<const bf16*>(dy), ldda, own_da ? m * ldda : ldda,
-                      dtype == GT_F32 ? 3 : 1, m, n};
+    Prep prep{dtype};
+    Operand oda{static_cast<const bf16*>(dy), lddy, lddy, 1, m, n}, ox{}, ow{};
+    if (own_da || db) prep.add(ytype, m, n, dy, lddy, pre, ldpre, bufs.da, db ? bufs.cols : nullptr);
+    if (own_da) oda = prep.in_planes(m, n, bufs.da);
+    if (dx) ow = prep.operand(k, n, w, ldw, bufs.w);
+    if (dw) ox = prep.operand(m, k, x, ldx, bufs.x);
+    if ((rc = prep.launch(s)) != GT_OK) return rc;
+    bool follows = prep.jobs.count > 0;
     const int ex = elem_bytes(dtype);
-    Operand o;
+    const bool f32 = dtype == GT_F32;
+    ColSum cs{db ? bufs.cols : nullptr, db, prep_grid(m, n).gy, n};
+    Epi epi{};
     if (dx) {
-        if ((rc = make_operand(dtype, k, n, w, ldw, bufs.w, &o, s)) != GT_OK) return rc;
-        const Epi epi{nullptr, add, dx, nullptr, ldadd, lddx, 0, false, dtype == GT_F32, false,
-                      row_access(add, ldadd, ex), row_access(dx, lddx, ex), 0};
-        if ((rc = run_gemm<false, false>(plan_gemm(m, k, n, terms_of(dtype), dtype == GT_F32), oda, o, epi, bufs.part, s)) != GT_OK)
-            return rc;
+        const GemmPlan plan = plan_gemm(m, k, n, terms_of(dtype), f32);
+        epi = make_epi(nullptr, GT_ACT_NONE, dtype, dtype, add, ldadd, ex, dx, lddx, nullptr, 0, ex);
+        if ((rc = run_gemm<false, false>(plan, oda, ow, epi, bufs.part, follows, s)) != GT_OK) return rc;
+        follows = true;
+        // the column sums go with the last join, or with this one if it is the last
+        if ((rc = run_join(&plan, bufs.part, epi, dw ? ColSum{} : cs, s)) != GT_OK) return rc;
     }
     if (dw) {
-        if ((rc = make_operand(dtype, m, k, x, ldx, bufs.x, &o, s)) != GT_OK) return rc;
-        const Epi epi{nullptr, nullptr, dw, nullptr, 0, lddw, 0, false, dtype == GT_F32, false,
-                      0, row_access(dw, lddw, ex), 0};
-        if ((rc = run_gemm<true, true>(plan_gemm(k, n, m, terms_of(dtype), dtype == GT_F32), o, oda, epi, bufs.part, s)) != GT_OK)
-            return rc;
+        const GemmPlan plan = plan_gemm(k, n, m, terms_of(dtype), f32);
+        epi = make_epi(nullptr, GT_ACT_NONE, dtype, dtype, nullptr, 0, ex, dw, lddw, nullptr, 0, ex);
+        if ((rc = run_gemm<true, true>(plan, ox, oda, epi, bufs.part, follows, s)) != GT_OK) return rc;
+        return run_join(&plan, bufs.part, epi, cs, s);
     }
-    return db ? launch_col_sum("linear_bias_sum", bufs.cols, prep_grid(m, n).gy, n, db, n, nullptr, s) : GT_OK;
+    return dx ? GT_OK : run_join(nullptr, nullptr, epi, cs, s);
 }
 
 }  // extern "C"

@@ -21,6 +21,7 @@
 #include <type_traits>
 
 #include "gt_common.cuh"
+#include "gt_sm100.cuh"
 #include "gt_stats.cuh"
 #include "gt_vec8.cuh"
 
@@ -168,6 +169,7 @@ norm_bwd(int64_t n, int c, const TY* __restrict__ dy, int64_t lddy, const TX* __
     constexpr int TPR = C::TPR, NV = C::NV, R = C::R, RG = C::RG, TH = C::TH;
     __shared__ float2 red[C::RED];
     RowSum<TPR, R, TH> rowsum{red, 0};
+    sm100::pdl_trigger();   // the column sums may start; they wait for this kernel
     const int t = threadIdx.x % TPR, g = threadIdx.x / TPR;
     const float inv_c = 1.0f / (float)c;
     float ag[NV][8], as[NV][8], gv[NV][8];
@@ -280,9 +282,10 @@ __global__ void __launch_bounds__(kColSumThreads) col_sum(const float* __restric
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int i = blockIdx.x * 32 + tx;
     float acc = 0.f;
+    sm100::pdl_wait();   // launched to overlap the end of the kernel that writes `part`
     if (i < cols) {
 #pragma unroll 8
-        for (int p = ty; p < rows; p += kColSumThreads / 32) acc += part[(int64_t)p * cols + i];
+        for (int p = ty; p < rows; p += kColSumThreads / 32) acc += __ldcg(part + (int64_t)p * cols + i);
     }
     red[ty][tx] = acc;
     __syncthreads();
@@ -359,15 +362,15 @@ int check_norm(int xt, int yt, int64_t n, int c) {
     return GT_OK;
 }
 
-}  // namespace
-
-int launch_col_sum(const char* name, const float* part, int rows, int cols, float* out0, int split, float* out1,
-                   cudaStream_t s) {
-    LaunchScope ls(name, s);
-    col_sum<<<(cols + 31) / 32, kColSumThreads, 0, s>>>(part, rows, cols, out0, split, out1);
+int launch_col_sum(const float* part, int rows, int cols, float* out0, int split, float* out1, cudaStream_t s) {
+    LaunchScope ls("norm_grad_sum", s);
+    if (launch_overlapped(col_sum, dim3((cols + 31) / 32), dim3(kColSumThreads), 0, s, part, rows, cols, out0, split,
+                          out1) != cudaSuccess)
+        return GT_ERR_CUDA;
     return check_launch();
 }
 
+}  // namespace
 }  // namespace gt
 
 extern "C" {
@@ -418,7 +421,7 @@ int gt_layer_norm_bwd(int32_t xtype, int32_t ytype, int32_t n, int32_t c, const 
                  ? run_bwd<B, float>(n, c, dy, lddy, x, ldx, gain, mean, rstd, dres, ldr, dx, lddx, part, s)
                  : run_bwd<B, B>(n, c, dy, lddy, x, ldx, gain, mean, rstd, dres, ldr, dx, lddx, part, s);
     if (rc != GT_OK) return rc;
-    return launch_col_sum("norm_grad_sum", part, ctas, 2 * c, dgain, c, dshift, s);
+    return launch_col_sum(part, ctas, 2 * c, dgain, c, dshift, s);
 }
 
 }  // extern "C"

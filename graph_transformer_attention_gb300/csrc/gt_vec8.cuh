@@ -1,6 +1,6 @@
 // gt_vec8.cuh -- eight consecutive row elements at a time, as the LayerNorm and
-// linear-layer kernels move them: 16-byte accesses where rows allow them, single
-// elements otherwise; and the fixed-order sum of per-CTA partial rows.
+// linear-layer kernels move them: 16- and 32-byte accesses where rows allow
+// them, single elements otherwise.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -8,7 +8,6 @@
 #include <stdint.h>
 
 #include "gt_common.cuh"
-#include "gt_stats.cuh"
 
 namespace gt {
 
@@ -51,6 +50,14 @@ __device__ __forceinline__ Raw8<T> load8(const T* p, int live, bool vec) {
         for (int i = 0; i < 8; ++i) w[i] = i < live ? (uint32_t)__ldg(s + i) : 0u;
         r.a = make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16));
     }
+    return r;
+}
+
+// Eight fp32 that the kernel before this one wrote (16-byte aligned).
+__device__ __forceinline__ Raw8<float> load8_cg(const float* p) {
+    Raw8<float> r;
+    r.a = __ldcg(reinterpret_cast<const uint4*>(p));
+    r.b = __ldcg(reinterpret_cast<const uint4*>(p) + 1);
     return r;
 }
 
@@ -110,10 +117,5 @@ __device__ __forceinline__ void stg32(void* p, const uint32_t (&w)[8]) {
                  "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
 }
-
-// Column sums of part [rows][cols] in a fixed order: column c of the first
-// `split` columns goes to out0[c], the others to out1[c - split].  In gt_norm.cu.
-int launch_col_sum(const char* name, const float* part, int rows, int cols, float* out0, int split, float* out1,
-                   cudaStream_t s);
 
 }  // namespace gt
