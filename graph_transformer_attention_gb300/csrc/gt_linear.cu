@@ -13,10 +13,10 @@
 //
 // fp32 operands: each value is the exact sum of three bf16 values, v = hi + mid +
 // lo (8 significand bits each), and a product of two such sums keeps the six terms
-// above 2^-24 of the largest:  lo hi, hi lo, mid mid, mid hi, hi mid, hi hi.  They
-// run as one contraction six times as long, the smallest terms first, so that they
-// are added while the fp32 accumulator is still small.  Six bf16 products cost a
-// sixth of the bf16 rate, which is four times what the fp32 pipes reach.
+// above 2^-24 of the largest:  lo hi, hi lo, mid mid, mid hi, hi mid, hi hi, added up
+// in this order, k-block by k-block, so that the small ones meet a small accumulator.
+// Six bf16 products run at a sixth of the bf16 rate, which is four times what the
+// fp32 pipes reach.
 //
 // Rows that TMA cannot read (a base or row stride that is no multiple of 16 bytes)
 // are first copied to padded rows in the workspace by the kernel that splits fp32.
@@ -51,32 +51,51 @@ __device__ __forceinline__ float rcp(float x) {
     return y;
 }
 
-__device__ __forceinline__ void gauss2(float2 a, float2 mag, float2& e, float2& u) {
-    const float2 d = __ffma2_rn(mag, f2(0.3275911f * 0.70710678118654752f), f2(1.0f));
+// The formula's constants as register pairs.  The compiler would rather build a pair anew at every
+// use than keep it, which doubles the instructions of the packed arithmetic; behind an empty asm
+// statement it has to keep them.
+struct GaussK {
+    float2 p, one, q, a5, a4, a3, a2, a1, half;
+};
+
+__device__ __forceinline__ float2 kept(float x) {
+    float2 r = f2(x);
+    asm volatile("" : "+f"(r.x), "+f"(r.y));
+    return r;
+}
+
+__device__ __forceinline__ GaussK gauss_constants() {
+    return GaussK{kept(0.3275911f * 0.70710678118654752f), kept(1.0f), kept(-0.5f * tc::kLog2e),
+                  kept(-0.5f * 1.061405429f), kept(0.5f * 1.453152027f), kept(-0.5f * 1.421413741f),
+                  kept(0.5f * 0.284496736f), kept(-0.5f * 0.254829592f), kept(0.5f)};
+}
+
+__device__ __forceinline__ void gauss2(const GaussK& k, float2 a, float2 mag, float2& e, float2& u) {
+    const float2 d = __ffma2_rn(mag, k.p, k.one);
     const float2 t = make_float2(rcp(d.x), rcp(d.y));
-    const float2 q = __fmul2_rn(__fmul2_rn(a, f2(-0.5f * tc::kLog2e)), a);
+    const float2 q = __fmul2_rn(__fmul2_rn(a, k.q), a);
     e = make_float2(ex2(q.x), ex2(q.y));
-    float2 s = __ffma2_rn(t, f2(-0.5f * 1.061405429f), f2(0.5f * 1.453152027f));
-    s = __ffma2_rn(t, s, f2(-0.5f * 1.421413741f));
-    s = __ffma2_rn(t, s, f2(0.5f * 0.284496736f));
-    s = __ffma2_rn(t, s, f2(-0.5f * 0.254829592f));
-    u = __ffma2_rn(__fmul2_rn(t, s), e, f2(0.5f));
+    float2 s = __ffma2_rn(t, k.a5, k.a4);
+    s = __ffma2_rn(t, s, k.a3);
+    s = __ffma2_rn(t, s, k.a2);
+    s = __ffma2_rn(t, s, k.a1);
+    u = __ffma2_rn(__fmul2_rn(t, s), e, k.half);
 }
 
 // a Phi(a) = a / 2 + |a| u
-__device__ __forceinline__ float2 gelu2(float2 a) {
+__device__ __forceinline__ float2 gelu2(const GaussK& k, float2 a) {
     const float2 mag = make_float2(fabsf(a.x), fabsf(a.y));
     float2 e, u;
-    gauss2(a, mag, e, u);
-    return __ffma2_rn(mag, u, __fmul2_rn(a, f2(0.5f)));
+    gauss2(k, a, mag, e, u);
+    return __ffma2_rn(mag, u, __fmul2_rn(a, k.half));
 }
 
 // Phi(a) + a phi(a), Phi(a) = 1/2 + sign(a) u
-__device__ __forceinline__ float2 gelu_grad2(float2 a) {
+__device__ __forceinline__ float2 gelu_grad2(const GaussK& k, float2 a) {
     float2 e, u;
-    gauss2(a, make_float2(fabsf(a.x), fabsf(a.y)), e, u);
+    gauss2(k, a, make_float2(fabsf(a.x), fabsf(a.y)), e, u);
     const float2 su = make_float2(copysignf(u.x, a.x), copysignf(u.y, a.y));
-    return __ffma2_rn(__fmul2_rn(a, f2(0.39894228040143268f)), e, __fadd2_rn(su, f2(0.5f)));
+    return __ffma2_rn(__fmul2_rn(a, f2(0.39894228040143268f)), e, __fadd2_rn(su, k.half));
 }
 
 // -------------------------------------------------- operands in the workspace
@@ -129,6 +148,7 @@ __device__ __forceinline__ void prep_rows(const PrepJob& J, int bx, int by) {
     const int m = J.m, n = J.n, tx = J.tx, ty = kPrepThreads / tx;
     const int cx = threadIdx.x % tx, ry = threadIdx.x / tx;
     const int col = (bx * tx + cx) * 8;
+    const GaussK gk = gauss_constants();
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.f;
@@ -153,7 +173,7 @@ __device__ __forceinline__ void prep_rows(const PrepJob& J, int bx, int by) {
                     unpack8(rp[k], a);
 #pragma unroll
                     for (int i = 0; i < 8; i += 2) {
-                        const float2 g = gelu_grad2(make_float2(a[i], a[i + 1]));
+                        const float2 g = gelu_grad2(gk, make_float2(a[i], a[i + 1]));
                         v[i] *= g.x;
                         v[i + 1] *= g.y;
                     }
@@ -332,9 +352,10 @@ __device__ __forceinline__ void epilogue(const Epi& e, int64_t row, int col, int
     }
     if (e.pre) put_row<CW>(e.pre, row * e.ldpre + col, e.pre_f32, v, live, e.pacc);
     if (e.gelu_act) {
+        const GaussK gk = gauss_constants();
 #pragma unroll
         for (int i = 0; i < CW; i += 2) {
-            const float2 y = gelu2(make_float2(v[i], v[i + 1]));
+            const float2 y = gelu2(gk, make_float2(v[i], v[i + 1]));
             v[i] = y.x;
             v[i + 1] = y.y;
         }
@@ -372,7 +393,7 @@ __device__ __forceinline__ void epilogue_single(const Epi& e, int64_t row0, int 
                 if (e.pre_f32) static_cast<float*>(e.pre)[at] = a;
                 else static_cast<bf16*>(e.pre)[at] = __float2bfloat16_rn(a);
             }
-            if (e.gelu_act) a = gelu2(make_float2(a, a)).x;
+            if (e.gelu_act) a = gelu2(gauss_constants(), make_float2(a, a)).x;
             if (e.r) {
                 const int64_t at = row * e.ldr + col + cc;
                 a += e.y_f32 ? static_cast<const float*>(e.r)[at] : __bfloat162float(static_cast<const bf16*>(e.r)[at]);
@@ -388,24 +409,31 @@ __device__ __forceinline__ void epilogue_single(const Epi& e, int64_t row0, int 
 
 constexpr int kBK = 64;          // contraction of a k-block: 128 bytes of bf16, one swizzle row
 constexpr int kEpiWarps = 16;
-constexpr int kGemmThreads = (kEpiWarps + 2) * 32;
-constexpr int kTmaWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
+constexpr int kGemmThreads = (kEpiWarps + 4) * 32;   // the fourth warp makes a whole warpgroup
+constexpr int kTmaWarp = kEpiWarps, kMmaWarp = kEpiWarps + 2;   // TMA: two warps, one per operand
 constexpr int kStageA = 128 * kBK * 2;
 
-// The terms of a split product, smallest first: planes of A and of B.
-__device__ __forceinline__ int term_plane_a(int t) { return (0x001120 >> (4 * t)) & 15; }   // 0 2 1 1 0 0
-__device__ __forceinline__ int term_plane_b(int t) { return (0x010102 >> (4 * t)) & 15; }   // 2 0 1 0 1 0
+// Division by a number known on the host: x / d = the high half of x times (2^64 / d rounded up),
+// exact for 32-bit x.
+struct Divider {
+    uint32_t d;
+    uint64_t inv;
+    static Divider of(uint32_t d) { return Divider{d, d > 1 ? ~uint64_t(0) / d + 1 : 0}; }
+    __device__ __forceinline__ int div(int x) const { return d == 1 ? x : (int)__umul64hi((uint64_t)(uint32_t)x, inv); }
+};
 
 struct GemmShape {
     int M, N;             // of D
     int kblocks;          // of the contraction
-    int terms;            // 1, or 6 for split operands
+    int planes;           // of the operands: 1, or 3 (hi, mid, lo)
     int chunk;            // k-blocks that an accumulator may sum (see linear_gemm)
     int tiles_m, tiles_n;
+    bool whole_a, whole_b;   // an operand with rows along D, as whole blocks of 64 columns
     int splits;           // of the contraction; split s takes k-blocks [s kblocks / splits, (s + 1) kblocks / splits)
+    Divider by_tiles, by_group, by_tail, by_splits;   // tiles, tiles of a whole group, tile rows of the last group, splits
     __host__ __device__ int items() const { return tiles_m * tiles_n * splits; }
-    __host__ __device__ int kb_lo(int s) const { return (int)((int64_t)s * kblocks / splits); }
 };
+constexpr int kGroup = 8;
 
 // A work item: tile (m, n) and the k-blocks [lo, hi) of split s.  Tiles run in groups of 8 tile
 // rows, down the group's column before the next, so that the CTAs of one wave share operands in L2.
@@ -413,13 +441,13 @@ struct Item {
     int m, n, s, lo, hi;
 };
 __device__ __forceinline__ Item item_of(const GemmShape& g, int i) {
-    constexpr int kGroup = 8;
-    const int tiles = g.tiles_m * g.tiles_n;
-    const int s = i / tiles, t = i - s * tiles;
-    const int per = kGroup * g.tiles_n;
-    const int grp = t / per, w = t - grp * per;
-    const int gm = g.tiles_m - grp * kGroup < kGroup ? g.tiles_m - grp * kGroup : kGroup;
-    return Item{grp * kGroup + w % gm, w / gm, s, g.kb_lo(s), g.kb_lo(s + 1)};
+    const int s = g.by_tiles.div(i), t = i - s * (int)g.by_tiles.d;
+    const int grp = g.by_group.div(t), w = t - grp * (int)g.by_group.d;
+    const bool tail = (grp + 1) * kGroup > g.tiles_m;
+    const int n = tail ? g.by_tail.div(w) : w / kGroup;
+    const int m = grp * kGroup + w - n * (tail ? (int)g.by_tail.d : kGroup);
+    // s kblocks stays below 2^32: a split has at least one of at most 2^18 k-blocks, and at most 128 are made
+    return Item{m, n, s, g.by_splits.div(s * g.kblocks), g.by_splits.div((s + 1) * g.kblocks)};
 }
 
 // CTAS CTAs (one, or a pair of a cluster) make a tile of 128 CTAS x BN.  SUM: an item may have
@@ -449,8 +477,8 @@ struct GemmBars {
 // finished sums go through `epi`; else split s stores its sums at
 // part + (s M + row) ldpart.
 //
-// Persistent: one CTA per SM, or pairs of CTAs, walk the items.  Warp kTmaWarp feeds a ring
-// of stages by TMA, warp kMmaWarp (of the pair's first CTA) issues the products into one of two
+// Persistent: one CTA per SM, or pairs of CTAs, walk the items.  Two warps feed a ring of stages by
+// TMA, one per operand, warp kMmaWarp (of the pair's first CTA) issues the products into one of two
 // TMEM accumulators, and sixteen warps take the other accumulator out (four per TMEM lane
 // quarter, a quarter of the columns each), so that a tile's epilogue runs under the next
 // tile's products.  A lane holds a row and stores whole 32-byte sectors of it.
@@ -499,47 +527,41 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     pdl_wait();      // the kernels before this one have finished
     const int items = g.items(), first = blockIdx.x / CTAS, stride = gridDim.x / CTAS;
 
-    if (warp == kTmaWarp) {
+    if (warp == kTmaWarp || warp == kTmaWarp + 1) {
         if (lane == 0) {
+            const bool is_a = warp == kTmaWarp;
             uint32_t it = 0;
             bool ok = true;
             for (int i = first; ok && i < items; i += stride) {
                 const Item w = item_of(g, i);
-                const int m0 = w.m * C::kBM + 128 * (int)rank, n0 = w.n * BN + BN / CTAS * (int)rank;
-                for (int c0 = w.lo; ok && c0 < w.hi; c0 += g.chunk) {
-                    const int c1 = c0 + g.chunk < w.hi ? c0 + g.chunk : w.hi;
-                    for (int t = 0; ok && t < g.terms; ++t) {
-                        const int pa = g.terms == 1 ? 0 : term_plane_a(t), pb = g.terms == 1 ? 0 : term_plane_b(t);
-                        for (int kb = c0; kb < c1; ++kb, ++it) {
-                            const int st = it % C::kStages;
-                            if (it >= (uint32_t)C::kStages &&
-                                !mbar_wait(&bars.empty[st], ((it / C::kStages) - 1) & 1, abort_flag, tc::kWaitNs)) {
-                                ok = false;
-                                break;
-                            }
-                            uint8_t* sa = smem + st * C::kStage;
-                            uint8_t* sb = sa + kStageA;
-                            uint64_t* full = &bars.full[st];
-                            // both halves of a pair's stage count on the first CTA's barrier
-                            const uint32_t pair_full = CTAS == 2 ? map_to_rank(full, 0) : 0;
-                            if (rank == 0) mbar_arrive_expect_tx(full, CTAS * C::kStage);
-                            auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y, int z) {
-                                if (CTAS == 2) tma_load_3d_pair(dst, map, x, y, z, pair_full);
-                                else tma_load_3d(dst, map, x, y, z, full);
-                            };
-                            if (A_MN) {
-#pragma unroll
-                                for (int b = 0; b < 2; ++b) load(sa + b * 8192, &map_a, m0 + 64 * b, kb * kBK, pa);
-                            } else {
-                                load(sa, &map_a, kb * kBK, m0, pa);
-                            }
-                            if (B_MN) {
-#pragma unroll
-                                for (int b = 0; b < BN / CTAS / 64; ++b)
-                                    load(sb + b * 8192, &map_b, n0 + 64 * b, kb * kBK, pb);
-                            } else {
-                                load(sb, &map_b, kb * kBK, n0, pb);
-                            }
+                // the operand's first row (or column) of this CTA's half
+                const int r0 = is_a ? w.m * C::kBM + 128 * (int)rank : w.n * BN + BN / CTAS * (int)rank;
+                for (int kb = w.lo; ok && kb < w.hi; ++kb) {
+                    for (int j = 0; j < g.planes; ++j, ++it) {
+                        const int plane = g.planes == 1 ? 0 : j == 0 ? 2 : j - 1;   // lo, hi, mid: as they are used
+                        const int st = it % C::kStages;
+                        if (it >= (uint32_t)C::kStages &&
+                            !mbar_wait(&bars.empty[st], ((it / C::kStages) - 1) & 1, abort_flag, tc::kWaitNs)) {
+                            ok = false;
+                            break;
+                        }
+                        uint64_t* full = &bars.full[st];
+                        // both halves of a pair's stage count on the first CTA's barrier
+                        const uint32_t pair_full = CTAS == 2 ? map_to_rank(full, 0) : 0;
+                        if (is_a && rank == 0) mbar_arrive_expect_tx(full, CTAS * C::kStage);
+                        auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y, int z) {
+                            if (CTAS == 2) tma_load_4d_pair(dst, map, x, y, z, plane, pair_full);
+                            else tma_load_4d(dst, map, x, y, z, plane, full);
+                        };
+                        uint8_t* dst = smem + st * C::kStage + (is_a ? 0 : kStageA);
+                        const CUtensorMap* map = is_a ? &map_a : &map_b;
+                        const int blocks = is_a ? 2 : BN / CTAS / 64;   // of 64 along the row
+                        if (!(is_a ? A_MN : B_MN)) {
+                            load(dst, map, kb * kBK, r0, 0);
+                        } else if (is_a ? g.whole_a : g.whole_b) {
+                            load(dst, map, 0, kb * kBK, r0 / 64);
+                        } else {
+                            for (int b = 0; b < blocks; ++b) load(dst + b * 8192, map, r0 + 64 * b, kb * kBK, 0);
                         }
                     }
                 }
@@ -564,41 +586,70 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             const SmemDesc db = smem_desc_split(smem_u32(smem) + kStageA, B_MN ? 8192 : 16, 1024, 2);
             uint32_t it = 0, n = 0;
             bool ok = true;
+            auto landed = [&](uint32_t i) {
+                const bool got = mbar_wait_all(&bars.full[i % C::kStages], (i / C::kStages) & 1, abort_flag, tc::kWaitNs);
+                tc_fence_after();
+                return got;
+            };
+            // one lane: D (+)= the k-block of A in stage sa times that of B in stage sb
+            auto product = [&](uint32_t d, uint32_t sa, uint32_t sb, bool add) {
+                const uint32_t oa = sa % C::kStages * C::kStage, ob = sb % C::kStages * C::kStage;
+#pragma unroll
+                for (int ks = 0; ks < kBK / 16; ++ks) {
+                    const uint64_t ad = desc_at(da, oa + (A_MN ? 2048 : 32) * ks);
+                    const uint64_t bd = desc_at(db, ob + (B_MN ? 2048 : 32) * ks);
+                    if (CTAS == 2) mma_ss_pair(d, ad, bd, id, add || ks > 0);
+                    else mma_ss(d, ad, bd, id, add || ks > 0);
+                }
+            };
+            auto commit = [&](uint64_t* bar) {
+                if (CTAS == 2) mma_commit_pair(bar);
+                else mma_commit(bar);
+            };
             for (int i = first; ok && i < items; i += stride) {
                 const Item w = item_of(g, i);
                 for (int c0 = w.lo; ok && c0 < w.hi; c0 += g.chunk, ++n) {
-                    const int steps = g.terms * (c0 + g.chunk < w.hi ? g.chunk : w.hi - c0);
+                    const int c1 = c0 + g.chunk < w.hi ? c0 + g.chunk : w.hi;
                     const uint32_t a = n & 1, d = tbase + a * BN;
                     if (n >= 2 && !mbar_wait_all(&bars.acc_empty[a], ((n >> 1) - 1) & 1, abort_flag, tc::kWaitNs)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    for (int k = 0; k < steps; ++k, ++it) {
-                        const int st = it % C::kStages;
-                        if (!mbar_wait_all(&bars.full[st], (it / C::kStages) & 1, abort_flag, tc::kWaitNs)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        if (elect_one()) {
-                            const uint32_t off = st * C::kStage;
-#pragma unroll
-                            for (int ks = 0; ks < kBK / 16; ++ks) {
-                                const uint64_t ad = desc_at(da, off + (A_MN ? 2048 : 32) * ks);
-                                const uint64_t bd = desc_at(db, off + (B_MN ? 2048 : 32) * ks);
-                                if (CTAS == 2) mma_ss_pair(d, ad, bd, id, k > 0 || ks > 0);
-                                else mma_ss(d, ad, bd, id, k > 0 || ks > 0);
+                    for (int kb = c0; kb < c1; ++kb) {
+                        if (g.planes == 1) {
+                            if (!(ok = landed(it))) break;
+                            if (elect_one()) {
+                                product(d, it, it, kb > c0);
+                                commit(&bars.empty[it % C::kStages]);
+                                if (kb == c1 - 1) commit(&bars.acc_full[a]);
                             }
-                            if (CTAS == 2) {
-                                mma_commit_pair(&bars.empty[st]);
-                                if (k == steps - 1) mma_commit_pair(&bars.acc_full[a]);
-                            } else {
-                                mma_commit(&bars.empty[st]);
-                                if (k == steps - 1) mma_commit(&bars.acc_full[a]);
+                            __syncwarp();
+                            ++it;
+                        } else {
+                            // stages it, it + 1, it + 2 hold lo, hi, mid; a stage is given back
+                            // after its last term
+                            const uint32_t lo = it, hi = it + 1, mid = it + 2;
+                            if (!(ok = landed(lo) && landed(hi))) break;
+                            if (elect_one()) {
+                                product(d, lo, hi, kb > c0);
+                                product(d, hi, lo, true);
+                                commit(&bars.empty[lo % C::kStages]);
                             }
+                            __syncwarp();
+                            if (!(ok = landed(mid))) break;
+                            if (elect_one()) {
+                                product(d, mid, mid, true);
+                                product(d, mid, hi, true);
+                                product(d, hi, mid, true);
+                                commit(&bars.empty[mid % C::kStages]);
+                                product(d, hi, hi, true);
+                                commit(&bars.empty[hi % C::kStages]);
+                                if (kb == c1 - 1) commit(&bars.acc_full[a]);
+                            }
+                            __syncwarp();
+                            it += 3;
                         }
-                        __syncwarp();
                     }
                 }
             }
@@ -613,22 +664,31 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                 mbar_wait_all(&bars.fin, 0, &never, tc::kWaitNs);
             }
         }
-    } else {
+    } else if (warp < kEpiWarps) {
         constexpr int CW = C::kCW, NC = C::kCols / C::kCW;
         const int q = warp & 3, c0 = (warp >> 2) * C::kCols;
         const uint32_t tl = tbase + ((uint32_t)(32 * q) << 16) + c0, bias = smem_u32(bias_s[warp]);
+        constexpr int NB = C::kCols > 32 ? C::kCols / 32 : 1;
+        float next_b[NB];
+        auto fetch_bias = [&](int col) {
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+                next_b[j] = epi.bias && col + 32 * j + lane < g.N ? __ldg(epi.bias + col + 32 * j + lane) : 0.f;
+        };
+        if (first < items) fetch_bias(item_of(g, first).n * BN + c0);
         uint32_t n = 0;
         bool ok = true;
         for (int i = first; ok && i < items; i += stride) {
             const Item w = item_of(g, i);
             const int64_t row = (int64_t)w.m * C::kBM + 128 * rank + 32 * q + lane;
             const int col0 = w.n * BN + c0;
-            // this warp's columns of the bias, fetched while the products run
+            // this warp's columns of the bias, fetched an item ahead
             __syncwarp();
 #pragma unroll
-            for (int j = lane; j < C::kCols; j += 32)
-                bias_s[warp][j] = epi.bias && col0 + j < g.N ? __ldg(epi.bias + col0 + j) : 0.f;
+            for (int j = 0; j < NB; ++j)
+                if (NB > 1 || lane < C::kCols) bias_s[warp][32 * j + lane] = next_b[j];
             __syncwarp();
+            if (i + stride < items) fetch_bias(item_of(g, i + stride).n * BN + c0);
             float sum[SUM ? NC : 1][CW];
 #pragma unroll
             for (int c = 0; c < (SUM ? NC : 1); ++c)
@@ -754,12 +814,13 @@ struct GemmPlan {
 };
 
 // k-blocks an accumulator may sum: 256 deep for an fp32 result (2e-7 lost at most), 4096 deep
-// for a bf16 one (1.1e-5, against a rounding of 3.9e-3).
-int chunk_of(bool f32_out) { return f32_out ? 4 : 64; }
+// for a bf16 one (1.1e-5, against a rounding of 3.9e-3); one k-block of split operands, whose large
+// terms are the last four of 24 steps.
+int chunk_of(bool f32_out, int planes) { return planes == 3 ? 1 : f32_out ? 4 : 64; }
 
 // The tile and the splits of the contraction with the least modelled time: waves of k-block steps
 // (microseconds each as measured per tile), and for splits the partial sums' traffic and a second kernel.
-GemmPlan plan_gemm(int M, int N, int K, int terms, bool f32_out) {
+GemmPlan plan_gemm(int M, int N, int K, int planes, bool f32_out) {
     GemmPlan best{};
     double best_us = 1e30;
     const int sms = num_sms();
@@ -770,19 +831,24 @@ GemmPlan plan_gemm(int M, int N, int K, int terms, bool f32_out) {
         const int tm = (M + bm - 1) / bm, tn = (N + t.bn - 1) / t.bn;
         const int64_t n = (int64_t)tm * tn;
         for (int sp = 1; sp <= 128; sp = sp < 8 ? sp + 1 : sp + sp / 4) {
-            if (sp > 1 && (sp * n > 2 * units || kb / sp < (terms == 1 ? 4 : 2))) break;
+            if (sp > 1 && (sp * n > 2 * units || kb / sp < (planes == 1 ? 4 : 2))) break;
             const int64_t waves = (n * sp + units - 1) / units;
-            const int64_t steps = (int64_t)((kb + sp - 1) / sp) * terms;
+            const int64_t steps = (int64_t)((kb + sp - 1) / sp) * (planes == 1 ? 1 : 6);
             double us = waves * steps * t.us_kb + 3.0 + 0.004 * t.bn * (waves < 4 ? waves : 4);
             if (sp > 1) us += 3.0 + (double)M * N * (sp + 2) * 4 / 4e6;
             if (us < best_us) {
                 best_us = us;
-                best.g = GemmShape{M, N, kb, terms, chunk_of(f32_out), tm, tn, sp};
+                best.g = GemmShape{M, N, kb, planes, chunk_of(f32_out, planes), tm, tn, M % 64 == 0, N % 64 == 0, sp};
                 best.ctas = t.ctas;
                 best.bn = t.bn;
             }
         }
     }
+    GemmShape& g = best.g;
+    g.by_tiles = Divider::of(g.tiles_m * g.tiles_n);
+    g.by_group = Divider::of(kGroup * g.tiles_n);
+    g.by_tail = Divider::of(g.tiles_m % kGroup ? g.tiles_m % kGroup : kGroup);
+    g.by_splits = Divider::of(g.splits);
     return best;
 }
 
@@ -819,6 +885,21 @@ int launch_gemm(const GemmPlan& p, const CUtensorMap& ma, const CUtensorMap& mb,
                                                                                                       : GT_ERR_CUDA;
 }
 
+// The map of an operand of which a CTA takes `across` rows (columns, where mn) and 64 of the
+// contraction at a time.  Blocks of 64 elements make the 128 bytes of a swizzled row: an operand with
+// rows along D that is whole in them (mn, whole) comes as [plane][block][row][64], and all of a CTA's
+// blocks with one load; else a load brings one block, ends filled with zeros.
+bool operand_map(CUtensorMap* map, const Operand& o, bool mn, bool whole, int across) {
+    const uint64_t row = (uint64_t)o.ld * 2, plane = (uint64_t)o.plane * 2;
+    const uint64_t rows = o.rows, cols = o.cols, planes = o.planes;
+    const CUtensorMapDataType ty = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    if (mn && whole)
+        return make_map_4d(map, o.p, ty, {64, rows, cols / 64, planes}, {row, 128, plane}, {64, (uint32_t)kBK, (uint32_t)across / 64, 1},
+                           CU_TENSOR_MAP_SWIZZLE_128B);
+    return make_map_4d(map, o.p, ty, {cols, rows, 1, planes}, {row, row, plane}, {64, (uint32_t)(mn ? kBK : across), 1, 1},
+                       CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 // D = A B through the epilogue, or its splits' sums to `part`.  A_MN / B_MN: the operand's rows run
 // along the contraction and its columns along D (stored [contraction][M] or [contraction][N]).
 // follows: a kernel of the same call precedes (this one may start while that one ends).
@@ -826,11 +907,7 @@ template <bool A_MN, bool B_MN>
 int run_gemm(const GemmPlan& p, const Operand& a, const Operand& b, const Epi& epi, float* part, bool follows,
              cudaStream_t s) {
     CUtensorMap ma, mb;
-    const CUtensorMapDataType ty = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    if (!make_map_3d(&ma, a.p, ty, a.planes, a.rows, a.cols, a.plane * 2, a.ld * 2, A_MN ? kBK : 128, 64,
-                     CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_map_3d(&mb, b.p, ty, b.planes, b.rows, b.cols, b.plane * 2, b.ld * 2, B_MN ? kBK : p.bn / p.ctas, 64,
-                     CU_TENSOR_MAP_SWIZZLE_128B))
+    if (!operand_map(&ma, a, A_MN, p.g.whole_a, 128) || !operand_map(&mb, b, B_MN, p.g.whole_b, p.bn / p.ctas))
         return GT_ERR_CUDA;
     float* out = p.g.splits > 1 ? part : nullptr;
     const bool one_chunk = (p.g.kblocks + p.g.splits - 1) / p.g.splits <= p.g.chunk;
@@ -912,7 +989,7 @@ struct Prep {
 
 size_t operand_elems(int dtype, int m, int n) { return (size_t)m * pad8(n) * (dtype == GT_F32 ? 3 : 1); }
 
-int terms_of(int dtype) { return dtype == GT_F32 ? 6 : 1; }
+int planes_of(int dtype) { return dtype == GT_F32 ? 3 : 1; }
 
 constexpr int kMaxWidth = 65536, kMaxRows = 1 << 24;
 
@@ -935,7 +1012,7 @@ size_t fwd_bufs(int dtype, bool y_f32, int m, int k, int n, bool pack_x, bool pa
     FwdBufs b;
     b.x = pack_x ? c.take<bf16>(operand_elems(dtype, m, k)) : nullptr;
     b.w = pack_w ? c.take<bf16>(operand_elems(dtype, k, n)) : nullptr;
-    b.part = c.take<float>(part_floats(plan_gemm(m, n, k, terms_of(dtype), y_f32)));
+    b.part = c.take<float>(part_floats(plan_gemm(m, n, k, planes_of(dtype), y_f32)));
     if (out) *out = b;
     return c.off;
 }
@@ -953,8 +1030,8 @@ size_t bwd_bufs(int dtype, int m, int k, int n, bool pack_x, bool pack_w, bool o
     b.x = pack_x ? c.take<bf16>(operand_elems(dtype, m, k)) : nullptr;
     b.w = pack_w ? c.take<bf16>(operand_elems(dtype, k, n)) : nullptr;
     b.da = own_da ? c.take<bf16>(operand_elems(dtype, m, n)) : nullptr;
-    const size_t px = part_floats(plan_gemm(m, k, n, terms_of(dtype), dtype == GT_F32));
-    const size_t pw = part_floats(plan_gemm(k, n, m, terms_of(dtype), dtype == GT_F32));
+    const size_t px = part_floats(plan_gemm(m, k, n, planes_of(dtype), dtype == GT_F32));
+    const size_t pw = part_floats(plan_gemm(k, n, m, planes_of(dtype), dtype == GT_F32));
     b.part = c.take<float>(px > pw ? px : pw);
     b.cols = c.take<float>((size_t)prep_grid(m, n).gy * n);
     if (out) *out = b;
@@ -1009,7 +1086,7 @@ int gt_linear_fwd(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n,
     if ((rc = prep.launch(s)) != GT_OK) return rc;
     const int ey = elem_bytes(ytype), ex = elem_bytes(dtype);
     const Epi epi = make_epi(b, act, ytype, dtype, r, ldr, ey, y, ldy, pre, ldpre, ex);
-    const GemmPlan plan = plan_gemm(m, n, k, terms_of(dtype), ytype == GT_F32);
+    const GemmPlan plan = plan_gemm(m, n, k, planes_of(dtype), ytype == GT_F32);
     if ((rc = run_gemm<false, true>(plan, ox, ow, epi, bufs.part, prep.jobs.count > 0, s)) != GT_OK) return rc;
     return run_join(&plan, bufs.part, epi, ColSum{}, s);
 }
@@ -1046,7 +1123,7 @@ int gt_linear_bwd(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n,
     ColSum cs{db ? bufs.cols : nullptr, db, prep_grid(m, n).gy, n};
     Epi epi{};
     if (dx) {
-        const GemmPlan plan = plan_gemm(m, k, n, terms_of(dtype), f32);
+        const GemmPlan plan = plan_gemm(m, k, n, planes_of(dtype), f32);
         epi = make_epi(nullptr, GT_ACT_NONE, dtype, dtype, add, ldadd, ex, dx, lddx, nullptr, 0, ex);
         if ((rc = run_gemm<false, false>(plan, oda, ow, epi, bufs.part, follows, s)) != GT_OK) return rc;
         follows = true;
@@ -1054,7 +1131,7 @@ int gt_linear_bwd(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n,
         if ((rc = run_join(&plan, bufs.part, epi, dw ? ColSum{} : cs, s)) != GT_OK) return rc;
     }
     if (dw) {
-        const GemmPlan plan = plan_gemm(k, n, m, terms_of(dtype), f32);
+        const GemmPlan plan = plan_gemm(k, n, m, planes_of(dtype), f32);
         epi = make_epi(nullptr, GT_ACT_NONE, dtype, dtype, nullptr, 0, ex, dw, lddw, nullptr, 0, ex);
         if ((rc = run_gemm<true, true>(plan, ox, oda, epi, bufs.part, follows, s)) != GT_OK) return rc;
         return run_join(&plan, bufs.part, epi, cs, s);

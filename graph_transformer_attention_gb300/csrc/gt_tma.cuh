@@ -44,19 +44,18 @@ inline bool make_map_2d(CUtensorMap* map, void* base, CUtensorMapDataType type, 
                CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 3-D row-major tensor [planes][rows][cols]: box [1][box_rows][box_cols]; zero
-// fill outside the tensor.
-inline bool make_map_3d(CUtensorMap* map, const void* base, CUtensorMapDataType type, uint64_t planes, uint64_t rows,
-                        uint64_t cols, uint64_t plane_stride_bytes, uint64_t row_stride_bytes, uint32_t box_rows,
-                        uint32_t box_cols, CUtensorMapSwizzle swizzle) {
+// 4-D tensor (innermost extent first) with the strides of dimensions 1..3 in bytes; zero fill
+// outside the tensor.
+inline bool make_map_4d(CUtensorMap* map, const void* base, CUtensorMapDataType type, const uint64_t (&extent)[4],
+                        const uint64_t (&stride_bytes)[3], const uint32_t (&box)[4], CUtensorMapSwizzle swizzle) {
     EncodeTiledFn enc = encode_tiled_fn();
     if (!enc) return false;
-    cuuint64_t dims[3] = {cols, rows, planes};
-    cuuint64_t strides[2] = {row_stride_bytes, plane_stride_bytes};
-    cuuint32_t box[3] = {box_cols, box_rows, 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    return enc(map, type, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    cuuint64_t dims[4] = {extent[0], extent[1], extent[2], extent[3]};
+    cuuint64_t strides[3] = {stride_bytes[0], stride_bytes[1], stride_bytes[2]};
+    cuuint32_t b[4] = {box[0], box[1], box[2], box[3]};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(map, type, 4, const_cast<void*>(base), dims, strides, b, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace gt
