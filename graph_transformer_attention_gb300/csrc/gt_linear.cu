@@ -24,6 +24,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <type_traits>
 
 #include "gt_common.cuh"
 #include "gt_sm100.cuh"
@@ -528,55 +529,69 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     const int items = g.items(), first = blockIdx.x / CTAS, stride = gridDim.x / CTAS;
 
     if (warp == kTmaWarp || warp == kTmaWarp + 1) {
-        if (lane == 0) {
-            const bool is_a = warp == kTmaWarp;
-            uint32_t it = 0;
+        // The whole warp runs the loop and waits; the elected lane issues (from a diverged warp a
+        // TMA instruction costs far more).  MN: the operand's rows run along the contraction; `blocks`
+        // of 64 elements along D; r0: this CTA's first row or column of the tile.
+        auto feed = [&](auto is_a_, auto mn_, const CUtensorMap& map, bool whole, int across) {
+            constexpr bool is_a = decltype(is_a_)::value, mn = decltype(mn_)::value;
+            constexpr int blocks = is_a ? 2 : BN / CTAS / 64;
+            uint32_t st = 0, round = 0;   // stage, and times round the ring
             bool ok = true;
             for (int i = first; ok && i < items; i += stride) {
                 const Item w = item_of(g, i);
-                // the operand's first row (or column) of this CTA's half
-                const int r0 = is_a ? w.m * C::kBM + 128 * (int)rank : w.n * BN + BN / CTAS * (int)rank;
+                const int r0 = (is_a ? w.m : w.n) * across * CTAS + across * (int)rank;
                 for (int kb = w.lo; ok && kb < w.hi; ++kb) {
-                    for (int j = 0; j < g.planes; ++j, ++it) {
+                    for (int j = 0; j < g.planes; ++j) {
                         const int plane = g.planes == 1 ? 0 : j == 0 ? 2 : j - 1;   // lo, hi, mid: as they are used
-                        const int st = it % C::kStages;
-                        if (it >= (uint32_t)C::kStages &&
-                            !mbar_wait(&bars.empty[st], ((it / C::kStages) - 1) & 1, abort_flag, tc::kWaitNs)) {
+                        if (round > 0 && !mbar_wait_all(&bars.empty[st], (round - 1) & 1, abort_flag, tc::kWaitNs)) {
                             ok = false;
                             break;
                         }
-                        uint64_t* full = &bars.full[st];
-                        // both halves of a pair's stage count on the first CTA's barrier
-                        const uint32_t pair_full = CTAS == 2 ? map_to_rank(full, 0) : 0;
-                        if (is_a && rank == 0) mbar_arrive_expect_tx(full, CTAS * C::kStage);
-                        auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y, int z) {
-                            if (CTAS == 2) tma_load_4d_pair(dst, map, x, y, z, plane, pair_full);
-                            else tma_load_4d(dst, map, x, y, z, plane, full);
-                        };
-                        uint8_t* dst = smem + st * C::kStage + (is_a ? 0 : kStageA);
-                        const CUtensorMap* map = is_a ? &map_a : &map_b;
-                        const int blocks = is_a ? 2 : BN / CTAS / 64;   // of 64 along the row
-                        if (!(is_a ? A_MN : B_MN)) {
-                            load(dst, map, kb * kBK, r0, 0);
-                        } else if (is_a ? g.whole_a : g.whole_b) {
-                            load(dst, map, 0, kb * kBK, r0 / 64);
-                        } else {
-                            for (int b = 0; b < blocks; ++b) load(dst + b * 8192, map, r0 + 64 * b, kb * kBK, 0);
+                        if (elect_one()) {
+                            uint64_t* full = &bars.full[st];
+                            // both halves of a pair's stage count on the first CTA's barrier
+                            const uint32_t pair_full = CTAS == 2 ? map_to_rank(full, 0) : 0;
+                            if (is_a && rank == 0) mbar_arrive_expect_tx(full, CTAS * C::kStage);
+                            uint8_t* dst = smem + st * C::kStage + (is_a ? 0 : kStageA);
+                            auto load = [&](int at, int x, int y, int z) {
+                                if (CTAS == 2) tma_load_4d_pair(dst + at, &map, x, y, z, plane, pair_full);
+                                else tma_load_4d(dst + at, &map, x, y, z, plane, full);
+                            };
+                            if (!mn) {
+                                load(0, kb * kBK, r0, 0);
+                            } else if (whole) {
+                                load(0, 0, kb * kBK, r0 / 64);
+                            } else {
+#pragma unroll
+                                for (int b = 0; b < blocks; ++b) load(b * 8192, r0 + 64 * b, kb * kBK, 0);
+                            }
+                        }
+                        __syncwarp();
+                        if (++st == C::kStages) {
+                            st = 0;
+                            ++round;
                         }
                     }
                 }
             }
-            if (!ok) tc::fail(&bars.abort, status);
+            if (!ok && lane == 0) tc::fail(&bars.abort, status);
             // Nothing may still be on its way into shared memory, or to a barrier in it, when the
             // CTA ends: every stage's last load has landed, and, unless a wait gave up, has been
             // consumed by products that have completed.  (A pair's second CTA has no barrier of its
             // own for its loads; where its wait gave up, they were issued that wait's limit ago.)
             int never = 0;
-            for (uint32_t b = it > (uint32_t)C::kStages ? it - C::kStages : 0; b < it; ++b) {
-                if (rank == 0) mbar_wait(&bars.full[b % C::kStages], (b / C::kStages) & 1, &never, tc::kWaitNs);
-                if (ok) ok = mbar_wait(&bars.empty[b % C::kStages], (b / C::kStages) & 1, abort_flag, tc::kWaitNs);
+            for (int k = 0; k < C::kStages; ++k) {   // from the oldest stage on
+                const uint32_t times = k < (int)(C::kStages - st) ? round : round + 1;   // loads of stage (st + k) % kStages
+                const uint32_t s = st + k < (uint32_t)C::kStages ? st + k : st + k - C::kStages;
+                if (times == 0) continue;
+                if (rank == 0) mbar_wait_all(&bars.full[s], (times - 1) & 1, &never, tc::kWaitNs);
+                if (ok) ok = mbar_wait_all(&bars.empty[s], (times - 1) & 1, abort_flag, tc::kWaitNs);
             }
-        }
+        };
+        using Yes = std::true_type;
+        using No = std::false_type;
+        if (warp == kTmaWarp) feed(Yes(), std::integral_constant<bool, A_MN>(), map_a, g.whole_a, 128);
+        else feed(No(), std::integral_constant<bool, B_MN>(), map_b, g.whole_b, BN / CTAS);
     } else if (warp == kMmaWarp) {
         if (rank == 0) {
             constexpr uint32_t id = idesc_bf16(C::kBM, BN, A_MN, B_MN);
@@ -584,16 +599,21 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             // row: 64-element blocks 8192 bytes apart, 8-deep groups 1024 bytes apart, 2048 bytes per k-step
             const SmemDesc da = smem_desc_split(smem_u32(smem), A_MN ? 8192 : 16, 1024, 2);
             const SmemDesc db = smem_desc_split(smem_u32(smem) + kStageA, B_MN ? 8192 : 16, 1024, 2);
-            uint32_t it = 0, n = 0;
+            uint32_t st = 0, phase = 0, n = 0;   // the next stage and the parity of its loads
             bool ok = true;
-            auto landed = [&](uint32_t i) {
-                const bool got = mbar_wait_all(&bars.full[i % C::kStages], (i / C::kStages) & 1, abort_flag, tc::kWaitNs);
+            auto landed = [&](uint32_t& s) {     // waits for the next stage, and names it
+                s = st;
+                const bool got = mbar_wait_all(&bars.full[st], phase, abort_flag, tc::kWaitNs);
+                if (++st == C::kStages) {
+                    st = 0;
+                    phase ^= 1u;
+                }
                 tc_fence_after();
                 return got;
             };
             // one lane: D (+)= the k-block of A in stage sa times that of B in stage sb
             auto product = [&](uint32_t d, uint32_t sa, uint32_t sb, bool add) {
-                const uint32_t oa = sa % C::kStages * C::kStage, ob = sb % C::kStages * C::kStage;
+                const uint32_t oa = sa * C::kStage, ob = sb * C::kStage;
 #pragma unroll
                 for (int ks = 0; ks < kBK / 16; ++ks) {
                     const uint64_t ad = desc_at(da, oa + (A_MN ? 2048 : 32) * ks);
@@ -618,23 +638,22 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                     tc_fence_after();
                     for (int kb = c0; kb < c1; ++kb) {
                         if (g.planes == 1) {
-                            if (!(ok = landed(it))) break;
+                            uint32_t s;
+                            if (!(ok = landed(s))) break;
                             if (elect_one()) {
-                                product(d, it, it, kb > c0);
-                                commit(&bars.empty[it % C::kStages]);
+                                product(d, s, s, kb > c0);
+                                commit(&bars.empty[s]);
                                 if (kb == c1 - 1) commit(&bars.acc_full[a]);
                             }
                             __syncwarp();
-                            ++it;
                         } else {
-                            // stages it, it + 1, it + 2 hold lo, hi, mid; a stage is given back
-                            // after its last term
-                            const uint32_t lo = it, hi = it + 1, mid = it + 2;
+                            // three stages hold lo, hi, mid; each is given back after its last term
+                            uint32_t lo, hi, mid;
                             if (!(ok = landed(lo) && landed(hi))) break;
                             if (elect_one()) {
                                 product(d, lo, hi, kb > c0);
                                 product(d, hi, lo, true);
-                                commit(&bars.empty[lo % C::kStages]);
+                                commit(&bars.empty[lo]);
                             }
                             __syncwarp();
                             if (!(ok = landed(mid))) break;
@@ -642,13 +661,12 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                                 product(d, mid, mid, true);
                                 product(d, mid, hi, true);
                                 product(d, hi, mid, true);
-                                commit(&bars.empty[mid % C::kStages]);
+                                commit(&bars.empty[mid]);
                                 product(d, hi, hi, true);
-                                commit(&bars.empty[hi % C::kStages]);
+                                commit(&bars.empty[hi]);
                                 if (kb == c1 - 1) commit(&bars.acc_full[a]);
                             }
                             __syncwarp();
-                            it += 3;
                         }
                     }
                 }
