@@ -247,6 +247,7 @@ struct Epi {
     int64_t ldr, ldy, ldpre;
     bool gelu_act, y_f32, pre_f32;
     bool single;   // some rows can only be reached by single elements
+    bool bulk;     // bf16 results go out as TMA boxes (the pair kernel; maps in the kernel's arguments)
     int racc, yacc, pacc;
 };
 
@@ -343,7 +344,7 @@ __device__ __forceinline__ void add_row(const void* base, int64_t at, bool f32, 
 
 // Columns col .. col + CW - 1 (live of them, >= 1) of row `row`; bias: theirs, in shared memory.
 template <int CW>
-__device__ __forceinline__ void epilogue(const Epi& e, int64_t row, int col, int live, float (&v)[CW], uint32_t bias) {
+__device__ __forceinline__ void add_bias(float (&v)[CW], uint32_t bias) {
 #pragma unroll
     for (int i = 0; i < CW; i += 4) {
         const uint4 w = lds_u4(bias + 4 * i);
@@ -351,16 +352,24 @@ __device__ __forceinline__ void epilogue(const Epi& e, int64_t row, int col, int
         const float2 b = __fadd2_rn(make_float2(v[i + 2], v[i + 3]), make_float2(__uint_as_float(w.z), __uint_as_float(w.w)));
         v[i] = a.x; v[i + 1] = a.y; v[i + 2] = b.x; v[i + 3] = b.y;
     }
-    if (e.pre) put_row<CW>(e.pre, row * e.ldpre + col, e.pre_f32, v, live, e.pacc);
-    if (e.gelu_act) {
-        const GaussK gk = gauss_constants();
+}
+
+template <int CW>
+__device__ __forceinline__ void apply_gelu(float (&v)[CW]) {
+    const GaussK gk = gauss_constants();
 #pragma unroll
-        for (int i = 0; i < CW; i += 2) {
-            const float2 y = gelu2(gk, make_float2(v[i], v[i + 1]));
-            v[i] = y.x;
-            v[i + 1] = y.y;
-        }
+    for (int i = 0; i < CW; i += 2) {
+        const float2 y = gelu2(gk, make_float2(v[i], v[i + 1]));
+        v[i] = y.x;
+        v[i + 1] = y.y;
     }
+}
+
+template <int CW>
+__device__ __forceinline__ void epilogue(const Epi& e, int64_t row, int col, int live, float (&v)[CW], uint32_t bias) {
+    add_bias<CW>(v, bias);
+    if (e.pre) put_row<CW>(e.pre, row * e.ldpre + col, e.pre_f32, v, live, e.pacc);
+    if (e.gelu_act) apply_gelu<CW>(v);
     if (e.r) add_row<CW>(e.r, row * e.ldr + col, e.y_f32, v, live, e.racc);
     put_row<CW>(e.y, row * e.ldy + col, e.y_f32, v, live, e.yacc);
 }
@@ -404,6 +413,39 @@ __device__ __forceinline__ void epilogue_single(const Epi& e, int64_t row0, int 
             else static_cast<bf16*>(e.y)[at] = __float2bfloat16_rn(a);
         }
     }
+}
+
+// The same for a whole warp and 32 columns of bf16 results, through the warp's 2 KB staging tile and
+// TMA: rows of 64 bytes, 64-byte swizzle.  A lane's row in 32-byte pieces costs the L1 four times
+// the cycles of whole lines, and the products need that memory's bandwidth (32768x1024x4096, GELU and pre: 195 -> 185 us alone).
+constexpr int kBoxCols = 32, kBoxBytes = 32 * kBoxCols * 2;
+
+__device__ __forceinline__ void put_box(const CUtensorMap* map, int64_t row0, int col, const float (&v)[32], uint32_t stg) {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) bulk_wait_read();   // the tile's last box has been read
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        sts_u4(stg + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), pack_bf16x2(v[8 * j], v[8 * j + 1]),
+               pack_bf16x2(v[8 * j + 2], v[8 * j + 3]), pack_bf16x2(v[8 * j + 4], v[8 * j + 5]),
+               pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+        tma_store_2d(map, stg, col, (int)row0);
+        bulk_commit();
+    }
+}
+
+__device__ __forceinline__ void epilogue_bulk(const Epi& e, const CUtensorMap* map_y, const CUtensorMap* map_pre,
+                                              int64_t row0, int M, int col, int live, float (&v)[32], uint32_t bias,
+                                              uint32_t stg) {
+    add_bias<32>(v, bias);
+    if (e.pre) put_box(map_pre, row0, col, v, stg);
+    if (e.gelu_act) apply_gelu<32>(v);
+    const int64_t row = row0 + (threadIdx.x & 31);
+    if (e.r && row < M) add_row<32>(e.r, row * e.ldr + col, false, v, live, e.racc);
+    put_box(map_y, row0, col, v, stg);
 }
 
 // ------------------------------------------------------------- the product kernel
@@ -458,8 +500,10 @@ struct GemmCfg {
     static constexpr int kBM = 128 * CTAS;
     static constexpr int kStageB = BN / CTAS * kBK * 2;   // a CTA of a pair holds half of B's columns
     static constexpr int kStage = kStageA + kStageB;
-    static constexpr int kStages = 192 * 1024 / kStage;
-    static constexpr int kSmem = kStages * kStage + 1024;
+    static constexpr bool kBulk = CTAS == 2 && !SUM;      // bf16 results, which go out as TMA boxes
+    static constexpr int kStages = (kBulk ? 160 : 192) * 1024 / kStage;
+    static constexpr int kStg = kBulk ? kBoxBytes : (kStgBytes + 127) / 128 * 128;   // staging of an epilogue warp
+    static constexpr int kSmem = kStages * kStage + kEpiWarps * kStg + 1024;
     static constexpr uint32_t kTmemCols = 2 * BN;
     static constexpr int kCols = BN / 4;                  // accumulator columns of an epilogue warp
     static constexpr int kCW = kCols < 32 || (SUM && kCols > 32) ? 16 : 32;   // columns taken out at once
@@ -489,14 +533,14 @@ struct GemmBars {
 // g.chunk k-blocks; the warps that take it out add the chunks up in registers, rounding to nearest.
 template <int CTAS, int BN, bool SUM, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kGemmThreads, 1)
-linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const GemmShape g,
+linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+            const __grid_constant__ CUtensorMap map_y, const __grid_constant__ CUtensorMap map_pre, const GemmShape g,
             const Epi epi, float* __restrict__ part, int64_t ldpart, int* status) {
     using C = GemmCfg<CTAS, BN, SUM>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ GemmBars bars;
     __shared__ alignas(16) float bias_s[kEpiWarps][BN / 4];
-    __shared__ float stg_s[kEpiWarps][kStgBytes / 4];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CTAS == 2 ? cluster_ctarank() : 0;
     if (threadIdx.x == kTmaWarp * 32) {
@@ -686,6 +730,7 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         constexpr int CW = C::kCW, NC = C::kCols / C::kCW;
         const int q = warp & 3, c0 = (warp >> 2) * C::kCols;
         const uint32_t tl = tbase + ((uint32_t)(32 * q) << 16) + c0, bias = smem_u32(bias_s[warp]);
+        uint8_t* stg = smem + C::kStages * C::kStage + warp * C::kStg;
         constexpr int NB = C::kCols > 32 ? C::kCols / 32 : 1;
         float next_b[NB];
         auto fetch_bias = [&](int col) {
@@ -739,8 +784,15 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
 #pragma unroll
                     for (int j = 0; j < CW; ++j) f[j] = SUM ? f[j] + __uint_as_float(v[j]) : __uint_as_float(v[j]);
                     if (!SUM || last) {
-                        if (epi.single && !part) {
-                            if (live > 0) epilogue_single<CW>(epi, row - lane, g.M, col, live, f, bias + 4 * c * CW, stg_s[warp]);
+                        if (C::kBulk && epi.bulk && !part) {
+                            if constexpr (C::kBulk) {
+                                if (live > 0 && row - lane < g.M)
+                                    epilogue_bulk(epi, &map_y, &map_pre, row - lane, g.M, col, live, f, bias + 4 * c * CW,
+                                                  smem_u32(stg));
+                            }
+                        } else if (epi.single && !part) {
+                            if (live > 0) epilogue_single<CW>(epi, row - lane, g.M, col, live, f, bias + 4 * c * CW,
+                                                              reinterpret_cast<float*>(stg));
                         } else if (row < g.M && live > 0) {
                             if (part) put_row<CW>(part, ((int64_t)w.s * g.M + row) * ldpart + col, true, f, (live + 7) & ~7, 2);
                             else epilogue<CW>(epi, row, col, live, f, bias + 4 * c * CW);
@@ -751,6 +803,7 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             }
         }
         if (!ok && lane == 0) tc::fail(&bars.abort, status);
+        if (C::kBulk && lane == 0) bulk_wait();   // the last boxes are written
     }
     tc_fence_before();
     __syncthreads();
@@ -875,8 +928,17 @@ size_t part_floats(const GemmPlan& p) {
 }
 
 template <int CTAS, int BN, bool SUM, bool A_MN, bool B_MN>
-int launch_gemm(const GemmPlan& p, const CUtensorMap& ma, const CUtensorMap& mb, const Epi& epi, float* part,
+int launch_gemm(const GemmPlan& p, const CUtensorMap& ma, const CUtensorMap& mb, const Epi& e, float* part,
                 bool follows, cudaStream_t s) {
+    Epi epi = e;
+    CUtensorMap my{}, mp{};
+    if (GemmCfg<CTAS, BN, SUM>::kBulk && !part && !epi.single && !epi.y_f32 && !epi.pre_f32) {
+        const CUtensorMapDataType ty = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+        if (!make_map_2d(&my, epi.y, ty, p.g.M, p.g.N, epi.ldy * 2, 32, kBoxCols, CU_TENSOR_MAP_SWIZZLE_64B) ||
+            (epi.pre && !make_map_2d(&mp, epi.pre, ty, p.g.M, p.g.N, epi.ldpre * 2, 32, kBoxCols, CU_TENSOR_MAP_SWIZZLE_64B)))
+            return GT_ERR_CUDA;
+        epi.bulk = true;
+    }
     using C = GemmCfg<CTAS, BN, SUM>;
     auto kern = linear_gemm<CTAS, BN, SUM, A_MN, B_MN>;
     static std::atomic<uint64_t> allowed;
@@ -899,7 +961,7 @@ int launch_gemm(const GemmPlan& p, const CUtensorMap& ma, const CUtensorMap& mb,
     cfg.attrs = attr;
     cfg.numAttrs = CTAS;
     LaunchScope ls("linear_gemm", s);
-    return cudaLaunchKernelEx(&cfg, kern, ma, mb, p.g, epi, part, pad8(p.g.N), status) == cudaSuccess ? check_launch()
+    return cudaLaunchKernelEx(&cfg, kern, ma, mb, my, mp, p.g, epi, part, pad8(p.g.N), status) == cudaSuccess ? check_launch()
                                                                                                       : GT_ERR_CUDA;
 }
 
@@ -1058,7 +1120,7 @@ size_t bwd_bufs(int dtype, int m, int k, int n, bool pack_x, bool pack_w, bool o
 
 Epi make_epi(const float* bias, int act, int ytype, int ptype, const void* r, int64_t ldr, int ey, void* y, int64_t ldy,
              void* pre, int64_t ldpre, int ep) {
-    Epi e{bias, r, y, pre, ldr, ldy, ldpre, act == GT_ACT_GELU, ytype == GT_F32, ptype == GT_F32, false,
+    Epi e{bias, r, y, pre, ldr, ldy, ldpre, act == GT_ACT_GELU, ytype == GT_F32, ptype == GT_F32, false, false,
           row_access(r, ldr, ey), row_access(y, ldy, ey), row_access(pre, ldpre, ep)};
     e.single = e.yacc == 0 || (r && e.racc == 0) || (pre && e.pacc == 0);
     return e;
