@@ -139,11 +139,12 @@ struct PrepJobs {
     int count;
 };
 
-// What a thread has in flight covers the latency: 4 rows of 16 bytes of each input, 2 of 32.
+// Two rows of each input are in flight per thread, four CTAs on an SM (measured on da of 32768 x 4096 bf16:
+// 134 us, 89 % of the copy rate; four rows and two CTAs 145 us).
 template <typename TI, int PARTS>
 __device__ __forceinline__ void prep_rows(const PrepJob& J, int bx, int by) {
     using TP = typename std::conditional<PARTS == 3, float, bf16>::type;
-    constexpr int R = PARTS == 3 ? 2 : 4;   // rows in flight per thread
+    constexpr int R = 2;   // rows in flight per thread
     const TI* src = static_cast<const TI*>(J.src);
     const TP* pre = static_cast<const TP*>(J.pre);
     const int m = J.m, n = J.n, tx = J.tx, ty = kPrepThreads / tx;
@@ -218,7 +219,7 @@ __device__ __forceinline__ void prep_rows(const PrepJob& J, int bx, int by) {
 
 // One launch prepares all of a call's operands, a range of CTAs each.
 template <int PARTS>
-__global__ void __launch_bounds__(kPrepThreads) linear_prep(const PrepJobs jobs) {
+__global__ void __launch_bounds__(kPrepThreads, PARTS == 3 ? 3 : 4) linear_prep(const PrepJobs jobs) {
     pdl_trigger();
     int b = blockIdx.x, k = 0;
     while (k + 1 < jobs.count && b >= jobs.j[k].gx * jobs.j[k].gy) {
