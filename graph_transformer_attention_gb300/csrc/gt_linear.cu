@@ -378,10 +378,40 @@ __device__ __forceinline__ void epilogue(const Epi& e, int64_t row, int col, int
 // The same for a whole warp whose lanes hold rows row0 .. row0 + 31 of an M-row result, where some
 // row can only be reached by single elements: blocks of 16 rows x 16 columns pass through the
 // warp's staging tile `stg`, so that the warp's accesses cover 16 consecutive elements of two rows.
+// The second half is a call, which keeps its registers out of the product kernel.
 constexpr int kStgPitch = 17;
 constexpr int kStgBytes = 16 * kStgPitch * 4;
+
+// Rows row, row + 2, ..., row + 14 (below M) of column col, whose sums are v[0], v[2 kStgPitch], ...
+__device__ __noinline__ void finish_column(const Epi* e, int64_t row, int M, int col, float bias, const float* v) {
+    float r[8] = {};
+    if (e->r) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t at = (row + 2 * i) * e->ldr + col;
+            if (row + 2 * i >= M) continue;
+            r[i] = e->y_f32 ? static_cast<const float*>(e->r)[at] : __bfloat162float(static_cast<const bf16*>(e->r)[at]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (row + 2 * i >= M) continue;
+        float a = v[2 * i * kStgPitch] + bias;
+        if (e->pre) {
+            const int64_t at = (row + 2 * i) * e->ldpre + col;
+            if (e->pre_f32) static_cast<float*>(e->pre)[at] = a;
+            else static_cast<bf16*>(e->pre)[at] = __float2bfloat16_rn(a);
+        }
+        if (e->gelu_act) a = gelu2(gauss_constants(), make_float2(a, a)).x;
+        a += r[i];
+        const int64_t at = (row + 2 * i) * e->ldy + col;
+        if (e->y_f32) static_cast<float*>(e->y)[at] = a;
+        else static_cast<bf16*>(e->y)[at] = __float2bfloat16_rn(a);
+    }
+}
+
 template <int CW>
-__device__ __forceinline__ void epilogue_single(const Epi& e, int64_t row0, int M, int col, int live, float (&v)[CW],
+__device__ __forceinline__ void epilogue_single(const Epi& e, int64_t row0, int M, int col, int live, const float (&v)[CW],
                                                 uint32_t bias, float* stg) {
     const int lane = threadIdx.x & 31, c = lane & 15;
 #pragma unroll
@@ -393,26 +423,9 @@ __device__ __forceinline__ void epilogue_single(const Epi& e, int64_t row0, int 
         }
         __syncwarp();
         const int cc = 16 * (h >> 1) + c;
-        const float b = __uint_as_float(lds_u32(bias + 4 * cc));
-#pragma unroll 1
-        for (int p = lane >> 4; p < 16; p += 2) {
-            const int64_t row = row0 + 16 * (h & 1) + p;
-            if (row >= M || cc >= live) break;
-            float a = stg[p * kStgPitch + c] + b;
-            if (e.pre) {
-                const int64_t at = row * e.ldpre + col + cc;
-                if (e.pre_f32) static_cast<float*>(e.pre)[at] = a;
-                else static_cast<bf16*>(e.pre)[at] = __float2bfloat16_rn(a);
-            }
-            if (e.gelu_act) a = gelu2(gauss_constants(), make_float2(a, a)).x;
-            if (e.r) {
-                const int64_t at = row * e.ldr + col + cc;
-                a += e.y_f32 ? static_cast<const float*>(e.r)[at] : __bfloat162float(static_cast<const bf16*>(e.r)[at]);
-            }
-            const int64_t at = row * e.ldy + col + cc;
-            if (e.y_f32) static_cast<float*>(e.y)[at] = a;
-            else static_cast<bf16*>(e.y)[at] = __float2bfloat16_rn(a);
-        }
+        if (cc < live)
+            finish_column(&e, row0 + 16 * (h & 1) + (lane >> 4), M, col + cc, __uint_as_float(lds_u32(bias + 4 * cc)),
+                          stg + (lane >> 4) * kStgPitch + c);
     }
 }
 
@@ -502,7 +515,7 @@ struct GemmCfg {
     static constexpr int kStageB = BN / CTAS * kBK * 2;   // a CTA of a pair holds half of B's columns
     static constexpr int kStage = kStageA + kStageB;
     static constexpr bool kBulk = CTAS == 2 && !SUM;      // bf16 results, which go out as TMA boxes
-    static constexpr int kStages = (kBulk ? 160 : 192) * 1024 / kStage;
+    static constexpr int kStages = (kBulk ? 160 : 192) * 1024 / kStage;   // 5 to 8
     static constexpr int kStg = kBulk ? kBoxBytes : (kStgBytes + 127) / 128 * 128;   // staging of an epilogue warp
     static constexpr int kSmem = kStages * kStage + kEpiWarps * kStg + 1024;
     static constexpr uint32_t kTmemCols = 2 * BN;
@@ -510,8 +523,9 @@ struct GemmCfg {
     static constexpr int kCW = kCols < 32 || (SUM && kCols > 32) ? 16 : 32;   // columns taken out at once
 };
 
+constexpr int kMaxStages = 8;
 struct GemmBars {
-    uint64_t full[8], empty[8];
+    uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t fin;
     uint32_t tmem_base;
@@ -536,7 +550,7 @@ template <int CTAS, int BN, bool SUM, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kGemmThreads, 1)
 linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
             const __grid_constant__ CUtensorMap map_y, const __grid_constant__ CUtensorMap map_pre, const GemmShape g,
-            const Epi epi, float* __restrict__ part, int64_t ldpart, int* status) {
+            const __grid_constant__ Epi epi, float* __restrict__ part, int64_t ldpart, int* status) {
     using C = GemmCfg<CTAS, BN, SUM>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -897,7 +911,7 @@ GemmPlan plan_gemm(int M, int N, int K, int planes, bool f32_out) {
     double best_us = 1e30;
     const int sms = num_sms();
     const int kb = (K + kBK - 1) / kBK;
-    const struct { int ctas, bn; double us_kb; } tiles[3] = {{2, 256, 0.30}, {1, 128, 0.17}, {1, 64, 0.11}};
+    const struct { int ctas, bn; double us_kb; } tiles[3] = {{2, 256, 0.30}, {2, 128, 0.17}, {1, 64, 0.11}};
     for (const auto& t : tiles) {
         const int bm = 128 * t.ctas, units = sms / t.ctas;
         const int tm = (M + bm - 1) / bm, tn = (N + t.bn - 1) / t.bn;
@@ -992,10 +1006,13 @@ int run_gemm(const GemmPlan& p, const Operand& a, const Operand& b, const Epi& e
         return GT_ERR_CUDA;
     float* out = p.g.splits > 1 ? part : nullptr;
     const bool one_chunk = (p.g.kblocks + p.g.splits - 1) / p.g.splits <= p.g.chunk;
-    return p.bn == 256   ? (one_chunk ? launch_gemm<2, 256, false, A_MN, B_MN>(p, ma, mb, epi, out, follows, s)
-                                      : launch_gemm<2, 256, true, A_MN, B_MN>(p, ma, mb, epi, out, follows, s))
-           : p.bn == 128 ? launch_gemm<1, 128, true, A_MN, B_MN>(p, ma, mb, epi, out, follows, s)
-                         : launch_gemm<1, 64, true, A_MN, B_MN>(p, ma, mb, epi, out, follows, s);
+    if (p.bn == 256)
+        return one_chunk ? launch_gemm<2, 256, false, A_MN, B_MN>(p, ma, mb, epi, out, follows, s)
+                         : launch_gemm<2, 256, true, A_MN, B_MN>(p, ma, mb, epi, out, follows, s);
+    if (p.bn == 128)
+        return one_chunk ? launch_gemm<2, 128, false, A_MN, B_MN>(p, ma, mb, epi, out, follows, s)
+                         : launch_gemm<2, 128, true, A_MN, B_MN>(p, ma, mb, epi, out, follows, s);
+    return launch_gemm<1, 64, true, A_MN, B_MN>(p, ma, mb, epi, out, follows, s);
 }
 
 // The join of p's splits (if it has any) and the column sums (if any), in one launch.
