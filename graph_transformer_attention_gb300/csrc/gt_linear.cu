@@ -532,6 +532,29 @@ struct GemmBars {
     int abort;
 };
 
+// A warp's walk round a ring of stage barriers.  A successful wait takes over 100 cycles from issue to
+// use, which a step cannot hide, so the barrier of the next stage is asked about a step ahead (measured
+// on a step of a wait, an election and an arrival: 281 cycles, 144 with the question ahead).
+template <int STAGES>
+struct Ring {
+    uint64_t* bar;
+    uint32_t st, parity;
+    bool ahead;
+    __device__ __forceinline__ Ring(uint64_t* b, uint32_t p) : bar(b), st(0), parity(p) { ahead = mbar_test(bar, p); }
+    // Waits for the current stage, names it in `s` and moves on; false where the wait gave up.
+    __device__ __forceinline__ bool next(uint32_t& s, volatile int* abort_flag) {
+        s = st;
+        bool ok = true;
+        if (!__all_sync(0xffffffffu, ahead)) ok = mbar_wait_all(bar + st, parity, abort_flag, tc::kWaitNs);
+        if (++st == STAGES) {
+            st = 0;
+            parity ^= 1u;
+        }
+        ahead = mbar_test(bar + st, parity);
+        return ok;
+    }
+};
+
 // D = A B.  A is [M][contraction] (A_MN false) or [contraction][M] (true), B is
 // [N][contraction] (B_MN false) or [contraction][N] (true).  part NULL: the
 // finished sums go through `epi`; else split s stores its sums at
@@ -594,43 +617,45 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
         auto feed = [&](auto is_a_, auto mn_, const CUtensorMap& map, bool whole, int across) {
             constexpr bool is_a = decltype(is_a_)::value, mn = decltype(mn_)::value;
             constexpr int blocks = is_a ? 2 : BN / CTAS / 64;
-            uint32_t st = 0, round = 0;   // stage, and times round the ring
+            Ring<C::kStages> ring(bars.empty, 1);   // the first time round finds every stage empty
+            uint32_t loads = 0;
             bool ok = true;
+            const uint32_t full0 = CTAS == 2 ? map_to_rank(bars.full, 0) : 0;   // a pair's stages count on its first CTA's barriers
+            auto load_stage = [&](uint32_t st, int kb, int r0, int plane) {
+                if (elect_one()) {
+                    uint64_t* full = &bars.full[st];
+                    if (is_a && rank == 0) mbar_arrive_expect_tx(full, CTAS * C::kStage);
+                    uint8_t* dst = smem + st * C::kStage + (is_a ? 0 : kStageA);
+                    auto load = [&](int at, int x, int y, int z) {
+                        if (CTAS == 2) tma_load_4d_pair(dst + at, &map, x, y, z, plane, full0 + 8 * st);
+                        else tma_load_4d(dst + at, &map, x, y, z, plane, full);
+                    };
+                    if (!mn) {
+                        load(0, kb * kBK, r0, 0);
+                    } else if (whole) {
+                        load(0, 0, kb * kBK, r0 / 64);
+                    } else {
+#pragma unroll
+                        for (int b = 0; b < blocks; ++b) load(b * 8192, r0 + 64 * b, kb * kBK, 0);
+                    }
+                }
+                __syncwarp();
+            };
             for (int i = first; ok && i < items; i += stride) {
                 const Item w = item_of(g, i);
                 const int r0 = (is_a ? w.m : w.n) * across * CTAS + across * (int)rank;
-                for (int kb = w.lo; ok && kb < w.hi; ++kb) {
-                    for (int j = 0; j < g.planes; ++j) {
-                        const int plane = g.planes == 1 ? 0 : j == 0 ? 2 : j - 1;   // lo, hi, mid: as they are used
-                        if (round > 0 && !mbar_wait_all(&bars.empty[st], (round - 1) & 1, abort_flag, tc::kWaitNs)) {
-                            ok = false;
-                            break;
-                        }
-                        if (elect_one()) {
-                            uint64_t* full = &bars.full[st];
-                            // both halves of a pair's stage count on the first CTA's barrier
-                            const uint32_t pair_full = CTAS == 2 ? map_to_rank(full, 0) : 0;
-                            if (is_a && rank == 0) mbar_arrive_expect_tx(full, CTAS * C::kStage);
-                            uint8_t* dst = smem + st * C::kStage + (is_a ? 0 : kStageA);
-                            auto load = [&](int at, int x, int y, int z) {
-                                if (CTAS == 2) tma_load_4d_pair(dst + at, &map, x, y, z, plane, pair_full);
-                                else tma_load_4d(dst + at, &map, x, y, z, plane, full);
-                            };
-                            if (!mn) {
-                                load(0, kb * kBK, r0, 0);
-                            } else if (whole) {
-                                load(0, 0, kb * kBK, r0 / 64);
-                            } else {
-#pragma unroll
-                                for (int b = 0; b < blocks; ++b) load(b * 8192, r0 + 64 * b, kb * kBK, 0);
-                            }
-                        }
-                        __syncwarp();
-                        if (++st == C::kStages) {
-                            st = 0;
-                            ++round;
-                        }
+                uint32_t st;
+                if (g.planes == 1) {
+                    for (int kb = w.lo; kb < w.hi; ++kb, ++loads) {
+                        if (!(ok = ring.next(st, abort_flag))) break;
+                        load_stage(st, kb, r0, 0);
                     }
+                } else {
+                    for (int kb = w.lo; ok && kb < w.hi; ++kb)
+                        for (int j = 0; j < 3; ++j, ++loads) {
+                            if (!(ok = ring.next(st, abort_flag))) break;
+                            load_stage(st, kb, r0, j == 0 ? 2 : j - 1);   // lo, hi, mid: as they are used
+                        }
                 }
             }
             if (!ok && lane == 0) tc::fail(&bars.abort, status);
@@ -639,12 +664,10 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             // consumed by products that have completed.  (A pair's second CTA has no barrier of its
             // own for its loads; where its wait gave up, they were issued that wait's limit ago.)
             int never = 0;
-            for (int k = 0; k < C::kStages; ++k) {   // from the oldest stage on
-                const uint32_t times = k < (int)(C::kStages - st) ? round : round + 1;   // loads of stage (st + k) % kStages
-                const uint32_t s = st + k < (uint32_t)C::kStages ? st + k : st + k - C::kStages;
-                if (times == 0) continue;
-                if (rank == 0) mbar_wait_all(&bars.full[s], (times - 1) & 1, &never, tc::kWaitNs);
-                if (ok) ok = mbar_wait_all(&bars.empty[s], (times - 1) & 1, abort_flag, tc::kWaitNs);
+            for (uint32_t b = loads > (uint32_t)C::kStages ? loads - C::kStages : 0; b < loads; ++b) {
+                const uint32_t s = b % C::kStages, p = (b / C::kStages) & 1;
+                if (rank == 0) mbar_wait_all(&bars.full[s], p, &never, tc::kWaitNs);
+                if (ok) ok = mbar_wait_all(&bars.empty[s], p, abort_flag, tc::kWaitNs);
             }
         };
         using Yes = std::true_type;
@@ -658,15 +681,11 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
             // row: 64-element blocks 8192 bytes apart, 8-deep groups 1024 bytes apart, 2048 bytes per k-step
             const SmemDesc da = smem_desc_split(smem_u32(smem), A_MN ? 8192 : 16, 1024, 2);
             const SmemDesc db = smem_desc_split(smem_u32(smem) + kStageA, B_MN ? 8192 : 16, 1024, 2);
-            uint32_t st = 0, phase = 0, n = 0;   // the next stage and the parity of its loads
+            Ring<C::kStages> ring(bars.full, 0);
+            uint32_t n = 0;
             bool ok = true;
-            auto landed = [&](uint32_t& s) {     // waits for the next stage, and names it
-                s = st;
-                const bool got = mbar_wait_all(&bars.full[st], phase, abort_flag, tc::kWaitNs);
-                if (++st == C::kStages) {
-                    st = 0;
-                    phase ^= 1u;
-                }
+            auto landed = [&](uint32_t& s) {
+                const bool got = ring.next(s, abort_flag);
                 tc_fence_after();
                 return got;
             };
