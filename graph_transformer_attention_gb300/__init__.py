@@ -565,11 +565,12 @@ def gt_linear_fwd(x, w, b=None, act: int = GT_ACT_NONE, r=None, out_dtype=None, 
     if pre is None and save_pre:
         pre = torch.empty((m, n), dtype=xt, device=dev)
     pp, ldp = (None, 0) if pre is None else (pre.data_ptr(), _matrix("pre", pre, m, n, xt, dev))
-    xp, wp = x.data_ptr(), w.data_ptr()
-    # rows of whole 16 bytes: a multiple of 8 bf16 (fp32 is split in the workspace in any case)
-    aligned = (xp | wp) % 16 == 0 and (ldx | ldw) % 8 == 0
+    xp, wp, yp = x.data_ptr(), w.data_ptr(), out.data_ptr()
+    # rows of whole 16 bytes
+    ex, ey = x.element_size(), out.element_size()
+    aligned = (xp | wp | yp | (rp or 0) | (pp or 0) | (ldx | ldw | ldp) * ex | (ldy | ldr) * ey) % 16 == 0
     workspace, sp, sn = _room(workspace, _linear_fwd_room(dev.index, dt, m, k, n, aligned), dev)
-    rc = lib.gt_linear_fwd(dt, _dtype_code(out), m, k, n, xp, ldx, wp, ldw, bp, act, rp, ldr, out.data_ptr(), ldy, pp,
+    rc = lib.gt_linear_fwd(dt, _dtype_code(out), m, k, n, xp, ldx, wp, ldw, bp, act, rp, ldr, yp, ldy, pp,
                            ldp, sp, sn, _raw_stream(dev.index))
     if rc:
         raise GtError("gt_linear_fwd", rc)
@@ -604,7 +605,8 @@ def gt_linear_bwd(dy, x, w, pre=None, act: int = GT_ACT_NONE, dx_add=None, need_
     dwp, lddw = (None, 0) if dw is None else (dw.data_ptr(), _matrix("dw", dw, k, n, xt, dev))
     dbp = None if db is None else _vector("db", db, n, dev)
     xp, wp, dyp = x.data_ptr(), w.data_ptr(), dy.data_ptr()
-    aligned = (xp | wp | dyp) % 16 == 0 and (ldx | ldw | lddy) % 8 == 0
+    aligned = (xp | wp | dyp | (pp or 0) | (ap or 0) | (dxp or 0) | (dwp or 0) | lddy * dy.element_size() |
+               (ldx | ldw | ldp | lda | lddx | lddw) * x.element_size()) % 16 == 0
     workspace, sp, sn = _room(workspace, _linear_bwd_room(dev.index, dt, yt, m, k, n, act, aligned), dev)
     rc = lib.gt_linear_bwd(dt, yt, m, k, n, dyp, lddy, xp, ldx, wp, ldw, pp, ldp, act, ap, lda, dxp, lddx, dwp, lddw,
                            dbp, sp, sn, _raw_stream(dev.index))

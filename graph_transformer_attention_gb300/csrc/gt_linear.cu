@@ -247,7 +247,7 @@ struct Epi {
     void* pre;
     int64_t ldr, ldy, ldpre;
     bool gelu_act, y_f32, pre_f32;
-    bool single;   // some rows can only be reached by single elements
+    bool single;   // some rows can only be reached by single elements: left to linear_join
     bool bulk;     // bf16 results go out as TMA boxes (the pair kernel; maps in the kernel's arguments)
     int racc, yacc, pacc;
 };
@@ -375,60 +375,6 @@ __device__ __forceinline__ void epilogue(const Epi& e, int64_t row, int col, int
     put_row<CW>(e.y, row * e.ldy + col, e.y_f32, v, live, e.yacc);
 }
 
-// The same for a whole warp whose lanes hold rows row0 .. row0 + 31 of an M-row result, where some
-// row can only be reached by single elements: blocks of 16 rows x 16 columns pass through the
-// warp's staging tile `stg`, so that the warp's accesses cover 16 consecutive elements of two rows.
-// The second half is a call, which keeps its registers out of the product kernel.
-constexpr int kStgPitch = 17;
-constexpr int kStgBytes = 16 * kStgPitch * 4;
-
-// Rows row, row + 2, ..., row + 14 (below M) of column col, whose sums are v[0], v[2 kStgPitch], ...
-__device__ __noinline__ void finish_column(const Epi* e, int64_t row, int M, int col, float bias, const float* v) {
-    float r[8] = {};
-    if (e->r) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t at = (row + 2 * i) * e->ldr + col;
-            if (row + 2 * i >= M) continue;
-            r[i] = e->y_f32 ? static_cast<const float*>(e->r)[at] : __bfloat162float(static_cast<const bf16*>(e->r)[at]);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (row + 2 * i >= M) continue;
-        float a = v[2 * i * kStgPitch] + bias;
-        if (e->pre) {
-            const int64_t at = (row + 2 * i) * e->ldpre + col;
-            if (e->pre_f32) static_cast<float*>(e->pre)[at] = a;
-            else static_cast<bf16*>(e->pre)[at] = __float2bfloat16_rn(a);
-        }
-        if (e->gelu_act) a = gelu2(gauss_constants(), make_float2(a, a)).x;
-        a += r[i];
-        const int64_t at = (row + 2 * i) * e->ldy + col;
-        if (e->y_f32) static_cast<float*>(e->y)[at] = a;
-        else static_cast<bf16*>(e->y)[at] = __float2bfloat16_rn(a);
-    }
-}
-
-template <int CW>
-__device__ __forceinline__ void epilogue_single(const Epi& e, int64_t row0, int M, int col, int live, const float (&v)[CW],
-                                                uint32_t bias, float* stg) {
-    const int lane = threadIdx.x & 31, c = lane & 15;
-#pragma unroll
-    for (int h = 0; h < 2 * (CW / 16); ++h) {
-        __syncwarp();
-        if ((lane >> 4) == (h & 1)) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) stg[c * kStgPitch + i] = v[16 * (h >> 1) + i];
-        }
-        __syncwarp();
-        const int cc = 16 * (h >> 1) + c;
-        if (cc < live)
-            finish_column(&e, row0 + 16 * (h & 1) + (lane >> 4), M, col + cc, __uint_as_float(lds_u32(bias + 4 * cc)),
-                          stg + (lane >> 4) * kStgPitch + c);
-    }
-}
-
 // The same for a whole warp and 32 columns of bf16 results, through the warp's 2 KB staging tile and
 // TMA: rows of 64 bytes, 64-byte swizzle.  A lane's row in 32-byte pieces costs the L1 four times
 // the cycles of whole lines, and the products need that memory's bandwidth (32768x1024x4096, GELU and pre: 195 -> 185 us alone).
@@ -516,7 +462,7 @@ struct GemmCfg {
     static constexpr int kStage = kStageA + kStageB;
     static constexpr bool kBulk = CTAS == 2 && !SUM;      // bf16 results, which go out as TMA boxes
     static constexpr int kStages = (kBulk ? 160 : 192) * 1024 / kStage;   // 5 to 8
-    static constexpr int kStg = kBulk ? kBoxBytes : (kStgBytes + 127) / 128 * 128;   // staging of an epilogue warp
+    static constexpr int kStg = kBulk ? kBoxBytes : 0;    // staging of an epilogue warp
     static constexpr int kSmem = kStages * kStage + kEpiWarps * kStg + 1024;
     static constexpr uint32_t kTmemCols = 2 * BN;
     static constexpr int kCols = BN / 4;                  // accumulator columns of an epilogue warp
@@ -824,9 +770,6 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
                                     epilogue_bulk(epi, &map_y, &map_pre, row - lane, g.M, col, live, f, bias + 4 * c * CW,
                                                   smem_u32(stg));
                             }
-                        } else if (epi.single && !part) {
-                            if (live > 0) epilogue_single<CW>(epi, row - lane, g.M, col, live, f, bias + 4 * c * CW,
-                                                              reinterpret_cast<float*>(stg));
                         } else if (row < g.M && live > 0) {
                             if (part) put_row<CW>(part, ((int64_t)w.s * g.M + row) * ldpart + col, true, f, (live + 7) & ~7, 2);
                             else epilogue<CW>(epi, row, col, live, f, bias + 4 * c * CW);
@@ -849,15 +792,31 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     }
 }
 
-// The end of a call in one launch: the splits' sums added in a fixed order, then the epilogue (CTAs
-// below `join`, a thread per 8 columns), and the column sums of the preparation's partial rows (the
-// CTAs from there on, 32 columns each, as col_sum in gt_norm.cu).
+// The end of a call in one launch: the sums that the product kernel left (of the contraction's splits,
+// added in a fixed order, and any whose rows can only be reached by single elements) through the
+// epilogue (CTAs below `join`), and the column sums of the preparation's partial rows (the CTAs from there on,
+// 32 columns each, as col_sum in gt_norm.cu).  A thread takes 8 consecutive columns of a row, or
+// single: every 32nd of 256, so that a warp's accesses are consecutive elements (4099 x 321 x 1001, fp32 y and
+// residual: 58 us with those in the product kernel's epilogue, where a lane holds a row, 14 + 14 us so).
 constexpr int kJoinThreads = 256;
 struct ColSum {
     const float* part;
     float* out;
     int rows, cols;
 };
+
+__host__ __device__ __forceinline__ int64_t join_threads(int m, int n, bool single) {
+    return (int64_t)m * (single ? (n + 255) / 256 * 32 : (n + 7) / 8);
+}
+
+__device__ __forceinline__ float load_one(const void* p, int64_t at, bool f32) {
+    return f32 ? static_cast<const float*>(p)[at] : __bfloat162float(static_cast<const bf16*>(p)[at]);
+}
+__device__ __forceinline__ void store_one(void* p, int64_t at, bool f32, float v) {
+    if (f32) static_cast<float*>(p)[at] = v;
+    else static_cast<bf16*>(p)[at] = __float2bfloat16_rn(v);
+}
+
 __global__ void __launch_bounds__(kJoinThreads)
 linear_join(int join, int m, int n, int splits, const float* __restrict__ part, int64_t ldpart, const Epi epi,
             const ColSum cs) {
@@ -871,7 +830,7 @@ linear_join(int join, int m, int n, int splits, const float* __restrict__ part, 
         float acc = 0.f;
         if (i < cs.cols) {
 #pragma unroll 8
-            for (int p = ty; p < cs.rows; p += kJoinThreads / 32) acc += cs.part[(int64_t)p * cs.cols + i];
+            for (int p = ty; p < cs.rows; p += kJoinThreads / 32) acc += __ldcg(cs.part + (int64_t)p * cs.cols + i);
         }
         red[tx][ty] = acc;
         __syncthreads();
@@ -883,16 +842,43 @@ linear_join(int join, int m, int n, int splits, const float* __restrict__ part, 
         }
         return;
     }
-    const int per_row = (n + 7) / 8;
     const int64_t idx = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x;
-    if (idx >= (int64_t)m * per_row) return;
+    if (idx >= join_threads(m, n, epi.single)) return;
+    const int64_t plane = (int64_t)m * ldpart;
+    float v[8] = {};
+    if (epi.single) {
+        const int per_row = (n + 255) / 256 * 32;
+        const int64_t row = idx / per_row;
+        const int at = (int)(idx - row * per_row), col = at / 32 * 256 + at % 32;   // then col + 32, ...
+        for (int s = 0; s < splits; ++s)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (col + 32 * i < n) v[i] += __ldcg(part + s * plane + row * ldpart + col + 32 * i);
+        float r[8] = {};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (col + 32 * i >= n) continue;
+            if (epi.r) r[i] = load_one(epi.r, row * epi.ldr + col + 32 * i, epi.y_f32);
+            if (epi.bias) v[i] += __ldg(epi.bias + col + 32 * i);
+        }
+        if (epi.pre) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (col + 32 * i < n) store_one(epi.pre, row * epi.ldpre + col + 32 * i, epi.pre_f32, v[i]);
+        }
+        if (epi.gelu_act) apply_gelu<8>(v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (col + 32 * i < n) store_one(epi.y, row * epi.ldy + col + 32 * i, epi.y_f32, v[i] + r[i]);
+        return;
+    }
+    const int per_row = (n + 7) / 8;
     const int64_t row = idx / per_row;
     const int col = (int)(idx - row * per_row) * 8, live = n - col;
-    float v[8] = {};
 #pragma unroll 4
     for (int s = 0; s < splits; ++s) {
         float f[8];
-        unpack8(load8_cg(part + ((int64_t)s * m + row) * ldpart + col), f);
+        unpack8(load8_cg(part + s * plane + row * ldpart + col), f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += f[i];
     }
@@ -957,8 +943,9 @@ GemmPlan plan_gemm(int M, int N, int K, int planes, bool f32_out) {
     return best;
 }
 
-size_t part_floats(const GemmPlan& p) {
-    return p.g.splits > 1 ? (size_t)p.g.splits * p.g.M * pad8(p.g.N) : 0;
+// Floats of the sums that the product kernel leaves to linear_join.
+size_t part_floats(const GemmPlan& p, bool single) {
+    return p.g.splits > 1 || single ? (size_t)p.g.splits * p.g.M * pad8(p.g.N) : 0;
 }
 
 template <int CTAS, int BN, bool SUM, bool A_MN, bool B_MN>
@@ -1023,7 +1010,7 @@ int run_gemm(const GemmPlan& p, const Operand& a, const Operand& b, const Epi& e
     CUtensorMap ma, mb;
     if (!operand_map(&ma, a, A_MN, p.g.whole_a, 128) || !operand_map(&mb, b, B_MN, p.g.whole_b, p.bn / p.ctas))
         return GT_ERR_CUDA;
-    float* out = p.g.splits > 1 ? part : nullptr;
+    float* out = p.g.splits > 1 || epi.single ? part : nullptr;
     const bool one_chunk = (p.g.kblocks + p.g.splits - 1) / p.g.splits <= p.g.chunk;
     if (p.bn == 256)
         return one_chunk ? launch_gemm<2, 256, false, A_MN, B_MN>(p, ma, mb, epi, out, follows, s)
@@ -1034,12 +1021,12 @@ int run_gemm(const GemmPlan& p, const Operand& a, const Operand& b, const Epi& e
     return launch_gemm<1, 64, true, A_MN, B_MN>(p, ma, mb, epi, out, follows, s);
 }
 
-// The join of p's splits (if it has any) and the column sums (if any), in one launch.
+// linear_join of p's sums (if it has left any) and the column sums (if any).
 int run_join(const GemmPlan* p, const float* part, const Epi& epi, const ColSum& cs, cudaStream_t s) {
-    const bool join = p && p->g.splits > 1;
+    const bool join = p && (p->g.splits > 1 || epi.single);
     if (!join && !cs.out) return GT_OK;
     const int M = join ? p->g.M : 0, N = join ? p->g.N : 0;
-    const int nj = (int)(((int64_t)M * ((N + 7) / 8) + kJoinThreads - 1) / kJoinThreads);
+    const int nj = (int)((join_threads(M, N, epi.single) + kJoinThreads - 1) / kJoinThreads);
     const int nc = cs.out ? (cs.cols + 31) / 32 : 0;
     LaunchScope ls("linear_join", s);
     if (launch_overlapped(linear_join, dim3(nj + nc), dim3(kJoinThreads), 0, s, nj, M, N, join ? p->g.splits : 0, part,
@@ -1123,13 +1110,13 @@ struct FwdBufs {
     bf16 *x, *w;
     float* part;
 };
-size_t fwd_bufs(int dtype, bool y_f32, int m, int k, int n, bool pack_x, bool pack_w, void* ws, size_t bytes,
-                FwdBufs* out) {
+size_t fwd_bufs(int dtype, bool y_f32, int m, int k, int n, bool pack_x, bool pack_w, bool single, void* ws,
+                size_t bytes, FwdBufs* out) {
     Carve c(ws, bytes);
     FwdBufs b;
     b.x = pack_x ? c.take<bf16>(operand_elems(dtype, m, k)) : nullptr;
     b.w = pack_w ? c.take<bf16>(operand_elems(dtype, k, n)) : nullptr;
-    b.part = c.take<float>(part_floats(plan_gemm(m, n, k, planes_of(dtype), y_f32)));
+    b.part = c.take<float>(part_floats(plan_gemm(m, n, k, planes_of(dtype), y_f32), single));
     if (out) *out = b;
     return c.off;
 }
@@ -1140,15 +1127,15 @@ struct BwdBufs {
     bf16 *x, *w, *da;
     float *part, *cols;
 };
-size_t bwd_bufs(int dtype, int m, int k, int n, bool pack_x, bool pack_w, bool own_da, void* ws, size_t bytes,
-                BwdBufs* out) {
+size_t bwd_bufs(int dtype, int m, int k, int n, bool pack_x, bool pack_w, bool own_da, bool single_x, bool single_w,
+                void* ws, size_t bytes, BwdBufs* out) {
     Carve c(ws, bytes);
     BwdBufs b;
     b.x = pack_x ? c.take<bf16>(operand_elems(dtype, m, k)) : nullptr;
     b.w = pack_w ? c.take<bf16>(operand_elems(dtype, k, n)) : nullptr;
     b.da = own_da ? c.take<bf16>(operand_elems(dtype, m, n)) : nullptr;
-    const size_t px = part_floats(plan_gemm(m, k, n, planes_of(dtype), dtype == GT_F32));
-    const size_t pw = part_floats(plan_gemm(k, n, m, planes_of(dtype), dtype == GT_F32));
+    const size_t px = part_floats(plan_gemm(m, k, n, planes_of(dtype), dtype == GT_F32), single_x);
+    const size_t pw = part_floats(plan_gemm(k, n, m, planes_of(dtype), dtype == GT_F32), single_w);
     b.part = c.take<float>(px > pw ? px : pw);
     b.cols = c.take<float>((size_t)prep_grid(m, n).gy * n);
     if (out) *out = b;
@@ -1174,7 +1161,9 @@ size_t gt_linear_fwd_workspace_size(int32_t dtype, int32_t m, int32_t k, int32_t
     using namespace gt;
     if (check_linear(dtype, GT_F32, m, k, n, GT_ACT_NONE) != GT_OK) return 0;
     const bool pack = dtype == GT_F32 || !aligned;
-    return fwd_bufs(dtype, false, m, k, n, pack, pack, nullptr, 0, nullptr);
+    const size_t a = fwd_bufs(dtype, false, m, k, n, pack, pack, !aligned, nullptr, 0, nullptr);
+    const size_t b = fwd_bufs(dtype, true, m, k, n, pack, pack, !aligned, nullptr, 0, nullptr);
+    return a > b ? a : b;   // for either type of y
 }
 
 size_t gt_linear_bwd_workspace_size(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n, int32_t act,
@@ -1182,7 +1171,8 @@ size_t gt_linear_bwd_workspace_size(int32_t dtype, int32_t ytype, int32_t m, int
     using namespace gt;
     if (check_linear(dtype, ytype, m, k, n, act) != GT_OK) return 0;
     const bool pack = dtype == GT_F32 || !aligned;
-    return bwd_bufs(dtype, m, k, n, pack, pack, pack || act != GT_ACT_NONE || ytype != dtype, nullptr, 0, nullptr);
+    return bwd_bufs(dtype, m, k, n, pack, pack, pack || act != GT_ACT_NONE || ytype != dtype, !aligned, !aligned, nullptr, 0,
+                    nullptr);
 }
 
 int gt_linear_fwd(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n, const void* x, int64_t ldx,
@@ -1194,15 +1184,15 @@ int gt_linear_fwd(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n,
     if (!x || !w || !y || ldx < k || ldw < n || ldy < n || !ranges_ok(r, ldr, n) || !ranges_ok(pre, ldpre, n))
         return GT_ERR_INVALID_ARG;
     const bool pack_x = dtype == GT_F32 || !rows16(x, ldx, 2), pack_w = dtype == GT_F32 || !rows16(w, ldw, 2);
+    const int ey = elem_bytes(ytype), ex = elem_bytes(dtype);
+    const Epi epi = make_epi(b, act, ytype, dtype, r, ldr, ey, y, ldy, pre, ldpre, ex);
     FwdBufs bufs;
-    const size_t need = fwd_bufs(dtype, ytype == GT_F32, m, k, n, pack_x, pack_w, workspace, ws_bytes, &bufs);
+    const size_t need = fwd_bufs(dtype, ytype == GT_F32, m, k, n, pack_x, pack_w, epi.single, workspace, ws_bytes, &bufs);
     if (need > 0 && (!workspace || !aligned16(workspace) || ws_bytes < need)) return GT_ERR_WORKSPACE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     Prep prep{dtype};
     const Operand ox = prep.operand(m, k, x, ldx, bufs.x), ow = prep.operand(k, n, w, ldw, bufs.w);
     if ((rc = prep.launch(s)) != GT_OK) return rc;
-    const int ey = elem_bytes(ytype), ex = elem_bytes(dtype);
-    const Epi epi = make_epi(b, act, ytype, dtype, r, ldr, ey, y, ldy, pre, ldpre, ex);
     const GemmPlan plan = plan_gemm(m, n, k, planes_of(dtype), ytype == GT_F32);
     if ((rc = run_gemm<false, true>(plan, ox, ow, epi, bufs.part, prep.jobs.count > 0, s)) != GT_OK) return rc;
     return run_join(&plan, bufs.part, epi, ColSum{}, s);
@@ -1223,8 +1213,12 @@ int gt_linear_bwd(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n,
     const bool pack_x = dw && (dtype == GT_F32 || !rows16(x, ldx, 2));
     const bool pack_w = dx && (dtype == GT_F32 || !rows16(w, ldw, 2));
     const bool own_da = products && (dtype == GT_F32 || ytype != dtype || act != GT_ACT_NONE || !rows16(dy, lddy, 2));
+    const int ex = elem_bytes(dtype);
+    const Epi epi_x = make_epi(nullptr, GT_ACT_NONE, dtype, dtype, add, ldadd, ex, dx, lddx, nullptr, 0, ex);
+    const Epi epi_w = make_epi(nullptr, GT_ACT_NONE, dtype, dtype, nullptr, 0, ex, dw, lddw, nullptr, 0, ex);
     BwdBufs bufs;
-    const size_t need = bwd_bufs(dtype, m, k, n, pack_x, pack_w, own_da, workspace, ws_bytes, &bufs);
+    const size_t need = bwd_bufs(dtype, m, k, n, pack_x, pack_w, own_da, dx && epi_x.single, dw && epi_w.single, workspace,
+                                 ws_bytes, &bufs);
     if (!workspace || !aligned16(workspace) || ws_bytes < need) return GT_ERR_WORKSPACE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     Prep prep{dtype};
@@ -1235,25 +1229,21 @@ int gt_linear_bwd(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n,
     if (dw) ox = prep.operand(m, k, x, ldx, bufs.x);
     if ((rc = prep.launch(s)) != GT_OK) return rc;
     bool follows = prep.jobs.count > 0;
-    const int ex = elem_bytes(dtype);
     const bool f32 = dtype == GT_F32;
-    ColSum cs{db ? bufs.cols : nullptr, db, prep_grid(m, n).gy, n};
-    Epi epi{};
+    const ColSum cs{db ? bufs.cols : nullptr, db, prep_grid(m, n).gy, n};
     if (dx) {
         const GemmPlan plan = plan_gemm(m, k, n, planes_of(dtype), f32);
-        epi = make_epi(nullptr, GT_ACT_NONE, dtype, dtype, add, ldadd, ex, dx, lddx, nullptr, 0, ex);
-        if ((rc = run_gemm<false, false>(plan, oda, ow, epi, bufs.part, follows, s)) != GT_OK) return rc;
+        if ((rc = run_gemm<false, false>(plan, oda, ow, epi_x, bufs.part, follows, s)) != GT_OK) return rc;
         follows = true;
         // the column sums go with the last join, or with this one if it is the last
-        if ((rc = run_join(&plan, bufs.part, epi, dw ? ColSum{} : cs, s)) != GT_OK) return rc;
+        if ((rc = run_join(&plan, bufs.part, epi_x, dw ? ColSum{} : cs, s)) != GT_OK) return rc;
     }
     if (dw) {
         const GemmPlan plan = plan_gemm(k, n, m, planes_of(dtype), f32);
-        epi = make_epi(nullptr, GT_ACT_NONE, dtype, dtype, nullptr, 0, ex, dw, lddw, nullptr, 0, ex);
-        if ((rc = run_gemm<true, true>(plan, ox, oda, epi, bufs.part, follows, s)) != GT_OK) return rc;
-        return run_join(&plan, bufs.part, epi, cs, s);
+        if ((rc = run_gemm<true, true>(plan, ox, oda, epi_w, bufs.part, follows, s)) != GT_OK) return rc;
+        return run_join(&plan, bufs.part, epi_w, cs, s);
     }
-    return dx ? GT_OK : run_join(nullptr, nullptr, epi, cs, s);
+    return dx ? GT_OK : run_join(nullptr, nullptr, epi_x, cs, s);
 }
 
 }  // extern "C"

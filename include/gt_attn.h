@@ -416,8 +416,9 @@ typedef enum { GT_ACT_NONE = 0, GT_ACT_GELU = 1 } gt_act;
  *   y  device [m][ldy >= n] (output); pre device [m][ldpre >= n] or NULL (output): a,
  *   rounded to dtype, which the backward of a GELU layer takes.
  *   workspace: at least gt_linear_fwd_workspace_size bytes (may be NULL where that
- *   is 0).  `aligned`: non-zero when the bases and row strides of x and W are
- *   multiples of 16 bytes; else the size includes the copies that bf16 matrices need.
+ *   is 0).  `aligned`: non-zero when the bases and row strides of all the call's
+ *   matrices are multiples of 16 bytes; else the size includes the copies of x and W
+ *   and the fp32 result ([m][n]) that such rows may need.
  * Supported: 1 <= m <= 2^24, 1 <= k, n <= 65536.
  * Errors: GT_ERR_INVALID_ARG for a NULL x, W or y, an unknown type or activation, m,
  * k or n < 1, or a leading dimension below its row; GT_ERR_UNSUPPORTED for larger
@@ -434,8 +435,8 @@ typedef enum { GT_ACT_NONE = 0, GT_ACT_GELU = 1 } gt_act;
  *          fp32 [n] (outputs, overwritten).
  *   With dtype GT_BF16 da is rounded to bf16 for the two products (db is summed before
  *   that rounding).
- *   workspace: at least gt_linear_bwd_workspace_size bytes (`aligned` as above, for
- *   dy, x and W).
+ *   workspace: at least gt_linear_bwd_workspace_size bytes (`aligned` as above; else
+ *   with copies of dy, x and W and an fp32 result, [m][k] or [k][n]).
  * Errors as the forward's, plus GT_ERR_INVALID_ARG when dx, dw and db are all NULL,
  * pre and act disagree, or add comes without dx.
  */
