@@ -887,6 +887,201 @@ linear_join(int join, int m, int n, int splits, const float* __restrict__ part, 
     epilogue<8>(epi, row, col, live, v, smem_u32(bias_s[threadIdx.x]));
 }
 
+// -------------------------------------------------------------- small products
+//
+// fp32 products of a few tens of millions of multiplications spend their time on launches: here a
+// whole call is one kernel on the fp32 pipes, exact products with no operand split first.  A CTA makes a 64 x 64
+// tile, 4 x 4 sums to a thread, its contraction in steps of 32 through shared memory, the next step's
+// elements in registers meanwhile.  Forward: tiles of y.  Backward: tiles of dx, then tiles of dw, each by a
+// cluster of CTAs that share its rows and add up their sums in a fixed order through each other's shared memory; the
+// first row of these tiles makes db too.  da is formed from dy and pre where it is read.
+// Elements move singly, consecutive ones to consecutive threads, so any rows will do.
+struct Small {
+    const float *x, *w, *dy, *pre;
+    int64_t ldx, ldw, lddy, ldpre;
+    int m, k, n;
+    Epi out, dw;          // y or dx; dw
+    float* db;
+    int tiles;            // of y or dx (backward: their CTAs, whole clusters); then the clusters of dw and db
+};
+
+constexpr int kSmT = 64, kSmK = 32, kSmThreads = 256, kSmPitch = kSmT + 4, kSmCluster = 8;
+
+struct SmallSmem {
+    union {
+        struct {
+            float a[kSmK][kSmPitch], b[kSmK][kSmPitch];
+        } in;
+        struct {
+            float tile[kSmT][kSmT], col[kSmT];   // a CTA's share of a dw tile and of db
+        } out;
+    };
+};
+
+// acc += A B over depths d0 .. d1 - 1: A(i, j) is the tile's row i and B(i, j) its column i at depth j, zero outside, as a
+// pair (v, a): the element is v gelu'(a) where pre is set for that operand (A_DA, B_DA), else v.
+// ALONG: memory runs along the depth.  each(b): every element of B, in the order this thread reads them.
+template <bool A_ALONG, bool B_ALONG, bool A_DA, bool B_DA, typename FA, typename FB, typename FE>
+__device__ __forceinline__ void small_tile(int d0, int d1, FA A, FB B, FE each, bool product, bool gelu,
+                                           float (&acc)[4][4], SmallSmem& S) {
+    constexpr int E = kSmT * kSmK / kSmThreads;
+    const int t = threadIdx.x, tx = t & 15, ty = t >> 4;
+    const GaussK gk = gauss_constants();
+    // element e of a thread: ALONG, depth t % 32, row t / 32 + 8 e; else depth t / 64 + 4 e, row t % 64
+    auto row = [&](bool along, int e) { return along ? t / 32 + 8 * e : t & 63; };
+    auto dep = [&](bool along, int e) { return along ? t & 31 : t / 64 + 4 * e; };
+    float2 a[E], b[E];
+    auto fetch = [&](int at) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            a[e] = product ? A(row(A_ALONG, e), at + dep(A_ALONG, e)) : make_float2(0.f, 0.f);
+            b[e] = B(row(B_ALONG, e), at + dep(B_ALONG, e));
+        }
+    };
+    auto value = [&](bool da, float2 v) { return da && gelu ? v.x * gelu_grad2(gk, make_float2(v.y, v.y)).x : v.x; };
+    fetch(d0);
+    for (int at = d0; at < d1; at += kSmK) {
+        __syncthreads();   // the tile before has been read
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            S.in.a[dep(A_ALONG, e)][row(A_ALONG, e)] = value(A_DA, a[e]);
+            const float v = value(B_DA, b[e]);
+            S.in.b[dep(B_ALONG, e)][row(B_ALONG, e)] = v;
+            each(v);
+        }
+        __syncthreads();
+        if (at + kSmK < d1) fetch(at + kSmK);
+        if (!product) continue;
+#pragma unroll 8
+        for (int d = 0; d < kSmK; ++d) {
+            const float4 u = *reinterpret_cast<const float4*>(&S.in.a[d][4 * ty]);
+            const float4 v = *reinterpret_cast<const float4*>(&S.in.b[d][4 * tx]);
+            const float p[4] = {u.x, u.y, u.z, u.w}, q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(p[i], q[j], acc[i][j]);
+        }
+    }
+}
+
+__device__ __forceinline__ void small_store(const Epi& e, int M, int N, int r0, int c0, float (&acc)[4][4]) {
+    const int row0 = r0 + 4 * (threadIdx.x >> 4), col0 = c0 + 4 * (threadIdx.x & 15);
+    const GaussK gk = gauss_constants();
+    const float* r = static_cast<const float*>(e.r);
+    float b[4], res[4][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        b[j] = e.bias && col0 + j < N ? __ldg(e.bias + col0 + j) : 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            res[i][j] = r && row0 + i < M && col0 + j < N ? r[(row0 + i) * e.ldr + col0 + j] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t row = row0 + i;
+        if (row >= M) break;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int col = col0 + j;
+            if (col >= N) break;
+            float a = acc[i][j] + b[j];
+            if (e.pre) static_cast<float*>(e.pre)[row * e.ldpre + col] = a;
+            if (e.gelu_act) a = gelu2(gk, make_float2(a, a)).x;
+            static_cast<float*>(e.y)[row * e.ldy + col] = a + res[i][j];
+        }
+    }
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+template <bool BACKWARD>
+__global__ void __launch_bounds__(kSmThreads) linear_small(const Small p) {
+    __shared__ alignas(16) SmallSmem S;
+    float acc[4][4] = {};
+    auto none = [](float) {};
+    if constexpr (!BACKWARD) {
+        const int tn = (p.n + kSmT - 1) / kSmT, r0 = blockIdx.x / tn * kSmT, c0 = blockIdx.x % tn * kSmT;
+        small_tile<true, false, false, false>(
+            0, p.k,
+            [&](int i, int d) {
+                return make_float2(r0 + i < p.m && d < p.k ? __ldg(p.x + (int64_t)(r0 + i) * p.ldx + d) : 0.f, 0.f);
+            },
+            [&](int i, int d) {
+                return make_float2(c0 + i < p.n && d < p.k ? __ldg(p.w + (int64_t)d * p.ldw + c0 + i) : 0.f, 0.f);
+            },
+            none, true, false, acc, S);
+        small_store(p.out, p.m, p.n, r0, c0, acc);
+    } else {
+        const bool gelu = p.pre != nullptr;
+        auto da = [&](int row, int col) {
+            const bool in = row < p.m && col < p.n;
+            return make_float2(in ? __ldg(p.dy + (int64_t)row * p.lddy + col) : 0.f,
+                               in && gelu ? __ldg(p.pre + (int64_t)row * p.ldpre + col) : 0.f);
+        };
+        if ((int)blockIdx.x < p.tiles) {
+            const int tn = (p.k + kSmT - 1) / kSmT, r0 = blockIdx.x / tn * kSmT, c0 = blockIdx.x % tn * kSmT;
+            if (r0 >= p.m) return;   // up to a whole cluster; its CTAs share nothing
+            small_tile<true, true, true, false>(
+                0, p.n, [&](int i, int d) { return da(r0 + i, d); },
+                [&](int i, int d) {
+                    return make_float2(c0 + i < p.k && d < p.n ? __ldg(p.w + (int64_t)(c0 + i) * p.ldw + d) : 0.f, 0.f);
+                },
+                none, true, gelu, acc, S);
+            small_store(p.out, p.m, p.k, r0, c0, acc);
+        } else {
+            const int b = (blockIdx.x - p.tiles) / kSmCluster, tn = (p.n + kSmT - 1) / kSmT;
+            const int r0 = b / tn * kSmT, c0 = b % tn * kSmT;
+            const int rank = (int)cluster_ctarank();
+            const bool product = p.dw.y != nullptr;
+            const int t = threadIdx.x;
+            float sum = 0.f;   // of column c0 + t % 64, over a quarter of this CTA's rows
+            const int lo = (int)((int64_t)p.m * rank / kSmCluster), hi = (int)((int64_t)p.m * (rank + 1) / kSmCluster);
+            small_tile<false, false, false, true>(
+                lo, hi,
+                [&](int i, int d) {
+                    return make_float2(r0 + i < p.k && d < hi ? __ldg(p.x + (int64_t)d * p.ldx + r0 + i) : 0.f, 0.f);
+                },
+                [&](int i, int d) { return d < hi ? da(d, c0 + i) : make_float2(0.f, 0.f); }, [&](float v) { sum += v; },
+                product, gelu, acc, S);
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) S.out.tile[4 * (t >> 4) + i][4 * (t & 15) + j] = acc[i][j];
+            if (t < kSmT) S.out.col[t] = 0.f;
+            for (int q = 0; q < kSmThreads / kSmT; ++q) {   // the quarters in order
+                __syncthreads();
+                if (t / kSmT == q) S.out.col[t & 63] += sum;
+            }
+            cluster_sync();
+            // rows 8 rank .. 8 rank + 7 of the tile, and the first CTA its part of db
+            if (product) {
+#pragma unroll
+                for (int e = 0; e < kSmT * kSmT / kSmCluster / kSmThreads; ++e) {
+                    const int i = kSmT / kSmCluster * rank + t / 64 + 4 * e, j = t & 63;
+                    float v = 0.f;
+#pragma unroll
+                    for (int q = 0; q < kSmCluster; ++q) v += ld_cluster_f32(map_to_rank(&S.out.tile[i][j], q));
+                    if (r0 + i < p.k && c0 + j < p.n)
+                        static_cast<float*>(p.dw.y)[(int64_t)(r0 + i) * p.dw.ldy + c0 + j] = v;
+                }
+            }
+            if (p.db && r0 == 0 && rank == 0 && t < kSmT) {
+                float v = 0.f;
+#pragma unroll
+                for (int q = 0; q < kSmCluster; ++q) v += ld_cluster_f32(map_to_rank(&S.out.col[t], q));
+                if (c0 + t < p.n) p.db[c0 + t] = v;
+            }
+            cluster_sync();   // the CTAs' shared memory has been read
+        }
+    }
+}
+
 // -------------------------------------------------------------------------- host
 
 // A bf16 operand as the product reads it: planes of rows [rows][ld].
@@ -909,23 +1104,26 @@ struct GemmPlan {
 // terms are the last four of 24 steps.
 int chunk_of(bool f32_out, int planes) { return planes == 3 ? 1 : f32_out ? 4 : 64; }
 
-// The tile and the splits of the contraction with the least modelled time: waves of k-block steps
-// (microseconds each as measured per tile), and for splits the partial sums' traffic and a second kernel.
+// The tile and the splits of the contraction with the least modelled time, in microseconds as measured:
+// what a product costs but its steps, a 64-deep step, what a further tile of the same CTAs adds; for splits
+// the partial sums' traffic and the joining kernel.  (256 x 256 tiles step at 94 % of the tensor rate, 256 x 128
+// at 64 %, 128 x 64 at 13 %; the smaller tiles are for results that leave SMs idle otherwise: 4096x512x512 bf16
+// 8.0, 7.0 and 8.3 us, 512 nodes of 64x64 fp32 8.5, 7.4 and 6.7 us.)
 GemmPlan plan_gemm(int M, int N, int K, int planes, bool f32_out) {
     GemmPlan best{};
     double best_us = 1e30;
     const int sms = num_sms();
     const int kb = (K + kBK - 1) / kBK;
-    const struct { int ctas, bn; double us_kb; } tiles[3] = {{2, 256, 0.30}, {2, 128, 0.17}, {1, 64, 0.11}};
+    const struct { int ctas, bn; double once, step, step3, more; } tiles[3] = {
+        {2, 256, 6.2, 0.264, 1.57, 0.8}, {2, 128, 5.2, 0.200, 0.79, 0.6}, {1, 64, 4.0, 0.252, 1.09, 0.5}};
     for (const auto& t : tiles) {
         const int bm = 128 * t.ctas, units = sms / t.ctas;
         const int tm = (M + bm - 1) / bm, tn = (N + t.bn - 1) / t.bn;
         const int64_t n = (int64_t)tm * tn;
         for (int sp = 1; sp <= 128; sp = sp < 8 ? sp + 1 : sp + sp / 4) {
-            if (sp > 1 && (sp * n > 2 * units || kb / sp < (planes == 1 ? 4 : 2))) break;
+            if (sp > 1 && (sp * n > units || kb / sp < (planes == 1 ? 4 : 2))) break;
             const int64_t waves = (n * sp + units - 1) / units;
-            const int64_t steps = (int64_t)((kb + sp - 1) / sp) * (planes == 1 ? 1 : 6);
-            double us = waves * steps * t.us_kb + 3.0 + 0.004 * t.bn * (waves < 4 ? waves : 4);
+            double us = t.once + waves * ((kb + sp - 1) / sp) * (planes == 1 ? t.step : t.step3) + (waves - 1) * t.more;
             if (sp > 1) us += 3.0 + (double)M * N * (sp + 2) * 4 / 4e6;
             if (us < best_us) {
                 best_us = us;
@@ -1150,6 +1348,19 @@ Epi make_epi(const float* bias, int act, int ytype, int ptype, const void* r, in
     return e;
 }
 
+int small_tiles(int rows, int cols) { return (rows + kSmT - 1) / kSmT * ((cols + kSmT - 1) / kSmT); }
+// Whether a fp32 call goes to the fp32 pipes in one kernel: short contractions and few multiplications.
+// Measured against the split products (device time of the call): forward 512x64x64 5.7 against 6.8 us,
+// 16384x64x64 8.3 against 9.3, 6800x64x192 11.0 against 9.9 (but one launch for two, and no workspace), 6800x128x128
+// 13.2 against 9.5; backward 512x64x64 7.8 against 14.2, 512x64x192 15.5 against 16.2, 300x512x100 13.0 against
+// 20.5, 1024x512x128 17.9 against 18.4, 512x512x512 44 against 27.
+bool small_fwd(int dtype, int m, int k, int n) {
+    return dtype == GT_F32 && k <= 64 && (int64_t)m * k * n <= (96 << 20);
+}
+bool small_bwd(int dtype, int m, int k, int n) {
+    return dtype == GT_F32 && m <= 1024 && n <= 192 && (int64_t)m * k * n <= (64 << 20);
+}
+
 bool ranges_ok(const void* p, int64_t ld, int cols) { return !p || ld >= cols; }
 
 }  // namespace
@@ -1160,6 +1371,7 @@ extern "C" {
 size_t gt_linear_fwd_workspace_size(int32_t dtype, int32_t m, int32_t k, int32_t n, int32_t aligned) {
     using namespace gt;
     if (check_linear(dtype, GT_F32, m, k, n, GT_ACT_NONE) != GT_OK) return 0;
+    if (small_fwd(dtype, m, k, n)) return 0;
     const bool pack = dtype == GT_F32 || !aligned;
     const size_t a = fwd_bufs(dtype, false, m, k, n, pack, pack, !aligned, nullptr, 0, nullptr);
     const size_t b = fwd_bufs(dtype, true, m, k, n, pack, pack, !aligned, nullptr, 0, nullptr);
@@ -1169,7 +1381,7 @@ size_t gt_linear_fwd_workspace_size(int32_t dtype, int32_t m, int32_t k, int32_t
 size_t gt_linear_bwd_workspace_size(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n, int32_t act,
                                     int32_t aligned) {
     using namespace gt;
-    if (check_linear(dtype, ytype, m, k, n, act) != GT_OK) return 0;
+    if (check_linear(dtype, ytype, m, k, n, act) != GT_OK || small_bwd(dtype, m, k, n)) return 0;
     const bool pack = dtype == GT_F32 || !aligned;
     return bwd_bufs(dtype, m, k, n, pack, pack, pack || act != GT_ACT_NONE || ytype != dtype, !aligned, !aligned, nullptr, 0,
                     nullptr);
@@ -1186,6 +1398,18 @@ int gt_linear_fwd(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n,
     const bool pack_x = dtype == GT_F32 || !rows16(x, ldx, 2), pack_w = dtype == GT_F32 || !rows16(w, ldw, 2);
     const int ey = elem_bytes(ytype), ex = elem_bytes(dtype);
     const Epi epi = make_epi(b, act, ytype, dtype, r, ldr, ey, y, ldy, pre, ldpre, ex);
+    if (small_fwd(dtype, m, k, n)) {
+        Small p{};
+        p.x = static_cast<const float*>(x);
+        p.w = static_cast<const float*>(w);
+        p.ldx = ldx; p.ldw = ldw;
+        p.m = m; p.k = k; p.n = n;
+        p.out = epi;
+        p.tiles = small_tiles(m, n);
+        LaunchScope ls("linear_small", static_cast<cudaStream_t>(stream));
+        linear_small<false><<<p.tiles, kSmThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+        return check_launch();
+    }
     FwdBufs bufs;
     const size_t need = fwd_bufs(dtype, ytype == GT_F32, m, k, n, pack_x, pack_w, epi.single, workspace, ws_bytes, &bufs);
     if (need > 0 && (!workspace || !aligned16(workspace) || ws_bytes < need)) return GT_ERR_WORKSPACE;
@@ -1216,6 +1440,33 @@ int gt_linear_bwd(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n,
     const int ex = elem_bytes(dtype);
     const Epi epi_x = make_epi(nullptr, GT_ACT_NONE, dtype, dtype, add, ldadd, ex, dx, lddx, nullptr, 0, ex);
     const Epi epi_w = make_epi(nullptr, GT_ACT_NONE, dtype, dtype, nullptr, 0, ex, dw, lddw, nullptr, 0, ex);
+    if (small_bwd(dtype, m, k, n)) {
+        Small p{};
+        p.x = static_cast<const float*>(x);
+        p.w = static_cast<const float*>(w);
+        p.dy = static_cast<const float*>(dy);
+        p.pre = static_cast<const float*>(pre);
+        p.ldx = ldx; p.ldw = ldw; p.lddy = lddy; p.ldpre = ldpre;
+        p.m = m; p.k = k; p.n = n;
+        p.out = epi_x;
+        p.dw = epi_w;
+        p.db = db;
+        p.tiles = dx ? (small_tiles(m, k) + kSmCluster - 1) / kSmCluster * kSmCluster : 0;
+        const int more = kSmCluster * (dw ? small_tiles(k, n) : db ? small_tiles(1, n) : 0);
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(p.tiles + more));
+        cfg.blockDim = dim3(kSmThreads);
+        cfg.stream = static_cast<cudaStream_t>(stream);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = kSmCluster;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        LaunchScope ls("linear_small", cfg.stream);
+        return cudaLaunchKernelEx(&cfg, linear_small<true>, p) == cudaSuccess ? check_launch() : GT_ERR_CUDA;
+    }
     BwdBufs bufs;
     const size_t need = bwd_bufs(dtype, m, k, n, pack_x, pack_w, own_da, dx && epi_x.single, dw && epi_w.single, workspace,
                                  ws_bytes, &bufs);

@@ -55,8 +55,10 @@ def _backward(gt, m, k, n, xt, yt, act, add=True, pad=0, offset=0):
 
 TYPES = [(B, B), (B, F), (F, F)]
 # one row, one feature, tiles exact and one past each of their edges, contractions that end inside a k-block
+# and short of one, fp32 sizes on both sides of the one-kernel path (k 64 forward, m 1024 or n 192 backward)
 SHAPES = [(1, 1, 1), (1, 64, 64), (2, 8, 200), (128, 64, 64), (129, 65, 65), (127, 63, 129), (64, 16, 256),
-          (300, 200, 257), (257, 72, 512), (640, 136, 72), (130, 1000, 40), (17, 520, 1016)]
+          (300, 200, 257), (257, 72, 512), (640, 136, 72), (130, 1000, 40), (17, 520, 1016), (65, 512, 33), (66, 64, 192), (67, 65, 193),
+          (1024, 33, 65), (1025, 72, 40), (257, 600, 1025), (1, 777, 1500), (9, 140, 192)]
 
 
 @pytest.mark.parametrize("act", [0, 1])
@@ -75,10 +77,11 @@ def test_backward(gt, m, k, n, xt, yt, act):
 
 @pytest.mark.parametrize("xt,yt", TYPES)
 @pytest.mark.parametrize("pad,offset", [(8, 0), (5, 0), (0, 8), (8, 1), (0, 3)])
-def test_strided_and_unaligned_operands(gt, xt, yt, pad, offset):
-    _forward(gt, 150, 104, 88, xt, yt, 1, pad=pad, offset=offset)
-    _backward(gt, 150, 104, 88, xt, yt, 1, pad=pad, offset=offset)
-    _backward(gt, 150, 104, 88, xt, yt, 0, pad=pad, offset=offset)
+@pytest.mark.parametrize("m,k,n", [(150, 104, 88), (1100, 520, 88)])
+def test_strided_and_unaligned_operands(gt, m, k, n, xt, yt, pad, offset):
+    _forward(gt, m, k, n, xt, yt, 1, pad=pad, offset=offset)
+    _backward(gt, m, k, n, xt, yt, 1, pad=pad, offset=offset)
+    _backward(gt, m, k, n, xt, yt, 0, pad=pad, offset=offset)
 
 
 @pytest.mark.parametrize("m,k,n,xt,yt", [
@@ -102,8 +105,8 @@ def test_without_bias_residual_or_add(gt):
         _backward(gt, 70, 90, 110, xt, yt, 0, add=False)
 
 
-def test_outputs_into_slices_leave_the_rest_alone(gt):
-    m, k, n = 75, 48, 40
+@pytest.mark.parametrize("m,k,n", [(75, 48, 40), (1030, 530, 300)])
+def test_outputs_into_slices_leave_the_rest_alone(gt, m, k, n):
     for xt, yt in TYPES:
         for pad in (8, 3):
             x, w, dy = _mat(m, k, xt, 1), _mat(k, n, xt, 2), _mat(m, n, yt, 3)
@@ -119,10 +122,11 @@ def test_outputs_into_slices_leave_the_rest_alone(gt):
                 assert (t[:, :pad] == 7).all() and (t[:, -pad:] == 7).all()
 
 
-def test_parts_of_the_backward(gt):
+@pytest.mark.parametrize("m", [200, 1100])
+def test_parts_of_the_backward(gt, m):
     """Each gradient alone equals the one of the whole call."""
     for xt, yt in TYPES:
-        dy, x, w, pre = _mat(200, 90, yt, 1), _mat(200, 70, xt, 2), _mat(70, 90, xt, 3), _mat(200, 90, xt, 4)
+        dy, x, w, pre = _mat(m, 90, yt, 1), _mat(m, 70, xt, 2), _mat(70, 90, xt, 3), _mat(m, 90, xt, 4)
         for act, p in ((0, None), (1, pre)):
             dx, dw, db = gt.gt_linear_bwd(dy, x, w, pre=p, act=act)
             one = gt.gt_linear_bwd(dy, x, w, pre=p, act=act, need_dw=False, need_db=False)
@@ -133,14 +137,15 @@ def test_parts_of_the_backward(gt):
             assert torch.equal(three[2], db) and three[0] is None and three[1] is None
 
 
-def test_in_place_residual_and_accumulated_gradient(gt):
+@pytest.mark.parametrize("m,k", [(90, 60), (1100, 600), (1100, 603)])
+def test_in_place_residual_and_accumulated_gradient(gt, m, k):
     for xt, yt in TYPES:
-        x, w, b, r, dy = _mat(90, 60, xt, 1), _mat(60, 70, xt, 2), _vec(70, 3), _mat(90, 70, yt, 4), _mat(90, 70, yt, 5)
+        x, w, b, r, dy = _mat(m, k, xt, 1), _mat(k, 70, xt, 2), _vec(70, 3), _mat(m, 70, yt, 4), _mat(m, 70, yt, 5)
         want, _ = gt.gt_linear_fwd(x, w, b, act=1, r=r)
         buf = r.clone()
         got, _ = gt.gt_linear_fwd(x, w, b, act=1, r=buf, out=buf)
         assert got is buf and torch.equal(got, want)
-        add = _mat(90, 60, xt, 6)
+        add = _mat(m, k, xt, 6)
         want, _, _ = gt.gt_linear_bwd(dy, x, w, dx_add=add)
         buf = add.clone()
         got, _, _ = gt.gt_linear_bwd(dy, x, w, dx_add=buf, dx=buf)
@@ -148,7 +153,7 @@ def test_in_place_residual_and_accumulated_gradient(gt):
 
 
 def test_same_result_every_time(gt):
-    for m, k, n, xt in ((4000, 64, 64, B), (3, 2000, 300, B), (700, 100, 60, F)):
+    for m, k, n, xt in ((4000, 64, 64, B), (3, 2000, 300, B), (700, 100, 60, F), (3000, 1000, 60, F)):
         x, w, dy = _mat(m, k, xt, 1), _mat(k, n, xt, 2), _mat(m, n, xt, 3)
         y = gt.gt_linear_fwd(x, w)[0]
         g = gt.gt_linear_bwd(dy, x, w)
@@ -157,29 +162,45 @@ def test_same_result_every_time(gt):
             assert all(torch.equal(a, b) for a, b in zip(gt.gt_linear_bwd(dy, x, w), g))
 
 
-def test_fp32_products_keep_fp32_accuracy(gt):
-    """Values over the range of fp32, cancelling sums and exact cases."""
-    # exact: small whole numbers, whose products and sums are whole
+@pytest.mark.parametrize("k", [64, 640])
+def test_fp32_products_keep_fp32_accuracy(gt, k):
+    """Exact cases, for the one-kernel path and the split products."""
+    # small whole numbers, whose products and sums are whole
     g = torch.Generator(device="cuda").manual_seed(1)
-    x = torch.randint(-2000, 2001, (50, 100), generator=g, device="cuda").float()
-    w = torch.randint(-40, 41, (100, 30), generator=g, device="cuda").float()
+    x = torch.randint(-2000, 2001, (50, k), generator=g, device="cuda").float()
+    w = torch.randint(-12, 13, (k, 30), generator=g, device="cuda").float()
     assert torch.equal(gt.gt_linear_fwd(x, w)[0].double(), x.double() @ w.double())
     # 24-bit values times powers of two: hi, mid and lo all matter, nothing rounds
-    x = (torch.randint(2 ** 23, 2 ** 24, (40, 64), generator=g, device="cuda").float()
+    x = (torch.randint(2 ** 23, 2 ** 24, (40, k), generator=g, device="cuda").float()
          * 2.0 ** torch.randint(-40, 41, (40, 1), generator=g, device="cuda"))
-    w = torch.zeros(64, 64, device="cuda")
-    w[torch.arange(64), torch.arange(64).flip(0)] = 2.0 ** torch.randint(-20, 21, (64,), generator=g, device="cuda")
+    w = torch.zeros(k, k, device="cuda")
+    w[torch.arange(k), torch.arange(k).flip(0)] = 2.0 ** torch.randint(-20, 21, (k,), generator=g, device="cuda")
     assert torch.equal(gt.gt_linear_fwd(x, w)[0].double(), x.double() @ w.double())
     # the largest finite value is split without overflow
-    x = torch.full((2, 8), torch.finfo(F).max, device="cuda")
-    w = torch.zeros(8, 8, device="cuda")
+    x = torch.full((2, k), torch.finfo(F).max, device="cuda")
+    w = torch.zeros(k, 8, device="cuda")
     w[3] = 0.5
     assert torch.equal(gt.gt_linear_fwd(x, w)[0], torch.full((2, 8), torch.finfo(F).max / 2, device="cuda"))
 
 
+def test_long_positive_sums(gt):
+    """All-positive sums 20000 long, where an accumulator that drops low bits would lag by 1e-4 in fp32: within
+    1e-6 (measured 3e-7; two roundings of a sum of 80 chunks, 2^-23 each, and 4.4e-8 per 16-deep step of one chunk)."""
+    for xt in (F, B):
+        x, w = _mat(300, 20000, F, 1).abs().to(xt), _mat(20000, 200, F, 2).abs().to(xt)
+        y, _ = gt.gt_linear_fwd(x, w, out_dtype=F)
+        ref = R.d(x) @ R.d(w)
+        assert float(((R.d(y) - ref).abs() / ref).max()) < 1e-6
+        # dW sums over the 20000 rows
+        x, dy = _mat(20000, 130, F, 3).abs().to(xt), _mat(20000, 100, F, 4).abs().to(xt)
+        _, dw, _ = gt.gt_linear_bwd(dy, x, _mat(130, 100, xt, 5), need_dx=False)
+        ref = R.d(x).t() @ R.d(dy)
+        assert float(((R.d(dw) - ref).abs() / ref).max()) < (1e-6 if xt == F else 2.0 ** -8 + 2e-5)
+
+
 @pytest.mark.parametrize("xt,yt", TYPES)
-def test_nonfinite_inputs_stay_in_their_rows(gt, xt, yt):
-    m, k, n = 140, 70, 90
+@pytest.mark.parametrize("m,k,n", [(140, 70, 90), (1100, 520, 90)])
+def test_nonfinite_inputs_stay_in_their_rows(gt, m, k, n, xt, yt):
     x, w, dy = _mat(m, k, xt, 1), _mat(k, n, xt, 2, 0.1), _mat(m, n, yt, 3)
     x[5, 3] = float("inf")
     x[130, 69] = float("nan")
