@@ -376,8 +376,9 @@ def gt_layer_bwd(x, params: dict, spd, T, saved: dict, dy, workspace=None, strea
     return dx, grads, dT
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# the handle of a device's current stream and the current device, without the objects around them
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _elsewhere(call, first, stream, args):
@@ -432,6 +433,30 @@ def _vector(name, t, size, device):
     if t.shape != (size,) or t.dtype is not torch.float32 or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous fp32 [{size}] on {device}")
     return t.data_ptr()
+
+
+def _result(name, t, size, device):
+    """(t, address) of an fp32 [size] result: the caller's, or a new one."""
+    if t is None:
+        t = torch.empty(size, dtype=torch.float32, device=device)
+        return t, t.data_ptr()
+    return t, _vector(name, t, size, device)
+
+
+def _matrix_result(name, t, rows, cols, dtype, device):
+    """(t, address, leading dimension) of a [rows][cols] result: the caller's, or a new one."""
+    if t is None:
+        t = torch.empty((rows, cols), dtype=dtype, device=device)
+        return t, t.data_ptr(), cols if rows > 1 else (cols + 7) // 8 * 8
+    return t, t.data_ptr(), _matrix(name, t, rows, cols, dtype, device)
+
+
+def _type_code(name, t):
+    if t.dtype is torch.float32:
+        return GT_F32
+    if t.dtype is torch.bfloat16:
+        return GT_BF16
+    raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
 
 
 def _two_dims(name, t):
@@ -495,16 +520,10 @@ def gt_layer_norm_fwd(x, gain, shift, eps: float = 1e-5, out_dtype=None, out=Non
     yt = out_dtype or (xt if out is None else out.dtype)
     ldx = _matrix("x", x, n, c, xt, dev)
     gp, sp = _vector("gain", gain, c, dev), _vector("shift", shift, c, dev)
-    if out is None:
-        out, ldy = torch.empty((n, c), dtype=yt, device=dev), c
-    else:
-        ldy = _matrix("out", out, n, c, yt, dev)
-    if mean is None:
-        mean = torch.empty(n, dtype=torch.float32, device=dev)
-    if rstd is None:
-        rstd = torch.empty(n, dtype=torch.float32, device=dev)
-    rc = lib.gt_layer_norm_fwd(_dtype_code(x), _dtype_code(out), n, c, x.data_ptr(), ldx, gp, sp, eps, out.data_ptr(),
-                               ldy, _vector("mean", mean, n, dev), _vector("rstd", rstd, n, dev),
+    out, yp, ldy = _matrix_result("out", out, n, c, yt, dev)
+    mean, mp = _result("mean", mean, n, dev)
+    rstd, rp = _result("rstd", rstd, n, dev)
+    rc = lib.gt_layer_norm_fwd(_type_code("x", x), _type_code("out", out), n, c, x.data_ptr(), ldx, gp, sp, eps, yp, ldy, mp, rp,
                                _raw_stream(dev.index))
     if rc:
         raise GtError("gt_layer_norm_fwd", rc)
@@ -525,18 +544,12 @@ def gt_layer_norm_bwd(dy, x, gain, mean, rstd, dres=None, dx=None, dgain=None, d
     lddy = _matrix("dy", dy, n, c, dy.dtype, dev)
     gp, mp, rp = _vector("gain", gain, c, dev), _vector("mean", mean, n, dev), _vector("rstd", rstd, n, dev)
     ap, lda = (None, 0) if dres is None else (dres.data_ptr(), _matrix("dres", dres, n, c, xt, dev))
-    if dx is None:
-        dx, lddx = torch.empty((n, c), dtype=xt, device=dev), c
-    else:
-        lddx = _matrix("dx", dx, n, c, xt, dev)
-    if dgain is None:
-        dgain = torch.empty(c, dtype=torch.float32, device=dev)
-    if dshift is None:
-        dshift = torch.empty(c, dtype=torch.float32, device=dev)
+    dx, dxp, lddx = _matrix_result("dx", dx, n, c, xt, dev)
+    dgain, dgp = _result("dgain", dgain, c, dev)
+    dshift, dsp = _result("dshift", dshift, c, dev)
     workspace, wp, wn = _room(workspace, _norm_room(dev.index, n, c), dev)
-    rc = lib.gt_layer_norm_bwd(_dtype_code(x), _dtype_code(dy), n, c, dy.data_ptr(), lddy, x.data_ptr(), ldx, gp, mp,
-                               rp, ap, lda, dx.data_ptr(), lddx, _vector("dgain", dgain, c, dev),
-                               _vector("dshift", dshift, c, dev), wp, wn, _raw_stream(dev.index))
+    rc = lib.gt_layer_norm_bwd(_type_code("x", x), _type_code("dy", dy), n, c, dy.data_ptr(), lddy, x.data_ptr(), ldx, gp, mp,
+                               rp, ap, lda, dxp, lddx, dgp, dsp, wp, wn, _raw_stream(dev.index))
     if rc:
         raise GtError("gt_layer_norm_bwd", rc)
     return dx, dgain, dshift
@@ -553,24 +566,21 @@ def gt_linear_fwd(x, w, b=None, act: int = GT_ACT_NONE, r=None, out_dtype=None, 
     m, k = _two_dims("x", x)
     n = _two_dims("w", w)[1]
     xt, dev = x.dtype, x.device
-    dt = _dtype_code(x)
+    dt = _type_code("x", x)
     ldx, ldw = _matrix("x", x, m, k, xt, dev), _matrix("w", w, k, n, xt, dev)
     yt = out_dtype or (out.dtype if out is not None else r.dtype if r is not None else xt)
     bp = None if b is None else _vector("b", b, n, dev)
     rp, ldr = (None, 0) if r is None else (r.data_ptr(), _matrix("r", r, m, n, yt, dev))
-    if out is None:
-        out, ldy = torch.empty((m, n), dtype=yt, device=dev), n
-    else:
-        ldy = _matrix("out", out, m, n, yt, dev)
-    if pre is None and save_pre:
-        pre = torch.empty((m, n), dtype=xt, device=dev)
-    pp, ldp = (None, 0) if pre is None else (pre.data_ptr(), _matrix("pre", pre, m, n, xt, dev))
-    xp, wp, yp = x.data_ptr(), w.data_ptr(), out.data_ptr()
+    out, yp, ldy = _matrix_result("out", out, m, n, yt, dev)
+    pp, ldp = None, 0
+    if save_pre or pre is not None:
+        pre, pp, ldp = _matrix_result("pre", pre, m, n, xt, dev)
+    xp, wp = x.data_ptr(), w.data_ptr()
     # rows of whole 16 bytes
     ex, ey = x.element_size(), out.element_size()
     aligned = (xp | wp | yp | (rp or 0) | (pp or 0) | (ldx | ldw | ldp) * ex | (ldy | ldr) * ey) % 16 == 0
     workspace, sp, sn = _room(workspace, _linear_fwd_room(dev.index, dt, m, k, n, aligned), dev)
-    rc = lib.gt_linear_fwd(dt, _dtype_code(out), m, k, n, xp, ldx, wp, ldw, bp, act, rp, ldr, yp, ldy, pp,
+    rc = lib.gt_linear_fwd(dt, _type_code("out", out), m, k, n, xp, ldx, wp, ldw, bp, act, rp, ldr, yp, ldy, pp,
                            ldp, sp, sn, _raw_stream(dev.index))
     if rc:
         raise GtError("gt_linear_fwd", rc)
@@ -590,20 +600,18 @@ def gt_linear_bwd(dy, x, w, pre=None, act: int = GT_ACT_NONE, dx_add=None, need_
     m, k = _two_dims("x", x)
     n = _two_dims("w", w)[1]
     xt, dev = x.dtype, x.device
-    dt, yt = _dtype_code(x), _dtype_code(dy)
+    dt, yt = _type_code("x", x), _type_code("dy", dy)
     ldx, ldw = _matrix("x", x, m, k, xt, dev), _matrix("w", w, k, n, xt, dev)
     lddy = _matrix("dy", dy, m, n, dy.dtype, dev)
     pp, ldp = (None, 0) if pre is None else (pre.data_ptr(), _matrix("pre", pre, m, n, xt, dev))
     ap, lda = (None, 0) if dx_add is None else (dx_add.data_ptr(), _matrix("dx_add", dx_add, m, k, xt, dev))
-    if need_dx and dx is None:
-        dx = torch.empty((m, k), dtype=xt, device=dev)
-    if need_dw and dw is None:
-        dw = torch.empty((k, n), dtype=xt, device=dev)
-    if need_db and db is None:
-        db = torch.empty(n, dtype=torch.float32, device=dev)
-    dxp, lddx = (None, 0) if dx is None else (dx.data_ptr(), _matrix("dx", dx, m, k, xt, dev))
-    dwp, lddw = (None, 0) if dw is None else (dw.data_ptr(), _matrix("dw", dw, k, n, xt, dev))
-    dbp = None if db is None else _vector("db", db, n, dev)
+    dxp, lddx, dwp, lddw, dbp = None, 0, None, 0, None
+    if need_dx or dx is not None:
+        dx, dxp, lddx = _matrix_result("dx", dx, m, k, xt, dev)
+    if need_dw or dw is not None:
+        dw, dwp, lddw = _matrix_result("dw", dw, k, n, xt, dev)
+    if need_db or db is not None:
+        db, dbp = _result("db", db, n, dev)
     xp, wp, dyp = x.data_ptr(), w.data_ptr(), dy.data_ptr()
     aligned = (xp | wp | dyp | (pp or 0) | (ap or 0) | (dxp or 0) | (dwp or 0) | lddy * dy.element_size() |
                (ldx | ldw | ldp | lda | lddx | lddw) * x.element_size()) % 16 == 0

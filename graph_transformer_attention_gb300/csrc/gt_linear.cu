@@ -1117,7 +1117,7 @@ GemmPlan plan_gemm(int M, int N, int K, int planes, bool f32_out) {
     const struct { int ctas, bn; double once, step, step3, more; } tiles[3] = {
         {2, 256, 6.2, 0.264, 1.57, 0.8}, {2, 128, 5.2, 0.200, 0.79, 0.6}, {1, 64, 4.0, 0.252, 1.09, 0.5}};
     for (const auto& t : tiles) {
-        const int bm = 128 * t.ctas, units = sms / t.ctas;
+        const int bm = 128 * t.ctas, units = sms > t.ctas ? sms / t.ctas : 1;
         const int tm = (M + bm - 1) / bm, tn = (N + t.bn - 1) / t.bn;
         const int64_t n = (int64_t)tm * tn;
         for (int sp = 1; sp <= 128; sp = sp < 8 ? sp + 1 : sp + sp / 4) {
@@ -1151,7 +1151,8 @@ int launch_gemm(const GemmPlan& p, const CUtensorMap& ma, const CUtensorMap& mb,
                 bool follows, cudaStream_t s) {
     Epi epi = e;
     CUtensorMap my{}, mp{};
-    if (GemmCfg<CTAS, BN, SUM>::kBulk && !part && !epi.single && !epi.y_f32 && !epi.pre_f32) {
+    // (whole 16 bytes of columns: a box that ends at an odd column of bf16 writes one column more)
+    if (GemmCfg<CTAS, BN, SUM>::kBulk && !part && !epi.single && !epi.y_f32 && !epi.pre_f32 && p.g.N % 8 == 0) {
         const CUtensorMapDataType ty = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
         if (!make_map_2d(&my, epi.y, ty, p.g.M, p.g.N, epi.ldy * 2, 32, kBoxCols, CU_TENSOR_MAP_SWIZZLE_64B) ||
             (epi.pre && !make_map_2d(&mp, epi.pre, ty, p.g.M, p.g.N, epi.ldpre * 2, 32, kBoxCols, CU_TENSOR_MAP_SWIZZLE_64B)))
@@ -1164,7 +1165,7 @@ int launch_gemm(const GemmPlan& p, const CUtensorMap& ma, const CUtensorMap& mb,
     if (!allow_smem(allowed, reinterpret_cast<const void*>(kern), C::kSmem)) return GT_ERR_CUDA;
     int* status = device_status_ptr();
     if (!status) return GT_ERR_CUDA;
-    const int units = num_sms() / CTAS, items = p.g.items();
+    const int sms = num_sms(), units = sms > CTAS ? sms / CTAS : 1, items = p.g.items();
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(CTAS * (items < units ? items : units)));
     cfg.blockDim = dim3(kGemmThreads);

@@ -122,6 +122,38 @@ def test_outputs_into_slices_leave_the_rest_alone(gt, m, k, n):
                 assert (t[:, :pad] == 7).all() and (t[:, -pad:] == 7).all()
 
 
+@pytest.mark.parametrize("fill", [300.0, float("nan")])
+def test_margins_of_the_inputs_do_not_count(gt, fill):
+    """Inputs whose rows end at odd columns inside 16 bytes, with large values or NaN behind them: read in
+    place, what lies behind a row's end must not enter any sum."""
+    def odd(rows, cols, seed, std=1.0):
+        wide = torch.full((rows + 2, (cols + 7) // 8 * 8 + 8), fill, dtype=B, device="cuda")
+        wide[:rows, :cols] = _mat(rows, cols, B, seed, std)
+        return wide[:rows, :cols]
+
+    for m, k, n in ((300, 65, 129), (257, 321, 1001), (40, 1003, 67), (3000, 257, 511)):
+        x, w, dy, pre, r = odd(m, k, 1), odd(k, n, 2, 1 / math.sqrt(k)), odd(m, n, 3), odd(m, n, 4), odd(m, n, 5)
+        y, a = gt.gt_linear_fwd(x, w, act=1, r=r, save_pre=True)
+        R.check({"y": y, "pre": a}, R.linear_fwd(x, w, None, True, r, B))
+        for p, act in ((None, 0), (pre, 1)):
+            dx, dw, db = gt.gt_linear_bwd(dy, x, w, pre=p, act=act)
+            R.check({"dx": dx, "dw": dw, "db": db}, R.linear_bwd(dy, x, w, p, act == 1, None))
+
+
+@pytest.mark.parametrize("k", [200, 5000])        # one accumulator chunk (results leave as TMA boxes), and several
+def test_box_edges_leave_the_rest_alone(gt, k):
+    """Results whose last columns and rows end inside a tile, in rows of whole 16 bytes with a margin."""
+    for m, n in ((600, 300), (257, 1001), (130, 33), (3000, 999)):
+        x, w, b = _mat(m, k, B, 1), _mat(k, n, B, 2, 0.1), _vec(n, 3)
+        width = (n + 7) // 8 * 8 + 8
+        buf = [torch.full((m + 3, width), 7.0, dtype=B, device="cuda") for _ in range(2)]
+        y, pre = (t[:m, :n] for t in buf)
+        gt.gt_linear_fwd(x, w, b, act=1, out=y, pre=pre)
+        R.check({"y": y, "pre": pre}, R.linear_fwd(x, w, b, True, None, B))
+        for t in buf:
+            assert (t[m:] == 7).all() and (t[:, n:] == 7).all()
+
+
 @pytest.mark.parametrize("m", [200, 1100])
 def test_parts_of_the_backward(gt, m):
     """Each gradient alone equals the one of the whole call."""
@@ -278,6 +310,27 @@ def test_streams_and_graph(gt):
     assert all(torch.equal(a, c) for a, c in zip(held, both()))
 
 
+def test_two_graphs_share_a_workspace(gt):
+    """Two captured calls with one workspace, replayed in turn, leave nothing behind in it."""
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    sets = []
+    for seed, (m, k, n, xt) in enumerate(((3000, 64, 72, B), (40, 3000, 96, F))):
+        x, w, dy = _mat(m, k, xt, seed), _mat(k, n, xt, seed + 5, 0.1), _mat(m, n, xt, seed + 9)
+        call = lambda x=x, w=w, dy=dy: (gt.gt_linear_fwd(x, w, workspace=ws)[0],  # noqa: E731
+                                        *gt.gt_linear_bwd(dy, x, w, workspace=ws))
+        want = call()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            held = call()
+        sets.append((graph, held, want))
+    for _ in range(3):
+        for graph, held, want in sets:
+            ws.fill_(255)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(held, want))
+
+
 @pytest.mark.parametrize("width,heads,ffn,t", [(128, 8, 320, F), (96, 8, 200, B), (72, 4, 130, F)])
 def test_whole_encoder_layer_at_other_widths(gt, width, heads, ffn, t):
     """LayerNorm, projections, biased attention and FFN together, forward and backward, against the fp64
@@ -335,3 +388,50 @@ def test_whole_encoder_layer_at_other_widths(gt, width, heads, ffn, t):
 
     errs = {"y": rel(y, fw["y"]), **{s: rel(gr[s], ref[s]) for s in gr}}
     assert all(e <= tol for e in errs.values()), errs
+
+
+def test_binding_refusals(gt):
+    """Shapes, types, strides, devices and streams that the binding turns away before any launch."""
+    x, w, b, dy = _mat(6, 8, B, 1), _mat(8, 10, B, 2), _vec(10, 3), _mat(6, 10, B, 4)
+    value = (
+        lambda: gt.gt_linear_fwd(x[0], w),                                    # one dimension
+        lambda: gt.gt_linear_fwd(x, w[0]),
+        lambda: gt.gt_linear_fwd(x, w[:7]),                                   # inner sizes differ
+        lambda: gt.gt_linear_fwd(x, w, b[:9]),
+        lambda: gt.gt_linear_fwd(x, w, b.double()),
+        lambda: gt.gt_linear_fwd(x, w, r=dy[:5]),
+        lambda: gt.gt_linear_fwd(x, w.t().contiguous().t()),                  # columns not contiguous
+        lambda: gt.gt_linear_fwd(x[:1].expand(6, 8), w),                      # rows overlap
+        lambda: gt.gt_linear_fwd(x, w.cpu()),
+        lambda: gt.gt_linear_fwd(x, w, out=torch.empty(6, 9, dtype=B, device="cuda")),
+        lambda: gt.gt_linear_fwd(x, w, workspace=torch.empty(64, dtype=torch.uint8)),
+        lambda: gt.gt_linear_bwd(dy[:5], x, w),
+        lambda: gt.gt_linear_bwd(dy, x, w, dx_add=x[:, :7]),
+        lambda: gt.gt_layer_norm_fwd(x, b, b),
+        lambda: gt.gt_layer_norm_fwd(x[0], b[:8], b[:8]),
+    )
+    for call in value:
+        with pytest.raises(ValueError):
+            call()
+    kind = (
+        lambda: gt.gt_linear_fwd(x.half(), w.half()),
+        lambda: gt.gt_linear_fwd(x, w.float()),
+        lambda: gt.gt_linear_fwd(x, w, r=dy.float(), out_dtype=B),
+        lambda: gt.gt_linear_fwd(x, w, out_dtype=torch.float16),
+        lambda: gt.gt_linear_bwd(dy.half(), x, w),
+        lambda: gt.gt_layer_norm_fwd(x.double(), b[:8].contiguous(), b[:8].contiguous()),
+    )
+    for call in kind:
+        with pytest.raises(TypeError):
+            call()
+    for call in (lambda: gt.gt_linear_fwd(x.float(), w.float(), out_dtype=B),           # bf16 result of fp32 products
+                 lambda: gt.gt_linear_fwd(x, w, act=5),
+                 lambda: gt.gt_linear_fwd(x[:0], w),                                    # no rows
+                 lambda: gt.gt_linear_bwd(dy, x, w, act=gt.GT_ACT_GELU),                # GELU without pre
+                 lambda: gt.gt_linear_bwd(dy, x, w, need_dx=False, need_dw=False, need_db=False),
+                 lambda: gt.gt_linear_bwd(dy, x, w, dx_add=x, need_dx=False),
+                 lambda: gt.gt_linear_bwd(dy, x, w, workspace=torch.empty(16, dtype=torch.uint8, device="cuda")),
+                 lambda: gt.gt_layer_norm_fwd(x, b[:8].contiguous(), b[:8].contiguous(), eps=0.0),
+                 lambda: gt.gt_layer_norm_fwd(x[:0], b[:8].contiguous(), b[:8].contiguous())):
+        with pytest.raises(gt.GtError):
+            call()
