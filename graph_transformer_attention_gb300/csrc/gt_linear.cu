@@ -131,7 +131,8 @@ struct PrepJob {
     float* colsum;
     int64_t lds, ldp, ldd, plane;
     int m, n, tx, gx, gy;
-    bool f32, svec, pvec;
+    bool f32;
+    int svec, pvec;   // row_access()
 };
 constexpr int kPrepJobs = 3;
 struct PrepJobs {
@@ -184,7 +185,7 @@ __device__ __forceinline__ void prep_rows(const PrepJob& J, int bx, int by) {
                 for (int i = 0; i < 8; ++i) acc[i] += v[i];
                 if (!J.dst || row >= m) continue;
                 if constexpr (PARTS == 1) {
-                    store8(J.dst + row * J.ldd + col, v, 8, true);
+                    store8(J.dst + row * J.ldd + col, v, 8, 1);
                 } else {
                     uint32_t w[3][4];
 #pragma unroll
@@ -272,7 +273,7 @@ __device__ __forceinline__ void put_row(void* base, int64_t at, bool f32, const 
             float t[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) t[i] = v[8 * g + i];
-            store8(p + 8 * g, t, live - 8 * g, acc > 0);
+            store8(p + 8 * g, t, live - 8 * g, acc);
         }
     } else {
         bf16* p = static_cast<bf16*>(base) + at;
@@ -291,7 +292,7 @@ __device__ __forceinline__ void put_row(void* base, int64_t at, bool f32, const 
             float t[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) t[i] = v[8 * g + i];
-            store8(p + 8 * g, t, live - 8 * g, acc > 0);
+            store8(p + 8 * g, t, live - 8 * g, acc);
         }
     }
 }
@@ -314,7 +315,7 @@ __device__ __forceinline__ void add_row(const void* base, int64_t at, bool f32, 
 #pragma unroll
         for (int g = 0; g < CW / 8; ++g) {
             float t[8];
-            unpack8(load8(p + 8 * g, live - 8 * g, acc > 0), t);
+            unpack8(load8(p + 8 * g, live - 8 * g, acc), t);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[8 * g + i] += t[i];
         }
@@ -336,7 +337,7 @@ __device__ __forceinline__ void add_row(const void* base, int64_t at, bool f32, 
 #pragma unroll
         for (int g = 0; g < CW / 8; ++g) {
             float t[8];
-            unpack8(load8(p + 8 * g, live - 8 * g, acc > 0), t);
+            unpack8(load8(p + 8 * g, live - 8 * g, acc), t);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[8 * g + i] += t[i];
         }
@@ -1267,8 +1268,8 @@ struct Prep {
         j.lds = lds; j.ldp = ldp; j.ldd = pad8(n); j.plane = m * j.ldd;
         j.m = m; j.n = n; j.tx = pg.tx; j.gx = pg.gx; j.gy = pg.gy;
         j.f32 = t == GT_F32;
-        j.svec = rows16(src, lds, elem_bytes(t));
-        j.pvec = pre && rows16(pre, ldp, elem_bytes(dtype));
+        j.svec = row_access(src, lds, elem_bytes(t));
+        j.pvec = row_access(pre, ldp, elem_bytes(dtype));
         ctas += pg.gx * pg.gy;
     }
     // src [m][n] of the compute type as an operand: read in place (buf NULL), or through buf,

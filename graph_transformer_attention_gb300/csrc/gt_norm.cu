@@ -18,6 +18,9 @@
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+
+#include <algorithm>
+#include <initializer_list>
 #include <type_traits>
 
 #include "gt_common.cuh"
@@ -84,7 +87,7 @@ template <typename TX, typename TY, typename C>
 __global__ void __launch_bounds__(C::TH, C::OCC)
 norm_fwd(int64_t n, int c, const TX* __restrict__ x, int64_t ldx, const float* __restrict__ gain,
          const float* __restrict__ shift, float eps, TY* __restrict__ y, int64_t ldy, float* __restrict__ mean,
-         float* __restrict__ rstd, bool vec) {
+         float* __restrict__ rstd, int vec) {
     constexpr int TPR = C::TPR, NV = C::NV, R = C::R, RG = C::RG;
     __shared__ float2 red[C::RED];
     RowSum<TPR, R, C::TH> rowsum{red, 0};
@@ -102,7 +105,7 @@ norm_fwd(int64_t n, int c, const TX* __restrict__ x, int64_t ldx, const float* _
         }
     };
     // Rows of bf16 are fetched a turn ahead, by as many CTAs as are resident; of fp32, whose rows take twice the
-    // registers, more CTAs take turns instead (32768 x 1024: bf16 28 against 31 us, fp32 in and bf16 out 36 against 37 us).
+    // registers, more CTAs take turns instead (32768 x 1024: bf16 26 against 31 us, fp32 in and bf16 out 34 against 37 us).
     constexpr bool kAhead = sizeof(TX) == 2;
     Raw8<TX> raw[R][NV];
     const int64_t step = (int64_t)gridDim.x * C::ROWS;
@@ -175,7 +178,7 @@ __global__ void __launch_bounds__(C::TH, C::OCC)
 norm_bwd(int64_t n, int c, const TY* __restrict__ dy, int64_t lddy, const TX* __restrict__ x, int64_t ldx,
          const float* __restrict__ gain, const float* __restrict__ mean, const float* __restrict__ rstd,
          const TX* __restrict__ dres, int64_t ldr, TX* __restrict__ dx, int64_t lddx, float* __restrict__ part,
-         bool vec) {
+         int vec) {
     constexpr int TPR = C::TPR, NV = C::NV, R = C::R, RG = C::RG, TH = C::TH;
     __shared__ float2 red[C::RED];
     RowSum<TPR, R, TH> rowsum{red, 0};
@@ -269,8 +272,8 @@ norm_bwd(int64_t n, int c, const TY* __restrict__ dy, int64_t lddy, const TX* __
         for (int i = 0; i < NV; ++i) {
             const int col = (i * TPR + t) * 8;
             if (col >= c) continue;
-            store8(pr + col, ag[i], c - col, false);
-            store8(pr + c + col, as[i], c - col, false);
+            store8(pr + col, ag[i], c - col, 0);
+            store8(pr + c + col, as[i], c - col, 0);
         }
     } else {
         constexpr int W = TPR * 8;            // columns of one turn
@@ -356,12 +359,15 @@ int norm_bwd_ctas(int64_t n, int c) {
     });
 }
 
+int least(std::initializer_list<int> v) { return std::min(v); }
+
 bool valid_type(int t) { return t == GT_F32 || t == GT_BF16; }
 
 template <typename TX, typename TY>
 int run_fwd(int64_t n, int c, const void* x, int64_t ldx, const float* gain, const float* shift, float eps, void* y,
             int64_t ldy, float* mean, float* rstd, cudaStream_t s) {
-    const bool vec = rows16(x, ldx, sizeof(TX)) && rows16(y, ldy, sizeof(TY)) && aligned16(gain) && aligned16(shift);
+    const int vec = least({row_access(x, ldx, sizeof(TX)), row_access(y, ldy, sizeof(TY)), row_access(gain, 0, 4),
+                           row_access(shift, 0, 4)});
     return fwd_dispatch(c, [&](auto cfg) {
         using C = decltype(cfg);
         const int64_t want = (n + C::ROWS - 1) / C::ROWS, most = (sizeof(TX) == 2 ? C::OCC : 16) * (int64_t)num_sms();
@@ -376,8 +382,8 @@ template <typename TX, typename TY>
 int run_bwd(int64_t n, int c, const void* dy, int64_t lddy, const void* x, int64_t ldx, const float* gain,
             const float* mean, const float* rstd, const void* dres, int64_t ldr, void* dx, int64_t lddx, float* part,
             cudaStream_t s) {
-    const bool vec = rows16(x, ldx, sizeof(TX)) && rows16(dy, lddy, sizeof(TY)) && rows16(dx, lddx, sizeof(TX)) &&
-                     (!dres || rows16(dres, ldr, sizeof(TX))) && aligned16(gain);
+    const int vec = least({row_access(x, ldx, sizeof(TX)), row_access(dy, lddy, sizeof(TY)),
+                           row_access(dx, lddx, sizeof(TX)), row_access(dres, ldr, sizeof(TX)), row_access(gain, 0, 4)});
     return bwd_dispatch(c, [&](auto cfg) {
         using C = decltype(cfg);
         LaunchScope ls("norm_bwd", s);

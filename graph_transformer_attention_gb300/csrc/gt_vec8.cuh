@@ -11,8 +11,8 @@
 
 namespace gt {
 
-// Whether rows of `ld` elements of type T at p can be moved 16 bytes at a time
-// at column offsets that are multiples of 8 elements.
+// Whether rows of `ld` elements at p can be moved 16 bytes at a time at column
+// offsets that are multiples of 8 elements.
 inline bool rows16(const void* p, int64_t ld, int elem_bytes) {
     return aligned16(p) && (ld * elem_bytes) % 16 == 0;
 }
@@ -29,14 +29,22 @@ template <typename T> struct Raw8;
 template <> struct Raw8<__nv_bfloat16> { uint4 a; };
 template <> struct Raw8<float> { uint4 a, b; };
 
-// Elements p[0 .. 7], those at or past `live` as zeros.
+// Elements p[0 .. 7], those at or past `live` as zeros; acc: the row's row_access().
 template <typename T>
-__device__ __forceinline__ Raw8<T> load8(const T* p, int live, bool vec) {
+__device__ __forceinline__ Raw8<T> load8(const T* p, int live, int acc) {
     Raw8<T> r;
-    if (vec && live >= 8) {
+    if (acc > 0 && live >= 8) {
         const uint4* s = reinterpret_cast<const uint4*>(p);
-        r.a = __ldg(s);
-        if constexpr (sizeof(T) == 4) r.b = __ldg(s + 1);
+        if constexpr (sizeof(T) == 2) {
+            r.a = __ldg(s);
+        } else if (acc == 2) {   // one access of 32 bytes: whole sectors
+            asm("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                : "=r"(r.a.x), "=r"(r.a.y), "=r"(r.a.z), "=r"(r.a.w), "=r"(r.b.x), "=r"(r.b.y), "=r"(r.b.z), "=r"(r.b.w)
+                : "l"(p));
+        } else {
+            r.a = __ldg(s);
+            r.b = __ldg(s + 1);
+        }
     } else if constexpr (sizeof(T) == 4) {
         uint32_t w[8];
 #pragma unroll
@@ -81,29 +89,6 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
     return r;
 }
 
-// p[0 .. 7] = v, the elements at or past `live` left alone.
-__device__ __forceinline__ void store8(float* p, const float (&v)[8], int live, bool vec) {
-    if (vec && live >= 8) {
-        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < live) p[i] = v[i];
-    }
-}
-
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8], int live, bool vec) {
-    if (vec && live >= 8) {
-        *reinterpret_cast<uint4*>(p) = make_uint4(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]),
-                                                  bf16x2_bits(v[4], v[5]), bf16x2_bits(v[6], v[7]));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < live) p[i] = __float2bfloat16_rn(v[i]);
-    }
-}
-
 // 32 bytes at once (32-byte aligned).
 __device__ __forceinline__ void ldg32(const void* p, uint32_t (&w)[8]) {
     asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -116,6 +101,34 @@ __device__ __forceinline__ void stg32(void* p, const uint32_t (&w)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
                  "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
+}
+
+// p[0 .. 7] = v, the elements at or past `live` left alone.
+__device__ __forceinline__ void store8(float* p, const float (&v)[8], int live, int acc) {
+    if (acc == 2 && live >= 8) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[i]);
+        stg32(p, w);
+    } else if (acc > 0 && live >= 8) {
+        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < live) p[i] = v[i];
+    }
+}
+
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8], int live, int acc) {
+    if (acc > 0 && live >= 8) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]),
+                                                  bf16x2_bits(v[4], v[5]), bf16x2_bits(v[6], v[7]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < live) p[i] = __float2bfloat16_rn(v[i]);
+    }
 }
 
 }  // namespace gt
