@@ -876,7 +876,7 @@ linear_join(int join, int m, int n, int splits, const float* __restrict__ part, 
     const int per_row = (n + 7) / 8;
     const int64_t row = idx / per_row;
     const int col = (int)(idx - row * per_row) * 8, live = n - col;
-#pragma unroll 4
+#pragma unroll 8
     for (int s = 0; s < splits; ++s) {
         float f[8];
         unpack8(load8_cg(part + s * plane + row * ldpart + col), f);
@@ -1125,7 +1125,7 @@ GemmPlan plan_gemm(int M, int N, int K, int planes, bool f32_out) {
             if (sp > 1 && (sp * n > units || kb / sp < (planes == 1 ? 4 : 2))) break;
             const int64_t waves = (n * sp + units - 1) / units;
             double us = t.once + waves * ((kb + sp - 1) / sp) * (planes == 1 ? t.step : t.step3) + (waves - 1) * t.more;
-            if (sp > 1) us += 3.0 + (double)M * N * (sp + 2) * 4 / 4e6;
+            if (sp > 1) us += 4.0 + (double)M * N * (sp + 2) * 4 / 2.5e6;
             if (us < best_us) {
                 best_us = us;
                 best.g = GemmShape{M, N, kb, planes, chunk_of(f32_out, planes), tm, tn, M % 64 == 0, N % 64 == 0, sp};

@@ -407,9 +407,10 @@ typedef enum { GT_ACT_NONE = 0, GT_ACT_GELU = 1 } gt_act;
 /*
  * gt_linear_fwd: a = x W + b, y = act(a) + r.
  *   dtype  type of x, W and pre: GT_BF16 (bf16 products, fp32 sums) or GT_F32
- *          (products of three-part bf16 splits, fp32 sums: fp32 accuracy; a
- *          non-finite input makes the sums it enters non-finite, NaN where exact
- *          arithmetic may give an infinity).
+ *          (products of three-part bf16 splits, fp32 sums: fp32 accuracy for inputs
+ *          above 2^-100 in magnitude, smaller ones lose low bits; a non-finite input
+ *          makes the sums it enters non-finite, NaN where exact arithmetic may give
+ *          an infinity).
  *   ytype  type of y and r: GT_F32, or GT_BF16 with dtype GT_BF16.
  *   x  device [m][ldx >= k]; W device [k][ldw >= n] (in x out); b device fp32 [n] or
  *   NULL; r device [m][ldr >= n] or NULL (it may be y itself).
