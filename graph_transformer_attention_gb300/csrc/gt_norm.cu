@@ -83,7 +83,7 @@ struct NormCfg {
     static constexpr int RED = TPR > 32 ? 2 * (TH / 32) * R : 1;
 };
 
-template <typename TX, typename TY, typename C>
+template <typename TX, typename TY, typename C, bool WHOLE>
 __global__ void __launch_bounds__(C::TH, C::OCC)
 norm_fwd(int64_t n, int c, const TX* __restrict__ x, int64_t ldx, const float* __restrict__ gain,
          const float* __restrict__ shift, float eps, TY* __restrict__ y, int64_t ldy, float* __restrict__ mean,
@@ -100,7 +100,7 @@ norm_fwd(int64_t n, int c, const TX* __restrict__ x, int64_t ldx, const float* _
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int col = (i * TPR + t) * 8;
-                raw[k][i] = load8(x + (row < n ? row : 0) * ldx + col, row < n ? c - col : 0, vec);
+                raw[k][i] = load8_row<WHOLE>(x + (row < n ? row : 0) * ldx + col, row < n ? c - col : 0, vec);
             }
         }
     };
@@ -113,18 +113,17 @@ norm_fwd(int64_t n, int c, const TX* __restrict__ x, int64_t ldx, const float* _
     // every thread of a CTA makes the same number of turns (the sums' barriers and shuffles)
     for (int64_t r0 = (int64_t)blockIdx.x * C::ROWS; r0 < n; r0 += step) {
         if (!kAhead) fetch(r0, raw);
-        float v[R][NV][8];
-        float2 s[R];
+        float2 v[R][NV][4], s[R];
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            float a = 0.f;
+            float2 a = make_float2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 unpack8(raw[k][i], v[k][i]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) a += v[k][i][j];
+                for (int j = 0; j < 4; ++j) a = __fadd2_rn(a, v[k][i][j]);
             }
-            s[k] = make_float2(a, 0.f);
+            s[k] = make_float2(a.x + a.y, 0.f);
         }
         if (kAhead && r0 + step < n) fetch(r0 + step, raw);
         rowsum(s);
@@ -132,17 +131,23 @@ norm_fwd(int64_t n, int c, const TX* __restrict__ x, int64_t ldx, const float* _
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             mu[k] = s[k].x * inv_c;
-            float q = 0.f;
+            const float2 minus = make_float2(-mu[k], -mu[k]);
+            float2 q = make_float2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int col = (i * TPR + t) * 8;
+                const int live = c - (i * TPR + t) * 8;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    v[k][i][j] -= mu[k];
-                    if (col + j < c) q = fmaf(v[k][i][j], v[k][i][j], q);
+                for (int j = 0; j < 4; ++j) {
+                    float2& u = v[k][i][j];
+                    u = __fadd2_rn(u, minus);
+                    if (WHOLE ? live <= 0 : live < 8) {   // columns past the end do not count
+                        if (2 * j >= live) u.x = 0.f;
+                        if (2 * j + 1 >= live) u.y = 0.f;
+                    }
+                    q = __ffma2_rn(u, u, q);
                 }
             }
-            s[k] = make_float2(q, 0.f);
+            s[k] = make_float2(q.x + q.y, 0.f);
         }
         rowsum(s);
 #pragma unroll
@@ -158,22 +163,28 @@ norm_fwd(int64_t n, int c, const TX* __restrict__ x, int64_t ldx, const float* _
         for (int i = 0; i < NV; ++i) {
             const int col = (i * TPR + t) * 8;
             if (col >= c) continue;
-            float gv[8], sv[8];
-            unpack8(load8(gain + col, c - col, vec), gv);
-            unpack8(load8(shift + col, c - col, vec), sv);
+            float2 gv[4], sv[4];
+            unpack8(load8_row<WHOLE>(gain + col, c - col, vec), gv);
+            unpack8(load8_row<WHOLE>(shift + col, c - col, vec), sv);
 #pragma unroll
             for (int k = 0; k < R; ++k) {
                 const int64_t row = r0 + k * RG + g;
                 if (row >= n) continue;
+                const float2 r = make_float2(s[k].x, s[k].x);
+                float o[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[k][i][j] = fmaf(v[k][i][j] * s[k].x, gv[j], sv[j]);
-                store8(y + row * ldy + col, v[k][i], c - col, vec);
+                for (int j = 0; j < 4; ++j) {
+                    const float2 u = __ffma2_rn(__fmul2_rn(v[k][i][j], r), gv[j], sv[j]);
+                    o[2 * j] = u.x;
+                    o[2 * j + 1] = u.y;
+                }
+                store8(y + row * ldy + col, o, WHOLE ? 8 : c - col, WHOLE ? max(vec, 1) : vec);
             }
         }
     }
 }
 
-template <typename TX, typename TY, typename C>
+template <typename TX, typename TY, typename C, bool WHOLE>
 __global__ void __launch_bounds__(C::TH, C::OCC)
 norm_bwd(int64_t n, int c, const TY* __restrict__ dy, int64_t lddy, const TX* __restrict__ x, int64_t ldx,
          const float* __restrict__ gain, const float* __restrict__ mean, const float* __restrict__ rstd,
@@ -185,13 +196,13 @@ norm_bwd(int64_t n, int c, const TY* __restrict__ dy, int64_t lddy, const TX* __
     sm100::pdl_trigger();   // the column sums may start; they wait for this kernel
     const int t = threadIdx.x % TPR, g = threadIdx.x / TPR;
     const float inv_c = 1.0f / (float)c;
-    float ag[NV][8], as[NV][8], gv[NV][8];
+    float2 ag[NV][4], as[NV][4], gv[NV][4];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int col = (i * TPR + t) * 8;
-        unpack8(load8(gain + col, c - col, vec), gv[i]);
+        unpack8(load8_row<WHOLE>(gain + col, c - col, vec), gv[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ag[i][j] = as[i][j] = 0.f;
+        for (int j = 0; j < 4; ++j) ag[i][j] = as[i][j] = make_float2(0.f, 0.f);
     }
     struct Rows {   // the inputs of R rows
         Raw8<TX> x[R][NV], res[R][NV];
@@ -205,12 +216,13 @@ norm_bwd(int64_t n, int c, const TY* __restrict__ dy, int64_t lddy, const TX* __
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int col = (i * TPR + t) * 8, live = row < n ? c - col : 0;
-                in.x[k][i] = load8(x + ra * ldx + col, live, vec);
-                in.dy[k][i] = load8(dy + ra * lddy + col, live, vec);
-                if (dres) in.res[k][i] = load8(dres + ra * ldr + col, live, vec);
+                in.x[k][i] = load8_row<WHOLE>(x + ra * ldx + col, live, vec);
+                in.dy[k][i] = load8_row<WHOLE>(dy + ra * lddy + col, live, vec);
+                if (dres) in.res[k][i] = load8_row<WHOLE>(dres + ra * ldr + col, live, vec);
             }
-            in.mu[k] = mean[ra];
-            in.rs[k] = rstd[ra];
+            // a row past the end is all zeros, and so are its xh and its sums
+            in.mu[k] = row < n ? mean[ra] : 0.f;
+            in.rs[k] = row < n ? rstd[ra] : 0.f;
         }
     };
     // the next rows are on their way while these are computed
@@ -220,48 +232,54 @@ norm_bwd(int64_t n, int c, const TY* __restrict__ dy, int64_t lddy, const TX* __
     for (int64_t r0 = (int64_t)blockIdx.x * C::ROWS; r0 < n; r0 += step) {
         const Rows in = next;
         if (r0 + step < n) fetch(r0 + step, next);
-        // xh of element j, zero where the row or the column is dead (there dy is zero, and
-        // its xh must not bring a NaN into the sums)
-        auto xhat = [&](int k, int i, const float (&xv)[8], int j) {
-            return r0 + k * RG + g < n && (i * TPR + t) * 8 + j < c ? (xv[j] - in.mu[k]) * in.rs[k] : 0.f;
+        // A column past the end has x = dy = 0: it adds nothing to the row's sums (or NaN to a row whose
+        // statistics are NaN), and its own sums are not stored.
+        auto xhat = [&](int k, float2 x2) {
+            return __fmul2_rn(__fadd2_rn(x2, make_float2(-in.mu[k], -in.mu[k])), make_float2(in.rs[k], in.rs[k]));
         };
         float2 m[R];
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            float m1 = 0.f, m2 = 0.f;
+            float2 m1 = make_float2(0.f, 0.f), m2 = m1;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                float xv[8], d[8];
+                float2 xv[4], d[4];
                 unpack8(in.x[k][i], xv);
                 unpack8(in.dy[k][i], d);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float xh = xhat(k, i, xv, j);
-                    ag[i][j] = fmaf(d[j], xh, ag[i][j]);
-                    as[i][j] += d[j];
-                    const float dg = d[j] * gv[i][j];
-                    m1 += dg;
-                    m2 = fmaf(dg, xh, m2);
+                for (int j = 0; j < 4; ++j) {
+                    const float2 xh = xhat(k, xv[j]), dg = __fmul2_rn(d[j], gv[i][j]);
+                    ag[i][j] = __ffma2_rn(d[j], xh, ag[i][j]);
+                    as[i][j] = __fadd2_rn(as[i][j], d[j]);
+                    m1 = __fadd2_rn(m1, dg);
+                    m2 = __ffma2_rn(dg, xh, m2);
                 }
             }
-            m[k] = make_float2(m1, m2);
+            m[k] = make_float2(m1.x + m1.y, m2.x + m2.y);
         }
         rowsum(m);
 #pragma unroll
         for (int k = 0; k < R; ++k) {
             const int64_t row = r0 + k * RG + g;
-            const float m1 = m[k].x * inv_c, m2 = m[k].y * inv_c;
+            const float2 m1 = make_float2(-m[k].x * inv_c, -m[k].x * inv_c), m2 = make_float2(-m[k].y * inv_c, -m[k].y * inv_c);
+            const float2 rs = make_float2(in.rs[k], in.rs[k]);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int col = (i * TPR + t) * 8;
                 if (row >= n || col >= c) continue;
-                float xv[8], d[8], o[8] = {};
+                float2 xv[4], d[4], o[4] = {};
                 unpack8(in.x[k][i], xv);
                 unpack8(in.dy[k][i], d);
                 if (dres) unpack8(in.res[k][i], o);
+                float out[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = fmaf(in.rs[k], fmaf(d[j], gv[i][j], -m1) - xhat(k, i, xv, j) * m2, o[j]);
-                store8(dx + row * lddx + col, o, c - col, vec);
+                for (int j = 0; j < 4; ++j) {
+                    const float2 u = __ffma2_rn(xhat(k, xv[j]), m2, __ffma2_rn(d[j], gv[i][j], m1));
+                    const float2 w = __ffma2_rn(rs, u, o[j]);
+                    out[2 * j] = w.x;
+                    out[2 * j + 1] = w.y;
+                }
+                store8(dx + row * lddx + col, out, WHOLE ? 8 : c - col, WHOLE ? max(vec, 1) : vec);
             }
         }
     }
@@ -272,18 +290,27 @@ norm_bwd(int64_t n, int c, const TY* __restrict__ dy, int64_t lddy, const TX* __
         for (int i = 0; i < NV; ++i) {
             const int col = (i * TPR + t) * 8;
             if (col >= c) continue;
-            store8(pr + col, ag[i], c - col, 0);
-            store8(pr + c + col, as[i], c - col, 0);
+            float u[8], w[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                u[2 * j] = ag[i][j].x; u[2 * j + 1] = ag[i][j].y;
+                w[2 * j] = as[i][j].x; w[2 * j + 1] = as[i][j].y;
+            }
+            store8(pr + col, u, c - col, 0);
+            store8(pr + c + col, w, c - col, 0);
         }
     } else {
         constexpr int W = TPR * 8;            // columns of one turn
         __shared__ float sum[RG][W + 4];
 #pragma unroll
         for (int i = 0; i < 2 * NV; ++i) {
-            float(&a)[8] = i < NV ? ag[i % NV] : as[i % NV];
+            const float2(&a)[4] = i < NV ? ag[i % NV] : as[i % NV];
             __syncthreads();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum[g][t * 8 + j] = a[j];
+            for (int j = 0; j < 4; ++j) {
+                sum[g][t * 8 + 2 * j] = a[j].x;
+                sum[g][t * 8 + 2 * j + 1] = a[j].y;
+            }
             __syncthreads();
             for (int k = threadIdx.x; k < W; k += TH) {
                 const int col = (i % NV) * W + k;
@@ -372,8 +399,9 @@ int run_fwd(int64_t n, int c, const void* x, int64_t ldx, const float* gain, con
         using C = decltype(cfg);
         const int64_t want = (n + C::ROWS - 1) / C::ROWS, most = (sizeof(TX) == 2 ? C::OCC : 16) * (int64_t)num_sms();
         LaunchScope ls("norm_fwd", s);
-        norm_fwd<TX, TY, C><<<(int)(want < most ? want : most), C::TH, 0, s>>>(
-            n, c, static_cast<const TX*>(x), ldx, gain, shift, eps, static_cast<TY*>(y), ldy, mean, rstd, vec);
+        auto kern = vec > 0 && c % 8 == 0 ? norm_fwd<TX, TY, C, true> : norm_fwd<TX, TY, C, false>;
+        kern<<<(int)(want < most ? want : most), C::TH, 0, s>>>(n, c, static_cast<const TX*>(x), ldx, gain, shift, eps,
+                                                                static_cast<TY*>(y), ldy, mean, rstd, vec);
         return check_launch();
     });
 }
@@ -387,7 +415,8 @@ int run_bwd(int64_t n, int c, const void* dy, int64_t lddy, const void* x, int64
     return bwd_dispatch(c, [&](auto cfg) {
         using C = decltype(cfg);
         LaunchScope ls("norm_bwd", s);
-        norm_bwd<TX, TY, C><<<norm_bwd_ctas(n, c), C::TH, 0, s>>>(
+        auto kern = vec > 0 && c % 8 == 0 ? norm_bwd<TX, TY, C, true> : norm_bwd<TX, TY, C, false>;
+        kern<<<norm_bwd_ctas(n, c), C::TH, 0, s>>>(
             n, c, static_cast<const TY*>(dy), lddy, static_cast<const TX*>(x), ldx, gain, mean, rstd,
             static_cast<const TX*>(dres), ldr, static_cast<TX*>(dx), lddx, part, vec);
         return check_launch();

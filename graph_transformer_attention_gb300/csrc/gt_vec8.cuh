@@ -69,6 +69,20 @@ __device__ __forceinline__ Raw8<float> load8_cg(const float* p) {
     return r;
 }
 
+// load8 where WHOLE says that rows are whole eights in 16-byte accesses: `live` is then 8 or more, or nothing.
+template <bool WHOLE, typename T>
+__device__ __forceinline__ Raw8<T> load8_row(const T* p, int live, int acc) {
+    if constexpr (!WHOLE) {
+        return load8(p, live, acc);
+    } else {
+        Raw8<T> r;
+        r.a = make_uint4(0, 0, 0, 0);
+        if constexpr (sizeof(T) == 4) r.b = r.a;
+        if (live > 0) r = load8(p, 8, sizeof(T) == 2 ? 1 : acc == 2 ? 2 : 1);
+        return r;
+    }
+}
+
 __device__ __forceinline__ void unpack8(const Raw8<float>& r, float (&v)[8]) {
     v[0] = __uint_as_float(r.a.x); v[1] = __uint_as_float(r.a.y); v[2] = __uint_as_float(r.a.z); v[3] = __uint_as_float(r.a.w);
     v[4] = __uint_as_float(r.b.x); v[5] = __uint_as_float(r.b.y); v[6] = __uint_as_float(r.b.z); v[7] = __uint_as_float(r.b.w);
@@ -81,6 +95,15 @@ __device__ __forceinline__ void unpack8(const Raw8<__nv_bfloat16>& r, float (&v)
         v[2 * i] = __uint_as_float(w[i] << 16);
         v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
+}
+
+// The same as pairs, for the packed arithmetic.
+template <typename T>
+__device__ __forceinline__ void unpack8(const Raw8<T>& r, float2 (&v)[4]) {
+    float t[8];
+    unpack8(r, t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = make_float2(t[2 * i], t[2 * i + 1]);
 }
 
 __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
