@@ -362,24 +362,28 @@ auto fwd_dispatch(int c, F&& f) {
     return f(NormCfg<1024, 2, 1, 1>());
 }
 
-// The backward's: one eight to a thread, whose gradient sums stay in registers beside the next row
-// (two next rows where a row group is a warp or less).
-template <typename F>
+// The backward's: one or two eights to a thread, whose gradient sums stay in registers beside the next rows.
+// Rows of bf16 are half as wide in registers, so more of them are on their way.  Measured (share of the copy rate,
+// dres with it): 65536 x 512 bf16 64 % with one row of 64 threads and three CTAs, 86 % with two rows and two CTAs
+// (fp32 93 and 83 %, with four rows and one CTA 98 %); 16384 x 2048 bf16 63 % with 256 threads to a row, 82 % with
+// 128 (fp32 81 and 96 %); 16384 x 4096 bf16 72 % with one row of 512 threads, 86 % with two of 256 (fp32 90 and 74 %).
+template <bool HALF, typename F>
 auto bwd_dispatch(int c, F&& f) {
     if (c <= 64) return f(NormCfg<8, 1, 2, 2>());
     if (c <= 128) return f(NormCfg<16, 1, 2, 2>());
     if (c <= 256) return f(NormCfg<32, 1, 2, 2>());
-    if (c <= 512) return f(NormCfg<64, 1, 1, 3>());
-    if (c <= 1024) return f(NormCfg<128, 1, 1, 3>());
-    if (c <= 2048) return f(NormCfg<256, 1, 1, 3>());
-    if (c <= 4096) return f(NormCfg<512, 1, 1, 1>());
-    if (c <= 8192) return f(NormCfg<1024, 1, 1, 1>());
+    if (c <= 512) return f(NormCfg<64, 1, HALF ? 2 : 4, HALF ? 2 : 1>());
+    if (c <= 1024) return f(NormCfg<128, 1, HALF ? 2 : 4, HALF ? 2 : 1>());
+    if (c <= 2048) return f(NormCfg<128, 2, 2, 1>());
+    if (c <= 4096) return f(NormCfg<HALF ? 256 : 512, HALF ? 2 : 1, HALF ? 2 : 1, 1>());
+    if (c <= 8192) return f(NormCfg<512, 2, 1, 1>());
     return f(NormCfg<1024, 2, 1, 1>());
 }
 
 // CTAs of the backward, each of which makes one partial row: those that are resident at once.
+template <bool HALF>
 int norm_bwd_ctas(int64_t n, int c) {
-    return bwd_dispatch(c, [&](auto cfg) {
+    return bwd_dispatch<HALF>(c, [&](auto cfg) {
         using C = decltype(cfg);
         const int64_t want = (n + C::ROWS - 1) / C::ROWS, most = (int64_t)C::OCC * num_sms();
         return (int)(want < most ? want : most);
@@ -409,14 +413,14 @@ int run_fwd(int64_t n, int c, const void* x, int64_t ldx, const float* gain, con
 template <typename TX, typename TY>
 int run_bwd(int64_t n, int c, const void* dy, int64_t lddy, const void* x, int64_t ldx, const float* gain,
             const float* mean, const float* rstd, const void* dres, int64_t ldr, void* dx, int64_t lddx, float* part,
-            cudaStream_t s) {
+            int ctas, cudaStream_t s) {
     const int vec = least({row_access(x, ldx, sizeof(TX)), row_access(dy, lddy, sizeof(TY)),
                            row_access(dx, lddx, sizeof(TX)), row_access(dres, ldr, sizeof(TX)), row_access(gain, 0, 4)});
-    return bwd_dispatch(c, [&](auto cfg) {
+    return bwd_dispatch<sizeof(TX) == 2>(c, [&](auto cfg) {
         using C = decltype(cfg);
         LaunchScope ls("norm_bwd", s);
         auto kern = vec > 0 && c % 8 == 0 ? norm_bwd<TX, TY, C, true> : norm_bwd<TX, TY, C, false>;
-        kern<<<norm_bwd_ctas(n, c), C::TH, 0, s>>>(
+        kern<<<ctas, C::TH, 0, s>>>(
             n, c, static_cast<const TY*>(dy), lddy, static_cast<const TX*>(x), ldx, gain, mean, rstd,
             static_cast<const TX*>(dres), ldr, static_cast<TX*>(dx), lddx, part, vec);
         return check_launch();
@@ -444,7 +448,7 @@ extern "C" {
 
 size_t gt_layer_norm_workspace_size(int32_t n, int32_t c) {
     if (gt::check_norm(GT_F32, GT_F32, n, c) != GT_OK) return 0;
-    return (size_t)gt::norm_bwd_ctas(n, c) * 2 * c * sizeof(float) + 256;
+    return (size_t)std::max(gt::norm_bwd_ctas<false>(n, c), gt::norm_bwd_ctas<true>(n, c)) * 2 * c * sizeof(float) + 256;
 }
 
 int gt_layer_norm_fwd(int32_t xtype, int32_t ytype, int32_t n, int32_t c, const void* x, int64_t ldx,
@@ -473,7 +477,7 @@ int gt_layer_norm_bwd(int32_t xtype, int32_t ytype, int32_t n, int32_t c, const 
     if (rc != GT_OK) return rc;
     if (!dy || !x || !gain || !mean || !rstd || !dx || !dgain || !dshift) return GT_ERR_INVALID_ARG;
     if (lddy < c || ldx < c || lddx < c || (dres && ldr < c)) return GT_ERR_INVALID_ARG;
-    const int ctas = norm_bwd_ctas(n, c);
+    const int ctas = xtype == GT_F32 ? norm_bwd_ctas<false>(n, c) : norm_bwd_ctas<true>(n, c);
     Carve cv(workspace, ws_bytes);
     float* part = cv.take<float>((size_t)ctas * 2 * c);
     if (!workspace || !aligned16(workspace) || !cv.fits()) return GT_ERR_WORKSPACE;
@@ -481,12 +485,12 @@ int gt_layer_norm_bwd(int32_t xtype, int32_t ytype, int32_t n, int32_t c, const 
     using B = __nv_bfloat16;
     if (xtype == GT_F32)
         rc = ytype == GT_F32
-                 ? run_bwd<float, float>(n, c, dy, lddy, x, ldx, gain, mean, rstd, dres, ldr, dx, lddx, part, s)
-                 : run_bwd<float, B>(n, c, dy, lddy, x, ldx, gain, mean, rstd, dres, ldr, dx, lddx, part, s);
+                 ? run_bwd<float, float>(n, c, dy, lddy, x, ldx, gain, mean, rstd, dres, ldr, dx, lddx, part, ctas, s)
+                 : run_bwd<float, B>(n, c, dy, lddy, x, ldx, gain, mean, rstd, dres, ldr, dx, lddx, part, ctas, s);
     else
         rc = ytype == GT_F32
-                 ? run_bwd<B, float>(n, c, dy, lddy, x, ldx, gain, mean, rstd, dres, ldr, dx, lddx, part, s)
-                 : run_bwd<B, B>(n, c, dy, lddy, x, ldx, gain, mean, rstd, dres, ldr, dx, lddx, part, s);
+                 ? run_bwd<B, float>(n, c, dy, lddy, x, ldx, gain, mean, rstd, dres, ldr, dx, lddx, part, ctas, s)
+                 : run_bwd<B, B>(n, c, dy, lddy, x, ldx, gain, mean, rstd, dres, ldr, dx, lddx, part, ctas, s);
     if (rc != GT_OK) return rc;
     return launch_col_sum(part, ctas, 2 * c, dgain, c, dshift, s);
 }
