@@ -105,7 +105,7 @@ norm_fwd(int64_t n, int c, const TX* __restrict__ x, int64_t ldx, const float* _
         }
     };
     // Rows of bf16 are fetched a turn ahead, by as many CTAs as are resident; of fp32, whose rows take twice the
-    // registers, more CTAs take turns instead (32768 x 1024: bf16 26 against 31 us, fp32 in and bf16 out 34 against 37 us).
+    // registers, more CTAs take turns instead (32768 x 1024: bf16 26 against 31 us; fp32 in and bf16 out 34, and 37 with rows fetched ahead).
     constexpr bool kAhead = sizeof(TX) == 2;
     Raw8<TX> raw[R][NV];
     const int64_t step = (int64_t)gridDim.x * C::ROWS;
@@ -225,8 +225,8 @@ norm_bwd(int64_t n, int c, const TY* __restrict__ dy, int64_t lddy, const TX* __
             in.rs[k] = row < n ? rstd[ra] : 0.f;
         }
     };
-    // The next rows are on their way while these are computed, where the registers hold both (4096 x 8192: bf16
-    // 71 against 79 us, fp32, which spills then, 117 against 101).
+    // The next rows are on their way while these are computed, where the registers hold both (4096 x 8192
+    // with 512 threads to a row: bf16 71 against 79 us, fp32, which spills then, 117 against 101).
     constexpr bool kAhead = TPR * NV * sizeof(TX) <= 2048;
     Rows next;
     const int64_t step = (int64_t)gridDim.x * C::ROWS;
@@ -351,21 +351,26 @@ __global__ void __launch_bounds__(kColSumThreads) col_sum(const float* __restric
     }
 }
 
-// The forward's layout by width: two eights to a thread, so that a warp holds rows of up to 512 features.
-template <typename F>
+// The forward's layout by width: two eights to a thread, so that a warp holds rows of up to 512 features.  Measured
+// with three and four CTAs on an SM: 32768 x 1024 fp32 to bf16 34.1 and 32.5 us, 65536 x 512 fp32 42.2 and 43.0;
+// with one row and two rows of 256 threads: 16384 x 4096 bf16 51.1 and 49.5 us, fp32 to bf16 68.7 and 76.0;
+// 8192 x 8192 bf16 59 us with 512 threads to a row, 50 with 256.
+template <typename TX, typename TY, typename F>
 auto fwd_dispatch(int c, F&& f) {
-    if (c <= 64) return f(NormCfg<8, 1, 2, 3>());
-    if (c <= 128) return f(NormCfg<8, 2, 2, 3>());
-    if (c <= 256) return f(NormCfg<16, 2, 2, 3>());
-    if (c <= 512) return f(NormCfg<32, 2, 2, 3>());
-    if (c <= 1024) return f(NormCfg<64, 2, 2, 3>());
-    if (c <= 2048) return f(NormCfg<128, 2, 2, 3>());
-    if (c <= 4096) return f(NormCfg<256, 2, 1, 4>());
-    if (c <= 8192) return f(NormCfg<512, 2, 1, 2>());
-    return f(NormCfg<1024, 2, 1, 1>());
+    constexpr bool HALF = sizeof(TX) == 2;
+    constexpr int OCC = sizeof(TX) > sizeof(TY) ? 4 : 3;
+    if (c <= 64) return f(NormCfg<8, 1, 2, OCC>());
+    if (c <= 128) return f(NormCfg<8, 2, 2, OCC>());
+    if (c <= 256) return f(NormCfg<16, 2, 2, OCC>());
+    if (c <= 512) return f(NormCfg<32, 2, 2, OCC>());
+    if (c <= 1024) return f(NormCfg<64, 2, 2, OCC>());
+    if (c <= 2048) return f(NormCfg<128, 2, 2, OCC>());
+    if (c <= 4096) return f(NormCfg<256, 2, HALF ? 2 : 1, HALF ? 2 : 4>());
+    if (c <= 8192) return f(NormCfg<256, 4, 1, 2>());
+    return f(NormCfg<512, 4, 1, HALF ? 1 : 2>());
 }
 
-// The backward's: one or two eights to a thread, whose gradient sums stay in registers beside the next rows.
+// The backward's: one eight to a thread (more from 1024 features on), whose gradient sums stay in registers beside the next rows.
 // Rows of bf16 are half as wide in registers, so more of them are on their way.  Measured (share of the copy rate,
 // dres with it): 65536 x 512 bf16 64 % with one row of 64 threads and three CTAs, 86 % with two rows and two CTAs
 // (fp32 93 and 83 %, with four rows and one CTA 98 %); 16384 x 2048 bf16 63 % with 256 threads to a row, 82 % with
@@ -379,7 +384,7 @@ auto bwd_dispatch(int c, F&& f) {
     if (c <= 1024) return f(NormCfg<128, 1, HALF ? 2 : 4, HALF ? 2 : 1>());
     if (c <= 2048) return f(NormCfg<128, 2, 2, 1>());
     if (c <= 4096) return f(NormCfg<HALF ? 256 : 512, HALF ? 2 : 1, HALF ? 2 : 1, 1>());
-    if (c <= 8192) return f(NormCfg<512, 2, 1, 1>());
+    if (c <= 8192) return f(NormCfg<256, 4, 1, 1>());
     return f(NormCfg<512, 4, 1, 1>());
 }
 
@@ -402,7 +407,7 @@ int run_fwd(int64_t n, int c, const void* x, int64_t ldx, const float* gain, con
             int64_t ldy, float* mean, float* rstd, cudaStream_t s) {
     const int vec = least({row_access(x, ldx, sizeof(TX)), row_access(y, ldy, sizeof(TY)), row_access(gain, 0, 4),
                            row_access(shift, 0, 4)});
-    return fwd_dispatch(c, [&](auto cfg) {
+    return fwd_dispatch<TX, TY>(c, [&](auto cfg) {
         using C = decltype(cfg);
         const int64_t want = (n + C::ROWS - 1) / C::ROWS, most = (sizeof(TX) == 2 ? C::OCC : 16) * (int64_t)num_sms();
         LaunchScope ls("norm_fwd", s);
