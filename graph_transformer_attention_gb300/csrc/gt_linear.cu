@@ -248,7 +248,7 @@ struct Epi {
     void* pre;
     int64_t ldr, ldy, ldpre;
     bool gelu_act, y_f32, pre_f32;
-    bool single;   // some rows can only be reached by single elements: left to linear_join
+    bool single;   // some rows can only be reached by single elements: through the staging tiles, or left to linear_join
     bool bulk;     // bf16 results go out as TMA boxes (the pair kernel; maps in the kernel's arguments)
     int racc, yacc, pacc;
 };
@@ -376,20 +376,33 @@ __device__ __forceinline__ void epilogue(const Epi& e, int64_t row, int col, int
     put_row<CW>(e.y, row * e.ldy + col, e.y_f32, v, live, e.yacc);
 }
 
-// The same for a whole warp and 32 columns of bf16 results, through the warp's 2 KB staging tile and
-// TMA: rows of 64 bytes, 64-byte swizzle.  A lane's row in 32-byte pieces costs the L1 four times
-// the cycles of whole lines, and the products need that memory's bandwidth (32768x1024x4096, GELU and pre: 195 -> 185 us alone).
+// The same for a whole warp and 32 columns of bf16 results, through the warp's 2 KB staging tile: rows of
+// 64 bytes, 64-byte swizzle.  They leave by TMA (a lane's row in 32-byte pieces costs the L1 four times
+// the cycles of whole lines, and the products need that memory's bandwidth: 32768x1024x4096, GELU and pre, 195 -> 185 us
+// alone), or, where rows can only be reached so, by single elements, a row of the tile at a time
+// (20000x1001x999 with a residual: 142 us with linear_join's help, 86 us so).
 constexpr int kBoxCols = 32, kBoxBytes = 32 * kBoxCols * 2;
+
+__device__ __forceinline__ uint32_t box_unit(uint32_t stg, int row, int unit) {   // 16 bytes, eight columns
+    return stg + row * 64 + ((unit ^ ((row >> 1) & 3)) << 4);
+}
+__device__ __forceinline__ uint32_t box_element(uint32_t stg, int row, int col) {
+    return box_unit(stg, row, col >> 3) + (col & 7) * 2;
+}
+
+__device__ __forceinline__ void fill_box(const float (&v)[32], uint32_t stg) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        sts_u4(box_unit(stg, lane, j), pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+               pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+}
 
 __device__ __forceinline__ void put_box(const CUtensorMap* map, int64_t row0, int col, const float (&v)[32], uint32_t stg) {
     const int lane = threadIdx.x & 31;
     if (lane == 0) bulk_wait_read();   // the tile's last box has been read
     __syncwarp();
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        sts_u4(stg + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4), pack_bf16x2(v[8 * j], v[8 * j + 1]),
-               pack_bf16x2(v[8 * j + 2], v[8 * j + 3]), pack_bf16x2(v[8 * j + 4], v[8 * j + 5]),
-               pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+    fill_box(v, stg);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     if (lane == 0) {
@@ -398,15 +411,61 @@ __device__ __forceinline__ void put_box(const CUtensorMap* map, int64_t row0, in
     }
 }
 
-__device__ __forceinline__ void epilogue_bulk(const Epi& e, const CUtensorMap* map_y, const CUtensorMap* map_pre,
-                                              int64_t row0, int M, int col, int live, float (&v)[32], uint32_t bias,
-                                              uint32_t stg) {
+// p: the array at the box's first row and column, of which `rows` rows and `live` columns exist.
+__device__ __forceinline__ void put_elements(bf16* p, int64_t ld, int rows, int live, const float (&v)[32], uint32_t stg) {
+    const int lane = threadIdx.x & 31;
+    fill_box(v, stg);
+    __syncwarp();
+#pragma unroll 8
+    for (int i = 0; i < 32; ++i) {
+        uint16_t e;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e) : "r"(box_element(stg, i, lane)) : "memory");
+        if (i < rows && lane < live) p[i * ld + lane] = __ushort_as_bfloat16(e);
+    }
+    __syncwarp();
+}
+__device__ __forceinline__ void add_elements(const bf16* p, int64_t ld, int rows, int live, float (&v)[32], uint32_t stg) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = 0; h < 32; h += 16) {
+        uint16_t e[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) e[i] = h + i < rows && lane < live ? __bfloat16_as_ushort(p[(h + i) * ld + lane]) : 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(box_element(stg, h + i, lane)), "h"(e[i]) : "memory");
+    }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint4 w = lds_u4(box_unit(stg, lane, j));
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[8 * j + 2 * i] += __uint_as_float(u[i] << 16);
+            v[8 * j + 2 * i + 1] += __uint_as_float(u[i] & 0xffff0000u);
+        }
+    }
+    __syncwarp();
+}
+
+__device__ __forceinline__ void epilogue_box(const Epi& e, const CUtensorMap* map_y, const CUtensorMap* map_pre,
+                                             int64_t row0, int M, int col, int live, float (&v)[32], uint32_t bias,
+                                             uint32_t stg) {
+    const int rows = (int)(M - row0);
     add_bias<32>(v, bias);
-    if (e.pre) put_box(map_pre, row0, col, v, stg);
+    if (e.pre) {
+        if (e.bulk) put_box(map_pre, row0, col, v, stg);
+        else put_elements(static_cast<bf16*>(e.pre) + row0 * e.ldpre + col, e.ldpre, rows, live, v, stg);
+    }
     if (e.gelu_act) apply_gelu<32>(v);
-    const int64_t row = row0 + (threadIdx.x & 31);
-    if (e.r && row < M) add_row<32>(e.r, row * e.ldr + col, false, v, live, e.racc);
-    put_box(map_y, row0, col, v, stg);
+    if (e.r) {
+        const int64_t row = row0 + (threadIdx.x & 31);
+        if (!e.bulk) add_elements(static_cast<const bf16*>(e.r) + row0 * e.ldr + col, e.ldr, rows, live, v, stg);
+        else if (row < M) add_row<32>(e.r, row * e.ldr + col, false, v, live, e.racc);
+    }
+    if (e.bulk) put_box(map_y, row0, col, v, stg);
+    else put_elements(static_cast<bf16*>(e.y) + row0 * e.ldy + col, e.ldy, rows, live, v, stg);
 }
 
 // ------------------------------------------------------------- the product kernel
@@ -461,7 +520,7 @@ struct GemmCfg {
     static constexpr int kBM = 128 * CTAS;
     static constexpr int kStageB = BN / CTAS * kBK * 2;   // a CTA of a pair holds half of B's columns
     static constexpr int kStage = kStageA + kStageB;
-    static constexpr bool kBulk = CTAS == 2 && !SUM;      // bf16 results, which go out as TMA boxes
+    static constexpr bool kBulk = CTAS == 2 && !SUM;      // bf16 results, which go out by staging tiles
     static constexpr int kStages = (kBulk ? 160 : 192) * 1024 / kStage;   // 5 to 8
     static constexpr int kStg = kBulk ? kBoxBytes : 0;    // staging of an epilogue warp
     static constexpr int kSmem = kStages * kStage + kEpiWarps * kStg + 1024;
@@ -765,11 +824,11 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
 #pragma unroll
                     for (int j = 0; j < CW; ++j) f[j] = SUM ? f[j] + __uint_as_float(v[j]) : __uint_as_float(v[j]);
                     if (!SUM || last) {
-                        if (C::kBulk && epi.bulk && !part) {
+                        if (C::kBulk && (epi.bulk || epi.single) && !part) {
                             if constexpr (C::kBulk) {
                                 if (live > 0 && row - lane < g.M)
-                                    epilogue_bulk(epi, &map_y, &map_pre, row - lane, g.M, col, live, f, bias + 4 * c * CW,
-                                                  smem_u32(stg));
+                                    epilogue_box(epi, &map_y, &map_pre, row - lane, g.M, col, live, f, bias + 4 * c * CW,
+                                                 smem_u32(stg));
                             }
                         } else if (row < g.M && live > 0) {
                             if (part) put_row<CW>(part, ((int64_t)w.s * g.M + row) * ldpart + col, true, f, (live + 7) & ~7, 2);
@@ -1142,9 +1201,16 @@ GemmPlan plan_gemm(int M, int N, int K, int planes, bool f32_out) {
     return best;
 }
 
-// Floats of the sums that the product kernel leaves to linear_join.
-size_t part_floats(const GemmPlan& p, bool single) {
-    return p.g.splits > 1 || single ? (size_t)p.g.splits * p.g.M * pad8(p.g.N) : 0;
+bool one_chunk(const GemmPlan& p) { return (p.g.kblocks + p.g.splits - 1) / p.g.splits <= p.g.chunk; }
+
+// Whether the product kernel leaves its sums to linear_join: splits, and rows that can only be reached by single
+// elements, unless its staging tiles can (bf16: GemmCfg's kBulk).  For fp32 results the joining kernel, with its many
+// more warps, is the faster way (4099x321x1001 with a fp32 residual: 30 us, through staging tiles 35).
+bool leaves_sums(const GemmPlan& p, bool single, bool f32_out) {
+    return p.g.splits > 1 || (single && (f32_out || p.ctas == 1 || !one_chunk(p)));
+}
+size_t part_floats(const GemmPlan& p, bool single, bool f32_out) {
+    return leaves_sums(p, single, f32_out) ? (size_t)p.g.splits * p.g.M * pad8(p.g.N) : 0;
 }
 
 template <int CTAS, int BN, bool SUM, bool A_MN, bool B_MN>
@@ -1210,20 +1276,20 @@ int run_gemm(const GemmPlan& p, const Operand& a, const Operand& b, const Epi& e
     CUtensorMap ma, mb;
     if (!operand_map(&ma, a, A_MN, p.g.whole_a, 128) || !operand_map(&mb, b, B_MN, p.g.whole_b, p.bn / p.ctas))
         return GT_ERR_CUDA;
-    float* out = p.g.splits > 1 || epi.single ? part : nullptr;
-    const bool one_chunk = (p.g.kblocks + p.g.splits - 1) / p.g.splits <= p.g.chunk;
+    float* out = leaves_sums(p, epi.single, epi.y_f32 || epi.pre_f32) ? part : nullptr;
+    const bool whole = one_chunk(p);
     if (p.bn == 256)
-        return one_chunk ? launch_gemm<2, 256, false, A_MN, B_MN>(p, ma, mb, epi, out, follows, s)
+        return whole ? launch_gemm<2, 256, false, A_MN, B_MN>(p, ma, mb, epi, out, follows, s)
                          : launch_gemm<2, 256, true, A_MN, B_MN>(p, ma, mb, epi, out, follows, s);
     if (p.bn == 128)
-        return one_chunk ? launch_gemm<2, 128, false, A_MN, B_MN>(p, ma, mb, epi, out, follows, s)
+        return whole ? launch_gemm<2, 128, false, A_MN, B_MN>(p, ma, mb, epi, out, follows, s)
                          : launch_gemm<2, 128, true, A_MN, B_MN>(p, ma, mb, epi, out, follows, s);
     return launch_gemm<1, 64, true, A_MN, B_MN>(p, ma, mb, epi, out, follows, s);
 }
 
 // linear_join of p's sums (if it has left any) and the column sums (if any).
 int run_join(const GemmPlan* p, const float* part, const Epi& epi, const ColSum& cs, cudaStream_t s) {
-    const bool join = p && (p->g.splits > 1 || epi.single);
+    const bool join = p && leaves_sums(*p, epi.single, epi.y_f32 || epi.pre_f32);
     if (!join && !cs.out) return GT_OK;
     const int M = join ? p->g.M : 0, N = join ? p->g.N : 0;
     const int nj = (int)((join_threads(M, N, epi.single) + kJoinThreads - 1) / kJoinThreads);
@@ -1316,7 +1382,7 @@ size_t fwd_bufs(int dtype, bool y_f32, int m, int k, int n, bool pack_x, bool pa
     FwdBufs b;
     b.x = pack_x ? c.take<bf16>(operand_elems(dtype, m, k)) : nullptr;
     b.w = pack_w ? c.take<bf16>(operand_elems(dtype, k, n)) : nullptr;
-    b.part = c.take<float>(part_floats(plan_gemm(m, n, k, planes_of(dtype), y_f32), single));
+    b.part = c.take<float>(part_floats(plan_gemm(m, n, k, planes_of(dtype), y_f32), single, y_f32));
     if (out) *out = b;
     return c.off;
 }
@@ -1334,8 +1400,8 @@ size_t bwd_bufs(int dtype, int m, int k, int n, bool pack_x, bool pack_w, bool o
     b.x = pack_x ? c.take<bf16>(operand_elems(dtype, m, k)) : nullptr;
     b.w = pack_w ? c.take<bf16>(operand_elems(dtype, k, n)) : nullptr;
     b.da = own_da ? c.take<bf16>(operand_elems(dtype, m, n)) : nullptr;
-    const size_t px = part_floats(plan_gemm(m, k, n, planes_of(dtype), dtype == GT_F32), single_x);
-    const size_t pw = part_floats(plan_gemm(k, n, m, planes_of(dtype), dtype == GT_F32), single_w);
+    const size_t px = part_floats(plan_gemm(m, k, n, planes_of(dtype), dtype == GT_F32), single_x, dtype == GT_F32);
+    const size_t pw = part_floats(plan_gemm(k, n, m, planes_of(dtype), dtype == GT_F32), single_w, dtype == GT_F32);
     b.part = c.take<float>(px > pw ? px : pw);
     b.cols = c.take<float>((size_t)prep_grid(m, n).gy * n);
     if (out) *out = b;
