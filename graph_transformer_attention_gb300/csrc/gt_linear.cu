@@ -575,6 +575,12 @@ struct Ring {
 // The tensor core drops what does not fit when it adds to its fp32 accumulator (measured on
 // all-positive sums: 4.4e-8 of the sum lost per 16-deep step).  So an accumulator takes at most
 // g.chunk k-blocks; the warps that take it out add the chunks up in registers, rounding to nearest.
+//
+// Measured (single calls on one GB300): 32768 x 1024 x 4096 bf16 150 us (1.83 PFLOP/s, 97 % of the library product's
+// rate), with GELU 156, with GELU and pre 183 (its boxes take shared memory's cycles from the products' operands);
+// dx 150, dW 156 (64 tiles for 76 pairs of SMs); fp32, 4096 x 1024 x 4096: 160 us, preparation included.
+// The products of 256 x 256 tiles run at the tensor rate but for the ends of tiles; calls one after another
+// run into the power limit, as the library's do.
 template <int CTAS, int BN, bool SUM, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kGemmThreads, 1)
 linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,

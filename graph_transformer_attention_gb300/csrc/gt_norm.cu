@@ -14,6 +14,10 @@
 // over all its rows; a CTA adds its row groups' sums in shared memory and stores
 // one partial row, and a second kernel adds the partial rows in a fixed order
 // (no atomics: the same result on every run).
+//
+// Measured (one GB300, inputs larger than the L2; share of the copy rate, 6.79 TB/s): forward 32768 x 1024
+// fp32 to bf16 32.5 us (91 %), bf16 26.4 us (75 %); backward with dres 32768 x 1024 bf16 46.5 us (85 %), 16384 x 4096
+// bf16 92 us (86 %), 65536 x 512 fp32 81 us (98 %); small inputs are latency: 6800 x 64 fp32 3.0 us and 4.9 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -411,6 +415,7 @@ int run_fwd(int64_t n, int c, const void* x, int64_t ldx, const float* gain, con
         using C = decltype(cfg);
         const int64_t want = (n + C::ROWS - 1) / C::ROWS, most = (sizeof(TX) == 2 ? C::OCC : 16) * (int64_t)num_sms();
         LaunchScope ls("norm_fwd", s);
+        // rows of whole eights need no bounds inside an eight (16384 x 4096 bf16 51 us, 53 with them)
         auto kern = vec > 0 && c % 8 == 0 ? norm_fwd<TX, TY, C, true> : norm_fwd<TX, TY, C, false>;
         kern<<<(int)(want < most ? want : most), C::TH, 0, s>>>(n, c, static_cast<const TX*>(x), ldx, gain, shift, eps,
                                                                 static_cast<TY*>(y), ldy, mean, rstd, vec);
