@@ -24,6 +24,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <algorithm>
 #include <type_traits>
 
 #include "gt_common.cuh"
@@ -581,12 +583,23 @@ struct Ring {
 // dx 150, dW 156 (64 tiles for 76 pairs of SMs); fp32, 4096 x 1024 x 4096: 160 us, preparation included.
 // The products of 256 x 256 tiles run at the tensor rate but for the ends of tiles; calls one after another
 // run into the power limit, as the library's do.
+struct GemmJob {
+    CUtensorMap a, b, y, pre;
+    GemmShape g;
+    Epi epi;
+    float* part;
+    int64_t ldpart;
+};
+
+// The job's items first, first + stride, ... by one CTA, or a pair.
 template <int CTAS, int BN, bool SUM, bool A_MN, bool B_MN>
-__global__ void __launch_bounds__(kGemmThreads, 1)
-linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-            const __grid_constant__ CUtensorMap map_y, const __grid_constant__ CUtensorMap map_pre, const GemmShape g,
-            const __grid_constant__ Epi epi, float* __restrict__ part, int64_t ldpart, int* status) {
+__device__ __forceinline__ void gemm_job(const GemmJob& job, const int first, const int stride, int* status) {
     using C = GemmCfg<CTAS, BN, SUM>;
+    const CUtensorMap &map_a = job.a, &map_b = job.b, &map_y = job.y, &map_pre = job.pre;
+    const GemmShape& g = job.g;
+    const Epi& epi = job.epi;
+    float* __restrict__ part = job.part;
+    const int64_t ldpart = job.ldpart;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ GemmBars bars;
@@ -620,7 +633,7 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     volatile int* abort_flag = &bars.abort;
     pdl_trigger();   // the call's next kernel may start; it waits for this one before it reads
     pdl_wait();      // the kernels before this one have finished
-    const int items = g.items(), first = blockIdx.x / CTAS, stride = gridDim.x / CTAS;
+    const int items = g.items();
 
     if (warp == kTmaWarp || warp == kTmaWarp + 1) {
         // The whole warp runs the loop and waits; the elected lane issues (from a diverged warp a
@@ -858,9 +871,26 @@ linear_gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ C
     }
 }
 
+template <int CTAS, int BN, bool SUM, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(kGemmThreads, 1) linear_gemm(const __grid_constant__ GemmJob job, int* status) {
+    gemm_job<CTAS, BN, SUM, A_MN, B_MN>(job, blockIdx.x / CTAS, gridDim.x / CTAS, status);
+}
+
+// Both products of a backward in one launch, where each alone would leave pairs of SMs idle and pay a launch: the first
+// units_x pairs make da W^T, the others x^T da (device time of the call, before and after: 6800x256x1024 bf16 with GELU
+// 34.8 and 29.1 us, 4096x512x512 fp32 45.8 and 39.9, 512x512x2048 bf16 23.0 and 18.1).
+constexpr int kBothBN = 128;
+template <bool SUM>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+linear_gemm_both(const __grid_constant__ GemmJob x, const __grid_constant__ GemmJob w, const int units_x, int* status) {
+    const int unit = blockIdx.x / 2, units = gridDim.x / 2;
+    if (unit < units_x) gemm_job<2, kBothBN, SUM, false, false>(x, unit, units_x, status);
+    else gemm_job<2, kBothBN, SUM, true, true>(w, unit - units_x, units - units_x, status);
+}
+
 // The end of a call in one launch: the sums that the product kernel left (of the contraction's splits,
 // added in a fixed order, and any whose rows can only be reached by single elements) through the
-// epilogue (CTAs below `join`), and the column sums of the preparation's partial rows (the CTAs from there on,
+// epilogue (of up to two products: the first j0.ctas CTAs, the next j1.ctas), and the column sums of the preparation's partial rows (the CTAs from there on,
 // 32 columns each, as col_sum in gt_norm.cu).  A thread takes 8 consecutive columns of a row, or
 // single: every 32nd of 256, so that a warp's accesses are consecutive elements (4099 x 321 x 1001, fp32 y and
 // residual: 58 us with those in the product kernel's epilogue, where a lane holds a row, 14 + 14 us so).
@@ -883,12 +913,19 @@ __device__ __forceinline__ void store_one(void* p, int64_t at, bool f32, float v
     else static_cast<bf16*>(p)[at] = __float2bfloat16_rn(v);
 }
 
+struct JoinJob {
+    int ctas, m, n, splits;
+    const float* part;
+    int64_t ldpart;
+    Epi epi;
+};
+
 __global__ void __launch_bounds__(kJoinThreads)
-linear_join(int join, int m, int n, int splits, const float* __restrict__ part, int64_t ldpart, const Epi epi,
-            const ColSum cs) {
+linear_join(const __grid_constant__ JoinJob j0, const __grid_constant__ JoinJob j1, const ColSum cs) {
     __shared__ alignas(16) float bias_s[kJoinThreads][8];
     pdl_trigger();
     pdl_wait();
+    const int join = j0.ctas + j1.ctas;
     if ((int)blockIdx.x >= join) {
         float(&red)[kJoinThreads][8] = bias_s;
         const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
@@ -908,7 +945,13 @@ linear_join(int join, int m, int n, int splits, const float* __restrict__ part, 
         }
         return;
     }
-    const int64_t idx = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x;
+    const bool second = (int)blockIdx.x >= j0.ctas;
+    // (values, not references: those of a chosen parameter would be read through the memory pipe)
+    const Epi epi = second ? j1.epi : j0.epi;
+    const int m = second ? j1.m : j0.m, n = second ? j1.n : j0.n, splits = second ? j1.splits : j0.splits;
+    const int64_t ldpart = second ? j1.ldpart : j0.ldpart;
+    const float* __restrict__ part = second ? j1.part : j0.part;
+    const int64_t idx = (int64_t)(blockIdx.x - (second ? j0.ctas : 0)) * kJoinThreads + threadIdx.x;
     if (idx >= join_threads(m, n, epi.single)) return;
     const int64_t plane = (int64_t)m * ldpart;
     float v[8] = {};
@@ -1163,6 +1206,7 @@ int64_t pad8(int64_t n) { return (n + 7) / 8 * 8; }
 struct GemmPlan {
     GemmShape g;
     int ctas, bn;
+    double us;   // modelled
 };
 
 // k-blocks an accumulator may sum: 256 deep for an fp32 result (2e-7 lost at most), 4096 deep
@@ -1171,40 +1215,63 @@ struct GemmPlan {
 int chunk_of(bool f32_out, int planes) { return planes == 3 ? 1 : f32_out ? 4 : 64; }
 
 // The tile and the splits of the contraction with the least modelled time, in microseconds as measured:
-// what a product costs but its steps, a 64-deep step, what a further tile of the same CTAs adds; for splits
+// what a product costs but its steps, a 64-deep step, what a further tile of the same CTAs adds (much with fp32
+// operands, whose accumulators change with every step: a tile's results are in the way of the next one's sums); for splits
 // the partial sums' traffic and the joining kernel.  (256 x 256 tiles step at 94 % of the tensor rate, 256 x 128
 // at 64 %, 128 x 64 at 13 %; the smaller tiles are for results that leave SMs idle otherwise: 4096x512x512 bf16
 // 8.0, 7.0 and 8.3 us, 512 nodes of 64x64 fp32 8.5, 7.4 and 6.7 us.)
+struct TileCost {
+    int ctas, bn;
+    double once, step, more, step3, more3;   // (3: of fp32 operands)
+};
+constexpr TileCost kTileCost[3] = {
+    {2, 256, 6.2, 0.264, 0.8, 1.57, 6.0}, {2, kBothBN, 5.2, 0.200, 0.6, 0.79, 4.0}, {1, 64, 4.0, 0.252, 0.5, 1.09, 1.5}};
+constexpr double kJoinUs = 4.0;
+double join_traffic_us(int M, int N, int splits) { return (double)M * N * (splits + 2) * 4 / 2.5e6; }
+
+// The time of a product's steps on `units` CTAs or pairs, and whether so many splits are sensible.
+bool cost_of(const TileCost& t, int M, int N, int K, int planes, int units, int splits, double* us) {
+    const int bm = 128 * t.ctas, kb = (K + kBK - 1) / kBK;
+    const int64_t n = (int64_t)((M + bm - 1) / bm) * ((N + t.bn - 1) / t.bn);
+    if (splits > 1 && (splits * n > units || kb / splits < (planes == 1 ? 4 : 2))) return false;
+    const int64_t waves = (n * splits + units - 1) / units;
+    *us = waves * ((kb + splits - 1) / splits) * (planes == 1 ? t.step : t.step3) + (waves - 1) * (planes == 1 ? t.more : t.more3);
+    return true;
+}
+
+GemmPlan make_plan(const TileCost& t, int M, int N, int K, int planes, bool f32_out, int splits, double us) {
+    const int bm = 128 * t.ctas, tm = (M + bm - 1) / bm, tn = (N + t.bn - 1) / t.bn;
+    GemmPlan p{};
+    GemmShape& g = p.g;
+    g = GemmShape{M, N, (K + kBK - 1) / kBK, planes, chunk_of(f32_out, planes), tm, tn, M % 64 == 0, N % 64 == 0, splits};
+    g.by_tiles = Divider::of(tm * tn);
+    g.by_group = Divider::of(kGroup * tn);
+    g.by_tail = Divider::of(tm % kGroup ? tm % kGroup : kGroup);
+    g.by_splits = Divider::of(splits);
+    p.ctas = t.ctas;
+    p.bn = t.bn;
+    p.us = us;
+    return p;
+}
+
+int next_splits(int sp) { return sp < 8 ? sp + 1 : sp + sp / 4; }
+
 GemmPlan plan_gemm(int M, int N, int K, int planes, bool f32_out) {
-    GemmPlan best{};
-    double best_us = 1e30;
-    const int sms = num_sms();
-    const int kb = (K + kBK - 1) / kBK;
-    const struct { int ctas, bn; double once, step, step3, more; } tiles[3] = {
-        {2, 256, 6.2, 0.264, 1.57, 0.8}, {2, 128, 5.2, 0.200, 0.79, 0.6}, {1, 64, 4.0, 0.252, 1.09, 0.5}};
-    for (const auto& t : tiles) {
-        const int bm = 128 * t.ctas, units = sms > t.ctas ? sms / t.ctas : 1;
-        const int tm = (M + bm - 1) / bm, tn = (N + t.bn - 1) / t.bn;
-        const int64_t n = (int64_t)tm * tn;
-        for (int sp = 1; sp <= 128; sp = sp < 8 ? sp + 1 : sp + sp / 4) {
-            if (sp > 1 && (sp * n > units || kb / sp < (planes == 1 ? 4 : 2))) break;
-            const int64_t waves = (n * sp + units - 1) / units;
-            double us = t.once + waves * ((kb + sp - 1) / sp) * (planes == 1 ? t.step : t.step3) + (waves - 1) * t.more;
-            if (sp > 1) us += 4.0 + (double)M * N * (sp + 2) * 4 / 2.5e6;
+    const TileCost* best = nullptr;
+    int splits = 1;
+    double best_us = 1e30, us;
+    for (const TileCost& t : kTileCost) {
+        const int units = num_sms() > t.ctas ? num_sms() / t.ctas : 1;
+        for (int sp = 1; sp <= 128 && cost_of(t, M, N, K, planes, units, sp, &us); sp = next_splits(sp)) {
+            us += t.once + (sp > 1 ? kJoinUs + join_traffic_us(M, N, sp) : 0.0);
             if (us < best_us) {
                 best_us = us;
-                best.g = GemmShape{M, N, kb, planes, chunk_of(f32_out, planes), tm, tn, M % 64 == 0, N % 64 == 0, sp};
-                best.ctas = t.ctas;
-                best.bn = t.bn;
+                best = &t;
+                splits = sp;
             }
         }
     }
-    GemmShape& g = best.g;
-    g.by_tiles = Divider::of(g.tiles_m * g.tiles_n);
-    g.by_group = Divider::of(kGroup * g.tiles_n);
-    g.by_tail = Divider::of(g.tiles_m % kGroup ? g.tiles_m % kGroup : kGroup);
-    g.by_splits = Divider::of(g.splits);
-    return best;
+    return make_plan(*best, M, N, K, planes, f32_out, splits, best_us);
 }
 
 bool one_chunk(const GemmPlan& p) { return (p.g.kblocks + p.g.splits - 1) / p.g.splits <= p.g.chunk; }
@@ -1219,11 +1286,58 @@ size_t part_floats(const GemmPlan& p, bool single, bool f32_out) {
     return leaves_sums(p, single, f32_out) ? (size_t)p.g.splits * p.g.M * pad8(p.g.N) : 0;
 }
 
-template <int CTAS, int BN, bool SUM, bool A_MN, bool B_MN>
-int launch_gemm(const GemmPlan& p, const CUtensorMap& ma, const CUtensorMap& mb, const Epi& e, float* part,
-                bool follows, cudaStream_t s) {
-    Epi epi = e;
-    CUtensorMap my{}, mp{};
+// The plans of a backward's products: each for a launch of its own, or, where that is modelled as faster, for one launch,
+// of which units_x pairs make dx.  A call for one of them uses the same plan, so that its result is the same.
+struct BwdPlan {
+    GemmPlan x, w;
+    int units_x = 0;   // 0: launches of their own
+};
+
+BwdPlan plan_bwd(int m, int k, int n, int planes, bool f32_out) {
+    BwdPlan p;
+    p.x = plan_gemm(m, k, n, planes, f32_out);
+    p.w = plan_gemm(k, n, m, planes, f32_out);
+    const TileCost& t = kTileCost[1];
+    const int units = num_sms() / 2;
+    double best_us = p.x.us + p.w.us;
+    GemmPlan x{}, w{};
+    constexpr int kShares = 12;
+    for (int i = 1; i < kShares && units >= kShares; ++i) {
+        const int ux = units * i / kShares;
+        int sx = 1, sw = 1;
+        double tx, tw, us;
+        const auto steps = [&](int M, int N, int K, int u, int& splits, double& best) {
+            cost_of(t, M, N, K, planes, u, 1, &best);
+            const int64_t n = (int64_t)((M + 255) / 256) * ((N + t.bn - 1) / t.bn);
+            const int most = (int)std::min<int64_t>({u / n, (K + kBK - 1) / kBK / (planes == 1 ? 4 : 2), 128});
+            if (most > 1 && cost_of(t, M, N, K, planes, u, most, &us) && (us += join_traffic_us(M, N, most)) < best) {
+                best = us;
+                splits = most;
+            }
+        };
+        steps(m, k, n, ux, sx, tx);
+        steps(k, n, m, units - ux, sw, tw);
+        const double total = t.once + (tx > tw ? tx : tw) + (sx > 1 || sw > 1 ? kJoinUs : 0.0);
+        if (total >= best_us) continue;
+        const GemmPlan bx = make_plan(t, m, k, n, planes, f32_out, sx, total), bw = make_plan(t, k, n, m, planes, f32_out, sw, total);
+        if (planes == 1 && !(one_chunk(bx) && one_chunk(bw))) continue;   // one kernel serves both
+        best_us = total;
+        x = bx;
+        w = bw;
+        p.units_x = ux;
+    }
+    if (p.units_x > 0) {
+        p.x = x;
+        p.w = w;
+    }
+    return p;
+}
+
+template <int CTAS, int BN, bool SUM>
+int make_job(GemmJob* job, const GemmPlan& p, const CUtensorMap& ma, const CUtensorMap& mb, const Epi& e, float* part) {
+    *job = GemmJob{ma, mb, {}, {}, p.g, e, part, pad8(p.g.N)};
+    Epi& epi = job->epi;
+    CUtensorMap &my = job->y, &mp = job->pre;
     // (whole 16 bytes of columns: a box that ends at an odd column of bf16 writes one column more)
     if (GemmCfg<CTAS, BN, SUM>::kBulk && !part && !epi.single && !epi.y_f32 && !epi.pre_f32 && p.g.N % 8 == 0) {
         const CUtensorMapDataType ty = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -1232,15 +1346,19 @@ int launch_gemm(const GemmPlan& p, const CUtensorMap& ma, const CUtensorMap& mb,
             return GT_ERR_CUDA;
         epi.bulk = true;
     }
+    return GT_OK;
+}
+
+// kern on `units` CTAs or pairs; `allowed`: its own set of devices.
+template <int CTAS, int BN, bool SUM, typename... P, typename... A>
+int launch_products(void (*kern)(P...), std::atomic<uint64_t>& allowed, int units, bool follows, cudaStream_t s,
+                    const A&... args) {
     using C = GemmCfg<CTAS, BN, SUM>;
-    auto kern = linear_gemm<CTAS, BN, SUM, A_MN, B_MN>;
-    static std::atomic<uint64_t> allowed;
     if (!allow_smem(allowed, reinterpret_cast<const void*>(kern), C::kSmem)) return GT_ERR_CUDA;
     int* status = device_status_ptr();
     if (!status) return GT_ERR_CUDA;
-    const int sms = num_sms(), units = sms > CTAS ? sms / CTAS : 1, items = p.g.items();
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(CTAS * (items < units ? items : units)));
+    cfg.gridDim = dim3((unsigned)(CTAS * units));
     cfg.blockDim = dim3(kGemmThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = s;
@@ -1254,8 +1372,19 @@ int launch_gemm(const GemmPlan& p, const CUtensorMap& ma, const CUtensorMap& mb,
     cfg.attrs = attr;
     cfg.numAttrs = CTAS;
     LaunchScope ls("linear_gemm", s);
-    return cudaLaunchKernelEx(&cfg, kern, ma, mb, my, mp, p.g, epi, part, pad8(p.g.N), status) == cudaSuccess ? check_launch()
-                                                                                                      : GT_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kern, args..., status) == cudaSuccess ? check_launch() : GT_ERR_CUDA;
+}
+
+template <int CTAS, int BN, bool SUM, bool A_MN, bool B_MN>
+int launch_gemm(const GemmPlan& p, const CUtensorMap& ma, const CUtensorMap& mb, const Epi& epi, float* part,
+                bool follows, cudaStream_t s) {
+    GemmJob job;
+    const int rc = make_job<CTAS, BN, SUM>(&job, p, ma, mb, epi, part);
+    if (rc != GT_OK) return rc;
+    static std::atomic<uint64_t> allowed;
+    const int sms = num_sms(), units = sms > CTAS ? sms / CTAS : 1, items = p.g.items();
+    return launch_products<CTAS, BN, SUM>(linear_gemm<CTAS, BN, SUM, A_MN, B_MN>, allowed, items < units ? items : units,
+                                          follows, s, job);
 }
 
 // The map of an operand of which a CTA takes `across` rows (columns, where mn) and 64 of the
@@ -1293,17 +1422,41 @@ int run_gemm(const GemmPlan& p, const Operand& a, const Operand& b, const Epi& e
     return launch_gemm<1, 64, true, A_MN, B_MN>(p, ma, mb, epi, out, follows, s);
 }
 
-// linear_join of p's sums (if it has left any) and the column sums (if any).
-int run_join(const GemmPlan* p, const float* part, const Epi& epi, const ColSum& cs, cudaStream_t s) {
-    const bool join = p && leaves_sums(*p, epi.single, epi.y_f32 || epi.pre_f32);
-    if (!join && !cs.out) return GT_OK;
-    const int M = join ? p->g.M : 0, N = join ? p->g.N : 0;
-    const int nj = (int)((join_threads(M, N, epi.single) + kJoinThreads - 1) / kJoinThreads);
-    const int nc = cs.out ? (cs.cols + 31) / 32 : 0;
-    LaunchScope ls("linear_join", s);
-    if (launch_overlapped(linear_join, dim3(nj + nc), dim3(kJoinThreads), 0, s, nj, M, N, join ? p->g.splits : 0, part,
-                          pad8(N), epi, cs) != cudaSuccess)
+template <bool SUM>
+int launch_both(const BwdPlan& p, const CUtensorMap (&mx)[2], const CUtensorMap (&mw)[2], const Epi& epi_x,
+                const Epi& epi_w, float* part_x, float* part_w, bool follows, cudaStream_t s) {
+    GemmJob x, w;
+    int rc = make_job<2, kBothBN, SUM>(&x, p.x, mx[0], mx[1], epi_x, part_x);
+    if (rc == GT_OK) rc = make_job<2, kBothBN, SUM>(&w, p.w, mw[0], mw[1], epi_w, part_w);
+    if (rc != GT_OK) return rc;
+    static std::atomic<uint64_t> allowed;
+    return launch_products<2, kBothBN, SUM>(linear_gemm_both<SUM>, allowed, num_sms() / 2, follows, s, x, w, p.units_x);
+}
+
+// da W^T and x^T da in one launch.
+int run_both(const BwdPlan& p, const Operand& da, const Operand& w, const Operand& x, const Epi& epi_x, const Epi& epi_w,
+             float* part_x, float* part_w, bool follows, cudaStream_t s) {
+    CUtensorMap mx[2], mw[2];
+    const GemmShape &gx = p.x.g, &gw = p.w.g;
+    if (!operand_map(&mx[0], da, false, gx.whole_a, 128) || !operand_map(&mx[1], w, false, gx.whole_b, kBothBN / 2) ||
+        !operand_map(&mw[0], x, true, gw.whole_a, 128) || !operand_map(&mw[1], da, true, gw.whole_b, kBothBN / 2))
         return GT_ERR_CUDA;
+    return gx.planes == 3 ? launch_both<true>(p, mx, mw, epi_x, epi_w, part_x, part_w, follows, s)
+                          : launch_both<false>(p, mx, mw, epi_x, epi_w, part_x, part_w, follows, s);
+}
+
+JoinJob join_job(const GemmPlan& p, const float* part, const Epi& epi) {
+    if (!leaves_sums(p, epi.single, epi.y_f32 || epi.pre_f32)) return JoinJob{};
+    const int M = p.g.M, N = p.g.N;
+    return JoinJob{(int)((join_threads(M, N, epi.single) + kJoinThreads - 1) / kJoinThreads), M, N, p.g.splits, part, pad8(N), epi};
+}
+
+// linear_join of the sums that two products (or one: JoinJob{}) have left, and of the column sums, if any.
+int run_joins(const JoinJob& j0, const JoinJob& j1, const ColSum& cs, cudaStream_t s) {
+    const int ctas = j0.ctas + j1.ctas + (cs.out ? (cs.cols + 31) / 32 : 0);
+    if (ctas == 0) return GT_OK;
+    LaunchScope ls("linear_join", s);
+    if (launch_overlapped(linear_join, dim3(ctas), dim3(kJoinThreads), 0, s, j0, j1, cs) != cudaSuccess) return GT_ERR_CUDA;
     return check_launch();
 }
 
@@ -1394,21 +1547,21 @@ size_t fwd_bufs(int dtype, bool y_f32, int m, int k, int n, bool pack_x, bool pa
 }
 
 // ... and of the backward, with da (where dy itself does not serve), the column sums' partial
-// rows, and one buffer for the splits' sums of both products in turn.
+// rows, and one buffer for the splits' sums of both products, in turn or at once.
 struct BwdBufs {
     bf16 *x, *w, *da;
     float *part, *cols;
 };
-size_t bwd_bufs(int dtype, int m, int k, int n, bool pack_x, bool pack_w, bool own_da, bool single_x, bool single_w,
-                void* ws, size_t bytes, BwdBufs* out) {
+size_t bwd_bufs(const BwdPlan& p, int dtype, int m, int k, int n, bool pack_x, bool pack_w, bool own_da, bool single_x,
+                bool single_w, void* ws, size_t bytes, BwdBufs* out) {
     Carve c(ws, bytes);
     BwdBufs b;
     b.x = pack_x ? c.take<bf16>(operand_elems(dtype, m, k)) : nullptr;
     b.w = pack_w ? c.take<bf16>(operand_elems(dtype, k, n)) : nullptr;
     b.da = own_da ? c.take<bf16>(operand_elems(dtype, m, n)) : nullptr;
-    const size_t px = part_floats(plan_gemm(m, k, n, planes_of(dtype), dtype == GT_F32), single_x, dtype == GT_F32);
-    const size_t pw = part_floats(plan_gemm(k, n, m, planes_of(dtype), dtype == GT_F32), single_w, dtype == GT_F32);
-    b.part = c.take<float>(px > pw ? px : pw);
+    const bool f32 = dtype == GT_F32;
+    const size_t px = part_floats(p.x, single_x, f32), pw = part_floats(p.w, single_w, f32);
+    b.part = c.take<float>(p.units_x > 0 ? px + pw : std::max(px, pw));
     b.cols = c.take<float>((size_t)prep_grid(m, n).gy * n);
     if (out) *out = b;
     return c.off;
@@ -1426,13 +1579,14 @@ int small_tiles(int rows, int cols) { return (rows + kSmT - 1) / kSmT * ((cols +
 // Whether a fp32 call goes to the fp32 pipes in one kernel: short contractions and few multiplications.
 // Measured against the split products (device time of the call): forward 512x64x64 5.7 against 6.8 us,
 // 16384x64x64 8.3 against 9.3, 6800x64x192 11.0 against 9.9 (but one launch for two, and no workspace), 6800x128x128
-// 13.2 against 9.5; backward 512x64x64 7.8 against 14.2, 512x64x192 15.5 against 16.2, 300x512x100 13.0 against
-// 20.5, 1024x512x128 17.9 against 18.4, 512x512x512 44 against 27.
+// 13.2 against 9.5; backward (one launch for three) 512x64x64 8.2 against 10.7, 100x256x64 7.2 against 10.4, 512x128x128
+// 11.5 against 12.3, 300x512x100 13.3 against 12.9, 1024x64x128 12.3 against 11.7, 512x64x192 15.6 against 12.3,
+// 1024x512x128 17.7 against 16.4.
 bool small_fwd(int dtype, int m, int k, int n) {
     return dtype == GT_F32 && k <= 64 && (int64_t)m * k * n <= (96 << 20);
 }
 bool small_bwd(int dtype, int m, int k, int n) {
-    return dtype == GT_F32 && m <= 1024 && n <= 192 && (int64_t)m * k * n <= (64 << 20);
+    return dtype == GT_F32 && m <= 1024 && n <= 128 && (int64_t)m * k * n <= (16 << 20);
 }
 
 bool ranges_ok(const void* p, int64_t ld, int cols) { return !p || ld >= cols; }
@@ -1457,7 +1611,7 @@ size_t gt_linear_bwd_workspace_size(int32_t dtype, int32_t ytype, int32_t m, int
     using namespace gt;
     if (check_linear(dtype, ytype, m, k, n, act) != GT_OK || small_bwd(dtype, m, k, n)) return 0;
     const bool pack = dtype == GT_F32 || !aligned;
-    return bwd_bufs(dtype, m, k, n, pack, pack, pack || act != GT_ACT_NONE || ytype != dtype, !aligned, !aligned, nullptr, 0,
+    return bwd_bufs(plan_bwd(m, k, n, planes_of(dtype), dtype == GT_F32), dtype, m, k, n, pack, pack, pack || act != GT_ACT_NONE || ytype != dtype, !aligned, !aligned, nullptr, 0,
                     nullptr);
 }
 
@@ -1493,7 +1647,7 @@ int gt_linear_fwd(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n,
     if ((rc = prep.launch(s)) != GT_OK) return rc;
     const GemmPlan plan = plan_gemm(m, n, k, planes_of(dtype), ytype == GT_F32);
     if ((rc = run_gemm<false, true>(plan, ox, ow, epi, bufs.part, prep.jobs.count > 0, s)) != GT_OK) return rc;
-    return run_join(&plan, bufs.part, epi, ColSum{}, s);
+    return run_joins(join_job(plan, bufs.part, epi), JoinJob{}, ColSum{}, s);
 }
 
 int gt_linear_bwd(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n, const void* dy, int64_t lddy,
@@ -1542,7 +1696,9 @@ int gt_linear_bwd(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n,
         return cudaLaunchKernelEx(&cfg, linear_small<true>, p) == cudaSuccess ? check_launch() : GT_ERR_CUDA;
     }
     BwdBufs bufs;
-    const size_t need = bwd_bufs(dtype, m, k, n, pack_x, pack_w, own_da, dx && epi_x.single, dw && epi_w.single, workspace,
+    const bool f32 = dtype == GT_F32;
+    const BwdPlan plan = plan_bwd(m, k, n, planes_of(dtype), f32);
+    const size_t need = bwd_bufs(plan, dtype, m, k, n, pack_x, pack_w, own_da, dx && epi_x.single, dw && epi_w.single, workspace,
                                  ws_bytes, &bufs);
     if (!workspace || !aligned16(workspace) || ws_bytes < need) return GT_ERR_WORKSPACE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1554,21 +1710,26 @@ int gt_linear_bwd(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n,
     if (dw) ox = prep.operand(m, k, x, ldx, bufs.x);
     if ((rc = prep.launch(s)) != GT_OK) return rc;
     bool follows = prep.jobs.count > 0;
-    const bool f32 = dtype == GT_F32;
     const ColSum cs{db ? bufs.cols : nullptr, db, prep_grid(m, n).gy, n};
+    if (dx && dw && plan.units_x > 0) {
+        float* part_w = bufs.part + part_floats(plan.x, epi_x.single, f32);
+        const JoinJob jx = join_job(plan.x, bufs.part, epi_x), jw = join_job(plan.w, part_w, epi_w);
+        if ((rc = run_both(plan, oda, ow, ox, epi_x, epi_w, jx.ctas ? bufs.part : nullptr, jw.ctas ? part_w : nullptr, follows,
+                           s)) != GT_OK)
+            return rc;
+        return run_joins(jx, jw, cs, s);
+    }
     if (dx) {
-        const GemmPlan plan = plan_gemm(m, k, n, planes_of(dtype), f32);
-        if ((rc = run_gemm<false, false>(plan, oda, ow, epi_x, bufs.part, follows, s)) != GT_OK) return rc;
+        if ((rc = run_gemm<false, false>(plan.x, oda, ow, epi_x, bufs.part, follows, s)) != GT_OK) return rc;
         follows = true;
         // the column sums go with the last join, or with this one if it is the last
-        if ((rc = run_join(&plan, bufs.part, epi_x, dw ? ColSum{} : cs, s)) != GT_OK) return rc;
+        if ((rc = run_joins(join_job(plan.x, bufs.part, epi_x), JoinJob{}, dw ? ColSum{} : cs, s)) != GT_OK) return rc;
     }
     if (dw) {
-        const GemmPlan plan = plan_gemm(k, n, m, planes_of(dtype), f32);
-        if ((rc = run_gemm<true, true>(plan, ox, oda, epi_w, bufs.part, follows, s)) != GT_OK) return rc;
-        return run_join(&plan, bufs.part, epi_w, cs, s);
+        if ((rc = run_gemm<true, true>(plan.w, ox, oda, epi_w, bufs.part, follows, s)) != GT_OK) return rc;
+        return run_joins(join_job(plan.w, bufs.part, epi_w), JoinJob{}, cs, s);
     }
-    return dx ? GT_OK : run_join(nullptr, nullptr, epi_x, cs, s);
+    return dx ? GT_OK : run_joins(JoinJob{}, JoinJob{}, cs, s);
 }
 
 }  // extern "C"
