@@ -893,7 +893,7 @@ linear_gemm_both(const __grid_constant__ GemmJob x, const __grid_constant__ Gemm
 // epilogue (of up to two products: the first j0.ctas CTAs, the next j1.ctas), and the column sums of the preparation's partial rows (the CTAs from there on,
 // 32 columns each, as col_sum in gt_norm.cu).  A thread takes 8 consecutive columns of a row, or
 // single: every 32nd of 256, so that a warp's accesses are consecutive elements (4099 x 321 x 1001, fp32 y and
-// residual: 58 us with those in the product kernel's epilogue, where a lane holds a row, 14 + 14 us so).
+// residual: 58 us with those in the product kernel's epilogue, where a lane holds a row, 13 + 9 us so).
 constexpr int kJoinThreads = 256;
 struct ColSum {
     const float* part;
@@ -905,12 +905,32 @@ __host__ __device__ __forceinline__ int64_t join_threads(int m, int n, bool sing
     return (int64_t)m * (single ? (n + 255) / 256 * 32 : (n + 7) / 8);
 }
 
-__device__ __forceinline__ float load_one(const void* p, int64_t at, bool f32) {
-    return f32 ? static_cast<const float*>(p)[at] : __bfloat162float(static_cast<const bf16*>(p)[at]);
+// Elements at, at + 32, ... (eight, of which those below `live` exist).
+__device__ __forceinline__ void load_every32(const void* p, int64_t at, bool f32, int live, float (&v)[8]) {
+    if (f32) {
+        const float* q = static_cast<const float*>(p) + at;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (32 * i < live) v[i] = q[32 * i];
+    } else {
+        const bf16* q = static_cast<const bf16*>(p) + at;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (32 * i < live) v[i] = __bfloat162float(q[32 * i]);
+    }
 }
-__device__ __forceinline__ void store_one(void* p, int64_t at, bool f32, float v) {
-    if (f32) static_cast<float*>(p)[at] = v;
-    else static_cast<bf16*>(p)[at] = __float2bfloat16_rn(v);
+__device__ __forceinline__ void store_every32(void* p, int64_t at, bool f32, int live, const float (&v)[8]) {
+    if (f32) {
+        float* q = static_cast<float*>(p) + at;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (32 * i < live) q[32 * i] = v[i];
+    } else {
+        bf16* q = static_cast<bf16*>(p) + at;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (32 * i < live) q[32 * i] = __float2bfloat16_rn(v[i]);
+    }
 }
 
 struct JoinJob {
@@ -959,26 +979,21 @@ linear_join(const __grid_constant__ JoinJob j0, const __grid_constant__ JoinJob 
         const int per_row = (n + 255) / 256 * 32;
         const int64_t row = idx / per_row;
         const int at = (int)(idx - row * per_row), col = at / 32 * 256 + at % 32;   // then col + 32, ...
+        // the residual and the bias are on their way while the sums are added
+        float r[8] = {}, b[8] = {};
+        if (epi.r) load_every32(epi.r, row * epi.ldr + col, epi.y_f32, n - col, r);
+        if (epi.bias) load_every32(epi.bias, col, true, n - col, b);
         for (int s = 0; s < splits; ++s)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 if (col + 32 * i < n) v[i] += __ldcg(part + s * plane + row * ldpart + col + 32 * i);
-        float r[8] = {};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (col + 32 * i >= n) continue;
-            if (epi.r) r[i] = load_one(epi.r, row * epi.ldr + col + 32 * i, epi.y_f32);
-            if (epi.bias) v[i] += __ldg(epi.bias + col + 32 * i);
-        }
-        if (epi.pre) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (col + 32 * i < n) store_one(epi.pre, row * epi.ldpre + col + 32 * i, epi.pre_f32, v[i]);
-        }
+        for (int i = 0; i < 8; ++i) v[i] += b[i];
+        if (epi.pre) store_every32(epi.pre, row * epi.ldpre + col, epi.pre_f32, n - col, v);
         if (epi.gelu_act) apply_gelu<8>(v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (col + 32 * i < n) store_one(epi.y, row * epi.ldy + col + 32 * i, epi.y_f32, v[i] + r[i]);
+        for (int i = 0; i < 8; ++i) v[i] += r[i];
+        store_every32(epi.y, row * epi.ldy + col, epi.y_f32, n - col, v);
         return;
     }
     const int per_row = (n + 7) / 8;
@@ -1278,7 +1293,7 @@ bool one_chunk(const GemmPlan& p) { return (p.g.kblocks + p.g.splits - 1) / p.g.
 
 // Whether the product kernel leaves its sums to linear_join: splits, and rows that can only be reached by single
 // elements, unless its staging tiles can (bf16: GemmCfg's kBulk).  For fp32 results the joining kernel, with its many
-// more warps, is the faster way (4099x321x1001 with a fp32 residual: 30 us, through staging tiles 35).
+// more warps, is the faster way (4099x321x1001 with a fp32 residual: 25 us, through staging tiles 35).
 bool leaves_sums(const GemmPlan& p, bool single, bool f32_out) {
     return p.g.splits > 1 || (single && (f32_out || p.ctas == 1 || !one_chunk(p)));
 }
