@@ -55,7 +55,7 @@ def _backward(gt, m, k, n, xt, yt, act, add=True, pad=0, offset=0):
 
 TYPES = [(B, B), (B, F), (F, F)]
 # one row, one feature, tiles exact and one past each of their edges, contractions that end inside a k-block
-# and short of one, fp32 sizes on both sides of the one-kernel path (k 64 forward, m 1024 or n 192 backward)
+# and short of one, fp32 sizes on both sides of the one-kernel path (k 64 forward, m 1024 or n 128 backward)
 SHAPES = [(1, 1, 1), (1, 64, 64), (2, 8, 200), (128, 64, 64), (129, 65, 65), (127, 63, 129), (64, 16, 256),
           (300, 200, 257), (257, 72, 512), (640, 136, 72), (130, 1000, 40), (17, 520, 1016), (65, 512, 33), (66, 64, 192), (67, 65, 193),
           (1024, 33, 65), (1025, 72, 40), (257, 600, 1025), (1, 777, 1500), (9, 140, 192)]
@@ -97,6 +97,40 @@ def test_larger_shapes(gt, m, k, n, xt, yt):
     for act in (0, 1):
         _forward(gt, m, k, n, xt, yt, act, res=act == 0)
         _backward(gt, m, k, n, xt, yt, act, add=act == 0)
+
+
+@pytest.mark.parametrize("m,k,n,xt,yt", [
+    (900, 40, 128, F, F), (900, 40, 129, F, F),       # both sides of the one-kernel path of the backward
+    (2000, 300, 600, B, B), (2000, 303, 601, B, B),   # both products in one launch, dW's contraction split
+    (2000, 303, 601, B, F), (2000, 303, 601, F, F),
+    (777, 1032, 520, B, B),                           # ... dx's contraction split too
+    (9000, 520, 264, F, F),                           # several tiles to a pair of SMs in both
+])
+def test_both_products_in_one_launch(gt, m, k, n, xt, yt):
+    for act in (0, 1):
+        _backward(gt, m, k, n, xt, yt, act, add=act == 1)
+    dy, x, w = _mat(m, n, yt, 1), _mat(m, k, xt, 2), _mat(k, n, xt, 3)
+    dx, dw, _ = gt.gt_linear_bwd(dy, x, w)
+    assert torch.equal(dx, gt.gt_linear_bwd(dy, x, w, need_dw=False)[0])
+    assert torch.equal(dw, gt.gt_linear_bwd(dy, x, w, need_dx=False, need_db=False)[1])
+
+
+@pytest.mark.parametrize("m,k,n", [(2500, 136, 801), (2499, 75, 1030), (33, 64, 2111)])
+@pytest.mark.parametrize("pad", [0, 3])
+def test_odd_bf16_rows(gt, m, k, n, pad):
+    """Rows that only single elements can reach, each array alone and all, with the residual in place."""
+    x, w, b, r = _mat(m, k, B, 1), _mat(k, n, B, 2, 0.1), _vec(n, 3), _mat(m, n, B, 4, pad=pad)
+    wide = [torch.full((m + 1, n + 8), 7.0, dtype=B, device="cuda") for _ in range(2)]
+    out, pre = (t[:m, 1:n + 1] for t in wide)
+    out.copy_(r)
+    gt.gt_linear_fwd(x, w, b, act=1, r=out, out=out, pre=pre)
+    gt.gt_check_device_status()
+    ref = R.linear_fwd(x, w, b, True, r, B)
+    R.check({"y": out, "pre": pre}, ref)
+    for t in wide:
+        assert (t[m] == 7).all() and (t[:, 0] == 7).all() and (t[:, n + 1:] == 7).all()
+    y, a = gt.gt_linear_fwd(x, w, b, act=1, r=r, save_pre=True)
+    assert torch.equal(y, out) and torch.equal(a, pre)
 
 
 def test_without_bias_residual_or_add(gt):

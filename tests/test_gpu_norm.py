@@ -76,6 +76,20 @@ def test_many_rows(gt):
         assert all(torch.equal(a, b) for a, b in zip((dx, dg, ds), again))
 
 
+@pytest.mark.parametrize("t", [F, B])
+@pytest.mark.parametrize("n,c", [(5000, 512), (3000, 1000), (1500, 2048), (1300, 2051), (700, 4096), (800, 8192), (400, 12000),
+                                 (350, 16384)])
+def test_many_wide_rows(gt, n, c, t):
+    """Several turns of every CTA in each layout, with the next rows fetched ahead and without."""
+    x, gain, shift, dy, dres = _rows(n, c, t, 1), _vec(c, 2, 0.1, 1.0), _vec(c, 3, 0.02), _rows(n, c, t, 4), _rows(n, c, t, 5)
+    y, mean, rstd = gt.gt_layer_norm_fwd(x, gain, shift)
+    R.check({"y": y, "mean": mean, "rstd": rstd}, R.ln_fwd(x, gain, shift, 1e-5, t))
+    want = R.ln_bwd(dy, x, gain, mean, rstd, dres)
+    dx, dg, ds = gt.gt_layer_norm_bwd(dy, x, gain, mean, rstd, dres=dres)
+    R.check({"dx": dx, "dgain": dg, "dshift": ds}, want)
+    assert torch.equal(dx, gt.gt_layer_norm_bwd(dy, x, gain, mean, rstd, dres=dres, dx=dres)[0])
+
+
 def test_constant_and_nonfinite_rows(gt):
     """A constant row has variance 0: y is the shift.  A NaN or an infinity stays in its own row of
     y and dx, and in dgain's columns."""
