@@ -1221,6 +1221,7 @@ int64_t pad8(int64_t n) { return (n + 7) / 8 * 8; }
 struct GemmPlan {
     GemmShape g;
     int ctas, bn;
+    bool sum;    // the kernel's SUM: several chunks to an item
     double us;   // modelled
 };
 
@@ -1265,6 +1266,7 @@ GemmPlan make_plan(const TileCost& t, int M, int N, int K, int planes, bool f32_
     g.by_splits = Divider::of(splits);
     p.ctas = t.ctas;
     p.bn = t.bn;
+    p.sum = t.ctas == 1 || (g.kblocks + splits - 1) / splits > g.chunk;
     p.us = us;
     return p;
 }
@@ -1289,14 +1291,10 @@ GemmPlan plan_gemm(int M, int N, int K, int planes, bool f32_out) {
     return make_plan(*best, M, N, K, planes, f32_out, splits, best_us);
 }
 
-bool one_chunk(const GemmPlan& p) { return (p.g.kblocks + p.g.splits - 1) / p.g.splits <= p.g.chunk; }
-
 // Whether the product kernel leaves its sums to linear_join: splits, and rows that can only be reached by single
 // elements, unless its staging tiles can (bf16: GemmCfg's kBulk).  For fp32 results the joining kernel, with its many
 // more warps, is the faster way (4099x321x1001 with a fp32 residual: 25 us, through staging tiles 35).
-bool leaves_sums(const GemmPlan& p, bool single, bool f32_out) {
-    return p.g.splits > 1 || (single && (f32_out || p.ctas == 1 || !one_chunk(p)));
-}
+bool leaves_sums(const GemmPlan& p, bool single, bool f32_out) { return p.g.splits > 1 || (single && (f32_out || p.sum)); }
 size_t part_floats(const GemmPlan& p, bool single, bool f32_out) {
     return leaves_sums(p, single, f32_out) ? (size_t)p.g.splits * p.g.M * pad8(p.g.N) : 0;
 }
@@ -1334,11 +1332,10 @@ BwdPlan plan_bwd(int m, int k, int n, int planes, bool f32_out) {
         steps(k, n, m, units - ux, sw, tw);
         const double total = t.once + (tx > tw ? tx : tw) + (sx > 1 || sw > 1 ? kJoinUs : 0.0);
         if (total >= best_us) continue;
-        const GemmPlan bx = make_plan(t, m, k, n, planes, f32_out, sx, total), bw = make_plan(t, k, n, m, planes, f32_out, sw, total);
-        if (planes == 1 && !(one_chunk(bx) && one_chunk(bw))) continue;   // one kernel serves both
         best_us = total;
-        x = bx;
-        w = bw;
+        x = make_plan(t, m, k, n, planes, f32_out, sx, total);
+        w = make_plan(t, k, n, m, planes, f32_out, sw, total);
+        x.sum = w.sum = x.sum || w.sum;   // one kernel serves both
         p.units_x = ux;
     }
     if (p.units_x > 0) {
@@ -1427,12 +1424,11 @@ int run_gemm(const GemmPlan& p, const Operand& a, const Operand& b, const Epi& e
     if (!operand_map(&ma, a, A_MN, p.g.whole_a, 128) || !operand_map(&mb, b, B_MN, p.g.whole_b, p.bn / p.ctas))
         return GT_ERR_CUDA;
     float* out = leaves_sums(p, epi.single, epi.y_f32 || epi.pre_f32) ? part : nullptr;
-    const bool whole = one_chunk(p);
     if (p.bn == 256)
-        return whole ? launch_gemm<2, 256, false, A_MN, B_MN>(p, ma, mb, epi, out, follows, s)
+        return !p.sum ? launch_gemm<2, 256, false, A_MN, B_MN>(p, ma, mb, epi, out, follows, s)
                          : launch_gemm<2, 256, true, A_MN, B_MN>(p, ma, mb, epi, out, follows, s);
     if (p.bn == 128)
-        return whole ? launch_gemm<2, 128, false, A_MN, B_MN>(p, ma, mb, epi, out, follows, s)
+        return !p.sum ? launch_gemm<2, 128, false, A_MN, B_MN>(p, ma, mb, epi, out, follows, s)
                          : launch_gemm<2, 128, true, A_MN, B_MN>(p, ma, mb, epi, out, follows, s);
     return launch_gemm<1, 64, true, A_MN, B_MN>(p, ma, mb, epi, out, follows, s);
 }
@@ -1456,7 +1452,7 @@ int run_both(const BwdPlan& p, const Operand& da, const Operand& w, const Operan
     if (!operand_map(&mx[0], da, false, gx.whole_a, 128) || !operand_map(&mx[1], w, false, gx.whole_b, kBothBN / 2) ||
         !operand_map(&mw[0], x, true, gw.whole_a, 128) || !operand_map(&mw[1], da, true, gw.whole_b, kBothBN / 2))
         return GT_ERR_CUDA;
-    return gx.planes == 3 ? launch_both<true>(p, mx, mw, epi_x, epi_w, part_x, part_w, follows, s)
+    return p.x.sum ? launch_both<true>(p, mx, mw, epi_x, epi_w, part_x, part_w, follows, s)
                           : launch_both<false>(p, mx, mw, epi_x, epi_w, part_x, part_w, follows, s);
 }
 
