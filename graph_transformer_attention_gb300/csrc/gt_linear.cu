@@ -890,8 +890,8 @@ linear_gemm_both(const __grid_constant__ GemmJob x, const __grid_constant__ Gemm
 
 // The end of a call in one launch: the sums that the product kernel left (of the contraction's splits,
 // added in a fixed order, and any whose rows can only be reached by single elements) through the
-// epilogue (of up to two products: the first j0.ctas CTAs, the next j1.ctas), and the column sums of the preparation's partial rows (the CTAs from there on,
-// 32 columns each, as col_sum in gt_norm.cu).  A thread takes 8 consecutive columns of a row, or
+// epilogue (of up to two products: the first j0.ctas CTAs, the next j1.ctas), and the column sums of the
+// preparation's partial rows (the CTAs from there on, 32 columns each, as col_sum in gt_norm.cu).  A thread takes 8 consecutive columns of a row, or
 // single: every 32nd of 256, so that a warp's accesses are consecutive elements (4099 x 321 x 1001, fp32 y and
 // residual: 58 us with those in the product kernel's epilogue, where a lane holds a row, 13 + 9 us so).
 constexpr int kJoinThreads = 256;
@@ -1622,8 +1622,8 @@ size_t gt_linear_bwd_workspace_size(int32_t dtype, int32_t ytype, int32_t m, int
     using namespace gt;
     if (check_linear(dtype, ytype, m, k, n, act) != GT_OK || small_bwd(dtype, m, k, n)) return 0;
     const bool pack = dtype == GT_F32 || !aligned;
-    return bwd_bufs(plan_bwd(m, k, n, planes_of(dtype), dtype == GT_F32), dtype, m, k, n, pack, pack, pack || act != GT_ACT_NONE || ytype != dtype, !aligned, !aligned, nullptr, 0,
-                    nullptr);
+    return bwd_bufs(plan_bwd(m, k, n, planes_of(dtype), dtype == GT_F32), dtype, m, k, n, pack, pack,
+                    pack || act != GT_ACT_NONE || ytype != dtype, !aligned, !aligned, nullptr, 0, nullptr);
 }
 
 int gt_linear_fwd(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n, const void* x, int64_t ldx,

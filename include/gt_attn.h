@@ -437,7 +437,7 @@ typedef enum { GT_ACT_NONE = 0, GT_ACT_GELU = 1 } gt_act;
  *   With dtype GT_BF16 da is rounded to bf16 for the two products (db is summed before
  *   that rounding).
  *   workspace: at least gt_linear_bwd_workspace_size bytes (`aligned` as above; else
- *   with copies of dy, x and W and an fp32 result, [m][k] or [k][n]).
+ *   with copies of dy, x and W and fp32 results, [m][k] and [k][n]).
  * Errors as the forward's, plus GT_ERR_INVALID_ARG when dx, dw and db are all NULL,
  * pre and act disagree, or add comes without dx.
  */
