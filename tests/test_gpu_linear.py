@@ -133,6 +133,30 @@ def test_odd_bf16_rows(gt, m, k, n, pad):
     assert torch.equal(y, out) and torch.equal(a, pre)
 
 
+@pytest.mark.parametrize("xt,k,n", [(B, 24, 2200), (F, 2200, 24), (B, 2200, 24)])
+def test_offsets_past_32_bits(gt, xt, k, n):
+    """A million rows, whose wide matrix has more than 2^31 elements: its last rows, and sums over all of them."""
+    m, tail = 1 << 20, 300
+    x, w, dy = _mat(m, k, xt, 1), _mat(k, n, xt, 2, 0.1), _mat(m, n, xt, 3)
+    y, pre = gt.gt_linear_fwd(x, w, act=1, save_pre=True)
+    dx = gt.gt_linear_bwd(dy, x, w, pre=pre, act=1, need_dw=False, need_db=False)[0]
+    gt.gt_check_device_status()
+    ref = R.linear_fwd(x[-tail:], w, None, True, None, xt)
+    R.check({"y": y[-tail:], "pre": pre[-tail:]}, ref)
+    R.check({"dx": dx[-tail:]}, {"dx": R.linear_bwd(dy[-tail:], x[-tail:], w, pre[-tail:], True, None)["dx"]})
+    # The sums over rows, of positive terms: an accumulator drops at most 2^-23 of itself in each of 256 steps (six times 4
+    # for fp32), m / 64 chunks and a thousand partial sums are added with 2^-24 each.
+    del y, pre, dx
+    x.abs_(), dy.abs_()
+    _, dw, db = gt.gt_linear_bwd(dy, x, w, need_dx=False)
+    rows = range(0, m, 1 << 16)
+    ref = {"dw": sum(x[i:i + (1 << 16)].double().T @ dy[i:i + (1 << 16)].double() for i in rows),
+           "db": sum(dy[i:i + (1 << 16)].double().sum(0) for i in rows)}
+    for got, want in ((dw, ref["dw"]), (db, ref["db"])):
+        tol = (R.half_step(got.dtype) + 256 * 2 * R.U32 + (m / 64 + 1024) * R.U32) * want
+        assert ((got.double() - want).abs() <= tol).all()
+
+
 def test_without_bias_residual_or_add(gt):
     for xt, yt in TYPES:
         _forward(gt, 70, 90, 110, xt, yt, 1, bias=False, res=False)

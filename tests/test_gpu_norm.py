@@ -90,6 +90,18 @@ def test_many_wide_rows(gt, n, c, t):
     assert torch.equal(dx, gt.gt_layer_norm_bwd(dy, x, gain, mean, rstd, dres=dres, dx=dres)[0])
 
 
+@pytest.mark.parametrize("t", [F, B])
+def test_offsets_past_32_bits(gt, t):
+    """More than 2^31 elements: the last rows equal those of a call for them alone."""
+    n, c, tail = 270000, 8008, 64
+    x, gain, shift = _rows(n, c, t, 1), _vec(c, 2, 0.1, 1.0), _vec(c, 3, 0.02)
+    y, mean, rstd = gt.gt_layer_norm_fwd(x, gain, shift)
+    R.check({"y": y[-tail:], "mean": mean[-tail:], "rstd": rstd[-tail:]}, R.ln_fwd(x[-tail:], gain, shift, 1e-5, t))
+    one = gt.gt_layer_norm_bwd(y, x, gain, mean, rstd)[0]
+    part = gt.gt_layer_norm_bwd(y[-tail:], x[-tail:], gain, mean[-tail:], rstd[-tail:])[0]
+    assert torch.equal(one[-tail:], part)
+
+
 def test_constant_and_nonfinite_rows(gt):
     """A constant row has variance 0: y is the shift.  A NaN or an infinity stays in its own row of
     y and dx, and in dgain's columns."""
