@@ -589,6 +589,7 @@ struct GemmJob {
     Epi epi;
     float* part;
     int64_t ldpart;
+    int part_access;   // row_access() of part: a workspace need only be 16-byte aligned
 };
 
 // The job's items first, first + stride, ... by one CTA, or a pair.
@@ -850,7 +851,8 @@ __device__ __forceinline__ void gemm_job(const GemmJob& job, const int first, co
                                                  smem_u32(stg));
                             }
                         } else if (row < g.M && live > 0) {
-                            if (part) put_row<CW>(part, ((int64_t)w.s * g.M + row) * ldpart + col, true, f, (live + 7) & ~7, 2);
+                            if (part) put_row<CW>(part, ((int64_t)w.s * g.M + row) * ldpart + col, true, f, (live + 7) & ~7,
+                                                  job.part_access);
                             else epilogue<CW>(epi, row, col, live, f, bias + 4 * c * CW);
                         }
                         __syncwarp();
@@ -1347,7 +1349,7 @@ BwdPlan plan_bwd(int m, int k, int n, int planes, bool f32_out) {
 
 template <int CTAS, int BN, bool SUM>
 int make_job(GemmJob* job, const GemmPlan& p, const CUtensorMap& ma, const CUtensorMap& mb, const Epi& e, float* part) {
-    *job = GemmJob{ma, mb, {}, {}, p.g, e, part, pad8(p.g.N)};
+    *job = GemmJob{ma, mb, {}, {}, p.g, e, part, pad8(p.g.N), row_access(part, pad8(p.g.N), 4)};
     Epi& epi = job->epi;
     CUtensorMap &my = job->y, &mp = job->pre;
     // (whole 16 bytes of columns: a box that ends at an odd column of bf16 writes one column more)

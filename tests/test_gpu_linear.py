@@ -493,3 +493,33 @@ def test_binding_refusals(gt):
                  lambda: gt.gt_layer_norm_fwd(x[:0], b[:8].contiguous(), b[:8].contiguous())):
         with pytest.raises(gt.GtError):
             call()
+
+
+@pytest.mark.parametrize("m,k,n,xt,yt", [
+    (2, 4000, 24, B, B), (2, 4000, 24, F, F),         # the forward's contraction split
+    (1100, 520, 89, B, F), (300, 200, 257, F, F),     # fp32 sums of rows that only single elements can reach
+    (40, 24, 4000, F, F), (40, 24, 4000, B, B),       # dx's contraction split
+    (4100, 64, 64, B, B), (4100, 40, 72, F, F),       # dW's, in a launch of its own or with dx
+    (2000, 303, 601, B, F), (2000, 303, 601, F, F),   # both products in one launch, both leave sums
+])
+def test_workspace_of_any_16_byte_alignment(gt, m, k, n, xt, yt):
+    """A workspace 16 bytes past a 32-byte boundary serves as any other: the same results, and nothing outside it written."""
+    x, w, dy, b = _mat(m, k, xt, 1), _mat(k, n, xt, 2, 1 / math.sqrt(k)), _mat(m, n, yt, 3), _vec(n, 4)
+
+    def room(need):
+        buf = torch.full((need + 64,), 7, dtype=torch.uint8, device="cuda")
+        assert buf.data_ptr() % 32 == 0
+        return buf, buf[16:16 + need]
+
+    code = gt.GT_F32 if xt == F else gt.GT_BF16
+    buf, ws = room(gt.gt_linear_fwd_workspace_size(code, m, k, n, aligned=False))
+    got = gt.gt_linear_fwd(x, w, b, out_dtype=yt, workspace=ws)[0]
+    assert torch.equal(got, gt.gt_linear_fwd(x, w, b, out_dtype=yt)[0])
+    assert (buf[:16] == 7).all() and (buf[16 + ws.numel():] == 7).all()
+    buf, ws = room(gt.gt_linear_bwd_workspace_size(code, gt.GT_F32 if yt == F else gt.GT_BF16, m, k, n, aligned=False))
+    for parts in ({}, {"need_dw": False}, {"need_dx": False}):
+        got = gt.gt_linear_bwd(dy, x, w, workspace=ws, **parts)
+        for a, c in zip(got, gt.gt_linear_bwd(dy, x, w, **parts)):
+            assert (a is None and c is None) or torch.equal(a, c)
+    gt.gt_check_device_status()
+    assert (buf[:16] == 7).all() and (buf[16 + ws.numel():] == 7).all()

@@ -177,3 +177,15 @@ def test_streams_and_graph(gt):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(held, both()))
+
+
+@pytest.mark.parametrize("n,c,t", [(300, 64, F), (41, 1000, B), (20, 8192, F)])
+def test_workspace_of_any_16_byte_alignment(gt, n, c, t):
+    """A workspace 16 bytes past a 32-byte boundary serves as any other."""
+    x, gain, shift, dy = _rows(n, c, t, 1), _vec(c, 2, 0.1, 1.0), _vec(c, 3, 0.02), _rows(n, c, t, 4)
+    _, mean, rstd = gt.gt_layer_norm_fwd(x, gain, shift)
+    need = gt.gt_layer_norm_workspace_size(n, c)
+    buf = torch.full((need + 64,), 7, dtype=torch.uint8, device="cuda")
+    got = gt.gt_layer_norm_bwd(dy, x, gain, mean, rstd, workspace=buf[16:16 + need])
+    assert all(torch.equal(a, b) for a, b in zip(got, gt.gt_layer_norm_bwd(dy, x, gain, mean, rstd)))
+    assert (buf[:16] == 7).all() and (buf[16 + need:] == 7).all()
