@@ -299,7 +299,7 @@ __device__ __forceinline__ void put_row(void* base, int64_t at, bool f32, const 
     }
 }
 
-// v[i] += base[at + i]
+// v[i] += base[at + i], which may be the output itself
 template <int CW>
 __device__ __forceinline__ void add_row(const void* base, int64_t at, bool f32, float (&v)[CW], int live, int acc) {
     if (f32) {
@@ -317,7 +317,7 @@ __device__ __forceinline__ void add_row(const void* base, int64_t at, bool f32, 
 #pragma unroll
         for (int g = 0; g < CW / 8; ++g) {
             float t[8];
-            unpack8(load8(p + 8 * g, live - 8 * g, acc), t);
+            unpack8(load8<Mem::kOutput>(p + 8 * g, live - 8 * g, acc), t);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[8 * g + i] += t[i];
         }
@@ -339,7 +339,7 @@ __device__ __forceinline__ void add_row(const void* base, int64_t at, bool f32, 
 #pragma unroll
         for (int g = 0; g < CW / 8; ++g) {
             float t[8];
-            unpack8(load8(p + 8 * g, live - 8 * g, acc), t);
+            unpack8(load8<Mem::kOutput>(p + 8 * g, live - 8 * g, acc), t);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[8 * g + i] += t[i];
         }

@@ -192,8 +192,7 @@ template <typename TX, typename TY, typename C, bool WHOLE>
 __global__ void __launch_bounds__(C::TH, C::OCC)
 norm_bwd(int64_t n, int c, const TY* __restrict__ dy, int64_t lddy, const TX* __restrict__ x, int64_t ldx,
          const float* __restrict__ gain, const float* __restrict__ mean, const float* __restrict__ rstd,
-         const TX* __restrict__ dres, int64_t ldr, TX* __restrict__ dx, int64_t lddx, float* __restrict__ part,
-         int vec) {
+         const TX* dres, int64_t ldr, TX* dx, int64_t lddx, float* __restrict__ part, int vec) {   // dres may be dx
     constexpr int TPR = C::TPR, NV = C::NV, R = C::R, RG = C::RG, TH = C::TH;
     __shared__ float2 red[C::RED];
     RowSum<TPR, R, TH> rowsum{red, 0};
@@ -222,7 +221,7 @@ norm_bwd(int64_t n, int c, const TY* __restrict__ dy, int64_t lddy, const TX* __
                 const int col = (i * TPR + t) * 8, live = row < n ? c - col : 0;
                 in.x[k][i] = load8_row<WHOLE>(x + ra * ldx + col, live, vec);
                 in.dy[k][i] = load8_row<WHOLE>(dy + ra * lddy + col, live, vec);
-                if (dres) in.res[k][i] = load8_row<WHOLE>(dres + ra * ldr + col, live, vec);
+                if (dres) in.res[k][i] = load8_row<WHOLE, Mem::kOutput>(dres + ra * ldr + col, live, vec);
             }
             // a row past the end is all zeros, and so are its xh and its sums
             in.mu[k] = row < n ? mean[ra] : 0.f;

@@ -29,33 +29,59 @@ template <typename T> struct Raw8;
 template <> struct Raw8<__nv_bfloat16> { uint4 a; };
 template <> struct Raw8<float> { uint4 a, b; };
 
+// 32 bytes at once (32-byte aligned).
+__device__ __forceinline__ void ldg32(const void* p, uint32_t (&w)[8]) {
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p)
+                 : "memory");
+}
+
+// Whether a kernel only reads an array, so that its loads may go through the read-only path, or may also write it: a
+// residual that the caller lets be the output itself.
+enum class Mem { kReadOnly, kOutput };
+
+template <Mem MEM, typename T>
+__device__ __forceinline__ T load1(const T* p) {
+    if constexpr (MEM == Mem::kReadOnly) return __ldg(p);
+    else return *p;
+}
+
 // Elements p[0 .. 7], those at or past `live` as zeros; acc: the row's row_access().
-template <typename T>
+template <Mem MEM = Mem::kReadOnly, typename T>
 __device__ __forceinline__ Raw8<T> load8(const T* p, int live, int acc) {
     Raw8<T> r;
     if (acc > 0 && live >= 8) {
         const uint4* s = reinterpret_cast<const uint4*>(p);
         if constexpr (sizeof(T) == 2) {
-            r.a = __ldg(s);
+            r.a = load1<MEM>(s);
         } else if (acc == 2) {   // one access of 32 bytes: whole sectors
-            asm("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                : "=r"(r.a.x), "=r"(r.a.y), "=r"(r.a.z), "=r"(r.a.w), "=r"(r.b.x), "=r"(r.b.y), "=r"(r.b.z), "=r"(r.b.w)
-                : "l"(p));
+            if constexpr (MEM == Mem::kReadOnly) {
+                asm("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                    : "=r"(r.a.x), "=r"(r.a.y), "=r"(r.a.z), "=r"(r.a.w), "=r"(r.b.x), "=r"(r.b.y), "=r"(r.b.z), "=r"(r.b.w)
+                    : "l"(p));
+            } else {
+                uint32_t w[8];
+                ldg32(p, w);
+                r.a = make_uint4(w[0], w[1], w[2], w[3]);
+                r.b = make_uint4(w[4], w[5], w[6], w[7]);
+            }
         } else {
-            r.a = __ldg(s);
-            r.b = __ldg(s + 1);
+            r.a = load1<MEM>(s);
+            r.b = load1<MEM>(s + 1);
         }
     } else if constexpr (sizeof(T) == 4) {
         uint32_t w[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = i < live ? __float_as_uint(__ldg(reinterpret_cast<const float*>(p) + i)) : 0u;
+        for (int i = 0; i < 8; ++i)
+            w[i] = i < live ? __float_as_uint(load1<MEM>(reinterpret_cast<const float*>(p) + i)) : 0u;
         r.a = make_uint4(w[0], w[1], w[2], w[3]);
         r.b = make_uint4(w[4], w[5], w[6], w[7]);
     } else {
         const unsigned short* s = reinterpret_cast<const unsigned short*>(p);
         uint32_t w[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = i < live ? (uint32_t)__ldg(s + i) : 0u;
+        for (int i = 0; i < 8; ++i) w[i] = i < live ? (uint32_t)load1<MEM>(s + i) : 0u;
         r.a = make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16));
     }
     return r;
@@ -70,15 +96,15 @@ __device__ __forceinline__ Raw8<float> load8_cg(const float* p) {
 }
 
 // load8 where WHOLE says that rows are whole eights in 16-byte accesses: `live` is then 8 or more, or nothing.
-template <bool WHOLE, typename T>
+template <bool WHOLE, Mem MEM = Mem::kReadOnly, typename T>
 __device__ __forceinline__ Raw8<T> load8_row(const T* p, int live, int acc) {
     if constexpr (!WHOLE) {
-        return load8(p, live, acc);
+        return load8<MEM>(p, live, acc);
     } else {
         Raw8<T> r;
         r.a = make_uint4(0, 0, 0, 0);
         if constexpr (sizeof(T) == 4) r.b = r.a;
-        if (live > 0) r = load8(p, 8, sizeof(T) == 2 ? 1 : acc == 2 ? 2 : 1);
+        if (live > 0) r = load8<MEM>(p, 8, sizeof(T) == 2 ? 1 : acc == 2 ? 2 : 1);
         return r;
     }
 }
@@ -112,14 +138,7 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
     return r;
 }
 
-// 32 bytes at once (32-byte aligned).
-__device__ __forceinline__ void ldg32(const void* p, uint32_t (&w)[8]) {
-    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-                 : "l"(p)
-                 : "memory");
-}
-
+// (32-byte aligned)
 __device__ __forceinline__ void stg32(void* p, const uint32_t (&w)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
                  "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])

@@ -523,3 +523,24 @@ def test_workspace_of_any_16_byte_alignment(gt, m, k, n, xt, yt):
             assert (a is None and c is None) or torch.equal(a, c)
     gt.gt_check_device_status()
     assert (buf[:16] == 7).all() and (buf[16 + ws.numel():] == 7).all()
+
+
+@pytest.mark.parametrize("pad,offset", [(0, 0), (16, 0), (4, 4), (8, 8), (5, 0), (0, 1)])
+@pytest.mark.parametrize("xt,yt", TYPES)
+@pytest.mark.parametrize("m,k,n", [(1100, 512, 320), (90, 60, 72), (3, 2000, 304), (2000, 304, 600)])
+def test_residual_in_place_at_every_access(gt, m, k, n, xt, yt, pad, offset):
+    """r and y, and dx_add and dx, one buffer each, in rows of 32-byte, 16-byte and single-element accesses."""
+    x, w, b, dy = _mat(m, k, xt, 1), _mat(k, n, xt, 2, 1 / math.sqrt(k)), _vec(n, 3), _mat(m, n, yt, 4)
+    buf, other = _mat(m, n, yt, 5, pad=pad, offset=offset), _mat(m, n, yt, 6, pad=pad, offset=offset)
+    r = buf.clone()
+    want = gt.gt_linear_fwd(x, w, b, act=1, r=r, out=other)[0]
+    got = gt.gt_linear_fwd(x, w, b, act=1, r=buf, out=buf)[0]
+    assert got is buf and torch.equal(got, want)
+    R.check({"y": got}, R.linear_fwd(x, w, b, True, r, yt))
+    buf, other = _mat(m, k, xt, 7, pad=pad, offset=offset), _mat(m, k, xt, 8, pad=pad, offset=offset)
+    add = buf.clone()
+    want = gt.gt_linear_bwd(dy, x, w, dx_add=add, dx=other)
+    got = gt.gt_linear_bwd(dy, x, w, dx_add=buf, dx=buf)
+    assert got[0] is buf and all(torch.equal(a, c) for a, c in zip(got, want))
+    R.check({"dx": got[0]}, R.linear_bwd(dy, x, w, None, False, add))
+    gt.gt_check_device_status()

@@ -189,3 +189,17 @@ def test_workspace_of_any_16_byte_alignment(gt, n, c, t):
     got = gt.gt_layer_norm_bwd(dy, x, gain, mean, rstd, workspace=buf[16:16 + need])
     assert all(torch.equal(a, b) for a, b in zip(got, gt.gt_layer_norm_bwd(dy, x, gain, mean, rstd)))
     assert (buf[:16] == 7).all() and (buf[16 + need:] == 7).all()
+
+
+@pytest.mark.parametrize("pad,offset", [(0, 0), (16, 0), (4, 4), (8, 8), (5, 0), (0, 1)])
+@pytest.mark.parametrize("n,c,t", [(700, 64, F), (700, 64, B), (6000, 512, B), (2500, 1000, F), (900, 4096, B), (350, 8192, F)])
+def test_residual_gradient_in_place_at_every_access(gt, n, c, t, pad, offset):
+    """dres and dx one buffer, in rows of 32-byte, 16-byte and single-element accesses, several turns of a CTA."""
+    x, gain, shift, dy = _rows(n, c, t, 1), _vec(c, 2, 0.1, 1.0), _vec(c, 3, 0.02), _rows(n, c, t, 4)
+    _, mean, rstd = gt.gt_layer_norm_fwd(x, gain, shift)
+    buf = _rows(n, c, t, 5, pad, offset)
+    kept = buf.clone()
+    want = gt.gt_layer_norm_bwd(dy, x, gain, mean, rstd, dres=kept, dx=_rows(n, c, t, 6, pad, offset))
+    got = gt.gt_layer_norm_bwd(dy, x, gain, mean, rstd, dres=buf, dx=buf)
+    assert got[0] is buf and all(torch.equal(a, b) for a, b in zip(got, want))
+    R.check({"dx": buf}, R.ln_bwd(dy, x, gain, mean, rstd, kept))
