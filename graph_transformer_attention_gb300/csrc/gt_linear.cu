@@ -43,9 +43,15 @@ using bf16 = __nv_bfloat16;
 
 // ------------------------------------------------------------------------ GELU
 
-// For two values: e = exp(-a^2 / 2) and u = 1/2 - (the normal CDF at -|a|).  That CDF is half of
-// erfc(|a| / sqrt 2) = t (a1 + a2 t + ... + a5 t^4) exp(-a^2 / 2), t = 1 / (1 + p |a| / sqrt 2),
-// Abramowitz and Stegun 7.1.26: at most 1.5e-7 off, the size of an fp32 rounding of the CDF.
+// For two values: e = exp(-a^2 / 2) and the tail of the normal CDF,
+//   Phi(-|a|) = e h(|a|),  h(x) = erfcx(x / sqrt 2) / 2 = t (c1 + c2 t + ... + c7 t^6),  t = 1 / (r + k x),
+// where h falls smoothly from 1/2, so that the tail keeps its relative accuracy: for Phi(a) = 1/2 - sign(a) (1/2 - tail)
+// all digits of a GELU below -5 would cancel.  k = sqrt(log2(e) / 2), so that e = 2^-(k a)^2 shares the product, and r = 4 k.
+// The c are this code's own fit: a linear programme for the least largest error on 0 <= x <= 13.5 (beyond, e is 0),
+// weighted so that the tail times max(1, x) is 0.5e-8 off at most, or 5e-5 of itself where that is less.
+// In fp32 GELU and slope are within 1.1e-7 and 1.9e-7 of the exact ones for |a| <= 2, and GELU within 6e-5 of itself down to
+// a = -13.  Abramowitz and Stegun 7.1.26 with that difference (2.3e-7 and 2.6e-7, 2.6e-7 at -4 .. -2, 5 % of itself at -5) has two
+// terms less and is the faster by 1 to 2 % (32768x1024x4096 bf16: forward with pre 187 against 190 us, backward 444 against 452).
 __device__ __forceinline__ float2 f2(float x) { return make_float2(x, x); }
 
 __device__ __forceinline__ float rcp(float x) {
@@ -58,8 +64,9 @@ __device__ __forceinline__ float rcp(float x) {
 // use than keep it, which doubles the instructions of the packed arithmetic; behind an empty asm
 // statement it has to keep them.
 struct GaussK {
-    float2 p, one, q, a5, a4, a3, a2, a1, half;
+    float2 c7, c6, c5, c4, c3, c2, c1;   // (the c negated)
 };
+constexpr float kGaussK = 0.849321783f, kGaussR = 3.39728713f;
 
 __device__ __forceinline__ float2 kept(float x) {
     float2 r = f2(x);
@@ -68,37 +75,40 @@ __device__ __forceinline__ float2 kept(float x) {
 }
 
 __device__ __forceinline__ GaussK gauss_constants() {
-    return GaussK{kept(0.3275911f * 0.70710678118654752f), kept(1.0f), kept(-0.5f * tc::kLog2e),
-                  kept(-0.5f * 1.061405429f), kept(0.5f * 1.453152027f), kept(-0.5f * 1.421413741f),
-                  kept(0.5f * 0.284496736f), kept(-0.5f * 0.254829592f), kept(0.5f)};
+    return GaussK{kept(483.096161f), kept(-531.246826f), kept(124.012375f), kept(-38.318634f), kept(-0.846040547f),
+                  kept(-1.3042357f), kept(-0.33545205f)};
 }
 
-__device__ __forceinline__ void gauss2(const GaussK& k, float2 a, float2 mag, float2& e, float2& u) {
-    const float2 d = __ffma2_rn(mag, k.p, k.one);
-    const float2 t = make_float2(rcp(d.x), rcp(d.y));
-    const float2 q = __fmul2_rn(__fmul2_rn(a, k.q), a);
-    e = make_float2(ex2(q.x), ex2(q.y));
-    float2 s = __ffma2_rn(t, k.a5, k.a4);
-    s = __ffma2_rn(t, s, k.a3);
-    s = __ffma2_rn(t, s, k.a2);
-    s = __ffma2_rn(t, s, k.a1);
-    u = __ffma2_rn(__fmul2_rn(t, s), e, k.half);
+// e and minus the tail
+__device__ __forceinline__ void gauss2(const GaussK& k, float2 a, float2& e, float2& minus) {
+    // (k a by single factors: one constant less in registers, where the 256 x 256 tiles have none left)
+    const float2 b = make_float2(a.x * kGaussK, a.y * kGaussK), q = __fmul2_rn(b, b);
+    const float2 t = make_float2(rcp(fabsf(b.x) + kGaussR), rcp(fabsf(b.y) + kGaussR));
+    e = make_float2(ex2(-q.x), ex2(-q.y));
+    float2 s = __ffma2_rn(t, k.c7, k.c6);
+    s = __ffma2_rn(t, s, k.c5);
+    s = __ffma2_rn(t, s, k.c4);
+    s = __ffma2_rn(t, s, k.c3);
+    s = __ffma2_rn(t, s, k.c2);
+    s = __ffma2_rn(t, s, k.c1);
+    minus = __fmul2_rn(__fmul2_rn(t, s), e);
 }
 
-// a Phi(a) = a / 2 + |a| u
+// a Phi(a) = max(a, 0) - |a| tail, with the step's factor 0 or 1 for the maximum and a bounded |a|, so that infinities give
+// what the product a Phi(a) does: infinity and, for the negative one, NaN.
 __device__ __forceinline__ float2 gelu2(const GaussK& k, float2 a) {
-    const float2 mag = make_float2(fabsf(a.x), fabsf(a.y));
-    float2 e, u;
-    gauss2(k, a, mag, e, u);
-    return __ffma2_rn(mag, u, __fmul2_rn(a, k.half));
+    float2 e, minus;
+    gauss2(k, a, e, minus);
+    const float2 step = make_float2(__saturatef(a.x * 1e38f), __saturatef(a.y * 1e38f));
+    return __ffma2_rn(a, step, __fmul2_rn(make_float2(fminf(fabsf(a.x), 1e30f), fminf(fabsf(a.y), 1e30f)), minus));
 }
 
-// Phi(a) + a phi(a), Phi(a) = 1/2 + sign(a) u
+// Phi(a) + a phi(a)
 __device__ __forceinline__ float2 gelu_grad2(const GaussK& k, float2 a) {
-    float2 e, u;
-    gauss2(k, a, make_float2(fabsf(a.x), fabsf(a.y)), e, u);
-    const float2 su = make_float2(copysignf(u.x, a.x), copysignf(u.y, a.y));
-    return __ffma2_rn(__fmul2_rn(a, f2(0.39894228040143268f)), e, __fadd2_rn(su, k.half));
+    float2 e, minus;
+    gauss2(k, a, e, minus);
+    const float2 cdf = make_float2(a.x >= 0.f ? 1.f + minus.x : -minus.x, a.y >= 0.f ? 1.f + minus.y : -minus.y);
+    return __ffma2_rn(__fmul2_rn(a, f2(0.39894228040143268f)), e, cdf);
 }
 
 // -------------------------------------------------- operands in the workspace

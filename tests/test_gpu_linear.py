@@ -544,3 +544,53 @@ def test_residual_in_place_at_every_access(gt, m, k, n, xt, yt, pad, offset):
     assert got[0] is buf and all(torch.equal(a, c) for a, c in zip(got, want))
     R.check({"dx": got[0]}, R.linear_bwd(dy, x, w, None, False, add))
     gt.gt_check_device_status()
+
+
+def _gelu_exact(a):
+    """GELU and its slope at the fp64 values a, |a| <= 13, and the bounds of both as fp32 arithmetic makes them from the CDF's tail.
+    (Exact values from erfc: torch.special.ndtr is 1/2 + erf / 2, which below -8 has no digit left in fp64 either.)
+    The tail: its fit (0.5e-8 / max(1, |a|), 5e-5 of itself at most), and relative roundings: a polynomial of seven
+    terms whose magnitudes add up to 2.5 times its value (2 x 7 x 2.5), its argument (four units, which count 3.2 times), two
+    products, two units of the power (4), 60 with the rest; the power's own argument a^2 / 2 carries four roundings: 2 a^2.
+    """
+    x = a.abs()
+    tail, dens = 0.5 * torch.special.erfc(x * math.sqrt(0.5)), torch.exp(-0.5 * a * a) / math.sqrt(2 * math.pi)
+    tail_off = torch.minimum(0.5e-8 / x.clamp(min=1), 5e-5 * tail) + R.U32 * (60 + 2 * a * a) * tail
+    cdf = torch.where(a >= 0, 1 - tail, tail)
+    cdf_off = tail_off + (a >= 0) * R.U32
+    y, slope = a * cdf, cdf + a * dens
+    return (y, x * cdf_off + R.U32 * y.abs()), (slope, cdf_off + x * dens * R.U32 * (8 + 2 * a * a) + R.U32 * slope.abs())
+
+
+@pytest.mark.parametrize("path", ["one kernel", "product", "join", "bf16 operands"])
+def test_gelu_keeps_its_relative_accuracy(gt, path):
+    """Far below zero too, where 1/2 and the CDF's other half cancel: the epilogues of the forward."""
+    a = torch.cat([torch.linspace(-13, 13, 26001), torch.linspace(-0.01, 0.01, 201), torch.tensor([0.0, -0.0])]).cuda()
+    k, n, t = {"one kernel": (1, 1, F), "product": (128, 8, F), "join": (128, 3, F), "bf16 operands": (16, 8, B)}[path]
+    x = torch.zeros(a.numel(), k, dtype=t, device="cuda")
+    x[:, 0] = a
+    w = torch.zeros(k, n, dtype=t, device="cuda")
+    w[0] = 1
+    y, _ = gt.gt_linear_fwd(x, w, act=gt.GT_ACT_GELU, out_dtype=F)
+    want, _ = _gelu_exact(R.d(x[:, :1]))
+    R.check({"y": y}, {"y": tuple(v.expand(-1, n) for v in want)}, floor=1e-37)
+
+
+@pytest.mark.parametrize("n", [100, 26203])           # one kernel, and the pass that forms da
+def test_gelu_slope_keeps_its_relative_accuracy(gt, n):
+    a = torch.cat([torch.linspace(-13, 13, n - 3), torch.tensor([0.0, -0.0, -0.75179])]).cuda()[None, :]
+    one = torch.ones(1, 1, device="cuda")
+    db = gt.gt_linear_bwd(torch.ones_like(a), one, torch.ones_like(a), pre=a, act=gt.GT_ACT_GELU, need_dx=False, need_dw=False)[2]
+    _, want = _gelu_exact(R.d(a[0]))
+    R.check({"db": db}, {"db": want}, floor=1e-37)
+
+
+@pytest.mark.parametrize("t", [F, B])
+def test_gelu_of_infinities_and_nan(gt, t):
+    """a Phi(a): infinity, and NaN for minus infinity (times 0) and NaN; a / 2 for the smallest, as accurate as the tail."""
+    a = torch.tensor([[float("inf")], [float("-inf")], [float("nan")], [1e38], [-1e38], [1e-30], [-1e-30]], dtype=t, device="cuda")
+    y, _ = gt.gt_linear_fwd(a, torch.ones(1, 1, dtype=t, device="cuda"), act=gt.GT_ACT_GELU, out_dtype=F)
+    y, a = y[:, 0], a[:, 0].float()
+    assert y[0] == float("inf") and y[1].isnan() and y[2].isnan()
+    assert y[3] == a[3] and y[4] == 0
+    assert float((y[5:] / (a[5:] / 2) - 1).abs().max()) <= 62 * R.U32
