@@ -459,10 +459,16 @@ def _type_code(name, t):
     raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
 
 
+_MOST = 2 ** 31 - 1      # the C calls' sizes are 32-bit, and ctypes would pass a larger one's low bits
+
+
 def _two_dims(name, t):
     if t.dim() != 2:
         raise ValueError(f"{name} must have 2 dimensions, got {t.dim()}")
-    return t.shape
+    rows, cols = t.shape
+    if rows > _MOST or cols > _MOST:
+        raise ValueError(f"{name} has more than 2^31 - 1 rows or columns")
+    return rows, cols
 
 
 def _room(workspace, need, device):
@@ -494,17 +500,23 @@ def _linear_bwd_room(device_index, dt, yt, m, k, n, act, aligned):
 
 def gt_layer_norm_workspace_size(n: int, c: int) -> int:
     """Workspace bytes of gt_layer_norm_bwd (0 for sizes that are not supported)."""
+    if max(n, c) > _MOST:
+        return 0
     return int(load_library().gt_layer_norm_workspace_size(n, c))
 
 
 def gt_linear_fwd_workspace_size(dtype: int, m: int, k: int, n: int, aligned: bool = True) -> int:
     """Workspace bytes of gt_linear_fwd (0: none needed, or sizes that are not supported)."""
+    if max(m, k, n) > _MOST:
+        return 0
     return int(load_library().gt_linear_fwd_workspace_size(dtype, m, k, n, int(aligned)))
 
 
 def gt_linear_bwd_workspace_size(dtype: int, ytype: int, m: int, k: int, n: int, act: int = GT_ACT_NONE,
                                  aligned: bool = True) -> int:
-    """Workspace bytes of gt_linear_bwd (0 for sizes that are not supported)."""
+    """Workspace bytes of gt_linear_bwd (0: none needed, or sizes that are not supported)."""
+    if max(m, k, n) > _MOST:
+        return 0
     return int(load_library().gt_linear_bwd_workspace_size(dtype, ytype, m, k, n, act, int(aligned)))
 
 

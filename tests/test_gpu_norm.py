@@ -203,3 +203,15 @@ def test_residual_gradient_in_place_at_every_access(gt, n, c, t, pad, offset):
     got = gt.gt_layer_norm_bwd(dy, x, gain, mean, rstd, dres=buf, dx=buf)
     assert got[0] is buf and all(torch.equal(a, b) for a, b in zip(got, want))
     R.check({"dx": buf}, R.ln_bwd(dy, x, gain, mean, rstd, kept))
+
+
+def test_more_rows_than_32_bits_count_are_refused(gt):
+    """2^32 + 5 rows: not the call of 5 rows that the low 32 bits would make."""
+    x, one = torch.empty((1 << 32) + 5, 1, dtype=B, device="cuda"), torch.ones(1, device="cuda")
+    stats = torch.empty(1, device="cuda").expand(x.shape[0])
+    with pytest.raises(ValueError, match="rows"):
+        gt.gt_layer_norm_fwd(x, one, one)
+    with pytest.raises(ValueError, match="rows"):
+        gt.gt_layer_norm_bwd(x, x, one, stats, stats)
+    with pytest.raises(ValueError, match="rows"):
+        gt.gt_linear_fwd(x, torch.ones(1, 1, dtype=B, device="cuda"))

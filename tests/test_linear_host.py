@@ -106,3 +106,11 @@ def test_binding_refuses_tensors_off_the_gpu(gt):
                  lambda: gt.gt_linear_fwd(x, w), lambda: gt.gt_linear_bwd(torch.zeros(3, 5), x, w)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_sizes_past_32_bits_are_not_cut(gt):
+    """A size above 2^31 - 1 is not supported: its low 32 bits must not be taken for it."""
+    big = (1 << 32) + 4
+    assert gt.gt_layer_norm_workspace_size(big, 64) == gt.gt_layer_norm_workspace_size(4, big) == 0
+    for sizes in ((big, 64, 32), (4, big, 32), (4, 64, big)):
+        assert gt.gt_linear_fwd_workspace_size(0, *sizes) == gt.gt_linear_bwd_workspace_size(1, 1, *sizes, act=1) == 0
