@@ -604,29 +604,35 @@ def gt_linear_bwd(dy, x, w, pre=None, act: int = GT_ACT_NONE, dx_add=None, need_
                   stream=None):
     """Backward of gt_linear_fwd from dy = dL/dy [m][n]: (dx [m][k], dw [k][n], db fp32 [n]), dx
     and dw of x's type, None for those not needed.  pre: the forward's, with GELU.  dx_add
-    [m][k]: a gradient that reaches x another way, added to dx."""
-    if not _is_here(x, stream):
-        return _elsewhere(gt_linear_bwd, x, stream, (dy, x, w, pre, act, dx_add, need_dx, need_dw, need_db, dx, dw, db,
-                                                     workspace))
+    [m][k]: a gradient that reaches x another way, added to dx.  x may be None where dw is not
+    needed, w where dx is not (one of the two gives the sizes and the type)."""
+    if not _is_here(dy, stream):
+        return _elsewhere(gt_linear_bwd, dy, stream, (dy, x, w, pre, act, dx_add, need_dx, need_dw, need_db, dx, dw, db,
+                                                      workspace))
     lib = _lib or load_library()
-    m, k = _two_dims("x", x)
-    n = _two_dims("w", w)[1]
-    xt, dev = x.dtype, x.device
-    dt, yt = _type_code("x", x), _type_code("dy", dy)
-    ldx, ldw = _matrix("x", x, m, k, xt, dev), _matrix("w", w, k, n, xt, dev)
+    need_dx, need_dw = need_dx or dx is not None, need_dw or dw is not None
+    if (x is None and (need_dw or w is None)) or (w is None and need_dx):
+        raise ValueError("x may be None only where dw is not needed, w where dx is not, and not both")
+    m, n = _two_dims("dy", dy)
+    k = _two_dims("w", w)[0] if x is None else _two_dims("x", x)[1]
+    given = w if x is None else x
+    xt, dev = given.dtype, dy.device
+    dt, yt = _type_code("w" if x is None else "x", given), _type_code("dy", dy)
+    xp, ldx = (None, 0) if x is None else (x.data_ptr(), _matrix("x", x, m, k, xt, dev))
+    wp, ldw = (None, 0) if w is None else (w.data_ptr(), _matrix("w", w, k, n, xt, dev))
     lddy = _matrix("dy", dy, m, n, dy.dtype, dev)
     pp, ldp = (None, 0) if pre is None else (pre.data_ptr(), _matrix("pre", pre, m, n, xt, dev))
     ap, lda = (None, 0) if dx_add is None else (dx_add.data_ptr(), _matrix("dx_add", dx_add, m, k, xt, dev))
     dxp, lddx, dwp, lddw, dbp = None, 0, None, 0, None
-    if need_dx or dx is not None:
+    if need_dx:
         dx, dxp, lddx = _matrix_result("dx", dx, m, k, xt, dev)
-    if need_dw or dw is not None:
+    if need_dw:
         dw, dwp, lddw = _matrix_result("dw", dw, k, n, xt, dev)
     if need_db or db is not None:
         db, dbp = _result("db", db, n, dev)
-    xp, wp, dyp = x.data_ptr(), w.data_ptr(), dy.data_ptr()
-    aligned = (xp | wp | dyp | (pp or 0) | (ap or 0) | (dxp or 0) | (dwp or 0) | lddy * dy.element_size() |
-               (ldx | ldw | ldp | lda | lddx | lddw) * x.element_size()) % 16 == 0
+    dyp = dy.data_ptr()
+    aligned = ((xp or 0) | (wp or 0) | dyp | (pp or 0) | (ap or 0) | (dxp or 0) | (dwp or 0) | lddy * dy.element_size() |
+               (ldx | ldw | ldp | lda | lddx | lddw) * given.element_size()) % 16 == 0
     workspace, sp, sn = _room(workspace, _linear_bwd_room(dev.index, dt, yt, m, k, n, act, aligned), dev)
     rc = lib.gt_linear_bwd(dt, yt, m, k, n, dyp, lddy, xp, ldx, wp, ldw, pp, ldp, act, ap, lda, dxp, lddx, dwp, lddw,
                            dbp, sp, sn, _raw_stream(dev.index))

@@ -594,3 +594,30 @@ def test_gelu_of_infinities_and_nan(gt, t):
     assert y[0] == float("inf") and y[1].isnan() and y[2].isnan()
     assert y[3] == a[3] and y[4] == 0
     assert float((y[5:] / (a[5:] / 2) - 1).abs().max()) <= 62 * R.U32
+
+
+@pytest.mark.parametrize("m,k,n", [(200, 70, 90), (1100, 70, 90), (2000, 304, 600)])
+def test_backward_without_what_it_does_not_read(gt, m, k, n):
+    """dx needs no x, dw no w, db one of them: the same results as with both."""
+    for xt, yt in TYPES:
+        dy, x, w, pre = _mat(m, n, yt, 1), _mat(m, k, xt, 2), _mat(k, n, xt, 3), _mat(m, n, xt, 4)
+        for act, p in ((0, None), (1, pre)):
+            dx, dw, db = gt.gt_linear_bwd(dy, x, w, pre=p, act=act)
+            got = gt.gt_linear_bwd(dy, None, w, pre=p, act=act, need_dw=False)
+            assert torch.equal(got[0], dx) and got[1] is None and torch.equal(got[2], db)
+            got = gt.gt_linear_bwd(dy, x, None, pre=p, act=act, need_dx=False)
+            assert got[0] is None and torch.equal(got[1], dw) and torch.equal(got[2], db)
+            for a, c in ((x, None), (None, w)):
+                assert torch.equal(gt.gt_linear_bwd(dy, a, c, pre=p, act=act, need_dx=False, need_dw=False)[2], db)
+    for call in (lambda: gt.gt_linear_bwd(dy, None, w), lambda: gt.gt_linear_bwd(dy, x, None),
+                 lambda: gt.gt_linear_bwd(dy, None, w, need_dw=False, dw=torch.empty_like(w)),
+                 lambda: gt.gt_linear_bwd(dy, None, None, need_dx=False, need_dw=False),
+                 lambda: gt.gt_linear_bwd(dy, x, w[:, :5], need_dx=False),
+                 lambda: gt.gt_linear_bwd(dy, None, w[:, :5], need_dw=False)):
+        with pytest.raises(ValueError):
+            call()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = gt.gt_linear_bwd(dy, None, w, pre=pre, act=1, need_dw=False, stream=side)[0]
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(got, dx)
