@@ -621,3 +621,14 @@ def test_backward_without_what_it_does_not_read(gt, m, k, n):
     got = gt.gt_linear_bwd(dy, None, w, pre=pre, act=1, need_dw=False, stream=side)[0]
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(got, dx)
+
+
+@pytest.mark.parametrize("xt,yt", TYPES)
+def test_column_sums_of_many_rows(gt, xt, yt):
+    """db of a million positive rows: 64 additions in a thread (2^20 rows over 512 x 32), 32 in the CTA, 512 / 8 and 8 in the join,
+    half a unit each at most; 200 of them counted."""
+    m = 1 << 20
+    dy, x, w = _mat(m, 64, yt, 1).abs(), _mat(m, 8, xt, 2), _mat(8, 64, xt, 3)
+    db = gt.gt_linear_bwd(dy, x, w, need_dx=False, need_dw=False)[2]
+    want = dy.double().sum(0)
+    assert float(((db.double() - want).abs() / want).max()) <= 200 * R.U32

@@ -215,3 +215,19 @@ def test_more_rows_than_32_bits_count_are_refused(gt):
         gt.gt_layer_norm_bwd(x, x, one, stats, stats)
     with pytest.raises(ValueError, match="rows"):
         gt.gt_linear_fwd(x, torch.ones(1, 1, dtype=B, device="cuda"))
+
+
+@pytest.mark.parametrize("c", [64, 512])
+@pytest.mark.parametrize("t", [F, B])
+def test_column_sums_of_many_rows(gt, c, t):
+    """dgain and dshift of many rows of positive terms (mean 0, rstd 1, dy and x positive): the additions of a thread, of
+    its CTA's row groups and of the partial rows, half a unit each at most, and one rounding of the product.  64 features:
+    304 CTAs of 64 rows at a time make 54 turns of 2 rows, then 32, 10 and 32 additions; 512: 152 CTAs of 16 rows in fp32, 108 turns
+    of 4 and 4 + 5 + 32, and 304 of 8 in bf16, 108 of 2 and 4 + 10 + 32."""
+    n = 1 << (20 if c == 64 else 18)
+    adds = 185 if c == 64 else 476 if t == F else 265
+    x, dy = _rows(n, c, t, 1).abs(), _rows(n, c, t, 2).abs()
+    mean, rstd = torch.zeros(n, device="cuda"), torch.ones(n, device="cuda")
+    dx, dg, ds = gt.gt_layer_norm_bwd(dy, x, torch.ones(c, device="cuda"), mean, rstd)
+    for got, want in ((dg, (dy.double() * x.double()).sum(0)), (ds, dy.double().sum(0))):
+        assert float(((got.double() - want).abs() / want).max()) <= adds * R.U32
