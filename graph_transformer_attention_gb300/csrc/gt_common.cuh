@@ -55,9 +55,10 @@ inline bool allow_smem(std::atomic<uint64_t>& done, const void* kern, size_t byt
 // Launches `kern` so that it may overlap the kernel before it in the stream
 // (programmatic dependent launch): its CTAs can be scheduled once every CTA of
 // that kernel has executed griddepcontrol.launch_dependents or exited, while
-// that kernel still runs.  A kernel launched this way reads nothing the one
-// before it writes, and ends with griddepcontrol.wait, so that it completes
-// after it and the stream's later work sees both.
+// that kernel still runs.  A kernel launched this way executes griddepcontrol.wait
+// before it reads anything that the kernels before it write, or, if it reads none
+// of it, before it ends: so it completes after them, and the stream's later work
+// sees all of them.
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_overlapped(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
                                      cudaStream_t s, Args&&... args) {

@@ -152,8 +152,13 @@ struct PrepJobs {
     int count;
 };
 
-// Two rows of each input are in flight per thread, four CTAs on an SM (measured on da of 32768 x 4096 bf16:
-// 134 us, 89 % of the copy rate; four rows and two CTAs 145 us).
+// With bf16 operands (PARTS 1) da is rounded to bf16, also where dy came in fp32: both products want it in the operands'
+// type, and a second plane for what the rounding drops would double their time (154 and 158 us each at 32768x1024x4096).
+// dx and dW are 2.3e-3 off in the mean with it, against 1.7e-3 by their own rounding alone; the column sums are
+// taken before it.  Callers who want da whole pass fp32 operands (PARTS 3).
+//
+// Two rows of each input are in flight per thread, four CTAs on an SM (measured on da of 32768 x 4096 bf16 with
+// GELU, which issues in 63 % of the cycles: 143 us, 83 % of the copy rate; four rows and two CTAs were 8 % slower).
 template <typename TI, int PARTS>
 __device__ __forceinline__ void prep_rows(const PrepJob& J, int bx, int by) {
     using TP = typename std::conditional<PARTS == 3, float, bf16>::type;
@@ -585,12 +590,13 @@ struct Ring {
 // tile's products.  A lane holds a row and stores whole 32-byte sectors of it.
 //
 // The tensor core drops what does not fit when it adds to its fp32 accumulator (measured on
-// all-positive sums: 4.4e-8 of the sum lost per 16-deep step).  So an accumulator takes at most
-// g.chunk k-blocks; the warps that take it out add the chunks up in registers, rounding to nearest.
+// all-positive sums: 4.4e-8 of the sum lost per 16-deep step in the mean; a whole unit of it, 1.2e-7, at most).  So an
+// accumulator takes at most g.chunk k-blocks; the warps that take it out add the chunks up in registers, rounding to nearest.
 //
-// Measured (single calls on one GB300): 32768 x 1024 x 4096 bf16 150 us (1.83 PFLOP/s, 97 % of the library product's
-// rate), with GELU 156, with GELU and pre 183 (its boxes take shared memory's cycles from the products' operands);
-// dx 150, dW 156 (64 tiles for 76 pairs of SMs); fp32, 4096 x 1024 x 4096: 160 us, preparation included.
+// Measured (single calls on one GB300, the library's product of the same operands beside it): 32768 x 1024 x 4096 bf16 153 to
+// 156 us (1.78 PFLOP/s, 95 % of the measured peak; library 140 to 142), with GELU 166 to 171, with GELU and pre 187 to 191
+// (its boxes take shared memory's cycles from the products' operands); dx 154 (146), dW 158 to 160 (142 to 146; 64 tiles for
+// 76 pairs of SMs); fp32, 4096 x 1024 x 4096: 132 us, preparation included.
 // The products of 256 x 256 tiles run at the tensor rate but for the ends of tiles; calls one after another
 // run into the power limit, as the library's do.
 struct GemmJob {
@@ -1237,9 +1243,9 @@ struct GemmPlan {
     double us;   // modelled
 };
 
-// k-blocks an accumulator may sum: 256 deep for an fp32 result (2e-7 lost at most), 4096 deep
-// for a bf16 one (1.1e-5, against a rounding of 3.9e-3); one k-block of split operands, whose large
-// terms are the last four of 24 steps.
+// k-blocks an accumulator may sum: 256 deep for an fp32 result (16 steps: 7e-7 of an all-positive sum lost by the mean
+// above, 1.9e-6 at most; 3e-7 measured), 4096 deep for a bf16 one (1.1e-5 and 3e-5, against a rounding of 3.9e-3); one
+// k-block of split operands, whose large terms are the last four of 24 steps.
 int chunk_of(bool f32_out, int planes) { return planes == 3 ? 1 : f32_out ? 4 : 64; }
 
 // The tile and the splits of the contraction with the least modelled time, in microseconds as measured:
@@ -1599,12 +1605,17 @@ Epi make_epi(const float* bias, int act, int ytype, int ptype, const void* r, in
 }
 
 int small_tiles(int rows, int cols) { return (rows + kSmT - 1) / kSmT * ((cols + kSmT - 1) / kSmT); }
-// Whether a fp32 call goes to the fp32 pipes in one kernel: short contractions and few multiplications.
-// Measured against the split products (device time of the call): forward 512x64x64 5.7 against 6.8 us,
-// 16384x64x64 8.3 against 9.3, 6800x64x192 11.0 against 9.9 (but one launch for two, and no workspace), 6800x128x128
-// 13.2 against 9.5; backward (one launch for three) 512x64x64 8.2 against 10.7, 100x256x64 7.2 against 10.4, 512x128x128
-// 11.5 against 12.3, 300x512x100 13.3 against 12.9, 1024x64x128 12.3 against 11.7, 512x64x192 15.6 against 12.3,
-// 1024x512x128 17.7 against 16.4.
+// Whether a fp32 call goes to the fp32 pipes in one kernel: short contractions and few multiplications.  One launch
+// without a workspace for two launches (three in the backward) saves a caller from Python 8 us (12), so the cut-offs let the
+// device lose up to 8 % of its time on the way there.  Measured against the split products (us on the device in a captured
+// graph, split and this; then as called one after another, split and this):
+//   forward   512x64x64 7.2, 5.6; 20, 12     16384x64x64 9.8, 8.3; 21, 12     65536x64x16 24.2, 21.8; 27, 24
+//             6800x64x192 10.7, 11.0; 21, 13     512x64x2048 7.7, 8.1; 21, 13     1700x16x2048 17.3, 13.0; 21, 15
+//   past it   6800x128x128 9.8, 13.2; 21, 16     512x128x128 8.3, 9.0; 21, 13     1x512x512 9.5, 28.2; 26, 31
+//   backward  512x64x64 10.5, 6.9; 31, 17     100x256x64 10.2, 6.1; 30, 17     512x256x128 11.9, 10.2; 30, 17
+//             1024x64x128 11.0, 10.9; 31, 17     1000x64x64 10.6, 10.8; 30, 17     300x512x100 12.1, 11.9; 31, 17
+//             1024x16x16 10.0, 10.8; 31, 17     64x16x128 8.8, 9.5; 29, 17
+//   past it   2048x64x64 11.9, 18.7; 30, 21     512x64x192 11.6, 14.0; 30, 17     1024x256x128 12.5, 15.7; 30, 18
 bool small_fwd(int dtype, int m, int k, int n) {
     return dtype == GT_F32 && k <= 64 && (int64_t)m * k * n <= (96 << 20);
 }

@@ -16,8 +16,9 @@
 // (no atomics: the same result on every run).
 //
 // Measured (one GB300, inputs larger than the L2; share of the copy rate, 6.79 TB/s): forward 32768 x 1024
-// fp32 to bf16 32.5 us (91 %), bf16 26.4 us (75 %); backward with dres 32768 x 1024 bf16 46.5 us (85 %), 16384 x 4096
-// bf16 92 us (86 %), 65536 x 512 fp32 81 us (98 %); small inputs are latency: 6800 x 64 fp32 3.0 us and 4.9 us.
+// fp32 to bf16 34 us (87 %), bf16 26.4 us (75 %), bf16 to fp32 39.5 us (75 %); backward with dres 32768 x 1024 bf16 48 us (82 %),
+// x fp32 and dy bf16 73.5 us (94 %), 16384 x 4096 bf16 93 us (85 %), 65536 x 512 fp32 82 us (97 %); small inputs are latency:
+// 6800 x 64 fp32 3.0 us and 5.2 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -228,8 +229,9 @@ norm_bwd(int64_t n, int c, const TY* __restrict__ dy, int64_t lddy, const TX* __
             in.rs[k] = row < n ? rstd[ra] : 0.f;
         }
     };
-    // The next rows are on their way while these are computed, where the registers hold both (4096 x 8192
-    // with 512 threads to a row: bf16 71 against 79 us, fp32, which spills then, 117 against 101).
+    // The next rows are on their way while these are computed, where the registers hold both (with them ahead and without:
+    // 8192 x 4096 bf16 46.5 and 64 us, fp32 77 and 107; 4096 x 8192 bf16 61 and 71, fp32, which spills then, 109 and 90;
+    // 2048 x 16384 bf16 150 and 113).
     constexpr bool kAhead = TPR * NV * sizeof(TX) <= 2048;
     Rows next;
     const int64_t step = (int64_t)gridDim.x * C::ROWS;

@@ -401,16 +401,20 @@ int gt_layer_norm_bwd(int32_t xtype, int32_t ytype, int32_t n, int32_t c, const 
                       const void* dres, int64_t ldr, void* dx, int64_t lddx, float* dgain, float* dshift,
                       void* workspace, size_t ws_bytes, void* stream);
 
-/* Activations of the linear layer: none, or GELU(a) = a Phi(a) (Phi the normal CDF). */
+/*
+ * Activations of the linear layer: none, or GELU(a) = a Phi(a) (Phi the normal CDF), in fp32:
+ * 1.2e-7 off for |a| <= 2, 6e-5 of itself down to a = -13; infinity for infinity, NaN for minus
+ * infinity (its product with 0).
+ */
 typedef enum { GT_ACT_NONE = 0, GT_ACT_GELU = 1 } gt_act;
 
 /*
  * gt_linear_fwd: a = x W + b, y = act(a) + r.
  *   dtype  type of x, W and pre: GT_BF16 (bf16 products, fp32 sums) or GT_F32
  *          (products of three-part bf16 splits, fp32 sums: fp32 accuracy for inputs
- *          above 2^-100 in magnitude, smaller ones lose low bits; a non-finite input
- *          makes the sums it enters non-finite, NaN where exact arithmetic may give
- *          an infinity).
+ *          above 2^-100 in magnitude, smaller ones lose low bits; a non-finite input, or
+ *          a product past the range of fp32, makes the sums it enters non-finite, NaN
+ *          where exact arithmetic may give an infinity).
  *   ytype  type of y and r: GT_F32, or GT_BF16 with dtype GT_BF16.
  *   x  device [m][ldx >= k]; W device [k][ldw >= n] (in x out); b device fp32 [n] or
  *   NULL; r device [m][ldr >= n] or NULL (it may be y itself).
@@ -434,10 +438,10 @@ typedef enum { GT_ACT_NONE = 0, GT_ACT_GELU = 1 } gt_act;
  *          that reaches x another way.
  *   dx     device [m][lddx >= k] of dtype; dw device [k][lddw >= n] of dtype; db device
  *          fp32 [n] (outputs, overwritten).
- *   With dtype GT_BF16 da is rounded to bf16 for the two products (db is summed before
- *   that rounding).
- *   workspace: at least gt_linear_bwd_workspace_size bytes (`aligned` as above; else
- *   with copies of dy, x and W and fp32 results, [m][k] and [k][n]).
+ *   With dtype GT_BF16 da is rounded to bf16 for the two products, from fp32 dy too (db is
+ *   summed before that rounding); with GT_F32 (operands converted by the caller) it is not.
+ *   workspace: at least gt_linear_bwd_workspace_size bytes (may be NULL where that is 0;
+ *   `aligned` as above; else with copies of dy, x and W and fp32 results, [m][k] and [k][n]).
  * Errors as the forward's, plus GT_ERR_INVALID_ARG when dx, dw and db are all NULL,
  * pre and act disagree, or add comes without dx.
  */
