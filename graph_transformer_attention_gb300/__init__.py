@@ -14,6 +14,11 @@ Functions (same names as the C entry points):
     gt_layer_norm_bwd(dy, x, gain, mean, rstd, dres)          -> (dx, dgain, dshift)
     gt_linear_fwd(x, w, b, act, r)                            -> (y, pre)
     gt_linear_bwd(dy, x, w, pre, act, dx_add)                 -> (dx, dw, db)
+    gt_qk_norm_fwd(q, k, gain_q, gain_k, freq, pos_q, pos_k)  -> (yq, yk)
+    gt_qk_norm_bwd(dyq, dyk, q, k, gain_q, gain_k, freq, ..)  -> (dq, dk, dgain_q, dgain_k)
+    gt_cross_attn_fwd(q, k, v, q_off, kv_off, key_mask)       -> (o, lse)
+    gt_cross_attn_bwd(q, k, v, o, dO, lse, q_off, kv_off, ..) -> (dq, dk, dv)
+    gt_grad_clip(grads, max_norm, out)                        -> norm
 The operation follows MegaGraph (abstract: attention scores plus a
 topology-aware bias matrix; Fig. 4: blockwise KV streaming with the bias column
 slice formed per block) with the Graphormer bias b[h][i][j] = T[h][spd[i][j]].
@@ -35,6 +40,9 @@ __all__ = [
     "GT_SPD_AUTO", "GT_SPD_SCAN32", "GT_SPD_SCAN16", "GT_SPD_QUEUE32", "GT_SPD_GLOBAL64",
     "gt_layer_norm_fwd", "gt_layer_norm_bwd", "gt_layer_norm_workspace_size", "gt_linear_fwd", "gt_linear_bwd",
     "gt_linear_fwd_workspace_size", "gt_linear_bwd_workspace_size", "GT_ACT_NONE", "GT_ACT_GELU",
+    "gt_cross_attn_fwd", "gt_cross_attn_bwd", "gt_cross_attn_workspace_size", "gt_qk_norm_fwd", "gt_qk_norm_bwd",
+    "gt_qk_norm_workspace_size", "GT_ROT_HALVES", "GT_ROT_PAIRS", "gt_grad_clip", "gt_tensor_list",
+    "gt_grad_clip_workspace_size",
 ]
 
 GT_F32 = 0
@@ -140,6 +148,24 @@ def load_library():
         lib.gt_linear_bwd.argtypes = [i32, i32, i32, i32, i32, P, i64, P, i64, P, i64, P, i64, i32, P, i64, P, i64,
                                       P, i64, P, P, sz, P]
         lib.gt_linear_bwd.restype = ctypes.c_int
+        lib.gt_cross_attn_workspace_size.argtypes = [i32] * 9
+        lib.gt_cross_attn_workspace_size.restype = sz
+        view = [P, i64, i64]
+        lib.gt_cross_attn_fwd.argtypes = [i32] * 7 + view * 3 + [P, P, P, f32] + view + [P, P, sz, P]
+        lib.gt_cross_attn_fwd.restype = ctypes.c_int
+        lib.gt_cross_attn_bwd.argtypes = [i32] * 7 + view * 5 + [P, P, P, P, f32] + view * 3 + [P, sz, P]
+        lib.gt_cross_attn_bwd.restype = ctypes.c_int
+        lib.gt_qk_norm_fwd.argtypes = [i32, i32, i32, f32, P, i32, i32] + ([i32, i32] + view + [P, P] + view) * 2 + [P]
+        lib.gt_qk_norm_fwd.restype = ctypes.c_int
+        lib.gt_qk_norm_workspace_size.argtypes = [i32]
+        lib.gt_qk_norm_workspace_size.restype = sz
+        lib.gt_qk_norm_bwd.argtypes = ([i32, i32, i32, f32, P, i32, i32] +
+                                       ([i32, i32] + view * 2 + [P, P] + view + [P]) * 2 + [P, sz, P])
+        lib.gt_qk_norm_bwd.restype = ctypes.c_int
+        lib.gt_grad_clip_workspace_size.argtypes = [i32]
+        lib.gt_grad_clip_workspace_size.restype = sz
+        lib.gt_grad_clip.argtypes = [P, i32, f32, P, P, sz, P]
+        lib.gt_grad_clip.restype = ctypes.c_int
         lib.gt_kernel_stats_reset.argtypes = [i32]
         lib.gt_kernel_stats_reset.restype = ctypes.c_int
         lib.gt_kernel_stats_read.argtypes = [ctypes.POINTER(KernelStat), i32, ctypes.POINTER(i32)]
@@ -639,6 +665,334 @@ def gt_linear_bwd(dy, x, w, pre=None, act: int = GT_ACT_NONE, dx_add=None, need_
     if rc:
         raise GtError("gt_linear_bwd", rc)
     return dx, dw, db
+
+
+GT_ROT_HALVES = 0
+GT_ROT_PAIRS = 1
+
+
+def _heads(name, t, rows, heads, d, dtype, device, result=False):
+    """(address, row stride, head stride) of a [rows][heads][d] tensor with contiguous channels."""
+    if t.shape != (rows, heads, d):
+        raise ValueError(f"{name} must be [{rows}][{heads}][{d}], got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, not {t.device}")
+    ld, hd, unit = t.stride()
+    if unit != 1 and d > 1:
+        raise ValueError(f"the channels of {name} must be contiguous")
+    # the stride of a single head or row means nothing
+    if heads == 1:
+        hd = (d + 7) // 8 * 8
+    if rows == 1:
+        ld = (heads * hd + 7) // 8 * 8
+    if result and not ((heads == 1 or hd >= d) and (rows == 1 or ld >= (heads - 1) * hd + d) or
+                       (rows == 1 or ld >= d) and (heads == 1 or hd >= (rows - 1) * ld + d)):
+        raise ValueError(f"the rows of {name} overlap")
+    return t.data_ptr(), ld, hd
+
+
+def _heads_result(name, t, rows, heads, d, dtype, device):
+    """(t, (address, row stride, head stride)) of a [rows][heads][d] result: the caller's, or a new one."""
+    if t is None:
+        t = torch.empty((rows, heads, d), dtype=dtype, device=device)
+    return t, _heads(name, t, rows, heads, d, dtype, device, result=True)
+
+
+def _three_dims(name, t):
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dimensions, got {t.dim()}")
+    if max(t.shape) > _MOST:
+        raise ValueError(f"{name} has more than 2^31 - 1 rows, heads or channels")
+    return t.shape
+
+
+def _ints(name, t, size, device):
+    if t.shape != (size,) or t.dtype is not torch.int32 or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous int32 [{size}] on {device}")
+    return t.data_ptr()
+
+
+def _sequences(q_off, kv_off, nk, key_mask, device):
+    """(batch, addresses of the offsets and of the mask)"""
+    if (q_off is None) != (kv_off is None):
+        raise ValueError("q_off and kv_off belong together")
+    batch, qp, kp, mp = 1, None, None, None
+    if q_off is not None:
+        batch = q_off.numel() - 1
+        if batch < 1:
+            raise ValueError("q_off must have at least 2 values")
+        qp, kp = _ints("q_off", q_off, batch + 1, device), _ints("kv_off", kv_off, batch + 1, device)
+    if key_mask is not None:
+        if (key_mask.shape != (nk,) or key_mask.dtype not in (torch.bool, torch.uint8) or key_mask.device != device or
+                not key_mask.is_contiguous()):
+            raise ValueError(f"key_mask must be contiguous bool or uint8 [{nk}] on {device}")
+        mp = key_mask.data_ptr()
+    return batch, qp, kp, mp
+
+
+def _in_place(*views):
+    """Whether rows of bf16 are read without a copy: bases and strides of whole 16 bytes, no stride of 0."""
+    bits = 0
+    for p, ld, hd in views:
+        if ld == 0 or hd == 0:
+            return False
+        bits |= p | 2 * ld | 2 * hd
+    return bits % 16 == 0
+
+
+@functools.lru_cache(maxsize=4096)
+def _cross_room(device_index, dt, nq, nk, h, hk, d, batch, backward, aligned):
+    return int(load_library().gt_cross_attn_workspace_size(dt, nq, nk, h, hk, d, batch, backward, aligned))
+
+
+def gt_cross_attn_workspace_size(dtype: int, nq: int, nk: int, h: int, hk: int, d: int, batch: int = 1,
+                                 backward: bool = False, aligned: bool = True) -> int:
+    """Workspace bytes of gt_cross_attn_fwd or, with backward, of gt_cross_attn_bwd (0: none needed, or sizes
+    that are not supported).  aligned: all bf16 inputs have bases and strides of whole 16 bytes."""
+    if max(nq, nk, h, hk, d, batch) > _MOST:
+        return 0
+    return int(load_library().gt_cross_attn_workspace_size(dtype, nq, nk, h, hk, d, batch, int(backward), int(aligned)))
+
+
+def _lse_of(lse, h, nq, device):
+    if lse.shape != (h, nq) or lse.dtype is not torch.float32 or lse.device != device or not lse.is_contiguous():
+        raise ValueError(f"lse must be contiguous fp32 [{h}][{nq}] on {device}")
+    return lse.data_ptr()
+
+
+def gt_cross_attn_fwd(q, k, v, q_off=None, kv_off=None, key_mask=None, scale: float | None = None, out=None, lse=None,
+                      workspace=None, stream=None):
+    """Cross attention forward: o [nq][h][d] and lse fp32 [h][nq] of queries q [nq][h][d] over k and v [nk][hk][d]
+    (fp32 or bf16; query head j reads key head j / (h / hk); rows and heads may be strided).
+
+    q_off, kv_off int32 [batch + 1]: packed sequences, each with its own keys (default: one sequence).  key_mask bool
+    or uint8 [nk]: keys with 0 are not seen.  scale: 1 / sqrt(d) by default.  A query that sees no key has o = 0 and
+    lse = -infinity; rows outside the sequences are not written."""
+    if not _is_here(q, stream):
+        return _elsewhere(gt_cross_attn_fwd, q, stream, (q, k, v, q_off, kv_off, key_mask, scale, out, lse, workspace))
+    lib = _lib or load_library()
+    nq, h, d = _three_dims("q", q)
+    nk, hk, _ = _three_dims("k", k)
+    xt, dev, dt = q.dtype, q.device, _type_code("q", q)
+    qv, kv, vv = _heads("q", q, nq, h, d, xt, dev), _heads("k", k, nk, hk, d, xt, dev), _heads("v", v, nk, hk, d, xt, dev)
+    batch, qp, kp, mp = _sequences(q_off, kv_off, nk, key_mask, dev)
+    out, ov = _heads_result("out", out, nq, h, d, xt, dev)
+    if lse is None:
+        lse = torch.empty((h, nq), dtype=torch.float32, device=dev)
+    lp = _lse_of(lse, h, nq, dev)
+    workspace, wp, wn = _room(workspace, _cross_room(dev.index, dt, nq, nk, h, hk, d, batch, 0, _in_place(qv, kv, vv)), dev)
+    rc = lib.gt_cross_attn_fwd(dt, nq, nk, h, hk, d, batch, *qv, *kv, *vv, qp, kp, mp,
+                               1.0 / math.sqrt(d) if scale is None else scale, *ov, lp, wp, wn, _raw_stream(dev.index))
+    if rc:
+        raise GtError("gt_cross_attn_fwd", rc)
+    return out, lse
+
+
+def gt_cross_attn_bwd(q, k, v, o, dO, lse, q_off=None, kv_off=None, key_mask=None, scale: float | None = None, dq=None,
+                      dk=None, dv=None, workspace=None, stream=None):
+    """Gradients of sum(o * dO) of gt_cross_attn_fwd, from its inputs and results: (dq, dk, dv), of q's type.  Rows
+    outside the sequences are not written."""
+    if not _is_here(q, stream):
+        return _elsewhere(gt_cross_attn_bwd, q, stream,
+                          (q, k, v, o, dO, lse, q_off, kv_off, key_mask, scale, dq, dk, dv, workspace))
+    lib = _lib or load_library()
+    nq, h, d = _three_dims("q", q)
+    nk, hk, _ = _three_dims("k", k)
+    xt, dev, dt = q.dtype, q.device, _type_code("q", q)
+    qv, kv, vv = _heads("q", q, nq, h, d, xt, dev), _heads("k", k, nk, hk, d, xt, dev), _heads("v", v, nk, hk, d, xt, dev)
+    ov, gv, lp = _heads("o", o, nq, h, d, xt, dev), _heads("dO", dO, nq, h, d, xt, dev), _lse_of(lse, h, nq, dev)
+    batch, qp, kp, mp = _sequences(q_off, kv_off, nk, key_mask, dev)
+    dq, dqv = _heads_result("dq", dq, nq, h, d, xt, dev)
+    dk, dkv = _heads_result("dk", dk, nk, hk, d, xt, dev)
+    dv, dvv = _heads_result("dv", dv, nk, hk, d, xt, dev)
+    workspace, wp, wn = _room(workspace,
+                              _cross_room(dev.index, dt, nq, nk, h, hk, d, batch, 1, _in_place(qv, kv, vv, gv)), dev)
+    rc = lib.gt_cross_attn_bwd(dt, nq, nk, h, hk, d, batch, *qv, *kv, *vv, *ov, *gv, lp, qp, kp, mp,
+                               1.0 / math.sqrt(d) if scale is None else scale, *dqv, *dkv, *dvv, wp, wn,
+                               _raw_stream(dev.index))
+    if rc:
+        raise GtError("gt_cross_attn_bwd", rc)
+    return dq, dk, dv
+
+
+@functools.lru_cache(maxsize=256)
+def _qk_room(device_index, d):
+    return int(load_library().gt_qk_norm_workspace_size(d))
+
+
+def gt_qk_norm_workspace_size(d: int) -> int:
+    """Workspace bytes of gt_qk_norm_bwd (0 for a d that is not supported)."""
+    return 0 if d > _MOST else int(load_library().gt_qk_norm_workspace_size(d))
+
+
+def _rotation(freq, d, device):
+    """(address, channels that turn) of the rotation's frequencies"""
+    if freq is None:
+        return None, 0
+    if freq.dim() != 1 or 2 * freq.numel() > d or freq.numel() < 1:
+        raise ValueError(f"freq must be fp32 [rot / 2] with 2 <= rot <= {d}, got {tuple(freq.shape)}")
+    return _vector("freq", freq, freq.numel(), device), 2 * freq.numel()
+
+
+def gt_qk_norm_fwd(q, k, gain_q, gain_k=None, freq=None, pos_q=None, pos_k=None, pairs: int = GT_ROT_HALVES,
+                   eps: float = 1e-6, out_dtype=None, out_q=None, out_k=None, stream=None):
+    """Norm of every head of q [nq][h][d] and k [nk][hk][d] (one type; k may be None): gain x / sqrt(mean x^2 + eps),
+    and, with freq fp32 [rot / 2], the rotation of the first rot channels by pos * freq.  Returns (yq, yk) of out_dtype
+    (default: q's type).  pos_q, pos_k int32: the rows' positions (default: their index).  pairs: channels i and
+    i + rot / 2 turn together (GT_ROT_HALVES), or 2 i and 2 i + 1 (GT_ROT_PAIRS).  out_q may be q, out_k may be k."""
+    if not _is_here(q, stream):
+        return _elsewhere(gt_qk_norm_fwd, q, stream,
+                          (q, k, gain_q, gain_k, freq, pos_q, pos_k, pairs, eps, out_dtype, out_q, out_k))
+    lib = _lib or load_library()
+    nq, h, d = _three_dims("q", q)
+    xt, dev = q.dtype, q.device
+    yt = out_dtype or (xt if out_q is None else out_q.dtype)
+    fp, rot = _rotation(freq, d, dev)
+    qv, gq = _heads("q", q, nq, h, d, xt, dev), _vector("gain_q", gain_q, d, dev)
+    pq = None if pos_q is None else _ints("pos_q", pos_q, nq, dev)
+    out_q, yqv = _heads_result("out_q", out_q, nq, h, d, yt, dev)
+    keys = (1, 1, None, 0, 0, None, None, None, 0, 0)
+    if k is not None:
+        nk, hk, _ = _three_dims("k", k)
+        kv, gk = _heads("k", k, nk, hk, d, xt, dev), _vector("gain_k", gain_k, d, dev)
+        pk = None if pos_k is None else _ints("pos_k", pos_k, nk, dev)
+        out_k, ykv = _heads_result("out_k", out_k, nk, hk, d, yt, dev)
+        keys = (nk, hk, *kv, gk, pk, *ykv)
+    elif gain_k is not None or pos_k is not None or out_k is not None:
+        raise ValueError("gain_k, pos_k and out_k belong to k")
+    rc = lib.gt_qk_norm_fwd(_type_code("q", q), _type_code("out_q", out_q), d, eps, fp, rot, pairs, nq, h, *qv, gq, pq, *yqv,
+                            *keys, _raw_stream(dev.index))
+    if rc:
+        raise GtError("gt_qk_norm_fwd", rc)
+    return out_q, out_k
+
+
+def gt_qk_norm_bwd(dyq, dyk, q, k, gain_q, gain_k=None, freq=None, pos_q=None, pos_k=None, pairs: int = GT_ROT_HALVES,
+                   eps: float = 1e-6, dq=None, dk=None, dgain_q=None, dgain_k=None, workspace=None, stream=None):
+    """Backward of gt_qk_norm_fwd from dyq and dyk (one type) and the forward's inputs: (dq, dk, dgain_q, dgain_k), dq
+    and dk of q's type, the gains' gradients fp32 [d].  dyk and k may be None."""
+    if not _is_here(q, stream):
+        return _elsewhere(gt_qk_norm_bwd, q, stream, (dyq, dyk, q, k, gain_q, gain_k, freq, pos_q, pos_k, pairs, eps, dq, dk,
+                                                      dgain_q, dgain_k, workspace))
+    lib = _lib or load_library()
+    nq, h, d = _three_dims("q", q)
+    xt, yt, dev = q.dtype, dyq.dtype, q.device
+    fp, rot = _rotation(freq, d, dev)
+    qv, gq = _heads("q", q, nq, h, d, xt, dev), _vector("gain_q", gain_q, d, dev)
+    dyqv = _heads("dyq", dyq, nq, h, d, yt, dev)
+    pq = None if pos_q is None else _ints("pos_q", pos_q, nq, dev)
+    dq, dqv = _heads_result("dq", dq, nq, h, d, xt, dev)
+    dgain_q, dgq = _result("dgain_q", dgain_q, d, dev)
+    keys = (1, 1, None, 0, 0, None, 0, 0, None, None, None, 0, 0, None)
+    if k is not None:
+        if dyk is None:
+            raise ValueError("k comes with dyk")
+        nk, hk, _ = _three_dims("k", k)
+        kv, gk = _heads("k", k, nk, hk, d, xt, dev), _vector("gain_k", gain_k, d, dev)
+        dykv = _heads("dyk", dyk, nk, hk, d, yt, dev)
+        pk = None if pos_k is None else _ints("pos_k", pos_k, nk, dev)
+        dk, dkv = _heads_result("dk", dk, nk, hk, d, xt, dev)
+        dgain_k, dgk = _result("dgain_k", dgain_k, d, dev)
+        keys = (nk, hk, *dykv, *kv, gk, pk, *dkv, dgk)
+    elif any(t is not None for t in (dyk, gain_k, pos_k, dk, dgain_k)):
+        raise ValueError("dyk, gain_k, pos_k, dk and dgain_k belong to k")
+    workspace, wp, wn = _room(workspace, _qk_room(dev.index, d), dev)
+    rc = lib.gt_qk_norm_bwd(_type_code("q", q), _type_code("dyq", dyq), d, eps, fp, rot, pairs, nq, h, *dyqv, *qv, gq, pq,
+                            *dqv, dgq, *keys, wp, wn, _raw_stream(dev.index))
+    if rc:
+        raise GtError("gt_qk_norm_bwd", rc)
+    return dq, dk, dgain_q, dgain_k
+
+
+class _Grad(ctypes.Structure):
+    """gt_grad of the C ABI."""
+    _fields_ = [("g", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64), ("gtype", ctypes.c_int32),
+                ("otype", ctypes.c_int32)]
+
+
+def _dense(t):
+    """Whether t's elements fill a piece of memory, in whatever order."""
+    if t.is_contiguous():
+        return True
+    need = 1
+    for stride, size in sorted((st, n) for st, n in zip(t.stride(), t.shape) if n > 1):
+        if stride != need:
+            return False
+        need *= size
+    return True
+
+
+class TensorList:
+    """The gradients of a step, and where their clipped values go, laid out for gt_grad_clip once (gt_tensor_list).  It
+    holds the memory that the tensors have now."""
+
+    def __init__(self, grads, out=None):
+        grads = [t.detach() for t in grads]
+        out = grads if out is None else [t.detach() for t in out]
+        if not grads or len(out) != len(grads):
+            raise ValueError("gt_tensor_list needs at least one gradient, and as many outputs")
+        device = grads[0].device
+        table = (_Grad * len(grads))()
+        for i, (g, o) in enumerate(zip(grads, out)):
+            if not g.is_cuda:
+                raise ValueError("libgt works on CUDA tensors only")
+            if g.device != device or o.device != device:
+                raise ValueError(f"gradient {i} and its output must be on {device}")
+            if o.shape != g.shape or (o.stride() != g.stride() and not (g.is_contiguous() and o.is_contiguous())):
+                raise ValueError(f"output {i} must have its gradient's shape and strides")
+            if not _dense(g):
+                raise ValueError(f"the elements of gradient {i} must fill one piece of memory")
+            p, q = g.data_ptr(), o.data_ptr()
+            if p == q and p and g.dtype != o.dtype:
+                raise ValueError(f"output {i} is its gradient in another type")
+            table[i] = _Grad(p, q, g.numel(), _type_code(f"gradient {i}", g), _type_code(f"output {i}", o))
+        self.grads, self.out, self.device, self.table, self.count = grads, out, device, table, len(grads)
+        self.address = ctypes.addressof(table)
+
+
+def gt_tensor_list(grads, out=None) -> TensorList:
+    """The handle that gt_grad_clip takes instead of lists, for programs whose gradients stay where they are."""
+    return TensorList(grads, out)
+
+
+@functools.lru_cache(maxsize=256)
+def _clip_room(device_index, count):
+    return int(load_library().gt_grad_clip_workspace_size(count))
+
+
+def gt_grad_clip_workspace_size(count: int) -> int:
+    """Workspace bytes of gt_grad_clip over `count` tensors."""
+    return 0 if count > _MOST else int(load_library().gt_grad_clip_workspace_size(count))
+
+
+def _grad_clip(tensors, max_norm, norm, workspace):
+    lib = _lib or load_library()
+    dev = tensors.device
+    norm, np_ = _result("norm", norm, 1, dev)
+    workspace, wp, wn = _room(workspace, _clip_room(dev.index, tensors.count), dev)
+    rc = lib.gt_grad_clip(tensors.address, tensors.count, max_norm, np_, wp, wn, _raw_stream(dev.index))
+    if rc:
+        raise GtError("gt_grad_clip", rc)
+    return (norm,)
+
+
+def gt_grad_clip(grads, max_norm: float, out=None, norm=None, workspace=None, stream=None):
+    """Norm fp32 [1] of all gradients together (a list of fp32 and bf16 tensors, or a gt_tensor_list), which are scaled
+    to max_norm in place, or into `out`, where the norm exceeds it.  max_norm = inf only measures."""
+    if isinstance(grads, TensorList):
+        if out is not None:
+            raise ValueError("a gt_tensor_list has its outputs already")
+        tensors = grads
+    else:
+        tensors = TensorList(grads, out)
+    if stream is None and tensors.device.index == _current_device():
+        return _grad_clip(tensors, max_norm, norm, workspace)[0]
+    if stream is not None and stream.device == tensors.device:
+        for t in (*tensors.grads, *tensors.out):
+            t.record_stream(stream)
+    return _elsewhere(_grad_clip, tensors.grads[0], stream, (tensors, max_norm, norm, workspace))[0]
 
 
 def gt_check_device_status(stream=None) -> None:

@@ -1,0 +1,407 @@
+// gt_cross_attn.cu -- entry points of cross attention: checks, workspace, how a call is split over the SMs, and the small
+// kernels around the products.
+//
+//   cross_stats   D = <dO, o> and lse log2 e of every query and head, in the order of the tiles' rows
+//   cross_join    o and lse from the parts of a split forward, exactly: weights exp(lse_part - lse)
+//   cross_sum     the sum of a split backward's parts, in their order
+//   cross_pack    rows that TMA cannot read (a base or stride that is no multiple of 16 bytes, or a stride of 0) as padded
+//                 rows in the workspace
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "gt_cross.cuh"
+#include "gt_stats.cuh"
+
+namespace gt {
+namespace cross {
+namespace {
+
+using bf16 = __nv_bfloat16;
+constexpr int kThreads = 256;
+
+// Eight lanes to a query and head.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) cross_stats(const Shape S, const View o, const View dO, const float* __restrict__ lse,
+                                                        float2* __restrict__ stats, int vec) {
+    const int64_t item = (int64_t)blockIdx.x * (kThreads / 8) + (threadIdx.x >> 3);
+    const int part = threadIdx.x & 7;
+    const bool live = item < (int64_t)S.nq * S.h;
+    float sum = 0.f;
+    int64_t query = 0;
+    int head = 0;
+    if (live) {
+        query = item / S.h;
+        head = (int)(item - query * S.h);
+        const T* a = static_cast<const T*>(o.p) + query * o.row + head * o.head;
+        const T* b = static_cast<const T*>(dO.p) + query * dO.row + head * dO.head;
+        for (int c = part * 8; c < S.d; c += 64) {
+            float x[8], y[8];
+            unpack8(load8(a + c, S.d - c, vec), x);
+            unpack8(load8(b + c, S.d - c, vec), y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum = fmaf(x[i], y[i], sum);
+        }
+    }
+#pragma unroll
+    for (int k = 4; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+    if (live && part == 0) {
+        const float l = __ldg(lse + (int64_t)head * S.nq + query);
+        // a query without a key: every p and dS is 0, o (and D) of no matter
+        const bool none = l == -INFINITY;
+        stats[((int64_t)(head / S.g) * S.nq + query) * S.g + head % S.g] =
+            make_float2(none ? INFINITY : l * tc::kLog2e, none ? 0.f : sum);
+    }
+}
+
+// The rows of the sequences: [first, end)
+__device__ __forceinline__ bool in_batch(const int32_t* off, int batch, int n, int64_t row) {
+    return !off || (row >= clamp_off(off, 0, n) && row < clamp_off(off, batch, n));
+}
+
+constexpr int kJoinLanes = 16;
+template <typename T>
+__global__ void __launch_bounds__(kThreads) cross_join(const Shape S, const FwdOut out) {
+    const int64_t item = (int64_t)blockIdx.x * (kThreads / kJoinLanes) + threadIdx.x / kJoinLanes;
+    const int part = threadIdx.x % kJoinLanes;
+    if (item >= (int64_t)S.nq * S.h) return;
+    const int64_t query = item / S.h;
+    const int head = (int)(item - query * S.h);
+    if (!in_batch(S.q_off, S.batch, S.nq, query)) return;
+    const float* lp = out.lse_part + (int64_t)head * S.nq + query;
+    const int64_t step = (int64_t)S.h * S.nq;
+    float top = -INFINITY;
+    for (int z = 0; z < out.splits; ++z) top = fmaxf(top, __ldcg(lp + z * step));
+    float sum = 0.f;
+    for (int z = 0; z < out.splits; ++z) {
+        const float l = __ldcg(lp + z * step);
+        if (l != -INFINITY) sum += expf(l - top);      // (a NaN is not lost)
+    }
+    const bool seen = sum != 0.f;
+    if (part == 0) out.lse[(int64_t)head * S.nq + query] = seen ? top + logf(sum) : -INFINITY;
+    const float inv = seen ? 1.f / sum : 0.f;
+    T* o = static_cast<T*>(out.o.p) + query * out.o.row + head * out.o.head;
+    for (int c = part * 8; c < S.d; c += 8 * kJoinLanes) {
+        float acc[8] = {};
+        for (int z = 0; z < out.splits; ++z) {
+            const float l = __ldcg(lp + z * step);
+            if (l == -INFINITY) continue;      // nothing was written for this part
+            const float w = expf(l - top) * inv;
+            float x[8];
+            unpack8(load8<Mem::kOutput>(out.o_part + ((z * (int64_t)S.nq + query) * S.h + head) * S.d + c, S.d - c,
+                                        S.d % 4 == 0 ? 1 : 0),
+                    x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, x[i], acc[i]);
+        }
+        store8(o + c, acc, S.d - c, out.o.acc);
+    }
+}
+
+// One result of a split backward: [parts][rows][heads][d] summed into out; two at once (dk and dv) by blockIdx.y.
+struct SumJob {
+    const float* part;
+    Out out;
+};
+template <typename T>
+__global__ void __launch_bounds__(kThreads) cross_sum(const SumJob j0, const SumJob j1, const int32_t* off, int batch, int rows,
+                                                      int heads, int d, int parts) {
+    const SumJob& J = blockIdx.y == 0 ? j0 : j1;
+    const int pieces = (d + 7) / 8;
+    const int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x, item = at / pieces;
+    if (item >= (int64_t)rows * heads) return;
+    const int c = (int)(at - item * pieces) * 8;
+    const int64_t row = item / heads;
+    const int head = (int)(item - row * heads);
+    if (!in_batch(off, batch, rows, row)) return;
+    float acc[8] = {};
+    const float* p = J.part + item * d + c;
+    const int64_t step = (int64_t)rows * heads * d;
+    for (int z = 0; z < parts; ++z) {
+        float x[8];
+        unpack8(load8<Mem::kOutput>(p + z * step, d - c, d % 4 == 0 ? 1 : 0), x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] += x[i];
+    }
+    store8(static_cast<T*>(J.out.p) + row * J.out.row + head * J.out.head + c, acc, d - c, J.out.acc);
+}
+
+// dst: [rows][heads][dp], zeros past d
+struct PackJob {
+    View src;
+    bf16* dst;
+    int rows, heads;
+};
+struct PackJobs {
+    PackJob j[4];
+    int d, dp;
+};
+__global__ void __launch_bounds__(kThreads) cross_pack(const PackJobs P) {
+    const PackJob& J = P.j[blockIdx.y];
+    const int pieces = P.dp / 8;
+    const int64_t all = (int64_t)J.rows * J.heads * pieces;
+    for (int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x; at < all; at += (int64_t)gridDim.x * kThreads) {
+        const int64_t item = at / pieces, row = item / J.heads;
+        const int c = (int)(at - item * pieces) * 8, head = (int)(item - row * J.heads);
+        const unsigned short* s = static_cast<const unsigned short*>(J.src.p) + row * J.src.row + head * J.src.head + c;
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = c + i < P.d ? (uint32_t)__ldg(s + i) : 0u;
+        *reinterpret_cast<uint4*>(J.dst + at * 8) =
+            make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16));
+    }
+}
+
+// ------------------------------------------------------------------------------------------- plans
+
+int width_of(int d) { return (d + 7) / 8 * 8; }
+
+// Whether TMA reads the rows as they are.
+bool tma_rows(const View& v) {
+    return aligned16(v.p) && v.row % 8 == 0 && v.head % 8 == 0 && v.row > 0 && v.head > 0 &&
+           v.row < ((int64_t)1 << 38) && v.head < ((int64_t)1 << 38);
+}
+
+// Parts into which the streamed side is cut so that `ctas` tiles fill the SMs, each of at least `least` steps.
+int parts_for(int64_t ctas, int per_sm, int64_t steps, int least) {
+    const int64_t want = (int64_t)per_sm * num_sms();
+    int64_t parts = ctas >= want ? 1 : want / std::max<int64_t>(1, ctas);
+    parts = std::min<int64_t>(parts, std::max<int64_t>(1, steps / least));
+    return (int)std::min<int64_t>(parts, kMaxSplits);
+}
+
+int64_t tiles_of(int n, int batch, int rows) { return std::max<int64_t>(batch, ((int64_t)n + rows - 1) / rows); }
+
+struct Plan {
+    int fwd, dq, dkv;      // parts
+};
+
+Plan plan_of(const Shape& S, bool f32) {
+    Plan p;
+    if (f32) {
+        const int tq = tile_queries(64, S.g);
+        const int64_t qt = tiles_of(S.nq, S.batch, tq) * S.hk, kt = tiles_of(S.nk, S.batch, 64) * S.hk;
+        p.fwd = parts_for(qt, 2, S.nk / S.batch / 64, 2);
+        p.dq = parts_for(qt, 2, S.nk / S.batch / 64, 2);
+        p.dkv = parts_for(kt, 2, S.nq / S.batch / tq, 2);
+    } else {
+        const int keys = S.d <= 64 ? 128 : 64;
+        const int64_t qt = tiles_of(S.nq, S.batch, tile_queries(128, S.g)) * S.hk, kt = tiles_of(S.nk, S.batch, 128) * S.hk;
+        p.fwd = parts_for(qt, S.batch > 1 ? 4 : 2, S.nk / S.batch / keys, 4);
+        p.dq = parts_for(qt, S.batch > 1 ? 4 : 2, S.nk / S.batch / 64, 4);
+        p.dkv = parts_for(kt, S.d <= 64 ? 2 : 1, S.nq / S.batch / tile_queries(64, S.g), 4);
+    }
+    return p;
+}
+
+struct Room {
+    float *o_part, *lse_part, *dq_part, *dk_part, *dv_part;
+    float2* stats;
+    bf16 *q, *k, *v, *dO;
+};
+
+// The workspace of a call; pack[]: which of q, k, v, dO are copied
+Room carve(Carve& cv, const Shape& S, const Plan& p, bool bwd, const bool (&pack)[4]) {
+    Room r = {};
+    const size_t nqh = (size_t)S.nq * S.h, nkh = (size_t)S.nk * S.hk, d = S.d, dp = width_of(S.d);
+    if (!bwd && p.fwd > 1) {
+        r.o_part = cv.take<float>(p.fwd * nqh * d);
+        r.lse_part = cv.take<float>(p.fwd * nqh);
+    }
+    if (bwd) {
+        r.stats = cv.take<float2>(nqh);
+        if (p.dq > 1) r.dq_part = cv.take<float>(p.dq * nqh * d);
+        if (p.dkv > 1) {
+            r.dk_part = cv.take<float>(p.dkv * nkh * d);
+            r.dv_part = cv.take<float>(p.dkv * nkh * d);
+        }
+    }
+    if (pack[0]) r.q = cv.take<bf16>(nqh * dp);
+    if (pack[1]) r.k = cv.take<bf16>(nkh * dp);
+    if (pack[2]) r.v = cv.take<bf16>(nkh * dp);
+    if (pack[3]) r.dO = cv.take<bf16>(nqh * dp);
+    return r;
+}
+
+bool valid_type(int t) { return t == GT_F32 || t == GT_BF16; }
+
+int check_sizes(int dtype, int nq, int nk, int h, int hk, int d, int batch) {
+    if (!valid_type(dtype) || nq < 1 || nk < 1 || h < 1 || hk < 1 || d < 1 || batch < 1 || h % hk) return GT_ERR_INVALID_ARG;
+    if (d > kMaxD || h > kMaxHeads || h / hk > kMaxShare || batch > (1 << 20) || nq > (1 << 30) || nk > (1 << 30))
+        return GT_ERR_UNSUPPORTED;
+    return GT_OK;
+}
+
+Shape shape_of(int nq, int nk, int h, int hk, int d, int batch, const int32_t* q_off, const int32_t* kv_off,
+               const uint8_t* mask, float scale) {
+    return Shape{nq, nk, h, hk, h / hk, d, batch, q_off, kv_off, mask, scale};
+}
+
+int check_shape(const Shape& S) {
+    if ((S.q_off != nullptr) != (S.kv_off != nullptr) || (!S.q_off && S.batch != 1)) return GT_ERR_INVALID_ARG;
+    return S.scale > 0.f && isfinite(S.scale) ? GT_OK : GT_ERR_INVALID_ARG;
+}
+
+bool usable(const View& v) { return v.p && v.row >= 0 && v.head >= 0; }
+
+Out out_of(void* p, int64_t row, int64_t head, int bytes) {
+    return Out{p, row, head, rows16(p, row, bytes) && rows16(p, head, bytes) ? 1 : 0};
+}
+
+// Copies the inputs that need it and points their views at the copies.
+int pack_inputs(const Shape& S, View* (&views)[4], bf16* (&room)[4], cudaStream_t s) {
+    PackJobs P = {};
+    P.d = S.d;
+    P.dp = width_of(S.d);
+    int count = 0;
+    int64_t most = 0;
+    for (int i = 0; i < 4; ++i) {
+        if (!room[i]) continue;
+        const bool query = i == 0 || i == 3;
+        const int rows = query ? S.nq : S.nk, heads = query ? S.h : S.hk;
+        P.j[count++] = PackJob{*views[i], room[i], rows, heads};
+        most = std::max<int64_t>(most, (int64_t)rows * heads * (P.dp / 8));
+        *views[i] = View{room[i], (int64_t)heads * P.dp, P.dp};
+    }
+    if (!count) return GT_OK;
+    LaunchScope ls("cross_pack", s);
+    const int64_t ctas = std::min<int64_t>((most + kThreads - 1) / kThreads, 16 * (int64_t)num_sms());
+    cross_pack<<<dim3((unsigned)ctas, count), kThreads, 0, s>>>(P);
+    return check_launch();
+}
+
+template <typename T>
+int sum_parts(const SumJob& a, const SumJob& b, int jobs, const int32_t* off, int batch, int rows, int heads, int d, int parts,
+              cudaStream_t s) {
+    LaunchScope ls("cross_sum", s);
+    const int64_t all = (int64_t)rows * heads * ((d + 7) / 8);
+    cross_sum<T><<<dim3((unsigned)((all + kThreads - 1) / kThreads), jobs), kThreads, 0, s>>>(a, b, off, batch, rows, heads, d,
+                                                                                          parts);
+    return check_launch();
+}
+
+template <typename T>
+int run_bwd(Shape S, const Plan& plan, const Room& r, BwdIn in, const View& o, const float* lse, const Out& dq, const Out& dk,
+            const Out& dv, cudaStream_t s) {
+    constexpr bool F32 = sizeof(T) == 4;
+    {
+        LaunchScope ls("cross_stats", s);
+        const int64_t items = (int64_t)S.nq * S.h;
+        const int vec = rows16(o.p, o.row, sizeof(T)) && rows16(o.p, o.head, sizeof(T)) && rows16(in.dO.p, in.dO.row, sizeof(T)) &&
+                        rows16(in.dO.p, in.dO.head, sizeof(T));
+        cross_stats<T><<<(unsigned)((items + kThreads / 8 - 1) / (kThreads / 8)), kThreads, 0, s>>>(S, o, in.dO, lse, r.stats, vec);
+        const int rc = check_launch();
+        if (rc != GT_OK) return rc;
+    }
+    in.stats = r.stats;
+    int rc;
+    if constexpr (!F32) {
+        View* views[4] = {&in.q, &in.k, &in.v, &in.dO};
+        bf16* room[4] = {r.q, r.k, r.v, r.dO};
+        rc = pack_inputs(S, views, room, s);
+        if (rc != GT_OK) return rc;
+    }
+    rc = F32 ? bwd_dq_f32(S, in, dq, r.dq_part, plan.dq, s) : bwd_dq_tc(S, in, dq, r.dq_part, plan.dq, s);
+    if (rc != GT_OK) return rc;
+    rc = F32 ? bwd_dkv_f32(S, in, dk, dv, r.dk_part, r.dv_part, plan.dkv, s)
+             : bwd_dkv_tc(S, in, dk, dv, r.dk_part, r.dv_part, plan.dkv, s);
+    if (rc != GT_OK) return rc;
+    if (plan.dq > 1) {
+        const SumJob j{r.dq_part, dq};
+        rc = sum_parts<T>(j, j, 1, S.q_off, S.batch, S.nq, S.h, S.d, plan.dq, s);
+        if (rc != GT_OK) return rc;
+    }
+    if (plan.dkv > 1)
+        rc = sum_parts<T>(SumJob{r.dk_part, dk}, SumJob{r.dv_part, dv}, 2, S.kv_off, S.batch, S.nk, S.hk, S.d, plan.dkv, s);
+    return rc;
+}
+
+}  // namespace
+}  // namespace cross
+}  // namespace gt
+
+extern "C" {
+
+size_t gt_cross_attn_workspace_size(int32_t dtype, int32_t nq, int32_t nk, int32_t h, int32_t hk, int32_t d, int32_t batch,
+                                    int32_t backward, int32_t aligned) {
+    using namespace gt::cross;
+    if (check_sizes(dtype, nq, nk, h, hk, d, batch) != GT_OK) return 0;
+    const Shape S = shape_of(nq, nk, h, hk, d, batch, nullptr, nullptr, nullptr, 1.f);
+    const bool copies = dtype == GT_BF16 && !aligned;
+    gt::Carve cv(nullptr, 0);
+    const bool pack[4] = {copies, copies, copies, copies && backward};
+    carve(cv, S, plan_of(S, dtype == GT_F32), backward != 0, pack);
+    return cv.off == 0 ? 0 : cv.off + 256;
+}
+
+int gt_cross_attn_fwd(int32_t dtype, int32_t nq, int32_t nk, int32_t h, int32_t hk, int32_t d, int32_t batch, const void* q,
+                      int64_t ldq, int64_t hdq, const void* k, int64_t ldk, int64_t hdk, const void* v, int64_t ldv,
+                      int64_t hdv, const int32_t* q_off, const int32_t* kv_off, const uint8_t* key_mask, float scale, void* o,
+                      int64_t ldo, int64_t hdo, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+    using namespace gt::cross;
+    int rc = check_sizes(dtype, nq, nk, h, hk, d, batch);
+    if (rc != GT_OK) return rc;
+    const Shape S = shape_of(nq, nk, h, hk, d, batch, q_off, kv_off, key_mask, scale);
+    rc = check_shape(S);
+    if (rc != GT_OK) return rc;
+    View qv{q, ldq, hdq}, kv{k, ldk, hdk}, vv{v, ldv, hdv};
+    if (!usable(qv) || !usable(kv) || !usable(vv) || !o || !lse || ldo < 0 || hdo < 0) return GT_ERR_INVALID_ARG;
+    const bool f32 = dtype == GT_F32;
+    const Plan plan = plan_of(S, f32);
+    const bool pack[4] = {!f32 && !tma_rows(qv), !f32 && !tma_rows(kv), !f32 && !tma_rows(vv), false};
+    gt::Carve cv(workspace, ws_bytes);
+    const Room r = carve(cv, S, plan, false, pack);
+    if (cv.off > 0 && (!workspace || !gt::aligned16(workspace) || !cv.fits())) return GT_ERR_WORKSPACE;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const FwdOut out{out_of(o, ldo, hdo, f32 ? 4 : 2), lse, r.o_part, r.lse_part, plan.fwd};
+    if (f32) {
+        rc = fwd_f32(S, qv, kv, vv, out, s);
+    } else {
+        View* views[4] = {&qv, &kv, &vv, nullptr};
+        bf16* room[4] = {r.q, r.k, r.v, nullptr};
+        rc = pack_inputs(S, views, room, s);
+        if (rc == GT_OK) rc = fwd_tc(S, qv, kv, vv, out, s);
+    }
+    if (rc != GT_OK || plan.fwd == 1) return rc;
+    gt::LaunchScope ls("cross_join", s);
+    const int64_t items = (int64_t)nq * h;
+    const unsigned ctas = (unsigned)((items + kThreads / kJoinLanes - 1) / (kThreads / kJoinLanes));
+    if (f32) cross_join<float><<<ctas, kThreads, 0, s>>>(S, out);
+    else cross_join<bf16><<<ctas, kThreads, 0, s>>>(S, out);
+    return gt::check_launch();
+}
+
+int gt_cross_attn_bwd(int32_t dtype, int32_t nq, int32_t nk, int32_t h, int32_t hk, int32_t d, int32_t batch, const void* q,
+                      int64_t ldq, int64_t hdq, const void* k, int64_t ldk, int64_t hdk, const void* v, int64_t ldv,
+                      int64_t hdv, const void* o, int64_t ldo, int64_t hdo, const void* dO, int64_t lddo, int64_t hddo,
+                      const float* lse, const int32_t* q_off, const int32_t* kv_off, const uint8_t* key_mask, float scale,
+                      void* dq, int64_t lddq, int64_t hddq, void* dk, int64_t lddk, int64_t hddk, void* dv, int64_t lddv,
+                      int64_t hddv, void* workspace, size_t ws_bytes, void* stream) {
+    using namespace gt::cross;
+    int rc = check_sizes(dtype, nq, nk, h, hk, d, batch);
+    if (rc != GT_OK) return rc;
+    const Shape S = shape_of(nq, nk, h, hk, d, batch, q_off, kv_off, key_mask, scale);
+    rc = check_shape(S);
+    if (rc != GT_OK) return rc;
+    const View ov{o, ldo, hdo};
+    BwdIn in{View{q, ldq, hdq}, View{k, ldk, hdk}, View{v, ldv, hdv}, View{dO, lddo, hddo}, nullptr};
+    if (!usable(in.q) || !usable(in.k) || !usable(in.v) || !usable(in.dO) || !usable(ov) || !lse || !dq || !dk || !dv ||
+        lddq < 0 || hddq < 0 || lddk < 0 || hddk < 0 || lddv < 0 || hddv < 0)
+        return GT_ERR_INVALID_ARG;
+    const bool f32 = dtype == GT_F32;
+    const int e = f32 ? 4 : 2;
+    const Plan plan = plan_of(S, f32);
+    const bool pack[4] = {!f32 && !tma_rows(in.q), !f32 && !tma_rows(in.k), !f32 && !tma_rows(in.v),
+                          !f32 && !tma_rows(in.dO)};
+    gt::Carve cv(workspace, ws_bytes);
+    const Room r = carve(cv, S, plan, true, pack);
+    if (!workspace || !gt::aligned16(workspace) || !cv.fits()) return GT_ERR_WORKSPACE;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const Out oq = out_of(dq, lddq, hddq, e), ok = out_of(dk, lddk, hddk, e), okv = out_of(dv, lddv, hddv, e);
+    return f32 ? run_bwd<float>(S, plan, r, in, ov, lse, oq, ok, okv, s) : run_bwd<bf16>(S, plan, r, in, ov, lse, oq, ok, okv, s);
+}
+
+}  // extern "C"

@@ -1,0 +1,508 @@
+// gt_cross_bwd.cu -- cross attention backward, bf16, on the tensor cores: dq by CTAs that hold a tile of queries, dk
+// and dv by CTAs that hold a tile of keys.  Two kernels, seven products where one with sums in memory takes five: no
+// result depends on the order in which CTAs finish.
+//
+// In both the scores and dP are formed again tile by tile, p = exp(s - lse) and dS = p (dP - D) by warps that have a row
+// each, and p and dS go back to TMEM as bf16 operands (half a step, 2^-9, of each entry, independent from one to the
+// next).  The scores' scale comes last: dq = scale (dS k), dk = scale (dS^T q).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "gt_cross_tc.cuh"
+
+namespace gt {
+namespace cross {
+namespace {
+
+constexpr int kHeld = 128;      // rows a CTA holds
+constexpr int kStep = 64;       // rows of a streamed tile
+constexpr uint32_t kHeldPanel = kHeld * 128, kStepPanel = kStep * 128;
+
+// ---------------------------------------------------------------------------- dq
+
+template <int PANELS>
+struct DqCfg {
+    static constexpr int kStages = PANELS == 1 ? 3 : 1;
+    static constexpr uint32_t kHeldBytes = PANELS * kHeldPanel, kStepBytes = PANELS * kStepPanel;
+    static constexpr size_t kSmem = 1024 + 2 * kHeldBytes + 2 * kStages * kStepBytes;
+    // TMEM columns: S at 0, dP at 64, dq at 128; dS beside them where there is room, else over S
+    static constexpr bool kOver = PANELS == 2;
+    static constexpr uint32_t kDp = 64, kAcc = 128, kDs = kOver ? 0 : 192, kTmem = 256;
+    static constexpr int kThreads = 192, kTmaWarp = 4, kMmaWarp = 5;
+};
+
+struct DqBars {
+    uint64_t held_full, k_full[3], k_empty[3], v_full[3], v_empty[3];
+    uint64_t s_full, s_free, ds_full, acc_done, fin;
+    uint32_t tmem_base;
+    int abort;
+};
+
+template <int PANELS>
+__global__ void __launch_bounds__(DqCfg<PANELS>::kThreads, 2)
+cross_dq(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
+         const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+         const float2* __restrict__ stats, const Out dq, float* __restrict__ part, const int splits, int* status) {
+    using C = DqCfg<PANELS>;
+    constexpr int kStages = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    __shared__ DqBars bars;
+    const int tq = tile_queries(kHeld, S.g), head = blockIdx.y, z = blockIdx.z;
+    const Tile t = find_tile(S, true, tq, blockIdx.x);
+    if (!t.live) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int first = t.tile * tq, live = min(tq, t.lq - first) * S.g;
+    const int tiles = (t.lk + kStep - 1) / kStep;
+    const int t0 = part_begin(tiles, z, splits), n = part_begin(tiles, z + 1, splits) - t0;
+    const int steps = (S.d + 15) / 16;
+    uint8_t* sq = smem;
+    uint8_t* sdo = sq + C::kHeldBytes;
+    uint8_t* sk = sdo + C::kHeldBytes;
+    uint8_t* sv = sk + kStages * C::kStepBytes;
+    if (threadIdx.x == C::kTmaWarp * 32) {
+        mbar_init(&bars.held_full, 1);
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&bars.k_full[s], 1);
+            mbar_init(&bars.k_empty[s], 1);
+            mbar_init(&bars.v_full[s], 1);
+            mbar_init(&bars.v_empty[s], 1);
+        }
+        mbar_init(&bars.s_full, 1);
+        mbar_init(&bars.s_free, 4);
+        mbar_init(&bars.ds_full, 4);
+        mbar_init(&bars.acc_done, 1);
+        mbar_init(&bars.fin, 1);
+        bars.abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == C::kMmaWarp) tmem_alloc(&bars.tmem_base, C::kTmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tb = bars.tmem_base;
+    Waits w{&bars.abort, true};
+
+    if (warp == C::kTmaWarp) {
+        if (n > 0) {
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&bars.held_full, 2 * PANELS * tq * S.g * 128);
+                load_panels<PANELS>(sq, kHeldPanel, &map_q, head * S.g, t.q0 + first, &bars.held_full);
+                load_panels<PANELS>(sdo, kHeldPanel, &map_do, head * S.g, t.q0 + first, &bars.held_full);
+            }
+            __syncwarp();
+        }
+        int i = 0;
+        for (; i < n; ++i) {
+            const int s = i % kStages, row = t.k0 + (t0 + i) * kStep;
+            const uint32_t parity = ((i / kStages) & 1) ^ 1;
+            if (!w.all(&bars.v_empty[s], parity) || !w.all(&bars.k_empty[s], parity)) break;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&bars.k_full[s], C::kStepBytes);
+                load_panels<PANELS>(sk + s * C::kStepBytes, kStepPanel, &map_k, head, row, &bars.k_full[s]);
+                mbar_arrive_expect_tx(&bars.v_full[s], C::kStepBytes);
+                load_panels<PANELS>(sv + s * C::kStepBytes, kStepPanel, &map_v, head, row, &bars.v_full[s]);
+            }
+            __syncwarp();
+        }
+        if (!w.ok && lane == 0) tc::fail(&bars.abort, status);
+        int never = 0;      // nothing may still be on its way into shared memory when the CTA ends
+        if (n > 0) mbar_wait_all(&bars.held_full, 0, &never, tc::kWaitNs);
+        for (int b = max(0, i - kStages); b < i; ++b) {
+            mbar_wait_all(&bars.k_full[b % kStages], (b / kStages) & 1, &never, tc::kWaitNs);
+            mbar_wait_all(&bars.v_full[b % kStages], (b / kStages) & 1, &never, tc::kWaitNs);
+        }
+    } else if (warp == C::kMmaWarp) {
+        const uint32_t id_s = idesc_bf16(kHeld, kStep, false, false), id_acc = idesc_bf16(kHeld, 16 * steps, false, true);
+        const SmemDesc a_q = smem_desc_split(smem_u32(sq), 16, 1024, 2), a_do = smem_desc_split(smem_u32(sdo), 16, 1024, 2);
+        auto gradients = [&](int i) {      // dq += dS k of tile i
+            const int s = i % kStages;
+            if (!w.all(&bars.ds_full, i & 1)) return;
+            tc_fence_after();
+            const SmemDesc b_k = smem_desc_split(smem_u32(sk + s * C::kStepBytes), kStepPanel, 1024, 2);
+            if (elect_one()) {
+                product_rows<kStep>(tb + C::kAcc, tb + C::kDs, b_k, id_acc, i > 0);
+                mma_commit(&bars.k_empty[s]);
+                mma_commit(&bars.acc_done);
+            }
+            __syncwarp();
+        };
+        if (n > 0) w.all(&bars.held_full, 0);
+        for (int i = 0; i < n && w.ok; ++i) {
+            const int s = i % kStages;
+            if (C::kOver && i > 0) {      // dS of the last tile stands where these scores will
+                gradients(i - 1);
+                w.all(&bars.acc_done, (i - 1) & 1);
+            }
+            if (!w.all(&bars.k_full[s], (i / kStages) & 1) || !w.all(&bars.v_full[s], (i / kStages) & 1)) break;
+            uint32_t words[kStep / 32];
+            if (!valid_keys(S, t.k0 + (t0 + i) * kStep, t.k0 + t.lk, words))
+                clear_rows<kStep / 32, PANELS>(smem_u32(sk + s * C::kStepBytes), kStepPanel, words);
+            if (i > 0 && !w.all(&bars.s_free, (i - 1) & 1)) break;
+            tc_fence_after();
+            const SmemDesc b_k = smem_desc_split(smem_u32(sk + s * C::kStepBytes), 16, 1024, 2);
+            const SmemDesc b_v = smem_desc_split(smem_u32(sv + s * C::kStepBytes), 16, 1024, 2);
+            if (elect_one()) {
+                product_channels(tb, a_q, kHeldPanel, b_k, kStepPanel, steps, id_s);
+                product_channels(tb + C::kDp, a_do, kHeldPanel, b_v, kStepPanel, steps, id_s);
+                mma_commit(&bars.v_empty[s]);
+                mma_commit(&bars.s_full);
+            }
+            __syncwarp();
+            if (!C::kOver && i > 0) gradients(i - 1);
+        }
+        if (n > 0 && w.ok) gradients(n - 1);
+        if (!w.ok) {
+            if (lane == 0) tc::fail(&bars.abort, status);
+            int never = 0;
+            if (elect_one()) mma_commit(&bars.fin);
+            __syncwarp();
+            mbar_wait_all(&bars.fin, 0, &never, tc::kWaitNs);
+        }
+    } else {
+        const int r = warp * 32 + lane;
+        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        const bool some = warp * 32 < live, mine = r < live;
+        const float c = S.scale * tc::kLog2e;
+        const float2 st = mine ? __ldg(stats + ((int64_t)head * S.nq + t.q0 + first) * S.g + r) : make_float2(INFINITY, 0.f);
+        for (int i = 0; i < n; ++i) {
+            uint32_t words[kStep / 32];
+            const bool all = valid_keys(S, t.k0 + (t0 + i) * kStep, t.k0 + t.lk, words);
+            if (!w.all(&bars.s_full, i & 1)) break;
+            tc_fence_after();
+            uint32_t ds[2][16];
+            if (some) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t x[32], y[32];
+                    tmem_ld_x32(tb + lanes + 32 * k, x);
+                    tmem_ld_x32(tb + lanes + C::kDp + 32 * k, y);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        float e[2];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const float p = ex2(fmaf(__uint_as_float(x[j + u]), c, -st.x));
+                            e[u] = p * (__uint_as_float(y[j + u]) - st.y);
+                        }
+                        ds[k][j / 2] = pack_bf16x2(e[0], e[1]);
+                    }
+                    if (!all) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            ds[k][j] &= (((words[k] >> (2 * j)) & 1u) ? 0xffffu : 0u) |
+                                        (((words[k] >> (2 * j + 1)) & 1u) ? 0xffff0000u : 0u);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.s_free);
+            if (i > 0 && !w.all(&bars.acc_done, (i - 1) & 1)) break;      // the last dS has been read
+            if (some) {
+                tmem_st_x16(tb + lanes + C::kDs, ds[0]);
+                tmem_st_x16(tb + lanes + C::kDs + 16, ds[1]);
+                tmem_wait_st();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.ds_full);
+        }
+        if (n > 0 && w.ok) w.all(&bars.acc_done, (n - 1) & 1);
+        if (!w.ok && lane == 0) tc::fail(&bars.abort, status);
+        tc_fence_after();
+        if (some && w.ok) {
+            const int64_t query = t.q0 + first + r / S.g;
+            const int qh = head * S.g + r % S.g;
+            if (splits == 1) {
+                bf16* p = static_cast<bf16*>(dq.p) + query * dq.row + qh * dq.head;
+                if (n > 0) {
+                    tmem_row_out(tb + lanes + C::kAcc, steps, p, S.d, S.scale, mine, dq.acc);
+                } else if (mine) {
+                    const float zero[16] = {};
+                    for (int k = 0; k < steps; ++k) put16(p, 16 * k, S.d, zero, dq.acc);
+                }
+            } else {
+                float* p = part + ((z * (int64_t)S.nq + query) * S.h + qh) * S.d;
+                if (n > 0) {
+                    tmem_row_out(tb + lanes + C::kAcc, steps, p, S.d, S.scale, mine, S.d % 4 == 0 ? 1 : 0);
+                } else if (mine) {
+                    for (int k = 0; k < S.d; ++k) p[k] = 0.f;
+                }
+            }
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == C::kMmaWarp) tmem_dealloc(tb, C::kTmem);
+}
+
+// ---------------------------------------------------------------------------- dk, dv
+
+// Head dims up to 64: one group of four warps, 256 TMEM columns, two CTAs to an SM, each one's products beside the other's
+// arithmetic.  Above: two groups on alternate tiles, with scores of their own, and one CTA.
+template <int PANELS>
+struct DkvCfg {
+    static constexpr int kGroups = PANELS;
+    static constexpr int kStages = 3;
+    static constexpr uint32_t kHeldBytes = PANELS * kHeldPanel, kStepBytes = PANELS * kStepPanel;
+    static constexpr size_t kSmem = 1024 + 2 * kHeldBytes + 2 * kStages * kStepBytes;
+    // TMEM columns: a group's S and dP (p and dS over them), then dv, then dk
+    static constexpr uint32_t kDv = 128 * kGroups, kDk = kDv + 64 * PANELS, kTmem = 256 * PANELS;
+    static constexpr int kTmaWarp = 4 * kGroups, kMmaWarp = kTmaWarp + 1, kThreads = 32 * (kMmaWarp + 1);
+};
+
+struct DkvBars {
+    uint64_t held_full, q_full[3], q_empty[3];
+    uint64_t s_full[2], p_full[2], acc_done[2], fin;
+    uint32_t tmem_base;
+    int abort;
+};
+
+template <int PANELS>
+__global__ void __launch_bounds__(DkvCfg<PANELS>::kThreads, 3 - PANELS)
+cross_dkv(const Shape S, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+          const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
+          const float2* __restrict__ stats, const Out dk, const Out dv, float* __restrict__ dk_part,
+          float* __restrict__ dv_part, const int splits, int* status) {
+    using C = DkvCfg<PANELS>;
+    constexpr int kStages = C::kStages, kGroups = C::kGroups;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    __shared__ DkvBars bars;
+    __shared__ alignas(16) float2 st[kStages][kStep];
+    const int tq = tile_queries(kStep, S.g), head = blockIdx.y, z = blockIdx.z;
+    const Tile t = find_tile(S, false, kHeld, blockIdx.x);
+    if (!t.live) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int first = t.tile * kHeld;
+    const int tiles = (t.lq + tq - 1) / tq;
+    const int t0 = part_begin(tiles, z, splits), n = part_begin(tiles, z + 1, splits) - t0;
+    const int steps = (S.d + 15) / 16;
+    uint8_t* sk = smem;
+    uint8_t* sv = sk + C::kHeldBytes;
+    uint8_t* sq = sv + C::kHeldBytes;
+    uint8_t* sdo = sq + kStages * C::kStepBytes;
+    if (threadIdx.x == C::kTmaWarp * 32) {
+        mbar_init(&bars.held_full, 1);
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&bars.q_full[s], 1);
+            mbar_init(&bars.q_empty[s], 1);
+        }
+        for (int b = 0; b < kGroups; ++b) {
+            mbar_init(&bars.s_full[b], 1);
+            mbar_init(&bars.p_full[b], 4);
+            mbar_init(&bars.acc_done[b], 1);
+        }
+        mbar_init(&bars.fin, 1);
+        bars.abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == C::kMmaWarp) tmem_alloc(&bars.tmem_base, C::kTmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tb = bars.tmem_base;
+    Waits w{&bars.abort, true};
+    // rows of streamed tile i that exist
+    auto rows_of = [&](int i) { return min(tq, t.lq - (t0 + i) * tq) * S.g; };
+
+    if (warp == C::kTmaWarp) {
+        if (n > 0) {
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&bars.held_full, 2 * C::kHeldBytes);
+                load_panels<PANELS>(sk, kHeldPanel, &map_k, head, t.k0 + first, &bars.held_full);
+                load_panels<PANELS>(sv, kHeldPanel, &map_v, head, t.k0 + first, &bars.held_full);
+            }
+            __syncwarp();
+        }
+        int i = 0;
+        for (; i < n; ++i) {
+            const int s = i % kStages, q0 = t.q0 + (t0 + i) * tq, live = rows_of(i);
+            const float2* src = stats + ((int64_t)head * S.nq + q0) * S.g;
+            const float2 none = make_float2(INFINITY, 0.f);
+            const float2 a = lane < live ? __ldg(src + lane) : none, b = lane + 32 < live ? __ldg(src + lane + 32) : none;
+            if (!w.all(&bars.q_empty[s], ((i / kStages) & 1) ^ 1)) break;
+            st[s][lane] = a;
+            st[s][lane + 32] = b;
+            __syncwarp();
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&bars.q_full[s], 2 * PANELS * tq * S.g * 128);
+                load_panels<PANELS>(sq + s * C::kStepBytes, kStepPanel, &map_q, head * S.g, q0, &bars.q_full[s]);
+                load_panels<PANELS>(sdo + s * C::kStepBytes, kStepPanel, &map_do, head * S.g, q0, &bars.q_full[s]);
+            }
+            __syncwarp();
+        }
+        if (!w.ok && lane == 0) tc::fail(&bars.abort, status);
+        int never = 0;      // nothing may still be on its way into shared memory when the CTA ends
+        if (n > 0) mbar_wait_all(&bars.held_full, 0, &never, tc::kWaitNs);
+        for (int b = max(0, i - kStages); b < i; ++b)
+            mbar_wait_all(&bars.q_full[b % kStages], (b / kStages) & 1, &never, tc::kWaitNs);
+    } else if (warp == C::kMmaWarp) {
+        const uint32_t id_s = idesc_bf16(kHeld, kStep, false, false), id_acc = idesc_bf16(kHeld, 16 * steps, false, true);
+        const SmemDesc a_k = smem_desc_split(smem_u32(sk), 16, 1024, 2), a_v = smem_desc_split(smem_u32(sv), 16, 1024, 2);
+        auto gradients = [&](int i) {      // dv += p^T dO, dk += dS^T q of tile i
+            const int s = i % kStages, b = i % kGroups;
+            if (!w.all(&bars.p_full[b], (i / kGroups) & 1)) return;
+            tc_fence_after();
+            const SmemDesc b_q = smem_desc_split(smem_u32(sq + s * C::kStepBytes), kStepPanel, 1024, 2);
+            const SmemDesc b_do = smem_desc_split(smem_u32(sdo + s * C::kStepBytes), kStepPanel, 1024, 2);
+            if (elect_one()) {
+                product_rows<kStep>(tb + C::kDv, tb + 128 * b, b_do, id_acc, i > 0);
+                product_rows<kStep>(tb + C::kDk, tb + 128 * b + 64, b_q, id_acc, i > 0);
+                mma_commit(&bars.q_empty[s]);
+                mma_commit(&bars.acc_done[b]);
+            }
+            __syncwarp();
+        };
+        if (n > 0) w.all(&bars.held_full, 0);
+        for (int i = 0; i < n && w.ok; ++i) {
+            const int s = i % kStages, b = i % kGroups;
+            if (!w.all(&bars.q_full[s], (i / kStages) & 1)) break;
+            const int live = rows_of(i);
+            if (live < kStep) {      // the rows behind belong to the next sequence, or are nothing at all
+                clear_tail<PANELS>(smem_u32(sq + s * C::kStepBytes), kStepPanel, live, kStep);
+                clear_tail<PANELS>(smem_u32(sdo + s * C::kStepBytes), kStepPanel, live, kStep);
+            }
+            // p and dS of the group's last tile stand where these scores will
+            if (i >= kGroups && !w.all(&bars.acc_done[b], (i / kGroups - 1) & 1)) break;
+            tc_fence_after();
+            const SmemDesc b_q = smem_desc_split(smem_u32(sq + s * C::kStepBytes), 16, 1024, 2);
+            const SmemDesc b_do = smem_desc_split(smem_u32(sdo + s * C::kStepBytes), 16, 1024, 2);
+            if (elect_one()) {
+                product_channels(tb + 128 * b, a_k, kHeldPanel, b_q, kStepPanel, steps, id_s);
+                product_channels(tb + 128 * b + 64, a_v, kHeldPanel, b_do, kStepPanel, steps, id_s);
+                mma_commit(&bars.s_full[b]);
+            }
+            __syncwarp();
+            if (i >= kGroups - 1) gradients(i - kGroups + 1);
+        }
+        for (int i = max(0, n - kGroups + 1); i < n && w.ok; ++i) gradients(i);
+        if (!w.ok && lane == 0) tc::fail(&bars.abort, status);
+        int never = 0;
+        if (elect_one()) mma_commit(&bars.fin);      // all products
+        __syncwarp();
+        mbar_wait_all(&bars.fin, 0, &never, tc::kWaitNs);
+    } else {
+        const int group = warp >> 2, r = (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, ts = tb + lanes + 128 * group;
+        const float c = S.scale * tc::kLog2e;
+        for (int i = group; i < n; i += kGroups) {
+            const int s = i % kStages;
+            const uint32_t turn = (i / kGroups) & 1;
+            if (!w.all(&bars.q_full[s], (i / kStages) & 1) || !w.all(&bars.s_full[group], turn)) break;
+            tc_fence_after();
+            const uint32_t sst = smem_u32(st[s]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t x[32], y[32], p[16], ds[16];
+                tmem_ld_x32(ts + 32 * k, x);
+                tmem_ld_x32(ts + 64 + 32 * k, y);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                    const uint4 q4 = lds_u4(sst + 8 * (32 * k + j));     // lse and D of two queries
+                    const float pa = ex2(fmaf(__uint_as_float(x[j]), c, -__uint_as_float(q4.x)));
+                    const float pb = ex2(fmaf(__uint_as_float(x[j + 1]), c, -__uint_as_float(q4.z)));
+                    p[j / 2] = pack_bf16x2(pa, pb);
+                    ds[j / 2] = pack_bf16x2(pa * (__uint_as_float(y[j]) - __uint_as_float(q4.y)),
+                                            pb * (__uint_as_float(y[j + 1]) - __uint_as_float(q4.w)));
+                }
+                tmem_st_x16(ts + 16 * k, p);
+                tmem_st_x16(ts + 64 + 16 * k, ds);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.p_full[group]);
+        }
+        w.all(&bars.fin, 0);
+        if (!w.ok && lane == 0) tc::fail(&bars.abort, status);
+        tc_fence_after();
+        if (w.ok) {
+            const bool mine = first + r < t.lk;
+            const int64_t key = t.k0 + first + r;
+            const bool seen = n > 0 && mine && (!S.mask || __ldg(S.mask + key) != 0);
+            auto result = [&](const Out& g, float* part, uint32_t col, float by) {
+                const bool whole = splits == 1;
+                bf16* p = static_cast<bf16*>(g.p) + key * g.row + head * g.head;
+                float* f = part + ((z * (int64_t)S.nk + key) * S.hk + head) * S.d;
+                for (int k = 0; k < steps; ++k) {
+                    uint32_t o[16];
+                    if (n > 0) {
+                        tmem_ld_x16(tb + lanes + col + 16 * k, o);
+                        tmem_wait_ld();
+                    }
+                    float v[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = seen ? __uint_as_float(o[j]) * by : 0.f;
+                    if (mine && whole) put16(p, 16 * k, S.d, v, g.acc);
+                    else if (mine) put16(f, 16 * k, S.d, v, S.d % 4 == 0 ? 1 : 0);
+                }
+            };
+            if (group == 0) result(dv, dv_part, C::kDv, 1.f);
+            if (group == kGroups - 1) result(dk, dk_part, C::kDk, S.scale);
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == C::kMmaWarp) tmem_dealloc(tb, C::kTmem);
+}
+
+template <int PANELS>
+int launch_dq(const Shape& S, const BwdIn& in, const Out& dq, float* part, int splits, cudaStream_t s) {
+    using C = DqCfg<PANELS>;
+    CUtensorMap mq, mdo, mk, mv;
+    const int tq = tile_queries(kHeld, S.g);
+    if (!heads_map(&mq, in.q, S.nq, S.h, S.d, S.g, tq) || !heads_map(&mdo, in.dO, S.nq, S.h, S.d, S.g, tq) ||
+        !heads_map(&mk, in.k, S.nk, S.hk, S.d, 1, kStep) || !heads_map(&mv, in.v, S.nk, S.hk, S.d, 1, kStep))
+        return GT_ERR_CUDA;
+    int* status = device_status_ptr();
+    if (!status) return GT_ERR_CUDA;
+    static std::atomic<uint64_t> allowed;
+    if (!allow_smem(allowed, (const void*)cross_dq<PANELS>, C::kSmem)) return GT_ERR_CUDA;
+    LaunchScope ls("cross_dq", s);
+    cross_dq<PANELS><<<dim3(slots_of(S, true, tq), S.hk, splits), C::kThreads, C::kSmem, s>>>(S, mq, mdo, mk, mv, in.stats, dq,
+                                                                                              part, splits, status);
+    return check_launch();
+}
+
+template <int PANELS>
+int launch_dkv(const Shape& S, const BwdIn& in, const Out& dk, const Out& dv, float* dk_part, float* dv_part, int splits,
+               cudaStream_t s) {
+    using C = DkvCfg<PANELS>;
+    CUtensorMap mq, mdo, mk, mv;
+    const int tq = tile_queries(kStep, S.g);
+    if (!heads_map(&mq, in.q, S.nq, S.h, S.d, S.g, tq) || !heads_map(&mdo, in.dO, S.nq, S.h, S.d, S.g, tq) ||
+        !heads_map(&mk, in.k, S.nk, S.hk, S.d, 1, kHeld) || !heads_map(&mv, in.v, S.nk, S.hk, S.d, 1, kHeld))
+        return GT_ERR_CUDA;
+    int* status = device_status_ptr();
+    if (!status) return GT_ERR_CUDA;
+    static std::atomic<uint64_t> allowed;
+    if (!allow_smem(allowed, (const void*)cross_dkv<PANELS>, C::kSmem)) return GT_ERR_CUDA;
+    LaunchScope ls("cross_dkv", s);
+    cross_dkv<PANELS><<<dim3(slots_of(S, false, kHeld), S.hk, splits), C::kThreads, C::kSmem, s>>>(
+        S, mk, mv, mq, mdo, in.stats, dk, dv, dk_part, dv_part, splits, status);
+    return check_launch();
+}
+
+}  // namespace
+
+int bwd_dq_tc(const Shape& S, const BwdIn& in, const Out& dq, float* part, int splits, cudaStream_t s) {
+    return S.d <= 64 ? launch_dq<1>(S, in, dq, part, splits, s) : launch_dq<2>(S, in, dq, part, splits, s);
+}
+
+int bwd_dkv_tc(const Shape& S, const BwdIn& in, const Out& dk, const Out& dv, float* dk_part, float* dv_part, int splits,
+               cudaStream_t s) {
+    return S.d <= 64 ? launch_dkv<1>(S, in, dk, dv, dk_part, dv_part, splits, s)
+                     : launch_dkv<2>(S, in, dk, dv, dk_part, dv_part, splits, s);
+}
+
+}  // namespace cross
+}  // namespace gt

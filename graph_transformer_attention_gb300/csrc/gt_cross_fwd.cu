@@ -1,0 +1,315 @@
+// gt_cross_fwd.cu -- cross attention forward, bf16, on the tensor cores.
+//
+// A CTA holds 128 rows (query, head) of one key head and streams its sequence's keys: S = Q K^T into TMEM, an online
+// softmax by four warps (a row to a thread), P as bf16 back into TMEM, O += P V.  One warp loads by TMA, one issues
+// the products.  S and P have columns of their own (head dims up to 64: tiles of 128 keys; above: of 64), so the next
+// scores are formed while the softmax works on these.  256 TMEM columns and at most 97 KB of shared memory a CTA: two CTAs
+// share an SM, one's softmax beside the other's products.
+//
+// The maximum is lazy: a row's base is raised only when a score exceeds it by 2^8, so that O is hardly ever rescaled.  P is
+// rounded to bf16 for the product (half a step, 2^-9 of each weight, independent from key to key); its sum is not.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "gt_cross_tc.cuh"
+
+namespace gt {
+namespace cross {
+namespace {
+
+constexpr int kRows = 128;
+constexpr int kTmaWarp = 4, kMmaWarp = 5;
+constexpr int kThreads = 192;
+constexpr int kStages = 2;
+
+template <int PANELS>
+struct Cfg {
+    static constexpr int kKeys = PANELS == 1 ? 128 : 64;        // of a tile
+    static constexpr uint32_t kQPanel = kRows * 128, kKvPanel = kKeys * 128;
+    static constexpr uint32_t kQ = PANELS * kQPanel, kKv = PANELS * kKvPanel;
+    static constexpr size_t kSmem = 1024 + kQ + 2 * kStages * kKv;
+    static constexpr uint32_t kP = PANELS == 1 ? 128 : 64, kO = PANELS == 1 ? 192 : 128;   // TMEM columns; S at 0
+    static constexpr uint32_t kTmem = 256;
+};
+
+struct Bars {
+    uint64_t q_full, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+    uint64_t s_full, s_free, p_full, o_done, fin;
+    uint32_t tmem_base;
+    int abort;
+};
+
+template <int PANELS>
+__global__ void __launch_bounds__(kThreads, 2)
+cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+          const __grid_constant__ CUtensorMap map_v, const FwdOut out, int* status) {
+    using C = Cfg<PANELS>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    __shared__ Bars bars;
+    const int tq = tile_queries(kRows, S.g), head = blockIdx.y, z = blockIdx.z;
+    const Tile t = find_tile(S, true, tq, blockIdx.x);
+    if (!t.live) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int first = t.tile * tq, live = min(tq, t.lq - first) * S.g;
+    const int tiles = (t.lk + C::kKeys - 1) / C::kKeys;
+    const int t0 = part_begin(tiles, z, out.splits), n = part_begin(tiles, z + 1, out.splits) - t0;
+    const int steps = (S.d + 15) / 16;
+    uint8_t* sq = smem;
+    uint8_t* sk = sq + C::kQ;
+    uint8_t* sv = sk + kStages * C::kKv;
+    if (threadIdx.x == kTmaWarp * 32) {
+        mbar_init(&bars.q_full, 1);
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&bars.k_full[s], 1);
+            mbar_init(&bars.k_empty[s], 1);
+            mbar_init(&bars.v_full[s], 1);
+            mbar_init(&bars.v_empty[s], 1);
+        }
+        mbar_init(&bars.s_full, 1);
+        mbar_init(&bars.s_free, 4);
+        mbar_init(&bars.p_full, 4);
+        mbar_init(&bars.o_done, 1);
+        mbar_init(&bars.fin, 1);
+        bars.abort = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&map_q);
+        tma_prefetch_desc(&map_k);
+        tma_prefetch_desc(&map_v);
+    }
+    if (warp == kMmaWarp) tmem_alloc(&bars.tmem_base, C::kTmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tb = bars.tmem_base;
+    Waits w{&bars.abort, true};
+
+    if (warp == kTmaWarp) {
+        if (n > 0) {
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&bars.q_full, PANELS * tq * S.g * 128);
+                load_panels<PANELS>(sq, C::kQPanel, &map_q, head * S.g, t.q0 + first, &bars.q_full);
+            }
+            __syncwarp();
+        }
+        int i = 0;
+        for (; i < n; ++i) {
+            const int s = i % kStages, row = t.k0 + (t0 + i) * C::kKeys;
+            const uint32_t parity = ((i / kStages) & 1) ^ 1;      // (the first time round finds every stage empty)
+            if (!w.all(&bars.k_empty[s], parity)) break;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&bars.k_full[s], C::kKv);
+                load_panels<PANELS>(sk + s * C::kKv, C::kKvPanel, &map_k, head, row, &bars.k_full[s]);
+            }
+            __syncwarp();
+            if (!w.all(&bars.v_empty[s], parity)) {
+                // (the key tile of this turn is on its way; its value tile is not)
+                int never = 0;
+                mbar_wait_all(&bars.k_full[s], parity ^ 1, &never, tc::kWaitNs);
+                break;
+            }
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&bars.v_full[s], C::kKv);
+                load_panels<PANELS>(sv + s * C::kKv, C::kKvPanel, &map_v, head, row, &bars.v_full[s]);
+            }
+            __syncwarp();
+        }
+        if (!w.ok && lane == 0) tc::fail(&bars.abort, status);
+        // nothing may still be on its way into shared memory when the CTA ends
+        int never = 0;
+        if (n > 0) mbar_wait_all(&bars.q_full, 0, &never, tc::kWaitNs);
+        for (int b = max(0, i - kStages); b < i; ++b) {
+            mbar_wait_all(&bars.k_full[b % kStages], (b / kStages) & 1, &never, tc::kWaitNs);
+            mbar_wait_all(&bars.v_full[b % kStages], (b / kStages) & 1, &never, tc::kWaitNs);
+        }
+    } else if (warp == kMmaWarp) {
+        const uint32_t id_s = idesc_bf16(kRows, C::kKeys, false, false), id_o = idesc_bf16(kRows, 16 * steps, false, true);
+        const SmemDesc dq = smem_desc_split(smem_u32(sq), 16, 1024, 2);
+        auto values = [&](int i) {      // O += P V of tile i
+            const int s = i % kStages;
+            if (!w.all(&bars.v_full[s], (i / kStages) & 1)) return;
+            uint32_t words[C::kKeys / 32];
+            if (!valid_keys(S, t.k0 + (t0 + i) * C::kKeys, t.k0 + t.lk, words))
+                clear_rows<C::kKeys / 32, PANELS>(smem_u32(sv + s * C::kKv), C::kKvPanel, words);
+            if (!w.all(&bars.p_full, i & 1)) return;
+            tc_fence_after();
+            const SmemDesc dv = smem_desc_split(smem_u32(sv + s * C::kKv), C::kKvPanel, 1024, 2);
+            if (elect_one()) {
+                product_rows<C::kKeys>(tb + C::kO, tb + C::kP, dv, id_o, i > 0);
+                mma_commit(&bars.v_empty[s]);
+                mma_commit(&bars.o_done);
+            }
+            __syncwarp();
+        };
+        if (n > 0) w.all(&bars.q_full, 0);
+        for (int i = 0; i < n && w.ok; ++i) {
+            const int s = i % kStages;
+            if (!w.all(&bars.k_full[s], (i / kStages) & 1)) break;
+            if (i > 0 && !w.all(&bars.s_free, (i - 1) & 1)) break;
+            tc_fence_after();
+            const SmemDesc dk = smem_desc_split(smem_u32(sk + s * C::kKv), 16, 1024, 2);
+            if (elect_one()) {
+                product_channels(tb, dq, C::kQPanel, dk, C::kKvPanel, steps, id_s);
+                mma_commit(&bars.k_empty[s]);
+                mma_commit(&bars.s_full);
+            }
+            __syncwarp();
+            if (i > 0) values(i - 1);
+        }
+        if (n > 0 && w.ok) values(n - 1);
+        if (!w.ok) {
+            if (lane == 0) tc::fail(&bars.abort, status);
+            int never = 0;
+            if (elect_one()) mma_commit(&bars.fin);
+            __syncwarp();
+            mbar_wait_all(&bars.fin, 0, &never, tc::kWaitNs);
+        }
+    } else {
+        constexpr int kChunks = C::kKeys / 32;
+        const int r = warp * 32 + lane;
+        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        const bool some = warp * 32 < live;      // a warp without rows only keeps the barriers going
+        const float c = S.scale * tc::kLog2e;
+        const float most = 8.f / c;              // scores above the base
+        float base = -INFINITY, sum = 0.f;       // (the base in scores before scaling)
+        for (int i = 0; i < n; ++i) {
+            uint32_t words[C::kKeys / 32];
+            const bool all = valid_keys(S, t.k0 + (t0 + i) * C::kKeys, t.k0 + t.lk, words);
+            if (!w.all(&bars.s_full, i & 1)) break;
+            tc_fence_after();
+            if (!some) {
+                if (lane == 0) mbar_arrive(&bars.s_free);
+                if (i > 0 && !w.all(&bars.o_done, (i - 1) & 1)) break;     // (this turn's p_full only after the last one's)
+                if (lane == 0) mbar_arrive(&bars.p_full);
+                continue;
+            }
+            uint32_t x[kChunks][32];
+#pragma unroll
+            for (int k = 0; k < kChunks; ++k) tmem_ld_x32(tb + lanes + 32 * k, x[k]);
+            tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.s_free);
+            if (!all) {
+#pragma unroll
+                for (int k = 0; k < kChunks; ++k)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (!((words[k] >> j) & 1u)) x[k][j] = 0xff800000u;     // -infinity
+            }
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int k = 0; k < kChunks; ++k)
+#pragma unroll
+                for (int j = 0; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], __uint_as_float(x[k][j]));
+            const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+            if (i == 0) {
+                base = top;
+            } else if (__any_sync(0xffffffffu, r < live && (top > base + most || (base == -INFINITY && top != -INFINITY)))) {
+                // raise the bases of the warp's rows: O so far, and its sum, in the new ones (rows without a query have no say:
+                // what stands in theirs would change the others' roundings)
+                const float higher = fmaxf(base, top);
+                const float by = base == -INFINITY ? 0.f : ex2((base - higher) * c);
+                if (!w.all(&bars.o_done, (i - 1) & 1)) break;
+                tc_fence_after();
+                for (int k = 0; k < steps; ++k) {
+                    uint32_t o[16];
+                    tmem_ld_x16(tb + lanes + C::kO + 16 * k, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * by);
+                    tmem_st_x16(tb + lanes + C::kO + 16 * k, o);
+                }
+                sum *= by;
+                base = higher;
+            }
+            const float shift = base == -INFINITY ? 0.f : -base * c;
+            float s4[4] = {0.f, 0.f, 0.f, 0.f};
+            uint32_t p[kChunks][16];
+#pragma unroll
+            for (int k = 0; k < kChunks; ++k)
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                    const float a = ex2(fmaf(__uint_as_float(x[k][j]), c, shift));
+                    const float b = ex2(fmaf(__uint_as_float(x[k][j + 1]), c, shift));
+                    s4[j & 3] += a;
+                    s4[(j & 3) + 1] += b;
+                    p[k][j / 2] = pack_bf16x2(a, b);
+                }
+            sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+            if (i > 0 && !w.all(&bars.o_done, (i - 1) & 1)) break;     // the last P has been read
+#pragma unroll
+            for (int k = 0; k < kChunks; ++k) tmem_st_x16(tb + lanes + C::kP + 16 * k, p[k]);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.p_full);
+        }
+        if (n > 0 && w.ok) w.all(&bars.o_done, (n - 1) & 1);
+        if (!w.ok && lane == 0) tc::fail(&bars.abort, status);
+        tc_fence_after();
+        if (some && w.ok) {
+            const bool mine = r < live;
+            const int64_t query = t.q0 + first + r / S.g;
+            const int qh = head * S.g + r % S.g;
+            const bool seen = n > 0 && sum != 0.f;
+            const float inv = seen ? 1.f / sum : 0.f, lse = seen ? base * S.scale + logf(sum) : -INFINITY;
+            if (out.splits == 1) {
+                bf16* p = static_cast<bf16*>(out.o.p) + query * out.o.row + qh * out.o.head;
+                if (mine) out.lse[(int64_t)qh * S.nq + query] = lse;
+                if (n > 0) {
+                    for (int k = 0; k < steps; ++k) {
+                        uint32_t o[16];
+                        tmem_ld_x16(tb + lanes + C::kO + 16 * k, o);
+                        tmem_wait_ld();
+                        float v[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] = seen ? __uint_as_float(o[j]) * inv : 0.f;
+                        if (mine) put16(p, 16 * k, S.d, v, out.o.acc);
+                    }
+                } else if (mine) {
+                    const float zero[16] = {};
+                    for (int k = 0; k < steps; ++k) put16(p, 16 * k, S.d, zero, out.o.acc);
+                }
+            } else {
+                // (the join does not read the sums of a part without a key)
+                if (mine) out.lse_part[(z * (int64_t)S.h + qh) * S.nq + query] = lse;
+                float* p = out.o_part + ((z * (int64_t)S.nq + query) * S.h + qh) * S.d;
+                if (n > 0) tmem_row_out(tb + lanes + C::kO, steps, p, S.d, inv, mine && seen, S.d % 4 == 0 ? 1 : 0);
+            }
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(tb, C::kTmem);
+}
+
+template <int PANELS>
+int launch(const Shape& S, const View& q, const View& k, const View& v, const FwdOut& out, cudaStream_t s) {
+    using C = Cfg<PANELS>;
+    CUtensorMap mq, mk, mv;
+    const int tq = tile_queries(kRows, S.g);
+    if (!heads_map(&mq, q, S.nq, S.h, S.d, S.g, tq) || !heads_map(&mk, k, S.nk, S.hk, S.d, 1, C::kKeys) ||
+        !heads_map(&mv, v, S.nk, S.hk, S.d, 1, C::kKeys))
+        return GT_ERR_CUDA;
+    int* status = device_status_ptr();
+    if (!status) return GT_ERR_CUDA;
+    static std::atomic<uint64_t> allowed;
+    if (!allow_smem(allowed, (const void*)cross_fwd<PANELS>, C::kSmem)) return GT_ERR_CUDA;
+    LaunchScope ls("cross_fwd", s);
+    cross_fwd<PANELS><<<dim3(slots_of(S, true, tq), S.hk, out.splits), kThreads, C::kSmem, s>>>(S, mq, mk, mv, out, status);
+    return check_launch();
+}
+
+}  // namespace
+
+int fwd_tc(const Shape& S, const View& q, const View& k, const View& v, const FwdOut& out, cudaStream_t s) {
+    return S.d <= 64 ? launch<1>(S, q, k, v, out, s) : launch<2>(S, q, k, v, out, s);
+}
+
+}  // namespace cross
+}  // namespace gt

@@ -457,6 +457,125 @@ int gt_linear_bwd(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n,
                   int32_t act, const void* add, int64_t ldadd, void* dx, int64_t lddx, void* dw, int64_t lddw,
                   float* db, void* workspace, size_t ws_bytes, void* stream);
 
+/*
+ * Cross attention: queries of one side over the keys and values of another, of any lengths (a
+ * readout of a graph by a few learned queries, a decoder over the states of the nodes).  Per query
+ * i of head j, over the keys of its own sequence that are not hidden,
+ *   s = scale <q_i, k>,  o = softmax(s) v,  lse = log sum exp s  (natural log)
+ * and backward, with p = exp(s - lse) and D = <dO_i, o_i>,
+ *   dS = p (<dO_i, v> - D),  dq = scale sum dS k,  dk = scale sum dS q,  dv = sum p dO_i.
+ *   dtype   GT_BF16 (bf16 storage, tensor-core products with fp32 sums, fp32 softmax statistics;
+ *           p and dS are rounded to bf16 for the products they enter) or GT_F32 (fp32 throughout).
+ *   q, o, dO, dq  device [nq][h][d]; k, v, dk, dv device [nk][hk][d]; query head j reads key head
+ *           j / (h / hk), whose gradients are the sums over its query heads.  Channels are
+ *           contiguous; ld* is the stride of a row and hd* that of a head, in elements, so slices
+ *           of a fused projection serve as they are.  Any alignment of the type is accepted; bf16
+ *           inputs whose base and strides are multiples of 16 bytes are read in place, others are
+ *           copied to the workspace.
+ *   lse     device fp32 [h][nq].
+ *   batch   sequences, packed one after another: sequence b is rows q_off[b] .. q_off[b + 1] - 1
+ *           of the queries and kv_off[b] .. kv_off[b + 1] - 1 of the keys.  q_off, kv_off: device
+ *           int32 [batch + 1], not falling, within [0, nq] and [0, nk] (values outside are cut
+ *           to that; what falling ones give is not specified), or both NULL with batch = 1: all
+ *           rows.  A sequence may have no rows on either side.  Rows in front of the first sequence
+ *           and behind the last are not read into any result, and left as they were in outputs.
+ *   key_mask  device uint8 [nk] or NULL: keys with 0 are seen by no query (their dk and dv are 0,
+ *           and nothing of theirs, infinities and NaN included, reaches any result).
+ *   A query that sees no key has o = 0, lse = -infinity and dq = 0.
+ *   scale   finite and above 0.
+ *   workspace  at least gt_cross_attn_workspace_size bytes (`backward`: non-zero for the
+ *           backward; `aligned`: non-zero when all bf16 inputs are read in place), 16-byte aligned; may
+ *           be NULL where that is 0.
+ * Outputs must not overlap each other or any input.  Results do not change from run to run.
+ * Errors: GT_ERR_INVALID_ARG for a NULL pointer, an unknown type, a size below 1, h % hk != 0, a
+ * negative stride, one of q_off and kv_off without the other, batch > 1 without them, or a bad scale;
+ * GT_ERR_UNSUPPORTED for d > 128, h > 1024, h / hk > 64, batch > 2^20, nq or nk > 2^30;
+ * GT_ERR_WORKSPACE.
+ */
+size_t gt_cross_attn_workspace_size(int32_t dtype, int32_t nq, int32_t nk, int32_t h, int32_t hk, int32_t d,
+                                    int32_t batch, int32_t backward, int32_t aligned);
+int gt_cross_attn_fwd(int32_t dtype, int32_t nq, int32_t nk, int32_t h, int32_t hk, int32_t d, int32_t batch,
+                      const void* q, int64_t ldq, int64_t hdq, const void* k, int64_t ldk, int64_t hdk,
+                      const void* v, int64_t ldv, int64_t hdv, const int32_t* q_off, const int32_t* kv_off,
+                      const uint8_t* key_mask, float scale, void* o, int64_t ldo, int64_t hdo, float* lse,
+                      void* workspace, size_t ws_bytes, void* stream);
+int gt_cross_attn_bwd(int32_t dtype, int32_t nq, int32_t nk, int32_t h, int32_t hk, int32_t d, int32_t batch,
+                      const void* q, int64_t ldq, int64_t hdq, const void* k, int64_t ldk, int64_t hdk,
+                      const void* v, int64_t ldv, int64_t hdv, const void* o, int64_t ldo, int64_t hdo,
+                      const void* dO, int64_t lddo, int64_t hddo, const float* lse, const int32_t* q_off,
+                      const int32_t* kv_off, const uint8_t* key_mask, float scale, void* dq, int64_t lddq,
+                      int64_t hddq, void* dk, int64_t lddk, int64_t hddk, void* dv, int64_t lddv, int64_t hddv,
+                      void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Which channels of a head make a pair of the rotation: i and i + rot / 2, or 2 i and 2 i + 1.
+ */
+typedef enum { GT_ROT_HALVES = 0, GT_ROT_PAIRS = 1 } gt_rot;
+
+/*
+ * gt_qk_norm_fwd: the norm of every head of the queries and of the keys, and the rotation of their
+ * channels by position, in one pass (before gt_bias_attn_fwd or gt_cross_attn_fwd):
+ *   r = 1 / sqrt(sum_c x_c^2 / d + eps),  y = R (gain x r)
+ * where R turns pair i < rot / 2 of the first rot channels, (a, b) to (a cos - b sin, a sin + b cos),
+ * by the angle pos * freq[i] (radians; to fp32 accuracy for any int32 position while |freq| < 2^24),
+ * and leaves the channels past rot.
+ *   xtype, ytype  element types of q and k, and of yq and yk: any pair.
+ *   freq    device fp32 [rot / 2]; NULL with rot = 0: the norm alone.  rot even, 0 <= rot <= d.
+ *   q, yq   device [nq][h][d], k, yk device [nk][hk][d], channels contiguous, strides of rows (ld*)
+ *           and heads (hd*) in elements, any alignment; k NULL: the queries alone.  An output may
+ *           be its own input (same type, address and strides).
+ *   gain_q, gain_k  device fp32 [d].
+ *   pos_q, pos_k    device int32 [nq], [nk]; NULL: the row's index.
+ * Errors: GT_ERR_INVALID_ARG for a NULL pointer, an unknown type or pairing, a size below 1, a bad
+ * rot, freq with rot = 0 or rot without freq, a negative stride, or an eps that is not finite and
+ * positive; GT_ERR_UNSUPPORTED for d > 256, h or hk > 1024.
+ *
+ * gt_qk_norm_bwd: from dy = dL/dy (y's type), with g = R^T dy and w = gain g,
+ *   dx = r (w - x r^2 sum_c w_c x_c / d),  dgain = sum over rows and heads of g x r
+ *   dq, dk have x's type (either may be its own dy where the types are one), dgain_q, dgain_k are
+ *   device fp32 [d] (outputs, overwritten).  Nothing of the forward is needed but its inputs.
+ *   workspace  at least gt_qk_norm_workspace_size(d) bytes (0 for a d that is not supported).
+ * Errors as the forward's, plus GT_ERR_WORKSPACE.  Results do not change from run to run.
+ */
+int gt_qk_norm_fwd(int32_t xtype, int32_t ytype, int32_t d, float eps, const float* freq, int32_t rot, int32_t pairs,
+                   int32_t nq, int32_t h, const void* q, int64_t ldq, int64_t hdq, const float* gain_q,
+                   const int32_t* pos_q, void* yq, int64_t ldyq, int64_t hdyq, int32_t nk, int32_t hk,
+                   const void* k, int64_t ldk, int64_t hdk, const float* gain_k, const int32_t* pos_k, void* yk,
+                   int64_t ldyk, int64_t hdyk, void* stream);
+size_t gt_qk_norm_workspace_size(int32_t d);
+int gt_qk_norm_bwd(int32_t xtype, int32_t ytype, int32_t d, float eps, const float* freq, int32_t rot, int32_t pairs,
+                   int32_t nq, int32_t h, const void* dyq, int64_t lddyq, int64_t hddyq, const void* q, int64_t ldq,
+                   int64_t hdq, const float* gain_q, const int32_t* pos_q, void* dq, int64_t lddq, int64_t hddq,
+                   float* dgain_q, int32_t nk, int32_t hk, const void* dyk, int64_t lddyk, int64_t hddyk,
+                   const void* k, int64_t ldk, int64_t hdk, const float* gain_k, const int32_t* pos_k, void* dk,
+                   int64_t lddk, int64_t hddk, float* dgain_k, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * gt_grad_clip: the norm of all gradients of a step together, and each of them scaled so that it
+ * does not exceed max_norm:
+ *   norm = sqrt(sum over all tensors of g^2),  out = g (norm <= max_norm ? 1 : max_norm / norm)
+ * over the whole range of fp32 (squares that leave it are summed in fp64).
+ *   list    host array of `count` tensors, read during the call only.  g: device, numel elements
+ *           in a row, of gtype; out: device, of otype (output: it may be g itself with the same
+ *           type; NULL: the tensor only counts).  numel may be 0.
+ *   max_norm  0 or more; infinity only measures (out is g in otype).  A norm that is not finite
+ *           scales by max_norm / norm all the same: 0 for infinity, NaN for NaN.
+ *   norm    device fp32 [1] (output).
+ *   workspace  at least gt_grad_clip_workspace_size(count) bytes, 16-byte aligned.
+ * Errors: GT_ERR_INVALID_ARG for a NULL list, norm or g, count < 1, an unknown type, out = g of
+ * another type, or a max_norm that is negative or NaN; GT_ERR_UNSUPPORTED for numel > 2^40 or more
+ * than 2^41 elements in 256 consecutive tensors; GT_ERR_WORKSPACE.  Results do not change from run to run.
+ */
+typedef struct {
+    const void* g;
+    void* out;
+    int64_t numel;
+    int32_t gtype, otype;
+} gt_grad;
+size_t gt_grad_clip_workspace_size(int32_t count);
+int gt_grad_clip(const gt_grad* list, int32_t count, float max_norm, float* norm, void* workspace, size_t ws_bytes,
+                 void* stream);
+
 /* Static English text for a gt_status value. */
 const char* gt_status_string(int status);
 

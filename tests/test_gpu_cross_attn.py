@@ -1,0 +1,345 @@
+"""Cross attention on the GPU against fp64, within derived bounds."""
+import math
+
+import pytest
+import torch
+
+import cross_ref as X
+import linear_ref as R
+
+pytestmark = pytest.mark.gpu
+F, B = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def gt():
+    import graph_transformer_attention_gb300 as m
+    from graph_transformer_attention_gb300 import build
+    build.build()
+    m.load_library()
+    return m
+
+
+def _t(shape, dtype, seed, std=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(shape, generator=g, device="cuda") * std).to(dtype)
+
+
+def _off(*cuts):
+    return torch.tensor(cuts, dtype=torch.int32, device="cuda")
+
+
+def _both(gt, q, k, v, q_off=None, kv_off=None, mask=None, scale=None, out=None):
+    """Forward and backward against the reference; returns the results."""
+    o, lse = gt.gt_cross_attn_fwd(q, k, v, q_off, kv_off, mask, scale, out=out)
+    rows = slice(None) if q_off is None else slice(int(q_off[0]), int(q_off[-1]))
+    keys = slice(None) if kv_off is None else slice(int(kv_off[0]), int(kv_off[-1]))
+    ref = X.attn_fwd(q, k, v, q_off, kv_off, mask, scale)
+    empty = ref["lse"][0][:, rows] == -math.inf
+    assert ((lse[:, rows].cpu() == -math.inf) == empty).all()
+    assert (o[rows].cpu()[empty.t()] == 0).all()
+    R.check({"o": o[rows], "lse": lse[:, rows].cpu().masked_fill(empty, 0)},
+            {"o": tuple(t[rows] for t in ref["o"]),
+             "lse": (ref["lse"][0][:, rows].masked_fill(empty, 0), ref["lse"][1][:, rows])})
+    do = _t(q.shape, q.dtype, 77)
+    saved = ref["o"][0].to(q.dtype).cuda()          # what the forward would have kept, exactly rounded
+    lse64 = ref["lse"][0].float().cuda()
+    got = gt.gt_cross_attn_bwd(q, k, v, saved, do, lse64, q_off, kv_off, mask, scale)
+    want = X.attn_bwd(q, k, v, saved, do, lse64, q_off, kv_off, mask, scale)
+    for name, t, part in zip(("dq", "dk", "dv"), got, (rows, keys, keys)):
+        R.check({name: t[part]}, {name: tuple(x[part] for x in want[name])})
+    return (o, lse, *got)
+
+
+# one row to many, odd counts, every head width's layout, shared heads, splits over either side
+SHAPES = [(1, 1, 1, 1, 8), (1, 512, 8, 8, 8), (3, 5, 2, 1, 16), (65, 129, 4, 4, 32), (130, 200, 2, 2, 64), (77, 300, 6, 2, 24),
+          (129, 65, 3, 1, 40), (40, 1000, 8, 1, 128), (200, 131, 4, 2, 96), (64, 64, 1, 1, 72), (1, 3000, 4, 1, 64),
+          (2000, 3, 2, 2, 16), (33, 257, 5, 5, 120), (5, 70, 64, 1, 16), (3, 66, 48, 1, 8), (700, 1100, 2, 1, 128)]
+
+
+@pytest.mark.parametrize("t", [F, B])
+@pytest.mark.parametrize("nq,nk,h,hk,c", SHAPES)
+def test_forward_and_backward(gt, nq, nk, h, hk, c, t):
+    q, k, v = _t((nq, h, c), t, 1), _t((nk, hk, c), t, 2), _t((nk, hk, c), t, 3)
+    first = _both(gt, q, k, v)
+    do = _t(q.shape, t, 77)
+    again = gt.gt_cross_attn_bwd(q, k, v, first[0], do, first[1])
+    assert all(torch.equal(a, b) for a, b in zip(gt.gt_cross_attn_bwd(q, k, v, first[0], do, first[1]), again))
+    assert all(torch.equal(a, b) for a, b in zip(gt.gt_cross_attn_fwd(q, k, v), first))
+
+
+@pytest.mark.parametrize("t", [F, B])
+@pytest.mark.parametrize("c", [1, 2, 7, 17, 33, 63, 65, 100, 127])
+def test_odd_widths(gt, c, t):
+    _both(gt, _t((70, 4, c), t, 1), _t((140, 2, c), t, 2), _t((140, 2, c), t, 3))
+
+
+BATCHES = [
+    ([0, 5, 9], [0, 70, 71]),
+    ([0, 0, 130, 131], [0, 64, 300, 301]),            # a sequence without queries
+    ([0, 3, 64, 200], [0, 0, 129, 130]),              # one without keys
+    ([0, 0, 0, 7, 7], [0, 0, 9, 9, 300]),
+    ([2, 40, 41, 170], [3, 131, 259, 260]),           # rows in front of the first sequence and behind the last
+    (list(range(0, 34)), [9 * i for i in range(34)]),
+    ([0, 128, 256, 384], [0, 128, 256, 384]),
+]
+
+
+@pytest.mark.parametrize("t", [F, B])
+@pytest.mark.parametrize("h,hk,c", [(4, 4, 16), (6, 2, 64), (4, 1, 128)])
+@pytest.mark.parametrize("cq,ck", BATCHES, ids=str)
+def test_packed_sequences(gt, cq, ck, h, hk, c, t):
+    nq, nk = cq[-1] + 5, ck[-1] + 3
+    q, k, v = _t((nq, h, c), t, 1), _t((nk, hk, c), t, 2), _t((nk, hk, c), t, 3)
+    # what belongs to no sequence is not a number, and stays out of every result
+    for x, cuts in ((q, cq), (k, ck), (v, ck)):
+        x[:cuts[0]] = math.nan
+        x[cuts[-1]:] = math.inf
+    out = torch.full_like(q, 7.0)
+    _both(gt, q, k, v, _off(*cq), _off(*ck), out=out)
+    assert (out[:cq[0]] == 7).all() and (out[cq[-1]:] == 7).all()
+    do, lse = _t(q.shape, t, 5), torch.full((h, nq), 7.0, device="cuda")
+    o, lse = gt.gt_cross_attn_fwd(q, k, v, _off(*cq), _off(*ck), lse=lse)
+    assert (lse[:, :cq[0]] == 7).all() and (lse[:, cq[-1]:] == 7).all()
+    do[:cq[0]], do[cq[-1]:], lse[:, cq[-1]:] = math.nan, math.inf, math.nan
+    grads = [torch.full_like(x, 7.0) for x in (q, k, v)]
+    gt.gt_cross_attn_bwd(q, k, v, o, do, lse, _off(*cq), _off(*ck), dq=grads[0], dk=grads[1], dv=grads[2])
+    for g, cuts in zip(grads, (cq, ck, ck)):
+        assert (g[:cuts[0]] == 7).all() and (g[cuts[-1]:] == 7).all() and g[cuts[0]:cuts[-1]].isfinite().all()
+
+
+@pytest.mark.parametrize("t", [F, B])
+@pytest.mark.parametrize("h,hk,c", [(4, 4, 16), (6, 2, 64), (4, 2, 128)])
+@pytest.mark.parametrize("keep", [0.0, 0.02, 0.5, 0.97])
+def test_hidden_keys(gt, keep, h, hk, c, t):
+    """Hidden keys that are not numbers, whole tiles of them, and sequences without any other."""
+    cq, ck = [0, 40, 200, 207], [0, 400, 900, 1003]
+    q, k, v = _t((207, h, c), t, 1), _t((1003, hk, c), t, 2), _t((1003, hk, c), t, 3)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    mask = torch.rand(1003, generator=g, device="cuda") < keep
+    mask[500:700] = False
+    k[~mask], v[~mask] = math.nan, math.inf
+    for offs in ((_off(*cq), _off(*ck)), (None, None)):
+        r = _both(gt, q, k, v, *offs, mask=mask)
+        assert (r[3][~mask] == 0).all() and (r[4][~mask] == 0).all()
+        same = gt.gt_cross_attn_fwd(q, k, v, *offs, mask.to(torch.uint8) * 3)
+        assert torch.equal(same[0], r[0])
+
+
+@pytest.mark.parametrize("t", [F, B])
+def test_padded_batch(gt, t):
+    """[batch][longest] rows with hidden padding equal the packed sequences, a length of 0 among them."""
+    lens, top, h, hk, c, nq = [50, 0, 128, 1, 77], 128, 4, 2, 64, 9
+    k, v = _t((5 * top, hk, c), t, 2), _t((5 * top, hk, c), t, 3)
+    mask = torch.cat([torch.arange(top, device="cuda") < n for n in lens])
+    k[~mask], v[~mask] = math.nan, math.nan
+    q = _t((5 * nq, h, c), t, 1)
+    qo = _off(*range(0, 5 * nq + 1, nq))
+    a = gt.gt_cross_attn_fwd(q, k, v, qo, _off(*range(0, 5 * top + 1, top)), mask)
+    ko = _off(*[sum(lens[:i]) for i in range(6)])
+    b = gt.gt_cross_attn_fwd(q, k[mask].contiguous(), v[mask].contiguous(), qo, ko)
+    for x, y in zip(a, b):
+        assert torch.equal(x.isinf(), y.isinf())
+        # (tiles and parts fall differently: fp32 sums in another order, and a bf16 step of the results)
+        x, y = x.float().nan_to_num(neginf=0.0), y.float().nan_to_num(neginf=0.0)
+        assert float((x - y).abs().max()) <= (2e-5 if t == F else 2.0 ** -6)
+    assert (a[0][nq:2 * nq] == 0).all() and (a[1][:, nq:2 * nq] == -math.inf).all()
+
+
+@pytest.mark.parametrize("t", [F, B])
+@pytest.mark.parametrize("c", [16, 64, 72, 128, 20])
+def test_strides_and_alignment(gt, c, t):
+    nq, nk, h, hk = 67, 150, 4, 2
+    fused = _t((nk, 2 * hk * c), t, 2)
+    k, v = fused[:, :hk * c].unflatten(1, (hk, c)), fused[:, hk * c:].unflatten(1, (hk, c))
+    q = _t((h, nq, c), t, 1).transpose(0, 1)                        # heads first
+    _both(gt, q, k, v)
+    odd = _t((nk, hk * c + 3), t, 4)[:, 1:1 + hk * c].unflatten(1, (hk, c))      # any base, any row stride
+    _both(gt, _t((nq + 1, h, c + 1), t, 5)[1:, :, 1:], odd, v)
+    shared = _t((nk, 1, c), t, 6).expand(nk, hk, c)                 # a stride of 0: the heads' gradients still apart
+    _both(gt, q, shared, odd)
+    _both(gt, q, _t((1, hk, c), t, 7).expand(nk, hk, c), v)         # one key many times
+    # results as slices of wider rows, the rest as it was
+    wq, wk = (torch.full((n, heads * c + 5), 7.0, dtype=t, device="cuda") for n, heads in ((nq, h), (nk, hk)))
+    dq, dk = wq[:, 2:2 + h * c].unflatten(1, (h, c)), wk[:, 1:1 + hk * c].unflatten(1, (hk, c))
+    o, lse = gt.gt_cross_attn_fwd(q, k, v)
+    assert torch.equal(gt.gt_cross_attn_fwd(q, k, v, out=dq)[0], o)
+    assert (wq[:, :2] == 7).all() and (wq[:, 2 + h * c:] == 7).all()
+    do = _t(q.shape, t, 9)
+    want = gt.gt_cross_attn_bwd(q, k, v, o, do, lse)
+    got = gt.gt_cross_attn_bwd(q, k, v, o, do, lse, dq=dq, dk=dk)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert (wq[:, :2] == 7).all() and (wk[:, :1] == 7).all() and (wk[:, 1 + hk * c:] == 7).all()
+
+
+@pytest.mark.parametrize("t", [F, B])
+def test_scores_of_any_size(gt, t):
+    """Large scores in rising, falling and alternating order (raised bases), equal ones, tiny ones."""
+    nq, nk, c = 40, 700, 64
+    v = _t((nk, 1, c), t, 3)
+    ramp = torch.linspace(-30, 30, nk, device="cuda")
+    for row in (ramp, -ramp, ramp * torch.where(torch.arange(nk, device="cuda") % 2 == 0, 1, -1), ramp * 0, ramp * 1e-20):
+        k = torch.zeros(nk, 1, c, device="cuda")
+        k[:, 0, 0] = row
+        q = torch.zeros(nq, 1, c, device="cuda")
+        q[:, 0, 0] = torch.linspace(-3, 3, nq, device="cuda")
+        _both(gt, q.to(t), k.to(t), v, scale=1.0)
+
+
+@pytest.mark.parametrize("t", [F, B])
+@pytest.mark.parametrize("scale", [1e-30, 0.01, 2.5])
+def test_scales(gt, scale, t):
+    _both(gt, _t((50, 2, 32), t, 1), _t((200, 2, 32), t, 2), _t((200, 2, 32), t, 3), scale=scale)
+
+
+@pytest.mark.parametrize("t", [F, B])
+def test_nonfinite_values_stay_where_they_belong(gt, t):
+    """A NaN in a query spoils its own rows only; one in a value, every query of its sequence and no other."""
+    q, k, v = _t((30, 2, 16), t, 1), _t((90, 2, 16), t, 2), _t((90, 2, 16), t, 3)
+    qo, ko = _off(0, 10, 30), _off(0, 50, 90)
+    clean = gt.gt_cross_attn_fwd(q, k, v, qo, ko)[0]
+    q2, v2 = q.clone(), v.clone()
+    q2[3, 1, 0] = math.nan
+    o = gt.gt_cross_attn_fwd(q2, k, v, qo, ko)[0]
+    assert o[3, 1].isnan().all()
+    o[3, 1] = clean[3, 1]
+    assert torch.equal(o, clean)
+    v2[60, 0, 5] = math.nan
+    o = gt.gt_cross_attn_fwd(q, k, v2, qo, ko)[0]
+    assert o[10:, 0, 5].isnan().all()
+    o[10:, 0, 5] = clean[10:, 0, 5]
+    assert torch.equal(o, clean)
+
+
+def test_gradients_by_differences(gt):
+    qo, ko, mask = _off(0, 3, 7), _off(0, 6, 11), torch.ones(11, dtype=torch.bool, device="cuda")
+    mask[4] = False
+    q, k, v, w = _t((7, 4, 5), F, 1), _t((11, 2, 5), F, 2), _t((11, 2, 5), F, 3), _t((7, 4, 5), F, 4)
+
+    def loss(q, k, v):
+        return float((X.attn_fwd(q, k, v, qo, ko, mask)["o"][0] * R.d(w)).sum())
+
+    o, lse = gt.gt_cross_attn_fwd(q, k, v, qo, ko, mask)
+    grads = gt.gt_cross_attn_bwd(q, k, v, o, w, lse, qo, ko, mask)
+    args = [t.double() for t in (q, k, v)]
+    for i, got in enumerate(grads):
+        for at in range(0, args[i].numel(), 5):
+            up, down = ([t.clone() for t in args] for _ in range(2))
+            up[i].view(-1)[at] += 1e-5
+            down[i].view(-1)[at] -= 1e-5
+            want = (loss(*up) - loss(*down)) / 2e-5
+            # the difference's own error: third derivatives x 1e-10, fp64 rounding / 1e-5; the kernels' fp32
+            assert abs(float(got.view(-1)[at]) - want) <= 2e-5 * max(1.0, abs(want)), (i, at)
+
+
+@pytest.mark.parametrize("t", [F, B])
+def test_long_sides(gt, t):
+    """Long keys for few queries, long queries for few keys: the split forms, against fp64 on some of the heads."""
+    for nq, nk, h, hk, c in ((4, 20011, 4, 2, 64), (5003, 70, 2, 2, 32), (1, 9001, 16, 2, 128), (300, 4099, 1, 1, 16)):
+        _both(gt, _t((nq, h, c), t, 1), _t((nk, hk, c), t, 2), _t((nk, hk, c), t, 3))
+
+
+def test_offsets_past_32_bits(gt):
+    """Keys and values of more than 2^31 elements each: the last sequence as a call for it alone."""
+    nk, hk, c, tail = 140001, 128, 128, 700
+    k, v = _t((nk, hk, c), B, 2), _t((nk, hk, c), B, 3)
+    q, do = _t((40, hk, c), B, 1), _t((40, hk, c), B, 4)
+    ko, qo = _off(0, nk - tail, nk), _off(0, 20, 40)
+    o, lse = gt.gt_cross_attn_fwd(q, k, v, qo, ko)
+    alone = gt.gt_cross_attn_fwd(q[20:], k[-tail:], v[-tail:])
+    assert float((o[20:].float() - alone[0].float()).abs().max()) <= 2.0 ** -6
+    assert float((lse[:, 20:] - alone[1]).abs().max()) <= 1e-5
+    dq, dk, dv = gt.gt_cross_attn_bwd(q, k, v, o, do, lse, qo, ko)
+    one = gt.gt_cross_attn_bwd(q[20:], k[-tail:], v[-tail:], o[20:], do[20:], lse[:, 20:].contiguous())
+    for a, b in zip((dq[20:], dk[-tail:], dv[-tail:]), one):
+        assert float((a.float() - b.float()).abs().max()) <= 2.0 ** -6 * max(1.0, float(b.float().abs().max()))
+
+
+def test_streams_graphs_and_shared_workspaces(gt):
+    q, k, v, do = _t((300, 4, 64), B, 1), _t((900, 2, 64), B, 2), _t((900, 2, 64), B, 3), _t((300, 4, 64), B, 4)
+    o, lse = gt.gt_cross_attn_fwd(q, k, v)
+    want = (o, lse, *gt.gt_cross_attn_bwd(q, k, v, o, do, lse))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    a = gt.gt_cross_attn_fwd(q, k, v, stream=side)
+    got = (*a, *gt.gt_cross_attn_bwd(q, k, v, o, do, lse, stream=side))
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+    work = torch.empty(max(gt.gt_cross_attn_workspace_size(1, 300, 900, 4, 2, 64, backward=b) for b in (False, True)),
+                       dtype=torch.uint8, device="cuda")
+    one, two = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(one):
+        fwd = gt.gt_cross_attn_fwd(q, k, v, workspace=work)
+    with torch.cuda.graph(two):
+        bwd = gt.gt_cross_attn_bwd(q, k, v, *(fwd[0], do, fwd[1]), workspace=work)
+    for _ in range(3):
+        work.fill_(255)
+        one.replay()
+        two.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(want, (*fwd, *bwd)))
+    gt.gt_check_device_status()
+
+
+def test_two_calls_at_once(gt):
+    """Two streams, a workspace each."""
+    q, k, v = _t((500, 4, 64), B, 1), _t((3000, 4, 64), B, 2), _t((3000, 4, 64), B, 3)
+    want = gt.gt_cross_attn_fwd(q, k, v)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [gt.gt_cross_attn_fwd(q, k, v, stream=streams[i % 2]) for i in range(6)]
+    torch.cuda.synchronize()
+    for r in got:
+        assert all(torch.equal(a, b) for a, b in zip(want, r))
+
+
+@pytest.mark.parametrize("t", [F, B])
+def test_a_step_of_a_cross_attention_layer(gt, t):
+    """Projections, norm and rotation, attention, their backward and the clipping of all gradients, as one step runs
+    them, against autograd of the same layer in fp64 on the GPU."""
+    nq, nk, h, hk, c, width = 37, 150, 4, 2, 16, 48
+    x, y = _t((nq, width), t, 1), _t((nk, width), t, 2)
+    wq, wkv, wo = (_t(s, t, i, 0.15) for i, s in ((3, (width, h * c)), (4, (width, 2 * hk * c)), (5, (h * c, width))))
+    gq, gk, f, do = _t((c,), F, 6) * 0.1 + 1, _t((c,), F, 7) * 0.1 + 1, torch.linspace(1, 0.01, c // 2, device="cuda"), _t((nq, width), t, 8)
+    qo, ko = _off(0, 20, 37), _off(0, 90, 150)
+
+    a, _ = gt.gt_linear_fwd(x, wq)
+    b, _ = gt.gt_linear_fwd(y, wkv)
+    qr, kr, vr = a.view(nq, h, c), b[:, :hk * c].unflatten(1, (hk, c)), b[:, hk * c:].unflatten(1, (hk, c))
+    qn, kn = gt.gt_qk_norm_fwd(qr, kr, gq, gk, freq=f)
+    o, lse = gt.gt_cross_attn_fwd(qn, kn, vr, qo, ko)
+    do_, dwo, _ = gt.gt_linear_bwd(do, o.view(nq, h * c), wo, need_db=False)
+    db = torch.empty_like(b)
+    dqn, dkn, _ = gt.gt_cross_attn_bwd(qn, kn, vr, o, do_.view(nq, h, c), lse, qo, ko, dv=db[:, hk * c:].unflatten(1, (hk, c)))
+    da, _, dgq, dgk = gt.gt_qk_norm_bwd(dqn, dkn, qr, kr, gq, gk, freq=f, dk=db[:, :hk * c].unflatten(1, (hk, c)))
+    dx, dwq, _ = gt.gt_linear_bwd(da.view(nq, h * c), x, wq, need_db=False)
+    dy, dwkv, _ = gt.gt_linear_bwd(db, y, wkv, need_db=False)
+    grads = [dwq, dwkv, dwo, dgq, dgk]
+    norm = gt.gt_grad_clip(grads, 0.5)
+
+    leaves = [u.double().requires_grad_() for u in (x, y, wq, wkv, wo, gq, gk)]
+    X_, Y_, WQ, WKV, WO, GQ, GK = leaves
+    def rotate(u):
+        ang = torch.arange(u.shape[0], device="cuda").double()[:, None] * f.double()
+        cs, sn = ang.cos()[:, None], ang.sin()[:, None]
+        p, r = u[..., :c // 2], u[..., c // 2:]
+        return torch.cat((p * cs - r * sn, p * sn + r * cs), -1)
+    def norm_of(u, g):
+        return rotate(u * (u.square().mean(-1, keepdim=True) + 1e-6) ** -0.5 * g)
+    Q = norm_of((X_ @ WQ).view(nq, h, c), GQ)
+    KV = Y_ @ WKV
+    K, V = norm_of(KV[:, :hk * c].reshape(nk, hk, c), GK), KV[:, hk * c:].reshape(nk, hk, c)
+    outs = []
+    for (i, j), (m, n) in (((0, 20), (0, 90)), ((20, 37), (90, 150))):
+        s = torch.einsum("ihc,jhc->hij", Q[i:j], K[m:n].repeat_interleave(h // hk, 1)) / math.sqrt(c)
+        outs.append(torch.einsum("hij,jhc->ihc", s.softmax(-1), V[m:n].repeat_interleave(h // hk, 1)))
+    ((torch.cat(outs).reshape(nq, h * c) @ WO) * do.double()).sum().backward()
+    total = math.sqrt(sum(float(u.grad.square().sum()) for u in leaves[2:]))
+    # fp32: products and sums of up to 150 terms, a chain of seven of them; bf16: each of the chain's tensors is rounded,
+    # 2^-8 of itself at most, and what follows carries that on: in norm, where the roundings are independent
+    tol = 2e-5 if t == F else 12 * 2.0 ** -8
+    assert abs(float(norm) - total) <= tol * total
+    for got, leaf in zip((*grads, dx, dy), (*leaves[2:], X_, Y_)):
+        want = leaf.grad * (0.5 / total if leaf is not X_ and leaf is not Y_ else 1.0)
+        assert float((got.double() - want).norm()) <= tol * float(want.norm())
