@@ -17,6 +17,8 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <initializer_list>
+#include <type_traits>
 
 #include "gt_common.cuh"
 #include "gt_sm100.cuh"
@@ -26,30 +28,41 @@
 namespace gt {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
 constexpr int kMaxD = 256;
 constexpr int kMaxHeads = 1024;
-constexpr int kAngles = 2048;   // cosines and sines of a CTA's rows: 16 KB
+constexpr int kAngles = 1024;            // cosines and sines of a CTA's rows: 8 KB
+constexpr int kWarpAngles = kAngles / kWarps;
 
-// cos and sin of pos * freq to fp32 accuracy however far the position.  pos * freq is N 2^e with a whole N < 2^55; the
-// angle in turns is that over 2 pi, and only its fraction matters (Payne and Hanek 1983): N times 96 binary digits of
-// 1 / (2 pi) in integers, which leaves the fraction off by less than 2^(e - 41) turns, e <= 0 for |freq| < 2^24 (a larger
-// freq loses digits).
-__device__ __forceinline__ float2 turn_of(int pos, float freq) {
+// The turns by which one position more turns a pair, as a binary fraction of 64 digits (whole turns dropped):
+// freq / (2 pi) mod 1, freq = mant 2^e, with 96 binary digits of 1 / (2 pi) (the reduction of Payne and Hanek, 1983).
+// pos times this, in integers mod 2^64, is the fraction of the angle in turns, off by less than 2^-33 turns for any int32
+// position while |freq| < 2^24 (a larger one loses digits: the digits of 1 / (2 pi) end 2^(e - 72) turns away).
+__device__ __forceinline__ uint64_t rate_of(float freq) {
     const uint32_t bits = __float_as_uint(freq), ex = (bits >> 23) & 255u;
-    if (ex == 255u) return make_float2(NAN, NAN);
-    const uint32_t mant = (bits & 0x7fffffu) | (ex ? 0x800000u : 0u);
-    const int e = (int)(ex ? ex : 1u) - 150;                        // freq = mant 2^e
-    const uint64_t n = (uint64_t)(pos < 0 ? 0u - (uint32_t)pos : (uint32_t)pos) * mant;
-    const uint64_t c_hi = 0x28BE60DB9391054Aull;                    // 1 / (2 pi): the first 64 digits and the next 32
-    const uint32_t c_lo = 0x7F09D5F4u;
-    const uint64_t tail = (uint64_t)((((unsigned __int128)n * c_lo)) >> 32);
-    const unsigned __int128 t = (unsigned __int128)n * c_hi + tail;   // 64 whole and 64 fraction digits
-    uint64_t f = e <= -128 ? 0u : e <= 0 ? (uint64_t)(t >> -e) : e < 64 ? (uint64_t)(t << e) : 0u;
-    if ((pos < 0) != ((bits >> 31) != 0)) f = 0u - f;
-    float s, c;
-    sincospif((float)(int64_t)f * 0x1p-63f, &s, &c);                // two half turns to a turn
-    return make_float2(c, s);
+    const uint64_t mant = (bits & 0x7fffffu) | (ex ? 0x800000u : 0u);
+    const int e = (int)(ex ? ex : 1u) - 150;
+    const uint64_t c_hi = 0x28BE60DB9391054Aull, c_lo = 0x7F09D5F4ull;   // 1 / (2 pi): the first 64 digits, the next 32
+    // mant / (2 pi) = (hi : lo), 64 whole and 64 fraction digits
+    const uint64_t tail = (mant * c_lo) >> 32, lo0 = mant * c_hi, lo = lo0 + tail;
+    const uint64_t hi = __umul64hi(mant, c_hi) + (lo < lo0 ? 1u : 0u);
+    uint64_t f;
+    if (e >= 0) f = e < 64 ? lo << e : 0u;
+    else if (e > -64) f = (lo >> -e) | (hi << (64 + e));
+    else f = e > -128 ? hi >> (-e - 64) : 0u;
+    return bits >> 31 ? 0u - f : f;
+}
+
+// cos and sin of pos times the rate; per_unit: the angle of 2^-32 turns (NaN spoils both).  The nearest quarter turn is
+// taken off in integers, Taylor's polynomials do the rest: 2e-9 and 3e-8 off at pi / 4, the roundings come on top.
+__device__ __forceinline__ float2 turn_of(int pos, uint64_t rate, float per_unit) {
+    const uint32_t f = (uint32_t)(((uint64_t)(int64_t)pos * rate) >> 32), quarter = (f + 0x20000000u) >> 30;
+    const float x = (float)(int32_t)(f - (quarter << 30)) * per_unit, z = x * x;
+    const float s = fmaf(x * z, fmaf(z, fmaf(z, fmaf(z, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), x);
+    const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, 1.f / 40320.f, -1.f / 720.f), 1.f / 24.f), -0.5f), 1.f);
+    const float a = quarter & 1 ? s : c, b = quarter & 1 ? c : s;      // turned by quarter: (c, s), (-s, c), (-c, -s), (s, -c)
+    return make_float2((quarter + 1) & 2 ? -a : a, quarter & 2 ? -b : b);
 }
 
 // One side of a call: queries or keys.  dy: the backward's; y is then dx.
@@ -63,7 +76,7 @@ struct Side {
     float* dgain;
     int64_t ldx, hdx, lddy, hddy, ldy, hdy;
     int n, h;
-    int rows;                // rows a CTA takes at a time
+    int rows;                // rows a warp (qk_norm_any: a CTA) takes at a time
     int ctas;
 };
 
@@ -76,227 +89,429 @@ struct Job {
     float eps, inv_d;
 };
 
-// V consecutive elements
-template <int V, typename T>
-__device__ __forceinline__ void get(const T* p, float (&v)[V]) {
-    if constexpr (V == 8) {
-        unpack8(load8(p, 8, 1), v);
-    } else if constexpr (V == 4 && sizeof(T) == 4) {
-        const float4 f = __ldg(reinterpret_cast<const float4*>(p));
-        v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-    } else if constexpr (V == 4) {
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
-        v[0] = __uint_as_float(w.x << 16); v[1] = __uint_as_float(w.x & 0xffff0000u);
-        v[2] = __uint_as_float(w.y << 16); v[3] = __uint_as_float(w.y & 0xffff0000u);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = to_f32(p[i]);
-    }
-}
+// V consecutive elements, as stored and as fp32 pairs
+template <int V, typename T> struct Raw;
+template <> struct Raw<8, __nv_bfloat16> { uint4 w; };
+template <> struct Raw<8, float> { Raw8<float> r; };
+template <> struct Raw<4, __nv_bfloat16> { uint2 w; };
+template <> struct Raw<4, float> { float4 w; };
 
 template <int V, typename T>
-__device__ __forceinline__ void put(T* p, const float (&v)[V]) {
-    if constexpr (V == 8) {
-        store8(p, v, 8, 1);
-    } else if constexpr (V == 4 && sizeof(T) == 4) {
-        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    } else if constexpr (V == 4) {
-        *reinterpret_cast<uint2*>(p) = make_uint2(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]));
+__device__ __forceinline__ Raw<V, T> get(const T* p) {
+    Raw<V, T> r;
+    if constexpr (V == 8 && sizeof(T) == 4) r.r = load8(p, 8, 1);
+    else r.w = __ldg(reinterpret_cast<const decltype(r.w)*>(p));
+    return r;
+}
+
+__device__ __forceinline__ float2 pair_of(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ void unpack(const Raw<8, __nv_bfloat16>& r, float2 (&v)[4]) {
+    v[0] = pair_of(r.w.x); v[1] = pair_of(r.w.y); v[2] = pair_of(r.w.z); v[3] = pair_of(r.w.w);
+}
+__device__ __forceinline__ void unpack(const Raw<8, float>& r, float2 (&v)[4]) { unpack8(r.r, v); }
+__device__ __forceinline__ void unpack(const Raw<4, __nv_bfloat16>& r, float2 (&v)[2]) {
+    v[0] = pair_of(r.w.x); v[1] = pair_of(r.w.y);
+}
+__device__ __forceinline__ void unpack(const Raw<4, float>& r, float2 (&v)[2]) {
+    v[0] = make_float2(r.w.x, r.w.y); v[1] = make_float2(r.w.z, r.w.w);
+}
+
+template <int P, typename T>
+__device__ __forceinline__ void put(T* p, const float2 (&v)[P]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < P; i += 2)
+            reinterpret_cast<float4*>(p)[i / 2] = make_float4(v[i].x, v[i].y, v[i + 1].x, v[i + 1].y);
+    } else if constexpr (P == 4) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(bf16x2_bits(v[0].x, v[0].y), bf16x2_bits(v[1].x, v[1].y),
+                                                  bf16x2_bits(v[2].x, v[2].y), bf16x2_bits(v[3].x, v[3].y));
     } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) p[i] = from_f32<T>(v[i]);
+        *reinterpret_cast<uint2*>(p) = make_uint2(bf16x2_bits(v[0].x, v[0].y), bf16x2_bits(v[1].x, v[1].y));
     }
 }
 
-// What a lane holds of a head: NS slots of two pieces of V channels.  With V > 1 slot s is the channels V s .. and
-// d / 2 + V s .. (all channels turn, or none); with V = 1 it is the pair s where s < rot / 2, and past the turning channels
-// two neighbours, the second of which may be missing.
-template <int V, int NS>
-struct Held {
-    float a[NS][V], b[NS][V];
-};
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-template <int V>
-struct Slot {
-    int a, b;    // channels; -1: none
-};
-
-template <int V>
-__device__ __forceinline__ Slot<V> slot_of(const Job& J, int s) {
-    if constexpr (V > 1) {
-        return Slot<V>{V * s < J.d / 2 ? V * s : -1, V * s < J.d / 2 ? J.d / 2 + V * s : -1};
-    } else {
-        const int half = J.rot >> 1;
-        if (s < half) return J.adjacent ? Slot<V>{2 * s, 2 * s + 1} : Slot<V>{s, s + half};
-        const int c = J.rot + 2 * (s - half);
-        return Slot<V>{c < J.d ? c : -1, c + 1 < J.d ? c + 1 : -1};
-    }
-}
-
-template <int V, int NS, typename T>
-__device__ __forceinline__ void load_held(const Slot<V> (&sl)[NS], const T* p, Held<V, NS>& v) {
-#pragma unroll
-    for (int i = 0; i < NS; ++i) {
-        if (sl[i].a >= 0) get<V>(p + sl[i].a, v.a[i]);
-        else
-#pragma unroll
-            for (int j = 0; j < V; ++j) v.a[i][j] = 0.f;
-        if (sl[i].b >= 0) get<V>(p + sl[i].b, v.b[i]);
-        else
-#pragma unroll
-            for (int j = 0; j < V; ++j) v.b[i][j] = 0.f;
-    }
-}
-
-template <int V, int NS, typename T>
-__device__ __forceinline__ void store_held(const Slot<V> (&sl)[NS], T* p, const Held<V, NS>& v) {
-#pragma unroll
-    for (int i = 0; i < NS; ++i) {
-        if (sl[i].a >= 0) put<V>(p + sl[i].a, v.a[i]);
-        if (sl[i].b >= 0) put<V>(p + sl[i].b, v.b[i]);
-    }
-}
-
-__device__ __forceinline__ void turn(float& a, float& b, float2 cs, bool back) {
-    const float s = back ? -cs.y : cs.y, t = a * cs.x - b * s;
-    b = a * s + b * cs.x;
+__device__ __forceinline__ void turn_pair(float& a, float& b, float c, float s) {
+    const float t = a * c - b * s;
+    b = a * s + b * c;
     a = t;
 }
 
-// R v, or R^T v; cs: the row's cosines and sines by pair
-template <int V, int NS>
-__device__ __forceinline__ void turn_held(const Job& J, const Slot<V> (&sl)[NS], int first, const float2* cs, Held<V, NS>& v,
-                                          bool back) {
-#pragma unroll
-    for (int i = 0; i < NS; ++i) {
-        if constexpr (V == 1) {
-            const int s = first + i * J.lanes;
-            if (s < (J.rot >> 1)) turn(v.a[i][0], v.b[i][0], cs[s], back);
-        } else if (sl[i].a >= 0) {
-            if (J.adjacent) {
-#pragma unroll
-                for (int j = 0; j < V; j += 2) {
-                    turn(v.a[i][j], v.a[i][j + 1], cs[(sl[i].a + j) >> 1], back);
-                    turn(v.b[i][j], v.b[i][j + 1], cs[(sl[i].b + j) >> 1], back);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < V; ++j) turn(v.a[i][j], v.b[i][j], cs[sl[i].a + j], back);
-            }
-        }
-    }
-}
-
 __device__ __forceinline__ float lanes_sum(float v, int lanes) {
-    for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        if (o < lanes) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
-// A CTA takes `rows` rows at a time; its threads are groups of `lanes`, a head each.
-template <typename TX, typename TY, int V, int NS, bool BWD>
+// What a CTA has in shared memory.
+struct Shared {
+    alignas(16) float cos[kAngles];
+    alignas(16) float sin[kAngles];
+    alignas(16) float minus[kAngles];  // -sin: a packed pair would be negated word by word
+    uint64_t rate[kMaxD / 2];
+    float per_unit[kMaxD / 2];
+    float red[kWarps][kMaxD];   // (backward)
+};
+
+__device__ __forceinline__ void make_rates(const Job& J, Shared& sh) {
+    for (int p = threadIdx.x; p < J.rot >> 1; p += kThreads) {
+        const float f = __ldg(J.freq + p);
+        sh.rate[p] = rate_of(f);
+        sh.per_unit[p] = isfinite(f) ? 6.28318531f * 0x1p-32f : NAN;
+    }
+}
+
+// The angles of rows row0 .. row0 + rows - 1, between two barriers.
+__device__ __forceinline__ void make_angles(const Job& J, const Side& S, int64_t row0, int rows, Shared& sh) {
+    const int half = J.rot >> 1;
+    __syncthreads();      // the rates are there, the last rows' angles have been read
+    for (int k = threadIdx.x; k < rows * half; k += kThreads) {
+        const int r = k / half, p = k - r * half;
+        const float2 t = turn_of(S.pos ? __ldg(S.pos + row0 + r) : (int)(row0 + r), sh.rate[p], sh.per_unit[p]);
+        sh.cos[k] = t.x;
+        sh.sin[k] = t.y;
+    }
+    __syncthreads();
+}
+
+// A CTA's sum of its groups' gradients of channel c, which stand in red[warp][c].
+__device__ __forceinline__ void put_gain_sums(const Job& J, const Side& S, int cta, Shared& sh) {
+    __syncthreads();
+    for (int c = threadIdx.x; c < J.d; c += kThreads) {
+        float t = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) t += sh.red[w][c];
+        S.part[(int64_t)cta * J.d + c] = t;
+    }
+}
+
+// Heads that a group of lanes has at once; those of the next turn are on their way meanwhile.
+constexpr int items_of(bool bwd) { return bwd ? 1 : 2; }
+
+// All channels turn, or none, and move in pieces of V: a lane has channels V s .. V s + V - 1 and d / 2 + V s ..,
+// s its place in the group.  Every warp is on its own: its turns are `rows` rows each, whose angles it forms (a lane an angle,
+// for all their heads) while the next turn's heads are on their way; no barrier of the CTA holds it up.  Arithmetic in packed
+// pairs: the issue slots are the next bound behind the bytes.
+template <typename TX, typename TY, int V, bool BWD>
 __global__ void __launch_bounds__(kThreads) qk_norm(const __grid_constant__ Job J) {
-    __shared__ float2 angles[kAngles];
-    __shared__ float red[BWD ? kThreads * 2 : 1];
+    constexpr int ITEMS = items_of(BWD), P = V / 2;
+    using TO = typename std::conditional<BWD, TX, TY>::type;
+    __shared__ Shared sh;
     const int which = blockIdx.x < J.side[0].ctas ? 0 : 1;
     const Side& S = J.side[which];
     const int cta = blockIdx.x - (which ? J.side[0].ctas : 0);
-    const int first = threadIdx.x & (J.lanes - 1), group = threadIdx.x / J.lanes, groups = kThreads / J.lanes;
-    const int half = J.rot >> 1, h = S.h;
-    Slot<V> sl[NS];
-    Held<V, NS> gain, sum;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int place = lane & (J.lanes - 1), group = lane / J.lanes, groups = 32 / J.lanes;
+    const int half = J.rot >> 1, mid = J.d >> 1;
+    const bool mine = V * place < mid;                    // (lanes past the head's channels read the first ones)
+    const int c0 = mine ? V * place : 0;
+    float* cos_w = sh.cos + warp * kWarpAngles;
+    float* sin_w = sh.sin + warp * kWarpAngles;
+    float* minus_w = sh.minus + warp * kWarpAngles;
+    // (copies: what is read through a reference into the arguments is read again at every use)
+    const int n = S.n, h = S.h, rows = S.rows, lanes = J.lanes, ldx = (int)S.ldx, lddy = (int)S.lddy, ldy = (int)S.ldy;
+    const int hdx = (int)S.hdx, hddy = (int)S.hddy, hdy = (int)S.hdy;
+    const int32_t* const pos = S.pos;
+    const float inv_d = J.inv_d, eps = J.eps;
+    const bool adjacent = J.adjacent;
+    const int turns = (int)(((int64_t)n + rows - 1) / rows), step = S.ctas * kWarps;
+    // deal() takes several rows only where their heads make one batch; with one row the batches are its heads
+    const int batch = ITEMS * groups, last = rows > 1 ? 0 : (h - 1) / batch;
+
+    // this lane's row in the turn and head in the batch, and where they stand
+    int row_k[ITEMS], head_k[ITEMS];
+    int64_t x_k[ITEMS], dy_k[ITEMS], y_k[ITEMS];
 #pragma unroll
-    for (int i = 0; i < NS; ++i) sl[i] = slot_of<V>(J, first + i * J.lanes);
+    for (int k = 0; k < ITEMS; ++k) {
+        const int it = k * groups + group;
+        row_k[k] = rows > 1 ? it / h : 0;
+        head_k[k] = it - row_k[k] * h;
+        if (row_k[k] >= rows) row_k[k] = INT32_MAX / 2;      // no such row
+        x_k[k] = (int64_t)row_k[k] * ldx + (int64_t)head_k[k] * hdx;
+        dy_k[k] = (int64_t)row_k[k] * lddy + (int64_t)head_k[k] * hddy;
+        y_k[k] = (int64_t)row_k[k] * ldy + (int64_t)head_k[k] * hdy;
+    }
+    int turn = cta * kWarps + warp;
+    const TX* x_t = static_cast<const TX*>(S.x) + (int64_t)turn * rows * ldx + c0;
+    const TY* dy_t = static_cast<const TY*>(S.dy) + (int64_t)turn * rows * lddy + c0;
+    TO* y_t = static_cast<TO*>(S.y) + (int64_t)turn * rows * ldy + c0;
+    const int64_t step_x = (int64_t)step * rows * ldx, step_dy = (int64_t)step * rows * lddy, step_y = (int64_t)step * rows * ldy;
+
+    struct Piece {
+        Raw<V, TX> xa, xb;
+        Raw<V, TY> da, db;
+    };
+    Piece next[ITEMS];
+    auto is_live = [&](int t, int b, int k) { return row_k[k] < n - t * rows && head_k[k] < h - b * batch; };
+    auto fetch = [&](int t, int b) {      // (heads that are not there: the turn's first)
 #pragma unroll
-    for (int i = 0; i < NS; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            gain.a[i][j] = sl[i].a >= 0 ? __ldg(S.gain + sl[i].a + j) : 0.f;
-            gain.b[i][j] = sl[i].b >= 0 ? __ldg(S.gain + sl[i].b + j) : 0.f;
-            sum.a[i][j] = sum.b[i][j] = 0.f;
-        }
-    for (int64_t row0 = (int64_t)cta * S.rows; row0 < S.n; row0 += (int64_t)S.ctas * S.rows) {
-        const int rows = (int)(S.n - row0 < S.rows ? S.n - row0 : S.rows);
-        if (half > 0) {
-            if (row0 != (int64_t)cta * S.rows) __syncthreads();   // the last rows' angles have been read
-            for (int k = threadIdx.x; k < rows * half; k += kThreads) {
-                const int r = k / half, p = k - r * half;
-                angles[k] = turn_of(S.pos ? __ldg(S.pos + row0 + r) : (int)(row0 + r), __ldg(J.freq + p));
+        for (int k = 0; k < ITEMS; ++k) {
+            const bool live = is_live(t, b, k);
+            const TX* x = x_t + (live ? x_k[k] + (int64_t)(b * batch) * hdx : 0);
+            next[k].xa = get<V>(x);
+            next[k].xb = get<V>(x + mid);
+            if constexpr (BWD) {
+                const TY* dy = dy_t + (live ? dy_k[k] + (int64_t)(b * batch) * hddy : 0);
+                next[k].da = get<V>(dy);
+                next[k].db = get<V>(dy + mid);
             }
-            __syncthreads();
         }
-        const int items = rows * h;
+    };
+    if (turn < turns) fetch(turn, 0);
+    if (half > 0) make_rates(J, sh);
+    float2 ga[P], gb[P], sa[P], sb[P];
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+        ga[j] = mine ? make_float2(__ldg(S.gain + c0 + 2 * j), __ldg(S.gain + c0 + 2 * j + 1)) : both(0.f);
+        gb[j] = mine ? make_float2(__ldg(S.gain + mid + c0 + 2 * j), __ldg(S.gain + mid + c0 + 2 * j + 1)) : both(0.f);
+        sa[j] = sb[j] = both(0.f);
+    }
+    // this lane's angles: k = lane, lane + 32, ... of the turn's rows x half
+    const int r_first = half > 0 ? lane / half : 0, p_first = half > 0 ? lane - r_first * half : 0;
+    const int r_step = half > 0 ? 32 / half : 0, p_step = half > 0 ? 32 - r_step * half : 0;
+    __syncthreads();      // the rates are there
+    int next_b = 0;
+    while (turn < turns) {
+        float2 x[ITEMS][P], z[ITEMS][P], dx[ITEMS][P], dz[ITEMS][P];
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k) {
+            unpack(next[k].xa, x[k]);
+            unpack(next[k].xb, z[k]);
+            if constexpr (BWD) {
+                unpack(next[k].da, dx[k]);
+                unpack(next[k].db, dz[k]);
+            }
+        }
+        const int t = turn, b = next_b;
+        TO* const y_now = y_t;
+        if (next_b++ == last) {
+            next_b = 0;
+            turn += step;
+            x_t += step_x;
+            if constexpr (BWD) dy_t += step_dy;
+            y_t += step_y;
+        }
+        if (turn < turns) fetch(turn, next_b);
+        if (half > 0 && b == 0) {
+            __syncwarp();      // the last turn's angles have been read
+            const int row0 = t * rows, count = min(rows, n - row0) * half;
+            for (int k = lane, r = r_first, p = p_first; k < count; k += 32) {
+                const float2 cs = turn_of(pos ? __ldg(pos + row0 + r) : row0 + r, sh.rate[p], sh.per_unit[p]);
+                cos_w[k] = cs.x;
+                sin_w[k] = cs.y;
+                minus_w[k] = -cs.y;
+                r += r_step;
+                p += p_step;
+                if (p >= half) {
+                    p -= half;
+                    ++r;
+                }
+            }
+            __syncwarp();
+        }
+        // (every lane makes every turn: the shuffles need them all)
+#pragma unroll
+        for (int k = 0; k < ITEMS; ++k) {
+            const bool live = is_live(t, b, k);
+            float2 u[P], w[P];
+            float2 ss = __fmul2_rn(x[k][0], x[k][0]);
+#pragma unroll
+            for (int j = 1; j < P; ++j) ss = __ffma2_rn(x[k][j], x[k][j], ss);
+#pragma unroll
+            for (int j = 0; j < P; ++j) ss = __ffma2_rn(z[k][j], z[k][j], ss);
+            const float rs = rsqrtf(lanes_sum(mine ? ss.x + ss.y : 0.f, lanes) * inv_d + eps);
+            const float2 rs2 = both(rs);
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                if constexpr (BWD) {
+                    u[j] = dx[k][j];
+                    w[j] = dz[k][j];
+                } else {
+                    u[j] = __fmul2_rn(__fmul2_rn(x[k][j], rs2), ga[j]);
+                    w[j] = __fmul2_rn(__fmul2_rn(z[k][j], rs2), gb[j]);
+                }
+            }
+            if (half > 0) {      // (u, w) = R (u, w), backward R^T
+                const int at = live && rows > 1 ? row_k[k] * half : 0;
+                if (!adjacent) {
+#pragma unroll
+                    for (int j = 0; j < P; j += 2) {
+                        const float4 c4 = *reinterpret_cast<const float4*>(cos_w + at + c0 + 2 * j);
+                        const float4 s4 = *reinterpret_cast<const float4*>(sin_w + at + c0 + 2 * j);
+                        const float4 m4 = *reinterpret_cast<const float4*>(minus_w + at + c0 + 2 * j);
+                        const float2 c[2] = {make_float2(c4.x, c4.y), make_float2(c4.z, c4.w)};
+                        const float2 s[2] = {make_float2(s4.x, s4.y), make_float2(s4.z, s4.w)};
+                        const float2 m[2] = {make_float2(m4.x, m4.y), make_float2(m4.z, m4.w)};
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float2 v = __ffma2_rn(w[j + i], BWD ? s[i] : m[i], __fmul2_rn(u[j + i], c[i]));
+                            w[j + i] = __ffma2_rn(u[j + i], BWD ? m[i] : s[i], __fmul2_rn(w[j + i], c[i]));
+                            u[j + i] = v;
+                        }
+                    }
+                } else {
+                    const float* cs = cos_w + at;
+                    const float* sn = (BWD ? minus_w : sin_w) + at;
+                    const int pa = c0 >> 1, pb = (mid + c0) >> 1;
+#pragma unroll
+                    for (int j = 0; j < P; ++j) {
+                        turn_pair(u[j].x, u[j].y, cs[pa + j], sn[pa + j]);
+                        turn_pair(w[j].x, w[j].y, cs[pb + j], sn[pb + j]);
+                    }
+                }
+            }
+            if constexpr (BWD) {
+                float2 wx = both(0.f);
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    x[k][j] = __fmul2_rn(x[k][j], rs2);
+                    z[k][j] = __fmul2_rn(z[k][j], rs2);
+                    const float2 pa = __fmul2_rn(u[j], x[k][j]), pb = __fmul2_rn(w[j], z[k][j]);
+                    if (live) {
+                        sa[j] = __fadd2_rn(sa[j], pa);
+                        sb[j] = __fadd2_rn(sb[j], pb);
+                    }
+                    wx = __ffma2_rn(pa, ga[j], wx);
+                    wx = __ffma2_rn(pb, gb[j], wx);
+                }
+                // dx = r (w - (x r) sum(w x r) / d)
+                const float2 back = both(-lanes_sum(mine ? wx.x + wx.y : 0.f, lanes) * inv_d);
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    u[j] = __fmul2_rn(rs2, __ffma2_rn(x[k][j], back, __fmul2_rn(u[j], ga[j])));
+                    w[j] = __fmul2_rn(rs2, __ffma2_rn(z[k][j], back, __fmul2_rn(w[j], gb[j])));
+                }
+            }
+            if (live && mine) {
+                TO* y = y_now + y_k[k] + (int64_t)(b * batch) * hdy;
+                put<P>(y, u);
+                put<P>(y + mid, w);
+            }
+        }
+    }
+    if constexpr (BWD) {
+        sm100::pdl_trigger();
+        // the groups' sums: those of a warp here, then the warps' in their order
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            for (int o = 16; o >= lanes; o >>= 1) {
+                sa[j].x += __shfl_xor_sync(0xffffffffu, sa[j].x, o);
+                sa[j].y += __shfl_xor_sync(0xffffffffu, sa[j].y, o);
+                sb[j].x += __shfl_xor_sync(0xffffffffu, sb[j].x, o);
+                sb[j].y += __shfl_xor_sync(0xffffffffu, sb[j].y, o);
+            }
+            if (lane < lanes && mine) {
+                float* red = sh.red[warp] + c0 + 2 * j;
+                red[0] = sa[j].x; red[1] = sa[j].y;
+                red[mid] = sb[j].x; red[mid + 1] = sb[j].y;
+            }
+        }
+        put_gain_sums(J, S, cta, sh);
+    }
+}
+
+// Any width, alignment and number of turning channels: a lane has NS pairs of channels.  Place s is pair s while
+// s < rot / 2; past the turning channels two neighbours, the second of which may be missing.
+template <typename TX, typename TY, int NS, bool BWD>
+__global__ void __launch_bounds__(kThreads) qk_norm_any(const __grid_constant__ Job J) {
+    __shared__ Shared sh;
+    const int which = blockIdx.x < J.side[0].ctas ? 0 : 1;
+    const Side& S = J.side[which];
+    const int cta = blockIdx.x - (which ? J.side[0].ctas : 0);
+    const int place = threadIdx.x & (J.lanes - 1), group = threadIdx.x / J.lanes, groups = kThreads / J.lanes;
+    const int half = J.rot >> 1, h = S.h;
+    if (half > 0) make_rates(J, sh);
+    int ca[NS], cb[NS];      // channels, -1: none
+    float ga[NS], gb[NS], sa[NS], sb[NS];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        const int s = place + i * J.lanes;
+        if (s < half) {
+            ca[i] = J.adjacent ? 2 * s : s;
+            cb[i] = J.adjacent ? 2 * s + 1 : s + half;
+        } else {
+            const int c = J.rot + 2 * (s - half);
+            ca[i] = c < J.d ? c : -1;
+            cb[i] = c + 1 < J.d ? c + 1 : -1;
+        }
+        ga[i] = ca[i] >= 0 ? __ldg(S.gain + ca[i]) : 0.f;
+        gb[i] = cb[i] >= 0 ? __ldg(S.gain + cb[i]) : 0.f;
+        sa[i] = sb[i] = 0.f;
+    }
+    for (int64_t row0 = (int64_t)cta * S.rows; row0 < S.n; row0 += (int64_t)S.ctas * S.rows) {
+        const int rows = (int)(S.n - row0 < S.rows ? S.n - row0 : S.rows), items = rows * h;
+        if (half > 0) make_angles(J, S, row0, rows, sh);
         // (every lane of a warp makes every turn: the shuffles need them all)
         for (int it0 = 0; it0 < items; it0 += groups) {
             const bool live = it0 + group < items;
             const int it = live ? it0 + group : 0, r = it / h, head = it - r * h;
             const int64_t row = row0 + r;
             const TX* x = static_cast<const TX*>(S.x) + row * S.ldx + head * S.hdx;
-            Held<V, NS> v;
-            load_held<V, NS>(sl, x, v);
-            float ss = 0.f;
+            const TY* dy = static_cast<const TY*>(S.dy) + row * S.lddy + head * S.hddy;
+            float a[NS], b[NS], u[NS], w[NS], ss = 0.f;
 #pragma unroll
-            for (int i = 0; i < NS; ++i)
+            for (int i = 0; i < NS; ++i) {
+                a[i] = ca[i] >= 0 ? to_f32(x[ca[i]]) : 0.f;
+                b[i] = cb[i] >= 0 ? to_f32(x[cb[i]]) : 0.f;
+                if constexpr (BWD) {
+                    u[i] = ca[i] >= 0 ? to_f32(dy[ca[i]]) : 0.f;
+                    w[i] = cb[i] >= 0 ? to_f32(dy[cb[i]]) : 0.f;
+                }
+                ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
+            }
+            const float rs = rsqrtf(lanes_sum(ss, J.lanes) * J.inv_d + J.eps);
+            float wx = 0.f;
 #pragma unroll
-                for (int j = 0; j < V; ++j) ss += v.a[i][j] * v.a[i][j] + v.b[i][j] * v.b[i][j];
-            if constexpr (!BWD) {
-                const float rs = 1.f / sqrtf(lanes_sum(ss, J.lanes) * J.inv_d + J.eps);
-#pragma unroll
-                for (int i = 0; i < NS; ++i)
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        v.a[i][j] *= rs * gain.a[i][j];
-                        v.b[i][j] *= rs * gain.b[i][j];
+            for (int i = 0; i < NS; ++i) {
+                const int s = place + i * J.lanes;
+                if constexpr (!BWD) {
+                    u[i] = a[i] * rs * ga[i];
+                    w[i] = b[i] * rs * gb[i];
+                }
+                if (s < half) turn_pair(u[i], w[i], sh.cos[r * half + s], BWD ? -sh.sin[r * half + s] : sh.sin[r * half + s]);
+                if constexpr (BWD) {
+                    a[i] *= rs;
+                    b[i] *= rs;
+                    const float pa = u[i] * a[i], pb = w[i] * b[i];
+                    if (live) {
+                        sa[i] += pa;
+                        sb[i] += pb;
                     }
-                if (half > 0) turn_held<V, NS>(J, sl, first, angles + r * half, v, false);
-                if (live) store_held<V, NS>(sl, static_cast<TY*>(S.y) + row * S.ldy + head * S.hdy, v);
-            } else {
-                Held<V, NS> g;
-                load_held<V, NS>(sl, static_cast<const TY*>(S.dy) + row * S.lddy + head * S.hddy, g);
-                if (half > 0) turn_held<V, NS>(J, sl, first, angles + r * half, g, true);
-                float wx = 0.f;
+                    wx = fmaf(pa, ga[i], fmaf(pb, gb[i], wx));
+                }
+            }
+            using TO = typename std::conditional<BWD, TX, TY>::type;
+            TO* y = static_cast<TO*>(S.y) + row * S.ldy + head * S.hdy;
+            const float back = BWD ? -lanes_sum(wx, J.lanes) * J.inv_d : 0.f;
 #pragma unroll
-                for (int i = 0; i < NS; ++i)
-#pragma unroll
-                    for (int j = 0; j < V; ++j)
-                        wx += gain.a[i][j] * g.a[i][j] * v.a[i][j] + gain.b[i][j] * g.b[i][j] * v.b[i][j];
-                const float rs = 1.f / sqrtf(lanes_sum(ss, J.lanes) * J.inv_d + J.eps);
-                const float back = rs * rs * lanes_sum(wx, J.lanes) * J.inv_d;
-#pragma unroll
-                for (int i = 0; i < NS; ++i)
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        if (live) {
-                            sum.a[i][j] += g.a[i][j] * (v.a[i][j] * rs);
-                            sum.b[i][j] += g.b[i][j] * (v.b[i][j] * rs);
-                        }
-                        v.a[i][j] = rs * (gain.a[i][j] * g.a[i][j] - v.a[i][j] * back);
-                        v.b[i][j] = rs * (gain.b[i][j] * g.b[i][j] - v.b[i][j] * back);
-                    }
-                if (live) store_held<V, NS>(sl, static_cast<TX*>(S.y) + row * S.ldy + head * S.hdy, v);
+            for (int i = 0; i < NS; ++i) {
+                if constexpr (BWD) {
+                    u[i] = rs * fmaf(a[i], back, u[i] * ga[i]);
+                    w[i] = rs * fmaf(b[i], back, w[i] * gb[i]);
+                }
+                if (live && ca[i] >= 0) y[ca[i]] = from_f32<TO>(u[i]);
+                if (live && cb[i] >= 0) y[cb[i]] = from_f32<TO>(w[i]);
             }
         }
     }
     if constexpr (BWD) {
         sm100::pdl_trigger();
-        // the groups' sums, one channel of each piece at a time, in the groups' order
 #pragma unroll
-        for (int i = 0; i < NS; ++i)
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                __syncthreads();
-                red[threadIdx.x] = sum.a[i][j];
-                red[kThreads + threadIdx.x] = sum.b[i][j];
-                __syncthreads();
-                if ((int)threadIdx.x < J.lanes) {
-                    float ta = 0.f, tb = 0.f;
-                    for (int k = 0; k < groups; ++k) {
-                        ta += red[k * J.lanes + threadIdx.x];
-                        tb += red[kThreads + k * J.lanes + threadIdx.x];
-                    }
-                    if (sl[i].a >= 0) S.part[(int64_t)cta * J.d + sl[i].a + j] = ta;
-                    if (sl[i].b >= 0) S.part[(int64_t)cta * J.d + sl[i].b + j] = tb;
-                }
+        for (int i = 0; i < NS; ++i) {
+            for (int o = 16; o >= J.lanes; o >>= 1) {
+                sa[i] += __shfl_xor_sync(0xffffffffu, sa[i], o);
+                sb[i] += __shfl_xor_sync(0xffffffffu, sb[i], o);
             }
+            if ((threadIdx.x & 31) < J.lanes) {
+                if (ca[i] >= 0) sh.red[threadIdx.x >> 5][ca[i]] = sa[i];
+                if (cb[i] >= 0) sh.red[threadIdx.x >> 5][cb[i]] = sb[i];
+            }
+        }
+        put_gain_sums(J, S, cta, sh);
     }
 }
 
@@ -326,66 +541,77 @@ bool pieces16(const void* p, int64_t ld, int64_t hd, int bytes, int piece) {
     return ((reinterpret_cast<uintptr_t>(p) | (uint64_t)(ld * bytes) | (uint64_t)(hd * bytes)) & (uint64_t)(piece - 1)) == 0;
 }
 
-// The largest V with which all of a call's pieces are aligned accesses: 16 bytes of x where they can be.
+// The largest V with which all of a call's pieces are aligned accesses of up to 16 bytes of x (32-bit strides); 1: single
+// elements.
 template <typename TX, typename TY>
 int piece_of(const Job& J, bool bwd) {
     if (J.rot != 0 && J.rot != J.d) return 1;
-    for (int v = sizeof(TX) == 2 ? 8 : 4; v > 1; v /= 2) {
-        bool ok = v >= 4 && (J.d / 2) % v == 0 && J.d % 2 == 0;
+    for (int v = sizeof(TX) == 2 ? 8 : 4; v >= 4; v /= 2) {
+        bool ok = J.d % (2 * v) == 0;
         for (const Side& S : J.side) {
             if (!S.x) continue;
             const int px = std::min<int>(16, v * (int)sizeof(TX)), py = std::min<int>(16, v * (int)sizeof(TY));
             ok = ok && pieces16(S.x, S.ldx, S.hdx, sizeof(TX), px);
             ok = ok && pieces16(S.y, S.ldy, S.hdy, bwd ? sizeof(TX) : sizeof(TY), bwd ? px : py);
             if (bwd) ok = ok && pieces16(S.dy, S.lddy, S.hddy, sizeof(TY), py);
+            for (int64_t stride : {S.ldx, S.hdx, S.ldy, S.hdy, S.lddy, S.hddy}) ok = ok && stride <= INT32_MAX;
         }
         if (ok) return v;
     }
     return 1;
 }
 
-// CTAs of the backward at most, each of which makes one partial row
+// CTAs at most: what is resident at once (each of the backward's makes one partial row)
 int most_ctas() { return 4 * num_sms(); }
 
-// How the rows are dealt: about four heads to a group of lanes at a time, as far as the angles' table goes.
-void deal(Job& J, int v, bool bwd) {
+// How the rows are dealt.  A warp takes as many rows at a time as make `items` heads for every group of its lanes (a CTA of
+// qk_norm_any: one), as far as the angles' table goes; the CTAs go to the two sides by their heads.
+void deal(Job& J, int v, int items) {
     const int slots = v > 1 ? J.d / 2 / v : (J.rot / 2 + (J.d - J.rot + 1) / 2);
     J.lanes = 1;
     while (J.lanes < slots && J.lanes < 32) J.lanes *= 2;
-    int64_t all = 0;
-    for (Side& S : J.side) {
-        if (!S.x) { S.ctas = 0; S.rows = 1; continue; }
-        const int groups = kThreads / J.lanes;
-        int64_t rows = std::max(1, 4 * groups / S.h);
-        if (J.rot) rows = std::min<int64_t>(rows, kAngles / (J.rot / 2));
-        // enough CTAs for every SM first
-        rows = std::max<int64_t>(1, std::min<int64_t>(rows, S.n / (2 * num_sms())));
-        S.rows = (int)rows;
-        S.ctas = (int)((S.n + rows - 1) / rows);
-        all += S.ctas;
+    int64_t want[2] = {0, 0}, all = 0;
+    for (int i = 0; i < 2; ++i) {
+        Side& S = J.side[i];
+        S.rows = 1;
+        if (!S.x) continue;
+        const int heads = (v > 1 ? items * 32 : kThreads) / J.lanes;
+        S.rows = std::max(1, heads / S.h);
+        if (J.rot) S.rows = std::min(S.rows, std::max(1, (v > 1 ? kWarpAngles : kAngles) / (J.rot / 2)));
+        // enough warps for every SM first
+        S.rows = (int)std::max<int64_t>(1, std::min<int64_t>(S.rows, S.n / (4 * num_sms())));
+        const int64_t turns = ((int64_t)S.n + S.rows - 1) / S.rows;
+        want[i] = v > 1 ? (turns + kWarps - 1) / kWarps : turns;
+        all += want[i];
     }
-    if (!bwd || all <= most_ctas()) return;
-    for (Side& S : J.side)
-        if (S.x) S.ctas = (int)std::max<int64_t>(1, (int64_t)S.ctas * (most_ctas() - 2) / all);
+    for (int i = 0; i < 2; ++i) {
+        Side& S = J.side[i];
+        S.ctas = (int)want[i];
+        if (S.x && all > most_ctas()) {
+            const int64_t a = (int64_t)J.side[0].n * J.side[0].h, b = J.side[1].x ? (int64_t)J.side[1].n * J.side[1].h : 0;
+            const int64_t share = (int64_t)(((double)(i ? b : a) / (double)(a + b)) * (most_ctas() - 2));
+            S.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(share, want[i]));
+        }
+    }
 }
 
 template <typename TX, typename TY, bool BWD>
 int run(Job& J, cudaStream_t s) {
     const int v = piece_of<TX, TY>(J, BWD);
-    deal(J, v, BWD);
+    deal(J, v, items_of(BWD));
     const int grid = J.side[0].ctas + J.side[1].ctas;
     // the keys' partial rows follow the queries'; deal() keeps both together within most_ctas()
     if (BWD) J.side[1].part = J.side[0].part + (int64_t)J.side[0].ctas * J.d;
     {
         LaunchScope ls(BWD ? "qk_norm_bwd" : "qk_norm_fwd", s);
         if (v == 8) {
-            if constexpr (sizeof(TX) == 2) qk_norm<TX, TY, 8, 1, BWD><<<grid, kThreads, 0, s>>>(J);
+            if constexpr (sizeof(TX) == 2) qk_norm<TX, TY, 8, BWD><<<grid, kThreads, 0, s>>>(J);
         } else if (v == 4) {
-            qk_norm<TX, TY, 4, 1, BWD><<<grid, kThreads, 0, s>>>(J);
-        } else if (J.d <= 63) {   // at most 32 slots
-            qk_norm<TX, TY, 1, 1, BWD><<<grid, kThreads, 0, s>>>(J);
+            qk_norm<TX, TY, 4, BWD><<<grid, kThreads, 0, s>>>(J);
+        } else if (J.d <= 63) {   // at most 32 pairs
+            qk_norm_any<TX, TY, 1, BWD><<<grid, kThreads, 0, s>>>(J);
         } else {
-            qk_norm<TX, TY, 1, 4, BWD><<<grid, kThreads, 0, s>>>(J);
+            qk_norm_any<TX, TY, 4, BWD><<<grid, kThreads, 0, s>>>(J);
         }
         const int rc = check_launch();
         if (rc != GT_OK) return rc;
