@@ -96,9 +96,11 @@ __host__ __device__ inline int tile_queries(int rows, int g) { return rows / g; 
 // Part z of `parts` of n steps
 __device__ __forceinline__ int part_begin(int n, int z, int parts) { return (int)((int64_t)n * z / parts); }
 
-// Bit c of word w: key first + 32 w + c is one of the sequence's (below `end`) and not hidden.  Every lane of a warp.
+// Whether all of the tile's keys are the sequence's (below `end`) and not hidden; if not, bit c of word w says so of key
+// first + 32 w + c.  Every lane of a warp.
 template <int N>
 __device__ __forceinline__ bool valid_keys(const Shape& S, int first, int end, uint32_t (&words)[N]) {
+    if (!S.mask && end - first >= 32 * N) return true;      // (the words are not set)
     bool all = true;
 #pragma unroll
     for (int w = 0; w < N; ++w) {

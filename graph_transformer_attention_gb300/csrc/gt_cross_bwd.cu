@@ -146,8 +146,8 @@ cross_dq(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_
             const SmemDesc b_k = smem_desc_split(smem_u32(sk + s * C::kStepBytes), 16, 1024, 2);
             const SmemDesc b_v = smem_desc_split(smem_u32(sv + s * C::kStepBytes), 16, 1024, 2);
             if (elect_one()) {
-                product_channels(tb, a_q, kHeldPanel, b_k, kStepPanel, steps, id_s);
-                product_channels(tb + C::kDp, a_do, kHeldPanel, b_v, kStepPanel, steps, id_s);
+                product_channels<PANELS>(tb, a_q, kHeldPanel, b_k, kStepPanel, steps, id_s);
+                product_channels<PANELS>(tb + C::kDp, a_do, kHeldPanel, b_v, kStepPanel, steps, id_s);
                 mma_commit(&bars.v_empty[s]);
                 mma_commit(&bars.s_full);
             }
@@ -375,8 +375,8 @@ cross_dkv(const Shape S, const __grid_constant__ CUtensorMap map_k, const __grid
             const SmemDesc b_q = smem_desc_split(smem_u32(sq + s * C::kStepBytes), 16, 1024, 2);
             const SmemDesc b_do = smem_desc_split(smem_u32(sdo + s * C::kStepBytes), 16, 1024, 2);
             if (elect_one()) {
-                product_channels(tb + 128 * b, a_k, kHeldPanel, b_q, kStepPanel, steps, id_s);
-                product_channels(tb + 128 * b + 64, a_v, kHeldPanel, b_do, kStepPanel, steps, id_s);
+                product_channels<PANELS>(tb + 128 * b, a_k, kHeldPanel, b_q, kStepPanel, steps, id_s);
+                product_channels<PANELS>(tb + 128 * b + 64, a_v, kHeldPanel, b_do, kStepPanel, steps, id_s);
                 mma_commit(&bars.s_full[b]);
             }
             __syncwarp();

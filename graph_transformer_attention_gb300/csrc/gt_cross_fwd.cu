@@ -6,8 +6,9 @@
 // scores are formed while the softmax works on these.  256 TMEM columns and at most 97 KB of shared memory a CTA: two CTAs
 // share an SM, one's softmax beside the other's products.
 //
-// The maximum is lazy: a row's base is raised only when a score exceeds it by 2^8, so that O is hardly ever rescaled.  P is
-// rounded to bf16 for the product (half a step, 2^-9 of each weight, independent from key to key); its sum is not.
+// The maximum is lazy: a row's base is raised only when a score exceeds it by 2^8, so that O is hardly ever rescaled.
+// The weights are formed in packed pairs: the issue slots of these warps are the bound.  P is rounded to bf16 for the product (half a step, 2^-8 of each weight at most, independent from key
+// to key); its sum is not.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -42,11 +43,29 @@ struct Bars {
     int abort;
 };
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float m;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
+
+// Weights of 32 scores to a base, packed, and their sums: p = 2^(x c + shift).
+__device__ __forceinline__ void weights(const uint32_t (&x)[32], float2 c, float2 shift, uint32_t (&p)[16], float2 (&sum)[2]) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+        const float2 t = __ffma2_rn(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), c, shift);
+        const float2 e = make_float2(ex2(t.x), ex2(t.y));
+        sum[(j >> 1) & 1] = __fadd2_rn(sum[(j >> 1) & 1], e);
+        p[j / 2] = pack_bf16x2(e.x, e.y);
+    }
+}
+
 template <int PANELS>
 __global__ void __launch_bounds__(kThreads, 2)
 cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
           const __grid_constant__ CUtensorMap map_v, const FwdOut out, int* status) {
     using C = Cfg<PANELS>;
+    constexpr int kKeys = C::kKeys, kChunks = kKeys / 32;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ Bars bars;
@@ -55,7 +74,7 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
     if (!t.live) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int first = t.tile * tq, live = min(tq, t.lq - first) * S.g;
-    const int tiles = (t.lk + C::kKeys - 1) / C::kKeys;
+    const int tiles = (t.lk + kKeys - 1) / kKeys;
     const int t0 = part_begin(tiles, z, out.splits), n = part_begin(tiles, z + 1, out.splits) - t0;
     const int steps = (S.d + 15) / 16;
     uint8_t* sq = smem;
@@ -97,7 +116,7 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
         }
         int i = 0;
         for (; i < n; ++i) {
-            const int s = i % kStages, row = t.k0 + (t0 + i) * C::kKeys;
+            const int s = i % kStages, row = t.k0 + (t0 + i) * kKeys;
             const uint32_t parity = ((i / kStages) & 1) ^ 1;      // (the first time round finds every stage empty)
             if (!w.all(&bars.k_empty[s], parity)) break;
             if (elect_one()) {
@@ -126,19 +145,21 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
             mbar_wait_all(&bars.v_full[b % kStages], (b / kStages) & 1, &never, tc::kWaitNs);
         }
     } else if (warp == kMmaWarp) {
-        const uint32_t id_s = idesc_bf16(kRows, C::kKeys, false, false), id_o = idesc_bf16(kRows, 16 * steps, false, true);
+        const uint32_t id_s = idesc_bf16(kRows, kKeys, false, false), id_o = idesc_bf16(kRows, 16 * steps, false, true);
         const SmemDesc dq = smem_desc_split(smem_u32(sq), 16, 1024, 2);
+        const SmemDesc dk = smem_desc_split(smem_u32(sk), 16, 1024, 2);
+        const SmemDesc dv = smem_desc_split(smem_u32(sv), C::kKvPanel, 1024, 2);
+        auto at = [](SmemDesc d, int s) { return SmemDesc{d.lo + s * (C::kKv >> 4), d.hi}; };
         auto values = [&](int i) {      // O += P V of tile i
             const int s = i % kStages;
             if (!w.all(&bars.v_full[s], (i / kStages) & 1)) return;
-            uint32_t words[C::kKeys / 32];
-            if (!valid_keys(S, t.k0 + (t0 + i) * C::kKeys, t.k0 + t.lk, words))
-                clear_rows<C::kKeys / 32, PANELS>(smem_u32(sv + s * C::kKv), C::kKvPanel, words);
+            uint32_t words[kChunks];
+            if (!valid_keys(S, t.k0 + (t0 + i) * kKeys, t.k0 + t.lk, words))
+                clear_rows<kChunks, PANELS>(smem_u32(sv + s * C::kKv), C::kKvPanel, words);
             if (!w.all(&bars.p_full, i & 1)) return;
             tc_fence_after();
-            const SmemDesc dv = smem_desc_split(smem_u32(sv + s * C::kKv), C::kKvPanel, 1024, 2);
             if (elect_one()) {
-                product_rows<C::kKeys>(tb + C::kO, tb + C::kP, dv, id_o, i > 0);
+                product_rows<kKeys>(tb + C::kO, tb + C::kP, at(dv, s), id_o, i > 0);
                 mma_commit(&bars.v_empty[s]);
                 mma_commit(&bars.o_done);
             }
@@ -150,9 +171,8 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
             if (!w.all(&bars.k_full[s], (i / kStages) & 1)) break;
             if (i > 0 && !w.all(&bars.s_free, (i - 1) & 1)) break;
             tc_fence_after();
-            const SmemDesc dk = smem_desc_split(smem_u32(sk + s * C::kKv), 16, 1024, 2);
             if (elect_one()) {
-                product_channels(tb, dq, C::kQPanel, dk, C::kKvPanel, steps, id_s);
+                product_channels<PANELS>(tb, dq, C::kQPanel, at(dk, s), C::kKvPanel, steps, id_s);
                 mma_commit(&bars.k_empty[s]);
                 mma_commit(&bars.s_full);
             }
@@ -168,16 +188,16 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
             mbar_wait_all(&bars.fin, 0, &never, tc::kWaitNs);
         }
     } else {
-        constexpr int kChunks = C::kKeys / 32;
         const int r = warp * 32 + lane;
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
         const bool some = warp * 32 < live;      // a warp without rows only keeps the barriers going
+        const bool mine = r < live;
         const float c = S.scale * tc::kLog2e;
         const float most = 8.f / c;              // scores above the base
         float base = -INFINITY, sum = 0.f;       // (the base in scores before scaling)
         for (int i = 0; i < n; ++i) {
-            uint32_t words[C::kKeys / 32];
-            const bool all = valid_keys(S, t.k0 + (t0 + i) * C::kKeys, t.k0 + t.lk, words);
+            uint32_t words[kChunks];
+            const bool all = valid_keys(S, t.k0 + (t0 + i) * kKeys, t.k0 + t.lk, words);
             if (!w.all(&bars.s_full, i & 1)) break;
             tc_fence_after();
             if (!some) {
@@ -200,21 +220,21 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
                     for (int j = 0; j < 32; ++j)
                         if (!((words[k] >> j) & 1u)) x[k][j] = 0xff800000u;     // -infinity
             }
-            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int k = 0; k < kChunks; ++k)
 #pragma unroll
-                for (int j = 0; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], __uint_as_float(x[k][j]));
-            const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                for (int j = 0; j < 32; j += 2)
+                    top4[(j >> 1) & 3] = max3(top4[(j >> 1) & 3], __uint_as_float(x[k][j]), __uint_as_float(x[k][j + 1]));
+            const float top = max3(fmaxf(top4[0], top4[1]), top4[2], top4[3]);
+            if (i > 0 && !w.all(&bars.o_done, (i - 1) & 1)) break;     // O is still, and the last P has been read
+            tc_fence_after();
             if (i == 0) {
                 base = top;
-            } else if (__any_sync(0xffffffffu, r < live && (top > base + most || (base == -INFINITY && top != -INFINITY)))) {
-                // raise the bases of the warp's rows: O so far, and its sum, in the new ones (rows without a query have no say:
-                // what stands in theirs would change the others' roundings)
-                const float higher = fmaxf(base, top);
-                const float by = base == -INFINITY ? 0.f : ex2((base - higher) * c);
-                if (!w.all(&bars.o_done, (i - 1) & 1)) break;
-                tc_fence_after();
+            } else if (__any_sync(0xffffffffu, mine && (top > base + most || (base == -INFINITY && top > -INFINITY)))) {
+                // raise the bases of the warp's rows: O so far, and its sum, in the new ones (rows without a query have no
+                // say: what stands in theirs would change the others' roundings)
+                const float higher = fmaxf(base, top), by = base == -INFINITY ? 0.f : ex2((base - higher) * c);
                 for (int k = 0; k < steps; ++k) {
                     uint32_t o[16];
                     tmem_ld_x16(tb + lanes + C::kO + 16 * k, o);
@@ -227,22 +247,15 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
                 base = higher;
             }
             const float shift = base == -INFINITY ? 0.f : -base * c;
-            float s4[4] = {0.f, 0.f, 0.f, 0.f};
-            uint32_t p[kChunks][16];
+            float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int k = 0; k < kChunks; ++k)
-#pragma unroll
-                for (int j = 0; j < 32; j += 2) {
-                    const float a = ex2(fmaf(__uint_as_float(x[k][j]), c, shift));
-                    const float b = ex2(fmaf(__uint_as_float(x[k][j + 1]), c, shift));
-                    s4[j & 3] += a;
-                    s4[(j & 3) + 1] += b;
-                    p[k][j / 2] = pack_bf16x2(a, b);
-                }
-            sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
-            if (i > 0 && !w.all(&bars.o_done, (i - 1) & 1)) break;     // the last P has been read
-#pragma unroll
-            for (int k = 0; k < kChunks; ++k) tmem_st_x16(tb + lanes + C::kP + 16 * k, p[k]);
+            for (int k = 0; k < kChunks; ++k) {
+                uint32_t p[16];
+                weights(x[k], make_float2(c, c), make_float2(shift, shift), p, sum2);
+                tmem_st_x16(tb + lanes + C::kP + 16 * k, p);
+            }
+            const float2 s = __fadd2_rn(sum2[0], sum2[1]);
+            sum += s.x + s.y;
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -252,7 +265,6 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
         if (!w.ok && lane == 0) tc::fail(&bars.abort, status);
         tc_fence_after();
         if (some && w.ok) {
-            const bool mine = r < live;
             const int64_t query = t.q0 + first + r / S.g;
             const int qh = head * S.g + r % S.g;
             const bool seen = n > 0 && sum != 0.f;
@@ -260,19 +272,16 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
             if (out.splits == 1) {
                 bf16* p = static_cast<bf16*>(out.o.p) + query * out.o.row + qh * out.o.head;
                 if (mine) out.lse[(int64_t)qh * S.nq + query] = lse;
-                if (n > 0) {
-                    for (int k = 0; k < steps; ++k) {
-                        uint32_t o[16];
+                for (int k = 0; k < steps; ++k) {
+                    uint32_t o[16];
+                    if (n > 0) {
                         tmem_ld_x16(tb + lanes + C::kO + 16 * k, o);
                         tmem_wait_ld();
-                        float v[16];
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] = seen ? __uint_as_float(o[j]) * inv : 0.f;
-                        if (mine) put16(p, 16 * k, S.d, v, out.o.acc);
                     }
-                } else if (mine) {
-                    const float zero[16] = {};
-                    for (int k = 0; k < steps; ++k) put16(p, 16 * k, S.d, zero, out.o.acc);
+                    float v[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = seen ? __uint_as_float(o[j]) * inv : 0.f;
+                    if (mine) put16(p, 16 * k, S.d, v, out.o.acc);
                 }
             } else {
                 // (the join does not read the sums of a part without a key)

@@ -33,12 +33,16 @@ __device__ __forceinline__ void load_panels(uint8_t* dst, uint32_t panel_bytes, 
     for (int p = 0; p < PANELS; ++p) tma_load_4d(dst + p * panel_bytes, map, 64 * p, head, row, 0, bar);
 }
 
-// D (+)= A B^T along the channels: rows of A and of B as panels of a_rows and b_rows rows.
+// D = A B^T along the channels (PANELS of them, `steps` 16-channel steps): rows of A and of B as panels of a_panel and
+// b_panel bytes.
+template <int PANELS>
 __device__ __forceinline__ void product_channels(uint32_t d_tmem, SmemDesc a, uint32_t a_panel, SmemDesc b, uint32_t b_panel,
                                                  int steps, uint32_t idesc) {
-    for (int k = 0; k < steps; ++k)
-        mma_ss(d_tmem, desc_at(a, (k >> 2) * a_panel + (k & 3) * 32), desc_at(b, (k >> 2) * b_panel + (k & 3) * 32), idesc,
-               k > 0);
+#pragma unroll
+    for (int k = 0; k < 4 * PANELS; ++k)
+        if (k < steps)
+            mma_ss(d_tmem, desc_at(a, (k >> 2) * a_panel + (k & 3) * 32), desc_at(b, (k >> 2) * b_panel + (k & 3) * 32), idesc,
+                   k > 0);
 }
 
 // D (+)= W B along B's ROWS rows, W in TMEM (bf16, 8 columns to 16 rows).
@@ -48,21 +52,16 @@ __device__ __forceinline__ void product_rows(uint32_t d_tmem, uint32_t w_tmem, S
     for (int k = 0; k < ROWS / 16; ++k) mma_ts(d_tmem, w_tmem + 8 * k, desc_at(b, k * 2048), idesc, add || k > 0);
 }
 
-// Waits of a role: once one gives up, all that follow do at once.
+// Waits of a role, by whole warps; a wait that gives up says so, and the role ends.
 struct Waits {
     volatile int* abort;
     bool ok;
     __device__ __forceinline__ bool all(uint64_t* bar, uint32_t parity) {
-        if (ok) ok = mbar_wait_all(bar, parity, abort, tc::kWaitNs);
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        ok = ok && mbar_wait_all(bar, parity, abort, tc::kWaitNs);
         return ok;
     }
 };
-
-// 32 values times `by` into v as 16 pairs' bf16
-__device__ __forceinline__ void pack32(const float (&v)[32], uint32_t (&w)[16]) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-}
 
 // A row of `steps` x 16 fp32 TMEM columns, times `by`, to p[0 .. d - 1].
 template <typename T>
