@@ -27,10 +27,13 @@
 namespace gt {
 namespace cross {
 
+using bf16 = __nv_bfloat16;
+
 constexpr int kMaxD = 128;
 constexpr int kMaxShare = 64;     // query heads to a key head
 constexpr int kMaxHeads = 1024;
 constexpr int kMaxSplits = 64;
+constexpr int kFewRows = 2;       // rows (query, head) of a sequence up to which the forward runs on the CUDA cores
 
 // [rows][heads][d], channels contiguous
 struct View {
@@ -178,9 +181,12 @@ struct FwdOut {
 
 struct BwdIn {
     View q, k, v, dO;
-    const float2* stats;     // [hk][nq][g]: lse log2 e (+infinity for a query without a key) and D
+    const float2* stats;     // [hk][nq][g]: -lse log2 e (-infinity for a query without a key) and -D
 };
 
+// Rows of a tile of the few-rows forward; 0: the call has too many.
+int few_rows(const Shape& S);
+int fwd_few(const Shape& S, bool f32, const View& q, const View& k, const View& v, const FwdOut& out, cudaStream_t s);
 int fwd_f32(const Shape& S, const View& q, const View& k, const View& v, const FwdOut& out, cudaStream_t s);
 int fwd_tc(const Shape& S, const View& q, const View& k, const View& v, const FwdOut& out, cudaStream_t s);
 // part: fp32 [splits][nq][h][d] where splits > 1

@@ -1,7 +1,7 @@
 // gt_cross_attn.cu -- entry points of cross attention: checks, workspace, how a call is split over the SMs, and the small
 // kernels around the products.
 //
-//   cross_stats   D = <dO, o> and lse log2 e of every query and head, in the order of the tiles' rows
+//   cross_stats   -lse log2 e and -D, D = <dO, o>, of every query and head, in the order of the tiles' rows
 //   cross_join    o and lse from the parts of a split forward, exactly: weights exp(lse_part - lse)
 //   cross_sum     the sum of a split backward's parts, in their order
 //   cross_pack    rows that TMA cannot read (a base or stride that is no multiple of 16 bytes, or a stride of 0) as padded
@@ -20,7 +20,6 @@ namespace gt {
 namespace cross {
 namespace {
 
-using bf16 = __nv_bfloat16;
 constexpr int kThreads = 256;
 
 // Eight lanes to a query and head.
@@ -53,7 +52,7 @@ __global__ void __launch_bounds__(kThreads) cross_stats(const Shape S, const Vie
         // a query without a key: every p and dS is 0, o (and D) of no matter
         const bool none = l == -INFINITY;
         stats[((int64_t)(head / S.g) * S.nq + query) * S.g + head % S.g] =
-            make_float2(none ? INFINITY : l * tc::kLog2e, none ? 0.f : sum);
+            make_float2(none ? -INFINITY : -l * tc::kLog2e, none ? 0.f : -sum);
     }
 }
 
@@ -62,42 +61,66 @@ __device__ __forceinline__ bool in_batch(const int32_t* off, int batch, int n, i
     return !off || (row >= clamp_off(off, 0, n) && row < clamp_off(off, batch, n));
 }
 
+// Sixteen lanes to a query and head: lane p weighs the parts p, p + 16, ...
 constexpr int kJoinLanes = 16;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) cross_join(const Shape S, const FwdOut out) {
     const int64_t item = (int64_t)blockIdx.x * (kThreads / kJoinLanes) + threadIdx.x / kJoinLanes;
     const int part = threadIdx.x % kJoinLanes;
-    if (item >= (int64_t)S.nq * S.h) return;
-    const int64_t query = item / S.h;
-    const int head = (int)(item - query * S.h);
-    if (!in_batch(S.q_off, S.batch, S.nq, query)) return;
-    const float* lp = out.lse_part + (int64_t)head * S.nq + query;
-    const int64_t step = (int64_t)S.h * S.nq;
-    float top = -INFINITY;
-    for (int z = 0; z < out.splits; ++z) top = fmaxf(top, __ldcg(lp + z * step));
-    float sum = 0.f;
-    for (int z = 0; z < out.splits; ++z) {
-        const float l = __ldcg(lp + z * step);
-        if (l != -INFINITY) sum += expf(l - top);      // (a NaN is not lost)
+    const bool there = item < (int64_t)S.nq * S.h;
+    const int64_t query = there ? item / S.h : 0;
+    const int head = there ? (int)(item - query * S.h) : 0;
+    const bool live = there && in_batch(S.q_off, S.batch, S.nq, query);
+    sm100::pdl_wait();   // launched to overlap the end of the kernel that writes the parts
+    constexpr int W = kMaxSplits / kJoinLanes;
+    float l[W], top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+        const int z = part + k * kJoinLanes;
+        l[k] = live && z < out.splits ? __ldcg(out.lse_part + ((int64_t)z * S.h + head) * S.nq + query) : -INFINITY;
+        top = fmaxf(top, l[k]);
     }
+#pragma unroll
+    for (int o = kJoinLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+        l[k] = l[k] == -INFINITY ? 0.f : expf(l[k] - top);      // (a NaN is not lost)
+        sum += l[k];
+    }
+#pragma unroll
+    for (int o = kJoinLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const bool seen = sum != 0.f;
-    if (part == 0) out.lse[(int64_t)head * S.nq + query] = seen ? top + logf(sum) : -INFINITY;
+    if (live && part == 0) out.lse[(int64_t)head * S.nq + query] = seen ? top + logf(sum) : -INFINITY;
     const float inv = seen ? 1.f / sum : 0.f;
     T* o = static_cast<T*>(out.o.p) + query * out.o.row + head * out.o.head;
-    for (int c = part * 8; c < S.d; c += 8 * kJoinLanes) {
+    const int vec = S.d % 4 == 0 ? 1 : 0;
+    for (int c0 = 0; c0 < S.d; c0 += 8 * kJoinLanes) {
+        const int c = c0 + part * 8;
+        const bool mine = live && c < S.d;
+        const float* src = out.o_part + (mine ? (query * S.h + head) * S.d + c : 0);
+        const int64_t step = (int64_t)S.nq * S.h * S.d;
         float acc[8] = {};
-        for (int z = 0; z < out.splits; ++z) {
-            const float l = __ldcg(lp + z * step);
-            if (l == -INFINITY) continue;      // nothing was written for this part
-            const float w = expf(l - top) * inv;
-            float x[8];
-            unpack8(load8<Mem::kOutput>(out.o_part + ((z * (int64_t)S.nq + query) * S.h + head) * S.d + c, S.d - c,
-                                        S.d % 4 == 0 ? 1 : 0),
-                    x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, x[i], acc[i]);
-        }
-        store8(o + c, acc, S.d - c, out.o.acc);
+        for (int k = 0; k < W; ++k)
+            for (int u = 0; u < kJoinLanes && k * kJoinLanes + u < out.splits; u += 4) {      // four loads at a time
+                Raw8<float> raw[4];
+                float weight[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int z = k * kJoinLanes + u + i;
+                    weight[i] = __shfl_sync(0xffffffffu, l[k], u + i, kJoinLanes) * inv;
+                    raw[i] = load8<Mem::kOutput>(src + (z < out.splits ? z : 0) * step, mine ? S.d - c : 0, vec);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float x[8];
+                    unpack8(raw[i], x);
+                    if (weight[i] != 0.f)      // (nothing was written for a part without a key)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) acc[j] = fmaf(weight[i], x[j], acc[j]);
+                }
+            }
+        if (live && c < S.d) store8(o + c, acc, S.d - c, out.o.acc);
     }
 }
 
@@ -117,9 +140,11 @@ __global__ void __launch_bounds__(kThreads) cross_sum(const SumJob j0, const Sum
     const int64_t row = item / heads;
     const int head = (int)(item - row * heads);
     if (!in_batch(off, batch, rows, row)) return;
+    sm100::pdl_wait();   // launched to overlap the end of the kernel that writes the parts
     float acc[8] = {};
     const float* p = J.part + item * d + c;
     const int64_t step = (int64_t)rows * heads * d;
+#pragma unroll 4
     for (int z = 0; z < parts; ++z) {
         float x[8];
         unpack8(load8<Mem::kOutput>(p + z * step, d - c, d % 4 == 0 ? 1 : 0), x);
@@ -165,15 +190,35 @@ bool tma_rows(const View& v) {
            v.row < ((int64_t)1 << 38) && v.head < ((int64_t)1 << 38);
 }
 
-// Parts into which the streamed side is cut so that `ctas` tiles fill the SMs, each of at least `least` steps.
-int parts_for(int64_t ctas, int per_sm, int64_t steps, int least) {
-    const int64_t want = (int64_t)per_sm * num_sms();
-    int64_t parts = ctas >= want ? 1 : want / std::max<int64_t>(1, ctas);
-    parts = std::min<int64_t>(parts, std::max<int64_t>(1, steps / least));
-    return (int)std::min<int64_t>(parts, kMaxSplits);
-}
-
 int64_t tiles_of(int n, int batch, int rows) { return std::max<int64_t>(batch, ((int64_t)n + rows - 1) / rows); }
+
+// What a pass costs: microseconds of a step of a CTA with the SM's other CTAs beside it, CTAs on an SM, and bytes that
+// each part writes and reads again.
+struct Cost {
+    double step;
+    int per_sm;
+    double bytes;
+};
+
+// Parts into which the streamed side is cut.  One sequence: `ctas` tiles of `steps` steps each run in whole waves; several: as many
+// of unlike length, so the longest (taken as twice the mean) ends last.  Every CTA starts and ends in about two steps' time;
+// parts are joined by another launch, and their sums go through L2 at about 5 TB/s.
+int parts_for(int64_t ctas, int64_t steps, int batch, const Cost& c) {
+    const int64_t slots = (int64_t)c.per_sm * num_sms();
+    double best = 0.0;
+    int64_t parts = 1;
+    for (int64_t p = 1; p <= std::min<int64_t>(kMaxSplits, std::max<int64_t>(1, steps / 2)); ++p) {
+        const double each = (double)((steps + p - 1) / p) + 2.0;
+        const double turns = batch == 1 ? (double)((ctas * p + slots - 1) / slots)
+                                        : std::max(1.0, (double)(ctas * p) / (double)slots) + 1.0;
+        const double us = turns * each * c.step + (p > 1 ? 5.0 + (double)p * c.bytes / 5e6 : 0.0);
+        if (p == 1 || us < best) {
+            best = us;
+            parts = p;
+        }
+    }
+    return (int)parts;
+}
 
 struct Plan {
     int fwd, dq, dkv;      // parts
@@ -181,18 +226,30 @@ struct Plan {
 
 Plan plan_of(const Shape& S, bool f32) {
     Plan p;
+    const double q_bytes = 12.0 * S.nq * S.h * S.d, k_bytes = 16.0 * S.nk * S.hk * S.d;
+    const double wide = S.d <= 64 ? 1.0 : 1.6;
+    const int few = few_rows(S);
+    if (few) {
+        // eight CTAs to an SM (more where the sequences are unlike), four turns of a CTA's warps at least to each
+        const int64_t tiles = tiles_of(S.nq, S.batch, few / S.g) * S.hk;
+        const int64_t want = (int64_t)(S.batch > 1 ? 16 : 8) * num_sms() / std::max<int64_t>(1, tiles);
+        int lanes = 1;
+        while (lanes * 8 < S.d) lanes *= 2;
+        p.fwd = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, kMaxSplits), S.nk / S.batch * lanes / 2048));
+    }
     if (f32) {
         const int tq = tile_queries(64, S.g);
         const int64_t qt = tiles_of(S.nq, S.batch, tq) * S.hk, kt = tiles_of(S.nk, S.batch, 64) * S.hk;
-        p.fwd = parts_for(qt, 2, S.nk / S.batch / 64, 2);
-        p.dq = parts_for(qt, 2, S.nk / S.batch / 64, 2);
-        p.dkv = parts_for(kt, 2, S.nq / S.batch / tq, 2);
+        const int64_t keys = (S.nk / S.batch + 63) / 64, queries = (S.nq / S.batch + tq - 1) / tq;
+        if (!few) p.fwd = parts_for(qt, keys, S.batch, Cost{2.0 * wide, 2, q_bytes});
+        p.dq = parts_for(qt, keys, S.batch, Cost{3.0 * wide, 2, q_bytes});
+        p.dkv = parts_for(kt, queries, S.batch, Cost{4.0 * wide, 2, k_bytes});
     } else {
-        const int keys = S.d <= 64 ? 128 : 64;
+        const int keys = S.d <= 64 ? 128 : 64, tq = tile_queries(64, S.g);
         const int64_t qt = tiles_of(S.nq, S.batch, tile_queries(128, S.g)) * S.hk, kt = tiles_of(S.nk, S.batch, 128) * S.hk;
-        p.fwd = parts_for(qt, S.batch > 1 ? 4 : 2, S.nk / S.batch / keys, 4);
-        p.dq = parts_for(qt, S.batch > 1 ? 4 : 2, S.nk / S.batch / 64, 4);
-        p.dkv = parts_for(kt, S.d <= 64 ? 2 : 1, S.nq / S.batch / tile_queries(64, S.g), 4);
+        if (!few) p.fwd = parts_for(qt, (S.nk / S.batch + keys - 1) / keys, S.batch, Cost{1.2, 2, q_bytes});
+        p.dq = parts_for(qt, (S.nk / S.batch + 63) / 64, S.batch, S.d <= 64 ? Cost{0.9, 2, q_bytes} : Cost{0.75, 1, q_bytes});
+        p.dkv = parts_for(kt, (S.nq / S.batch + tq - 1) / tq, S.batch, S.d <= 64 ? Cost{1.15, 2, k_bytes} : Cost{1.0, 1, k_bytes});
     }
     return p;
 }
@@ -278,8 +335,9 @@ int sum_parts(const SumJob& a, const SumJob& b, int jobs, const int32_t* off, in
               cudaStream_t s) {
     LaunchScope ls("cross_sum", s);
     const int64_t all = (int64_t)rows * heads * ((d + 7) / 8);
-    cross_sum<T><<<dim3((unsigned)((all + kThreads - 1) / kThreads), jobs), kThreads, 0, s>>>(a, b, off, batch, rows, heads, d,
-                                                                                          parts);
+    if (launch_overlapped(cross_sum<T>, dim3((unsigned)((all + kThreads - 1) / kThreads), jobs), dim3(kThreads), 0, s, a, b, off,
+                          batch, rows, heads, d, parts) != cudaSuccess)
+        return GT_ERR_CUDA;
     return check_launch();
 }
 
@@ -330,7 +388,7 @@ size_t gt_cross_attn_workspace_size(int32_t dtype, int32_t nq, int32_t nk, int32
     using namespace gt::cross;
     if (check_sizes(dtype, nq, nk, h, hk, d, batch) != GT_OK) return 0;
     const Shape S = shape_of(nq, nk, h, hk, d, batch, nullptr, nullptr, nullptr, 1.f);
-    const bool copies = dtype == GT_BF16 && !aligned;
+    const bool copies = dtype == GT_BF16 && !aligned && (backward || !few_rows(S));
     gt::Carve cv(nullptr, 0);
     const bool pack[4] = {copies, copies, copies, copies && backward};
     carve(cv, S, plan_of(S, dtype == GT_F32), backward != 0, pack);
@@ -351,13 +409,16 @@ int gt_cross_attn_fwd(int32_t dtype, int32_t nq, int32_t nk, int32_t h, int32_t 
     if (!usable(qv) || !usable(kv) || !usable(vv) || !o || !lse || ldo < 0 || hdo < 0) return GT_ERR_INVALID_ARG;
     const bool f32 = dtype == GT_F32;
     const Plan plan = plan_of(S, f32);
-    const bool pack[4] = {!f32 && !tma_rows(qv), !f32 && !tma_rows(kv), !f32 && !tma_rows(vv), false};
+    const bool few = few_rows(S) > 0, tma = !f32 && !few;
+    const bool pack[4] = {tma && !tma_rows(qv), tma && !tma_rows(kv), tma && !tma_rows(vv), false};
     gt::Carve cv(workspace, ws_bytes);
     const Room r = carve(cv, S, plan, false, pack);
     if (cv.off > 0 && (!workspace || !gt::aligned16(workspace) || !cv.fits())) return GT_ERR_WORKSPACE;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const FwdOut out{out_of(o, ldo, hdo, f32 ? 4 : 2), lse, r.o_part, r.lse_part, plan.fwd};
-    if (f32) {
+    if (few) {
+        rc = fwd_few(S, f32, qv, kv, vv, out, s);
+    } else if (f32) {
         rc = fwd_f32(S, qv, kv, vv, out, s);
     } else {
         View* views[4] = {&qv, &kv, &vv, nullptr};
@@ -369,9 +430,8 @@ int gt_cross_attn_fwd(int32_t dtype, int32_t nq, int32_t nk, int32_t h, int32_t 
     gt::LaunchScope ls("cross_join", s);
     const int64_t items = (int64_t)nq * h;
     const unsigned ctas = (unsigned)((items + kThreads / kJoinLanes - 1) / (kThreads / kJoinLanes));
-    if (f32) cross_join<float><<<ctas, kThreads, 0, s>>>(S, out);
-    else cross_join<bf16><<<ctas, kThreads, 0, s>>>(S, out);
-    return gt::check_launch();
+    const cudaError_t e = gt::launch_overlapped(f32 ? cross_join<float> : cross_join<bf16>, dim3(ctas), dim3(kThreads), 0, s, S, out);
+    return e == cudaSuccess ? gt::check_launch() : GT_ERR_CUDA;
 }
 
 int gt_cross_attn_bwd(int32_t dtype, int32_t nq, int32_t nk, int32_t h, int32_t hk, int32_t d, int32_t batch, const void* q,

@@ -21,33 +21,41 @@ constexpr int kHeld = 128;      // rows a CTA holds
 constexpr int kStep = 64;       // rows of a streamed tile
 constexpr uint32_t kHeldPanel = kHeld * 128, kStepPanel = kStep * 128;
 
+__device__ __forceinline__ float2 pair_of(uint32_t a, uint32_t b) {
+    return make_float2(__uint_as_float(a), __uint_as_float(b));
+}
+
 // ---------------------------------------------------------------------------- dq
 
+// Head dims up to 64: four warps, 256 TMEM columns, two CTAs to an SM, each one's products beside the other's
+// arithmetic.  Above: one CTA with two groups of four warps on tiles in turn, with scores of their own.  (What a CTA's
+// issuing warp does for a tile, one instruction after the other between the arithmetic warps', bounds it: one CTA with two or
+// three groups took longer than two CTAs with one, 4096x32768, 8 heads of 64: dq 567 and 422 us, dk and dv 599 and 495.)
 template <int PANELS>
 struct DqCfg {
-    static constexpr int kStages = PANELS == 1 ? 3 : 1;
+    static constexpr int kGroups = PANELS, kPerSm = 3 - PANELS;
+    static constexpr int kStages = PANELS == 1 ? 3 : 4;
     static constexpr uint32_t kHeldBytes = PANELS * kHeldPanel, kStepBytes = PANELS * kStepPanel;
     static constexpr size_t kSmem = 1024 + 2 * kHeldBytes + 2 * kStages * kStepBytes;
-    // TMEM columns: S at 0, dP at 64, dq at 128; dS beside them where there is room, else over S
-    static constexpr bool kOver = PANELS == 2;
-    static constexpr uint32_t kDp = 64, kAcc = 128, kDs = kOver ? 0 : 192, kTmem = 256;
-    static constexpr int kThreads = 192, kTmaWarp = 4, kMmaWarp = 5;
+    // TMEM columns: a group's S (dS over it) and dP, then dq
+    static constexpr uint32_t kAcc = 128 * kGroups, kTmem = 256 * PANELS;
+    static constexpr int kTmaWarp = 4 * kGroups, kMmaWarp = kTmaWarp + 1, kThreads = 32 * (kMmaWarp + 1);
 };
 
 struct DqBars {
-    uint64_t held_full, k_full[3], k_empty[3], v_full[3], v_empty[3];
-    uint64_t s_full, s_free, ds_full, acc_done, fin;
+    uint64_t held_full, k_full[4], k_empty[4], v_full[4], v_empty[4];
+    uint64_t s_full[2], ds_full[2], fin;
     uint32_t tmem_base;
     int abort;
 };
 
 template <int PANELS>
-__global__ void __launch_bounds__(DqCfg<PANELS>::kThreads, 2)
+__global__ void __launch_bounds__(DqCfg<PANELS>::kThreads, DqCfg<PANELS>::kPerSm)
 cross_dq(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
          const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
          const float2* __restrict__ stats, const Out dq, float* __restrict__ part, const int splits, int* status) {
     using C = DqCfg<PANELS>;
-    constexpr int kStages = C::kStages;
+    constexpr int kStages = C::kStages, kGroups = C::kGroups;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ DqBars bars;
@@ -71,10 +79,10 @@ cross_dq(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_
             mbar_init(&bars.v_full[s], 1);
             mbar_init(&bars.v_empty[s], 1);
         }
-        mbar_init(&bars.s_full, 1);
-        mbar_init(&bars.s_free, 4);
-        mbar_init(&bars.ds_full, 4);
-        mbar_init(&bars.acc_done, 1);
+        for (int b = 0; b < kGroups; ++b) {
+            mbar_init(&bars.s_full[b], 1);
+            mbar_init(&bars.ds_full[b], 4);
+        }
         mbar_init(&bars.fin, 1);
         bars.abort = 0;
         fence_barrier_init();
@@ -118,121 +126,115 @@ cross_dq(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_
     } else if (warp == C::kMmaWarp) {
         const uint32_t id_s = idesc_bf16(kHeld, kStep, false, false), id_acc = idesc_bf16(kHeld, 16 * steps, false, true);
         const SmemDesc a_q = smem_desc_split(smem_u32(sq), 16, 1024, 2), a_do = smem_desc_split(smem_u32(sdo), 16, 1024, 2);
-        auto gradients = [&](int i) {      // dq += dS k of tile i
+        const SmemDesc b_k = smem_desc_split(smem_u32(sk), 16, 1024, 2), b_v = smem_desc_split(smem_u32(sv), 16, 1024, 2);
+        const SmemDesc r_k = smem_desc_split(smem_u32(sk), kStepPanel, 1024, 2);      // along its rows
+        auto at = [](SmemDesc d, int s) { return SmemDesc{d.lo + s * (C::kStepBytes >> 4), d.hi}; };
+        // What can be done ahead of a tile's products: its keys have landed, those that nobody sees are cleared.
+        auto ready = [&](int i) {
             const int s = i % kStages;
-            if (!w.all(&bars.ds_full, i & 1)) return;
-            tc_fence_after();
-            const SmemDesc b_k = smem_desc_split(smem_u32(sk + s * C::kStepBytes), kStepPanel, 1024, 2);
-            if (elect_one()) {
-                product_rows<kStep>(tb + C::kAcc, tb + C::kDs, b_k, id_acc, i > 0);
-                mma_commit(&bars.k_empty[s]);
-                mma_commit(&bars.acc_done);
-            }
-            __syncwarp();
-        };
-        if (n > 0) w.all(&bars.held_full, 0);
-        for (int i = 0; i < n && w.ok; ++i) {
-            const int s = i % kStages;
-            if (C::kOver && i > 0) {      // dS of the last tile stands where these scores will
-                gradients(i - 1);
-                w.all(&bars.acc_done, (i - 1) & 1);
-            }
-            if (!w.all(&bars.k_full[s], (i / kStages) & 1) || !w.all(&bars.v_full[s], (i / kStages) & 1)) break;
+            if (!w.all(&bars.k_full[s], (i / kStages) & 1) || !w.all(&bars.v_full[s], (i / kStages) & 1)) return;
             uint32_t words[kStep / 32];
             if (!valid_keys(S, t.k0 + (t0 + i) * kStep, t.k0 + t.lk, words))
                 clear_rows<kStep / 32, PANELS>(smem_u32(sk + s * C::kStepBytes), kStepPanel, words);
-            if (i > 0 && !w.all(&bars.s_free, (i - 1) & 1)) break;
+        };
+        auto scores = [&](int i) {      // by one lane
+            const int s = i % kStages, b = i % kGroups;
+            product_channels<PANELS>(tb + 128 * b, a_q, kHeldPanel, at(b_k, s), kStepPanel, steps, id_s);
+            product_channels<PANELS>(tb + 128 * b + 64, a_do, kHeldPanel, at(b_v, s), kStepPanel, steps, id_s);
+            mma_commit(&bars.v_empty[s]);
+            mma_commit(&bars.s_full[b]);
+        };
+        if (n > 0) w.all(&bars.held_full, 0);
+        for (int i = 0; i < kGroups && i < n && w.ok; ++i) {
+            ready(i);
             tc_fence_after();
-            const SmemDesc b_k = smem_desc_split(smem_u32(sk + s * C::kStepBytes), 16, 1024, 2);
-            const SmemDesc b_v = smem_desc_split(smem_u32(sv + s * C::kStepBytes), 16, 1024, 2);
+            if (w.ok && elect_one()) scores(i);
+            __syncwarp();
+        }
+        for (int i = 0; i < n && w.ok; ++i) {
+            const int s = i % kStages, b = i % kGroups;
+            if (kGroups == 1 && i + 1 < n) ready(i + 1);
+            if (!w.ok || !w.all(&bars.ds_full[b], (i / kGroups) & 1)) break;
+            tc_fence_after();
             if (elect_one()) {
-                product_channels<PANELS>(tb, a_q, kHeldPanel, b_k, kStepPanel, steps, id_s);
-                product_channels<PANELS>(tb + C::kDp, a_do, kHeldPanel, b_v, kStepPanel, steps, id_s);
-                mma_commit(&bars.v_empty[s]);
-                mma_commit(&bars.s_full);
+                // dq += dS k, and behind it the next scores where dS stands (the tensor pipe runs one thread's products
+                // in order)
+                product_rows<kStep>(tb + C::kAcc, tb + 128 * b, at(r_k, s), id_acc, i > 0);
+                mma_commit(&bars.k_empty[s]);
+                if (kGroups == 1 && i + 1 < n) scores(i + 1);
             }
             __syncwarp();
-            if (!C::kOver && i > 0) gradients(i - 1);
+            if (kGroups > 1 && i + kGroups < n) {      // (these rows may still be on their way: not before the products)
+                ready(i + kGroups);
+                tc_fence_after();
+                if (w.ok && elect_one()) scores(i + kGroups);
+                __syncwarp();
+            }
         }
-        if (n > 0 && w.ok) gradients(n - 1);
-        if (!w.ok) {
-            if (lane == 0) tc::fail(&bars.abort, status);
-            int never = 0;
-            if (elect_one()) mma_commit(&bars.fin);
-            __syncwarp();
-            mbar_wait_all(&bars.fin, 0, &never, tc::kWaitNs);
-        }
+        if (!w.ok && lane == 0) tc::fail(&bars.abort, status);
+        int never = 0;
+        if (elect_one()) mma_commit(&bars.fin);      // all products
+        __syncwarp();
+        mbar_wait_all(&bars.fin, 0, &never, tc::kWaitNs);
     } else {
-        const int r = warp * 32 + lane;
-        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-        const bool some = warp * 32 < live, mine = r < live;
+        const int group = warp >> 2, r = (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, ts = tb + lanes + 128 * group;
+        const bool some = (warp & 3) * 32 < live, mine = r < live;      // a warp without rows only keeps the barriers going
         const float c = S.scale * tc::kLog2e;
-        const float2 st = mine ? __ldg(stats + ((int64_t)head * S.nq + t.q0 + first) * S.g + r) : make_float2(INFINITY, 0.f);
-        for (int i = 0; i < n; ++i) {
+        const float2 st = mine ? __ldg(stats + ((int64_t)head * S.nq + t.q0 + first) * S.g + r) : make_float2(-INFINITY, 0.f);
+        const float2 c2 = make_float2(c, c), minus_lse = make_float2(st.x, st.x), minus_d = make_float2(st.y, st.y);
+        for (int i = group; i < n; i += kGroups) {
             uint32_t words[kStep / 32];
             const bool all = valid_keys(S, t.k0 + (t0 + i) * kStep, t.k0 + t.lk, words);
-            if (!w.all(&bars.s_full, i & 1)) break;
+            if (!w.all(&bars.s_full[group], (i / kGroups) & 1)) break;
             tc_fence_after();
-            uint32_t ds[2][16];
             if (some) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    uint32_t x[32], y[32];
-                    tmem_ld_x32(tb + lanes + 32 * k, x);
-                    tmem_ld_x32(tb + lanes + C::kDp + 32 * k, y);
+                    uint32_t x[32], y[32], ds[16];
+                    tmem_ld_x32(ts + 32 * k, x);
+                    tmem_ld_x32(ts + 64 + 32 * k, y);
                     tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
-                        float e[2];
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const float p = ex2(fmaf(__uint_as_float(x[j + u]), c, -st.x));
-                            e[u] = p * (__uint_as_float(y[j + u]) - st.y);
-                        }
-                        ds[k][j / 2] = pack_bf16x2(e[0], e[1]);
+                        const float2 a = pair_of(x[j], x[j + 1]), b = pair_of(y[j], y[j + 1]);
+                        const float2 t = __ffma2_rn(a, c2, minus_lse);
+                        const float2 g = __fmul2_rn(make_float2(ex2(t.x), ex2(t.y)), __fadd2_rn(b, minus_d));
+                        ds[j / 2] = pack_bf16x2(g.x, g.y);
                     }
                     if (!all) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            ds[k][j] &= (((words[k] >> (2 * j)) & 1u) ? 0xffffu : 0u) |
-                                        (((words[k] >> (2 * j + 1)) & 1u) ? 0xffff0000u : 0u);
+                            ds[j] &= (((words[k] >> (2 * j)) & 1u) ? 0xffffu : 0u) |
+                                     (((words[k] >> (2 * j + 1)) & 1u) ? 0xffff0000u : 0u);
                     }
+                    tmem_st_x16(ts + 16 * k, ds);
                 }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.s_free);
-            if (i > 0 && !w.all(&bars.acc_done, (i - 1) & 1)) break;      // the last dS has been read
-            if (some) {
-                tmem_st_x16(tb + lanes + C::kDs, ds[0]);
-                tmem_st_x16(tb + lanes + C::kDs + 16, ds[1]);
                 tmem_wait_st();
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.ds_full);
+            if (lane == 0) mbar_arrive(&bars.ds_full[group]);
         }
-        if (n > 0 && w.ok) w.all(&bars.acc_done, (n - 1) & 1);
+        w.all(&bars.fin, 0);
         if (!w.ok && lane == 0) tc::fail(&bars.abort, status);
         tc_fence_after();
         if (some && w.ok) {
             const int64_t query = t.q0 + first + r / S.g;
             const int qh = head * S.g + r % S.g;
-            if (splits == 1) {
-                bf16* p = static_cast<bf16*>(dq.p) + query * dq.row + qh * dq.head;
+            bf16* p = static_cast<bf16*>(dq.p) + query * dq.row + qh * dq.head;
+            float* f = part + ((z * (int64_t)S.nq + query) * S.h + qh) * S.d;
+            for (int k = group; k < steps; k += kGroups) {      // the groups share the columns
+                uint32_t o[16];
                 if (n > 0) {
-                    tmem_row_out(tb + lanes + C::kAcc, steps, p, S.d, S.scale, mine, dq.acc);
-                } else if (mine) {
-                    const float zero[16] = {};
-                    for (int k = 0; k < steps; ++k) put16(p, 16 * k, S.d, zero, dq.acc);
+                    tmem_ld_x16(tb + lanes + C::kAcc + 16 * k, o);
+                    tmem_wait_ld();
                 }
-            } else {
-                float* p = part + ((z * (int64_t)S.nq + query) * S.h + qh) * S.d;
-                if (n > 0) {
-                    tmem_row_out(tb + lanes + C::kAcc, steps, p, S.d, S.scale, mine, S.d % 4 == 0 ? 1 : 0);
-                } else if (mine) {
-                    for (int k = 0; k < S.d; ++k) p[k] = 0.f;
-                }
+                float v[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = n > 0 ? __uint_as_float(o[j]) * S.scale : 0.f;
+                if (mine && splits == 1) put16(p, 16 * k, S.d, v, dq.acc);
+                else if (mine) put16(f, 16 * k, S.d, v, S.d % 4 == 0 ? 1 : 0);
             }
         }
         tc_fence_before();
@@ -244,12 +246,11 @@ cross_dq(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_
 
 // ---------------------------------------------------------------------------- dk, dv
 
-// Head dims up to 64: one group of four warps, 256 TMEM columns, two CTAs to an SM, each one's products beside the other's
-// arithmetic.  Above: two groups on alternate tiles, with scores of their own, and one CTA.
+// CTAs and groups as for dq.
 template <int PANELS>
 struct DkvCfg {
-    static constexpr int kGroups = PANELS;
-    static constexpr int kStages = 3;
+    static constexpr int kGroups = PANELS, kPerSm = 3 - PANELS;
+    static constexpr int kStages = PANELS == 1 ? 3 : 4;
     static constexpr uint32_t kHeldBytes = PANELS * kHeldPanel, kStepBytes = PANELS * kStepPanel;
     static constexpr size_t kSmem = 1024 + 2 * kHeldBytes + 2 * kStages * kStepBytes;
     // TMEM columns: a group's S and dP (p and dS over them), then dv, then dk
@@ -258,14 +259,14 @@ struct DkvCfg {
 };
 
 struct DkvBars {
-    uint64_t held_full, q_full[3], q_empty[3];
-    uint64_t s_full[2], p_full[2], acc_done[2], fin;
+    uint64_t held_full, q_full[4], q_empty[4];
+    uint64_t s_full[2], p_full[2], fin;
     uint32_t tmem_base;
     int abort;
 };
 
 template <int PANELS>
-__global__ void __launch_bounds__(DkvCfg<PANELS>::kThreads, 3 - PANELS)
+__global__ void __launch_bounds__(DkvCfg<PANELS>::kThreads, DkvCfg<PANELS>::kPerSm)
 cross_dkv(const Shape S, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
           const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
           const float2* __restrict__ stats, const Out dk, const Out dv, float* __restrict__ dk_part,
@@ -275,7 +276,7 @@ cross_dkv(const Shape S, const __grid_constant__ CUtensorMap map_k, const __grid
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ DkvBars bars;
-    __shared__ alignas(16) float2 st[kStages][kStep];
+    __shared__ alignas(16) float st_lse[kStages][kStep], st_d[kStages][kStep];
     const int tq = tile_queries(kStep, S.g), head = blockIdx.y, z = blockIdx.z;
     const Tile t = find_tile(S, false, kHeld, blockIdx.x);
     if (!t.live) return;
@@ -297,7 +298,6 @@ cross_dkv(const Shape S, const __grid_constant__ CUtensorMap map_k, const __grid
         for (int b = 0; b < kGroups; ++b) {
             mbar_init(&bars.s_full[b], 1);
             mbar_init(&bars.p_full[b], 4);
-            mbar_init(&bars.acc_done[b], 1);
         }
         mbar_init(&bars.fin, 1);
         bars.abort = 0;
@@ -325,11 +325,13 @@ cross_dkv(const Shape S, const __grid_constant__ CUtensorMap map_k, const __grid
         for (; i < n; ++i) {
             const int s = i % kStages, q0 = t.q0 + (t0 + i) * tq, live = rows_of(i);
             const float2* src = stats + ((int64_t)head * S.nq + q0) * S.g;
-            const float2 none = make_float2(INFINITY, 0.f);
+            const float2 none = make_float2(-INFINITY, 0.f);
             const float2 a = lane < live ? __ldg(src + lane) : none, b = lane + 32 < live ? __ldg(src + lane + 32) : none;
             if (!w.all(&bars.q_empty[s], ((i / kStages) & 1) ^ 1)) break;
-            st[s][lane] = a;
-            st[s][lane + 32] = b;
+            st_lse[s][lane] = a.x;
+            st_lse[s][lane + 32] = b.x;
+            st_d[s][lane] = a.y;
+            st_d[s][lane + 32] = b.y;
             __syncwarp();
             if (elect_one()) {
                 mbar_arrive_expect_tx(&bars.q_full[s], 2 * PANELS * tq * S.g * 128);
@@ -346,43 +348,54 @@ cross_dkv(const Shape S, const __grid_constant__ CUtensorMap map_k, const __grid
     } else if (warp == C::kMmaWarp) {
         const uint32_t id_s = idesc_bf16(kHeld, kStep, false, false), id_acc = idesc_bf16(kHeld, 16 * steps, false, true);
         const SmemDesc a_k = smem_desc_split(smem_u32(sk), 16, 1024, 2), a_v = smem_desc_split(smem_u32(sv), 16, 1024, 2);
-        auto gradients = [&](int i) {      // dv += p^T dO, dk += dS^T q of tile i
-            const int s = i % kStages, b = i % kGroups;
-            if (!w.all(&bars.p_full[b], (i / kGroups) & 1)) return;
-            tc_fence_after();
-            const SmemDesc b_q = smem_desc_split(smem_u32(sq + s * C::kStepBytes), kStepPanel, 1024, 2);
-            const SmemDesc b_do = smem_desc_split(smem_u32(sdo + s * C::kStepBytes), kStepPanel, 1024, 2);
-            if (elect_one()) {
-                product_rows<kStep>(tb + C::kDv, tb + 128 * b, b_do, id_acc, i > 0);
-                product_rows<kStep>(tb + C::kDk, tb + 128 * b + 64, b_q, id_acc, i > 0);
-                mma_commit(&bars.q_empty[s]);
-                mma_commit(&bars.acc_done[b]);
-            }
-            __syncwarp();
-        };
-        if (n > 0) w.all(&bars.held_full, 0);
-        for (int i = 0; i < n && w.ok; ++i) {
-            const int s = i % kStages, b = i % kGroups;
-            if (!w.all(&bars.q_full[s], (i / kStages) & 1)) break;
+        const SmemDesc b_q = smem_desc_split(smem_u32(sq), 16, 1024, 2), b_do = smem_desc_split(smem_u32(sdo), 16, 1024, 2);
+        const SmemDesc r_q = smem_desc_split(smem_u32(sq), kStepPanel, 1024, 2);      // along its rows
+        const SmemDesc r_do = smem_desc_split(smem_u32(sdo), kStepPanel, 1024, 2);
+        auto at = [](SmemDesc d, int s) { return SmemDesc{d.lo + s * (C::kStepBytes >> 4), d.hi}; };
+        // What can be done ahead of a tile's products: its rows have landed, those behind its sequence are cleared.
+        auto ready = [&](int i) {
+            const int s = i % kStages;
+            if (!w.all(&bars.q_full[s], (i / kStages) & 1)) return;
             const int live = rows_of(i);
-            if (live < kStep) {      // the rows behind belong to the next sequence, or are nothing at all
+            if (live < kStep) {
                 clear_tail<PANELS>(smem_u32(sq + s * C::kStepBytes), kStepPanel, live, kStep);
                 clear_tail<PANELS>(smem_u32(sdo + s * C::kStepBytes), kStepPanel, live, kStep);
             }
-            // p and dS of the group's last tile stand where these scores will
-            if (i >= kGroups && !w.all(&bars.acc_done[b], (i / kGroups - 1) & 1)) break;
+        };
+        auto scores = [&](int i) {      // by one lane
+            const int s = i % kStages, b = i % kGroups;
+            product_channels<PANELS>(tb + 128 * b, a_k, kHeldPanel, at(b_q, s), kStepPanel, steps, id_s);
+            product_channels<PANELS>(tb + 128 * b + 64, a_v, kHeldPanel, at(b_do, s), kStepPanel, steps, id_s);
+            mma_commit(&bars.s_full[b]);
+        };
+        if (n > 0) w.all(&bars.held_full, 0);
+        for (int i = 0; i < kGroups && i < n && w.ok; ++i) {
+            ready(i);
             tc_fence_after();
-            const SmemDesc b_q = smem_desc_split(smem_u32(sq + s * C::kStepBytes), 16, 1024, 2);
-            const SmemDesc b_do = smem_desc_split(smem_u32(sdo + s * C::kStepBytes), 16, 1024, 2);
+            if (w.ok && elect_one()) scores(i);
+            __syncwarp();
+        }
+        for (int i = 0; i < n && w.ok; ++i) {
+            const int s = i % kStages, b = i % kGroups;
+            if (kGroups == 1 && i + 1 < n) ready(i + 1);
+            if (!w.ok || !w.all(&bars.p_full[b], (i / kGroups) & 1)) break;
+            tc_fence_after();
             if (elect_one()) {
-                product_channels<PANELS>(tb + 128 * b, a_k, kHeldPanel, b_q, kStepPanel, steps, id_s);
-                product_channels<PANELS>(tb + 128 * b + 64, a_v, kHeldPanel, b_do, kStepPanel, steps, id_s);
-                mma_commit(&bars.s_full[b]);
+                // dv += p^T dO, dk += dS^T q, and behind them the next scores where p and dS stand (the tensor pipe runs one
+                // thread's products in order)
+                product_rows<kStep>(tb + C::kDv, tb + 128 * b, at(r_do, s), id_acc, i > 0);
+                product_rows<kStep>(tb + C::kDk, tb + 128 * b + 64, at(r_q, s), id_acc, i > 0);
+                mma_commit(&bars.q_empty[s]);
+                if (kGroups == 1 && i + 1 < n) scores(i + 1);
             }
             __syncwarp();
-            if (i >= kGroups - 1) gradients(i - kGroups + 1);
+            if (kGroups > 1 && i + kGroups < n) {      // (these rows may still be on their way: not before the products)
+                ready(i + kGroups);
+                tc_fence_after();
+                if (w.ok && elect_one()) scores(i + kGroups);
+                __syncwarp();
+            }
         }
-        for (int i = max(0, n - kGroups + 1); i < n && w.ok; ++i) gradients(i);
         if (!w.ok && lane == 0) tc::fail(&bars.abort, status);
         int never = 0;
         if (elect_one()) mma_commit(&bars.fin);      // all products
@@ -392,12 +405,13 @@ cross_dkv(const Shape S, const __grid_constant__ CUtensorMap map_k, const __grid
         const int group = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, ts = tb + lanes + 128 * group;
         const float c = S.scale * tc::kLog2e;
+        const float2 c2 = make_float2(c, c);
         for (int i = group; i < n; i += kGroups) {
             const int s = i % kStages;
             const uint32_t turn = (i / kGroups) & 1;
             if (!w.all(&bars.q_full[s], (i / kStages) & 1) || !w.all(&bars.s_full[group], turn)) break;
             tc_fence_after();
-            const uint32_t sst = smem_u32(st[s]);
+            const uint32_t s_lse = smem_u32(st_lse[s]), s_d = smem_u32(st_d[s]);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 uint32_t x[32], y[32], p[16], ds[16];
@@ -405,13 +419,17 @@ cross_dkv(const Shape S, const __grid_constant__ CUtensorMap map_k, const __grid
                 tmem_ld_x32(ts + 64 + 32 * k, y);
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 32; j += 2) {
-                    const uint4 q4 = lds_u4(sst + 8 * (32 * k + j));     // lse and D of two queries
-                    const float pa = ex2(fmaf(__uint_as_float(x[j]), c, -__uint_as_float(q4.x)));
-                    const float pb = ex2(fmaf(__uint_as_float(x[j + 1]), c, -__uint_as_float(q4.z)));
-                    p[j / 2] = pack_bf16x2(pa, pb);
-                    ds[j / 2] = pack_bf16x2(pa * (__uint_as_float(y[j]) - __uint_as_float(q4.y)),
-                                            pb * (__uint_as_float(y[j + 1]) - __uint_as_float(q4.w)));
+                for (int j = 0; j < 32; j += 4) {
+                    const uint4 l4 = lds_u4(s_lse + 4 * (32 * k + j)), d4 = lds_u4(s_d + 4 * (32 * k + j));   // of four queries
+#pragma unroll
+                    for (int u = 0; u < 4; u += 2) {
+                        const float2 a = pair_of(x[j + u], x[j + u + 1]), b = pair_of(y[j + u], y[j + u + 1]);
+                        const float2 t = __ffma2_rn(a, c2, u ? pair_of(l4.z, l4.w) : pair_of(l4.x, l4.y));
+                        const float2 e = make_float2(ex2(t.x), ex2(t.y));
+                        const float2 g = __fmul2_rn(e, __fadd2_rn(b, u ? pair_of(d4.z, d4.w) : pair_of(d4.x, d4.y)));
+                        p[(j + u) / 2] = pack_bf16x2(e.x, e.y);
+                        ds[(j + u) / 2] = pack_bf16x2(g.x, g.y);
+                    }
                 }
                 tmem_st_x16(ts + 16 * k, p);
                 tmem_st_x16(ts + 64 + 16 * k, ds);

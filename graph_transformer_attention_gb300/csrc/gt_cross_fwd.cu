@@ -70,6 +70,7 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ Bars bars;
     const int tq = tile_queries(kRows, S.g), head = blockIdx.y, z = blockIdx.z;
+    pdl_trigger();      // (the kernel that joins the parts may be scheduled; it waits for this one)
     const Tile t = find_tile(S, true, tq, blockIdx.x);
     if (!t.live) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -196,8 +197,6 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
         const float most = 8.f / c;              // scores above the base
         float base = -INFINITY, sum = 0.f;       // (the base in scores before scaling)
         for (int i = 0; i < n; ++i) {
-            uint32_t words[kChunks];
-            const bool all = valid_keys(S, t.k0 + (t0 + i) * kKeys, t.k0 + t.lk, words);
             if (!w.all(&bars.s_full, i & 1)) break;
             tc_fence_after();
             if (!some) {
@@ -213,7 +212,8 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.s_free);
-            if (!all) {
+            uint32_t words[kChunks];      // (not formed any earlier: the scores take nearly all registers)
+            if (!valid_keys(S, t.k0 + (t0 + i) * kKeys, t.k0 + t.lk, words)) {
 #pragma unroll
                 for (int k = 0; k < kChunks; ++k)
 #pragma unroll

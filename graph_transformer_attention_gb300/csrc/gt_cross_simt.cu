@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kThreads) cross_bwd_f32(const Shape S, const B
         if (threadIdx.x < kRows)
             stat[threadIdx.x] = (int)threadIdx.x < live
                                     ? __ldg(in.stats + ((int64_t)head * S.nq + t.q0 + first) * S.g + threadIdx.x)
-                                    : make_float2(INFINITY, 0.f);
+                                    : make_float2(-INFINITY, 0.f);
     };
     if (KEYS) keys_of(t.tile, a1, a2);
     else queries_of(t.tile, a1, a2);
@@ -308,9 +308,9 @@ __global__ void __launch_bounds__(kThreads) cross_bwd_f32(const Shape S, const B
                 const int held = 4 * ty + i, other = tx + 16 * j;
                 const float2 st = stat[KEYS ? other : held];
                 const bool seen = keep[KEYS ? held : other];
-                const float p = seen ? exp2f(fmaf(x[i][j], c, -st.x)) : 0.f;
+                const float p = seen ? exp2f(fmaf(x[i][j], c, st.x)) : 0.f;
                 x[i][j] = p;
-                y[i][j] = seen ? p * (y[i][j] - st.y) : 0.f;
+                y[i][j] = seen ? p * (y[i][j] + st.y) : 0.f;
             }
         put_weights<DP>(w1, ty, tx, y);
         if (KEYS) put_weights<DP>(w2, ty, tx, x);

@@ -16,7 +16,6 @@ namespace gt {
 namespace cross {
 
 using namespace sm100;
-using bf16 = __nv_bfloat16;
 
 // Map of [rows][heads][d] with a box of 64 channels, `heads_box` heads and `rows_box` rows.
 inline bool heads_map(CUtensorMap* map, const View& v, int rows, int heads, int d, int heads_box, int rows_box) {
@@ -38,11 +37,15 @@ __device__ __forceinline__ void load_panels(uint8_t* dst, uint32_t panel_bytes, 
 template <int PANELS>
 __device__ __forceinline__ void product_channels(uint32_t d_tmem, SmemDesc a, uint32_t a_panel, SmemDesc b, uint32_t b_panel,
                                                  int steps, uint32_t idesc) {
+    auto step = [&](int k) {
+        mma_ss(d_tmem, desc_at(a, (k >> 2) * a_panel + (k & 3) * 32), desc_at(b, (k >> 2) * b_panel + (k & 3) * 32), idesc, k > 0);
+    };
+    if (steps == 4 * PANELS) {      // (a fixed number goes out without a test between the products)
 #pragma unroll
-    for (int k = 0; k < 4 * PANELS; ++k)
-        if (k < steps)
-            mma_ss(d_tmem, desc_at(a, (k >> 2) * a_panel + (k & 3) * 32), desc_at(b, (k >> 2) * b_panel + (k & 3) * 32), idesc,
-                   k > 0);
+        for (int k = 0; k < 4 * PANELS; ++k) step(k);
+    } else {
+        for (int k = 0; k < steps; ++k) step(k);
+    }
 }
 
 // D (+)= W B along B's ROWS rows, W in TMEM (bf16, 8 columns to 16 rows).

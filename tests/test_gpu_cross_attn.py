@@ -239,6 +239,27 @@ def test_long_sides(gt, t):
         _both(gt, _t((nq, h, c), t, 1), _t((nk, hk, c), t, 2), _t((nk, hk, c), t, 3))
 
 
+@pytest.mark.parametrize("t", [F, B])
+@pytest.mark.parametrize("share", [1, 2, 3, 4, 8])
+@pytest.mark.parametrize("c", [5, 8, 16, 30, 64, 100, 128])
+def test_single_queries(gt, c, share, t):
+    """The next token of each of some decoders: ragged keys, an empty side, a sequence with more queries than most."""
+    ck = [0, 0, 1, 70, 571, 640, 2000]
+    cq = [0, 1, 2, 3, 3, 4, 6 + 2]
+    hk = 2
+    q, k, v = _t((cq[-1], share * hk, c), t, 1), _t((2004, hk, c), t, 2), _t((2004, hk, c), t, 3)
+    mask = torch.arange(2004, device="cuda") % 7 != 3
+    k[2000:], v[2000:], k[~mask] = math.nan, math.inf, math.nan
+    qo, ko = _off(*cq), _off(*ck)
+    o, lse = gt.gt_cross_attn_fwd(q, k, v, qo, ko, mask)
+    ref = X.attn_fwd(q, k, v, qo, ko, mask)
+    empty = ref["lse"][0] == -math.inf
+    assert ((lse.cpu() == -math.inf) == empty).all() and bool(empty[:, 0].all()) and (o.cpu()[empty.t()] == 0).all()
+    R.check({"o": o, "lse": lse.cpu().masked_fill(empty, 0)},
+            {"o": ref["o"], "lse": (ref["lse"][0].masked_fill(empty, 0), ref["lse"][1])})
+    assert all(torch.equal(a, b) for a, b in zip(gt.gt_cross_attn_fwd(q, k, v, qo, ko, mask), (o, lse)))
+
+
 def test_offsets_past_32_bits(gt):
     """Keys and values of more than 2^31 elements each: the last sequence as a call for it alone."""
     nk, hk, c, tail = 140001, 128, 128, 700
