@@ -12,7 +12,7 @@
 // Sequences come as device offsets, so the host does not know their lengths.  A tile of T rows of sequence b is slot
 // offset[b] / T + b + tile: ceil(length / T) <= offset[b + 1] / T - offset[b] / T + 1, so the slots of a sequence end
 // before the next one's begin, n / T + batch slots hold every tile whatever the lengths, and a CTA finds its tile by a
-// binary search over the offsets.  Slots without a tile return at once.
+// search over the offsets.  Slots without a tile return at once.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -69,12 +69,15 @@ __device__ __forceinline__ int clamp_off(const int32_t* off, int b, int n) {
 __device__ __forceinline__ Tile find_tile(const Shape& S, bool by_q, int rows, int slot) {
     if (!S.q_off) return Tile{0, S.nq, 0, S.nk, slot, (int64_t)slot * rows < (by_q ? S.nq : S.nk)};
     const int32_t* off = by_q ? S.q_off : S.kv_off;
-    const int n = by_q ? S.nq : S.nk;
-    int lo = 0, hi = S.batch;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (clamp_off(off, mid, n) / rows + mid <= slot) lo = mid;
-        else hi = mid;
+    const int n = by_q ? S.nq : S.nk, lane = threadIdx.x & 31;
+    // the last sequence whose slots begin at or in front of this one, a lane a candidate (whole warps)
+    int lo = 0, len = S.batch;
+    while (len > 1) {
+        const int step = (len + 31) / 32, at = lo + lane * step;
+        const bool in = lane * step < len && clamp_off(off, at, n) / rows + at <= slot;
+        const int last = max(__popc(__ballot_sync(0xffffffffu, in)) - 1, 0);
+        lo += last * step;
+        len = min(step, len - last * step);
     }
     Tile t;
     t.q0 = clamp_off(S.q_off, lo, S.nq);
@@ -184,6 +187,9 @@ struct BwdIn {
     const float2* stats;     // [hk][nq][g]: -lse log2 e (-infinity for a query without a key) and -D
 };
 
+// Whether the tensor-core forward takes tiles of kFewTile rows: a sequence of mean length has no more.
+constexpr int kFewTile = 32;
+bool few_tile(const Shape& S);
 // Rows of a tile of the few-rows forward; 0: the call has too many.
 int few_rows(const Shape& S);
 int fwd_few(const Shape& S, bool f32, const View& q, const View& k, const View& v, const FwdOut& out, cudaStream_t s);

@@ -24,21 +24,26 @@ namespace {
 constexpr int kRows = 128;
 constexpr int kTmaWarp = 4, kMmaWarp = 5;
 constexpr int kThreads = 192;
-constexpr int kStages = 2;
 
-template <int PANELS>
+// FEW: tiles of 32 rows.  The bytes of the keys bound these, and a third tile of keys and of values is on its way in the room
+// that the rows leave.  (The tensor core still reads 128 rows from where the queries begin: the rest is whatever stands
+// there, and stays in rows that nobody looks at.)
+template <int PANELS, bool FEW>
 struct Cfg {
+    static constexpr int kStages = FEW ? 3 : 2, kTile = FEW ? kFewTile : kRows;
     static constexpr int kKeys = PANELS == 1 ? 128 : 64;        // of a tile
-    static constexpr uint32_t kQPanel = kRows * 128, kKvPanel = kKeys * 128;
+    static constexpr uint32_t kQPanel = kTile * 128, kKvPanel = kKeys * 128;
     static constexpr uint32_t kQ = PANELS * kQPanel, kKv = PANELS * kKvPanel;
     static constexpr size_t kSmem = 1024 + kQ + 2 * kStages * kKv;
-    static constexpr uint32_t kP = PANELS == 1 ? 128 : 64, kO = PANELS == 1 ? 192 : 128;   // TMEM columns; S at 0
+    // TMEM columns: S at 0, then P (two buffers where there is room), then O
+    static constexpr int kBuffers = PANELS;
+    static constexpr uint32_t kP = kKeys, kO = PANELS == 1 ? 192 : 128;
     static constexpr uint32_t kTmem = 256;
 };
 
 struct Bars {
-    uint64_t q_full, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-    uint64_t s_full, s_free, p_full, o_done, fin;
+    uint64_t q_full, k_full[3], k_empty[3], v_full[3], v_empty[3];
+    uint64_t s_full, s_free, p_full[2], o_done[2], fin;
     uint32_t tmem_base;
     int abort;
 };
@@ -60,16 +65,16 @@ __device__ __forceinline__ void weights(const uint32_t (&x)[32], float2 c, float
     }
 }
 
-template <int PANELS>
+template <int PANELS, bool FEW>
 __global__ void __launch_bounds__(kThreads, 2)
 cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
           const __grid_constant__ CUtensorMap map_v, const FwdOut out, int* status) {
-    using C = Cfg<PANELS>;
-    constexpr int kKeys = C::kKeys, kChunks = kKeys / 32;
+    using C = Cfg<PANELS, FEW>;
+    constexpr int kKeys = C::kKeys, kChunks = kKeys / 32, kStages = C::kStages, kBuffers = C::kBuffers;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ Bars bars;
-    const int tq = tile_queries(kRows, S.g), head = blockIdx.y, z = blockIdx.z;
+    const int tq = tile_queries(C::kTile, S.g), head = blockIdx.y, z = blockIdx.z;
     pdl_trigger();      // (the kernel that joins the parts may be scheduled; it waits for this one)
     const Tile t = find_tile(S, true, tq, blockIdx.x);
     if (!t.live) return;
@@ -91,8 +96,10 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
         }
         mbar_init(&bars.s_full, 1);
         mbar_init(&bars.s_free, 4);
-        mbar_init(&bars.p_full, 4);
-        mbar_init(&bars.o_done, 1);
+        for (int b = 0; b < C::kBuffers; ++b) {
+            mbar_init(&bars.p_full[b], 4);
+            mbar_init(&bars.o_done[b], 1);
+        }
         mbar_init(&bars.fin, 1);
         bars.abort = 0;
         fence_barrier_init();
@@ -115,36 +122,36 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
             }
             __syncwarp();
         }
-        int i = 0;
-        for (; i < n; ++i) {
-            const int s = i % kStages, row = t.k0 + (t0 + i) * kKeys;
-            const uint32_t parity = ((i / kStages) & 1) ^ 1;      // (the first time round finds every stage empty)
-            if (!w.all(&bars.k_empty[s], parity)) break;
+        // keys a tile ahead of the values: their stage is free long before
+        auto load = [&](int i, uint8_t* to, const CUtensorMap* map, uint64_t* full, uint64_t* empty) {
+            const int s = i % kStages;
+            // (the first time round finds every stage empty)
+            if (!w.all(&empty[s], ((i / kStages) & 1) ^ 1)) return false;
             if (elect_one()) {
-                mbar_arrive_expect_tx(&bars.k_full[s], C::kKv);
-                load_panels<PANELS>(sk + s * C::kKv, C::kKvPanel, &map_k, head, row, &bars.k_full[s]);
+                mbar_arrive_expect_tx(&full[s], C::kKv);
+                load_panels<PANELS>(to + s * C::kKv, C::kKvPanel, map, head, t.k0 + (t0 + i) * kKeys, &full[s]);
             }
             __syncwarp();
-            if (!w.all(&bars.v_empty[s], parity)) {
-                // (the key tile of this turn is on its way; its value tile is not)
-                int never = 0;
-                mbar_wait_all(&bars.k_full[s], parity ^ 1, &never, tc::kWaitNs);
-                break;
+            return true;
+        };
+        int ik = 0, iv = 0;      // tiles under way
+        while (iv < n) {
+            if (ik < n && ik <= iv + 1) {
+                if (!load(ik, sk, &map_k, bars.k_full, bars.k_empty)) break;
+                ++ik;
+                if (ik <= iv + 1 && ik < n) continue;
             }
-            if (elect_one()) {
-                mbar_arrive_expect_tx(&bars.v_full[s], C::kKv);
-                load_panels<PANELS>(sv + s * C::kKv, C::kKvPanel, &map_v, head, row, &bars.v_full[s]);
-            }
-            __syncwarp();
+            if (!load(iv, sv, &map_v, bars.v_full, bars.v_empty)) break;
+            ++iv;
         }
         if (!w.ok && lane == 0) tc::fail(&bars.abort, status);
         // nothing may still be on its way into shared memory when the CTA ends
         int never = 0;
         if (n > 0) mbar_wait_all(&bars.q_full, 0, &never, tc::kWaitNs);
-        for (int b = max(0, i - kStages); b < i; ++b) {
+        for (int b = max(0, ik - kStages); b < ik; ++b)
             mbar_wait_all(&bars.k_full[b % kStages], (b / kStages) & 1, &never, tc::kWaitNs);
+        for (int b = max(0, iv - kStages); b < iv; ++b)
             mbar_wait_all(&bars.v_full[b % kStages], (b / kStages) & 1, &never, tc::kWaitNs);
-        }
     } else if (warp == kMmaWarp) {
         const uint32_t id_s = idesc_bf16(kRows, kKeys, false, false), id_o = idesc_bf16(kRows, 16 * steps, false, true);
         const SmemDesc dq = smem_desc_split(smem_u32(sq), 16, 1024, 2);
@@ -157,12 +164,13 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
             uint32_t words[kChunks];
             if (!valid_keys(S, t.k0 + (t0 + i) * kKeys, t.k0 + t.lk, words))
                 clear_rows<kChunks, PANELS>(smem_u32(sv + s * C::kKv), C::kKvPanel, words);
-            if (!w.all(&bars.p_full, i & 1)) return;
+            const int b = i % kBuffers;
+            if (!w.all(&bars.p_full[b], (i / kBuffers) & 1)) return;
             tc_fence_after();
             if (elect_one()) {
-                product_rows<kKeys>(tb + C::kO, tb + C::kP, at(dv, s), id_o, i > 0);
+                product_rows<kKeys>(tb + C::kO, tb + C::kP + kKeys / 2 * b, at(dv, s), id_o, i > 0);
                 mma_commit(&bars.v_empty[s]);
-                mma_commit(&bars.o_done);
+                mma_commit(&bars.o_done[b]);
             }
             __syncwarp();
         };
@@ -196,13 +204,16 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
         const float c = S.scale * tc::kLog2e;
         const float most = 8.f / c;              // scores above the base
         float base = -INFINITY, sum = 0.f;       // (the base in scores before scaling)
+        // the product of tile i is done
+        auto done = [&](int i) { return w.all(&bars.o_done[i % kBuffers], (i / kBuffers) & 1); };
         for (int i = 0; i < n; ++i) {
+            const int b = i % kBuffers;
             if (!w.all(&bars.s_full, i & 1)) break;
             tc_fence_after();
             if (!some) {
                 if (lane == 0) mbar_arrive(&bars.s_free);
-                if (i > 0 && !w.all(&bars.o_done, (i - 1) & 1)) break;     // (this turn's p_full only after the last one's)
-                if (lane == 0) mbar_arrive(&bars.p_full);
+                if (i >= kBuffers && !done(i - kBuffers)) break;     // (this turn's p_full only after the last one's)
+                if (lane == 0) mbar_arrive(&bars.p_full[b]);
                 continue;
             }
             uint32_t x[kChunks][32];
@@ -227,7 +238,7 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
                 for (int j = 0; j < 32; j += 2)
                     top4[(j >> 1) & 3] = max3(top4[(j >> 1) & 3], __uint_as_float(x[k][j]), __uint_as_float(x[k][j + 1]));
             const float top = max3(fmaxf(top4[0], top4[1]), top4[2], top4[3]);
-            if (i > 0 && !w.all(&bars.o_done, (i - 1) & 1)) break;     // O is still, and the last P has been read
+            if (i >= kBuffers && !done(i - kBuffers)) break;     // the buffer's last P has been read
             tc_fence_after();
             if (i == 0) {
                 base = top;
@@ -235,6 +246,8 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
                 // raise the bases of the warp's rows: O so far, and its sum, in the new ones (rows without a query have no
                 // say: what stands in theirs would change the others' roundings)
                 const float higher = fmaxf(base, top), by = base == -INFINITY ? 0.f : ex2((base - higher) * c);
+                if (kBuffers > 1 && !done(i - 1)) break;      // O is still
+                tc_fence_after();
                 for (int k = 0; k < steps; ++k) {
                     uint32_t o[16];
                     tmem_ld_x16(tb + lanes + C::kO + 16 * k, o);
@@ -252,16 +265,17 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
             for (int k = 0; k < kChunks; ++k) {
                 uint32_t p[16];
                 weights(x[k], make_float2(c, c), make_float2(shift, shift), p, sum2);
-                tmem_st_x16(tb + lanes + C::kP + 16 * k, p);
+                tmem_st_x16(tb + lanes + C::kP + kKeys / 2 * b + 16 * k, p);
             }
             const float2 s = __fadd2_rn(sum2[0], sum2[1]);
             sum += s.x + s.y;
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.p_full);
+            if (lane == 0) mbar_arrive(&bars.p_full[b]);
         }
-        if (n > 0 && w.ok) w.all(&bars.o_done, (n - 1) & 1);
+        if (kBuffers > 1 && n > 1 && w.ok) done(n - 2);
+        if (n > 0 && w.ok) done(n - 1);
         if (!w.ok && lane == 0) tc::fail(&bars.abort, status);
         tc_fence_after();
         if (some && w.ok) {
@@ -297,27 +311,30 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
     if (warp == kMmaWarp) tmem_dealloc(tb, C::kTmem);
 }
 
-template <int PANELS>
+template <int PANELS, bool FEW>
 int launch(const Shape& S, const View& q, const View& k, const View& v, const FwdOut& out, cudaStream_t s) {
-    using C = Cfg<PANELS>;
+    using C = Cfg<PANELS, FEW>;
     CUtensorMap mq, mk, mv;
-    const int tq = tile_queries(kRows, S.g);
+    const int tq = tile_queries(C::kTile, S.g);
     if (!heads_map(&mq, q, S.nq, S.h, S.d, S.g, tq) || !heads_map(&mk, k, S.nk, S.hk, S.d, 1, C::kKeys) ||
         !heads_map(&mv, v, S.nk, S.hk, S.d, 1, C::kKeys))
         return GT_ERR_CUDA;
     int* status = device_status_ptr();
     if (!status) return GT_ERR_CUDA;
     static std::atomic<uint64_t> allowed;
-    if (!allow_smem(allowed, (const void*)cross_fwd<PANELS>, C::kSmem)) return GT_ERR_CUDA;
+    if (!allow_smem(allowed, (const void*)cross_fwd<PANELS, FEW>, C::kSmem)) return GT_ERR_CUDA;
     LaunchScope ls("cross_fwd", s);
-    cross_fwd<PANELS><<<dim3(slots_of(S, true, tq), S.hk, out.splits), kThreads, C::kSmem, s>>>(S, mq, mk, mv, out, status);
+    cross_fwd<PANELS, FEW><<<dim3(slots_of(S, true, tq), S.hk, out.splits), kThreads, C::kSmem, s>>>(S, mq, mk, mv, out, status);
     return check_launch();
 }
 
 }  // namespace
 
+bool few_tile(const Shape& S) { return ((int64_t)S.nq + S.batch - 1) / S.batch * S.g <= kFewTile; }
+
 int fwd_tc(const Shape& S, const View& q, const View& k, const View& v, const FwdOut& out, cudaStream_t s) {
-    return S.d <= 64 ? launch<1>(S, q, k, v, out, s) : launch<2>(S, q, k, v, out, s);
+    if (few_tile(S)) return S.d <= 64 ? launch<1, true>(S, q, k, v, out, s) : launch<2, true>(S, q, k, v, out, s);
+    return S.d <= 64 ? launch<1, false>(S, q, k, v, out, s) : launch<2, false>(S, q, k, v, out, s);
 }
 
 }  // namespace cross
