@@ -26,7 +26,7 @@ SOURCES = ["gt_abi.cu", "gt_spd.cu", "gt_attn_simt.cu", "gt_noalloc.cu", "gt_att
            "gt_attn_bwd_tc.cu", "gt_attn_bwd_dq.cu",
            "gt_attn_bwd_dkdv.cu", "gt_stats.cu", "gt_selftest.cu", "gt_layer.cu", "gt_norm.cu",
            "gt_linear.cu", "gt_qk_norm.cu", "gt_grad_clip.cu", "gt_cross_attn.cu", "gt_cross_simt.cu",
-           "gt_cross_few.cu", "gt_cross_fwd.cu", "gt_cross_bwd.cu"]
+           "gt_cross_few.cu", "gt_cross_narrow.cu", "gt_cross_fwd.cu", "gt_cross_bwd.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", INCLUDE, "-I", CSRC]

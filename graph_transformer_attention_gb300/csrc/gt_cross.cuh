@@ -33,6 +33,7 @@ constexpr int kMaxD = 128;
 constexpr int kMaxShare = 64;     // query heads to a key head
 constexpr int kMaxHeads = 1024;
 constexpr int kMaxSplits = 64;
+constexpr int kNarrow = 16;       // head dims of fp32 storage with kernels of their own
 constexpr int kFewRows = 2;       // rows (query, head) of a sequence up to which the forward runs on the CUDA cores
 
 // [rows][heads][d], channels contiguous
@@ -193,12 +194,16 @@ bool few_tile(const Shape& S);
 // Rows of a tile of the few-rows forward; 0: the call has too many.
 int few_rows(const Shape& S);
 int fwd_few(const Shape& S, bool f32, const View& q, const View& k, const View& v, const FwdOut& out, cudaStream_t s);
+int fwd_narrow(const Shape& S, const View& q, const View& k, const View& v, const FwdOut& out, cudaStream_t s);   // d <= kNarrow
 int fwd_f32(const Shape& S, const View& q, const View& k, const View& v, const FwdOut& out, cudaStream_t s);
 int fwd_tc(const Shape& S, const View& q, const View& k, const View& v, const FwdOut& out, cudaStream_t s);
 // part: fp32 [splits][nq][h][d] where splits > 1
+int bwd_dq_narrow(const Shape& S, const BwdIn& in, const Out& dq, float* part, int splits, cudaStream_t s);
 int bwd_dq_f32(const Shape& S, const BwdIn& in, const Out& dq, float* part, int splits, cudaStream_t s);
 int bwd_dq_tc(const Shape& S, const BwdIn& in, const Out& dq, float* part, int splits, cudaStream_t s);
 // part: fp32 [splits][nk][hk][d] where splits > 1, of dk and of dv
+int bwd_dkv_narrow(const Shape& S, const BwdIn& in, const Out& dk, const Out& dv, float* dk_part, float* dv_part, int splits,
+                   cudaStream_t s);
 int bwd_dkv_f32(const Shape& S, const BwdIn& in, const Out& dk, const Out& dv, float* dk_part, float* dv_part, int splits,
                 cudaStream_t s);
 int bwd_dkv_tc(const Shape& S, const BwdIn& in, const Out& dk, const Out& dv, float* dk_part, float* dv_part, int splits,

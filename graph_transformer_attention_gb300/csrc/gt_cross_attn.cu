@@ -241,6 +241,14 @@ Plan plan_of(const Shape& S, bool f32) {
         const int tq = tile_queries(64, S.g);
         const int64_t qt = tiles_of(S.nq, S.batch, tq) * S.hk, kt = tiles_of(S.nk, S.batch, 64) * S.hk;
         const int64_t keys = (S.nk / S.batch + 63) / 64, queries = (S.nq / S.batch + tq - 1) / tq;
+        if (S.d <= kNarrow) {
+            const int64_t k128 = (S.nk / S.batch + 127) / 128, tq128 = tile_queries(128, S.g);
+            const double step = S.d <= 8 ? 1.0 : 2.0;
+            if (!few) p.fwd = parts_for(qt, k128, S.batch, Cost{step, 4, q_bytes});
+            p.dq = parts_for(qt, k128, S.batch, Cost{1.5 * step, 4, q_bytes});
+            p.dkv = parts_for(kt, (S.nq / S.batch + tq128 - 1) / tq128, S.batch, Cost{2.0 * step, 3, k_bytes});
+            return p;
+        }
         if (!few) p.fwd = parts_for(qt, keys, S.batch, Cost{2.0 * wide, 2, q_bytes});
         p.dq = parts_for(qt, keys, S.batch, Cost{3.0 * wide, 2, q_bytes});
         p.dkv = parts_for(kt, queries, S.batch, Cost{4.0 * wide, 2, k_bytes});
@@ -363,10 +371,14 @@ int run_bwd(Shape S, const Plan& plan, const Room& r, BwdIn in, const View& o, c
         rc = pack_inputs(S, views, room, s);
         if (rc != GT_OK) return rc;
     }
-    rc = F32 ? bwd_dq_f32(S, in, dq, r.dq_part, plan.dq, s) : bwd_dq_tc(S, in, dq, r.dq_part, plan.dq, s);
+    const bool narrow = F32 && S.d <= kNarrow;
+    rc = narrow ? bwd_dq_narrow(S, in, dq, r.dq_part, plan.dq, s)
+         : F32  ? bwd_dq_f32(S, in, dq, r.dq_part, plan.dq, s)
+                : bwd_dq_tc(S, in, dq, r.dq_part, plan.dq, s);
     if (rc != GT_OK) return rc;
-    rc = F32 ? bwd_dkv_f32(S, in, dk, dv, r.dk_part, r.dv_part, plan.dkv, s)
-             : bwd_dkv_tc(S, in, dk, dv, r.dk_part, r.dv_part, plan.dkv, s);
+    rc = narrow ? bwd_dkv_narrow(S, in, dk, dv, r.dk_part, r.dv_part, plan.dkv, s)
+         : F32  ? bwd_dkv_f32(S, in, dk, dv, r.dk_part, r.dv_part, plan.dkv, s)
+                : bwd_dkv_tc(S, in, dk, dv, r.dk_part, r.dv_part, plan.dkv, s);
     if (rc != GT_OK) return rc;
     if (plan.dq > 1) {
         const SumJob j{r.dq_part, dq};
@@ -420,7 +432,7 @@ int gt_cross_attn_fwd(int32_t dtype, int32_t nq, int32_t nk, int32_t h, int32_t 
     if (few) {
         rc = fwd_few(S, f32, qv, kv, vv, out, s);
     } else if (f32) {
-        rc = fwd_f32(S, qv, kv, vv, out, s);
+        rc = d <= kNarrow ? fwd_narrow(S, qv, kv, vv, out, s) : fwd_f32(S, qv, kv, vv, out, s);
     } else {
         View* views[4] = {&qv, &kv, &vv, nullptr};
         bf16* room[4] = {r.q, r.k, r.v, nullptr};

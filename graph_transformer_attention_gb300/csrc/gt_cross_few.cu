@@ -92,12 +92,12 @@ __global__ void __launch_bounds__(kThreads) cross_few(const Shape S, const View 
                 if (!seen[u]) s[u][r] = -INFINITY;
                 top = fmaxf(top, s[u][r]);
             }
-            const float base = top == -INFINITY ? 0.f : top, by = exp2f(m[r] - base);
+            const float base = top == -INFINITY ? 0.f : top, by = sm100::ex2(m[r] - base);
             m[r] = top;
             l[r] *= by;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                p[u][r] = exp2f(s[u][r] - base);
+                p[u][r] = sm100::ex2(s[u][r] - base);
                 l[r] += p[u][r];
             }
             const float2 by2 = make_float2(by, by);
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads) cross_few(const Shape S, const View 
     // the warp's groups, then the warps, on one base
     auto join = [](float& ma, float& la, float2 (&oa)[4], float mb, float lb, const float2 (&ob)[4]) {
         const float top = fmaxf(ma, mb), base = top == -INFINITY ? 0.f : top;
-        const float wa = exp2f(ma - base), wb = exp2f(mb - base);
+        const float wa = sm100::ex2(ma - base), wb = sm100::ex2(mb - base);
         la = la * wa + lb * wb;
         ma = top;
 #pragma unroll

@@ -1,4 +1,4 @@
-// gt_cross_simt.cu -- cross attention of fp32 storage: fp32 products on the CUDA cores.
+// gt_cross_simt.cu -- cross attention of fp32 storage, head dims above 16: fp32 products on the CUDA cores.
 //
 // One skeleton for the three passes.  A CTA holds a tile of 64 rows of one side (queries for o and dq, keys
 // for dk and dv) and streams tiles of 64 rows of the other: the 64 x 64 scores as 4 x 4 blocks of 256
@@ -82,7 +82,7 @@ __device__ __forceinline__ void tile_dot(const float* a, const float* b, int ty,
     }
 }
 
-// The columns of a DP-wide row that thread tx sums: 4 of every 64 (2 of 32, 1 of 16)
+// The columns of a DP-wide row that thread tx sums: 4 of every 64 (2 of 32)
 template <int DP> constexpr int cols_per_thread() { return DP / 16; }
 template <int DP>
 __device__ __forceinline__ int col_of(int tx, int n) {
@@ -208,12 +208,12 @@ __global__ void __launch_bounds__(kThreads) cross_fwd_f32(const Shape S, const V
             }
             top = row_max(top);
             const float base = top == -INFINITY ? 0.f : top;
-            by[i] = exp2f(m[i] - base);
+            by[i] = sm100::ex2(m[i] - base);
             m[i] = top;
             float sum = 0.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                x[i][j] = exp2f(x[i][j] - base);
+                x[i][j] = sm100::ex2(x[i][j] - base);
                 sum += x[i][j];
             }
             l[i] = fmaf(l[i], by[i], row_sum(sum));
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kThreads) cross_bwd_f32(const Shape S, const B
                 const int held = 4 * ty + i, other = tx + 16 * j;
                 const float2 st = stat[KEYS ? other : held];
                 const bool seen = keep[KEYS ? held : other];
-                const float p = seen ? exp2f(fmaf(x[i][j], c, st.x)) : 0.f;
+                const float p = seen ? sm100::ex2(fmaf(x[i][j], c, st.x)) : 0.f;
                 x[i][j] = p;
                 y[i][j] = seen ? p * (y[i][j] + st.y) : 0.f;
             }
@@ -348,7 +348,6 @@ __global__ void __launch_bounds__(kThreads) cross_bwd_f32(const Shape S, const B
 
 template <typename F>
 int by_width(int d, F&& f) {
-    if (d <= 16) return f(std::integral_constant<int, 16>());
     if (d <= 32) return f(std::integral_constant<int, 32>());
     if (d <= 64) return f(std::integral_constant<int, 64>());
     return f(std::integral_constant<int, 128>());
