@@ -173,6 +173,14 @@ __device__ __forceinline__ void put16(T* row, int col, int d, const float (&v)[1
     store8(row + col + 8, b, d - col - 8, acc);
 }
 
+// How the kernels of a call follow one another.  Each lets the next be scheduled while it ends.  The dq kernel waits for those
+// before it (the statistics, copies of the inputs) before it lets dk and dv start, so that these may read them without a wait
+// of their own while dq still runs; they wait at their end instead, so that whoever follows sees dq too.
+__device__ __forceinline__ void follow_stats() {
+    sm100::pdl_wait();
+    sm100::pdl_trigger();
+}
+
 // ---- entry points of the kernels' files; every one launches on s and returns a gt_status
 
 struct FwdOut {

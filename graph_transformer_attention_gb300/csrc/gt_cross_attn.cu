@@ -26,6 +26,7 @@ constexpr int kThreads = 256;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) cross_stats(const Shape S, const View o, const View dO, const float* __restrict__ lse,
                                                         float2* __restrict__ stats, int vec) {
+    sm100::pdl_trigger();
     const int64_t item = (int64_t)blockIdx.x * (kThreads / 8) + (threadIdx.x >> 3);
     const int part = threadIdx.x & 7;
     const bool live = item < (int64_t)S.nq * S.h;
@@ -144,7 +145,7 @@ __global__ void __launch_bounds__(kThreads) cross_sum(const SumJob j0, const Sum
     float acc[8] = {};
     const float* p = J.part + item * d + c;
     const int64_t step = (int64_t)rows * heads * d;
-#pragma unroll 4
+#pragma unroll 8
     for (int z = 0; z < parts; ++z) {
         float x[8];
         unpack8(load8<Mem::kOutput>(p + z * step, d - c, d % 4 == 0 ? 1 : 0), x);
@@ -165,6 +166,7 @@ struct PackJobs {
     int d, dp;
 };
 __global__ void __launch_bounds__(kThreads) cross_pack(const PackJobs P) {
+    sm100::pdl_trigger();
     const PackJob& J = P.j[blockIdx.y];
     const int pieces = P.dp / 8;
     const int64_t all = (int64_t)J.rows * J.heads * pieces;

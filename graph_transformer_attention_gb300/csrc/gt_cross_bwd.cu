@@ -61,6 +61,7 @@ cross_dq(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_
     __shared__ DqBars bars;
     const int tq = tile_queries(kHeld, S.g), head = blockIdx.y, z = blockIdx.z;
     const Tile t = find_tile(S, true, tq, blockIdx.x);
+    follow_stats();
     if (!t.live) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int first = t.tile * tq, live = min(tq, t.lq - first) * S.g;
@@ -278,8 +279,12 @@ cross_dkv(const Shape S, const __grid_constant__ CUtensorMap map_k, const __grid
     __shared__ DkvBars bars;
     __shared__ alignas(16) float st_lse[kStages][kStep], st_d[kStages][kStep];
     const int tq = tile_queries(kStep, S.g), head = blockIdx.y, z = blockIdx.z;
+    pdl_trigger();
     const Tile t = find_tile(S, false, kHeld, blockIdx.x);
-    if (!t.live) return;
+    if (!t.live) {
+        pdl_wait();
+        return;
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int first = t.tile * kHeld;
     const int tiles = (t.lq + tq - 1) / tq;
@@ -471,6 +476,7 @@ cross_dkv(const Shape S, const __grid_constant__ CUtensorMap map_k, const __grid
     __syncthreads();
     tc_fence_after();
     if (warp == C::kMmaWarp) tmem_dealloc(tb, C::kTmem);
+    pdl_wait();
 }
 
 template <int PANELS>
@@ -486,8 +492,9 @@ int launch_dq(const Shape& S, const BwdIn& in, const Out& dq, float* part, int s
     static std::atomic<uint64_t> allowed;
     if (!allow_smem(allowed, (const void*)cross_dq<PANELS>, C::kSmem)) return GT_ERR_CUDA;
     LaunchScope ls("cross_dq", s);
-    cross_dq<PANELS><<<dim3(slots_of(S, true, tq), S.hk, splits), C::kThreads, C::kSmem, s>>>(S, mq, mdo, mk, mv, in.stats, dq,
-                                                                                              part, splits, status);
+    if (launch_overlapped(cross_dq<PANELS>, dim3(slots_of(S, true, tq), S.hk, splits), dim3(C::kThreads), C::kSmem, s, S, mq, mdo,
+                          mk, mv, in.stats, dq, part, splits, status) != cudaSuccess)
+        return GT_ERR_CUDA;
     return check_launch();
 }
 
@@ -505,8 +512,9 @@ int launch_dkv(const Shape& S, const BwdIn& in, const Out& dk, const Out& dv, fl
     static std::atomic<uint64_t> allowed;
     if (!allow_smem(allowed, (const void*)cross_dkv<PANELS>, C::kSmem)) return GT_ERR_CUDA;
     LaunchScope ls("cross_dkv", s);
-    cross_dkv<PANELS><<<dim3(slots_of(S, false, kHeld), S.hk, splits), C::kThreads, C::kSmem, s>>>(
-        S, mk, mv, mq, mdo, in.stats, dk, dv, dk_part, dv_part, splits, status);
+    if (launch_overlapped(cross_dkv<PANELS>, dim3(slots_of(S, false, kHeld), S.hk, splits), dim3(C::kThreads), C::kSmem, s, S, mk,
+                          mv, mq, mdo, in.stats, dk, dv, dk_part, dv_part, splits, status) != cudaSuccess)
+        return GT_ERR_CUDA;
     return check_launch();
 }
 

@@ -220,8 +220,13 @@ __global__ void __launch_bounds__(kThreads) cross_bwd_narrow(const Shape S, cons
                                                              const Vec vec) {
     __shared__ Tiles<DP> T;
     const int tq = tile_queries(KEYS ? kStream : kHeld, S.g), head = blockIdx.y, z = blockIdx.z;
+    if (KEYS) sm100::pdl_trigger();
     const Tile t = find_tile(S, !KEYS, KEYS ? kHeld : tq, blockIdx.x);
-    if (!t.live) return;
+    if (!KEYS) follow_stats();
+    if (!t.live) {
+        if (KEYS) sm100::pdl_wait();
+        return;
+    }
     const int r = threadIdx.x / kPhases, phase = threadIdx.x % kPhases;
     const float c = S.scale * tc::kLog2e;
     const Rows qr = rows_of(in.q, t.q0, head * S.g, S.g, vec.q), dr = rows_of(in.dO, t.q0, head * S.g, S.g, vec.dO);
@@ -231,7 +236,6 @@ __global__ void __launch_bounds__(kThreads) cross_bwd_narrow(const Shape S, cons
     const int tiles = KEYS ? (t.lq + tq - 1) / tq : (t.lk + kStream - 1) / kStream;
     float x1[DP], x2[DP], a1[DP] = {}, a2[DP] = {};
     float2 own;      // dq: -lse and -D of the row; dk, dv: 0 or -infinity
-    sm100::pdl_wait();      // the statistics
     const float2* stats = in.stats + ((int64_t)head * S.nq + t.q0) * S.g;
     if (KEYS) {
         const bool seen = r < live && (!S.mask || __ldg(S.mask + t.k0 + first + r) != 0);
@@ -282,6 +286,7 @@ __global__ void __launch_bounds__(kThreads) cross_bwd_narrow(const Shape S, cons
     }
     phases_sum<DP>(a1);
     if (KEYS) phases_sum<DP>(a2);
+    if (KEYS) sm100::pdl_wait();
     if (r >= live) return;
     if (KEYS) {
         const int64_t key = t.k0 + first + r, at = ((z * (int64_t)S.nk + key) * S.hk + head) * S.d;
@@ -321,9 +326,10 @@ static int bwd_narrow(const Shape& S, const BwdIn& in, const Out& g1, const Out&
     return by_width(S.d, [&](auto width) {
         LaunchScope ls(KEYS ? "cross_dkv_narrow" : "cross_dq_narrow", s);
         const Vec vec{vec16(in.q), vec16(in.k), vec16(in.v), vec16(in.dO)};
-        cross_bwd_narrow<decltype(width)::value, KEYS>
-            <<<dim3(slots_of(S, !KEYS, KEYS ? kHeld : tile_queries(kHeld, S.g)), S.hk, splits), kThreads, 0, s>>>(S, in, g1, g2, p1,
-                                                                                                            p2, splits, vec);
+        if (launch_overlapped(cross_bwd_narrow<decltype(width)::value, KEYS>,
+                              dim3(slots_of(S, !KEYS, KEYS ? kHeld : tile_queries(kHeld, S.g)), S.hk, splits), dim3(kThreads), 0, s,
+                              S, in, g1, g2, p1, p2, splits, vec) != cudaSuccess)
+            return (int)GT_ERR_CUDA;
         return check_launch();
     });
 }

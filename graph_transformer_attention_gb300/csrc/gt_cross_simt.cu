@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(kThreads) cross_fwd_f32(const Shape S, const V
     float* sw = sv + kRows * ldt<DP>();
     __shared__ uint8_t keep[kRows];
     const int tq = tile_queries(kRows, S.g), head = blockIdx.y, z = blockIdx.z;
+    sm100::pdl_trigger();
     const Tile t = find_tile(S, true, tq, blockIdx.x);
     if (!t.live) return;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -262,8 +263,13 @@ __global__ void __launch_bounds__(kThreads) cross_bwd_f32(const Shape S, const B
     __shared__ uint8_t keep[kRows];
     __shared__ float2 stat[kRows];
     const int tq = tile_queries(kRows, S.g), head = blockIdx.y, z = blockIdx.z;
+    if (KEYS) sm100::pdl_trigger();
     const Tile t = find_tile(S, !KEYS, KEYS ? kRows : tq, blockIdx.x);
-    if (!t.live) return;
+    if (!KEYS) follow_stats();
+    if (!t.live) {
+        if (KEYS) sm100::pdl_wait();
+        return;
+    }
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const float c = S.scale * tc::kLog2e;
     const int tiles = KEYS ? (t.lq + tq - 1) / tq : (t.lk + kRows - 1) / kRows;
@@ -318,6 +324,7 @@ __global__ void __launch_bounds__(kThreads) cross_bwd_f32(const Shape S, const B
         tile_acc<DP>(w1, b1, ty, tx, acc1);
         if (KEYS) tile_acc<DP>(w2, b2, ty, tx, acc2);
     }
+    if (KEYS) sm100::pdl_wait();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = 4 * ty + i;
@@ -381,8 +388,10 @@ static int bwd_f32(const Shape& S, const BwdIn& in, const Out& g1, const Out& g2
         auto kern = cross_bwd_f32<DP, KEYS>;
         if (!allow_smem(allowed, (const void*)kern, smem)) return (int)GT_ERR_CUDA;
         LaunchScope ls(KEYS ? "cross_dkv_f32" : "cross_dq_f32", s);
-        kern<<<dim3(slots_of(S, !KEYS, KEYS ? kRows : tile_queries(kRows, S.g)), S.hk, splits), kThreads, smem, s>>>(
-            S, in, g1, g2, p1, p2, splits, Vec{vec16(in.q), vec16(in.k), vec16(in.v), vec16(in.dO)});
+        const Vec vec{vec16(in.q), vec16(in.k), vec16(in.v), vec16(in.dO)};
+        if (launch_overlapped(kern, dim3(slots_of(S, !KEYS, KEYS ? kRows : tile_queries(kRows, S.g)), S.hk, splits), dim3(kThreads),
+                              smem, s, S, in, g1, g2, p1, p2, splits, vec) != cudaSuccess)
+            return (int)GT_ERR_CUDA;
         return check_launch();
     });
 }
