@@ -46,13 +46,22 @@ __device__ __forceinline__ float4 get4(const Rows& R, int r, bool there, int c, 
     return v;
 }
 
+// A row in registers, as pairs for the packed arithmetic.
 template <int DP>
-__device__ __forceinline__ void get_row(const Rows& R, int r, bool there, int d, float (&x)[DP]) {
+struct Row {
+    float2 v[DP / 2];
+};
+
+template <int DP>
+__device__ __forceinline__ Row<DP> get_row(const Rows& R, int r, bool there, int d) {
+    Row<DP> x;
 #pragma unroll
     for (int c = 0; c < DP; c += 4) {
         const float4 v = get4(R, r, there, c, d);
-        x[c] = v.x; x[c + 1] = v.y; x[c + 2] = v.z; x[c + 3] = v.w;
+        x.v[c / 2] = make_float2(v.x, v.y);
+        x.v[c / 2 + 1] = make_float2(v.z, v.w);
     }
+    return x;
 }
 
 // The streamed rows: two arrays, two numbers to a row.
@@ -83,45 +92,55 @@ __device__ __forceinline__ void put(Tiles<DP>& T, const Staged<DP>& st) {
 }
 
 template <int DP>
-__device__ __forceinline__ void row_at(const float* tile, int r, float (&x)[DP]) {
+__device__ __forceinline__ Row<DP> row_at(const float* tile, int r) {
+    Row<DP> x;
 #pragma unroll
     for (int c = 0; c < DP; c += 4) {
         const float4 v = *reinterpret_cast<const float4*>(tile + r * Tiles<DP>::kLd + c);
-        x[c] = v.x; x[c + 1] = v.y; x[c + 2] = v.z; x[c + 3] = v.w;
+        x.v[c / 2] = make_float2(v.x, v.y);
+        x.v[c / 2 + 1] = make_float2(v.z, v.w);
     }
+    return x;
 }
 
 template <int DP>
-__device__ __forceinline__ float dot(const float (&x)[DP], const float (&y)[DP]) {
-    float a = x[0] * y[0], b = x[1] * y[1];
+__device__ __forceinline__ float dot(const Row<DP>& x, const Row<DP>& y) {
+    float2 a = __fmul2_rn(x.v[0], y.v[0]);
 #pragma unroll
-    for (int c = 2; c < DP; c += 2) {
-        a = fmaf(x[c], y[c], a);
-        b = fmaf(x[c + 1], y[c + 1], b);
-    }
-    return a + b;
+    for (int c = 1; c < DP / 2; ++c) a = __ffma2_rn(x.v[c], y.v[c], a);
+    return a.x + a.y;
 }
 
 template <int DP>
-__device__ __forceinline__ void axpy(float w, const float (&x)[DP], float (&y)[DP]) {
+__device__ __forceinline__ void axpy(float w, const Row<DP>& x, Row<DP>& y) {
+    const float2 w2 = make_float2(w, w);
 #pragma unroll
-    for (int c = 0; c < DP; ++c) y[c] = fmaf(w, x[c], y[c]);
+    for (int c = 0; c < DP / 2; ++c) y.v[c] = __ffma2_rn(w2, x.v[c], y.v[c]);
 }
 
 template <int DP>
-__device__ __forceinline__ void put_row(float* p, int d, int phase, const float (&v)[DP], float by) {
+__device__ __forceinline__ void times(float w, Row<DP>& y) {
+    const float2 w2 = make_float2(w, w);
+#pragma unroll
+    for (int c = 0; c < DP / 2; ++c) y.v[c] = __fmul2_rn(w2, y.v[c]);
+}
+
+template <int DP>
+__device__ __forceinline__ void put_row(float* p, int d, int phase, const Row<DP>& x, float by) {
 #pragma unroll
     for (int c = 0; c < DP; ++c)
-        if (c % kPhases == phase && c < d) p[c] = v[c] * by;      // (all four threads of the row have it)
+        if (c % kPhases == phase && c < d) p[c] = (c & 1 ? x.v[c / 2].y : x.v[c / 2].x) * by;      // (all four threads of the row have it)
 }
 
 template <int DP>
-__device__ __forceinline__ void phases_sum(float (&v)[DP]) {
+__device__ __forceinline__ void phases_sum(Row<DP>& x) {
 #pragma unroll
-    for (int c = 0; c < DP; ++c) {
-        v[c] += __shfl_xor_sync(0xffffffffu, v[c], 1);
-        v[c] += __shfl_xor_sync(0xffffffffu, v[c], 2);
-    }
+    for (int c = 0; c < DP / 2; ++c)
+#pragma unroll
+        for (int o = 1; o < kPhases; o <<= 1) {
+            x.v[c].x += __shfl_xor_sync(0xffffffffu, x.v[c].x, o);
+            x.v[c].y += __shfl_xor_sync(0xffffffffu, x.v[c].y, o);
+        }
 }
 
 struct Vec {
@@ -155,8 +174,9 @@ __global__ void __launch_bounds__(kThreads) cross_fwd_narrow(const Shape S, cons
     const int first = t.tile * tq, live = min(tq, t.lq - first) * S.g;
     const float c = S.scale * tc::kLog2e;
     const Rows kr = rows_of(k, t.k0, head, 1, vec.k), vr = rows_of(v, t.k0, head, 1, vec.v);
-    float x[DP], o[DP] = {}, m = -INFINITY, l = 0.f;
-    get_row<DP>(rows_of(q, t.q0 + first, head * S.g, S.g, vec.q), r, r < live, S.d, x);
+    float m = -INFINITY, l = 0.f;
+    Row<DP> o = {};
+    const Row<DP> x = get_row<DP>(rows_of(q, t.q0 + first, head * S.g, S.g, vec.q), r, r < live, S.d);
     const int tiles = (t.lk + kStream - 1) / kStream, end = part_begin(tiles, z + 1, out.splits);
     int n = part_begin(tiles, z, out.splits);
     Staged<DP> st;
@@ -171,23 +191,18 @@ __global__ void __launch_bounds__(kThreads) cross_fwd_narrow(const Shape S, cons
             float s[4], top = m;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                float y[DP];
-                row_at<DP>(T.a, j0 + u * kPhases, y);
-                s[u] = fmaf(dot<DP>(x, y), c, T.s[j0 + u * kPhases].x);
+                s[u] = fmaf(dot<DP>(x, row_at<DP>(T.a, j0 + u * kPhases)), c, T.s[j0 + u * kPhases].x);
                 top = fmaxf(top, s[u]);
             }
             const float base = top == -INFINITY ? 0.f : top, by = sm100::ex2(m - base);
             m = top;
             l *= by;
-#pragma unroll
-            for (int i = 0; i < DP; ++i) o[i] *= by;
+            times<DP>(by, o);
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                float y[DP];
-                row_at<DP>(T.b, j0 + u * kPhases, y);
                 const float p = sm100::ex2(s[u] - base);
                 l += p;
-                axpy<DP>(p, y, o);
+                axpy<DP>(p, row_at<DP>(T.b, j0 + u * kPhases), o);
             }
         }
     }
@@ -196,8 +211,7 @@ __global__ void __launch_bounds__(kThreads) cross_fwd_narrow(const Shape S, cons
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const float by = m == -INFINITY ? 0.f : sm100::ex2(m - top);
     l *= by;
-#pragma unroll
-    for (int i = 0; i < DP; ++i) o[i] *= by;
+    times<DP>(by, o);
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
     phases_sum<DP>(o);
@@ -215,7 +229,7 @@ __global__ void __launch_bounds__(kThreads) cross_fwd_narrow(const Shape S, cons
 
 // KEYS: the held side is the keys (dk, dv), else the queries (dq).
 template <int DP, bool KEYS>
-__global__ void __launch_bounds__(kThreads) cross_bwd_narrow(const Shape S, const BwdIn in, const Out g1, const Out g2,
+__global__ void __launch_bounds__(kThreads, DP == 8 ? 3 : 2) cross_bwd_narrow(const Shape S, const BwdIn in, const Out g1, const Out g2,
                                                              float* __restrict__ part1, float* __restrict__ part2, int splits,
                                                              const Vec vec) {
     __shared__ Tiles<DP> T;
@@ -234,17 +248,17 @@ __global__ void __launch_bounds__(kThreads) cross_bwd_narrow(const Shape S, cons
     const int first = t.tile * (KEYS ? kHeld : tq);
     const int live = KEYS ? min(kHeld, t.lk - first) : min(tq, t.lq - first) * S.g;
     const int tiles = KEYS ? (t.lq + tq - 1) / tq : (t.lk + kStream - 1) / kStream;
-    float x1[DP], x2[DP], a1[DP] = {}, a2[DP] = {};
+    Row<DP> x1, x2, a1 = {}, a2 = {};
     float2 own;      // dq: -lse and -D of the row; dk, dv: 0 or -infinity
     const float2* stats = in.stats + ((int64_t)head * S.nq + t.q0) * S.g;
     if (KEYS) {
         const bool seen = r < live && (!S.mask || __ldg(S.mask + t.k0 + first + r) != 0);
-        get_row<DP>(kr, first + r, seen, S.d, x1);
-        get_row<DP>(vr, first + r, seen, S.d, x2);
+        x1 = get_row<DP>(kr, first + r, seen, S.d);
+        x2 = get_row<DP>(vr, first + r, seen, S.d);
         own = make_float2(seen ? 0.f : -INFINITY, 0.f);
     } else {
-        get_row<DP>(qr, first * S.g + r, r < live, S.d, x1);
-        get_row<DP>(dr, first * S.g + r, r < live, S.d, x2);
+        x1 = get_row<DP>(qr, first * S.g + r, r < live, S.d);
+        x2 = get_row<DP>(dr, first * S.g + r, r < live, S.d);
         own = r < live ? __ldg(stats + first * S.g + r) : make_float2(-INFINITY, 0.f);
     }
     auto fetch = [&](int n, Staged<DP>& st) {
@@ -273,9 +287,7 @@ __global__ void __launch_bounds__(kThreads) cross_bwd_narrow(const Shape S, cons
         if (n + 1 < end) fetch(n + 1, st);
 #pragma unroll 4
         for (int j = phase; j < kStream; j += kPhases) {
-            float y1[DP], y2[DP];
-            row_at<DP>(T.a, j, y1);
-            row_at<DP>(T.b, j, y2);
+            const Row<DP> y1 = row_at<DP>(T.a, j), y2 = row_at<DP>(T.b, j);
             const float2 s = T.s[j];
             // (where nobody sees the key both factors are 0: the rows were cleared, the exponent is -infinity)
             const float p = sm100::ex2(fmaf(dot<DP>(x1, y1), c, own.x + s.x));
