@@ -259,7 +259,7 @@ Plan plan_of(const Shape& S, bool f32) {
         const int64_t qt = tiles_of(S.nq, S.batch, tile_queries(128, S.g)) * S.hk, kt = tiles_of(S.nk, S.batch, 128) * S.hk;
         if (!few) p.fwd = parts_for(qt, (S.nk / S.batch + keys - 1) / keys, S.batch,
                                      few_tile(S) ? Cost{0.7, 2, q_bytes} : Cost{1.2, 2, q_bytes});
-        p.dq = parts_for(qt, (S.nk / S.batch + 63) / 64, S.batch, S.d <= 64 ? Cost{0.9, 2, q_bytes} : Cost{0.75, 1, q_bytes});
+        p.dq = parts_for(qt, (S.nk / S.batch + 63) / 64, S.batch, Cost{S.d <= 64 ? 0.85 : 1.5, 2, q_bytes});
         p.dkv = parts_for(kt, (S.nq / S.batch + tq - 1) / tq, S.batch, S.d <= 64 ? Cost{1.15, 2, k_bytes} : Cost{1.0, 1, k_bytes});
     }
     return p;

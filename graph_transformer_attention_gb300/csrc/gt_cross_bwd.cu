@@ -27,42 +27,44 @@ __device__ __forceinline__ float2 pair_of(uint32_t a, uint32_t b) {
 
 // ---------------------------------------------------------------------------- dq
 
-// Head dims up to 64: four warps, 256 TMEM columns, two CTAs to an SM, each one's products beside the other's
-// arithmetic.  Above: one CTA with two groups of four warps on tiles in turn, with scores of their own.  (What a CTA's
+// Four warps, 256 TMEM columns, two CTAs to an SM, each one's products beside the other's arithmetic.  (What a CTA's
 // issuing warp does for a tile, one instruction after the other between the arithmetic warps', bounds it: one CTA with two or
-// three groups took longer than two CTAs with one, 4096x32768, 8 heads of 64: dq 567 and 422 us, dk and dv 599 and 495.)
+// three groups of four warps on tiles in turn took longer than two CTAs with one, 4096x32768, 8 heads of 64: dq 567 and
+// 422 us, dk and dv 599 and 495.)  Head dims above 64 leave room for one tile of values, which are done with before the keys.
 template <int PANELS>
 struct DqCfg {
-    static constexpr int kGroups = PANELS, kPerSm = 3 - PANELS;
-    static constexpr int kStages = PANELS == 1 ? 3 : 4;
+    static constexpr int kKStages = PANELS == 1 ? 3 : 2, kVStages = PANELS == 1 ? 3 : 1;
     static constexpr uint32_t kHeldBytes = PANELS * kHeldPanel, kStepBytes = PANELS * kStepPanel;
-    static constexpr size_t kSmem = 1024 + 2 * kHeldBytes + 2 * kStages * kStepBytes;
-    // TMEM columns: a group's S (dS over it) and dP, then dq
-    static constexpr uint32_t kAcc = 128 * kGroups, kTmem = 256 * PANELS;
-    static constexpr int kTmaWarp = 4 * kGroups, kMmaWarp = kTmaWarp + 1, kThreads = 32 * (kMmaWarp + 1);
+    static constexpr size_t kSmem = 2 * kHeldBytes + (kKStages + kVStages) * kStepBytes;
+    // TMEM columns: S (dS over it) at 0, dP at 64, dq at 128
+    static constexpr uint32_t kAcc = 128, kTmem = 256;
+    static constexpr int kTmaWarp = 4, kMmaWarp = kTmaWarp + 1, kThreads = 32 * (kMmaWarp + 1);
 };
 
 struct DqBars {
-    uint64_t held_full, k_full[4], k_empty[4], v_full[4], v_empty[4];
-    uint64_t s_full[2], ds_full[2], fin;
+    uint64_t held_full, k_full[3], k_empty[3], v_full[3], v_empty[3];
+    uint64_t s_full, ds_full, fin;
     uint32_t tmem_base;
     int abort;
 };
 
 template <int PANELS>
-__global__ void __launch_bounds__(DqCfg<PANELS>::kThreads, DqCfg<PANELS>::kPerSm)
+__global__ void __launch_bounds__(DqCfg<PANELS>::kThreads, 2)
 cross_dq(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_do,
          const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
          const float2* __restrict__ stats, const Out dq, float* __restrict__ part, const int splits, int* status) {
     using C = DqCfg<PANELS>;
-    constexpr int kStages = C::kStages, kGroups = C::kGroups;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    constexpr int kKStages = C::kKStages, kVStages = C::kVStages;
+    extern __shared__ __align__(1024) uint8_t smem[];      // (no room to align it by hand)
     __shared__ DqBars bars;
     const int tq = tile_queries(kHeld, S.g), head = blockIdx.y, z = blockIdx.z;
     const Tile t = find_tile(S, true, tq, blockIdx.x);
     follow_stats();
     if (!t.live) return;
+    if (smem_u32(smem) & 1023u) {      // the swizzled tiles would not be where the products look for them
+        if (threadIdx.x == 0) atomicOr(status, kStatusTimeout);
+        return;
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int first = t.tile * tq, live = min(tq, t.lq - first) * S.g;
     const int tiles = (t.lk + kStep - 1) / kStep;
@@ -71,19 +73,17 @@ cross_dq(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_
     uint8_t* sq = smem;
     uint8_t* sdo = sq + C::kHeldBytes;
     uint8_t* sk = sdo + C::kHeldBytes;
-    uint8_t* sv = sk + kStages * C::kStepBytes;
+    uint8_t* sv = sk + kKStages * C::kStepBytes;
     if (threadIdx.x == C::kTmaWarp * 32) {
         mbar_init(&bars.held_full, 1);
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < 3; ++s) {
             mbar_init(&bars.k_full[s], 1);
             mbar_init(&bars.k_empty[s], 1);
             mbar_init(&bars.v_full[s], 1);
             mbar_init(&bars.v_empty[s], 1);
         }
-        for (int b = 0; b < kGroups; ++b) {
-            mbar_init(&bars.s_full[b], 1);
-            mbar_init(&bars.ds_full[b], 4);
-        }
+        mbar_init(&bars.s_full, 1);
+        mbar_init(&bars.ds_full, 4);
         mbar_init(&bars.fin, 1);
         bars.abort = 0;
         fence_barrier_init();
@@ -104,26 +104,32 @@ cross_dq(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_
             }
             __syncwarp();
         }
-        int i = 0;
-        for (; i < n; ++i) {
-            const int s = i % kStages, row = t.k0 + (t0 + i) * kStep;
-            const uint32_t parity = ((i / kStages) & 1) ^ 1;
-            if (!w.all(&bars.v_empty[s], parity) || !w.all(&bars.k_empty[s], parity)) break;
+        auto load = [&](int i, int stages, uint8_t* to, const CUtensorMap* map, uint64_t* full, uint64_t* empty) {
+            const int s = i % stages;
+            if (!w.all(&empty[s], ((i / stages) & 1) ^ 1)) return false;
             if (elect_one()) {
-                mbar_arrive_expect_tx(&bars.k_full[s], C::kStepBytes);
-                load_panels<PANELS>(sk + s * C::kStepBytes, kStepPanel, &map_k, head, row, &bars.k_full[s]);
-                mbar_arrive_expect_tx(&bars.v_full[s], C::kStepBytes);
-                load_panels<PANELS>(sv + s * C::kStepBytes, kStepPanel, &map_v, head, row, &bars.v_full[s]);
+                mbar_arrive_expect_tx(&full[s], C::kStepBytes);
+                load_panels<PANELS>(to + s * C::kStepBytes, kStepPanel, map, head, t.k0 + (t0 + i) * kStep, &full[s]);
             }
             __syncwarp();
+            return true;
+        };
+        int ik = 0, iv = 0;      // tiles under way
+        while (iv < n) {
+            if (ik <= iv) {
+                if (!load(ik, kKStages, sk, &map_k, bars.k_full, bars.k_empty)) break;
+                ++ik;
+            }
+            if (!load(iv, kVStages, sv, &map_v, bars.v_full, bars.v_empty)) break;
+            ++iv;
         }
         if (!w.ok && lane == 0) tc::fail(&bars.abort, status);
         int never = 0;      // nothing may still be on its way into shared memory when the CTA ends
         if (n > 0) mbar_wait_all(&bars.held_full, 0, &never, tc::kWaitNs);
-        for (int b = max(0, i - kStages); b < i; ++b) {
-            mbar_wait_all(&bars.k_full[b % kStages], (b / kStages) & 1, &never, tc::kWaitNs);
-            mbar_wait_all(&bars.v_full[b % kStages], (b / kStages) & 1, &never, tc::kWaitNs);
-        }
+        for (int b = max(0, ik - kKStages); b < ik; ++b)
+            mbar_wait_all(&bars.k_full[b % kKStages], (b / kKStages) & 1, &never, tc::kWaitNs);
+        for (int b = max(0, iv - kVStages); b < iv; ++b)
+            mbar_wait_all(&bars.v_full[b % kVStages], (b / kVStages) & 1, &never, tc::kWaitNs);
     } else if (warp == C::kMmaWarp) {
         const uint32_t id_s = idesc_bf16(kHeld, kStep, false, false), id_acc = idesc_bf16(kHeld, 16 * steps, false, true);
         const SmemDesc a_q = smem_desc_split(smem_u32(sq), 16, 1024, 2), a_do = smem_desc_split(smem_u32(sdo), 16, 1024, 2);
@@ -132,45 +138,36 @@ cross_dq(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_
         auto at = [](SmemDesc d, int s) { return SmemDesc{d.lo + s * (C::kStepBytes >> 4), d.hi}; };
         // What can be done ahead of a tile's products: its keys have landed, those that nobody sees are cleared.
         auto ready = [&](int i) {
-            const int s = i % kStages;
-            if (!w.all(&bars.k_full[s], (i / kStages) & 1) || !w.all(&bars.v_full[s], (i / kStages) & 1)) return;
+            const int sk_ = i % kKStages, sv_ = i % kVStages;
+            if (!w.all(&bars.k_full[sk_], (i / kKStages) & 1)) return;
             uint32_t words[kStep / 32];
             if (!valid_keys(S, t.k0 + (t0 + i) * kStep, t.k0 + t.lk, words))
-                clear_rows<kStep / 32, PANELS>(smem_u32(sk + s * C::kStepBytes), kStepPanel, words);
+                clear_rows<kStep / 32, PANELS>(smem_u32(sk + sk_ * C::kStepBytes), kStepPanel, words);
+            w.all(&bars.v_full[sv_], (i / kVStages) & 1);
         };
         auto scores = [&](int i) {      // by one lane
-            const int s = i % kStages, b = i % kGroups;
-            product_channels<PANELS>(tb + 128 * b, a_q, kHeldPanel, at(b_k, s), kStepPanel, steps, id_s);
-            product_channels<PANELS>(tb + 128 * b + 64, a_do, kHeldPanel, at(b_v, s), kStepPanel, steps, id_s);
-            mma_commit(&bars.v_empty[s]);
-            mma_commit(&bars.s_full[b]);
+            product_channels<PANELS>(tb, a_q, kHeldPanel, at(b_k, i % kKStages), kStepPanel, steps, id_s);
+            product_channels<PANELS>(tb + 64, a_do, kHeldPanel, at(b_v, i % kVStages), kStepPanel, steps, id_s);
+            mma_commit(&bars.v_empty[i % kVStages]);
+            mma_commit(&bars.s_full);
         };
         if (n > 0) w.all(&bars.held_full, 0);
-        for (int i = 0; i < kGroups && i < n && w.ok; ++i) {
-            ready(i);
-            tc_fence_after();
-            if (w.ok && elect_one()) scores(i);
-            __syncwarp();
-        }
+        if (n > 0 && w.ok) ready(0);
+        tc_fence_after();
+        if (n > 0 && w.ok && elect_one()) scores(0);
+        __syncwarp();
         for (int i = 0; i < n && w.ok; ++i) {
-            const int s = i % kStages, b = i % kGroups;
-            if (kGroups == 1 && i + 1 < n) ready(i + 1);
-            if (!w.ok || !w.all(&bars.ds_full[b], (i / kGroups) & 1)) break;
+            if (i + 1 < n) ready(i + 1);
+            if (!w.ok || !w.all(&bars.ds_full, i & 1)) break;
             tc_fence_after();
             if (elect_one()) {
                 // dq += dS k, and behind it the next scores where dS stands (the tensor pipe runs one thread's products
                 // in order)
-                product_rows<kStep>(tb + C::kAcc, tb + 128 * b, at(r_k, s), id_acc, i > 0);
-                mma_commit(&bars.k_empty[s]);
-                if (kGroups == 1 && i + 1 < n) scores(i + 1);
+                product_rows<kStep>(tb + C::kAcc, tb, at(r_k, i % kKStages), id_acc, i > 0);
+                mma_commit(&bars.k_empty[i % kKStages]);
+                if (i + 1 < n) scores(i + 1);
             }
             __syncwarp();
-            if (kGroups > 1 && i + kGroups < n) {      // (these rows may still be on their way: not before the products)
-                ready(i + kGroups);
-                tc_fence_after();
-                if (w.ok && elect_one()) scores(i + kGroups);
-                __syncwarp();
-            }
         }
         if (!w.ok && lane == 0) tc::fail(&bars.abort, status);
         int never = 0;
@@ -178,16 +175,16 @@ cross_dq(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_
         __syncwarp();
         mbar_wait_all(&bars.fin, 0, &never, tc::kWaitNs);
     } else {
-        const int group = warp >> 2, r = (warp & 3) * 32 + lane;
-        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, ts = tb + lanes + 128 * group;
-        const bool some = (warp & 3) * 32 < live, mine = r < live;      // a warp without rows only keeps the barriers going
+        const int r = warp * 32 + lane;
+        const uint32_t lanes = (uint32_t)(warp * 32) << 16, ts = tb + lanes;
+        const bool some = warp * 32 < live, mine = r < live;      // a warp without rows only keeps the barriers going
         const float c = S.scale * tc::kLog2e;
         const float2 st = mine ? __ldg(stats + ((int64_t)head * S.nq + t.q0 + first) * S.g + r) : make_float2(-INFINITY, 0.f);
         const float2 c2 = make_float2(c, c), minus_lse = make_float2(st.x, st.x), minus_d = make_float2(st.y, st.y);
-        for (int i = group; i < n; i += kGroups) {
+        for (int i = 0; i < n; ++i) {
             uint32_t words[kStep / 32];
             const bool all = valid_keys(S, t.k0 + (t0 + i) * kStep, t.k0 + t.lk, words);
-            if (!w.all(&bars.s_full[group], (i / kGroups) & 1)) break;
+            if (!w.all(&bars.s_full, i & 1)) break;
             tc_fence_after();
             if (some) {
 #pragma unroll
@@ -215,7 +212,7 @@ cross_dq(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.ds_full[group]);
+            if (lane == 0) mbar_arrive(&bars.ds_full);
         }
         w.all(&bars.fin, 0);
         if (!w.ok && lane == 0) tc::fail(&bars.abort, status);
@@ -225,7 +222,7 @@ cross_dq(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_
             const int qh = head * S.g + r % S.g;
             bf16* p = static_cast<bf16*>(dq.p) + query * dq.row + qh * dq.head;
             float* f = part + ((z * (int64_t)S.nq + query) * S.h + qh) * S.d;
-            for (int k = group; k < steps; k += kGroups) {      // the groups share the columns
+            for (int k = 0; k < steps; ++k) {
                 uint32_t o[16];
                 if (n > 0) {
                     tmem_ld_x16(tb + lanes + C::kAcc + 16 * k, o);
@@ -247,7 +244,8 @@ cross_dq(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_
 
 // ---------------------------------------------------------------------------- dk, dv
 
-// CTAs and groups as for dq.
+// Head dims up to 64 as for dq; above, the results take half of TMEM, and one CTA has two groups of four warps on tiles in
+// turn, with scores of their own.
 template <int PANELS>
 struct DkvCfg {
     static constexpr int kGroups = PANELS, kPerSm = 3 - PANELS;
