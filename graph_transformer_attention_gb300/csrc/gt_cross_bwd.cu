@@ -27,7 +27,7 @@ __device__ __forceinline__ float2 pair_of(uint32_t a, uint32_t b) {
 
 // ---------------------------------------------------------------------------- dq
 
-// Four warps, 256 TMEM columns, two CTAs to an SM, each one's products beside the other's arithmetic.  (What a CTA's
+// Eight warps (four to each half of a tile), 256 TMEM columns, two CTAs to an SM, each one's products beside the other's arithmetic.  (What a CTA's
 // issuing warp does for a tile, one instruction after the other between the arithmetic warps', bounds it: one CTA with two or
 // three groups of four warps on tiles in turn took longer than two CTAs with one, 4096x32768, 8 heads of 64: dq 567 and
 // 422 us, dk and dv 599 and 495.)  Head dims above 64 leave room for one tile of values, which are done with before the keys.
@@ -36,9 +36,9 @@ struct DqCfg {
     static constexpr int kKStages = PANELS == 1 ? 3 : 2, kVStages = PANELS == 1 ? 3 : 1;
     static constexpr uint32_t kHeldBytes = PANELS * kHeldPanel, kStepBytes = PANELS * kStepPanel;
     static constexpr size_t kSmem = 2 * kHeldBytes + (kKStages + kVStages) * kStepBytes;
-    // TMEM columns: S (dS over it) at 0, dP at 64, dq at 128
+    // TMEM columns: S (each half's dS over it) at 0, dP at 64, dq at 128
     static constexpr uint32_t kAcc = 128, kTmem = 256;
-    static constexpr int kTmaWarp = 4, kMmaWarp = kTmaWarp + 1, kThreads = 32 * (kMmaWarp + 1);
+    static constexpr int kTmaWarp = 8, kMmaWarp = kTmaWarp + 1, kThreads = 32 * (kMmaWarp + 1);
 };
 
 struct DqBars {
@@ -83,7 +83,7 @@ cross_dq(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_
             mbar_init(&bars.v_empty[s], 1);
         }
         mbar_init(&bars.s_full, 1);
-        mbar_init(&bars.ds_full, 4);
+        mbar_init(&bars.ds_full, 8);
         mbar_init(&bars.fin, 1);
         bars.abort = 0;
         fence_barrier_init();
@@ -163,7 +163,7 @@ cross_dq(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_
             if (elect_one()) {
                 // dq += dS k, and behind it the next scores where dS stands (the tensor pipe runs one thread's products
                 // in order)
-                product_rows<kStep>(tb + C::kAcc, tb, at(r_k, i % kKStages), id_acc, i > 0);
+                product_rows<kStep, true>(tb + C::kAcc, tb, at(r_k, i % kKStages), id_acc, i > 0);
                 mma_commit(&bars.k_empty[i % kKStages]);
                 if (i + 1 < n) scores(i + 1);
             }
@@ -175,39 +175,35 @@ cross_dq(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_
         __syncwarp();
         mbar_wait_all(&bars.fin, 0, &never, tc::kWaitNs);
     } else {
-        const int r = warp * 32 + lane;
-        const uint32_t lanes = (uint32_t)(warp * 32) << 16, ts = tb + lanes;
-        const bool some = warp * 32 < live, mine = r < live;      // a warp without rows only keeps the barriers going
+        const int half = warp >> 2, r = (warp & 3) * 32 + lane;      // 32 of the tile's keys, one row
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, ts = tb + lanes + 32 * half;
+        const bool some = (warp & 3) * 32 < live, mine = r < live;      // a warp without rows only keeps the barriers going
         const float c = S.scale * tc::kLog2e;
         const float2 st = mine ? __ldg(stats + ((int64_t)head * S.nq + t.q0 + first) * S.g + r) : make_float2(-INFINITY, 0.f);
         const float2 c2 = make_float2(c, c), minus_lse = make_float2(st.x, st.x), minus_d = make_float2(st.y, st.y);
         for (int i = 0; i < n; ++i) {
-            uint32_t words[kStep / 32];
-            const bool all = valid_keys(S, t.k0 + (t0 + i) * kStep, t.k0 + t.lk, words);
+            uint32_t word[1];
+            const bool all = valid_keys(S, t.k0 + (t0 + i) * kStep + 32 * half, t.k0 + t.lk, word);
             if (!w.all(&bars.s_full, i & 1)) break;
             tc_fence_after();
             if (some) {
+                uint32_t x[32], y[32], ds[16];
+                tmem_ld_x32(ts, x);
+                tmem_ld_x32(ts + 64, y);
+                tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    uint32_t x[32], y[32], ds[16];
-                    tmem_ld_x32(ts + 32 * k, x);
-                    tmem_ld_x32(ts + 64 + 32 * k, y);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const float2 a = pair_of(x[j], x[j + 1]), b = pair_of(y[j], y[j + 1]);
-                        const float2 t = __ffma2_rn(a, c2, minus_lse);
-                        const float2 g = __fmul2_rn(make_float2(ex2(t.x), ex2(t.y)), __fadd2_rn(b, minus_d));
-                        ds[j / 2] = pack_bf16x2(g.x, g.y);
-                    }
-                    if (!all) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            ds[j] &= (((words[k] >> (2 * j)) & 1u) ? 0xffffu : 0u) |
-                                     (((words[k] >> (2 * j + 1)) & 1u) ? 0xffff0000u : 0u);
-                    }
-                    tmem_st_x16(ts + 16 * k, ds);
+                for (int j = 0; j < 32; j += 2) {
+                    const float2 a = pair_of(x[j], x[j + 1]), b = pair_of(y[j], y[j + 1]);
+                    const float2 e = __ffma2_rn(a, c2, minus_lse);
+                    const float2 g = __fmul2_rn(make_float2(ex2(e.x), ex2(e.y)), __fadd2_rn(b, minus_d));
+                    ds[j / 2] = pack_bf16x2(g.x, g.y);
                 }
+                if (!all) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        ds[j] &= (((word[0] >> (2 * j)) & 1u) ? 0xffffu : 0u) | (((word[0] >> (2 * j + 1)) & 1u) ? 0xffff0000u : 0u);
+                }
+                tmem_st_x16(ts, ds);
                 tmem_wait_st();
             }
             tc_fence_before();
@@ -222,7 +218,7 @@ cross_dq(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_
             const int qh = head * S.g + r % S.g;
             bf16* p = static_cast<bf16*>(dq.p) + query * dq.row + qh * dq.head;
             float* f = part + ((z * (int64_t)S.nq + query) * S.h + qh) * S.d;
-            for (int k = 0; k < steps; ++k) {
+            for (int k = half; k < steps; k += 2) {
                 uint32_t o[16];
                 if (n > 0) {
                     tmem_ld_x16(tb + lanes + C::kAcc + 16 * k, o);
@@ -244,7 +240,7 @@ cross_dq(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_
 
 // ---------------------------------------------------------------------------- dk, dv
 
-// Head dims up to 64 as for dq; above, the results take half of TMEM, and one CTA has two groups of four warps on tiles in
+// Head dims up to 64 as for dq; above, the results take half of TMEM, and one CTA has two groups of eight warps on tiles in
 // turn, with scores of their own.
 template <int PANELS>
 struct DkvCfg {
@@ -254,7 +250,7 @@ struct DkvCfg {
     static constexpr size_t kSmem = 1024 + 2 * kHeldBytes + 2 * kStages * kStepBytes;
     // TMEM columns: a group's S and dP (p and dS over them), then dv, then dk
     static constexpr uint32_t kDv = 128 * kGroups, kDk = kDv + 64 * PANELS, kTmem = 256 * PANELS;
-    static constexpr int kTmaWarp = 4 * kGroups, kMmaWarp = kTmaWarp + 1, kThreads = 32 * (kMmaWarp + 1);
+    static constexpr int kTmaWarp = 8 * kGroups, kMmaWarp = kTmaWarp + 1, kThreads = 32 * (kMmaWarp + 1);
 };
 
 struct DkvBars {
@@ -300,7 +296,7 @@ cross_dkv(const Shape S, const __grid_constant__ CUtensorMap map_k, const __grid
         }
         for (int b = 0; b < kGroups; ++b) {
             mbar_init(&bars.s_full[b], 1);
-            mbar_init(&bars.p_full[b], 4);
+            mbar_init(&bars.p_full[b], 8);
         }
         mbar_init(&bars.fin, 1);
         bars.abort = 0;
@@ -386,8 +382,8 @@ cross_dkv(const Shape S, const __grid_constant__ CUtensorMap map_k, const __grid
             if (elect_one()) {
                 // dv += p^T dO, dk += dS^T q, and behind them the next scores where p and dS stand (the tensor pipe runs one
                 // thread's products in order)
-                product_rows<kStep>(tb + C::kDv, tb + 128 * b, at(r_do, s), id_acc, i > 0);
-                product_rows<kStep>(tb + C::kDk, tb + 128 * b + 64, at(r_q, s), id_acc, i > 0);
+                product_rows<kStep, true>(tb + C::kDv, tb + 128 * b, at(r_do, s), id_acc, i > 0);
+                product_rows<kStep, true>(tb + C::kDk, tb + 128 * b + 64, at(r_q, s), id_acc, i > 0);
                 mma_commit(&bars.q_empty[s]);
                 if (kGroups == 1 && i + 1 < n) scores(i + 1);
             }
@@ -405,8 +401,8 @@ cross_dkv(const Shape S, const __grid_constant__ CUtensorMap map_k, const __grid
         __syncwarp();
         mbar_wait_all(&bars.fin, 0, &never, tc::kWaitNs);
     } else {
-        const int group = warp >> 2, r = (warp & 3) * 32 + lane;
-        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, ts = tb + lanes + 128 * group;
+        const int group = warp >> 3, half = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;      // 32 of the tile's rows, one key
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, ts = tb + lanes + 128 * group + 32 * half;
         const float c = S.scale * tc::kLog2e;
         const float2 c2 = make_float2(c, c);
         for (int i = group; i < n; i += kGroups) {
@@ -414,29 +410,26 @@ cross_dkv(const Shape S, const __grid_constant__ CUtensorMap map_k, const __grid
             const uint32_t turn = (i / kGroups) & 1;
             if (!w.all(&bars.q_full[s], (i / kStages) & 1) || !w.all(&bars.s_full[group], turn)) break;
             tc_fence_after();
-            const uint32_t s_lse = smem_u32(st_lse[s]), s_d = smem_u32(st_d[s]);
+            const uint32_t s_lse = smem_u32(st_lse[s]) + 128 * half, s_d = smem_u32(st_d[s]) + 128 * half;
+            uint32_t x[32], y[32], p[16], ds[16];
+            tmem_ld_x32(ts, x);
+            tmem_ld_x32(ts + 64, y);
+            tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                uint32_t x[32], y[32], p[16], ds[16];
-                tmem_ld_x32(ts + 32 * k, x);
-                tmem_ld_x32(ts + 64 + 32 * k, y);
-                tmem_wait_ld();
+            for (int j = 0; j < 32; j += 4) {
+                const uint4 l4 = lds_u4(s_lse + 4 * j), d4 = lds_u4(s_d + 4 * j);      // of four rows
 #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const uint4 l4 = lds_u4(s_lse + 4 * (32 * k + j)), d4 = lds_u4(s_d + 4 * (32 * k + j));   // of four queries
-#pragma unroll
-                    for (int u = 0; u < 4; u += 2) {
-                        const float2 a = pair_of(x[j + u], x[j + u + 1]), b = pair_of(y[j + u], y[j + u + 1]);
-                        const float2 t = __ffma2_rn(a, c2, u ? pair_of(l4.z, l4.w) : pair_of(l4.x, l4.y));
-                        const float2 e = make_float2(ex2(t.x), ex2(t.y));
-                        const float2 g = __fmul2_rn(e, __fadd2_rn(b, u ? pair_of(d4.z, d4.w) : pair_of(d4.x, d4.y)));
-                        p[(j + u) / 2] = pack_bf16x2(e.x, e.y);
-                        ds[(j + u) / 2] = pack_bf16x2(g.x, g.y);
-                    }
+                for (int u = 0; u < 4; u += 2) {
+                    const float2 a = pair_of(x[j + u], x[j + u + 1]), b = pair_of(y[j + u], y[j + u + 1]);
+                    const float2 t = __ffma2_rn(a, c2, u ? pair_of(l4.z, l4.w) : pair_of(l4.x, l4.y));
+                    const float2 e = make_float2(ex2(t.x), ex2(t.y));
+                    const float2 g = __fmul2_rn(e, __fadd2_rn(b, u ? pair_of(d4.z, d4.w) : pair_of(d4.x, d4.y)));
+                    p[(j + u) / 2] = pack_bf16x2(e.x, e.y);
+                    ds[(j + u) / 2] = pack_bf16x2(g.x, g.y);
                 }
-                tmem_st_x16(ts + 16 * k, p);
-                tmem_st_x16(ts + 64 + 16 * k, ds);
             }
+            tmem_st_x16(ts, p);
+            tmem_st_x16(ts + 64, ds);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -453,7 +446,7 @@ cross_dkv(const Shape S, const __grid_constant__ CUtensorMap map_k, const __grid
                 const bool whole = splits == 1;
                 bf16* p = static_cast<bf16*>(g.p) + key * g.row + head * g.head;
                 float* f = part + ((z * (int64_t)S.nk + key) * S.hk + head) * S.d;
-                for (int k = 0; k < steps; ++k) {
+                for (int k = group; k < steps; k += kGroups) {      // (the groups share the columns)
                     uint32_t o[16];
                     if (n > 0) {
                         tmem_ld_x16(tb + lanes + col + 16 * k, o);
@@ -466,8 +459,8 @@ cross_dkv(const Shape S, const __grid_constant__ CUtensorMap map_k, const __grid
                     else if (mine) put16(f, 16 * k, S.d, v, S.d % 4 == 0 ? 1 : 0);
                 }
             };
-            if (group == 0) result(dv, dv_part, C::kDv, 1.f);
-            if (group == kGroups - 1) result(dk, dk_part, C::kDk, S.scale);
+            if (half == 0) result(dv, dv_part, C::kDv, 1.f);
+            else result(dk, dk_part, C::kDk, S.scale);
         }
         tc_fence_before();
     }

@@ -48,11 +48,13 @@ __device__ __forceinline__ void product_channels(uint32_t d_tmem, SmemDesc a, ui
     }
 }
 
-// D (+)= W B along B's ROWS rows, W in TMEM (bf16, 8 columns to 16 rows).
-template <int ROWS>
+// D (+)= W B along B's ROWS rows, W in TMEM (bf16, 8 columns to 16 rows).  HALVES: the columns of rows 32 .. 63 begin 32
+// columns on, each half where the fp32 values it was made of stood.
+template <int ROWS, bool HALVES = false>
 __device__ __forceinline__ void product_rows(uint32_t d_tmem, uint32_t w_tmem, SmemDesc b, uint32_t idesc, bool add) {
 #pragma unroll
-    for (int k = 0; k < ROWS / 16; ++k) mma_ts(d_tmem, w_tmem + 8 * k, desc_at(b, k * 2048), idesc, add || k > 0);
+    for (int k = 0; k < ROWS / 16; ++k)
+        mma_ts(d_tmem, w_tmem + (HALVES ? 32 * (k >> 1) + 8 * (k & 1) : 8 * k), desc_at(b, k * 2048), idesc, add || k > 0);
 }
 
 // Waits of a role, by whole warps; a wait that gives up says so, and the role ends.
