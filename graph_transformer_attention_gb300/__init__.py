@@ -948,6 +948,9 @@ class TensorList:
             if p == q and p and g.dtype != o.dtype:
                 raise ValueError(f"output {i} is its gradient in another type")
             table[i] = _Grad(p, q, g.numel(), _type_code(f"gradient {i}", g), _type_code(f"output {i}", o))
+        written = [t.data_ptr() for t in out if t.numel()]
+        if len(set(written)) != len(written):
+            raise ValueError("an output is listed twice")
         self.grads, self.out, self.device, self.table, self.count = grads, out, device, table, len(grads)
         self.address = ctypes.addressof(table)
 

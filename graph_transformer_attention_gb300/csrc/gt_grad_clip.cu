@@ -37,7 +37,7 @@ struct Entry {
     int64_t numel;
     int32_t unit0;      // units before it
     int8_t g32, o32;    // fp32, else bf16
-    int8_t gvec, ovec;  // 16-byte accesses
+    int8_t gvec, ovec;  // accesses: 2 by 32 bytes, 1 by 16, 0 by single elements
 };
 
 struct Table {
@@ -59,15 +59,15 @@ __device__ __forceinline__ int tensor_of(const int* first, int count, int u) {
 
 // Eight elements of a lane: whole units of 16-byte rows as vectors, lane by lane; others element by element.
 template <typename T>
-__device__ __forceinline__ void get8(const T* p, int live, bool vec, float (&v)[8]) {
-    unpack8(load8<Mem::kOutput>(p, live, vec ? 1 : 0), v);
+__device__ __forceinline__ void get8(const T* p, int live, int vec, float (&v)[8]) {
+    unpack8(load8<Mem::kOutput>(p, live, vec), v);
 }
 
 // The element of a unit where lane `lane` starts its eighth k
 __device__ __forceinline__ int at_of(int k, int lane) { return k * 256 + lane * 8; }
 
 template <typename T>
-__device__ __forceinline__ float unit_squares(const T* p, int64_t left, bool vec, int lane, double& wide) {
+__device__ __forceinline__ float unit_squares(const T* p, int64_t left, int vec, int lane, double& wide) {
     float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -228,7 +228,8 @@ void fill(Table& t, const gt_grad* list, int count, int at) {
     int units = 0;
     for (int k = 0; k < t.count; ++k) {
         const gt_grad& g = list[at + k];
-        t.e[k] = Entry{g.g, g.out, g.numel, units, g.gtype == GT_F32, g.otype == GT_F32, aligned16(g.g), aligned16(g.out)};
+        t.e[k] = Entry{g.g, g.out, g.numel, units, g.gtype == GT_F32, g.otype == GT_F32,
+                       (int8_t)row_access(g.g, 0, 4), (int8_t)row_access(g.out, 0, 4)};
         units += (int)units_of(g.numel);
     }
     t.units = units;

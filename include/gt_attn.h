@@ -557,7 +557,8 @@ int gt_qk_norm_bwd(int32_t xtype, int32_t ytype, int32_t d, float eps, const flo
  * over the whole range of fp32 (squares that leave it are summed in fp64).
  *   list    host array of `count` tensors, read during the call only.  g: device, numel elements
  *           in a row, of gtype; out: device, of otype (output: it may be g itself with the same
- *           type; NULL: the tensor only counts).  numel may be 0.
+ *           type; NULL: the tensor only counts).  numel may be 0.  No output may overlap another
+ *           or another tensor's g.
  *   max_norm  0 or more; infinity only measures (out is g in otype).  A norm that is not finite
  *           scales by max_norm / norm all the same: 0 for infinity, NaN for NaN.
  *   norm    device fp32 [1] (output).

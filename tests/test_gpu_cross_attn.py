@@ -233,6 +233,27 @@ def test_gradients_by_differences(gt):
 
 
 @pytest.mark.parametrize("t", [F, B])
+def test_offsets_outside_the_rows_are_cut(gt, t):
+    q, k, v = _t((60, 2, 64), t, 1), _t((300, 2, 64), t, 2), _t((300, 2, 64), t, 3)
+    do = _t(q.shape, t, 4)
+    good, wide = (_off(0, 20, 60), _off(0, 100, 300)), (_off(-7, 20, 2 ** 31 - 1), _off(-2 ** 31, 100, 1000))
+    a, b = gt.gt_cross_attn_fwd(q, k, v, *good), gt.gt_cross_attn_fwd(q, k, v, *wide)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    a, b = (gt.gt_cross_attn_bwd(q, k, v, a[0], do, a[1], *offs) for offs in (good, wide))
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("t", [F, B])
+def test_many_short_sequences(gt, t):
+    """More sequences than one look at the offsets covers, most of them of no row, one or two."""
+    n = 1500
+    lq, lk = [(i * 7) % 3 for i in range(n)], [(i * 5) % 4 for i in range(n)]
+    lq[700], lk[700] = 300, 200
+    cq, ck = ([0] + torch.tensor(x).cumsum(0).tolist() for x in (lq, lk))
+    _both(gt, _t((cq[-1], 4, 32), t, 1), _t((ck[-1], 2, 32), t, 2), _t((ck[-1], 2, 32), t, 3), _off(*cq), _off(*ck))
+
+
+@pytest.mark.parametrize("t", [F, B])
 def test_long_sides(gt, t):
     """Long keys for few queries, long queries for few keys: the split forms, against fp64 on some of the heads."""
     for nq, nk, h, hk, c in ((4, 20011, 4, 2, 64), (5003, 70, 2, 2, 32), (1, 9001, 16, 2, 128), (300, 4099, 1, 1, 16)):

@@ -87,6 +87,14 @@ def test_small_beside_large(gt):
     _check(gt, [grads[0], grads[3]], 1e-22)
 
 
+def test_an_output_listed_twice_is_refused(gt):
+    g = _grads([50], [F])[0]
+    with pytest.raises(ValueError, match="twice"):
+        gt.gt_grad_clip([g, g], 1.0)
+    norm = gt.gt_grad_clip([g, g], 1.0, out=[torch.empty_like(g) for _ in range(2)])      # two outputs: it counts twice
+    R.check({"norm": norm}, X.clip([g, g], 1.0, [F, F]))
+
+
 def test_nonfinite(gt):
     for bad in (math.nan, math.inf):
         g = _grads([3000, 40], [F])
