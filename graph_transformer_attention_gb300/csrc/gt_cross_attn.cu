@@ -125,34 +125,39 @@ __global__ void __launch_bounds__(kThreads) cross_join(const Shape S, const FwdO
     }
 }
 
-// One result of a split backward: [parts][rows][heads][d] summed into out; two at once (dk and dv) by blockIdx.y.
+// One result of a split backward: [parts][rows][heads][d] summed into out; two at once (dk and dv) by blockIdx.y.  LANES
+// lanes share the parts of an eight of channels, z = lane, lane + LANES, ..., and join in a fixed order.
 struct SumJob {
     const float* part;
     Out out;
 };
-template <typename T>
+template <typename T, int LANES>
 __global__ void __launch_bounds__(kThreads) cross_sum(const SumJob j0, const SumJob j1, const int32_t* off, int batch, int rows,
                                                       int heads, int d, int parts) {
     const SumJob& J = blockIdx.y == 0 ? j0 : j1;
-    const int pieces = (d + 7) / 8;
-    const int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x, item = at / pieces;
-    if (item >= (int64_t)rows * heads) return;
+    const int pieces = (d + 7) / 8, lane = threadIdx.x % LANES;
+    const int64_t at = (int64_t)blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES, item = at / pieces;
     const int c = (int)(at - item * pieces) * 8;
     const int64_t row = item / heads;
     const int head = (int)(item - row * heads);
-    if (!in_batch(off, batch, rows, row)) return;
+    const bool live = row < rows && in_batch(off, batch, rows, row);
     sm100::pdl_wait();   // launched to overlap the end of the kernel that writes the parts
     float acc[8] = {};
-    const float* p = J.part + item * d + c;
+    const float* p = J.part + (live ? item * d + c : 0);
     const int64_t step = (int64_t)rows * heads * d;
 #pragma unroll 8
-    for (int z = 0; z < parts; ++z) {
+    for (int z = lane; z < parts; z += LANES) {
         float x[8];
-        unpack8(load8<Mem::kOutput>(p + z * step, d - c, d % 4 == 0 ? 1 : 0), x);
+        unpack8(load8<Mem::kOutput>(p + z * step, live ? d - c : 0, d % 4 == 0 ? 1 : 0), x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[i] += x[i];
     }
-    store8(static_cast<T*>(J.out.p) + row * J.out.row + head * J.out.head + c, acc, d - c, J.out.acc);
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+    if (live && lane == 0)
+        store8(static_cast<T*>(J.out.p) + row * J.out.row + head * J.out.head + c, acc, d - c, J.out.acc);
 }
 
 // dst: [rows][heads][dp], zeros past d
@@ -345,9 +350,13 @@ template <typename T>
 int sum_parts(const SumJob& a, const SumJob& b, int jobs, const int32_t* off, int batch, int rows, int heads, int d, int parts,
               cudaStream_t s) {
     LaunchScope ls("cross_sum", s);
-    const int64_t all = (int64_t)rows * heads * ((d + 7) / 8);
-    if (launch_overlapped(cross_sum<T>, dim3((unsigned)((all + kThreads - 1) / kThreads), jobs), dim3(kThreads), 0, s, a, b, off,
-                          batch, rows, heads, d, parts) != cudaSuccess)
+    // eight lanes to an eight where there are too few of them to fill the SMs (128 x 8 heads of 8 in 27 parts: 13 us with one
+    // lane, most of it one load after the other, 8 with eight; 4096 x 8 heads of 64 in 7 parts: 20 us with one, 25 with two)
+    const int64_t eights = (int64_t)rows * heads * ((d + 7) / 8);
+    const int lanes = eights < (int64_t)4 * num_sms() * kThreads ? 8 : 1;
+    if (launch_overlapped(lanes == 8 ? cross_sum<T, 8> : cross_sum<T, 1>,
+                          dim3((unsigned)((eights * lanes + kThreads - 1) / kThreads), jobs),
+                          dim3(kThreads), 0, s, a, b, off, batch, rows, heads, d, parts) != cudaSuccess)
         return GT_ERR_CUDA;
     return check_launch();
 }

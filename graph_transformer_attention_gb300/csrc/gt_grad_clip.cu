@@ -8,7 +8,7 @@
 // the SMs alike.  The second kernel takes the units in the opposite order: what the first read last is still cached.
 //
 // Squares of fp32 leave the range of fp32: a unit's sum of squares outside [2^-90, 2^100] is taken again in fp64 (a
-// lane's 64 squares below 2^-149 lose less than 2^-53 of a sum above 2^-90).  A lane's units are added in two fp32 words
+// lane's 32 squares below 2^-149 lose less than 2^-53 of a sum above 2^-90).  A lane's units are added in two fp32 words
 // (the rounding of each addition is kept), everything above in fp64, in a fixed order.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -27,8 +27,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnit = 2048;          // elements a warp takes at a time
-constexpr int kPerLane = kUnit / 32;
+constexpr int kUnit = 1024;          // elements a warp takes at a time, all on their way at once
+constexpr int kEights = kUnit / 256;  // eights of a lane
 constexpr int kTable = 256;          // tensors of a launch
 
 struct Entry {
@@ -69,35 +69,29 @@ __device__ __forceinline__ int at_of(int k, int lane) { return k * 256 + lane * 
 template <typename T>
 __device__ __forceinline__ float unit_squares(const T* p, int64_t left, int vec, int lane, double& wide) {
     float part[4] = {0.f, 0.f, 0.f, 0.f};
+    float v[kEights][8];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        float v[4][8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int at = at_of(half * 4 + k, lane);
-            const int64_t more = left - at;
-            get8(p + at, more >= 8 ? 8 : more > 0 ? (int)more : 0, vec, v[k]);
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) part[i & 3] = fmaf(v[k][i], v[k][i], part[i & 3]);
+    for (int k = 0; k < kEights; ++k) {
+        const int at = at_of(k, lane);
+        const int64_t more = left - at;
+        get8(p + at, more >= 8 ? 8 : more > 0 ? (int)more : 0, vec, v[k]);
     }
+#pragma unroll
+    for (int k = 0; k < kEights; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) part[i & 3] = fmaf(v[k][i], v[k][i], part[i & 3]);
     const float s = (part[0] + part[1]) + (part[2] + part[3]);
     if (s >= 0x1p-90f && s <= 0x1p100f) return s;
     // out of fp32's range, zero or not finite
     double d = 0.0;
-    for (int k = 0; k < kPerLane / 8; ++k) {
-        float v[8];
-        const int at = at_of(k, lane);
-        const int64_t more = left - at;
-        get8(p + at, more >= 8 ? 8 : more > 0 ? (int)more : 0, vec, v);
+#pragma unroll
+    for (int k = 0; k < kEights; ++k) {
         uint32_t any = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) any |= __float_as_uint(v[i]) << 1;
+        for (int i = 0; i < 8; ++i) any |= __float_as_uint(v[k][i]) << 1;
         if (any) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) d += (double)v[i] * (double)v[i];
+            for (int i = 0; i < 8; ++i) d += (double)v[k][i] * (double)v[k][i];
         }
     }
     wide += d;
@@ -162,24 +156,21 @@ __global__ void __launch_bounds__(kThreads) grad_scale(const __grid_constant__ T
         if (!e.out || (as_is && e.out == e.g)) continue;
         const int64_t at = (int64_t)(u - first[k]) * kUnit, left = e.numel - at;
         auto scale = [&](const auto* g, auto* out) {
+            float v[kEights][8];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                float v[4][8];
+            for (int j = 0; j < kEights; ++j) {
+                const int a = at_of(j, lane);
+                const int64_t more = left - a;
+                get8(g + at + a, more >= 8 ? 8 : more > 0 ? (int)more : 0, e.gvec, v[j]);
+            }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int a = at_of(half * 4 + j, lane);
-                    const int64_t more = left - a;
-                    get8(g + at + a, more >= 8 ? 8 : more > 0 ? (int)more : 0, e.gvec, v[j]);
-                }
+            for (int j = 0; j < kEights; ++j) {
+                const int a = at_of(j, lane);
+                const int64_t more = left - a;
+                if (!as_is)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int a = at_of(half * 4 + j, lane);
-                    const int64_t more = left - a;
-                    if (!as_is)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[j][i] *= factor;
-                    store8(out + at + a, v[j], more >= 8 ? 8 : more > 0 ? (int)more : 0, e.ovec);
-                }
+                    for (int i = 0; i < 8; ++i) v[j][i] *= factor;
+                store8(out + at + a, v[j], more >= 8 ? 8 : more > 0 ? (int)more : 0, e.ovec);
             }
         };
         if (e.g32) {

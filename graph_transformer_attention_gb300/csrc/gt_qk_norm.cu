@@ -524,6 +524,7 @@ __global__ void __launch_bounds__(kSumThreads) qk_gain_sum(const __grid_constant
     sm100::pdl_wait();   // launched to overlap the end of the kernel that writes the partial rows
     float acc = 0.f;
     if (c < J.d)
+#pragma unroll 8
         for (int p = ty; p < S.ctas; p += kSumThreads / 32) acc += __ldcg(S.part + (int64_t)p * J.d + c);
     red[ty][tx] = acc;
     __syncthreads();

@@ -565,7 +565,7 @@ int gt_qk_norm_bwd(int32_t xtype, int32_t ytype, int32_t d, float eps, const flo
  *   workspace  at least gt_grad_clip_workspace_size(count) bytes, 16-byte aligned.
  * Errors: GT_ERR_INVALID_ARG for a NULL list, norm or g, count < 1, an unknown type, out = g of
  * another type, or a max_norm that is negative or NaN; GT_ERR_UNSUPPORTED for numel > 2^40 or more
- * than 2^41 elements in 256 consecutive tensors; GT_ERR_WORKSPACE.  Results do not change from run to run.
+ * than 2^40 elements in 256 consecutive tensors; GT_ERR_WORKSPACE.  Results do not change from run to run.
  */
 typedef struct {
     const void* g;
