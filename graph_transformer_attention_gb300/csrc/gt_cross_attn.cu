@@ -260,7 +260,7 @@ Plan plan_of(const Shape& S, bool f32) {
         p.dq = parts_for(qt, keys, S.batch, Cost{3.0 * wide, 2, q_bytes});
         p.dkv = parts_for(kt, queries, S.batch, Cost{4.0 * wide, 2, k_bytes});
     } else {
-        const int keys = S.d <= 64 ? 128 : 64, tq = tile_queries(64, S.g);
+        const int keys = S.d <= 64 ? 96 : 64, tq = tile_queries(64, S.g);
         const int64_t qt = tiles_of(S.nq, S.batch, tile_queries(128, S.g)) * S.hk, kt = tiles_of(S.nk, S.batch, 128) * S.hk;
         if (!few) p.fwd = parts_for(qt, (S.nk / S.batch + keys - 1) / keys, S.batch,
                                      few_tile(S) ? Cost{0.7, 2, q_bytes} : Cost{1.2, 2, q_bytes});

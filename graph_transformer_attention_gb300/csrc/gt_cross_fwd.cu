@@ -31,19 +31,18 @@ constexpr int kThreads = 192;
 template <int PANELS, bool FEW>
 struct Cfg {
     static constexpr int kStages = FEW ? 3 : 2, kTile = FEW ? kFewTile : kRows;
-    static constexpr int kKeys = PANELS == 1 ? 128 : 64;        // of a tile
+    static constexpr int kKeys = PANELS == 1 ? 96 : 64;         // of a tile
     static constexpr uint32_t kQPanel = kTile * 128, kKvPanel = kKeys * 128;
     static constexpr uint32_t kQ = PANELS * kQPanel, kKv = PANELS * kKvPanel;
     static constexpr size_t kSmem = 1024 + kQ + 2 * kStages * kKv;
-    // TMEM columns: S at 0, then P (two buffers where there is room), then O
-    static constexpr int kBuffers = PANELS;
-    static constexpr uint32_t kP = kKeys, kO = PANELS == 1 ? 192 : 128;
+    // TMEM columns: the scores of two tiles (each one's P over them), then O
+    static constexpr uint32_t kO = 2 * kKeys;
     static constexpr uint32_t kTmem = 256;
 };
 
 struct Bars {
     uint64_t q_full, k_full[3], k_empty[3], v_full[3], v_empty[3];
-    uint64_t s_full, s_free, p_full[2], o_done[2], fin;
+    uint64_t s_full[2], p_full[2], o_done, fin;
     uint32_t tmem_base;
     int abort;
 };
@@ -70,7 +69,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
           const __grid_constant__ CUtensorMap map_v, const FwdOut out, int* status) {
     using C = Cfg<PANELS, FEW>;
-    constexpr int kKeys = C::kKeys, kChunks = kKeys / 32, kStages = C::kStages, kBuffers = C::kBuffers;
+    constexpr int kKeys = C::kKeys, kChunks = kKeys / 32, kStages = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ Bars bars;
@@ -94,12 +93,11 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
             mbar_init(&bars.v_full[s], 1);
             mbar_init(&bars.v_empty[s], 1);
         }
-        mbar_init(&bars.s_full, 1);
-        mbar_init(&bars.s_free, 4);
-        for (int b = 0; b < C::kBuffers; ++b) {
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&bars.s_full[b], 1);
             mbar_init(&bars.p_full[b], 4);
-            mbar_init(&bars.o_done[b], 1);
         }
+        mbar_init(&bars.o_done, 1);
         mbar_init(&bars.fin, 1);
         bars.abort = 0;
         fence_barrier_init();
@@ -158,37 +156,37 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
         const SmemDesc dk = smem_desc_split(smem_u32(sk), 16, 1024, 2);
         const SmemDesc dv = smem_desc_split(smem_u32(sv), C::kKvPanel, 1024, 2);
         auto at = [](SmemDesc d, int s) { return SmemDesc{d.lo + s * (C::kKv >> 4), d.hi}; };
-        auto values = [&](int i) {      // O += P V of tile i
+        // (by one lane)
+        auto scores = [&](int i) {
             const int s = i % kStages;
-            if (!w.all(&bars.v_full[s], (i / kStages) & 1)) return;
+            product_channels<PANELS>(tb + kKeys * (i & 1), dq, C::kQPanel, at(dk, s), C::kKvPanel, steps, id_s);
+            mma_commit(&bars.k_empty[s]);
+            mma_commit(&bars.s_full[i & 1]);
+        };
+        if (n > 0) w.all(&bars.q_full, 0);
+        for (int i = 0; i < min(n, 2) && w.ok; ++i) {
+            if (!w.all(&bars.k_full[i], 0)) break;
+            tc_fence_after();
+            if (elect_one()) scores(i);
+            __syncwarp();
+        }
+        for (int i = 0; i < n && w.ok; ++i) {      // O += P V of tile i, and behind it the scores of tile i + 2, over P
+            const int s = i % kStages;
+            if (!w.all(&bars.v_full[s], (i / kStages) & 1)) break;
             uint32_t words[kChunks];
             if (!valid_keys(S, t.k0 + (t0 + i) * kKeys, t.k0 + t.lk, words))
                 clear_rows<kChunks, PANELS>(smem_u32(sv + s * C::kKv), C::kKvPanel, words);
-            const int b = i % kBuffers;
-            if (!w.all(&bars.p_full[b], (i / kBuffers) & 1)) return;
+            if (i + 2 < n && !w.all(&bars.k_full[(i + 2) % kStages], ((i + 2) / kStages) & 1)) break;
+            if (!w.all(&bars.p_full[i & 1], (i >> 1) & 1)) break;
             tc_fence_after();
             if (elect_one()) {
-                product_rows<kKeys>(tb + C::kO, tb + C::kP + kKeys / 2 * b, at(dv, s), id_o, i > 0);
+                product_rows<kKeys>(tb + C::kO, tb + kKeys * (i & 1), at(dv, s), id_o, i > 0);
                 mma_commit(&bars.v_empty[s]);
-                mma_commit(&bars.o_done[b]);
+                mma_commit(&bars.o_done);
+                if (i + 2 < n) scores(i + 2);
             }
             __syncwarp();
-        };
-        if (n > 0) w.all(&bars.q_full, 0);
-        for (int i = 0; i < n && w.ok; ++i) {
-            const int s = i % kStages;
-            if (!w.all(&bars.k_full[s], (i / kStages) & 1)) break;
-            if (i > 0 && !w.all(&bars.s_free, (i - 1) & 1)) break;
-            tc_fence_after();
-            if (elect_one()) {
-                product_channels<PANELS>(tb, dq, C::kQPanel, at(dk, s), C::kKvPanel, steps, id_s);
-                mma_commit(&bars.k_empty[s]);
-                mma_commit(&bars.s_full);
-            }
-            __syncwarp();
-            if (i > 0) values(i - 1);
         }
-        if (n > 0 && w.ok) values(n - 1);
         if (!w.ok) {
             if (lane == 0) tc::fail(&bars.abort, status);
             int never = 0;
@@ -204,25 +202,18 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
         const float c = S.scale * tc::kLog2e;
         const float most = 8.f / c;              // scores above the base
         float base = -INFINITY, sum = 0.f;       // (the base in scores before scaling)
-        // the product of tile i is done
-        auto done = [&](int i) { return w.all(&bars.o_done[i % kBuffers], (i / kBuffers) & 1); };
         for (int i = 0; i < n; ++i) {
-            const int b = i % kBuffers;
-            if (!w.all(&bars.s_full, i & 1)) break;
+            if (!w.all(&bars.s_full[i & 1], (i >> 1) & 1)) break;
             tc_fence_after();
             if (!some) {
-                if (lane == 0) mbar_arrive(&bars.s_free);
-                if (i >= kBuffers && !done(i - kBuffers)) break;     // (this turn's p_full only after the last one's)
-                if (lane == 0) mbar_arrive(&bars.p_full[b]);
+                if (lane == 0) mbar_arrive(&bars.p_full[i & 1]);
                 continue;
             }
+            const uint32_t at = tb + lanes + kKeys * (i & 1);
             uint32_t x[kChunks][32];
 #pragma unroll
-            for (int k = 0; k < kChunks; ++k) tmem_ld_x32(tb + lanes + 32 * k, x[k]);
+            for (int k = 0; k < kChunks; ++k) tmem_ld_x32(at + 32 * k, x[k]);
             tmem_wait_ld();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.s_free);
             uint32_t words[kChunks];      // (not formed any earlier: the scores take nearly all registers)
             if (!valid_keys(S, t.k0 + (t0 + i) * kKeys, t.k0 + t.lk, words)) {
 #pragma unroll
@@ -238,15 +229,13 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
                 for (int j = 0; j < 32; j += 2)
                     top4[(j >> 1) & 3] = max3(top4[(j >> 1) & 3], __uint_as_float(x[k][j]), __uint_as_float(x[k][j + 1]));
             const float top = max3(fmaxf(top4[0], top4[1]), top4[2], top4[3]);
-            if (i >= kBuffers && !done(i - kBuffers)) break;     // the buffer's last P has been read
-            tc_fence_after();
             if (i == 0) {
                 base = top;
             } else if (__any_sync(0xffffffffu, mine && (top > base + most || (base == -INFINITY && top > -INFINITY)))) {
                 // raise the bases of the warp's rows: O so far, and its sum, in the new ones (rows without a query have no
                 // say: what stands in theirs would change the others' roundings)
                 const float higher = fmaxf(base, top), by = base == -INFINITY ? 0.f : ex2((base - higher) * c);
-                if (kBuffers > 1 && !done(i - 1)) break;      // O is still
+                if (!w.all(&bars.o_done, (i - 1) & 1)) break;      // O is still (the product before was ahead of these scores)
                 tc_fence_after();
                 for (int k = 0; k < steps; ++k) {
                     uint32_t o[16];
@@ -265,17 +254,17 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
             for (int k = 0; k < kChunks; ++k) {
                 uint32_t p[16];
                 weights(x[k], make_float2(c, c), make_float2(shift, shift), p, sum2);
-                tmem_st_x16(tb + lanes + C::kP + kKeys / 2 * b + 16 * k, p);
+                tmem_st_x16(at + 16 * k, p);
             }
             const float2 s = __fadd2_rn(sum2[0], sum2[1]);
             sum += s.x + s.y;
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.p_full[b]);
+            if (lane == 0) mbar_arrive(&bars.p_full[i & 1]);
         }
-        if (kBuffers > 1 && n > 1 && w.ok) done(n - 2);
-        if (n > 0 && w.ok) done(n - 1);
+        if (n > 1 && w.ok) w.all(&bars.o_done, (n - 2) & 1);
+        if (n > 0 && w.ok) w.all(&bars.o_done, (n - 1) & 1);
         if (!w.ok && lane == 0) tc::fail(&bars.abort, status);
         tc_fence_after();
         if (some && w.ok) {
