@@ -62,63 +62,63 @@ __device__ __forceinline__ bool in_batch(const int32_t* off, int batch, int n, i
     return !off || (row >= clamp_off(off, 0, n) && row < clamp_off(off, batch, n));
 }
 
-// Sixteen lanes to a query and head: lane p weighs the parts p, p + 16, ...
-constexpr int kJoinLanes = 16;
-template <typename T>
+// LANES lanes to a query and head, one to eight channels: lane p weighs the parts p, p + LANES, ...  The first parts' sums are on
+// their way while the weights are formed.
+template <typename T, int LANES>
 __global__ void __launch_bounds__(kThreads) cross_join(const Shape S, const FwdOut out) {
-    const int64_t item = (int64_t)blockIdx.x * (kThreads / kJoinLanes) + threadIdx.x / kJoinLanes;
-    const int part = threadIdx.x % kJoinLanes;
+    const int64_t item = (int64_t)blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
+    const int part = threadIdx.x % LANES;
     const bool there = item < (int64_t)S.nq * S.h;
     const int64_t query = there ? item / S.h : 0;
     const int head = there ? (int)(item - query * S.h) : 0;
     const bool live = there && in_batch(S.q_off, S.batch, S.nq, query);
     sm100::pdl_wait();   // launched to overlap the end of the kernel that writes the parts
-    constexpr int W = kMaxSplits / kJoinLanes;
+    constexpr int W = kMaxSplits / LANES;
+    const int vec = S.d % 4 == 0 ? 1 : 0;
+    const int64_t step = (int64_t)S.nq * S.h * S.d;
+    auto load = [&](Raw8<float>(&raw)[4], int c, int z) {      // parts z .. z + 3, from channel c
+        const bool mine = live && c < S.d;
+        const float* src = out.o_part + (mine ? (query * S.h + head) * S.d + c : 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) raw[i] = load8<Mem::kOutput>(src + (z + i < out.splits ? z + i : 0) * step, mine ? S.d - c : 0, vec);
+    };
+    Raw8<float> raw[4];
+    load(raw, part * 8, 0);
     float l[W], top = -INFINITY, sum = 0.f;
 #pragma unroll
     for (int k = 0; k < W; ++k) {
-        const int z = part + k * kJoinLanes;
+        const int z = part + k * LANES;
         l[k] = live && z < out.splits ? __ldcg(out.lse_part + ((int64_t)z * S.h + head) * S.nq + query) : -INFINITY;
         top = fmaxf(top, l[k]);
     }
 #pragma unroll
-    for (int o = kJoinLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int o = LANES / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
 #pragma unroll
     for (int k = 0; k < W; ++k) {
         l[k] = l[k] == -INFINITY ? 0.f : expf(l[k] - top);      // (a NaN is not lost)
         sum += l[k];
     }
 #pragma unroll
-    for (int o = kJoinLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const bool seen = sum != 0.f;
     if (live && part == 0) out.lse[(int64_t)head * S.nq + query] = seen ? top + logf(sum) : -INFINITY;
     const float inv = seen ? 1.f / sum : 0.f;
     T* o = static_cast<T*>(out.o.p) + query * out.o.row + head * out.o.head;
-    const int vec = S.d % 4 == 0 ? 1 : 0;
-    for (int c0 = 0; c0 < S.d; c0 += 8 * kJoinLanes) {
+    for (int c0 = 0; c0 < S.d; c0 += 8 * LANES) {
         const int c = c0 + part * 8;
-        const bool mine = live && c < S.d;
-        const float* src = out.o_part + (mine ? (query * S.h + head) * S.d + c : 0);
-        const int64_t step = (int64_t)S.nq * S.h * S.d;
         float acc[8] = {};
 #pragma unroll
         for (int k = 0; k < W; ++k)
-            for (int u = 0; u < kJoinLanes && k * kJoinLanes + u < out.splits; u += 4) {      // four loads at a time
-                Raw8<float> raw[4];
-                float weight[4];
+            for (int u = 0; u < LANES && k * LANES + u < out.splits; u += 4) {      // four loads at a time
+                if (c0 + k * LANES + u > 0) load(raw, c, k * LANES + u);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int z = k * kJoinLanes + u + i;
-                    weight[i] = __shfl_sync(0xffffffffu, l[k], u + i, kJoinLanes) * inv;
-                    raw[i] = load8<Mem::kOutput>(src + (z < out.splits ? z : 0) * step, mine ? S.d - c : 0, vec);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                    const float weight = __shfl_sync(0xffffffffu, l[k], u + i, LANES) * inv;
                     float x[8];
                     unpack8(raw[i], x);
-                    if (weight[i] != 0.f)      // (nothing was written for a part without a key)
+                    if (weight != 0.f)      // (nothing was written for a part without a key)
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) acc[j] = fmaf(weight[i], x[j], acc[j]);
+                        for (int j = 0; j < 8; ++j) acc[j] = fmaf(weight, x[j], acc[j]);
                 }
             }
         if (live && c < S.d) store8(o + c, acc, S.d - c, out.o.acc);
@@ -453,8 +453,10 @@ int gt_cross_attn_fwd(int32_t dtype, int32_t nq, int32_t nk, int32_t h, int32_t 
     if (rc != GT_OK || plan.fwd == 1) return rc;
     gt::LaunchScope ls("cross_join", s);
     const int64_t items = (int64_t)nq * h;
-    const unsigned ctas = (unsigned)((items + kThreads / kJoinLanes - 1) / (kThreads / kJoinLanes));
-    const cudaError_t e = gt::launch_overlapped(f32 ? cross_join<float> : cross_join<bf16>, dim3(ctas), dim3(kThreads), 0, s, S, out);
+    const int lanes = d <= 64 ? 8 : 16;
+    const unsigned ctas = (unsigned)((items * lanes + kThreads - 1) / kThreads);
+    auto join = lanes == 8 ? (f32 ? cross_join<float, 8> : cross_join<bf16, 8>) : (f32 ? cross_join<float, 16> : cross_join<bf16, 16>);
+    const cudaError_t e = gt::launch_overlapped(join, dim3(ctas), dim3(kThreads), 0, s, S, out);
     return e == cudaSuccess ? gt::check_launch() : GT_ERR_CUDA;
 }
 
