@@ -2,9 +2,14 @@
 // and dv by CTAs that hold a tile of keys.  Two kernels, seven products where one with sums in memory takes five: no
 // result depends on the order in which CTAs finish.
 //
-// In both the scores and dP are formed again tile by tile, p = exp(s - lse) and dS = p (dP - D) by warps that have a row
-// each, and p and dS go back to TMEM as bf16 operands (half a step, 2^-9, of each entry, independent from one to the
-// next).  The scores' scale comes last: dq = scale (dS k), dk = scale (dS^T q).
+//   p = exp(s - lse),  D = <dO, o>,  dS = p (dO v^T - D),  dq = scale dS k,  dk = scale dS^T q,  dv = p^T dO
+//
+// In both the scores and dP are formed again tile by tile, p and dS by warps that have a row each, and p and dS go back to
+// TMEM as bf16 operands (half a step, 2^-8 of each entry at most, independent from one to the next).  The scores' scale comes last.
+//
+// What bounds both is the way from products to arithmetic and back, tile by tile (with neither products nor arithmetic, only the
+// barriers: 248 us each for 4096 x 32768, 8 heads of 64; tensor pipes 47 to 49 % busy): 377 us for dq, 485 for dk and dv, 790
+// TFLOP/s of five products over the call.  4099 x 20001, 16 heads of 128 over 4: 105 and 127 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
