@@ -7,9 +7,10 @@
 // In both the scores and dP are formed again tile by tile, p and dS by warps that have a row each, and p and dS go back to
 // TMEM as bf16 operands (half a step, 2^-8 of each entry at most, independent from one to the next).  The scores' scale comes last.
 //
-// What bounds both is the way from products to arithmetic and back, tile by tile (with neither products nor arithmetic, only the
-// barriers: 248 us each for 4096 x 32768, 8 heads of 64; tensor pipes 47 to 49 % busy): 377 us for dq, 485 for dk and dv, 790
-// TFLOP/s of five products over the call.  4099 x 20001, 16 heads of 128 over 4: 105 and 127 us.
+// What bounds both is shared memory, which a product of two operands there reads at 128 bytes a cycle (128 x 64 x 16: 48 cycles, from
+// TMEM 32), and the way from products to arithmetic and back (with neither products nor arithmetic, only the barriers: 248 us each for
+// 4096 x 32768, 8 heads of 64).  There dq takes 327 us, dk and dv 485, 816 TFLOP/s of five products over the call; 4099 x 20001, 16 heads of
+// 128 over 4: 105 and 127 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -35,23 +36,35 @@ __device__ __forceinline__ float2 pair_of(uint32_t a, uint32_t b) {
 // Eight warps (four to each half of a tile), 256 TMEM columns, two CTAs to an SM, each one's products beside the other's arithmetic.  (What a CTA's
 // issuing warp does for a tile, one instruction after the other between the arithmetic warps', bounds it: one CTA with two or
 // three groups of four warps on tiles in turn took longer than two CTAs with one, 4096x32768, 8 heads of 64: dq 567 and
-// 422 us, dk and dv 599 and 495.)  Head dims above 64 leave room for one tile of values, which are done with before the keys.
+// 422 us, dk and dv 599 and 495.)  Up to 64 channels q and dO are moved to the columns that are left: 377 -> 327 us; with two tiles of 48
+// keys there instead 390.  Head dims above 64 leave room for one tile of values, which are done with before the keys.
 template <int PANELS>
 struct DqCfg {
     static constexpr int kKStages = PANELS == 1 ? 3 : 2, kVStages = PANELS == 1 ? 3 : 1;
     static constexpr uint32_t kHeldBytes = PANELS * kHeldPanel, kStepBytes = PANELS * kStepPanel;
     static constexpr size_t kSmem = 2 * kHeldBytes + (kKStages + kVStages) * kStepBytes;
-    // TMEM columns: S (each half's dS over it) at 0, dP at 64, dq at 128
-    static constexpr uint32_t kAcc = 128, kTmem = 256;
+    // TMEM columns: S (each half's dS over it) at 0, dP at 64, dq at 128; up to 64 channels, q and dO at 192 and 224
+    static constexpr uint32_t kAcc = 128, kOwn = 192, kTmem = 256;
+    static constexpr bool kInTmem = PANELS == 1;
     static constexpr int kTmaWarp = 8, kMmaWarp = kTmaWarp + 1, kThreads = 32 * (kMmaWarp + 1);
 };
 
 struct DqBars {
     uint64_t held_full, k_full[3], k_empty[3], v_full[3], v_empty[3];
-    uint64_t s_full, ds_full, fin;
+    uint64_t own_full, s_full, ds_full, fin;
     uint32_t tmem_base;
     int abort;
 };
+
+// D = A B^T along up to 64 channels, A in TMEM (8 columns to 16 channels).
+__device__ __forceinline__ void product_own(uint32_t d_tmem, uint32_t a_tmem, SmemDesc b, int steps, uint32_t idesc) {
+    if (steps == 4) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mma_ts(d_tmem, a_tmem + 8 * k, desc_at(b, k * 32), idesc, k > 0);
+    } else {
+        for (int k = 0; k < steps; ++k) mma_ts(d_tmem, a_tmem + 8 * k, desc_at(b, k * 32), idesc, k > 0);
+    }
+}
 
 template <int PANELS>
 __global__ void __launch_bounds__(DqCfg<PANELS>::kThreads, 2)
@@ -87,6 +100,7 @@ cross_dq(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_
             mbar_init(&bars.v_full[s], 1);
             mbar_init(&bars.v_empty[s], 1);
         }
+        mbar_init(&bars.own_full, 8);
         mbar_init(&bars.s_full, 1);
         mbar_init(&bars.ds_full, 8);
         mbar_init(&bars.fin, 1);
@@ -151,12 +165,17 @@ cross_dq(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_
             w.all(&bars.v_full[sv_], (i / kVStages) & 1);
         };
         auto scores = [&](int i) {      // by one lane
-            product_channels<PANELS>(tb, a_q, kHeldPanel, at(b_k, i % kKStages), kStepPanel, steps, id_s);
-            product_channels<PANELS>(tb + 64, a_do, kHeldPanel, at(b_v, i % kVStages), kStepPanel, steps, id_s);
+            if constexpr (C::kInTmem) {
+                product_own(tb, tb + C::kOwn, at(b_k, i % kKStages), steps, id_s);
+                product_own(tb + 64, tb + C::kOwn + 32, at(b_v, i % kVStages), steps, id_s);
+            } else {
+                product_channels<PANELS>(tb, a_q, kHeldPanel, at(b_k, i % kKStages), kStepPanel, steps, id_s);
+                product_channels<PANELS>(tb + 64, a_do, kHeldPanel, at(b_v, i % kVStages), kStepPanel, steps, id_s);
+            }
             mma_commit(&bars.v_empty[i % kVStages]);
             mma_commit(&bars.s_full);
         };
-        if (n > 0) w.all(&bars.held_full, 0);
+        if (n > 0) w.all(C::kInTmem ? &bars.own_full : &bars.held_full, 0);
         if (n > 0 && w.ok) ready(0);
         tc_fence_after();
         if (n > 0 && w.ok && elect_one()) scores(0);
@@ -186,7 +205,24 @@ cross_dq(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_
         const float c = S.scale * tc::kLog2e;
         const float2 st = mine ? __ldg(stats + ((int64_t)head * S.nq + t.q0 + first) * S.g + r) : make_float2(-INFINITY, 0.f);
         const float2 c2 = make_float2(c, c), minus_lse = make_float2(st.x, st.x), minus_d = make_float2(st.y, st.y);
-        for (int i = 0; i < n; ++i) {
+        if (C::kInTmem && n > 0 && w.all(&bars.held_full, 0)) {      // the row of q, or of dO, to TMEM
+            const uint32_t row = smem_u32(half ? sdo : sq) + r * 128;
+#pragma unroll
+            for (int j = 0; j < 8; j += 4) {
+                uint32_t x[16];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint4 u = lds_u4(row + (((j + k) ^ (r & 7)) << 4));      // (128-byte swizzle)
+                    x[4 * k] = u.x, x[4 * k + 1] = u.y, x[4 * k + 2] = u.z, x[4 * k + 3] = u.w;
+                }
+                tmem_st_x16(tb + lanes + C::kOwn + 32 * half + 4 * j, x);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.own_full);
+        }
+        for (int i = 0; i < n && w.ok; ++i) {
             uint32_t word[1];
             const bool all = valid_keys(S, t.k0 + (t0 + i) * kStep + 32 * half, t.k0 + t.lk, word);
             if (!w.all(&bars.s_full, i & 1)) break;
@@ -245,7 +281,7 @@ cross_dq(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_
 
 // ---------------------------------------------------------------------------- dk, dv
 
-// Head dims up to 64 as for dq; above, the results take half of TMEM, and one CTA has two groups of eight warps on tiles in
+// Head dims up to 64 as for dq (but TMEM has no room for k and v); above, the results take half of TMEM, and one CTA has two groups of eight warps on tiles in
 // turn, with scores of their own.
 template <int PANELS>
 struct DkvCfg {
