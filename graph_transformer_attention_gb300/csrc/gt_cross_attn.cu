@@ -145,12 +145,19 @@ __global__ void __launch_bounds__(kThreads) cross_sum(const SumJob j0, const Sum
     float acc[8] = {};
     const float* p = J.part + (live ? item * d + c : 0);
     const int64_t step = (int64_t)rows * heads * d;
-#pragma unroll 8
-    for (int z = lane; z < parts; z += LANES) {
-        float x[8];
-        unpack8(load8<Mem::kOutput>(p + z * step, live ? d - c : 0, d % 4 == 0 ? 1 : 0), x);
+    constexpr int U = LANES == 1 ? 8 : 4;      // loads on their way, those past the last part left out
+    for (int z = lane; z < parts; z += U * LANES) {
+        Raw8<float> raw[U];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] += x[i];
+        for (int u = 0; u < U; ++u)
+            raw[u] = load8<Mem::kOutput>(p + (z + u * LANES) * step, live && z + u * LANES < parts ? d - c : 0, d % 4 == 0 ? 1 : 0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float x[8];
+            unpack8(raw[u], x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i] += x[i];
+        }
     }
 #pragma unroll
     for (int o = LANES / 2; o > 0; o >>= 1)

@@ -143,7 +143,13 @@ __global__ void __launch_bounds__(kThreads) grad_scale(const __grid_constant__ T
     for (int k = threadIdx.x; k < T.count; k += kThreads) first[k] = T.e[k].unit0;
     sm100::pdl_wait();   // launched to overlap the end of the kernel that writes the partial sums
     double sum = 0.0;
-    for (int k = threadIdx.x; k < parts; k += kThreads) sum += __ldcg(part + k);
+    for (int k = threadIdx.x; k < parts; k += 4 * kThreads) {      // four loads on their way
+        double x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = k + u * kThreads < parts ? __ldcg(part + k + u * kThreads) : 0.0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) sum += x[u];
+    }
     const double norm = sqrt(block_sum(sum, red));
     if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
     // (a NaN norm makes every result NaN, unless there is no limit)

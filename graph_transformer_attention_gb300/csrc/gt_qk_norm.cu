@@ -525,9 +525,14 @@ __global__ void __launch_bounds__(kSumThreads) qk_gain_sum(const __grid_constant
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 32 + tx;
     sm100::pdl_wait();   // launched to overlap the end of the kernel that writes the partial rows
     float acc = 0.f;
-    if (c < J.d)
-#pragma unroll 8
-        for (int p = ty; p < S.ctas; p += kSumThreads / 32) acc += __ldcg(S.part + (int64_t)p * J.d + c);
+    constexpr int kStride = kSumThreads / 32, U = 16;      // loads on their way, those past the last row left out
+    for (int p = ty; p < S.ctas && c < J.d; p += U * kStride) {
+        float x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) x[u] = p + u * kStride < S.ctas ? __ldcg(S.part + (int64_t)(p + u * kStride) * J.d + c) : 0.f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) acc += x[u];
+    }
     red[ty][tx] = acc;
     __syncthreads();
     if (ty == 0 && c < J.d) {
