@@ -53,7 +53,7 @@ struct Cfg {
 
 struct Bars {
     uint64_t q_full, k_full[3], k_empty[3], v_full[3], v_empty[3];
-    uint64_t s_full[2], p_full[2], o_done, fin;
+    uint64_t s_full[2], p_full[2], o_done[2], fin;
     uint32_t tmem_base;
     int abort;
 };
@@ -107,8 +107,8 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
         for (int b = 0; b < 2; ++b) {
             mbar_init(&bars.s_full[b], 1);
             mbar_init(&bars.p_full[b], 4);
+            mbar_init(&bars.o_done[b], 1);
         }
-        mbar_init(&bars.o_done, 1);
         mbar_init(&bars.fin, 1);
         bars.abort = 0;
         fence_barrier_init();
@@ -193,18 +193,16 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
             if (elect_one()) {
                 product_rows<kKeys>(tb + C::kO, tb + kKeys * (i & 1), at(dv, s), id_o, i > 0);
                 mma_commit(&bars.v_empty[s]);
-                mma_commit(&bars.o_done);
+                mma_commit(&bars.o_done[i & 1]);
                 if (i + 2 < n) scores(i + 2);
             }
             __syncwarp();
         }
-        if (!w.ok) {
-            if (lane == 0) tc::fail(&bars.abort, status);
-            int never = 0;
-            if (elect_one()) mma_commit(&bars.fin);
-            __syncwarp();
-            mbar_wait_all(&bars.fin, 0, &never, tc::kWaitNs);
-        }
+        if (!w.ok && lane == 0) tc::fail(&bars.abort, status);
+        int never = 0;
+        if (elect_one()) mma_commit(&bars.fin);      // all products
+        __syncwarp();
+        mbar_wait_all(&bars.fin, 0, &never, tc::kWaitNs);
     } else {
         const int r = warp * 32 + lane;
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
@@ -246,7 +244,7 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
                 // raise the bases of the warp's rows: O so far, and its sum, in the new ones (rows without a query have no
                 // say: what stands in theirs would change the others' roundings)
                 const float higher = fmaxf(base, top), by = base == -INFINITY ? 0.f : ex2((base - higher) * c);
-                if (!w.all(&bars.o_done, (i - 1) & 1)) break;      // O is still (the product before was ahead of these scores)
+                if (!w.all(&bars.o_done[(i - 1) & 1], ((i - 1) >> 1) & 1)) break;      // O is still
                 tc_fence_after();
                 for (int k = 0; k < steps; ++k) {
                     uint32_t o[16];
@@ -274,8 +272,8 @@ cross_fwd(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.p_full[i & 1]);
         }
-        if (n > 1 && w.ok) w.all(&bars.o_done, (n - 2) & 1);
-        if (n > 0 && w.ok) w.all(&bars.o_done, (n - 1) & 1);
+        // all products, by a barrier of one phase (of o_done's, two may be over by the time a warp asks for the first)
+        if (w.ok) w.all(&bars.fin, 0);
         if (!w.ok && lane == 0) tc::fail(&bars.abort, status);
         tc_fence_after();
         if (some && w.ok) {
