@@ -358,7 +358,7 @@ int sum_parts(const SumJob& a, const SumJob& b, int jobs, const int32_t* off, in
               cudaStream_t s) {
     LaunchScope ls("cross_sum", s);
     // eight lanes to an eight where there are too few of them to fill the SMs (128 x 8 heads of 8 in 27 parts: 13 us with one
-    // lane, most of it one load after the other, 8 with eight; 4096 x 8 heads of 64 in 7 parts: 20 us with one, 25 with two)
+    // lane, 6 with eight; 4096 x 8 heads of 64 in 7 parts: 19 us with one, 25 with two)
     const int64_t eights = (int64_t)rows * heads * ((d + 7) / 8);
     const int lanes = eights < (int64_t)4 * num_sms() * kThreads ? 8 : 1;
     if (launch_overlapped(lanes == 8 ? cross_sum<T, 8> : cross_sum<T, 1>,

@@ -4,13 +4,14 @@
 //
 //   p = exp(s - lse),  D = <dO, o>,  dS = p (dO v^T - D),  dq = scale dS k,  dk = scale dS^T q,  dv = p^T dO
 //
-// In both the scores and dP are formed again tile by tile, p and dS by warps that have a row each, and p and dS go back to
-// TMEM as bf16 operands (half a step, 2^-8 of each entry at most, independent from one to the next).  The scores' scale comes last.
+// In both the scores and dP are formed again tile by tile, p and dS by warps that have a row each, and p and dS go back
+// to TMEM as bf16 operands (half a step, 2^-8 of each entry at most, independent from one to the next).  The scores'
+// scale comes last.
 //
-// What bounds both is shared memory, which a product of two operands there reads at 128 bytes a cycle (128 x 64 x 16: 48 cycles, from
-// TMEM 32), and the way from products to arithmetic and back (with neither products nor arithmetic, only the barriers: 248 us each for
-// 4096 x 32768, 8 heads of 64).  There dq takes 327 us, dk and dv 485, 816 TFLOP/s of five products over the call; 4099 x 20001, 16 heads of
-// 128 over 4: 105 and 127 us.
+// What bounds both is shared memory, which a product of two operands there reads at 128 bytes a cycle (128 x 64 x 16: 48
+// cycles, from TMEM 32), and the way from products to arithmetic and back (with neither products nor arithmetic, only the
+// barriers: 248 us each for 4096 x 32768, 8 heads of 64).  There dq takes 327 us, dk and dv 485, 816 TFLOP/s of five
+// products over the call; 4099 x 20001, 16 heads of 128 over 4: 105 and 127 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -33,11 +34,12 @@ __device__ __forceinline__ float2 pair_of(uint32_t a, uint32_t b) {
 
 // ---------------------------------------------------------------------------- dq
 
-// Eight warps (four to each half of a tile), 256 TMEM columns, two CTAs to an SM, each one's products beside the other's arithmetic.  (What a CTA's
-// issuing warp does for a tile, one instruction after the other between the arithmetic warps', bounds it: one CTA with two or
-// three groups of four warps on tiles in turn took longer than two CTAs with one, 4096x32768, 8 heads of 64: dq 567 and
-// 422 us, dk and dv 599 and 495.)  Up to 64 channels q and dO are moved to the columns that are left: 377 -> 327 us; with two tiles of 48
-// keys there instead 390.  Head dims above 64 leave room for one tile of values, which are done with before the keys.
+// Eight warps (four to each half of a tile), 256 TMEM columns, two CTAs to an SM, each one's products beside the other's
+// arithmetic.  (What a CTA's issuing warp does for a tile, one instruction after the other between the arithmetic warps',
+// bounds it: one CTA with two or three groups of four warps on tiles in turn took longer than two CTAs with one,
+// 4096x32768, 8 heads of 64: dq 567 and 422 us, dk and dv 599 and 495.)  Up to 64 channels q and dO are moved to the
+// columns that are left: 377 -> 327 us; with two tiles of 48 keys there instead 390.  Head dims above 64 leave room for
+// one tile of values, which are done with before the keys.
 template <int PANELS>
 struct DqCfg {
     static constexpr int kKStages = PANELS == 1 ? 3 : 2, kVStages = PANELS == 1 ? 3 : 1;
@@ -281,8 +283,8 @@ cross_dq(const Shape S, const __grid_constant__ CUtensorMap map_q, const __grid_
 
 // ---------------------------------------------------------------------------- dk, dv
 
-// Head dims up to 64 as for dq (but TMEM has no room for k and v); above, the results take half of TMEM, and one CTA has two groups of eight warps on tiles in
-// turn, with scores of their own.
+// Head dims up to 64 as for dq (but TMEM has no room for k and v); above, the results take half of TMEM, and one CTA has
+// two groups of eight warps on tiles in turn, with scores of their own.
 template <int PANELS>
 struct DkvCfg {
     static constexpr int kGroups = PANELS, kPerSm = 3 - PANELS;

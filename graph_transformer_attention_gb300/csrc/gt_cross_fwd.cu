@@ -6,20 +6,21 @@
 // softmax by four warps (a row to a thread), P as bf16 over the scores it was made of, O += P V.  One warp loads by TMA, one
 // issues the products.  256 TMEM columns (two tiles' scores and O) and at most 105 KB of shared memory: two CTAs share an SM.
 //
-// What bounds it is the softmax warps' stream of dependent instructions (half of the issue slots; tensor cores half, exponentials
-// half), so nothing else may hold them up: the scores of tile i + 2 go out right behind the product with P of tile i, whose columns they
-// take, and a warp finds its next scores there when it comes for them, with one barrier each way.  (One tile's scores in TMEM and P
-// beside them, the next scores formed while the softmax worked: the way there and back, 1100 cycles under load, showed: 304 us instead of
-// 258 for 4096 x 32768, 8 heads of 64, whatever the products cost.)  Two tiles of 96 keys beside 64 columns of O fill 256 columns; above 64
-// channels tiles of 64.  Other splits took longer: four CTAs with tiles of 64 keys 286 us, eight warps with half a tile's keys each 285, one
-// warp each for scores and for products with P 281.
+// What bounds it is the softmax warps' stream of dependent instructions (half of the issue slots; tensor cores half,
+// exponentials half), so nothing else may hold them up: the scores of tile i + 2 go out right behind the product with P
+// of tile i, whose columns they take, and a warp finds its next scores there when it comes for them, with one barrier
+// each way.  (One tile's scores in TMEM and P beside them, the next scores formed while the softmax worked: the way there
+// and back, 1100 cycles under load, showed: 304 us instead of 258 for 4096 x 32768, 8 heads of 64, whatever the products
+// cost.)  Two tiles of 96 keys beside 64 columns of O fill 256 columns; above 64 channels tiles of 64.  Other splits took
+// longer: four CTAs with tiles of 64 keys 286 us, eight warps with half a tile's keys each 285, one warp each for scores
+// and for products with P 281.
 //
 // The maximum is lazy: a row's base is raised only when a score exceeds it by 2^8, so that O is hardly ever rescaled.
 // The weights are formed in packed pairs.  P is rounded to bf16 for the product (half a step, 2^-8 of each weight at most,
 // independent from key to key); its sum is not.
 //
-// 4096 x 32768, 8 heads of 64: 257 us and 19 for joining seven parts, 1.01 PFLOP/s.  16 single queries over 65536 keys, 32 heads of 128 over
-// 8: 56 us, 4.8 TB/s, and 8.
+// 4096 x 32768, 8 heads of 64: 257 us and 19 for joining seven parts, 1.01 PFLOP/s.  16 single queries over 65536 keys,
+// 32 heads of 128 over 8: 56 us, 4.8 TB/s, and 8.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -1,11 +1,11 @@
 // gt_cross_narrow.cu -- cross attention of fp32 storage with head dims up to 16, on the CUDA cores.
 //
-// Four threads to a row of the held side (queries for o and dq, keys for dk and dv), each with the row in registers and every
-// fourth row of the streamed tiles, which stand in shared memory and are read by broadcast; the four join at the end.
-// A score then costs its d multiply-adds and nothing to lay down weights (the tiles of 64 x 64 of the wider head dims pad
-// d to 16 and move every weight through shared memory: 128 queries over 6800 keys, 8 heads of 8, dq 36.7 and dk, dv 47.1 us).
-// The next tile's rows are on their way while a tile is worked on.  The issue slots bound it, and
-// at the sizes that do not fill the SMs the latency of a tile: 128 queries over 6800 keys, 8 heads of 8, dq 23 us, dk and dv 27.
+// Four threads to a row of the held side (queries for o and dq, keys for dk and dv), each with the row in registers and
+// every fourth row of the streamed tiles, which stand in shared memory and are read by broadcast; the four join at the
+// end. A score then costs its d multiply-adds and nothing to lay down weights (the tiles of 64 x 64 of the wider head
+// dims pad d to 16 and move every weight through shared memory: 128 queries over 6800 keys, 8 heads of 8, dq 36.7 and dk,
+// dv 47.1 us). The next tile's rows are on their way while a tile is worked on.  The issue slots bound it, and at the
+// sizes that do not fill the SMs the latency of a tile: 128 queries over 6800 keys, 8 heads of 8, dq 23 us, dk and dv 27.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>

@@ -2,11 +2,11 @@
 // does not exceed a limit:  norm = sqrt(sum over all tensors of g^2),
 // out = g * (norm <= max_norm ? 1 : max_norm / norm).
 //
-// The bytes bound it: every gradient is read for the norm, then read again and written (8 layers of width 2048, 403 million fp32: 745 us,
-// 6.5 TB/s of three passes; 812 with 16-byte accesses).  Two kernels over a table of
-// the tensors in the launch's own arguments (nothing is copied to the device, so a captured graph holds it): the warps take
-// units of kUnit elements, whichever tensor they fall into, so that hundreds of small tensors and a few large ones fill
-// the SMs alike.  The second kernel takes the units in the opposite order: what the first read last is still cached.
+// The bytes bound it: every gradient is read for the norm, then read again and written (8 layers of width 2048, 403
+// million fp32: 745 us, 6.5 TB/s of three passes; 812 with 16-byte accesses).  Two kernels over a table of the tensors in
+// the launch's own arguments (nothing is copied to the device, so a captured graph holds it): the warps take units of
+// kUnit elements, whichever tensor they fall into, so that hundreds of small tensors and a few large ones fill the SMs
+// alike.  The second kernel takes the units in the opposite order: what the first read last is still cached.
 //
 // Squares of fp32 leave the range of fp32: a unit's sum of squares outside [2^-90, 2^100] is taken again in fp64 (a
 // lane's 32 squares below 2^-149 lose less than 2^-53 of a sum above 2^-90).  A lane's units are added in two fp32 words

@@ -7,12 +7,13 @@
 //
 // R turns the pair (a, b) of channels by the angle pos * freq: (a cos - b sin, a sin + b cos).
 //
-// The bytes of x, y (dy, dx) bound it.  A head's channels are dealt to a few lanes of a warp, both channels of a pair
-// to the same lane, so that the norm is a few shuffles and the turn none; every row is read once and nothing
-// but gradients is kept for the backward, which forms r again from the x it reads anyway.  The angles are the same for
-// all heads of a row: a warp computes the cosines and sines of its rows once, into shared memory, and fetches the heads of its next rows
-// meanwhile.  (CTAs of eight warps with a barrier between angles and rows: forward 56 us, backward 109, now 43 and 72 to 75, for 32768 rows
-// of 16 and 8 heads of 64, bf16: 4.7 and 4.0 TB/s.)  Next limits: issue slots (54 and 52 %) at 16 warps to an SM.
+// The bytes of x, y (dy, dx) bound it.  A head's channels are dealt to a few lanes of a warp, both channels of a pair to
+// the same lane, so that the norm is a few shuffles and the turn none; every row is read once and nothing but gradients
+// is kept for the backward, which forms r again from the x it reads anyway.  The angles are the same for all heads of a
+// row: a warp computes the cosines and sines of its rows once, into shared memory, and fetches the heads of its next rows
+// meanwhile.  (CTAs of eight warps with a barrier between angles and rows: forward 56 us, backward 109, now 43 and 72 to
+// 75, for 32768 rows of 16 and 8 heads of 64, bf16: 4.7 and 4.0 TB/s.)  Next limits: issue slots (54 and 52 %) at 16
+// warps to an SM.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -194,10 +195,10 @@ __device__ __forceinline__ void put_gain_sums(const Job& J, const Side& S, int c
 // Heads that a group of lanes has at once; those of the next turn are on their way meanwhile.
 constexpr int items_of(bool bwd) { return bwd ? 1 : 2; }
 
-// All channels turn, or none, and move in pieces of V: a lane has channels V s .. V s + V - 1 and d / 2 + V s ..,
-// s its place in the group.  Every warp is on its own: its turns are `rows` rows each, whose angles it forms (a lane an angle,
-// for all their heads) while the next turn's heads are on their way; no barrier of the CTA holds it up.  Arithmetic in packed
-// pairs: the issue slots are the next bound behind the bytes.
+// All channels turn, or none, and move in pieces of V: a lane has channels V s .. V s + V - 1 and d / 2 + V s .., s its
+// place in the group.  Every warp is on its own: its turns are `rows` rows each, whose angles it forms (a lane an angle,
+// for all their heads) while the next turn's heads are on their way; no barrier of the CTA holds it up.  Arithmetic in
+// packed pairs: the issue slots are the next bound behind the bytes.
 template <typename TX, typename TY, int V, bool BWD>
 __global__ void __launch_bounds__(kThreads) qk_norm(const __grid_constant__ Job J) {
     constexpr int ITEMS = items_of(BWD), P = V / 2;
