@@ -187,6 +187,29 @@ def test_scores_of_any_size(gt, t):
 
 
 @pytest.mark.parametrize("t", [F, B])
+@pytest.mark.parametrize("c", [64, 128])
+def test_raised_bases_over_many_tiles(gt, c, t):
+    """Scores that rise by more than the slack of a base from tile to tile, or jump late, in sequences of many tiles whose
+    heads fill the SMs, so that one CTA sees all of them."""
+    batch, lq, lk, h = 40, 33, 700, 8
+    offs = torch.arange(batch + 1, dtype=torch.int32, device="cuda")
+    v = _t((batch * lk, h, c), t, 3)
+    q, k = torch.zeros(batch * lq, h, c, device="cuda"), torch.zeros(batch * lk, h, c, device="cuda")
+    q[:, :, 0] = torch.linspace(0.5, 3, batch * lq, device="cuda")[:, None]
+    for row in (torch.linspace(-60, 60, lk), torch.where(torch.arange(lk) == lk - 2, 40.0, torch.linspace(3, -3, lk))):
+        k[:, :, 0] = row.cuda().repeat(batch)[:, None]
+        _both(gt, q.to(t), k.to(t), v, offs * lq, offs * lk, scale=1.0)
+
+
+@pytest.mark.parametrize("t", [F, B])
+@pytest.mark.parametrize("nk", [31, 47, 48, 63, 64, 65, 95, 96, 97, 127, 128, 191, 192, 193, 289])
+@pytest.mark.parametrize("c", [40, 64, 128])
+def test_ends_of_tiles(gt, nk, c, t):
+    """Keys that fill tiles of any of the kernels' sizes, all but one of one, or one more."""
+    _both(gt, _t((35, 2, c), t, 1), _t((nk, 2, c), t, 2), _t((nk, 2, c), t, 3))
+
+
+@pytest.mark.parametrize("t", [F, B])
 @pytest.mark.parametrize("scale", [1e-30, 0.01, 2.5])
 def test_scales(gt, scale, t):
     _both(gt, _t((50, 2, 32), t, 1), _t((200, 2, 32), t, 2), _t((200, 2, 32), t, 3), scale=scale)
