@@ -240,7 +240,7 @@ struct Plan {
 
 Plan plan_of(const Shape& S, bool f32) {
     Plan p;
-    const double q_bytes = 12.0 * S.nq * S.h * S.d, k_bytes = 16.0 * S.nk * S.hk * S.d;
+    const double q_bytes = 8.0 * S.nq * S.h * S.d, k_bytes = 16.0 * S.nk * S.hk * S.d;
     const double wide = S.d <= 64 ? 1.0 : 1.6;
     const int few = few_rows(S);
     if (few) {
@@ -270,8 +270,8 @@ Plan plan_of(const Shape& S, bool f32) {
         const int keys = S.d <= 64 ? 96 : 64, tq = tile_queries(64, S.g);
         const int64_t qt = tiles_of(S.nq, S.batch, tile_queries(128, S.g)) * S.hk, kt = tiles_of(S.nk, S.batch, 128) * S.hk;
         if (!few) p.fwd = parts_for(qt, (S.nk / S.batch + keys - 1) / keys, S.batch,
-                                     few_tile(S) ? Cost{0.7, 2, q_bytes} : Cost{1.2, 2, q_bytes});
-        p.dq = parts_for(qt, (S.nk / S.batch + 63) / 64, S.batch, Cost{S.d <= 64 ? 0.85 : 1.5, 2, q_bytes});
+                                     few_tile(S) ? Cost{0.7, 2, q_bytes} : Cost{S.d <= 64 ? 0.8 : 1.2, 2, q_bytes});
+        p.dq = parts_for(qt, (S.nk / S.batch + 63) / 64, S.batch, Cost{S.d <= 64 ? 0.72 : 1.5, 2, q_bytes});
         p.dkv = parts_for(kt, (S.nq / S.batch + tq - 1) / tq, S.batch, S.d <= 64 ? Cost{1.15, 2, k_bytes} : Cost{1.0, 1, k_bytes});
     }
     return p;
