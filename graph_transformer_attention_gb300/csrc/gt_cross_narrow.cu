@@ -244,38 +244,41 @@ __global__ void __launch_bounds__(kThreads, DP == 8 ? 3 : 2) cross_bwd_narrow(co
     }
     const int r = threadIdx.x / kPhases, phase = threadIdx.x % kPhases;
     const float c = S.scale * tc::kLog2e;
-    const Rows qr = rows_of(in.q, t.q0, head * S.g, S.g, vec.q), dr = rows_of(in.dO, t.q0, head * S.g, S.g, vec.dO);
+    // (a sequence may have more than 2^31 rows (query, head): a tile's rows are counted from its first query on)
+    auto q_rows = [&](int query) { return rows_of(in.q, t.q0 + (int64_t)query, head * S.g, S.g, vec.q); };
+    auto do_rows = [&](int query) { return rows_of(in.dO, t.q0 + (int64_t)query, head * S.g, S.g, vec.dO); };
+    auto stats_of = [&](int query) { return in.stats + ((int64_t)head * S.nq + t.q0 + query) * S.g; };
     const Rows kr = rows_of(in.k, t.k0, head, 1, vec.k), vr = rows_of(in.v, t.k0, head, 1, vec.v);
     const int first = t.tile * (KEYS ? kHeld : tq);
     const int live = KEYS ? min(kHeld, t.lk - first) : min(tq, t.lq - first) * S.g;
     const int tiles = KEYS ? (t.lq + tq - 1) / tq : (t.lk + kStream - 1) / kStream;
     Row<DP> x1, x2, a1 = {}, a2 = {};
     float2 own;      // dq: -lse and -D of the row; dk, dv: 0 or -infinity
-    const float2* stats = in.stats + ((int64_t)head * S.nq + t.q0) * S.g;
     if (KEYS) {
         const bool seen = r < live && (!S.mask || __ldg(S.mask + t.k0 + first + r) != 0);
         x1 = get_row<DP>(kr, first + r, seen, S.d);
         x2 = get_row<DP>(vr, first + r, seen, S.d);
         own = make_float2(seen ? 0.f : -INFINITY, 0.f);
     } else {
-        x1 = get_row<DP>(qr, first * S.g + r, r < live, S.d);
-        x2 = get_row<DP>(dr, first * S.g + r, r < live, S.d);
-        own = r < live ? __ldg(stats + first * S.g + r) : make_float2(-INFINITY, 0.f);
+        x1 = get_row<DP>(q_rows(first), r, r < live, S.d);
+        x2 = get_row<DP>(do_rows(first), r, r < live, S.d);
+        own = r < live ? __ldg(stats_of(first) + r) : make_float2(-INFINITY, 0.f);
     }
     auto fetch = [&](int n, Staged<DP>& st) {
         if (!KEYS) {
             fetch_keys<DP>(S, t, kr, vr, n, st);
             return;
         }
-        const int r0 = n * tq * S.g, rows = min(tq * S.g, t.lq * S.g - r0);
+        const int query = n * tq, rows = min(tq, t.lq - query) * S.g;
+        const Rows qr = q_rows(query), dr = do_rows(query);
 #pragma unroll
         for (int i = 0; i < Staged<DP>::N; ++i) {
             const int at = threadIdx.x + i * kThreads, row = at / (DP / 4), col = at % (DP / 4) * 4;
-            st.a[i] = get4(qr, r0 + row, row < rows, col, S.d);
-            st.b[i] = get4(dr, r0 + row, row < rows, col, S.d);
+            st.a[i] = get4(qr, row, row < rows, col, S.d);
+            st.b[i] = get4(dr, row, row < rows, col, S.d);
         }
         if (threadIdx.x < kStream)
-            st.s = (int)threadIdx.x < rows ? __ldg(stats + r0 + threadIdx.x) : make_float2(-INFINITY, 0.f);
+            st.s = (int)threadIdx.x < rows ? __ldg(stats_of(query) + threadIdx.x) : make_float2(-INFINITY, 0.f);
     };
     const int end = part_begin(tiles, z + 1, splits);
     int n = part_begin(tiles, z, splits);

@@ -408,3 +408,23 @@ def test_a_step_of_a_cross_attention_layer(gt, t):
     for got, leaf in zip((*grads, dx, dy), (*leaves[2:], X_, Y_)):
         want = leaf.grad * (0.5 / total if leaf is not X_ and leaf is not Y_ else 1.0)
         assert float((got.double() - want).norm()) <= tol * float(want.norm())
+
+
+def test_query_and_head_rows_past_32_bits(gt):
+    """More than 2^31 (query, head) rows on one key head, in fp32 of one channel: dO is 0 but for a few rows from both ends
+    and the middle, against fp64 of these (what the others add is exactly 0)."""
+    torch.cuda.empty_cache()
+    nq, h, nk = 2 ** 25 + 1003, 64, 5
+    q, k, v = _t((nq, h, 1), F, 1), _t((nk, 1, 1), F, 2), _t((nk, 1, 1), F, 3)
+    rows = torch.tensor([0, 1, 77, 2 ** 24 - 1, 2 ** 24, 2 ** 25 - 1, 2 ** 25, 2 ** 25 + 63, nq - 2, nq - 1], device="cuda")
+    do = torch.zeros(nq, h, 1, device="cuda")
+    do[rows] = _t((rows.numel(), h, 1), F, 4)
+    o, lse = gt.gt_cross_attn_fwd(q, k, v)
+    R.check({"o": o[rows], "lse": lse[:, rows]}, X.attn_fwd(q[rows], k, v))
+    dq, dk, dv = gt.gt_cross_attn_bwd(q, k, v, o, do, lse)
+    want = X.attn_bwd(q[rows], k, v, o[rows], do[rows], lse[:, rows])
+    R.check({"dq": dq[rows], "dk": dk, "dv": dv}, want)
+    dq[rows] = 0
+    assert int(torch.count_nonzero(dq)) == 0
+    del q, do, o, lse, dq
+    torch.cuda.empty_cache()
