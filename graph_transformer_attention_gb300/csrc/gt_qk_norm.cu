@@ -233,7 +233,10 @@ __global__ void __launch_bounds__(kThreads) qk_norm(const __grid_constant__ Job 
         const int it = k * groups + group;
         row_k[k] = rows > 1 ? it / h : 0;
         head_k[k] = it - row_k[k] * h;
-        if (row_k[k] >= rows) row_k[k] = INT32_MAX / 2;      // no such row
+        if (row_k[k] >= rows) {      // no such row in a turn: no head is that far, and no call has so many
+            row_k[k] = 0;
+            head_k[k] = INT32_MAX;
+        }
         x_k[k] = (int64_t)row_k[k] * ldx + (int64_t)head_k[k] * hdx;
         dy_k[k] = (int64_t)row_k[k] * lddy + (int64_t)head_k[k] * hddy;
         y_k[k] = (int64_t)row_k[k] * ldy + (int64_t)head_k[k] * hdy;

@@ -194,3 +194,29 @@ def test_streams_and_graphs(gt):
         graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def _tail_and_beginning(n):
+    """Rows at the beginning, around 2^30 rows before the end and at the end."""
+    return torch.cat([torch.arange(300), torch.arange(n // 2, n // 2 + 100), torch.arange(n - 300, n)]).cuda()
+
+
+def test_rows_past_2_to_the_30(gt):
+    """More than 2^30 rows whose heads do not fill the lanes of a warp, in place: each row once."""
+    torch.cuda.empty_cache()
+    n, c = 2 ** 30 + 150, 16
+    x, g, f = torch.empty(n, 1, c, dtype=B, device="cuda").normal_(), _gain(c, 2), _freq(c)
+    at = _tail_and_beginning(n)
+    want = X.qk_fwd(x[at], g, f, at.int(), 0, EPS, B)
+    gt.gt_qk_norm_fwd(x, None, g, freq=f, eps=EPS, out_q=x)
+    R.check({"y": x[at]}, want)
+    del x
+    torch.cuda.empty_cache()
+    # backward: one row of x many times, three heads to a row, dx over its own dy
+    h, c = 3, 8
+    x, dy, g = _t((1, h, c), B, 3).expand(n, h, c), torch.empty(n, h, c, dtype=B, device="cuda").normal_(), _gain(c, 4)
+    want = X.qk_bwd(dy[at], x[at], g, None, None, 0, EPS)
+    gt.gt_qk_norm_bwd(dy, None, x, None, g, eps=EPS, dq=dy)
+    R.check({"dx": dy[at]}, {"dx": want["dx"]})
+    del dy
+    torch.cuda.empty_cache()
