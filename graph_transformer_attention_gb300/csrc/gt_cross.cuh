@@ -149,6 +149,21 @@ __device__ __forceinline__ void clear_rows(uint32_t base, uint32_t panel_bytes, 
     __syncwarp();
 }
 
+// Copies of row 0 in rows first .. rows - 1 of a [rows][128 bytes] panel under the 128-byte swizzle (eights of channels
+// change places by the row's last three bits).
+template <int PANELS>
+__device__ __forceinline__ void repeat_row(uint32_t base, uint32_t panel_bytes, int first, int rows) {
+    const int lane = threadIdx.x & 31, piece = lane & 7;
+#pragma unroll
+    for (int p = 0; p < PANELS; ++p) {
+        const uint4 x = sm100::lds_u4(base + p * panel_bytes + piece * 16);
+        for (int r = first + (lane >> 3); r < rows; r += 4)
+            sm100::sts_u4(base + p * panel_bytes + r * 128 + ((piece ^ (r & 7)) << 4), x.x, x.y, x.z, x.w);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+}
+
 // Zeros in rows first .. rows - 1.
 template <int PANELS>
 __device__ __forceinline__ void clear_tail(uint32_t base, uint32_t panel_bytes, int first, int rows) {

@@ -394,13 +394,16 @@ cross_dkv(const Shape S, const __grid_constant__ CUtensorMap map_k, const __grid
         const SmemDesc r_q = smem_desc_split(smem_u32(sq), kStepPanel, 1024, 2);      // along its rows
         const SmemDesc r_do = smem_desc_split(smem_u32(sdo), kStepPanel, 1024, 2);
         auto at = [](SmemDesc d, int s) { return SmemDesc{d.lo + s * (C::kStepBytes >> 4), d.hi}; };
-        // What can be done ahead of a tile's products: its rows have landed, those behind its sequence are cleared.
+        // What can be done ahead of a tile's products: its rows have landed, and those behind its sequence weigh nothing: dO
+        // is 0, the statistic -infinity, and q the tile's first row, whose score with a key that holds an infinity is an
+        // infinity and no NaN (0 x infinity), unless that row spoils the key's gradients anyway.  (Masks of p and dS instead:
+        // 860 to 909 us a call instead of 830, 4096 x 32768, 8 heads of 64.)
         auto ready = [&](int i) {
             const int s = i % kStages;
             if (!w.all(&bars.q_full[s], (i / kStages) & 1)) return;
             const int live = rows_of(i);
             if (live < kStep) {
-                clear_tail<PANELS>(smem_u32(sq + s * C::kStepBytes), kStepPanel, live, kStep);
+                repeat_row<PANELS>(smem_u32(sq + s * C::kStepBytes), kStepPanel, live, kStep);
                 clear_tail<PANELS>(smem_u32(sdo + s * C::kStepBytes), kStepPanel, live, kStep);
             }
         };

@@ -289,8 +289,10 @@ __global__ void __launch_bounds__(kThreads, DP == 8 ? 3 : 2) cross_bwd_narrow(co
         put<DP>(T, st);
         __syncthreads();
         if (n + 1 < end) fetch(n + 1, st);
+        // (queries that are not there are left out: 0 times an infinity of the key would be NaN)
+        const int rows = KEYS ? min(tq, t.lq - n * tq) * S.g : kStream;
 #pragma unroll 4
-        for (int j = phase; j < kStream; j += kPhases) {
+        for (int j = phase; j < rows; j += kPhases) {
             const Row<DP> y1 = row_at<DP>(T.a, j), y2 = row_at<DP>(T.b, j);
             const float2 s = T.s[j];
             // (where nobody sees the key both factors are 0: the rows were cleared, the exponent is -infinity)

@@ -313,7 +313,9 @@ __global__ void __launch_bounds__(kThreads) cross_bwd_f32(const Shape S, const B
             for (int j = 0; j < 4; ++j) {
                 const int held = 4 * ty + i, other = tx + 16 * j;
                 const float2 st = stat[KEYS ? other : held];
-                const bool seen = keep[KEYS ? held : other];
+                // (a query without a key, or that is not there, weighs nothing, whatever its score: with an infinity in the
+                // key that may be NaN)
+                const bool seen = keep[KEYS ? held : other] && st.x != -INFINITY;
                 const float p = seen ? sm100::ex2(fmaf(x[i][j], c, st.x)) : 0.f;
                 x[i][j] = p;
                 y[i][j] = seen ? p * (y[i][j] + st.y) : 0.f;

@@ -428,3 +428,26 @@ def test_query_and_head_rows_past_32_bits(gt):
     assert int(torch.count_nonzero(dq)) == 0
     del q, do, o, lse, dq
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("t", [F, B])
+@pytest.mark.parametrize("h,hk,c", [(4, 4, 8), (3, 1, 16), (3, 1, 40), (4, 2, 64), (3, 1, 128)])
+@pytest.mark.parametrize("nq", [1, 37, 64, 131])
+def test_infinities_in_visible_keys(gt, nq, h, hk, c, t):
+    """Keys whose score is -infinity with every query weigh nothing, their gradients are 0, and whether the queries fill
+    their tiles makes no difference; against the same call with those keys hidden."""
+    q, k, v, do = _t((nq, h, c), t, 1), _t((200, hk, c), t, 2), _t((200, hk, c), t, 3), _t((nq, h, c), t, 4)
+    q[..., 0] = q[..., 0].abs() + 1
+    far = torch.zeros(200, dtype=torch.bool, device="cuda")
+    far[[0, 77, 130, 199]] = True
+    k[far, :, 0] = -math.inf
+    cut = nq // 3
+    for offs in ((None, None), (_off(0, cut, nq), _off(0, 90, 200))):
+        o, lse = gt.gt_cross_attn_fwd(q, k, v, *offs)
+        R.check({"o": o, "lse": lse}, X.attn_fwd(q, k, v, *offs, mask=~far))
+        dq, dk, dv = gt.gt_cross_attn_bwd(q, k, v, o, do, lse, *offs)
+        assert (dk[far] == 0).all() and (dv[far] == 0).all()
+        want = X.attn_bwd(q, k, v, o, do, lse, *offs, mask=~far)
+        # (channel 0 of dq is a sum with 0 x infinity in it, in the formula too)
+        R.check({"dk": dk, "dv": dv, "dq": dq[..., 1:]},
+                {"dk": want["dk"], "dv": want["dv"], "dq": tuple(x[..., 1:] for x in want["dq"])})
