@@ -295,7 +295,8 @@ __global__ void __launch_bounds__(kThreads, DP == 8 ? 3 : 2) cross_bwd_narrow(co
         for (int j = phase; j < rows; j += kPhases) {
             const Row<DP> y1 = row_at<DP>(T.a, j), y2 = row_at<DP>(T.b, j);
             const float2 s = T.s[j];
-            // (where nobody sees the key both factors are 0: the rows were cleared, the exponent is -infinity)
+            // (where nobody sees the key both factors are 0: the rows were cleared, the exponent is -infinity; but for queries
+            // that are not numbers)
             const float p = sm100::ex2(fmaf(dot<DP>(x1, y1), c, own.x + s.x));
             const float ds = p * (dot<DP>(x2, y2) + (KEYS ? s.y : own.y));
             if (KEYS) axpy<DP>(p, y2, a2);
@@ -306,6 +307,7 @@ __global__ void __launch_bounds__(kThreads, DP == 8 ? 3 : 2) cross_bwd_narrow(co
     if (KEYS) phases_sum<DP>(a2);
     if (KEYS) sm100::pdl_wait();
     if (r >= live) return;
+    if (KEYS && own.x == -INFINITY) a1 = a2 = Row<DP>{};
     if (KEYS) {
         const int64_t key = t.k0 + first + r, at = ((z * (int64_t)S.nk + key) * S.hk + head) * S.d;
         put_row<DP>(splits == 1 ? static_cast<float*>(g1.p) + key * g1.row + head * g1.head : part1 + at, S.d, phase, a1, S.scale);

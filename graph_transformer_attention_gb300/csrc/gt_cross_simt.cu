@@ -342,6 +342,9 @@ __global__ void __launch_bounds__(kThreads) cross_bwd_f32(const Shape S, const B
                 pk = part1 + at;
                 pv = part2 + at;
             }
+            if (!keep[r])      // (weights of 0 do not cancel queries that are not numbers)
+#pragma unroll
+                for (int n = 0; n < cols_per_thread<DP>(); ++n) acc1[i][n] = acc2[i][n] = 0.f;
             put_row<DP>(pk, tx, S.d, acc1[i], S.scale);
             put_row<DP>(pv, tx, S.d, acc2[i], 1.f);
         } else {

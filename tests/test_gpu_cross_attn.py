@@ -451,3 +451,28 @@ def test_infinities_in_visible_keys(gt, nq, h, hk, c, t):
         # (channel 0 of dq is a sum with 0 x infinity in it, in the formula too)
         R.check({"dk": dk, "dv": dv, "dq": dq[..., 1:]},
                 {"dk": want["dk"], "dv": want["dv"], "dq": tuple(x[..., 1:] for x in want["dq"])})
+
+
+@pytest.mark.parametrize("t", [F, B])
+@pytest.mark.parametrize("h,hk,c", [(4, 4, 8), (3, 1, 16), (3, 1, 40), (4, 2, 64), (3, 1, 128)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_hidden_keys_have_no_gradient_whatever_the_queries_hold(gt, bad, h, hk, c, t):
+    """A query, or its dO, that is not a number spoils the keys that it sees, and those only."""
+    cq, ck = [0, 70, 110], [0, 150, 290]
+    q, k, v, do = _t((110, h, c), t, 1), _t((290, hk, c), t, 2), _t((290, hk, c), t, 3), _t((110, h, c), t, 4)
+    mask = torch.arange(290, device="cuda") % 5 != 2
+    mask[64:140] = False
+    offs = _off(*cq), _off(*ck)
+    o, lse = gt.gt_cross_attn_fwd(q, k, v, *offs, mask)
+    clean = gt.gt_cross_attn_bwd(q, k, v, o, do, lse, *offs, mask)
+    for x in (q, do):
+        kept = x[5].clone()
+        x[5] = bad
+        o2 = o.clone()      # (an infinity may raise the bases of other rows, and with that their roundings)
+        o2[5] = gt.gt_cross_attn_fwd(q, k, v, *offs, mask)[0][5]
+        dq, dk, dv = gt.gt_cross_attn_bwd(q, k, v, o2, do, lse, *offs, mask)
+        assert (dk[~mask] == 0).all() and (dv[~mask] == 0).all()
+        assert torch.equal(dk[150:], clean[1][150:]) and torch.equal(dv[150:], clean[2][150:])
+        dq[5] = clean[0][5]
+        assert torch.equal(dq, clean[0])
+        x[5] = kept
