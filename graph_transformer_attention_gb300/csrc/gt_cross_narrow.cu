@@ -148,7 +148,8 @@ struct Vec {
     bool q, k, v, dO;
 };
 
-// Keys of streamed tile n, on their way: k, v and whether anyone sees the key (0 or -infinity).
+// Keys of streamed tile n, on their way: k, v and whether anyone sees the key: what is added to a score (0 or
+// -infinity), and what bounds it (either infinity).
 template <int DP>
 __device__ __forceinline__ void fetch_keys(const Shape& S, const Tile& t, const Rows& k, const Rows& v, int n, Staged<DP>& st) {
     const int k0 = n * kStream, keys = min(kStream, t.lk - k0);
@@ -160,7 +161,7 @@ __device__ __forceinline__ void fetch_keys(const Shape& S, const Tile& t, const 
         st.a[i] = get4(k, k0 + r, there, c, S.d);
         st.b[i] = get4(v, k0 + r, there, c, S.d);
     }
-    if (threadIdx.x < kStream) st.s = make_float2(seen(threadIdx.x) ? 0.f : -INFINITY, 0.f);
+    if (threadIdx.x < kStream) st.s = seen(threadIdx.x) ? make_float2(0.f, INFINITY) : make_float2(-INFINITY, -INFINITY);
 }
 
 template <int DP>
@@ -192,7 +193,9 @@ __global__ void __launch_bounds__(kThreads) cross_fwd_narrow(const Shape S, cons
             float s[4], top = m;
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                s[u] = fmaf(dot<DP>(x, row_at<DP>(T.a, j0 + u * kPhases)), c, T.s[j0 + u * kPhases].x);
+                // (the smaller of two is never a NaN: a key that nobody sees gives -infinity whatever the query holds; the NaN
+                // of a key that is seen becomes infinity, and its weight NaN again)
+                s[u] = fminf(dot<DP>(x, row_at<DP>(T.a, j0 + u * kPhases)) * c, T.s[j0 + u * kPhases].y);
                 top = fmaxf(top, s[u]);
             }
             const float base = top == -INFINITY ? 0.f : top, by = sm100::ex2(m - base);
@@ -295,8 +298,8 @@ __global__ void __launch_bounds__(kThreads, DP == 8 ? 3 : 2) cross_bwd_narrow(co
         for (int j = phase; j < rows; j += kPhases) {
             const Row<DP> y1 = row_at<DP>(T.a, j), y2 = row_at<DP>(T.b, j);
             const float2 s = T.s[j];
-            // (where nobody sees the key both factors are 0: the rows were cleared, the exponent is -infinity; but for queries
-            // that are not numbers)
+            // (where nobody sees the key both factors are 0: the rows were cleared, the exponent is -infinity; unless the query
+            // is not a number: see below)
             const float p = sm100::ex2(fmaf(dot<DP>(x1, y1), c, own.x + s.x));
             const float ds = p * (dot<DP>(x2, y2) + (KEYS ? s.y : own.y));
             if (KEYS) axpy<DP>(p, y2, a2);
@@ -307,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, DP == 8 ? 3 : 2) cross_bwd_narrow(co
     if (KEYS) phases_sum<DP>(a2);
     if (KEYS) sm100::pdl_wait();
     if (r >= live) return;
-    if (KEYS && own.x == -INFINITY) a1 = a2 = Row<DP>{};
+    if (own.x == -INFINITY) a1 = a2 = Row<DP>{};      // a key that nobody sees, a query that sees none
     if (KEYS) {
         const int64_t key = t.k0 + first + r, at = ((z * (int64_t)S.nk + key) * S.hk + head) * S.d;
         put_row<DP>(splits == 1 ? static_cast<float*>(g1.p) + key * g1.row + head * g1.head : part1 + at, S.d, phase, a1, S.scale);

@@ -476,3 +476,31 @@ def test_hidden_keys_have_no_gradient_whatever_the_queries_hold(gt, bad, h, hk, 
         dq[5] = clean[0][5]
         assert torch.equal(dq, clean[0])
         x[5] = kept
+
+
+@pytest.mark.parametrize("t", [F, B])
+@pytest.mark.parametrize("h,hk,c", [(4, 4, 8), (2, 1, 8), (3, 1, 16), (4, 4, 16), (3, 1, 40), (4, 2, 64), (3, 1, 128)])
+@pytest.mark.parametrize("lq", [1, 45])
+def test_queries_that_see_no_key_whatever_they_hold(gt, lq, h, hk, c, t):
+    """Sequences whose keys are all hidden, or that have none: o = 0, lse = -infinity and dq = 0 for queries, and with dO,
+    that are not numbers; with keys enough for several parts."""
+    lens = [300, 700, 0, 130]
+    ck = [sum(lens[:i]) for i in range(5)]
+    nq, nk = 4 * lq, ck[-1]
+    q, k, v, do = _t((nq, h, c), t, 1), _t((nk, hk, c), t, 2), _t((nk, hk, c), t, 3), _t((nq, h, c), t, 4)
+    mask = torch.ones(nk, dtype=torch.bool, device="cuda")
+    mask[ck[1]:ck[2]] = False
+    k[~mask] = math.nan
+    offs = _off(*range(0, nq + 1, lq)), _off(*ck)
+    clean = gt.gt_cross_attn_fwd(q, k, v, *offs, mask)
+    grads = gt.gt_cross_attn_bwd(q, k, v, clean[0], do, clean[1], *offs, mask)
+    empty = slice(lq, 3 * lq)
+    for bad in (math.nan, math.inf, -math.inf):
+        q[empty, :, c // 2] = bad
+        do[empty, :, c - 1] = bad
+        o, lse = gt.gt_cross_attn_fwd(q, k, v, *offs, mask)
+        assert (o[empty] == 0).all() and (lse[:, empty] == -math.inf).all()
+        assert torch.equal(o, clean[0]) and torch.equal(lse, clean[1])
+        got = gt.gt_cross_attn_bwd(q, k, v, o, do, lse, *offs, mask)
+        assert (got[0][empty] == 0).all()
+        assert all(torch.equal(a, b) for a, b in zip(got, grads))
