@@ -154,7 +154,11 @@ __global__ void __launch_bounds__(kThreads) grad_scale(const __grid_constant__ T
     if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
     // (a NaN norm makes every result NaN, unless there is no limit)
     const bool as_is = norm <= (double)max_norm || isinf(max_norm);
-    const float factor = as_is ? 1.f : (float)((double)max_norm / norm);
+    const double quotient = (double)max_norm / norm;
+    const float factor = as_is ? 1.f : (float)quotient;
+    // fp32 has fewer digits of a quotient below 2^-126, or none, though the products may be ordinary numbers: these are
+    // formed in fp64
+    const bool small = !as_is && quotient < 0x1p-126 && quotient > 0.0;
     const int lane = threadIdx.x & 31;
     for (int w = blockIdx.x * kWarps + (threadIdx.x >> 5); w < T.units; w += gridDim.x * kWarps) {
         const int u = T.units - 1 - w;
@@ -174,7 +178,10 @@ __global__ void __launch_bounds__(kThreads) grad_scale(const __grid_constant__ T
             for (int j = 0; j < kEights; ++j) {
                 const int a = at_of(j, lane);
                 const int64_t more = left - a;
-                if (!as_is)
+                if (small)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[j][i] = (float)((double)v[j][i] * quotient);
+                else if (!as_is)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[j][i] *= factor;
                 store8(out + at + a, v[j], more >= 8 ? 8 : more > 0 ? (int)more : 0, e.ovec);

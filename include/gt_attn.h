@@ -554,13 +554,14 @@ int gt_qk_norm_bwd(int32_t xtype, int32_t ytype, int32_t d, float eps, const flo
  * gt_grad_clip: the norm of all gradients of a step together, and each of them scaled so that it
  * does not exceed max_norm:
  *   norm = sqrt(sum over all tensors of g^2),  out = g (norm <= max_norm ? 1 : max_norm / norm)
- * over the whole range of fp32 (squares that leave it are summed in fp64).
+ * over the whole range of fp32 (squares that leave it are summed in fp64, and a quotient below 2^-126 multiplies in fp64;
+ * a norm past the range is stored as infinity, and the gradients are scaled by what it is).
  *   list    host array of `count` tensors, read during the call only.  g: device, numel elements
  *           in a row, of gtype; out: device, of otype (output: it may be g itself with the same
  *           type; NULL: the tensor only counts).  numel may be 0.  No output may overlap another
  *           or another tensor's g.
- *   max_norm  0 or more; infinity only measures (out is g in otype).  A norm that is not finite
- *           scales by max_norm / norm all the same: 0 for infinity, NaN for NaN.
+ *   max_norm  0 or more; infinity only measures (out is g in otype).  A sum of squares that is
+ *           not finite scales by max_norm / norm all the same: 0 for infinity, NaN for NaN.
  *   norm    device fp32 [1] (output).
  *   workspace  at least gt_grad_clip_workspace_size(count) bytes, 16-byte aligned.
  * Errors: GT_ERR_INVALID_ARG for a NULL list, norm or g, count < 1, an unknown type, out = g of

@@ -162,3 +162,22 @@ def test_streams_and_graphs(gt):
     grads[0].mul_(2.0)                                             # a replay reads what is there then
     graphs[0].replay()
     R.check({"norm": n1}, X.clip(grads, 0.3, [g.dtype for g in grads]))
+
+
+@pytest.mark.parametrize("t", [F, B])
+@pytest.mark.parametrize("size,limit", [(1e30, 1e-16), (1e36, 1.0), (1e36, 1e-3), (1e36, 1e-12), (1e38, 1.0), (1e38, 1e-3),
+                                        (3e38, 1e-20)])
+def test_large_gradients_and_a_small_limit(gt, size, limit, t):
+    """max_norm / norm below the smallest normal fp32 number, or below all of them; the results are ordinary numbers."""
+    for n in (1, 4096, 70001):
+        g = (torch.rand(n, generator=torch.Generator(device="cuda").manual_seed(n), device="cuda") * 0.5 + 0.5) * size
+        grads = [g.to(t), (g[:n // 2 + 1] * -1e-2).to(t)]
+        # past fp32's range the norm reads infinity; the gradients are scaled by what it is
+        fits = float(X.clip(grads, limit, [t, t])["norm"][0]) <= torch.finfo(F).max
+        for types in ([F, F], [B, B]):
+            out = [torch.full_like(x, 7.0, dtype=y) for x, y in zip(grads, types)]
+            norm = gt.gt_grad_clip(grads, limit, out=out)
+            ref = X.clip(grads, limit, types)
+            assert fits or math.isinf(float(norm))
+            got = {"norm": norm} if fits else {}
+            R.check({**got, "out0": out[0], "out1": out[1]}, {m: ref[m] for m in (*got, "out0", "out1")}, floor=0.0)
