@@ -247,7 +247,7 @@ Plan plan_of(const Shape& S, bool f32) {
         // eight CTAs to an SM (more where the sequences are unlike), four turns of a CTA's warps at least to each
         const int64_t tiles = tiles_of(S.nq, S.batch, few / S.g) * S.hk;
         const int64_t want = (int64_t)(S.batch > 1 ? 16 : 8) * num_sms() / std::max<int64_t>(1, tiles);
-        int lanes = 1;
+        int64_t lanes = 1;
         while (lanes * 8 < S.d) lanes *= 2;
         p.fwd = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, kMaxSplits), S.nk / S.batch * lanes / 2048));
     }

@@ -80,6 +80,16 @@ def test_cross_attention_workspace_sizes(gt):
     assert gt.gt_qk_norm_workspace_size(big) == gt.gt_grad_clip_workspace_size(big) == 0
 
 
+@pytest.mark.parametrize("c", [8, 40, 128])
+def test_parts_of_long_keys(gt, c):
+    """One query over ever more keys: as many parts as keys for them are there, and no fewer where keys x lanes passes 2^31."""
+    size = gt.gt_cross_attn_workspace_size
+    few = size(0, 1, 1 << 20, 1, 1, c)
+    assert few > 0
+    for nk in (1 << 26, (1 << 27) - 1, 1 << 27, (1 << 27) + 1, 1 << 28, 1 << 29, 1 << 30):
+        assert size(0, 1, nk, 1, 1, c) == size(1, 1, nk, 1, 1, c) == few, nk
+
+
 QK = dict(xt=1, yt=0, d=64, eps=1e-6, freq=A, rot=64, pairs=0)
 
 

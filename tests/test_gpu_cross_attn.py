@@ -504,3 +504,31 @@ def test_queries_that_see_no_key_whatever_they_hold(gt, lq, h, hk, c, t):
         got = gt.gt_cross_attn_bwd(q, k, v, o, do, lse, *offs, mask)
         assert (got[0][empty] == 0).all()
         assert all(torch.equal(a, b) for a, b in zip(got, grads))
+
+
+def test_one_query_over_2_to_the_27_keys(gt):
+    """Keys x lanes past 2^31 are split and joined as fewer are; against fp64, the keys being the values too."""
+    torch.cuda.empty_cache()
+    nk, c = 2 ** 27 + 5, 72
+    k = torch.empty(nk, 1, c, dtype=B, device="cuda").normal_(generator=torch.Generator(device="cuda").manual_seed(2))
+    q = _t((1, 1, c), B, 1, 2.0)
+    gt.gt_kernel_stats_reset(False)
+    o, lse = gt.gt_cross_attn_fwd(q, k, k)
+    assert {"cross_few", "cross_join"} <= set(gt.gt_kernel_stats())
+    top, total, out, mag = -math.inf, 0.0, torch.zeros(c, dtype=torch.float64, device="cuda"), 0.0
+    for a in range(0, nk, 2 ** 22):
+        x = k[a:a + 2 ** 22, 0].double()
+        s = x @ q[0, 0].double() / math.sqrt(c)
+        new = max(top, float(s.max()))
+        p = torch.exp(s - new)
+        total, out = total * math.exp(top - new) + float(p.sum()), out * math.exp(top - new) + p @ x
+        mag = mag * math.exp(top - new) + p @ x.abs()
+        top = new
+    # 64 parts, four warps, two groups of lanes share the keys; the exponent as for any number of keys
+    steps = nk / (64 * 4 * 2) + 80
+    e = 40 * R.U32 + (c + 4) * R.U32 * 30
+    bound = (steps * R.U32 + 2 * e) * mag / total + R.half_step(B) * (out / total).abs()
+    assert bool(((o[0, 0].double() - out / total).abs() <= bound).all()) and float((out / total).abs().max()) > 20 * float(bound.max())
+    assert abs(float(lse[0, 0]) - (top + math.log(total))) <= steps * R.U32 + e + 8 * R.U32 * 30
+    del k
+    torch.cuda.empty_cache()
