@@ -515,7 +515,7 @@ typedef enum { GT_ROT_HALVES = 0, GT_ROT_PAIRS = 1 } gt_rot;
 /*
  * gt_qk_norm_fwd: the norm of every head of the queries and of the keys, and the rotation of their
  * channels by position, in one pass (before gt_bias_attn_fwd or gt_cross_attn_fwd):
- *   r = 1 / sqrt(sum_c x_c^2 / d + eps),  y = R (gain x r)
+ *   r = 1 / sqrt(sum_c x_c^2 / d + eps),  y = R (gain x r)      (for x and eps over the whole range of fp32)
  * where R turns pair i < rot / 2 of the first rot channels, (a, b) to (a cos - b sin, a sin + b cos),
  * by the angle pos * freq[i] (radians; to fp32 accuracy for any int32 position while |freq| < 2^24),
  * and leaves the channels past rot.

@@ -220,3 +220,28 @@ def test_rows_past_2_to_the_30(gt):
     R.check({"dx": dy[at]}, {"dx": want["dx"]})
     del dy
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("t", [F, B])
+@pytest.mark.parametrize("c,rot", [(8, 8), (64, 64), (128, 0), (62, 62), (65, 20), (256, 256), (1, 0)])
+@pytest.mark.parametrize("size,eps", [(1e10, 1e-6), (3e18, 1e-6), (2e19, 1e-6), (1e25, 1e-6), (1e38, 1e-6), (1e20, 3e38), (1e-12, 1e-24),
+                                      (1e-22, 1e-43), (1e-30, 1e-45)])
+def test_the_whole_range_of_fp32(gt, size, eps, c, rot, t):
+    """Squares above the largest and below the smallest fp32 number, among rows of ordinary size."""
+    eps = float(torch.tensor(eps, dtype=F))
+    q, k, gq, gk = _t((70, 3, c), F, 1, 0.5), _t((33, 1, c), F, 2, 0.5), _gain(c, 3), _gain(c, 4)
+    for x in (q, k):
+        x[::3] *= size
+        x[5] = 0
+    q, k, f = q.to(t), k.to(t), _freq(rot)
+    yq, yk = gt.gt_qk_norm_fwd(q, k, gq, gk, freq=f, eps=eps, out_dtype=F)
+    R.check({"y": yq}, X.qk_fwd(q, gq, f, None, 0, eps, F))
+    R.check({"y": yk}, X.qk_fwd(k, gk, f, None, 0, eps, F))
+    # (dy of the size that makes dx ordinary numbers, and with them their rounding a share of each)
+    scale = torch.ones(70, 1, 1, device="cuda")
+    scale[::3] = min(max(size, 1.0), 1e9)
+    dyq = _t(yq.shape, F, 5) * scale
+    dq, _, dgq, _ = gt.gt_qk_norm_bwd(dyq, None, q, None, gq, freq=f, eps=eps)
+    want = X.qk_bwd(dyq, q, gq, f, None, 0, eps)
+    tiny = 2.0 ** -150 if t == F else 2.0 ** -134      # half of the smallest step there is
+    R.check({"dx": dq, "dgain": dgq}, {"dx": (want["dx"][0], want["dx"][1] + tiny), "dgain": want["dgain"]}, floor=0.0)
