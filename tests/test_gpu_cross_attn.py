@@ -532,3 +532,51 @@ def test_one_query_over_2_to_the_27_keys(gt):
     assert abs(float(lse[0, 0]) - (top + math.log(total))) <= steps * R.U32 + e + 8 * R.U32 * 30
     del k
     torch.cuda.empty_cache()
+
+
+def _launched(gt, call):
+    """The result of a call and the names of the kernels that it launched."""
+    gt.gt_kernel_stats_reset(False)
+    result = call()
+    names = set(gt.gt_kernel_stats())
+    gt.gt_kernel_stats_reset(False)
+    return result, names
+
+
+@pytest.mark.parametrize("t", [F, B])
+@pytest.mark.parametrize("share", [1, 2])
+@pytest.mark.parametrize("c", [1, 5, 8, 16, 30, 64, 100, 128])
+@pytest.mark.parametrize("hidden", [False, True])
+def test_one_query_to_a_sequence(gt, hidden, c, share, t):
+    """Six sequences of one query in the mean, one of them of none and one of two; ragged keys, a side without any."""
+    cq, ck, hk = [0, 1, 2, 2, 4, 5, 6], [0, 0, 1, 70, 571, 640, 2000], 2
+    q, k, v = _t((6, share * hk, c), t, 1), _t((2004, hk, c), t, 2), _t((2004, hk, c), t, 3)
+    k[2000:], v[2000:] = math.nan, math.inf
+    mask = None
+    if hidden:
+        mask = torch.arange(2004, device="cuda") % 7 != 3
+        mask[571:640] = False
+        k[~mask] = math.nan
+    offs = _off(*cq), _off(*ck)
+    (o, lse), names = _launched(gt, lambda: gt.gt_cross_attn_fwd(q, k, v, *offs, mask))
+    assert "cross_few" in names
+    ref = X.attn_fwd(q, k, v, *offs, mask)
+    empty = ref["lse"][0] == -math.inf
+    assert ((lse.cpu() == -math.inf) == empty).all() and bool(empty[:, 0].all()) and (o.cpu()[empty.t()] == 0).all()
+    R.check({"o": o, "lse": lse.cpu().masked_fill(empty, 0)},
+            {"o": ref["o"], "lse": (ref["lse"][0].masked_fill(empty, 0), ref["lse"][1])})
+    assert all(torch.equal(a, b) for a, b in zip(gt.gt_cross_attn_fwd(q, k, v, *offs, mask), (o, lse)))
+
+
+@pytest.mark.parametrize("t", [F, B])
+@pytest.mark.parametrize("share", [1, 2])
+@pytest.mark.parametrize("c", [16, 64, 100])
+def test_one_query_over_many_keys(gt, c, share, t):
+    """Keys in parts, joined by a second kernel; with and without hidden ones, whole parts of them."""
+    q, k, v = _t((1, share, c), t, 1), _t((9001, 1, c), t, 2), _t((9001, 1, c), t, 3)
+    mask = torch.arange(9001, device="cuda") % 3 != 1
+    mask[2000:6500] = False
+    for keep in (None, mask):
+        (o, lse), names = _launched(gt, lambda: gt.gt_cross_attn_fwd(q, k, v, key_mask=keep))
+        assert {"cross_few", "cross_join"} <= names
+        R.check({"o": o, "lse": lse}, X.attn_fwd(q, k, v, mask=keep))

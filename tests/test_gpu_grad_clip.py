@@ -181,3 +181,19 @@ def test_large_gradients_and_a_small_limit(gt, size, limit, t):
             assert fits or math.isinf(float(norm))
             got = {"norm": norm} if fits else {}
             R.check({**got, "out0": out[0], "out1": out[1]}, {m: ref[m] for m in (*got, "out0", "out1")}, floor=0.0)
+
+
+@pytest.mark.parametrize("t", [F, B])
+@pytest.mark.parametrize("n", [1, 100, 1024, 70001])
+def test_the_norm_within_its_own_roundings(gt, n, t):
+    """A lane adds 32 squares of positive sign in four chains of 8 and joins these in two steps: 10 roundings at most, half
+    of that after the root.  A lane's units are added in two fp32 words and the rest in fp64 (2^-40 and less), then the norm
+    is rounded, or the factor and each product."""
+    grads = _grads([n, n // 3 + 1], [t])
+    limit = 0.5 * math.sqrt(math.fsum(float((R.d(g) ** 2).sum()) for g in grads))
+    out = [torch.empty_like(g) for g in grads]
+    norm = gt.gt_grad_clip(grads, limit, out=out)
+    ref, off = X.clip(grads, limit, [t, t]), (5 + 2.0 ** -10) * R.U32
+    bounds = {"norm": off + R.U32, "out0": off + 2 * R.U32 + (R.half_step(t) if t == B else 0.0)}
+    bounds["out1"] = bounds["out0"]
+    R.check({"norm": norm, "out0": out[0], "out1": out[1]}, {m: (ref[m][0], ref[m][0].abs() * bounds[m]) for m in bounds})

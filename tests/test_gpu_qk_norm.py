@@ -245,3 +245,18 @@ def test_the_whole_range_of_fp32(gt, size, eps, c, rot, t):
     want = X.qk_bwd(dyq, q, gq, f, None, 0, eps)
     tiny = 2.0 ** -150 if t == F else 2.0 ** -134      # half of the smallest step there is
     R.check({"dx": dq, "dgain": dgq}, {"dx": (want["dx"][0], want["dx"][1] + tiny), "dgain": want["dgain"]}, floor=0.0)
+
+
+@pytest.mark.parametrize("t", [F, B])
+@pytest.mark.parametrize("n,h,c", [(1, 1, 8), (1, 1, 6), (1, 3, 64), (2, 1, 128), (5, 2, 62), (9, 4, 16), (3, 2, 65)])
+def test_gain_sums_of_few_heads(gt, n, h, c, t):
+    """A sum of as many terms as there are heads is rounded at most once for each but the first, wherever they are added
+    (the zeros of idle lanes and CTAs add nothing)."""
+    x, dy, g, f = _t((n, h, c), t, 1), _t((n, h, c), t, 2), _gain(c, 3), _freq(c // 2 * 2)
+    dgain = gt.gt_qk_norm_bwd(dy, None, x, None, g, freq=f, eps=EPS)[2]
+    value, bound = X.qk_bwd(dy, x, g, f, None, 0, EPS)["dgain"]
+    xd = R.d(x)
+    part = X.turn(R.d(dy), None, f, 0, back=True) * xd * ((xd * xd).mean(-1, keepdim=True) + EPS) ** -0.5
+    terms = part.abs().sum((0, 1))
+    bound = bound - (n * h / 64 + 1024) * R.U32 * terms + (n * h - 1) * R.U32 * terms      # the terms' own errors stay
+    R.check({"dgain": dgain}, {"dgain": (value, bound + R.U32 * value.abs())}, floor=1e-38)
