@@ -322,7 +322,8 @@ Shape shape_of(int nq, int nk, int h, int hk, int d, int batch, const int32_t* q
 
 int check_shape(const Shape& S) {
     if ((S.q_off != nullptr) != (S.kv_off != nullptr) || (!S.q_off && S.batch != 1)) return GT_ERR_INVALID_ARG;
-    return S.scale > 0.f && isfinite(S.scale) ? GT_OK : GT_ERR_INVALID_ARG;
+    // (the exponents are formed with scale log2 e)
+    return S.scale > 0.f && isfinite(S.scale * tc::kLog2e) ? GT_OK : GT_ERR_INVALID_ARG;
 }
 
 bool usable(const View& v) { return v.p && v.row >= 0 && v.head >= 0; }

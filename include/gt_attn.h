@@ -482,7 +482,7 @@ int gt_linear_bwd(int32_t dtype, int32_t ytype, int32_t m, int32_t k, int32_t n,
  *   key_mask  device uint8 [nk] or NULL: keys with 0 are seen by no query (their dk and dv are 0,
  *           and nothing of theirs, infinities and NaN included, reaches any result).
  *   A query that sees no key has o = 0, lse = -infinity and dq = 0.
- *   scale   finite and above 0.
+ *   scale   above 0, and finite times log2 e (up to 2.35e38).
  *   workspace  at least gt_cross_attn_workspace_size bytes (`backward`: non-zero for the
  *           backward; `aligned`: non-zero when all bf16 inputs are read in place), 16-byte aligned; may
  *           be NULL where that is 0.

@@ -80,6 +80,17 @@ def test_cross_attention_workspace_sizes(gt):
     assert gt.gt_qk_norm_workspace_size(big) == gt.gt_grad_clip_workspace_size(big) == 0
 
 
+def test_scales_beyond_the_exponents_range_are_refused(gt):
+    """scale log2 e is infinite from 2.36e38 on, and every score would be NaN."""
+    lib = gt.load_library()
+    fwd = dict(**SIZES, **INPUTS, qo=None, ko=None, mask=None, scale=0.125, o=A, ldo=256, hdo=64, lse=A, ws=None, bytes=0)
+    bwd = dict(**SIZES, **INPUTS, o=A, ldo=256, hdo=64, do=A, lddo=256, hddo=64, lse=A, qo=None, ko=None, mask=None,
+               scale=0.125, dq=A, lddq=256, hddq=64, dk=A, lddk=128, hddk=64, dv=A, lddv=128, hddv=64, ws=None, bytes=0)
+    fwd["hdq"] = 65      # (read through a copy: the next check is that for its room)
+    for call, good in ((lib.gt_cross_attn_fwd, fwd), (lib.gt_cross_attn_bwd, bwd)):
+        assert [call(*{**good, "scale": x}.values(), None) for x in (2.3e38, 1e-45, 2.4e38, 3e38)] == [-5, -5, -1, -1]
+
+
 @pytest.mark.parametrize("c", [8, 40, 128])
 def test_parts_of_long_keys(gt, c):
     """One query over ever more keys: as many parts as keys for them are there, and no fewer where keys x lanes passes 2^31."""
