@@ -206,8 +206,8 @@ bool tma_rows(const View& v) {
 
 int64_t tiles_of(int n, int batch, int rows) { return std::max<int64_t>(batch, ((int64_t)n + rows - 1) / rows); }
 
-// What a pass costs: microseconds of a step of a CTA with the SM's other CTAs beside it, CTAs on an SM, and bytes that
-// each part writes and reads again.
+// What a pass costs: microseconds of a step of a CTA with the SM's other CTAs beside it (measured for bf16; round estimates
+// for fp32), CTAs on an SM, and bytes that each part writes and reads again.
 struct Cost {
     double step;
     int per_sm;

@@ -10,8 +10,8 @@
 //
 // What bounds both is shared memory, which a product of two operands there reads at 128 bytes a cycle (128 x 64 x 16: 48
 // cycles, from TMEM 32), and the way from products to arithmetic and back (with neither products nor arithmetic, only the
-// barriers: 248 us each for 4096 x 32768, 8 heads of 64).  There dq takes 327 us, dk and dv 485, 816 TFLOP/s of five
-// products over the call; 4099 x 20001, 16 heads of 128 over 4: 105 and 127 us.
+// barriers: 248 us each for 4096 x 32768, 8 heads of 64).  There dq takes 329 us, dk and dv 484, 827 TFLOP/s of five
+// products over the call; 4099 x 20001, 16 heads of 128 over 4: 106 and 128 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -7,8 +7,9 @@
 // own for its share of the keys, joined at the end.  Nothing waits for anything but its own loads.
 //
 // At most two rows (kFewRows): every key costs R dot products and R updates on the fp32 pipes, and from four rows on the
-// tensor cores are quicker (16 queries over 65536 keys, 4 heads sharing keys of 128: 111 us here, 70 there).  One query
-// over 512 nodes, 8 heads of 8, fp32: 6 us, against 19 with the tiles for many rows.
+// tensor cores are quicker (bf16, 16 queries over 65536 keys, 4 heads sharing keys of 128: 111 us here, 64 there).  That is
+// bf16's limit; fp32 has it too, unmeasured, though its kernels for more rows take tiles of 64.  One query over 512 nodes, 8
+// heads of 8, fp32: 6 us, against 19 with the tiles for many rows.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>

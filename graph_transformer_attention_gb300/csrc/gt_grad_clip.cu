@@ -10,7 +10,8 @@
 //
 // Squares of fp32 leave the range of fp32: a unit's sum of squares outside [2^-90, 2^100] is taken again in fp64 (a
 // lane's 32 squares below 2^-149 lose less than 2^-53 of a sum above 2^-90).  A lane's units are added in two fp32 words
-// (the rounding of each addition is kept), everything above in fp64, in a fixed order.
+// (the rounding of each addition is kept), everything above in fp64, in a fixed order.  A factor below 2^-126 multiplies in
+// fp64 as well.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>

@@ -11,7 +11,7 @@
 // the same lane, so that the norm is a few shuffles and the turn none; every row is read once and nothing but gradients
 // is kept for the backward, which forms r again from the x it reads anyway.  The angles are the same for all heads of a
 // row: a warp computes the cosines and sines of its rows once, into shared memory, and fetches the heads of its next rows
-// meanwhile.  (CTAs of eight warps with a barrier between angles and rows: forward 56 us, backward 109, now 43 and 72 to
+// meanwhile.  (CTAs of eight warps with a barrier between angles and rows: forward 56 us, backward 109, now 43 and 74 to
 // 75, for 32768 rows of 16 and 8 heads of 64, bf16: 4.7 and 4.0 TB/s.)  Next limits: issue slots (54 and 52 %) at 16
 // warps to an SM.
 #include <cuda_bf16.h>
